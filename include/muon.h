@@ -62,7 +62,8 @@ typedef enum muon_status {
   MUON_ERR_DEVICE_TIMEOUT = -6,     /* a bounded on-device wait expired (results invalid) */
   MUON_ERR_UNSUPPORTED_DEVICE = -7, /* the current device is not compute capability 10.3 */
   MUON_ERR_TOO_LARGE = -8,          /* a dimension exceeds 2^31-1 elements per row/matrix */
-  MUON_ERR_SCRATCH_LIMIT = -9       /* ns5_noalloc: the call needs more than its static scratch */
+  MUON_ERR_SCRATCH_LIMIT = -9,      /* ns5_noalloc: the call needs more than its static scratch */
+  MUON_ERR_HOST_MEMORY = -10        /* host memory for the call's tables could not be had */
 } muon_status_t;
 
 typedef enum muon_dtype { MUON_BF16 = 0, MUON_F32 = 1 } muon_dtype_t;
@@ -286,6 +287,181 @@ typedef struct adam_tensor_desc {
  * per 64 tensors; needs no workspace. */
 muon_status_t adam_step(const adam_tensor_desc* tensors, int n_tensors, float lr, float beta1, float beta2,
                         float eps, float weight_decay, int step, int cautious, void* stream);
+
+/* One tensor of an AdamW step: caller-owned DEVICE memory, contiguous,
+ * aligned to its own element size (16-byte aligned arrays, 8-byte aligned
+ * codes, take the vector path). */
+typedef struct adamw_tensor_desc {
+  void* param;              /* numel values of param_dtype, updated in place */
+  const void* grad;         /* numel values of grad_dtype, read only */
+  void* exp_avg;            /* first moment: numel fp32 values, or E4M3 codes */
+  void* exp_avg_sq;         /* second moment: numel fp32 values, or E5M2 codes */
+  float* exp_avg_scale;     /* 8-bit moments: one scale per 256 elements (ceil(numel / 256)), else NULL */
+  float* exp_avg_sq_scale;
+  int64_t numel;            /* >= 0 */
+  double lr, weight_decay;  /* finite */
+  int32_t param_dtype;      /* MUON_BF16 or MUON_F32 */
+  int32_t grad_dtype;       /* MUON_BF16 or MUON_F32 */
+  int32_t state_bits;       /* 32 or 8 */
+  int32_t reserved;         /* 0 */
+} adamw_tensor_desc;
+
+/* AdamW step over many tensors at once, each with its own learning rate and
+ * weight decay: the parameters that the Muon step does not take (tables,
+ * gains, biases), moments in 32 bits or in 8.  Per element, t = step,
+ *   g' = *grad_scale * g                      (grad_scale NULL: g' = g)
+ *   m <- beta1 m + (1 - beta1) g';   v <- beta2 v + (1 - beta2) g'^2
+ *   u  = m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ *   p <- p - (lr / (1 - beta1^t) u + lr weight_decay p mask)
+ * with adam_step's mask when `cautious` is non-zero, 1 otherwise.  Float32
+ * arithmetic; the scalars are formed in double and rounded once.
+ * 8-bit moments: a block of 256 consecutive elements of a tensor (the last
+ * one may be shorter) shares a scale.  With E = floor(log2(max |x|)) of the
+ * block, at least -100, the first moment's scale is 2^(E-7) and its codes are
+ * E4M3, the second's 2^(E-14) and E5M2; a value is code * scale.  All-zero
+ * codes with finite scales are the zero state.  A block with a value that is
+ * not finite, or 2^127 or more, gets a NaN scale.
+ * Codes, and bfloat16 parameters, are rounded stochastically (up with the
+ * probability of the remainder), so that averages whose change per step is
+ * below their spacing stay unbiased.  The 32 random bits of element i of
+ * tensor k (position in the list) depend on (seed, step, k, i) alone:
+ *   mix(x): x = (x ^ x >> 16) * 0x6A09E667;  x = (x ^ x >> 15) * 0xBB67AE85;
+ *           x ^ x >> 16                              (modulo 2^32)
+ *   s   = mix(mix(lo(seed) + 0x9E3779B1 step) ^ hi(seed))
+ *   key = mix(s + 0x9E3779B1 k)
+ *   h   = mix(0x9E3779B1 lo(i) + key + 0x6A09E667 hi(i))
+ * the low 16 bits round m, the high 16 v, and the high 16 of 0x9E3779B1 h p.
+ * Results do not depend on the launch configuration.
+ *   tensors, n_tensors  host array (n_tensors = 0: no-op; numel = 0: the
+ *                       tensor is skipped);
+ *   step >= 1; beta1, beta2 in [0, 1); eps >= 0 and finite;
+ *   grad_scale          device pointer to one float (a clipping factor), or
+ *                       NULL; it must lie outside the written arrays.
+ * Errors (nothing enqueued): MUON_ERR_INVALID_ARG, MUON_ERR_MISALIGNED (a
+ * pointer not aligned to its element), MUON_ERR_ALIASING (a written array
+ * overlaps another array; gradients may be shared), MUON_ERR_TOO_LARGE,
+ * MUON_ERR_UNSUPPORTED_DEVICE, MUON_ERR_HOST_MEMORY; MUON_ERR_CUDA (launch
+ * failure).  Asynchronous on `stream`; no workspace; one launch per 400
+ * tensors of the same types. */
+muon_status_t adamw_step(const adamw_tensor_desc* tensors, int n_tensors, double beta1, double beta2, double eps,
+                         int cautious, int64_t step, uint64_t seed, const float* grad_scale, void* stream);
+
+/* The same step for a list of tensors that stays: the plan keeps the checked
+ * descriptors in host memory (no device memory), so a step only enqueues.
+ * The tensors must outlive the plan; grad may be NULL at creation and is then
+ * set before the first step.  A plan is used by one thread at a time. */
+typedef struct adamw_plan adamw_plan;
+muon_status_t adamw_plan_create(const adamw_tensor_desc* tensors, int n_tensors, adamw_plan** plan);
+/* Other gradients, one pointer and dtype per tensor (checked as at creation;
+ * on an error the plan is unchanged). */
+muon_status_t adamw_plan_set_grads(adamw_plan* plan, const void* const* grads, const int32_t* grad_dtypes);
+/* Other learning rates and weight decays, one each per tensor. */
+muon_status_t adamw_plan_set_rates(adamw_plan* plan, const double* lr, const double* weight_decay);
+muon_status_t adamw_plan_step(const adamw_plan* plan, double beta1, double beta2, double eps, int cautious,
+                              int64_t step, uint64_t seed, const float* grad_scale, void* stream);
+void adamw_plan_destroy(adamw_plan* plan);
+
+/* Log probabilities of given tokens, with the entropy of their distribution
+ * and its most likely alternatives.  logits: rows x vocab of `dtype`, row r
+ * at logits + r * row_stride elements (row_stride >= vocab; any alignment of
+ * the element).  With z = scale * logits of a row (scale is the reciprocal of
+ * a temperature; 0 < scale <= 1e6):
+ *   lse = log(sum_j exp(z_j)),   logprobs = z_target - lse,
+ *   entropy = -sum_j p_j log p_j,   p_j = exp(z_j - lse),
+ *   top_ids = the `top` largest logits in falling order, equal ones by the
+ *   lower index (top_logprobs: their z - lse).
+ * Sums are float32.  Entries of -inf (masked tokens) have probability 0 and
+ * contribute nothing.  A row of -inf only has lse = logprobs = top_logprobs =
+ * -inf and entropy 0.  A row with NaN or +inf has NaN results (NaN ranks
+ * below every number).  A negative target marks a row that is left out: its
+ * logits are not read, its outputs are 0 and its top_ids -1.  A target >=
+ * vocab gives NaN as logprobs of that row.
+ *   targets                        rows;
+ *   logprobs, lse, entropy         rows floats each, written;
+ *   top_logprobs, top_ids          rows x top, written (top = 0: may be NULL).
+ * Limits: 1 <= vocab <= 2^30, 0 <= top <= 32 and <= vocab.  rows = 0 is a
+ * no-op.  Written arrays overlap nothing else.  Asynchronous on `stream`; no
+ * workspace.  Returns MUON_OK, MUON_ERR_INVALID_ARG, MUON_ERR_MISALIGNED,
+ * MUON_ERR_ALIASING, MUON_ERR_TOO_LARGE, MUON_ERR_UNSUPPORTED_DEVICE,
+ * MUON_ERR_HOST_MEMORY or MUON_ERR_CUDA. */
+muon_status_t token_logprobs(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t row_stride,
+                             const int64_t* targets, float scale, int top, float* logprobs, float* lse,
+                             float* entropy, float* top_logprobs, int64_t* top_ids, void* stream);
+
+/* Gradient of a loss with respect to the logits, from its gradients with
+ * respect to logprobs and (optionally) entropy:
+ *   grad_j = scale * (gl (1[j = target] - p_j) - ge p_j (log p_j + entropy))
+ * in `dtype`, rounded once; 0 for rows that are left out (target < 0, not
+ * read) and for entries of -inf; NaN for a row whose target is >= vocab.
+ *   lse, entropy      as token_logprobs wrote them for the same logits,
+ *                     targets and scale (entropy is read with grad_entropy
+ *                     only and may be NULL otherwise);
+ *   grad_logprobs     rows floats; grad_entropy rows floats or NULL;
+ *   grad              rows x vocab, row pitch grad_stride elements; it may be
+ *                     `logits` itself (same pointer and pitch), else it
+ *                     overlaps nothing.
+ * Limits, errors and stream as token_logprobs. */
+muon_status_t token_logprobs_backward(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t row_stride,
+                                      const int64_t* targets, float scale, const float* lse, const float* entropy,
+                                      const float* grad_logprobs, const float* grad_entropy, void* grad,
+                                      int64_t grad_stride, void* stream);
+
+/* token_logprobs and token_logprobs_backward in one call, for a loss whose
+ * gradients with respect to logprobs and entropy are known beforehand (a
+ * weighted sum): rows that fit in shared memory are read once. */
+muon_status_t token_logprobs_loss(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t row_stride,
+                                  const int64_t* targets, float scale, int top, const float* grad_logprobs,
+                                  const float* grad_entropy, float* logprobs, float* lse, float* entropy,
+                                  float* top_logprobs, int64_t* top_ids, void* grad, int64_t grad_stride,
+                                  void* stream);
+
+/* Balance loss of a router and its per-expert counts.  The `tokens` rows of
+ * logits (tokens x experts of `dtype`, row pitch row_stride elements) form
+ * `groups` groups of tokens / groups consecutive rows (a sequence each, or one
+ * group for the batch).  p = softmax of a row.  Over the tokens of group g
+ * that the mask keeps:
+ *   counts[g][e] = how many of their top expert ids are e (an id outside
+ *                  0 .. experts-1, such as -1 for a dropped one, counts
+ *                  nowhere),   n_tokens[g] = how many tokens there are,
+ *   f = counts / sum_e counts,   mean_probs[g][e] = sum p_e / n_tokens[g],
+ *   balance = mean over the groups with tokens of experts * sum_e f_e mean_probs_e
+ *   z       = mean over all kept tokens of lse^2, lse = log(sum_e exp(logit_e)).
+ * A group without tokens has zeros, and without any token both losses are 0.
+ *   ids    tokens x top int64;   mask: tokens bytes (0: the token is left
+ *          out and its logits are not read), or NULL;
+ *   stats  4 floats, written: balance, z, 1 / (groups with tokens), 2 / (kept
+ *          tokens) (0 where there are none);
+ *   counts, n_tokens  int32, written;   mean_probs groups x experts floats;
+ *   weights           groups x experts floats, written: d balance / d p of a
+ *          token of the group up to 1 / (groups with tokens) and a constant
+ *          per group, for balance_loss_backward;
+ *   workspace  balance_loss_workspace_size() bytes, 256-byte aligned.
+ * Limits: 1 <= experts <= 1024, 1 <= top <= experts, groups >= 1 divides
+ * tokens, tokens * top < 2^31.  tokens = 0 gives zeros.  Sums are float32 in
+ * a fixed order: equal calls give equal bits.  Rows with NaN or +inf give
+ * NaN; entries of -inf have probability 0; a row of -inf only is NaN.
+ * Written arrays overlap nothing else.  Asynchronous on `stream`.  Returns
+ * MUON_OK, MUON_ERR_INVALID_ARG, MUON_ERR_MISALIGNED, MUON_ERR_ALIASING,
+ * MUON_ERR_WORKSPACE_TOO_SMALL, MUON_ERR_TOO_LARGE,
+ * MUON_ERR_UNSUPPORTED_DEVICE, MUON_ERR_HOST_MEMORY or MUON_ERR_CUDA. */
+muon_status_t balance_loss(const void* logits, int dtype, int64_t tokens, int experts, int64_t row_stride,
+                           const int64_t* ids, int top, const uint8_t* mask, int64_t groups, float* stats,
+                           int32_t* counts, int32_t* n_tokens, float* mean_probs, float* weights, void* workspace,
+                           size_t workspace_bytes, void* stream);
+size_t balance_loss_workspace_size(int64_t tokens, int experts, int64_t groups);
+
+/* Gradient of grad_balance * balance + grad_z * z with respect to the logits
+ * (counts are constants):
+ *   grad_e = p_e (a_e - sum_j a_j p_j) + grad_z 2 lse / n p_e,
+ *   a_e = grad_balance / (groups with tokens) * experts * f_e / n_tokens[g],
+ * in `dtype`, rounded once; 0 for masked tokens.  stats and weights as
+ * balance_loss wrote them for the same logits, ids and mask; grad_balance and
+ * grad_z are device pointers to one float each.  grad: tokens x experts, row
+ * pitch grad_stride; it may be `logits` itself (same pointer and pitch). */
+muon_status_t balance_loss_backward(const void* logits, int dtype, int64_t tokens, int experts, int64_t row_stride,
+                                    const uint8_t* mask, int64_t groups, const float* stats, const float* weights,
+                                    const float* grad_balance, const float* grad_z, void* grad, int64_t grad_stride,
+                                    void* stream);
 
 /* FP8 scaled matrix product, the forward of the page's FP8 matmul
  * (walk-through page, section "自定义FP8矩阵乘法实现"):

@@ -18,7 +18,8 @@ OBJ = os.path.join(PKG, "_build")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libmuon.so")
 DEBUG_LIB = os.path.join(LIBDIR, "libmuon_debug.so")  # device-side checks (MUON_DEBUG)
-SOURCES = ["muon_capi.cu", "elementwise.cu", "ns_gemm.cu", "fp8.cu", "noalloc.cu", "partition.cu", "adam.cu"]
+SOURCES = ["muon_capi.cu", "elementwise.cu", "ns_gemm.cu", "fp8.cu", "noalloc.cu", "partition.cu", "adam.cu",
+           "adamw.cu", "logprob.cu", "balance.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -43,4 +43,7 @@ cudaError_t check_failures_elementwise(int* out);
 cudaError_t check_failures_gemm(int* out);
 cudaError_t check_failures_fp8(int* out);
 cudaError_t check_failures_adam(int* out);
+cudaError_t check_failures_adamw(int* out);
+cudaError_t check_failures_logprob(int* out);
+cudaError_t check_failures_balance(int* out);
 }  // namespace muon

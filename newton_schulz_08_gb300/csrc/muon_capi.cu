@@ -30,6 +30,7 @@
 
 #include "../../include/muon.h"
 #include "check.cuh"
+#include "host.h"
 #include "plan.h"
 #include "ptx.cuh"
 
@@ -832,6 +833,9 @@ bool fp8_class(GemmClass& g, void* a, void* b, void* out, long long rows, long l
 
 using namespace muon;
 
+// For the entry points of the other units (host.h).
+muon_status_t muon::device_sms(int& sms) { return muon::current_device(sms); }
+
 extern "C" {
 
 size_t muon_workspace_size(const muon_mat_desc* mats, int n_mats) {
@@ -1008,6 +1012,7 @@ const char* muon_status_str(muon_status_t s) {
     case MUON_ERR_DEVICE_TIMEOUT: return "bounded device wait expired";
     case MUON_ERR_UNSUPPORTED_DEVICE: return "current device is not compute capability 10.3 (sm_103)";
     case MUON_ERR_TOO_LARGE: return "dimension too large";
+    case MUON_ERR_HOST_MEMORY: return "out of host memory";
     case MUON_ERR_SCRATCH_LIMIT: return "ns5_noalloc: problem needs more than the 64 MiB static scratch";
   }
   return "unknown status";
@@ -1064,7 +1069,8 @@ int muon_debug_check_failures(long long* failures) {
 #ifdef MUON_DEBUG
   long long total = 0;
   for (cudaError_t (*f)(int*) : {&check_failures_elementwise, &check_failures_gemm, &check_failures_fp8,
-                                 &check_failures_adam}) {
+                                 &check_failures_adam, &check_failures_adamw, &check_failures_logprob,
+                                 &check_failures_balance}) {
     int v = 0;
     if (f(&v) != cudaSuccess) {
       cudaGetLastError();

@@ -7,8 +7,10 @@ not pass one, and raises ``MuonError`` on a non-OK status.  It loads the
 library on first use and fails loudly if it has not been built.
 """
 
+import contextlib
 import ctypes
 import os
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -28,6 +30,7 @@ MUON_ERR_DEVICE_TIMEOUT = -6
 MUON_ERR_UNSUPPORTED_DEVICE = -7
 MUON_ERR_TOO_LARGE = -8
 MUON_ERR_SCRATCH_LIMIT = -9
+MUON_ERR_HOST_MEMORY = -10
 MUON_BF16 = 0
 MUON_F32 = 1
 
@@ -36,7 +39,10 @@ EXPORTS = ["muon_workspace_size", "muon_step", "ns5_workspace_size", "ns5", "ns5
            "ns5_bank_workspace_size", "muon_device_status", "muon_status_str",
            "ns5_workspace_layout", "muon_set_debug", "muon_kernel_times", "ns5_noalloc", "ns5_noalloc_status",
            "muon_partition", "adam_step", "fp8_mm", "muon_plan_cache_clear",
-           "fp8_mm_backward", "fp8_mm_backward_workspace_size", "muon_debug_check_failures"]
+           "fp8_mm_backward", "fp8_mm_backward_workspace_size", "muon_debug_check_failures",
+           "adamw_step", "adamw_plan_create", "adamw_plan_set_grads", "adamw_plan_set_rates", "adamw_plan_step",
+           "adamw_plan_destroy", "token_logprobs", "token_logprobs_backward", "token_logprobs_loss", "balance_loss",
+           "balance_loss_workspace_size", "balance_loss_backward"]
 
 #: bytes of the static device scratch ns5_noalloc uses (MUON_NOALLOC_SCRATCH_BYTES)
 NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -68,6 +74,14 @@ class adam_tensor_desc(ctypes.Structure):
     _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("exp_avg", ctypes.c_void_p),
                 ("exp_avg_sq", ctypes.c_void_p), ("numel", ctypes.c_int64),
                 ("grad_dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class adamw_tensor_desc(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("exp_avg", ctypes.c_void_p),
+                ("exp_avg_sq", ctypes.c_void_p), ("exp_avg_scale", ctypes.c_void_p),
+                ("exp_avg_sq_scale", ctypes.c_void_p), ("numel", ctypes.c_int64), ("lr", ctypes.c_double),
+                ("weight_decay", ctypes.c_double), ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
+                ("state_bits", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 _lib = None
@@ -128,6 +142,35 @@ def load(path):
     L.fp8_mm_backward.argtypes = [c_vp, c_vp, c_vp, c_f, c_f, c_f, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_vp,
                                   c_sz, c_vp]
     L.fp8_mm_backward.restype = c_int
+    c_d, c_u64 = ctypes.c_double, ctypes.c_uint64
+    L.adamw_step.argtypes = [P(adamw_tensor_desc), c_int, c_d, c_d, c_d, c_int, c_i64, c_u64, c_vp, c_vp]
+    L.adamw_step.restype = c_int
+    L.adamw_plan_create.argtypes = [P(adamw_tensor_desc), c_int, P(c_vp)]
+    L.adamw_plan_create.restype = c_int
+    L.adamw_plan_set_grads.argtypes = [c_vp, P(c_vp), P(ctypes.c_int32)]
+    L.adamw_plan_set_grads.restype = c_int
+    L.adamw_plan_set_rates.argtypes = [c_vp, P(c_d), P(c_d)]
+    L.adamw_plan_set_rates.restype = c_int
+    L.adamw_plan_step.argtypes = [c_vp, c_d, c_d, c_d, c_int, c_i64, c_u64, c_vp, c_vp]
+    L.adamw_plan_step.restype = c_int
+    L.adamw_plan_destroy.argtypes = [c_vp]
+    L.adamw_plan_destroy.restype = None
+    L.token_logprobs.argtypes = [c_vp, c_int, c_i64, c_i64, c_i64, c_vp, c_f, c_int, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp]
+    L.token_logprobs.restype = c_int
+    L.token_logprobs_backward.argtypes = [c_vp, c_int, c_i64, c_i64, c_i64, c_vp, c_f, c_vp, c_vp, c_vp, c_vp, c_vp,
+                                          c_i64, c_vp]
+    L.token_logprobs_backward.restype = c_int
+    L.token_logprobs_loss.argtypes = [c_vp, c_int, c_i64, c_i64, c_i64, c_vp, c_f, c_int, c_vp, c_vp, c_vp, c_vp, c_vp,
+                                      c_vp, c_vp, c_vp, c_i64, c_vp]
+    L.token_logprobs_loss.restype = c_int
+    L.balance_loss.argtypes = [c_vp, c_int, c_i64, c_int, c_i64, c_vp, c_int, c_vp, c_i64, c_vp, c_vp, c_vp, c_vp, c_vp,
+                               c_vp, c_sz, c_vp]
+    L.balance_loss.restype = c_int
+    L.balance_loss_workspace_size.argtypes = [c_i64, c_int, c_i64]
+    L.balance_loss_workspace_size.restype = c_sz
+    L.balance_loss_backward.argtypes = [c_vp, c_int, c_i64, c_int, c_i64, c_vp, c_i64, c_vp, c_vp, c_vp, c_vp, c_vp,
+                                        c_i64, c_vp]
+    L.balance_loss_backward.restype = c_int
     L.muon_plan_cache_clear.argtypes = []
     L.muon_plan_cache_clear.restype = None
     L.muon_debug_check_failures.argtypes = [P(ctypes.c_longlong)]
@@ -507,3 +550,352 @@ def fp8_mm_backward(g, x_f8, w_f8, x_s, w_s, grad_s, grad_x=None, grad_w=None, g
                                    workspace.numel(), _stream(stream))
     _check(st, "fp8_mm_backward")
     return grad_x, grad_w, g_f8.view(torch.float8_e5m2)
+
+
+def _on(dev):
+    """Makes `dev` the current device for a call (nothing to do when it is)."""
+    return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+#: elements that share one scale of an 8-bit moment
+ADAMW_BLOCK = 256
+
+
+def adamw_state(param, bits=32):
+    """Zero moments for one parameter of an AdamW step: (exp_avg, exp_avg_sq)
+    float32, or with bits=8 (exp_avg, exp_avg_scale, exp_avg_sq,
+    exp_avg_sq_scale): float8_e4m3fn and float8_e5m2 codes with one float32
+    scale per 256 elements."""
+    if bits == 32:
+        return tuple(torch.zeros(param.numel(), dtype=torch.float32, device=param.device) for _ in range(2))
+    if bits != 8:
+        raise ValueError("bits must be 32 or 8")
+    out = []
+    for kind in (torch.float8_e4m3fn, torch.float8_e5m2):
+        out.append(torch.zeros(param.numel(), dtype=torch.uint8, device=param.device).view(kind))
+        out.append(torch.zeros(-(-param.numel() // ADAMW_BLOCK), dtype=torch.float32, device=param.device))
+    return tuple(out)
+
+
+def adamw_state_values(state):
+    """The float32 values (exp_avg, exp_avg_sq) that a state stands for."""
+    if len(state) == 2:
+        return state
+    value = lambda c, s: c.float() * s.repeat_interleave(ADAMW_BLOCK)[:c.numel()]  # noqa: E731
+    return value(state[0], state[1]), value(state[2], state[3])
+
+
+def _per_tensor(x, n, what):
+    x = [float(x)] * n if isinstance(x, (int, float)) else [float(v) for v in x]
+    if len(x) != n:
+        raise ValueError(f"{what}: one number, or one per tensor")
+    return x
+
+
+def _adamw_descs(params, grads, states, lr, weight_decay):
+    n = len(params)
+    if len(states) != n or (grads is not None and len(grads) != n):
+        raise ValueError("params, grads and states must have the same length")
+    lr, weight_decay = _per_tensor(lr, n, "lr"), _per_tensor(weight_decay, n, "weight_decay")
+    arr, every = (adamw_tensor_desc * max(n, 1))(), []
+    for i, (p, s) in enumerate(zip(params, states)):
+        g = None if grads is None else grads[i]
+        if len(s) == 2:
+            (m, v), ms, vs, bits, kinds = s, None, None, 32, (torch.float32, torch.float32)
+        elif len(s) == 4:
+            (m, ms, v, vs), bits, kinds = s, 8, (torch.float8_e4m3fn, torch.float8_e5m2)
+        else:
+            raise ValueError(f"tensor {i}: a state has 2 tensors (32 bits) or 4 (8 bits)")
+        if m.dtype != kinds[0] or v.dtype != kinds[1] or m.numel() != p.numel() or v.numel() != p.numel():
+            raise ValueError(f"tensor {i}: moments must have the parameter's size and be float32, or float8_e4m3fn "
+                             "and float8_e5m2")
+        if bits == 8 and any(t.dtype != torch.float32 or t.numel() != -(-p.numel() // ADAMW_BLOCK) for t in (ms, vs)):
+            raise ValueError(f"tensor {i}: scales must be float32, one per {ADAMW_BLOCK} elements")
+        if g is not None and g.numel() != p.numel():
+            raise ValueError(f"tensor {i}: the gradient must have the parameter's size")
+        used = [t for t in (p, g, m, v, ms, vs) if t is not None]
+        if not all(t.is_contiguous() for t in used):
+            raise ValueError(f"tensor {i}: tensors must be contiguous")
+        every += used
+        arr[i] = adamw_tensor_desc(p.data_ptr(), g.data_ptr() if g is not None else 0, m.data_ptr(), v.data_ptr(),
+                                   ms.data_ptr() if ms is not None else 0, vs.data_ptr() if vs is not None else 0,
+                                   p.numel(), lr[i], weight_decay[i], _dtype_code(p),
+                                   _dtype_code(g) if g is not None else MUON_F32, bits, 0)
+    return arr, n, every
+
+
+def _grad_scale(t, dev):
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or t.numel() != 1 or t.device != dev:
+        raise ValueError("grad_scale must be one float32 value on the parameters' device")
+    return ctypes.c_void_p(t.data_ptr())
+
+
+def adamw_step(params, grads, states, step, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01,
+               cautious=False, grad_scale=None, seed=0, stream=None):
+    """AdamW step over lists of CUDA tensors, in place: float32 or bfloat16
+    params and grads, states from adamw_state (32 or 8 bits, tensor by
+    tensor).  lr and weight_decay: one number, or one per tensor.  grad_scale:
+    a one-element float32 CUDA tensor that the gradients are multiplied with
+    (a clipping factor).  seed: of the stochastic rounding of 8-bit states and
+    bfloat16 parameters.  See adamw_step in include/muon.h; AdamW keeps what
+    is the same in every step."""
+    arr, n, every = _adamw_descs(params, grads, states, lr, weight_decay)
+    if n == 0:
+        return
+    dev = _device_of(every, "adamw_step")
+    with _on(dev):
+        st = lib().adamw_step(arr, n, float(beta1), float(beta2), float(eps), int(bool(cautious)), int(step),
+                              int(seed) & (2 ** 64 - 1), _grad_scale(grad_scale, dev), _stream(stream))
+    _check(st, "adamw_step")
+
+
+class AdamW:
+    """AdamW over a fixed list of parameters, the checked descriptors kept
+    between steps (adamw_plan in include/muon.h), so that a step costs one
+    launch per combination of types.
+
+    states   from adamw_state (default: zeros, 32 bits for every tensor, or
+             `bits`);
+    grads    the gradients' tensors when they stay in place (a bucket);
+             otherwise pass them to step();
+    step     steps already taken.
+    """
+
+    def __init__(self, params, grads=None, states=None, bits=32, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8,
+                 weight_decay=0.01, cautious=False, seed=0, step=0):
+        self.params = list(params)
+        self.grads = None if grads is None else list(grads)
+        self.states = [adamw_state(p, bits) for p in self.params] if states is None else list(states)
+        self.beta1, self.beta2, self.eps, self.cautious = float(beta1), float(beta2), float(eps), int(bool(cautious))
+        self.seed, self.steps = int(seed) & (2 ** 64 - 1), int(step)
+        self._plan = ctypes.c_void_p()
+        if not self.params:
+            raise ValueError("AdamW needs at least one parameter")
+        arr, n, every = _adamw_descs(self.params, self.grads, self.states, lr, weight_decay)
+        self.device = _device_of(every, "AdamW")
+        _check(lib().adamw_plan_create(arr, n, ctypes.byref(self._plan)), "AdamW")
+
+    def __del__(self):
+        if getattr(self, "_plan", None):
+            lib().adamw_plan_destroy(self._plan)
+            self._plan = None
+
+    def set_rates(self, lr, weight_decay):
+        """Learning rate and weight decay from the next step on: one number, or one per tensor."""
+        n = len(self.params)
+        lr, wd = _per_tensor(lr, n, "lr"), _per_tensor(weight_decay, n, "weight_decay")
+        double = ctypes.c_double * n
+        _check(lib().adamw_plan_set_rates(self._plan, double(*lr), double(*wd)), "AdamW.set_rates")
+
+    def set_grads(self, grads):
+        """Other gradient tensors from the next step on."""
+        n, grads = len(self.params), list(grads)
+        if len(grads) != n or any(g.numel() != p.numel() or not g.is_contiguous()
+                                  for g, p in zip(grads, self.params)):
+            raise ValueError("AdamW: one contiguous gradient of the parameter's size per parameter")
+        if _device_of(grads, "AdamW") != self.device:
+            raise ValueError(f"AdamW: gradients must be on {self.device}")
+        ptrs = (ctypes.c_void_p * n)(*[g.data_ptr() for g in grads])
+        kinds = (ctypes.c_int32 * n)(*[_dtype_code(g) for g in grads])
+        _check(lib().adamw_plan_set_grads(self._plan, ptrs, kinds), "AdamW.set_grads")
+        self.grads = grads
+
+    def step(self, grads=None, grad_scale=None, stream=None):
+        """One step, in place; `grads` replaces the gradients' tensors."""
+        if grads is not None:
+            self.set_grads(grads)
+        elif self.grads is None:
+            raise ValueError("AdamW.step: no gradients given, here or at construction")
+        with _on(self.device):
+            st = lib().adamw_plan_step(self._plan, self.beta1, self.beta2, self.eps, self.cautious, self.steps + 1,
+                                       self.seed, _grad_scale(grad_scale, self.device), _stream(stream))
+        _check(st, "AdamW.step")
+        self.steps += 1
+
+    def state_values(self):
+        """The float32 moments (exp_avg, exp_avg_sq) of each parameter."""
+        return [adamw_state_values(s) for s in self.states]
+
+
+class TokenLogprobs(NamedTuple):
+    """What token_logprobs gives for each row."""
+    logprobs: torch.Tensor
+    lse: torch.Tensor
+    entropy: torch.Tensor
+    top_logprobs: Optional[torch.Tensor]
+    top_ids: Optional[torch.Tensor]
+    grad: Optional[torch.Tensor] = None
+
+
+def _matrix(t, what):
+    """(rows, columns, row pitch) of a 2-D CUDA tensor with unit column stride."""
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise ValueError(f"{what} must be 2-D with contiguous rows")
+    rows, cols = t.shape
+    pitch = t.stride(0) if rows > 1 else cols
+    if pitch < cols:
+        raise ValueError(f"{what}: rows overlap")
+    return rows, cols, pitch
+
+
+def _per_row(t, rows, dtype, what):
+    if t.shape != (rows,) or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor with one entry per row")
+    return ctypes.c_void_p(t.data_ptr())
+
+
+def _ptr(t):
+    return ctypes.c_void_p(t.data_ptr()) if t is not None else None
+
+
+def _score_outputs(rows, top, dev):
+    logprobs, lse, entropy = (torch.empty(rows, dtype=torch.float32, device=dev) for _ in range(3))
+    if not top:
+        return logprobs, lse, entropy, None, None
+    return (logprobs, lse, entropy, torch.empty((rows, top), dtype=torch.float32, device=dev),
+            torch.empty((rows, top), dtype=torch.int64, device=dev))
+
+
+def _grad_out(out, logits):
+    if out is None:
+        out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    if out.shape != logits.shape or out.dtype != logits.dtype:
+        raise ValueError("out must have the logits' shape and dtype")
+    return out
+
+
+def token_logprobs(logits, targets, top=0, scale=1.0, stream=None):
+    """Log probabilities of the targets (int64, one per row; negative: the row
+    is left out) under softmax(scale * logits), with log-sum-exp, entropy and
+    the `top` (<= 32) most likely entries: a TokenLogprobs.  logits: rows x
+    vocab, bfloat16 or float32, any row pitch.  See include/muon.h."""
+    rows, vocab, pitch = _matrix(logits, "logits")
+    dev = _device_of((logits, targets), "token_logprobs")
+    y = _per_row(targets, rows, torch.int64, "targets")
+    out = _score_outputs(rows, top, dev)
+    with _on(dev):
+        st = lib().token_logprobs(_ptr(logits), _dtype_code(logits), rows, vocab, pitch, y, float(scale), int(top),
+                                  _ptr(out[0]), _ptr(out[1]), _ptr(out[2]), _ptr(out[3]), _ptr(out[4]),
+                                  _stream(stream))
+    _check(st, "token_logprobs")
+    return TokenLogprobs(*out)
+
+
+def token_logprobs_backward(logits, targets, lse, grad_logprobs, entropy=None, grad_entropy=None, scale=1.0, out=None,
+                            stream=None):
+    """Gradient with respect to the logits from those with respect to
+    logprobs and, with `entropy` as token_logprobs gave it, entropy.  `out`
+    may be the logits themselves.  See include/muon.h."""
+    rows, vocab, pitch = _matrix(logits, "logits")
+    out = _grad_out(out, logits)
+    out_pitch = _matrix(out, "out")[2]
+    if grad_entropy is not None and entropy is None:
+        raise ValueError("grad_entropy needs entropy")
+    dev = _device_of([t for t in (logits, targets, lse, grad_logprobs, entropy, grad_entropy, out) if t is not None],
+                     "token_logprobs_backward")
+    f32 = torch.float32
+    with _on(dev):
+        st = lib().token_logprobs_backward(
+            _ptr(logits), _dtype_code(logits), rows, vocab, pitch, _per_row(targets, rows, torch.int64, "targets"),
+            float(scale), _per_row(lse, rows, f32, "lse"),
+            _per_row(entropy, rows, f32, "entropy") if entropy is not None else None,
+            _per_row(grad_logprobs, rows, f32, "grad_logprobs"),
+            _per_row(grad_entropy, rows, f32, "grad_entropy") if grad_entropy is not None else None,
+            _ptr(out), out_pitch, _stream(stream))
+    _check(st, "token_logprobs_backward")
+    return out
+
+
+def token_logprobs_loss(logits, targets, grad_logprobs, grad_entropy=None, top=0, scale=1.0, out=None, stream=None):
+    """token_logprobs together with the gradient with respect to the logits
+    (TokenLogprobs.grad), for a loss whose gradients with respect to logprobs
+    and entropy are known beforehand; `out` may be the logits themselves.
+    See include/muon.h."""
+    rows, vocab, pitch = _matrix(logits, "logits")
+    out = _grad_out(out, logits)
+    out_pitch = _matrix(out, "out")[2]
+    dev = _device_of([t for t in (logits, targets, grad_logprobs, grad_entropy, out) if t is not None],
+                     "token_logprobs_loss")
+    y, gl = _per_row(targets, rows, torch.int64, "targets"), _per_row(grad_logprobs, rows, torch.float32, "grad_logprobs")
+    ge = _per_row(grad_entropy, rows, torch.float32, "grad_entropy") if grad_entropy is not None else None
+    got = _score_outputs(rows, top, dev)
+    with _on(dev):
+        st = lib().token_logprobs_loss(_ptr(logits), _dtype_code(logits), rows, vocab, pitch, y, float(scale), int(top),
+                                       gl, ge, _ptr(got[0]), _ptr(got[1]), _ptr(got[2]), _ptr(got[3]), _ptr(got[4]),
+                                       _ptr(out), out_pitch, _stream(stream))
+    _check(st, "token_logprobs_loss")
+    return TokenLogprobs(*got, out)
+
+
+class BalanceLoss(NamedTuple):
+    """What balance_loss gives: the losses (0-d), int32 counts (groups x
+    experts) and token numbers (groups), mean router probabilities (groups x
+    experts), and what balance_loss_backward reads."""
+    balance: torch.Tensor
+    z: torch.Tensor
+    counts: torch.Tensor
+    tokens: torch.Tensor
+    mean_probs: torch.Tensor
+    stats: torch.Tensor
+    weights: torch.Tensor
+
+
+def balance_loss_workspace_size(tokens, experts, groups=1):
+    return lib().balance_loss_workspace_size(int(tokens), int(experts), int(groups))
+
+
+def _mask(mask, tokens):
+    if mask is None:
+        return None
+    if mask.shape != (tokens,) or mask.dtype not in (torch.bool, torch.uint8) or not mask.is_contiguous():
+        raise ValueError("mask must be a contiguous bool tensor with one entry per token")
+    return ctypes.c_void_p(mask.data_ptr())
+
+
+def balance_loss(logits, ids, mask=None, groups=1, workspace=None, stream=None):
+    """Balance loss and z loss of a router, with the experts' counts: logits
+    tokens x experts (bfloat16 or float32, any row pitch), ids tokens x top
+    int64 (the experts each token goes to), mask one bool per token (False:
+    left out), `groups` sequences of equal length.  See include/muon.h."""
+    tokens, experts, pitch = _matrix(logits, "logits")
+    if ids.dim() != 2 or ids.shape[0] != tokens or ids.dtype != torch.int64 or not ids.is_contiguous():
+        raise ValueError("ids must be a contiguous tokens x top int64 tensor")
+    dev = _device_of([t for t in (logits, ids, mask, workspace) if t is not None], "balance_loss")
+    f32, i32 = torch.float32, torch.int32
+    stats = torch.empty(4, dtype=f32, device=dev)
+    counts = torch.empty((groups, experts), dtype=i32, device=dev)
+    n_tokens = torch.empty(groups, dtype=i32, device=dev)
+    mean, weights = (torch.empty((groups, experts), dtype=f32, device=dev) for _ in range(2))
+    with _on(dev):
+        if workspace is None:
+            workspace = new_workspace(balance_loss_workspace_size(tokens, experts, groups), dev)
+        st = lib().balance_loss(_ptr(logits), _dtype_code(logits), tokens, experts, pitch, _ptr(ids), ids.shape[1],
+                                _mask(mask, tokens), int(groups), _ptr(stats), _ptr(counts), _ptr(n_tokens),
+                                _ptr(mean), _ptr(weights), _ptr(workspace), workspace.numel(), _stream(stream))
+    _check(st, "balance_loss")
+    return BalanceLoss(stats[0], stats[1], counts, n_tokens, mean, stats, weights)
+
+
+def balance_loss_backward(logits, result, grad_balance, grad_z, mask=None, out=None, stream=None):
+    """Gradient of grad_balance * balance + grad_z * z (one-element float32
+    CUDA tensors) with respect to the logits; `result` is balance_loss's for
+    the same logits and mask.  `out` may be the logits themselves."""
+    tokens, experts, pitch = _matrix(logits, "logits")
+    out = _grad_out(out, logits)
+    out_pitch = _matrix(out, "out")[2]
+    groups = result.counts.shape[0]
+    if result.counts.shape[1] != experts:
+        raise ValueError("result is of other logits")
+    for t in (grad_balance, grad_z):
+        if t.dtype != torch.float32 or t.numel() != 1:
+            raise ValueError("grad_balance and grad_z must be one-element float32 tensors")
+    dev = _device_of([t for t in (logits, mask, grad_balance, grad_z, out, result.stats) if t is not None],
+                     "balance_loss_backward")
+    with _on(dev):
+        st = lib().balance_loss_backward(_ptr(logits), _dtype_code(logits), tokens, experts, pitch,
+                                         _mask(mask, tokens), groups, _ptr(result.stats), _ptr(result.weights),
+                                         _ptr(grad_balance), _ptr(grad_z), _ptr(out), out_pitch, _stream(stream))
+    _check(st, "balance_loss_backward")
+    return out

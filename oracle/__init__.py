@@ -26,16 +26,25 @@ on the modded-nanogpt record "2026-06-11_RecursiveFromBest" (lqnn.cn,
 news/184262, section "3.3 bigram 与 value-embedding 银行上的 C-Optim / 谨慎
 Adam") describes for the embedding-type banks; its readings are stated there.
 
+``oracle.adamw`` and ``oracle.losses`` restate the operators at the two ends
+of a training step from their formulas: AdamW over tensors with moments in 32
+bits or in 8, token log probabilities, and the balance loss of a router.
+
 Pin status: every public function is pinned by the CPU tests
 (closed form via SVD, invariants, brute force in exact rational arithmetic,
 bit-exact bf16 rounding against an independent routine; for Adam: closed
 forms, torch.optim.Adam / AdamW special cases, hand-worked mask values; for
 FP8: bit-exact casts against torch's float8 conversions and a bit-field
 decoding of all 256 codes, exact products of representable operands, power-of-
-two scale invariance, brute force in rational arithmetic).
+two scale invariance, brute force in rational arithmetic; for AdamW and the
+losses: torch.optim.AdamW, torch's autograd and differences in float64, the
+formats' representable values, the mean of the stochastic rounding).
 """
 
 from .adam import ADAM_DEFAULTS, adam_constants, adam_step, cautious_mask
+from .adamw import (adamw_bits, adamw_dequantize, adamw_moments, adamw_quantize, adamw_update,
+                    bf16_stochastic)
+from .losses import balance_loss, balance_loss_grad, token_logprobs, token_logprobs_grad
 from .fp8 import FP8_FORMATS, fp8_mm, fp8_mm_backward, quantize, round_to_fp8
 from .bf16 import round_to_bf16, BF16_MAX
 from .muon import (
@@ -60,6 +69,16 @@ __all__ = [
     "fp8_mm_backward",
     "quantize",
     "round_to_fp8",
+    "adamw_bits",
+    "adamw_dequantize",
+    "adamw_moments",
+    "adamw_quantize",
+    "adamw_update",
+    "bf16_stochastic",
+    "balance_loss",
+    "balance_loss_grad",
+    "token_logprobs",
+    "token_logprobs_grad",
     "ADAM_DEFAULTS",
     "adam_constants",
     "adam_step",
