@@ -6,7 +6,20 @@
 //   lse = m + log S,   logprob = z_target - lse,   entropy = log S - W / S,
 //   grad_j = scale (gl 1[j = target] - p_j (gl + ge (log p_j + entropy))).
 //
-// One CTA per row.
+// HBM-bound: 2 or 4 bytes read per entry, and as many written for a
+// gradient; about five instructions an entry.  The logits of a row are read
+// once for whatever a call computes from them:
+//   - up to 8 KB (logprob_warp): the row stays in the registers of up to 32
+//     lanes, and no warp waits for another;
+//   - beyond (logprob_row): the row stays in shared memory, up to 104 KB a
+//     CTA so that two CTAs of an SM overlap one's loads with the other's
+//     arithmetic, spread over a cluster where it is longer or where rows are
+//     few; the CTAs exchange their sums through distributed shared memory;
+//   - rows that no cluster of eight holds are read again (logprob_stream).
+// The backward pass alone knows the sums and is elementwise (logprob_grad).
+// Entries of -inf: exponents are held above -1000, where 2^t is 0 and 0 * t
+// stays 0.
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -19,11 +32,27 @@
 #include "check.cuh"
 #include "host.h"
 
+namespace cg = cooperative_groups;
+
 namespace muon {
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kMaxTop = 32;
+constexpr int kMaxCluster = 8;
+constexpr int kWarpVecs = 512;            // longest row of logprob_warp in 16-byte vectors
+constexpr int kWarpThreads = 256;
+constexpr int kWarpCandidates = 192;
+constexpr int kSegmentBytes = 104 * 1024; // of a row in one CTA's shared memory
+constexpr int kGradThreads = 256;
+constexpr int kGradVecs = 4;              // 16-byte vectors per thread of logprob_grad
+constexpr int kStreamThreads = 512;
+constexpr int kCandidates = 512;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kFloor = -1000.0f;        // least exponent
+constexpr float kMasked = -1e30f;         // below: log S is lost beside the largest logit
+
+enum Mode { kScore = 0, kLoss = 1, kBackward = 2 };
 
 struct LogprobParams {
   const void* x;
@@ -36,9 +65,11 @@ struct LogprobParams {
   const float* gl;
   const float* ge;
   void* grad;
-  long long stride, grad_stride;
+  long long rows, stride, grad_stride;
   int vocab, top;
   float scale;
+  int lanes;        // logprob_warp: lanes per row
+  int chunks;       // logprob_grad: CTAs per row
 };
 
 template <bool BF16>
@@ -47,30 +78,703 @@ __device__ __forceinline__ float at(const void* x, long long i) {
   else return static_cast<const float*>(x)[i];
 }
 
-// A number's place in the order of alternatives: larger values first, then
-// lower indices; NaN below every number.
-__device__ __forceinline__ unsigned long long order_key(float x, int j) {
-  x = isnan(x) ? -INFINITY : x + 0.0f;  // -0 equals 0
-  const uint32_t u = __float_as_uint(x);
-  const uint32_t k = u & 0x80000000u ? ~u : u | 0x80000000u;
-  return static_cast<unsigned long long>(k) << 32 | (0xFFFFFFFFu - static_cast<uint32_t>(j));
+template <bool BF16>
+__device__ __forceinline__ void put(void* x, long long i, float v) {
+  if constexpr (BF16) static_cast<__nv_bfloat16*>(x)[i] = __float2bfloat16_rn(v);
+  else static_cast<float*>(x)[i] = v;
 }
 
-template <typename T, typename F>
-__device__ __forceinline__ T block_reduce(T v, F f, T* scratch) {
-  for (int d = 16; d > 0; d /= 2) v = f(v, __shfl_xor_sync(0xFFFFFFFFu, v, d));
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = scratch[0];
-  for (int w = 1; w < kThreads / 32; ++w) v = f(v, scratch[w]);
-  return v;
+// A 16-byte vector holds 8 or 4 entries.
+template <bool BF16>
+constexpr int kPer = BF16 ? 8 : 4;
+
+template <bool BF16>
+__device__ __forceinline__ void unpack(uint4 q, float (&x)[kPer<BF16>]) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if constexpr (BF16) {
+      x[2 * k] = __uint_as_float(w[k] << 16);
+      x[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+    } else {
+      x[k] = __uint_as_float(w[k]);
+    }
+  }
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads) logprob_score(const __grid_constant__ LogprobParams P) {
-  __shared__ float scratch[kThreads / 32];
-  __shared__ unsigned long long key_scratch[kThreads / 32];
+__device__ __forceinline__ uint4 pack(const float (&x)[kPer<BF16>]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if constexpr (BF16) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
+      w[k] = *reinterpret_cast<const uint32_t*>(&b);
+    } else {
+      w[k] = __float_as_uint(x[k]);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Largest entry of a vector (NaN left out).
+template <bool BF16>
+__device__ __forceinline__ float vec_max(uint4 q) {
+  if constexpr (BF16) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    __nv_bfloat162 b[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) b[k] = *reinterpret_cast<const __nv_bfloat162*>(&w[k]);
+    const __nv_bfloat162 m = __hmax2(__hmax2(b[0], b[1]), __hmax2(b[2], b[3]));
+    return fmaxf(__low2float(m), __high2float(m));
+  } else {
+    return fmaxf(fmaxf(__uint_as_float(q.x), __uint_as_float(q.y)), fmaxf(__uint_as_float(q.z), __uint_as_float(q.w)));
+  }
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
+// A number's place in the order of alternatives: larger values first, then
+// lower indices; NaN below every number.  0 is below every place.
+__device__ __forceinline__ uint32_t ordered(float x) {
+  x = isnan(x) ? -INFINITY : x + 0.0f;  // -0 equals 0
+  const uint32_t u = __float_as_uint(x);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ unsigned long long place(float x, int j) {
+  return static_cast<unsigned long long>(ordered(x)) << 32 | (0xFFFFFFFFu - static_cast<uint32_t>(j));
+}
+__device__ __forceinline__ int place_index(unsigned long long p) { return static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(p)); }
+__device__ __forceinline__ float place_value(unsigned long long p) {
+  const uint32_t k = static_cast<uint32_t>(p >> 32);
+  return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
+}
+
+// Sums of a row or of a part of it: s = sum 2^t, w = sum 2^t t with
+// t = (x - m) scale log2(e).
+struct Sums {
+  float m, s, w;
+};
+
+__device__ __forceinline__ float reference(float m) { return m == -INFINITY ? 0.0f : m; }
+
+// Adds N entries, two at a time (paired float32 instructions).
+template <int N>
+__device__ __forceinline__ void accumulate(float2& s, float2& w, const float (&x)[N], float ref, float c2) {
+  const float2 minus = make_float2(-ref, -ref), scale = make_float2(c2, c2);
+#pragma unroll
+  for (int k = 0; k < N; k += 2) {
+    float2 t = __fmul2_rn(__fadd2_rn(make_float2(x[k], x[k + 1]), minus), scale);
+    t = make_float2(max_nan(t.x, kFloor), max_nan(t.y, kFloor));
+    const float2 e = make_float2(ex2(t.x), ex2(t.y));
+    s = __fadd2_rn(s, e);
+    w = __ffma2_rn(e, t, w);
+  }
+}
+
+__device__ __forceinline__ Sums merge(const Sums& a, const Sums& b, float c2) {
+  Sums r;
+  r.m = fmaxf(a.m, b.m);
+  const float ref = reference(r.m);
+  const float ta = max_nan((a.m - ref) * c2, kFloor), tb = max_nan((b.m - ref) * c2, kFloor);
+  const float fa = ex2(ta), fb = ex2(tb);
+  r.s = a.s * fa + b.s * fb;
+  r.w = fmaf(a.s, ta, a.w) * fa + fmaf(b.s, tb, b.w) * fb;
+  return r;
+}
+
+// What follows from a row's sums.
+struct RowStats {
+  float m, log_s, entropy, lse;
+  bool empty;  // every entry -inf
+};
+
+__device__ __forceinline__ RowStats stats_of(const Sums& a, float scale) {
+  RowStats r;
+  r.empty = a.s == 0.0f;
+  r.m = reference(a.m);
+  r.log_s = r.empty ? 0.0f : logf(a.s);
+  r.entropy = r.empty ? 0.0f : r.log_s - kLn2 * (a.w / a.s);
+  r.lse = r.empty ? -INFINITY : fmaf(r.m, scale, r.log_s);
+  return r;
+}
+
+__device__ __forceinline__ float logprob_of(const RowStats& r, float x, float scale) {
+  return r.empty ? -INFINITY : (x - r.m) * scale - r.log_s;
+}
+
+// The gradient of a row: with d = log p_j = (x_j - m) scale - log_s,
+// grad_j = exp(d) (a d + b) [+ at_target at the target].
+struct RowGrad {
+  float m, log_s, a, b, at_target;
+};
+
+__device__ __forceinline__ RowGrad grad_of(const LogprobParams& P, const RowStats& r, long long row, int64_t target) {
+  RowGrad g;
+  const float gl = target < P.vocab ? P.gl[row] : NAN, ge = P.ge ? P.ge[row] : 0.0f;
+  g.m = r.m;
+  g.log_s = r.log_s;
+  g.a = r.empty ? 0.0f : -P.scale * ge;
+  g.b = r.empty ? 0.0f : -P.scale * (gl + ge * r.entropy);
+  if (isnan(r.log_s) || target >= P.vocab) g.b = NAN;
+  g.at_target = r.empty ? 0.0f : P.scale * gl;
+  return g;
+}
+
+// What the backward pass knows of a row.
+__device__ __forceinline__ RowStats stats_from_lse(const LogprobParams& P, long long row) {
+  RowStats r;
+  r.lse = P.lse[row];
+  r.empty = r.lse == -INFINITY;
+  r.m = 0.0f;
+  r.log_s = r.empty ? 0.0f : r.lse;
+  r.entropy = P.ge ? P.entropy[row] : 0.0f;
+  return r;
+}
+
+// Whether every logit of the row is so low (a mask of the type's lowest
+// value) that lse does not hold log S any more.
+__device__ __forceinline__ bool log_s_is_lost(const RowStats& r) { return r.lse < kMasked && !r.empty; }
+
+// x[k], entries j .. j+N-1 of the row, become their gradients.
+template <int N>
+__device__ __forceinline__ void grad_entries(const RowGrad& g, float scale, int64_t target, int j, float (&x)[N]) {
+  const float2 minus = make_float2(-g.m, -g.m), z = make_float2(scale, scale), log_s = make_float2(-g.log_s, -g.log_s);
+  const float2 a = make_float2(g.a, g.a), b = make_float2(g.b, g.b), log2e = make_float2(kLog2e, kLog2e);
+#pragma unroll
+  for (int k = 0; k < N; k += 2) {
+    float2 d = __ffma2_rn(__fadd2_rn(make_float2(x[k], x[k + 1]), minus), z, log_s);
+    d = make_float2(max_nan(d.x, kFloor), max_nan(d.y, kFloor));
+    const float2 t = __fmul2_rn(d, log2e);
+    const float2 v = __fmul2_rn(make_float2(ex2(t.x), ex2(t.y)), __ffma2_rn(a, d, b));
+    x[k] = v.x;
+    x[k + 1] = v.y;
+  }
+  const unsigned long long at = static_cast<unsigned long long>(target - j);
+  if (at < N) {
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (at == k) x[k] += g.at_target;
+  }
+}
+
+__device__ __forceinline__ float grad_entry(const RowGrad& g, float scale, int64_t target, int j, float x) {
+  const float d = max_nan(fmaf(x - g.m, scale, -g.log_s), kFloor);
+  return ex2(d * kLog2e) * fmaf(g.a, d, g.b) + (j == target ? g.at_target : 0.0f);
+}
+
+// The 16-byte vectors of a row, counted from the 16-byte boundary at or below
+// its first entry; `shift` entries of the first vector lie before the row.
+template <bool BF16>
+struct RowVectors {
+  const unsigned char* base;
+  int shift, count, vocab;
+  __device__ __forceinline__ RowVectors(const void* x, long long offset, int vocab_) : vocab(vocab_) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(x) + static_cast<uintptr_t>(offset) * (BF16 ? 2 : 4);
+    base = reinterpret_cast<const unsigned char*>(a & ~static_cast<uintptr_t>(15));
+    shift = static_cast<int>(a & 15) / (BF16 ? 2 : 4);
+    count = (shift + vocab + kPer<BF16> - 1) / kPer<BF16>;
+  }
+  __device__ __forceinline__ int first(int v) const { return v * kPer<BF16> - shift; }  // index of the vector's first entry
+  __device__ __forceinline__ bool whole(int v) const { return first(v) >= 0 && first(v) + kPer<BF16> <= vocab; }
+  // A vector at an end of the row from its entries; what lies outside counts as masked.
+  __device__ __forceinline__ uint4 end(int v) const {
+    float x[kPer<BF16>];
+#pragma unroll
+    for (int k = 0; k < kPer<BF16>; ++k) {
+      const int j = first(v) + k;
+      x[k] = j >= 0 && j < vocab ? at<BF16>(base, v * static_cast<long long>(kPer<BF16>) + k) : -INFINITY;
+    }
+    return pack<BF16>(x);
+  }
+};
+
+// --------------------------------------------------- rows in registers (warps)
+
+// Collected places of one warp, and of its first entries in order.
+struct WarpTop {
+  unsigned long long candidate[kWarpCandidates];
+  unsigned long long top[kMaxTop];
+  int n;
+};
+
+// The `top` first places of a row that a whole warp holds, into S.top; see
+// cta_top.  The groups are the lanes.
+template <bool BF16, int NV>
+__device__ __forceinline__ bool warp_top(const LogprobParams& P, const RowVectors<BF16>& R, const uint4 (&q)[NV], int lane,
+                                         WarpTop& S) {
+  constexpr int kN = kPer<BF16>;
+  float own = -INFINITY;
+#pragma unroll
+  for (int u = 0; u < NV; ++u) own = fmaxf(own, vec_max<BF16>(q[u]));
+  uint32_t left = ordered(own), bound = 0;
+  for (int k = 0; k < P.top; ++k) {
+    bound = __reduce_max_sync(0xFFFFFFFFu, left);
+    if (lane == __ffs(__ballot_sync(0xFFFFFFFFu, left == bound)) - 1) left = 0;
+  }
+  const float least = place_value(static_cast<unsigned long long>(bound) << 32);
+  if (lane == 0) S.n = 0;
+  __syncwarp();
+#pragma unroll
+  for (int u = 0; u < NV; ++u) {
+    if (vec_max<BF16>(q[u]) < least) continue;
+    float x[kN];
+    unpack<BF16>(q[u], x);
+#pragma unroll
+    for (int k = 0; k < kN; ++k) {
+      const int j = R.first(lane + 32 * u) + k;
+      if (j < 0 || j >= P.vocab || ordered(x[k]) < bound) continue;
+      const int i = atomicAdd(&S.n, 1);
+      if (i < kWarpCandidates) S.candidate[i] = place(x[k], j);
+    }
+  }
+  __syncwarp();
+  const int n = S.n;
+  if (n > kWarpCandidates) return false;
+  for (int i = lane; i < n; i += 32) {
+    const unsigned long long mine = S.candidate[i];
+    int rank = 0;
+    for (int j = 0; j < n; ++j) rank += S.candidate[j] > mine;
+    if (rank < P.top) S.top[rank] = mine;
+  }
+  __syncwarp();
+  return true;
+}
+
+template <bool BF16, int NV, int MODE>
+__global__ void __launch_bounds__(kWarpThreads, NV == 16 ? 2 : NV == 8 ? 3 : 4) logprob_warp(const __grid_constant__ LogprobParams P) {
+  constexpr int kN = kPer<BF16>;
+  __shared__ WarpTop S[MODE == kBackward ? 1 : kWarpThreads / 32];
+  const int lane = threadIdx.x & 31, sub = lane & (P.lanes - 1), rows_warp = 32 / P.lanes;
+  const long long row = (static_cast<long long>(blockIdx.x) * (kWarpThreads / 32) + (threadIdx.x >> 5)) * rows_warp + lane / P.lanes;
+  const bool in = row < P.rows;
+  const int64_t target = in ? P.targets[row] : -1;
+  const bool on = target >= 0;
+  const RowVectors<BF16> R(P.x, in ? row * P.stride : 0, P.vocab);
+  const uint4 masked = make_uint4(BF16 ? 0xFF80FF80u : 0xFF800000u, BF16 ? 0xFF80FF80u : 0xFF800000u,
+                                  BF16 ? 0xFF80FF80u : 0xFF800000u, BF16 ? 0xFF80FF80u : 0xFF800000u);
+  uint4 q[NV];
+#pragma unroll
+  for (int u = 0; u < NV; ++u) {
+    const int v = sub + P.lanes * u;
+    q[u] = masked;
+    if (!on || v >= R.count) continue;
+    if (R.whole(v)) q[u] = *reinterpret_cast<const uint4*>(R.base + v * 16LL);
+    else q[u] = R.end(v);
+  }
+  RowStats r{};
+  if (MODE == kBackward && on) r = stats_from_lse(P, row);
+  if (MODE != kBackward || __any_sync(0xFFFFFFFFu, on && log_s_is_lost(r))) {
+    Sums a{-INFINITY, 0.0f, 0.0f};
+#pragma unroll
+    for (int u = 0; u < NV; ++u) a.m = fmaxf(a.m, vec_max<BF16>(q[u]));
+    for (int d = P.lanes / 2; d > 0; d /= 2) a.m = fmaxf(a.m, __shfl_xor_sync(0xFFFFFFFFu, a.m, d));
+    float2 s{}, w{};
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      float x[kN];
+      unpack<BF16>(q[u], x);
+      accumulate(s, w, x, reference(a.m), P.scale * kLog2e);
+    }
+    a.s = s.x + s.y;
+    a.w = w.x + w.y;
+    for (int d = P.lanes / 2; d > 0; d /= 2) {
+      a.s += __shfl_xor_sync(0xFFFFFFFFu, a.s, d);
+      a.w += __shfl_xor_sync(0xFFFFFFFFu, a.w, d);
+    }
+    if (MODE != kBackward || log_s_is_lost(r)) r = stats_of(a, P.scale);
+  }
+  if constexpr (MODE != kBackward) {
+    if (in && sub == 0) {
+      P.lse[row] = on ? r.lse : 0.0f;
+      P.entropy[row] = on ? r.entropy : 0.0f;
+      P.logprobs[row] = !on ? 0.0f : target >= P.vocab ? NAN : logprob_of(r, at<BF16>(P.x, row * P.stride + target), P.scale);
+    }
+    if (P.top > 0) {
+      WarpTop& T = S[threadIdx.x >> 5];
+      if (!__any_sync(0xFFFFFFFFu, on)) {
+        if (in)
+          for (int k = sub; k < P.top; k += P.lanes) P.top_ids[row * P.top + k] = -1, P.top_logprobs[row * P.top + k] = 0.0f;
+      } else if (P.lanes == 32 && warp_top<BF16, NV>(P, R, q, lane, T)) {
+        if (in && lane < P.top) {
+          P.top_ids[row * P.top + lane] = place_index(T.top[lane]);
+          P.top_logprobs[row * P.top + lane] = logprob_of(r, place_value(T.top[lane]), P.scale);
+        }
+      } else {  // a few entries a lane, or a row of ties: one maximum after the other
+        unsigned long long last = ~0ull;
+        for (int k = 0; k < P.top; ++k) {
+          unsigned long long best = 0;
+#pragma unroll 1
+          for (int u = 0; u < NV; ++u) {
+            uint4 qu = q[0];
+#pragma unroll
+            for (int i = 1; i < NV; ++i) qu = i == u ? q[i] : qu;
+            float x[kN];
+            unpack<BF16>(qu, x);
+#pragma unroll
+            for (int i = 0; i < kN; ++i) {
+              const int j = R.first(sub + P.lanes * u) + i;
+              const unsigned long long v = j >= 0 && j < P.vocab ? place(x[i], j) : 0;
+              if (v < last && v > best) best = v;
+            }
+          }
+          for (int d = P.lanes / 2; d > 0; d /= 2) {
+            const unsigned long long o = __shfl_xor_sync(0xFFFFFFFFu, best, d);
+            best = o > best ? o : best;
+          }
+          last = best;
+          if (in && sub == 0) {
+            P.top_ids[row * P.top + k] = on ? place_index(best) : -1;
+            P.top_logprobs[row * P.top + k] = on ? logprob_of(r, place_value(best), P.scale) : 0.0f;
+          }
+        }
+      }
+    }
+  }
+  if constexpr (MODE != kScore) {
+    __syncwarp();  // in place: the target's logit has been read
+    if (!in) return;
+    RowGrad g{};
+    if (on) g = grad_of(P, r, row, target);
+    const RowVectors<BF16> O(P.grad, row * P.grad_stride, P.vocab);
+    uint4* const o = reinterpret_cast<uint4*>(const_cast<unsigned char*>(O.base));
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      const int v = sub + P.lanes * u, j = R.first(v);
+      if (v >= R.count) continue;
+      float x[kN] = {};
+      if (on) {
+        unpack<BF16>(q[u], x);
+        grad_entries(g, P.scale, target, j, x);
+      }
+      if (O.shift == R.shift && R.whole(v)) {
+        o[v] = pack<BF16>(x);
+      } else {
+#pragma unroll
+        for (int k = 0; k < kN; ++k)
+          if (j + k >= 0 && j + k < P.vocab) put<BF16>(P.grad, row * P.grad_stride + j + k, x[k]);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------ rows in shared memory (CTAs)
+
+template <int THREADS, typename F>
+__device__ __forceinline__ float cta_reduce(float v, F f, float* scratch) {
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) v = f(v, __shfl_xor_sync(0xFFFFFFFFu, v, d));
+  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = scratch[0];
+#pragma unroll
+  for (int w = 1; w < THREADS / 32; ++w) v = f(v, scratch[w]);
+  return v;
+}
+
+template <int THREADS>
+__device__ __forceinline__ float2 cta_sum2(float2 v, float2* scratch) {
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) {
+    v.x += __shfl_xor_sync(0xFFFFFFFFu, v.x, d);
+    v.y += __shfl_xor_sync(0xFFFFFFFFu, v.y, d);
+  }
+  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = scratch[0];
+#pragma unroll
+  for (int w = 1; w < THREADS / 32; ++w) v = __fadd2_rn(v, scratch[w]);
+  return v;
+}
+
+// What the CTAs of a cluster tell one another.
+struct Exchange {
+  Sums sums[kMaxCluster];
+  unsigned long long top[kMaxCluster][kMaxTop];
+};
+
+template <int THREADS>
+struct TopScratch {
+  uint32_t group_max[128];
+  uint32_t bound;
+  int n;
+  unsigned long long candidate[kCandidates];
+  unsigned long long best[THREADS / 32];
+  unsigned long long top[kMaxTop];
+};
+
+// The `top` first places among this CTA's entries, into S.top (0 where there
+// are fewer).  own_max: the thread's largest entry.  `each(least, f)` calls
+// f(value, index) for the thread's entries that are at least `least` (for
+// others too, if that is cheaper).
+//   bound: the top-th largest of 128 groups' maxima; at least `top` entries
+//   reach it, and seldom many more do.  Those are collected and ranked by
+//   counting.  Rows where more than kCandidates reach it (ties, masks that
+//   leave fewer than `top` entries) take one maximum after the other.
+template <int THREADS, typename E>
+__device__ __forceinline__ void cta_top(int top, float own_max, E each, TopScratch<THREADS>& S) {
+  const int t = threadIdx.x, lane = t & 31;
+  const uint32_t own = ordered(own_max);
+  uint32_t g = own;
+#pragma unroll
+  for (int d = 1; d < THREADS / 128; d *= 2) g = max(g, __shfl_xor_sync(0xFFFFFFFFu, g, d));
+  if (t % (THREADS / 128) == 0) S.group_max[t / (THREADS / 128)] = g;
+  if (t == 0) S.n = 0;
+  if (t < kMaxTop) S.top[t] = 0;
+  __syncthreads();
+  if (t < 32) {
+    uint32_t v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = S.group_max[lane + 32 * k];
+    uint32_t bound = 0;
+    for (int q = 0; q < top; ++q) {
+      const uint32_t m = max(max(v[0], v[1]), max(v[2], v[3]));
+      bound = __reduce_max_sync(0xFFFFFFFFu, m);
+      if (lane == __ffs(__ballot_sync(0xFFFFFFFFu, m == bound)) - 1) {  // one group leaves
+        bool gone = false;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (!gone && v[k] == bound) v[k] = 0, gone = true;
+      }
+    }
+    if (lane == 0) S.bound = bound;
+  }
+  __syncthreads();
+  const uint32_t bound = S.bound;
+  if (own >= bound) {
+    each(place_value(static_cast<unsigned long long>(bound) << 32), [&](float x, int j) {
+      if (ordered(x) < bound) return;
+      const int i = atomicAdd(&S.n, 1);
+      if (i < kCandidates) S.candidate[i] = place(x, j);
+    });
+  }
+  __syncthreads();
+  const int n = S.n;
+  if (n <= kCandidates) {
+    for (int i = t; i < n; i += THREADS) {
+      const unsigned long long mine = S.candidate[i];
+      int rank = 0;
+      for (int j = 0; j < n; ++j) rank += S.candidate[j] > mine;
+      if (rank < top) S.top[rank] = mine;
+    }
+  } else {
+    unsigned long long last = ~0ull;
+    for (int q = 0; q < top; ++q) {
+      unsigned long long best = 0;
+      each(-INFINITY, [&](float x, int j) {
+        const unsigned long long v = place(x, j);
+        if (v < last && v > best) best = v;
+      });
+#pragma unroll
+      for (int d = 16; d > 0; d /= 2) {
+        const unsigned long long o = __shfl_xor_sync(0xFFFFFFFFu, best, d);
+        best = o > best ? o : best;
+      }
+      if (lane == 0) S.best[t >> 5] = best;
+      __syncthreads();
+      for (int w = 0; w < THREADS / 32; ++w) best = S.best[w] > best ? S.best[w] : best;
+      if (t == 0) S.top[q] = best;
+      last = best;
+      __syncthreads();
+    }
+  }
+  __syncthreads();
+}
+
+template <bool BF16, int THREADS, int MODE>
+__global__ void __launch_bounds__(THREADS) logprob_row(const __grid_constant__ LogprobParams P) {
+  extern __shared__ __align__(16) unsigned char segment[];
+  __shared__ float scratch[2][THREADS / 32];
+  __shared__ float2 pair_scratch[2][THREADS / 32];
+  __shared__ Exchange X;
+  __shared__ TopScratch<THREADS> S;
+  constexpr int kN = kPer<BF16>;
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int ranks = cluster.num_blocks(), rank = cluster.block_rank();
+  const int t = threadIdx.x;
+  const long long row = blockIdx.x / ranks;
+  const int64_t target = P.targets[row];
+  const RowVectors<BF16> R(P.x, row * P.stride, P.vocab);
+  const int v0 = static_cast<int>(static_cast<long long>(R.count) * rank / ranks);
+  const int n = static_cast<int>(static_cast<long long>(R.count) * (rank + 1) / ranks) - v0;
+  uint4* const q = reinterpret_cast<uint4*>(segment);
+  const long long out = row * P.grad_stride;
+  // the gradient's vectors begin where the row's do
+  const bool same = MODE == kLoss && RowVectors<BF16>(P.grad, out, P.vocab).shift == R.shift;
+
+  if (target < 0) {  // every CTA of the cluster returns
+    if (rank == 0 && t == 0) P.logprobs[row] = P.lse[row] = P.entropy[row] = 0.0f;
+    if (rank == 0 && t < P.top) P.top_logprobs[row * P.top + t] = 0.0f, P.top_ids[row * P.top + t] = -1;
+    if constexpr (MODE == kLoss) {
+      const int j0 = max(0, R.first(v0)), j1 = min(P.vocab, R.first(v0 + n));
+      if (same) {
+        uint4* const o = reinterpret_cast<uint4*>(const_cast<unsigned char*>(RowVectors<BF16>(P.grad, out, P.vocab).base));
+        for (int i = t; i < n; i += THREADS) {
+          if (R.whole(v0 + i)) {
+            o[v0 + i] = make_uint4(0, 0, 0, 0);
+          } else {
+            for (int k = 0; k < kN; ++k) {
+              const int j = R.first(v0 + i) + k;
+              if (j >= 0 && j < P.vocab) put<BF16>(P.grad, out + j, 0.0f);
+            }
+          }
+        }
+      } else {
+        for (int j = j0 + t; j < j1; j += THREADS) put<BF16>(P.grad, out + j, 0.0f);
+      }
+    }
+    return;
+  }
+
+  // a CTA's shared memory is written by others only once it has begun
+  if (ranks > 1) cg::cluster_group::barrier_arrive();
+  // four groups of copies; a thread's vectors are the ones it copies, so it
+  // adds a group up without waiting for other threads
+  const int lo = R.shift > 0 ? 1 : 0, wholes = (R.shift + P.vocab) / kN - lo;  // vectors inside the row
+  const int per = (n + 4 * THREADS - 1) / (4 * THREADS) * THREADS;
+#pragma unroll
+  for (int group = 0; group < 4; ++group) {
+    const int end = min(n, (group + 1) * per);
+    const unsigned char* src = R.base + static_cast<long long>(v0 + group * per + t) * 16;
+    for (int i = group * per + t; i < end; i += THREADS, src += THREADS * 16) {
+      if (static_cast<unsigned>(v0 + i - lo) < static_cast<unsigned>(wholes)) {
+        const unsigned dst = static_cast<unsigned>(__cvta_generic_to_shared(q + i));
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+      } else {
+        q[i] = R.end(v0 + i);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  float x_target = 0.0f;
+  if (t == 0 && rank == 0 && target < P.vocab) x_target = at<BF16>(P.x, row * P.stride + target);
+
+  // Sums against the largest of the first vectors, which is near enough to
+  // the row's largest entry unless S says otherwise.
+  const float c2 = P.scale * kLog2e;
+  auto largest = [](float x, float y) { return fmaxf(x, y); };
+  float own_max = -INFINITY;
+  float2 s{}, w{};
+  Sums a{0.0f, 0.0f, 0.0f};
+  auto group_sums = [&](int group) {
+    const int end = min(n, (group + 1) * per);
+#pragma unroll 2
+    for (int i = group * per + t; i < end; i += THREADS) {
+      const uint4 v = q[i];
+      if (P.top > 0) own_max = fmaxf(own_max, vec_max<BF16>(v));
+      float x[kN];
+      unpack<BF16>(v, x);
+      accumulate(s, w, x, reference(a.m), c2);
+    }
+  };
+  asm volatile("cp.async.wait_group 3;" ::: "memory");
+  a.m = cta_reduce<THREADS>(t < n ? vec_max<BF16>(q[t]) : -INFINITY, largest, scratch[0]);
+  group_sums(0);
+  asm volatile("cp.async.wait_group 2;" ::: "memory");
+  group_sums(1);
+  asm volatile("cp.async.wait_group 1;" ::: "memory");
+  group_sums(2);
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  group_sums(3);
+  float2 sums = cta_sum2<THREADS>(make_float2(s.x + s.y, w.x + w.y), pair_scratch[0]);
+  if (!(sums.x >= 0.5f && sums.x < 0x1p60f)) {  // again, against the row's own largest entry
+    float m = -INFINITY;
+    for (int i = t; i < n; i += THREADS) m = fmaxf(m, vec_max<BF16>(q[i]));
+    a.m = cta_reduce<THREADS>(m, largest, scratch[1]);
+    s = w = make_float2(0.0f, 0.0f);
+    for (int group = 0; group < 4; ++group) group_sums(group);
+    sums = cta_sum2<THREADS>(make_float2(s.x + s.y, w.x + w.y), pair_scratch[1]);
+  }
+  a.s = sums.x;
+  a.w = sums.y;
+  if (ranks > 1) {
+    cg::cluster_group::barrier_wait();
+    if (t < ranks) cluster.map_shared_rank(&X, t)->sums[rank] = a;
+    cluster.sync();
+    a = X.sums[0];
+    for (int k = 1; k < ranks; ++k) a = merge(a, X.sums[k], c2);
+  }
+  const RowStats r = stats_of(a, P.scale);
+  if (rank == 0 && t == 0) {
+    P.lse[row] = r.lse;
+    P.entropy[row] = r.entropy;
+    P.logprobs[row] = target < P.vocab ? logprob_of(r, x_target, P.scale) : NAN;
+  }
+
+  if constexpr (MODE == kLoss) {
+    const RowGrad g = grad_of(P, r, row, target);
+    if (same) {
+      uint4* const o = reinterpret_cast<uint4*>(const_cast<unsigned char*>(RowVectors<BF16>(P.grad, out, P.vocab).base));
+      for (int i = t; i < n; i += THREADS) {
+        const int j = R.first(v0 + i);
+        float x[kN];
+        unpack<BF16>(q[i], x);
+        grad_entries(g, P.scale, target, j, x);
+        if (static_cast<unsigned>(v0 + i - lo) < static_cast<unsigned>(wholes)) {
+          o[v0 + i] = pack<BF16>(x);
+        } else {
+          for (int k = 0; k < kN; ++k)
+            if (j + k >= 0 && j + k < P.vocab) put<BF16>(P.grad, out + j + k, x[k]);
+        }
+      }
+    } else {
+      const int j0 = max(0, R.first(v0)), j1 = min(P.vocab, R.first(v0 + n)), from = R.first(v0);
+      for (int j = j0 + t; j < j1; j += THREADS)
+        put<BF16>(P.grad, out + j, grad_entry(g, P.scale, target, j, at<BF16>(segment, j - from)));
+    }
+  }
+
+  if (P.top > 0) {
+    cta_top<THREADS>(P.top, own_max, [&](float least, auto f) {
+      for (int i = t; i < n; i += THREADS) {
+        if (vec_max<BF16>(q[i]) < least) continue;
+        float x[kN];
+        unpack<BF16>(q[i], x);
+#pragma unroll
+        for (int k = 0; k < kN; ++k) {
+          const int j = R.first(v0 + i) + k;
+          if (j >= 0 && j < P.vocab) f(x[k], j);
+        }
+      }
+    }, S);
+    unsigned long long mine = 0;
+    if (ranks > 1) {
+      if (t < P.top) cluster.map_shared_rank(&X, 0)->top[rank][t] = S.top[t];
+      cluster.sync();
+      if (rank != 0) return;
+      const int all = ranks * P.top;
+      for (int i = t; i < all; i += THREADS) {
+        mine = X.top[i / P.top][i % P.top];
+        int place_ = 0;
+        for (int j = 0; j < all; ++j) place_ += X.top[j / P.top][j % P.top] > mine;
+        if (mine != 0 && place_ < P.top) S.top[place_] = mine;
+      }
+      __syncthreads();
+    }
+    if (t < P.top) {
+      P.top_ids[row * P.top + t] = place_index(S.top[t]);
+      P.top_logprobs[row * P.top + t] = logprob_of(r, place_value(S.top[t]), P.scale);
+    }
+  }
+}
+
+// --------------------------------------------------- rows of any length (CTA)
+
+template <bool BF16>
+__global__ void __launch_bounds__(kStreamThreads) logprob_stream(const __grid_constant__ LogprobParams P) {
+  __shared__ float scratch[kStreamThreads / 32];
+  __shared__ float2 pair_scratch[kStreamThreads / 32];
+  __shared__ TopScratch<kStreamThreads> S;
   const long long row = blockIdx.x, base = row * P.stride;
   const int64_t target = P.targets[row];
   const int t = threadIdx.x;
@@ -79,62 +783,106 @@ __global__ void __launch_bounds__(kThreads) logprob_score(const __grid_constant_
     if (t < P.top) P.top_logprobs[row * P.top + t] = 0.0f, P.top_ids[row * P.top + t] = -1;
     return;
   }
-  auto add = [](float a, float b) { return a + b; };
-  float m = -INFINITY;
-  for (int j = t; j < P.vocab; j += kThreads) m = fmaxf(m, at<BF16>(P.x, base + j) * P.scale);
-  m = block_reduce(m, [](float a, float b) { return fmaxf(a, b); }, scratch);
-  const float ref = m == -INFINITY ? 0.0f : m;
-  float s = 0.0f, w = 0.0f;
-  for (int j = t; j < P.vocab; j += kThreads) {
-    const float d = at<BF16>(P.x, base + j) * P.scale - ref;
-    const float e = expf(d);
-    s += e;
-    if (e > 0.0f) w += e * d;
+  const float c2 = P.scale * kLog2e;
+  float own_max = -INFINITY;
+#pragma unroll 8
+  for (int j = t; j < P.vocab; j += kStreamThreads) own_max = fmaxf(own_max, at<BF16>(P.x, base + j));
+  Sums a{0.0f, 0.0f, 0.0f};
+  a.m = cta_reduce<kStreamThreads>(own_max, [](float x, float y) { return fmaxf(x, y); }, scratch);
+  float2 s{}, w{};
+#pragma unroll 4
+  for (int j = t; j < P.vocab; j += 2 * kStreamThreads) {
+    const float x[2] = {at<BF16>(P.x, base + j), j + kStreamThreads < P.vocab ? at<BF16>(P.x, base + j + kStreamThreads) : -INFINITY};
+    accumulate(s, w, x, reference(a.m), c2);
   }
-  s = block_reduce(s, add, scratch);
-  w = block_reduce(w, add, scratch);
-  const float lse = m + logf(s);
+  const float2 sums = cta_sum2<kStreamThreads>(make_float2(s.x + s.y, w.x + w.y), pair_scratch);
+  a.s = sums.x;
+  a.w = sums.y;
+  const RowStats r = stats_of(a, P.scale);
   if (t == 0) {
-    P.lse[row] = lse;
-    P.entropy[row] = s == 0.0f ? 0.0f : logf(s) - w / s;
-    P.logprobs[row] = target >= P.vocab ? NAN
-                      : lse == -INFINITY ? -INFINITY : at<BF16>(P.x, base + target) * P.scale - lse;
+    P.lse[row] = r.lse;
+    P.entropy[row] = r.entropy;
+    P.logprobs[row] = target < P.vocab ? logprob_of(r, at<BF16>(P.x, base + target), P.scale) : NAN;
   }
-  unsigned long long last = ~0ull;
-  for (int k = 0; k < P.top; ++k) {
-    unsigned long long best = 0;
-    for (int j = t; j < P.vocab; j += kThreads) {
-      const unsigned long long q = order_key(at<BF16>(P.x, base + j), j);
-      if (q < last && q > best) best = q;
-    }
-    best = block_reduce(best, [](unsigned long long a, unsigned long long b) { return a > b ? a : b; }, key_scratch);
-    last = best;
-    if (t == 0) {
-      const int j = static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(best));
-      P.top_ids[row * P.top + k] = j;
-      P.top_logprobs[row * P.top + k] = lse == -INFINITY ? -INFINITY : at<BF16>(P.x, base + j) * P.scale - lse;
-    }
+  if (P.top == 0) return;
+  cta_top<kStreamThreads>(P.top, own_max, [&](float, auto f) {
+    for (int j = t; j < P.vocab; j += kStreamThreads) f(at<BF16>(P.x, base + j), j);
+  }, S);
+  if (t < P.top) {
+    P.top_ids[row * P.top + t] = place_index(S.top[t]);
+    P.top_logprobs[row * P.top + t] = logprob_of(r, place_value(S.top[t]), P.scale);
   }
 }
 
+// ---------------------------------------------------- backward, elementwise
+
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads) logprob_grad(const __grid_constant__ LogprobParams P) {
-  const long long row = blockIdx.x, base = row * P.stride, out = row * P.grad_stride;
+__global__ void __launch_bounds__(kGradThreads) logprob_grad(const __grid_constant__ LogprobParams P) {
+  __shared__ float scratch[2][kGradThreads / 32];
+  constexpr int kN = kPer<BF16>;
+  const long long row = blockIdx.x / P.chunks;
+  const int chunk = blockIdx.x % P.chunks, t = threadIdx.x;
   const int64_t target = P.targets[row];
   const bool on = target >= 0;
-  const float lse = on ? P.lse[row] : 0.0f;
-  const float gl = !on ? 0.0f : target < P.vocab ? P.gl[row] : NAN;
-  const float ge = on && P.ge ? P.ge[row] : 0.0f, h = on && P.ge ? P.entropy[row] : 0.0f;
-  for (int j = threadIdx.x; j < P.vocab; j += kThreads) {
-    float v = 0.0f;
-    if (on) {
-      const float d = at<BF16>(P.x, base + j) * P.scale - lse;
-      const float p = lse == -INFINITY ? 0.0f : expf(d);
-      v = p == 0.0f ? (isnan(gl) ? gl : 0.0f) : -p * (gl + ge * (d + h));
-      if (j == target) v += gl;
+  const long long base = row * P.stride, out = row * P.grad_stride;
+  const RowVectors<BF16> R(P.x, base, P.vocab), O(P.grad, out, P.vocab);
+  const int v0 = chunk * kGradThreads * kGradVecs, v1 = min(R.count, v0 + kGradThreads * kGradVecs);
+  const bool same = R.shift == O.shift;
+  uint4 q[kGradVecs];
+  if (on && same) {
+#pragma unroll
+    for (int u = 0; u < kGradVecs; ++u) {
+      const int v = v0 + u * kGradThreads + t;
+      if (v < v1 && R.whole(v)) q[u] = *reinterpret_cast<const uint4*>(R.base + static_cast<long long>(v) * 16);
     }
-    if constexpr (BF16) static_cast<__nv_bfloat16*>(P.grad)[out + j] = __float2bfloat16_rn(v * P.scale);
-    else static_cast<float*>(P.grad)[out + j] = v * P.scale;
+  }
+  RowStats r{};
+  if (on) r = stats_from_lse(P, row);
+  if (on && log_s_is_lost(r)) {  // the row's first CTA takes all of it, with its own sums
+    if (chunk != 0) return;
+    Sums a{-INFINITY, 0.0f, 0.0f};
+    for (int j = t; j < P.vocab; j += kGradThreads) a.m = fmaxf(a.m, at<BF16>(P.x, base + j));
+    a.m = cta_reduce<kGradThreads>(a.m, [](float x, float y) { return fmaxf(x, y); }, scratch[0]);
+    float2 s{}, w{};
+    for (int j = t; j < P.vocab; j += kGradThreads) {
+      const float x[2] = {at<BF16>(P.x, base + j), -INFINITY};
+      accumulate(s, w, x, reference(a.m), P.scale * kLog2e);
+    }
+    a.s = cta_reduce<kGradThreads>(s.x + s.y, [](float x, float y) { return x + y; }, scratch[1]);
+    const float entropy = r.entropy;
+    r = stats_of(a, P.scale);
+    r.entropy = entropy;
+    const RowGrad g = grad_of(P, r, row, target);
+    for (int j = t; j < P.vocab; j += kGradThreads)
+      put<BF16>(P.grad, out + j, grad_entry(g, P.scale, target, j, at<BF16>(P.x, base + j)));
+    return;
+  }
+  RowGrad g{};
+  if (on) g = grad_of(P, r, row, target);
+  if (same) {
+    uint4* const o = reinterpret_cast<uint4*>(const_cast<unsigned char*>(O.base));
+#pragma unroll
+    for (int u = 0; u < kGradVecs; ++u) {
+      const int v = v0 + u * kGradThreads + t;
+      if (v >= v1) continue;
+      const int j = R.first(v);
+      if (R.whole(v)) {
+        float x[kN] = {};
+        if (on) {
+          unpack<BF16>(q[u], x);
+          grad_entries(g, P.scale, target, j, x);
+        }
+        o[v] = pack<BF16>(x);
+      } else {
+        for (int k = 0; k < kN; ++k)
+          if (j + k >= 0 && j + k < P.vocab) put<BF16>(P.grad, out + j + k, on ? grad_entry(g, P.scale, target, j + k, at<BF16>(P.x, base + j + k)) : 0.0f);
+      }
+    }
+  } else {
+    const int j0 = max(0, R.first(v0)), j1 = min(P.vocab, R.first(v1));
+#pragma unroll 8
+    for (int j = j0 + t; j < j1; j += kGradThreads)
+      put<BF16>(P.grad, out + j, on ? grad_entry(g, P.scale, target, j, at<BF16>(P.x, base + j)) : 0.0f);
   }
 }
 
@@ -152,6 +900,48 @@ muon_status_t check_logits(const void* logits, int dtype, int64_t rows, int64_t 
 
 uint64_t matrix_bytes(int64_t rows, int64_t cols, int64_t stride, int dtype) {
   return (static_cast<uint64_t>(rows - 1) * stride + cols) * (dtype == MUON_F32 ? 4 : 2);
+}
+
+using KernelPtr = void (*)(LogprobParams);
+
+#define WARPS(BF16, MODE)                                                                                  \
+  logprob_warp<BF16, 1, MODE>, logprob_warp<BF16, 2, MODE>, logprob_warp<BF16, 4, MODE>, logprob_warp<BF16, 8, MODE>, \
+      logprob_warp<BF16, 16, MODE>
+// Index: 0 .. 4 for 1, 2, 4, 8, 16 vectors a lane; + 5 mode; + 15 for bfloat16.
+const KernelPtr kWarpKernels[30] = {WARPS(false, kScore), WARPS(false, kLoss), WARPS(false, kBackward),
+                                    WARPS(true, kScore),  WARPS(true, kLoss),  WARPS(true, kBackward)};
+#undef WARPS
+
+// Index: 512 threads | loss << 1 | bfloat16 << 2.
+const KernelPtr kRowKernels[8] = {
+    logprob_row<false, 256, kScore>, logprob_row<false, 512, kScore>, logprob_row<false, 256, kLoss>,
+    logprob_row<false, 512, kLoss>,  logprob_row<true, 256, kScore>,  logprob_row<true, 512, kScore>,
+    logprob_row<true, 256, kLoss>,   logprob_row<true, 512, kLoss>,
+};
+
+cudaError_t launch_rows(const LogprobParams& P, bool bf16, bool loss, long long bytes, int sms, cudaStream_t stream) {
+  int ranks = 1;
+  while (bytes > static_cast<long long>(ranks) * kSegmentBytes) ranks *= 2;
+  // few rows: spread each over more CTAs while every one keeps 4 KB and the GPU has SMs to spare
+  while (ranks < kMaxCluster && P.rows * ranks * 2 <= 2LL * sms && bytes / (ranks * 2) >= 4096) ranks *= 2;
+  const long long part = (bytes + 15) / 16 / ranks + 1;  // vectors
+  const bool wide = part > 2048;                         // 32 KB: 256 threads take eight vectors each
+  const KernelPtr f = kRowKernels[(wide ? 1 : 0) | (loss ? 2 : 0) | (bf16 ? 4 : 0)];
+  const size_t smem = static_cast<size_t>(part) * 16;
+  cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(f), cudaFuncAttributeMaxDynamicSharedMemorySize, kSegmentBytes + 64);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(P.rows * ranks));
+  cfg.blockDim = dim3(wide ? 512 : 256);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(ranks);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, f, P);
 }
 
 // What both directions check and launch; grad, gl: null for a score alone,
@@ -172,6 +962,12 @@ muon_status_t run(const void* logits, int dtype, int64_t rows, int64_t vocab, in
       !aligned_to(top_ids, 8) || !aligned_to(gl, 4) || !aligned_to(ge, 4) ||
       !aligned_to(grad, dtype == MUON_F32 ? 4 : 2))
     return MUON_ERR_MISALIGNED;
+  const int size = dtype == MUON_F32 ? 4 : 2;
+  const int64_t bytes = vocab * size + 32;  // of a row, with both ends' partial vectors
+  const bool held = bytes <= static_cast<int64_t>(kMaxCluster) * kSegmentBytes;
+  const int64_t per_cta = 16 * kGradThreads * kGradVecs, chunks = (bytes + per_cta - 1) / per_cta;
+  const int64_t vecs = (bytes - 2) / 16;   // at most: rows begin anywhere
+  if (vecs > kWarpVecs && rows > INT32_MAX / std::max<int64_t>(kMaxCluster, chunks)) return MUON_ERR_TOO_LARGE;
   const uint64_t r = static_cast<uint64_t>(rows);
   try {
     std::vector<Span> v = {span_of(targets, r * 8, false)};
@@ -207,24 +1003,39 @@ muon_status_t run(const void* logits, int dtype, int64_t rows, int64_t vocab, in
   P.gl = gl;
   P.ge = ge;
   P.grad = grad;
+  P.rows = rows;
   P.stride = row_stride;
   P.grad_stride = grad_stride;
   P.vocab = static_cast<int>(vocab);
   P.top = score ? top : 0;
   P.scale = scale;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const unsigned grid = static_cast<unsigned>(rows);
-  if (score) {
-    if (dtype == MUON_BF16) logprob_score<true><<<grid, kThreads, 0, s>>>(P);
-    else logprob_score<false><<<grid, kThreads, 0, s>>>(P);
-    if (cudaGetLastError() != cudaSuccess) return MUON_ERR_CUDA;
+  const cudaStream_t str = static_cast<cudaStream_t>(stream);
+  const bool bf16 = dtype == MUON_BF16;
+  cudaError_t err = cudaSuccess;
+  if (vecs <= kWarpVecs) {
+    P.lanes = 1;
+    while (P.lanes < 32 && P.lanes < vecs) P.lanes *= 2;
+    int k = 0;
+    while (P.lanes << k < vecs) ++k;
+    const long long per = static_cast<long long>(kWarpThreads / 32) * (32 / P.lanes);
+    const unsigned grid = static_cast<unsigned>((rows + per - 1) / per);
+    const int mode = !backward ? kScore : score ? kLoss : kBackward;
+    kWarpKernels[k + 5 * mode + (bf16 ? 15 : 0)]<<<grid, kWarpThreads, 0, str>>>(P);
+    err = cudaGetLastError();
+  } else {
+    if (score && held) {
+      err = launch_rows(P, bf16, backward, bytes, sms, str);
+    } else if (score) {
+      (bf16 ? logprob_stream<true> : logprob_stream<false>)<<<static_cast<unsigned>(rows), kStreamThreads, 0, str>>>(P);
+      err = cudaGetLastError();
+    }
+    if (err == cudaSuccess && backward && !(score && held)) {
+      P.chunks = static_cast<int>(chunks);
+      (bf16 ? logprob_grad<true> : logprob_grad<false>)<<<static_cast<unsigned>(rows * P.chunks), kGradThreads, 0, str>>>(P);
+      err = cudaGetLastError();
+    }
   }
-  if (backward) {
-    if (dtype == MUON_BF16) logprob_grad<true><<<grid, kThreads, 0, s>>>(P);
-    else logprob_grad<false><<<grid, kThreads, 0, s>>>(P);
-    if (cudaGetLastError() != cudaSuccess) return MUON_ERR_CUDA;
-  }
-  return MUON_OK;
+  return err == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
 }
 
 }  // namespace

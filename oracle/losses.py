@@ -36,7 +36,8 @@ def token_logprobs(x, targets, scale=1.0, top=0):
             s = e.sum()
             lse[r] = m + np.log(s)
             h[r] = np.log(s) - (e[e > 0] * d[e > 0]).sum() / s
-        value = lambda j: -np.inf if lse[r] == -np.inf else z[j] - lse[r]  # noqa: E731
+        # z_j - lse, with log s kept apart from a largest logit that may be the type's lowest value
+        value = lambda j: -np.inf if lse[r] == -np.inf else (np.nan if nan else d[j] - np.log(s))  # noqa: E731
         lp[r] = np.nan if t >= vocab else value(t)
         rank = np.where(np.isnan(x[r]), -np.inf, x[r])
         ids[r] = np.argsort(-rank, kind="stable")[:top]
