@@ -45,8 +45,10 @@ constexpr int kWarpCandidates = 192;
 constexpr int kSegmentBytes = 104 * 1024; // of a row in one CTA's shared memory
 constexpr int kGradThreads = 256;
 constexpr int kGradVecs = 4;              // 16-byte vectors per thread of logprob_grad
-constexpr int kStreamThreads = 512;
+constexpr int kScoreThreads = 256;
 constexpr int kCandidates = 512;
+constexpr int kTopGroups = 128;
+constexpr int kLossStatic = 10 * 1024;     // shared memory of a logprob_loss CTA beside its part of the row, at most
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kFloor = -1000.0f;        // least exponent
@@ -69,6 +71,7 @@ struct LogprobParams {
   int vocab, top;
   float scale;
   int lanes;        // logprob_warp: lanes per row
+  int log_ranks;    // logprob_row: CTAs per row, as a power of two
   int chunks;       // logprob_grad: CTAs per row
 };
 
@@ -115,6 +118,19 @@ __device__ __forceinline__ uint4 pack(const float (&x)[kPer<BF16>]) {
     }
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Read once: it goes past L1.
+__device__ __forceinline__ uint4 load_once(const uint4* p) {
+  uint4 v;
+  asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint4 masked_vector() {
+  const uint32_t w = BF16 ? 0xFF80FF80u : 0xFF800000u;  // -inf
+  return make_uint4(w, w, w, w);
 }
 
 // Largest entry of a vector (NaN left out).
@@ -179,6 +195,32 @@ __device__ __forceinline__ void accumulate(float2& s, float2& w, const float (&x
     const float2 e = make_float2(ex2(t.x), ex2(t.y));
     s = __fadd2_rn(s, e);
     w = __ffma2_rn(e, t, w);
+  }
+}
+
+// Adds a vector.  bfloat16: entries are held above -1e30 in pairs before they
+// are widened, and the exponent is one fused operation of K = -ref c2 (44
+// instructions a vector against 52); a reference for which that does not do
+// gives sums that are no number of order 1, and they are taken again.
+template <bool BF16>
+__device__ __forceinline__ void accumulate_near(float2& s, float2& w, uint4 q, float ref, float c2) {
+  if constexpr (BF16) {
+    const __nv_bfloat162 floor2 = __floats2bfloat162_rn(kMasked, kMasked);
+    uint32_t v[4] = {q.x, q.y, q.z, q.w};
+    const float2 scale = make_float2(c2, c2), K = make_float2(-ref * c2, -ref * c2);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const __nv_bfloat162 b = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&v[k]), floor2);
+      v[k] = *reinterpret_cast<const uint32_t*>(&b);
+      const float2 t = __ffma2_rn(make_float2(__uint_as_float(v[k] << 16), __uint_as_float(v[k] & 0xFFFF0000u)), scale, K);
+      const float2 e = make_float2(ex2(t.x), ex2(t.y));
+      s = __fadd2_rn(s, e);
+      w = __ffma2_rn(e, t, w);
+    }
+  } else {
+    float x[4];
+    unpack<false>(q, x);
+    accumulate(s, w, x, ref, c2);
   }
 }
 
@@ -283,12 +325,12 @@ struct RowVectors {
     const uintptr_t a = reinterpret_cast<uintptr_t>(x) + static_cast<uintptr_t>(offset) * (BF16 ? 2 : 4);
     base = reinterpret_cast<const unsigned char*>(a & ~static_cast<uintptr_t>(15));
     shift = static_cast<int>(a & 15) / (BF16 ? 2 : 4);
-    count = (shift + vocab + kPer<BF16> - 1) / kPer<BF16>;
+    count = static_cast<unsigned>(shift + vocab + kPer<BF16> - 1) / kPer<BF16>;
   }
   __device__ __forceinline__ int first(int v) const { return v * kPer<BF16> - shift; }  // index of the vector's first entry
   __device__ __forceinline__ bool whole(int v) const { return first(v) >= 0 && first(v) + kPer<BF16> <= vocab; }
   // A vector at an end of the row from its entries; what lies outside counts as masked.
-  __device__ __forceinline__ uint4 end(int v) const {
+  __device__ __noinline__ uint4 end(int v) const {
     float x[kPer<BF16>];
 #pragma unroll
     for (int k = 0; k < kPer<BF16>; ++k) {
@@ -308,8 +350,9 @@ struct WarpTop {
   int n;
 };
 
-// The `top` first places of a row that a whole warp holds, into S.top; see
-// cta_top.  The groups are the lanes.
+// The `top` first places of a row that a whole warp holds, into S.top, found
+// as described at TopScratch with the lanes as groups; false where more
+// entries reach the bound than there is room for.
 template <bool BF16, int NV>
 __device__ __forceinline__ bool warp_top(const LogprobParams& P, const RowVectors<BF16>& R, const uint4 (&q)[NV], int lane,
                                          WarpTop& S) {
@@ -327,15 +370,18 @@ __device__ __forceinline__ bool warp_top(const LogprobParams& P, const RowVector
   __syncwarp();
 #pragma unroll
   for (int u = 0; u < NV; ++u) {
-    if (vec_max<BF16>(q[u]) < least) continue;
+    if (!__any_sync(0xFFFFFFFFu, vec_max<BF16>(q[u]) >= least)) continue;
     float x[kN];
     unpack<BF16>(q[u], x);
 #pragma unroll
     for (int k = 0; k < kN; ++k) {
       const int j = R.first(lane + 32 * u) + k;
-      if (j < 0 || j >= P.vocab || ordered(x[k]) < bound) continue;
-      const int i = atomicAdd(&S.n, 1);
-      if (i < kWarpCandidates) S.candidate[i] = place(x[k], j);
+      const unsigned m = __ballot_sync(0xFFFFFFFFu, j >= 0 && j < P.vocab && ordered(x[k]) >= bound);
+      const int i = S.n + __popc(m & ((1u << lane) - 1));
+      if ((m >> lane & 1) && i < kWarpCandidates) S.candidate[i] = place(x[k], j);
+      __syncwarp();
+      if (lane == 0) S.n += __popc(m);
+      __syncwarp();
     }
   }
   __syncwarp();
@@ -361,13 +407,11 @@ __global__ void __launch_bounds__(kWarpThreads, NV == 16 ? 2 : NV == 8 ? 3 : 4) 
   const int64_t target = in ? P.targets[row] : -1;
   const bool on = target >= 0;
   const RowVectors<BF16> R(P.x, in ? row * P.stride : 0, P.vocab);
-  const uint4 masked = make_uint4(BF16 ? 0xFF80FF80u : 0xFF800000u, BF16 ? 0xFF80FF80u : 0xFF800000u,
-                                  BF16 ? 0xFF80FF80u : 0xFF800000u, BF16 ? 0xFF80FF80u : 0xFF800000u);
   uint4 q[NV];
 #pragma unroll
   for (int u = 0; u < NV; ++u) {
     const int v = sub + P.lanes * u;
-    q[u] = masked;
+    q[u] = masked_vector<BF16>();
     if (!on || v >= R.count) continue;
     if (R.whole(v)) q[u] = *reinterpret_cast<const uint4*>(R.base + v * 16LL);
     else q[u] = R.end(v);
@@ -497,15 +541,11 @@ __device__ __forceinline__ float2 cta_sum2(float2 v, float2* scratch) {
   return v;
 }
 
-// What the CTAs of a cluster tell one another.
-struct Exchange {
-  Sums sums[kMaxCluster];
-  unsigned long long top[kMaxCluster][kMaxTop];
-};
-
+// The alternatives of the row at hand, or of a CTA's part of it.  Collected
+// are the entries that reach a bound; `top` at least of the row's entries do.
 template <int THREADS>
 struct TopScratch {
-  uint32_t group_max[128];
+  uint32_t group_max[kTopGroups];
   uint32_t bound;
   int n;
   unsigned long long candidate[kCandidates];
@@ -513,118 +553,239 @@ struct TopScratch {
   unsigned long long top[kMaxTop];
 };
 
-// The `top` first places among this CTA's entries, into S.top (0 where there
-// are fewer).  own_max: the thread's largest entry.  `each(least, f)` calls
-// f(value, index) for the thread's entries that are at least `least` (for
-// others too, if that is cheaper).
-//   bound: the top-th largest of 128 groups' maxima; at least `top` entries
-//   reach it, and seldom many more do.  Those are collected and ranked by
-//   counting.  Rows where more than kCandidates reach it (ties, masks that
-//   leave fewer than `top` entries) take one maximum after the other.
-template <int THREADS, typename E>
-__device__ __forceinline__ void cta_top(int top, float own_max, E each, TopScratch<THREADS>& S) {
-  const int t = threadIdx.x, lane = t & 31;
-  const uint32_t own = ordered(own_max);
-  uint32_t g = own;
+// The bound: the top-th largest of the maxima of kTopGroups groups of
+// threads, each over the entries it has seen (`own`).  Two barriers.
+template <int THREADS>
+__device__ __forceinline__ void top_bound(int top, float own, TopScratch<THREADS>& S) {
+  const int t = threadIdx.x;
+  uint32_t g = ordered(own);
 #pragma unroll
-  for (int d = 1; d < THREADS / 128; d *= 2) g = max(g, __shfl_xor_sync(0xFFFFFFFFu, g, d));
-  if (t % (THREADS / 128) == 0) S.group_max[t / (THREADS / 128)] = g;
+  for (int d = 1; d < THREADS / kTopGroups; d *= 2) g = max(g, __shfl_xor_sync(0xFFFFFFFFu, g, d));
+  if (t % (THREADS / kTopGroups) == 0) S.group_max[t / (THREADS / kTopGroups)] = g;
   if (t == 0) S.n = 0;
   if (t < kMaxTop) S.top[t] = 0;
   __syncthreads();
-  if (t < 32) {
-    uint32_t v[4];
+  if (t < kTopGroups) {
+    const uint32_t mine = S.group_max[t];
+    int rank = 0;  // equal ones by their number
+#pragma unroll 8
+    for (int j = 0; j < kTopGroups; j += 4) {
+      const uint4 o = *reinterpret_cast<const uint4*>(&S.group_max[j]);
+      rank += (o.x > mine || (o.x == mine && j < t)) + (o.y > mine || (o.y == mine && j + 1 < t)) +
+              (o.z > mine || (o.z == mine && j + 2 < t)) + (o.w > mine || (o.w == mine && j + 3 < t));
+    }
+    if (rank == top - 1) S.bound = mine;
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ void collect_one(bool on, float x, int j, int* n, unsigned long long* candidate) {
+  const unsigned m = __ballot_sync(0xFFFFFFFFu, on);
+  const int lane = threadIdx.x & 31;
+  int i = 0;
+  if (lane == 0) i = atomicAdd(n, __popc(m));
+  i = __shfl_sync(0xFFFFFFFFu, i, 0) + __popc(m & ((1u << lane) - 1));
+  if (on && i < kCandidates) candidate[i] = place(x, j);
+}
+
+// Collects from the vectors that the threads whose largest entry reaches the
+// bound have seen: the warp takes one such thread after the other and reads
+// its vectors again, a vector a lane, so that it never splits.  vector(i) is
+// vector i of the CTA's part, of which thread t has seen t, t + THREADS, ...
+template <bool BF16, int THREADS, typename V>
+__device__ __forceinline__ void collect_seen(float own, int n, int first, int vocab, V vector, TopScratch<THREADS>& S) {
+  constexpr int kN = kPer<BF16>;
+  const int lane = threadIdx.x & 31;
+  const uint32_t bound = S.bound;
+  const float least = place_value(static_cast<unsigned long long>(bound) << 32);
+  for (unsigned hits = __ballot_sync(0xFFFFFFFFu, ordered(own) >= bound); hits != 0; hits &= hits - 1) {
+    const int seen = (threadIdx.x & ~31) + __ffs(hits) - 1;  // the thread
+    for (int i0 = seen; i0 < n; i0 += 32 * THREADS) {
+      const int i = i0 + lane * THREADS;
+      const uint4 v = i < n ? vector(i) : masked_vector<BF16>();
+      const bool reach = i < n && !(vec_max<BF16>(v) < least);
+      if (!__any_sync(0xFFFFFFFFu, reach)) continue;
+      float x[kN];
+      unpack<BF16>(v, x);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = S.group_max[lane + 32 * k];
-    uint32_t bound = 0;
-    for (int q = 0; q < top; ++q) {
-      const uint32_t m = max(max(v[0], v[1]), max(v[2], v[3]));
-      bound = __reduce_max_sync(0xFFFFFFFFu, m);
-      if (lane == __ffs(__ballot_sync(0xFFFFFFFFu, m == bound)) - 1) {  // one group leaves
-        bool gone = false;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (!gone && v[k] == bound) v[k] = 0, gone = true;
+      for (int k = 0; k < kN; ++k) {
+        const int j = first + i * kN + k;
+        const bool on = reach && j >= 0 && j < vocab && ordered(x[k]) >= bound;
+        if (__any_sync(0xFFFFFFFFu, on)) collect_one(on, x[k], j, &S.n, S.candidate);
       }
     }
-    if (lane == 0) S.bound = bound;
   }
-  __syncthreads();
-  const uint32_t bound = S.bound;
-  if (own >= bound) {
-    each(place_value(static_cast<unsigned long long>(bound) << 32), [&](float x, int j) {
-      if (ordered(x) < bound) return;
-      const int i = atomicAdd(&S.n, 1);
-      if (i < kCandidates) S.candidate[i] = place(x, j);
-    });
-  }
-  __syncthreads();
-  const int n = S.n;
+}
+
+// Ranks what was collected by counting, into S.top (0 where there are fewer).
+// Where more was collected than there is room for (ties, masks that leave
+// fewer than `top` entries) it takes one maximum after the other of `x`, the
+// entries first .. last-1 of a row in global memory.
+template <bool BF16, int THREADS>
+__device__ __forceinline__ void top_rank(int top, const void* x, long long base, int first, int last, TopScratch<THREADS>& S) {
+  const int t = threadIdx.x, n = S.n;
   if (n <= kCandidates) {
     for (int i = t; i < n; i += THREADS) {
       const unsigned long long mine = S.candidate[i];
       int rank = 0;
+#pragma unroll 4
       for (int j = 0; j < n; ++j) rank += S.candidate[j] > mine;
       if (rank < top) S.top[rank] = mine;
     }
   } else {
-    unsigned long long last = ~0ull;
-    for (int q = 0; q < top; ++q) {
+    unsigned long long before = ~0ull;
+    for (int k = 0; k < top; ++k) {
       unsigned long long best = 0;
-      each(-INFINITY, [&](float x, int j) {
-        const unsigned long long v = place(x, j);
-        if (v < last && v > best) best = v;
-      });
+#pragma unroll 4
+      for (int j = first + t; j < last; j += THREADS) {
+        const unsigned long long v = place(at<BF16>(x, base + j), j);
+        if (v < before && v > best) best = v;
+      }
 #pragma unroll
       for (int d = 16; d > 0; d /= 2) {
         const unsigned long long o = __shfl_xor_sync(0xFFFFFFFFu, best, d);
         best = o > best ? o : best;
       }
-      if (lane == 0) S.best[t >> 5] = best;
+      if ((t & 31) == 0) S.best[t >> 5] = best;
       __syncthreads();
       for (int w = 0; w < THREADS / 32; ++w) best = S.best[w] > best ? S.best[w] : best;
-      if (t == 0) S.top[q] = best;
-      last = best;
+      if (t == 0) S.top[k] = best;
+      before = best;
       __syncthreads();
     }
   }
   __syncthreads();
 }
 
-template <bool BF16, int THREADS, int MODE>
-__global__ void __launch_bounds__(THREADS) logprob_row(const __grid_constant__ LogprobParams P) {
+// Sums of the entries first .. last-1 of a row in global memory against their
+// largest: where a nearer reference was too far off.
+template <bool BF16, int THREADS>
+__device__ __noinline__ Sums sums_again(const void* x, long long base, int first, int last, float c2, float* scratch, float2* pair_scratch) {
+  float m = -INFINITY;
+#pragma unroll 4
+  for (int j = first + static_cast<int>(threadIdx.x); j < last; j += THREADS) m = fmaxf(m, at<BF16>(x, base + j));
+  Sums a{};
+  a.m = cta_reduce<THREADS>(m, [](float p, float q) { return fmaxf(p, q); }, scratch);
+  float2 s{}, w{};
+#pragma unroll 2
+  for (int j = first + static_cast<int>(threadIdx.x); j < last; j += 2 * THREADS) {
+    const float v[2] = {at<BF16>(x, base + j), j + THREADS < last ? at<BF16>(x, base + j + THREADS) : -INFINITY};
+    accumulate(s, w, v, reference(a.m), c2);
+  }
+  const float2 sums = cta_sum2<THREADS>(make_float2(s.x + s.y, w.x + w.y), pair_scratch);
+  a.s = sums.x;
+  a.w = sums.y;
+  return a;
+}
+
+// What the CTAs of a cluster tell one another.  Sums of one row are read while
+// the next row's are written.
+struct Exchange {
+  Sums sums[2][kMaxCluster];
+  unsigned long long top[kMaxCluster][kMaxTop];
+};
+
+// One CTA's part of a row: vectors v0 .. v0+n-1, `per` of each of four groups.
+template <bool BF16>
+struct RowPart {
+  const unsigned char* src;  // vector v0
+  int shift, v0, n, per;
+  int lo, wholes;            // the row's whole vectors: lo .. lo+wholes-1
+  __device__ __forceinline__ int first(int i) const { return (v0 + i) * kPer<BF16> - shift; }
+  __device__ __forceinline__ bool whole(int i) const { return static_cast<unsigned>(v0 + i - lo) < static_cast<unsigned>(wholes); }
+};
+
+template <bool BF16, int THREADS>
+__device__ __forceinline__ RowPart<BF16> part_of(const LogprobParams& P, long long row, int rank) {
+  const RowVectors<BF16> R(P.x, row * P.stride, P.vocab);
+  RowPart<BF16> p;
+  // fewer than 2^17 vectors and a power of two of CTAs: no division
+  p.v0 = static_cast<int>(static_cast<unsigned>(R.count * rank) >> P.log_ranks);
+  p.n = static_cast<int>(static_cast<unsigned>(R.count * (rank + 1)) >> P.log_ranks) - p.v0;
+  p.per = static_cast<unsigned>(p.n + 4 * THREADS - 1) / (4 * THREADS) * THREADS;
+  p.src = R.base + p.v0 * 16LL;
+  p.shift = R.shift;
+  p.lo = R.shift > 0 ? 1 : 0;
+  p.wholes = static_cast<unsigned>(R.shift + P.vocab) / kPer<BF16> - p.lo;
+  return p;
+}
+
+// A cluster takes one row after the other (persistent).  A CTA's part of a
+// row lies in its shared memory as vectors in four groups; a thread's vectors
+// are the ones it copies, so it works on a group without waiting for other
+// threads, and copies the next row's group as soon as it is done with one:
+// the loads go on while sums are exchanged and alternatives ranked.
+template <bool BF16, int THREADS, bool TOP>
+__global__ void __launch_bounds__(THREADS, THREADS == 128 ? 8 : 3) logprob_loss(const __grid_constant__ LogprobParams P) {
   extern __shared__ __align__(16) unsigned char segment[];
   __shared__ float scratch[2][THREADS / 32];
   __shared__ float2 pair_scratch[2][THREADS / 32];
   __shared__ Exchange X;
-  __shared__ TopScratch<THREADS> S;
+  __shared__ __align__(16) TopScratch<TOP ? THREADS : 32> S;
   constexpr int kN = kPer<BF16>;
   const cg::cluster_group cluster = cg::this_cluster();
-  const int ranks = cluster.num_blocks(), rank = cluster.block_rank();
+  const int ranks = 1 << P.log_ranks, rank = blockIdx.x & (ranks - 1);
   const int t = threadIdx.x;
-  const long long row = blockIdx.x / ranks;
-  const int64_t target = P.targets[row];
-  const RowVectors<BF16> R(P.x, row * P.stride, P.vocab);
-  const int v0 = static_cast<int>(static_cast<long long>(R.count) * rank / ranks);
-  const int n = static_cast<int>(static_cast<long long>(R.count) * (rank + 1) / ranks) - v0;
+  const long long clusters = gridDim.x >> P.log_ranks;
   uint4* const q = reinterpret_cast<uint4*>(segment);
-  const long long out = row * P.grad_stride;
-  // the gradient's vectors begin where the row's do
-  const bool same = MODE == kLoss && RowVectors<BF16>(P.grad, out, P.vocab).shift == R.shift;
+  const float c2 = P.scale * kLog2e;
+  auto largest = [](float x, float y) { return fmaxf(x, y); };
 
-  if (target < 0) {  // every CTA of the cluster returns
-    if (rank == 0 && t == 0) P.logprobs[row] = P.lse[row] = P.entropy[row] = 0.0f;
-    if (rank == 0 && t < P.top) P.top_logprobs[row * P.top + t] = 0.0f, P.top_ids[row * P.top + t] = -1;
-    if constexpr (MODE == kLoss) {
-      const int j0 = max(0, R.first(v0)), j1 = min(P.vocab, R.first(v0 + n));
+  // one group of copies, empty past the last row and for rows that are left out
+  auto copy = [&](const RowPart<BF16>& p, bool on, int group) {
+    if (on) {
+      const int end = min(p.n, (group + 1) * p.per);
+      int i = group * p.per + t;
+      const unsigned char* src = p.src + i * 16LL;
+      unsigned dst = static_cast<unsigned>(__cvta_generic_to_shared(q + i));
+      for (; i < end; i += THREADS, src += THREADS * 16, dst += THREADS * 16) {
+        if (p.whole(i)) {
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+        } else {  // an end of the row; what lies outside counts as masked
+          float x[kN];
+#pragma unroll
+          for (int k = 0; k < kN; ++k) {
+            const int j = p.first(i) + k;
+            x[k] = j >= 0 && j < P.vocab ? at<BF16>(src, k) : -INFINITY;
+          }
+          q[i] = pack<BF16>(x);
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+
+  long long row = blockIdx.x >> P.log_ranks;
+  int64_t target = P.targets[row];
+  RowPart<BF16> p = part_of<BF16, THREADS>(P, row, rank);
+  // a CTA's shared memory is written by others only once it has begun
+  if (ranks > 1) cg::cluster_group::barrier_arrive();
+#pragma unroll 1
+  for (int g = 0; g < 4; ++g) copy(p, target >= 0, g);
+  if (ranks > 1) cg::cluster_group::barrier_wait();
+
+  for (int turn = 0; row < P.rows; turn ^= 1) {
+    const long long next = row + clusters;
+    const int64_t next_target = next < P.rows ? P.targets[next] : -1;
+    const bool next_on = next_target >= 0;
+    const RowPart<BF16> np = part_of<BF16, THREADS>(P, next_on ? next : row, rank);
+    const long long base = row * P.stride, out = row * P.grad_stride;
+    const int j0 = max(0, p.first(0)), j1 = min(P.vocab, p.first(p.n));  // this CTA's entries
+    // the gradient's vectors begin where the row's do
+    const RowVectors<BF16> O(P.grad, out, P.vocab);
+    const bool same = O.shift == p.shift;
+    uint4* const o = reinterpret_cast<uint4*>(const_cast<unsigned char*>(O.base)) + p.v0;
+
+    if (target < 0) {
+      if (rank == 0 && t == 0) P.logprobs[row] = P.lse[row] = P.entropy[row] = 0.0f;
+      if (TOP && rank == 0 && t < P.top) P.top_logprobs[row * P.top + t] = 0.0f, P.top_ids[row * P.top + t] = -1;
       if (same) {
-        uint4* const o = reinterpret_cast<uint4*>(const_cast<unsigned char*>(RowVectors<BF16>(P.grad, out, P.vocab).base));
-        for (int i = t; i < n; i += THREADS) {
-          if (R.whole(v0 + i)) {
-            o[v0 + i] = make_uint4(0, 0, 0, 0);
+        for (int i = t; i < p.n; i += THREADS) {
+          if (p.whole(i)) {
+            o[i] = make_uint4(0, 0, 0, 0);
           } else {
             for (int k = 0; k < kN; ++k) {
-              const int j = R.first(v0 + i) + k;
+              const int j = p.first(i) + k;
               if (j >= 0 && j < P.vocab) put<BF16>(P.grad, out + j, 0.0f);
             }
           }
@@ -632,183 +793,247 @@ __global__ void __launch_bounds__(THREADS) logprob_row(const __grid_constant__ L
       } else {
         for (int j = j0 + t; j < j1; j += THREADS) put<BF16>(P.grad, out + j, 0.0f);
       }
+#pragma unroll 1
+      for (int g = 0; g < 4; ++g) copy(np, next_on, g);
+      row = next;
+      target = next_target;
+      p = np;
+      continue;
     }
-    return;
-  }
 
-  // a CTA's shared memory is written by others only once it has begun
-  if (ranks > 1) cg::cluster_group::barrier_arrive();
-  // four groups of copies; a thread's vectors are the ones it copies, so it
-  // adds a group up without waiting for other threads
-  const int lo = R.shift > 0 ? 1 : 0, wholes = (R.shift + P.vocab) / kN - lo;  // vectors inside the row
-  const int per = (n + 4 * THREADS - 1) / (4 * THREADS) * THREADS;
-#pragma unroll
-  for (int group = 0; group < 4; ++group) {
-    const int end = min(n, (group + 1) * per);
-    const unsigned char* src = R.base + static_cast<long long>(v0 + group * per + t) * 16;
-    for (int i = group * per + t; i < end; i += THREADS, src += THREADS * 16) {
-      if (static_cast<unsigned>(v0 + i - lo) < static_cast<unsigned>(wholes)) {
-        const unsigned dst = static_cast<unsigned>(__cvta_generic_to_shared(q + i));
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-      } else {
-        q[i] = R.end(v0 + i);
-      }
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  }
-  float x_target = 0.0f;
-  if (t == 0 && rank == 0 && target < P.vocab) x_target = at<BF16>(P.x, row * P.stride + target);
+    float x_target = 0.0f;
+    if (t == 0 && rank == 0 && target < P.vocab) x_target = at<BF16>(P.x, base + target);
 
-  // Sums against the largest of the first vectors, which is near enough to
-  // the row's largest entry unless S says otherwise.
-  const float c2 = P.scale * kLog2e;
-  auto largest = [](float x, float y) { return fmaxf(x, y); };
-  float own_max = -INFINITY;
-  float2 s{}, w{};
-  Sums a{0.0f, 0.0f, 0.0f};
-  auto group_sums = [&](int group) {
-    const int end = min(n, (group + 1) * per);
+    // Sums against the largest of the first vectors, which is near enough to
+    // the row's largest entry unless S says otherwise.
+    float2 s{}, w{};
+    Sums a{};
+    float own = -INFINITY;
+    asm volatile("cp.async.wait_group 3;" ::: "memory");
+    a.m = reference(cta_reduce<THREADS>(t < p.n ? vec_max<BF16>(q[t]) : -INFINITY, largest, scratch[turn]));
+    // three newer groups at any time: this row's, then empty ones
+#pragma unroll 1
+    for (int group = 0; group < 4; ++group) {
+      asm volatile("cp.async.wait_group 3;" ::: "memory");
+      const int end = min(p.n, (group + 1) * p.per);
 #pragma unroll 2
-    for (int i = group * per + t; i < end; i += THREADS) {
-      const uint4 v = q[i];
-      if (P.top > 0) own_max = fmaxf(own_max, vec_max<BF16>(v));
-      float x[kN];
-      unpack<BF16>(v, x);
-      accumulate(s, w, x, reference(a.m), c2);
+      for (int i = group * p.per + t; i < end; i += THREADS) {
+        const uint4 v = q[i];
+        if (TOP) own = fmaxf(own, vec_max<BF16>(v));
+        accumulate_near<BF16>(s, w, v, a.m, c2);
+      }
+      copy(np, false, group);
     }
-  };
-  asm volatile("cp.async.wait_group 3;" ::: "memory");
-  a.m = cta_reduce<THREADS>(t < n ? vec_max<BF16>(q[t]) : -INFINITY, largest, scratch[0]);
-  group_sums(0);
-  asm volatile("cp.async.wait_group 2;" ::: "memory");
-  group_sums(1);
-  asm volatile("cp.async.wait_group 1;" ::: "memory");
-  group_sums(2);
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
-  group_sums(3);
-  float2 sums = cta_sum2<THREADS>(make_float2(s.x + s.y, w.x + w.y), pair_scratch[0]);
-  if (!(sums.x >= 0.5f && sums.x < 0x1p60f)) {  // again, against the row's own largest entry
-    float m = -INFINITY;
-    for (int i = t; i < n; i += THREADS) m = fmaxf(m, vec_max<BF16>(q[i]));
-    a.m = cta_reduce<THREADS>(m, largest, scratch[1]);
-    s = w = make_float2(0.0f, 0.0f);
-    for (int group = 0; group < 4; ++group) group_sums(group);
-    sums = cta_sum2<THREADS>(make_float2(s.x + s.y, w.x + w.y), pair_scratch[1]);
-  }
-  a.s = sums.x;
-  a.w = sums.y;
-  if (ranks > 1) {
-    cg::cluster_group::barrier_wait();
-    if (t < ranks) cluster.map_shared_rank(&X, t)->sums[rank] = a;
-    cluster.sync();
-    a = X.sums[0];
-    for (int k = 1; k < ranks; ++k) a = merge(a, X.sums[k], c2);
-  }
-  const RowStats r = stats_of(a, P.scale);
-  if (rank == 0 && t == 0) {
-    P.lse[row] = r.lse;
-    P.entropy[row] = r.entropy;
-    P.logprobs[row] = target < P.vocab ? logprob_of(r, x_target, P.scale) : NAN;
-  }
+    const float2 sums = cta_sum2<THREADS>(make_float2(s.x + s.y, w.x + w.y), pair_scratch[turn]);
+    a.s = sums.x;
+    a.w = sums.y;
+    if (!(a.s >= 0.5f && a.s < 0x1p60f)) {
+      __syncthreads();  // the scratch arrays have been read
+      a = sums_again<BF16, THREADS>(P.x, base, j0, j1, c2, scratch[turn], pair_scratch[turn]);
+    }
+    if (ranks > 1) {
+      if (t < ranks) cluster.map_shared_rank(&X, t)->sums[turn][rank] = a;
+      cluster.sync();
+    }
+    if (ranks > 1) {
+      a = X.sums[turn][0];
+      for (int k = 1; k < ranks; ++k) a = merge(a, X.sums[turn][k], c2);
+    }
+    const RowStats r = stats_of(a, P.scale);
+    if (rank == 0 && t == 0) {
+      P.lse[row] = r.lse;
+      P.entropy[row] = r.entropy;
+      P.logprobs[row] = target < P.vocab ? logprob_of(r, x_target, P.scale) : NAN;
+    }
+    if constexpr (TOP) {
+      top_bound(P.top, own, S);
+      collect_seen<BF16, THREADS>(own, p.n, p.first(0), P.vocab, [&](int i) { return q[i]; }, S);
+      __syncthreads();
+      top_rank<BF16, THREADS>(P.top, P.x, base, j0, j1, S);
+      if (ranks > 1) {
+        if (t < P.top) cluster.map_shared_rank(&X, 0)->top[rank][t] = S.top[t];
+        cluster.sync();
+        if (rank == 0) {
+          const int all = ranks * P.top;
+          for (int i = t; i < all; i += THREADS) {
+            const unsigned long long mine = X.top[i / P.top][i % P.top];
+            int place_ = 0;
+            for (int j = 0; j < all; ++j) place_ += X.top[j / P.top][j % P.top] > mine;
+            if (mine != 0 && place_ < P.top) S.top[place_] = mine;
+          }
+          __syncthreads();
+        }
+      }
+      if (rank == 0 && t < P.top) {
+        P.top_ids[row * P.top + t] = place_index(S.top[t]);
+        P.top_logprobs[row * P.top + t] = logprob_of(r, place_value(S.top[t]), P.scale);
+      }
+      __syncthreads();  // S is free for the next row
+    }
 
-  if constexpr (MODE == kLoss) {
     const RowGrad g = grad_of(P, r, row, target);
     if (same) {
-      uint4* const o = reinterpret_cast<uint4*>(const_cast<unsigned char*>(RowVectors<BF16>(P.grad, out, P.vocab).base));
-      for (int i = t; i < n; i += THREADS) {
-        const int j = R.first(v0 + i);
-        float x[kN];
-        unpack<BF16>(q[i], x);
-        grad_entries(g, P.scale, target, j, x);
-        if (static_cast<unsigned>(v0 + i - lo) < static_cast<unsigned>(wholes)) {
-          o[v0 + i] = pack<BF16>(x);
-        } else {
-          for (int k = 0; k < kN; ++k)
-            if (j + k >= 0 && j + k < P.vocab) put<BF16>(P.grad, out + j + k, x[k]);
+#pragma unroll 1
+      for (int group = 0; group < 4; ++group) {
+        const int end = min(p.n, (group + 1) * p.per);
+#pragma unroll 2
+        for (int i = group * p.per + t; i < end; i += THREADS) {
+          const int j = p.first(i);
+          float x[kN];
+          unpack<BF16>(q[i], x);
+          grad_entries(g, P.scale, target, j, x);
+          if (p.whole(i)) {
+            o[i] = pack<BF16>(x);
+          } else {
+            for (int k = 0; k < kN; ++k)
+              if (j + k >= 0 && j + k < P.vocab) put<BF16>(P.grad, out + j + k, x[k]);
+          }
         }
+        copy(np, next_on, group);
       }
-    } else {
-      const int j0 = max(0, R.first(v0)), j1 = min(P.vocab, R.first(v0 + n)), from = R.first(v0);
+    } else {  // entry by entry, whichever thread copied it
+      const int from = p.first(0);
+#pragma unroll 4
       for (int j = j0 + t; j < j1; j += THREADS)
         put<BF16>(P.grad, out + j, grad_entry(g, P.scale, target, j, at<BF16>(segment, j - from)));
+      __syncthreads();
+#pragma unroll 1
+      for (int group = 0; group < 4; ++group) copy(np, next_on, group);
+    }
+    row = next;
+    target = next_target;
+    p = np;
+  }
+  // others may still write this CTA's sums or alternatives
+  if (ranks > 1) cluster.sync();
+}
+
+// ------------------------------------------------- scores of long rows (CTAs)
+
+// One row per CTA, or per cluster where rows are few.  The logits pass through
+// registers, two batches of four vectors a thread; four CTAs of an SM overlap
+// one's loads with another's reductions.  Each warp adds up against the
+// largest entry of its own first batch.
+template <bool BF16, bool TOP>
+__global__ void __launch_bounds__(kScoreThreads, 4) logprob_score(const __grid_constant__ LogprobParams P) {
+  constexpr int kWarps = kScoreThreads / 32, kU = 4, kBatch = kU * kScoreThreads;
+  __shared__ Sums warp_sums[kWarps];
+  __shared__ float scratch[kWarps];
+  __shared__ float2 pair_scratch[kWarps];
+  __shared__ Exchange X;
+  __shared__ __align__(16) TopScratch<TOP ? kScoreThreads : 32> S;
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int ranks = 1 << P.log_ranks, rank = blockIdx.x & (ranks - 1);
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const long long row = blockIdx.x >> P.log_ranks, base = row * P.stride;
+  const int64_t target = P.targets[row];
+  if (target < 0) {  // every CTA of the cluster returns
+    if (rank == 0 && t == 0) P.logprobs[row] = P.lse[row] = P.entropy[row] = 0.0f;
+    if (TOP && rank == 0 && t < P.top) P.top_logprobs[row * P.top + t] = 0.0f, P.top_ids[row * P.top + t] = -1;
+    return;
+  }
+  // a CTA's shared memory is written by others only once it has begun
+  if (ranks > 1) cg::cluster_group::barrier_arrive();
+  const RowPart<BF16> p = part_of<BF16, kScoreThreads>(P, row, rank);
+  const uint4* const src = reinterpret_cast<const uint4*>(p.src);
+  const float c2 = P.scale * kLog2e;
+  auto vector = [&](int i) {  // an end of the row is put together from its entries
+    if (p.whole(i)) return load_once(src + i);
+    return RowVectors<BF16>(P.x, base, P.vocab).end(p.v0 + i);
+  };
+  uint4 a[kU], b[kU];
+#pragma unroll
+  for (int u = 0; u < kU; ++u) a[u] = t + u * kScoreThreads < p.n ? vector(t + u * kScoreThreads) : masked_vector<BF16>();
+  float x_target = 0.0f;
+  if (t == 0 && rank == 0 && target < P.vocab) x_target = at<BF16>(P.x, base + target);
+  float own = -INFINITY;
+#pragma unroll
+  for (int u = 0; u < kU; ++u) own = fmaxf(own, vec_max<BF16>(a[u]));
+  Sums sums{};
+  sums.m = own;
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) sums.m = fmaxf(sums.m, __shfl_xor_sync(0xFFFFFFFFu, sums.m, d));
+  float2 s{}, w{};
+  bool found = sums.m != -INFINITY;
+  for (int i = t; i - t < p.n; i += kBatch) {
+    if (!found) {  // masked entries alone so far
+#pragma unroll
+      for (int u = 0; u < kU; ++u) sums.m = i + u * kScoreThreads < p.n ? fmaxf(sums.m, vec_max<BF16>(a[u])) : sums.m;
+#pragma unroll
+      for (int d = 16; d > 0; d /= 2) sums.m = fmaxf(sums.m, __shfl_xor_sync(0xFFFFFFFFu, sums.m, d));
+      found = sums.m != -INFINITY;
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int k = i + kBatch + u * kScoreThreads;
+      if (k < p.n) b[u] = vector(k);
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      if (i + u * kScoreThreads < p.n) {
+        if (TOP) own = fmaxf(own, vec_max<BF16>(a[u]));
+        accumulate_near<BF16>(s, w, a[u], reference(sums.m), c2);
+      }
+      a[u] = b[u];
     }
   }
-
-  if (P.top > 0) {
-    cta_top<THREADS>(P.top, own_max, [&](float least, auto f) {
-      for (int i = t; i < n; i += THREADS) {
-        if (vec_max<BF16>(q[i]) < least) continue;
-        float x[kN];
-        unpack<BF16>(q[i], x);
+  sums.s = s.x + s.y;
+  sums.w = w.x + w.y;
 #pragma unroll
-        for (int k = 0; k < kN; ++k) {
-          const int j = R.first(v0 + i) + k;
-          if (j >= 0 && j < P.vocab) f(x[k], j);
-        }
-      }
-    }, S);
-    unsigned long long mine = 0;
-    if (ranks > 1) {
-      if (t < P.top) cluster.map_shared_rank(&X, 0)->top[rank][t] = S.top[t];
-      cluster.sync();
-      if (rank != 0) return;
+  for (int d = 16; d > 0; d /= 2) {
+    sums.s += __shfl_xor_sync(0xFFFFFFFFu, sums.s, d);
+    sums.w += __shfl_xor_sync(0xFFFFFFFFu, sums.w, d);
+  }
+  // A warp that saw masked entries alone has m = -inf and no sum; any other sum
+  // out of range means that its reference was too far off.
+  if (lane == 0) warp_sums[warp] = sums;
+  if constexpr (TOP) top_bound(P.top, own, S);
+  else __syncthreads();
+  bool far = false;
+#pragma unroll
+  for (int k = 0; k < kWarps; ++k)
+    far |= !(warp_sums[k].s >= 0.5f && warp_sums[k].s < 0x1p60f) && !(warp_sums[k].s == 0.0f && warp_sums[k].m == -INFINITY);
+  if (far) {
+    sums = sums_again<BF16, kScoreThreads>(P.x, base, max(0, p.first(0)), min(P.vocab, p.first(p.n)), c2, scratch, pair_scratch);
+  } else if (warp == 0) {
+    sums = warp_sums[0];
+#pragma unroll
+    for (int k = 1; k < kWarps; ++k) sums = merge(sums, warp_sums[k], c2);
+  }
+  if constexpr (TOP) {
+    collect_seen<BF16, kScoreThreads>(own, p.n, p.first(0), P.vocab, vector, S);
+    __syncthreads();
+    top_rank<BF16, kScoreThreads>(P.top, P.x, base, max(0, p.first(0)), min(P.vocab, p.first(p.n)), S);
+  }
+  if (ranks > 1) {
+    cg::cluster_group::barrier_wait();
+    if (t == 0) cluster.map_shared_rank(&X, 0)->sums[0][rank] = sums;
+    if (TOP && t < P.top) cluster.map_shared_rank(&X, 0)->top[rank][t] = S.top[t];
+    cluster.sync();
+    if (rank != 0) return;
+    if (warp == 0) {
+      sums = X.sums[0][0];
+      for (int k = 1; k < ranks; ++k) sums = merge(sums, X.sums[0][k], c2);
+    }
+    if constexpr (TOP) {
       const int all = ranks * P.top;
-      for (int i = t; i < all; i += THREADS) {
-        mine = X.top[i / P.top][i % P.top];
+      for (int i = t; i < all; i += kScoreThreads) {
+        const unsigned long long mine = X.top[i / P.top][i % P.top];
         int place_ = 0;
         for (int j = 0; j < all; ++j) place_ += X.top[j / P.top][j % P.top] > mine;
         if (mine != 0 && place_ < P.top) S.top[place_] = mine;
       }
       __syncthreads();
     }
-    if (t < P.top) {
-      P.top_ids[row * P.top + t] = place_index(S.top[t]);
-      P.top_logprobs[row * P.top + t] = logprob_of(r, place_value(S.top[t]), P.scale);
-    }
   }
-}
-
-// --------------------------------------------------- rows of any length (CTA)
-
-template <bool BF16>
-__global__ void __launch_bounds__(kStreamThreads) logprob_stream(const __grid_constant__ LogprobParams P) {
-  __shared__ float scratch[kStreamThreads / 32];
-  __shared__ float2 pair_scratch[kStreamThreads / 32];
-  __shared__ TopScratch<kStreamThreads> S;
-  const long long row = blockIdx.x, base = row * P.stride;
-  const int64_t target = P.targets[row];
-  const int t = threadIdx.x;
-  if (target < 0) {
-    if (t == 0) P.logprobs[row] = P.lse[row] = P.entropy[row] = 0.0f;
-    if (t < P.top) P.top_logprobs[row * P.top + t] = 0.0f, P.top_ids[row * P.top + t] = -1;
-    return;
-  }
-  const float c2 = P.scale * kLog2e;
-  float own_max = -INFINITY;
-#pragma unroll 8
-  for (int j = t; j < P.vocab; j += kStreamThreads) own_max = fmaxf(own_max, at<BF16>(P.x, base + j));
-  Sums a{0.0f, 0.0f, 0.0f};
-  a.m = cta_reduce<kStreamThreads>(own_max, [](float x, float y) { return fmaxf(x, y); }, scratch);
-  float2 s{}, w{};
-#pragma unroll 4
-  for (int j = t; j < P.vocab; j += 2 * kStreamThreads) {
-    const float x[2] = {at<BF16>(P.x, base + j), j + kStreamThreads < P.vocab ? at<BF16>(P.x, base + j + kStreamThreads) : -INFINITY};
-    accumulate(s, w, x, reference(a.m), c2);
-  }
-  const float2 sums = cta_sum2<kStreamThreads>(make_float2(s.x + s.y, w.x + w.y), pair_scratch);
-  a.s = sums.x;
-  a.w = sums.y;
-  const RowStats r = stats_of(a, P.scale);
+  if (warp != 0) return;
+  const RowStats r = stats_of(sums, P.scale);
   if (t == 0) {
     P.lse[row] = r.lse;
     P.entropy[row] = r.entropy;
-    P.logprobs[row] = target < P.vocab ? logprob_of(r, at<BF16>(P.x, base + target), P.scale) : NAN;
+    P.logprobs[row] = target < P.vocab ? logprob_of(r, x_target, P.scale) : NAN;
   }
-  if (P.top == 0) return;
-  cta_top<kStreamThreads>(P.top, own_max, [&](float, auto f) {
-    for (int j = t; j < P.vocab; j += kStreamThreads) f(at<BF16>(P.x, base + j), j);
-  }, S);
-  if (t < P.top) {
+  if (TOP && t < P.top) {
     P.top_ids[row * P.top + t] = place_index(S.top[t]);
     P.top_logprobs[row * P.top + t] = logprob_of(r, place_value(S.top[t]), P.scale);
   }
@@ -912,36 +1137,60 @@ const KernelPtr kWarpKernels[30] = {WARPS(false, kScore), WARPS(false, kLoss), W
                                     WARPS(true, kScore),  WARPS(true, kLoss),  WARPS(true, kBackward)};
 #undef WARPS
 
-// Index: 512 threads | loss << 1 | bfloat16 << 2.
-const KernelPtr kRowKernels[8] = {
-    logprob_row<false, 256, kScore>, logprob_row<false, 512, kScore>, logprob_row<false, 256, kLoss>,
-    logprob_row<false, 512, kLoss>,  logprob_row<true, 256, kScore>,  logprob_row<true, 512, kScore>,
-    logprob_row<true, 256, kLoss>,   logprob_row<true, 512, kLoss>,
+// Index: 256 threads | alternatives << 1 | bfloat16 << 2.
+const KernelPtr kLossKernels[8] = {
+    logprob_loss<false, 128, false>, logprob_loss<false, 256, false>, logprob_loss<false, 128, true>,
+    logprob_loss<false, 256, true>,  logprob_loss<true, 128, false>,  logprob_loss<true, 256, false>,
+    logprob_loss<true, 128, true>,   logprob_loss<true, 256, true>,
 };
 
-cudaError_t launch_rows(const LogprobParams& P, bool bf16, bool loss, long long bytes, int sms, cudaStream_t stream) {
-  int ranks = 1;
-  while (bytes > static_cast<long long>(ranks) * kSegmentBytes) ranks *= 2;
-  // few rows: spread each over more CTAs while every one keeps 4 KB and the GPU has SMs to spare
-  while (ranks < kMaxCluster && P.rows * ranks * 2 <= 2LL * sms && bytes / (ranks * 2) >= 4096) ranks *= 2;
-  const long long part = (bytes + 15) / 16 / ranks + 1;  // vectors
-  const bool wide = part > 2048;                         // 32 KB: 256 threads take eight vectors each
-  const KernelPtr f = kRowKernels[(wide ? 1 : 0) | (loss ? 2 : 0) | (bf16 ? 4 : 0)];
-  const size_t smem = static_cast<size_t>(part) * 16;
-  cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(f), cudaFuncAttributeMaxDynamicSharedMemorySize, kSegmentBytes + 64);
-  if (e != cudaSuccess) return e;
+// Index: alternatives | bfloat16 << 1.
+const KernelPtr kScoreKernels[4] = {logprob_score<false, false>, logprob_score<false, true>, logprob_score<true, false>,
+                                    logprob_score<true, true>};
+
+cudaError_t launch_clusters(KernelPtr f, const LogprobParams& P, long long clusters, int threads, size_t smem, cudaStream_t stream) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(P.rows * ranks));
-  cfg.blockDim = dim3(wide ? 512 : 256);
+  cfg.gridDim = dim3(static_cast<unsigned>(clusters << P.log_ranks));
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(ranks);
+  attr[0].val.clusterDim.x = 1u << P.log_ranks;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, f, P);
+}
+
+// CTAs per row: at least `ranks`; where rows are few more, while every one
+// keeps 4 KB of the row and the GPU has room for them.
+int spread(int ranks, long long rows, long long bytes, int sms) {
+  while (ranks < kMaxCluster && rows * ranks * 2 <= 2LL * sms && bytes / (ranks * 2) >= 4096) ranks *= 2;
+  return ranks;
+}
+
+cudaError_t launch_score(LogprobParams P, bool bf16, long long bytes, int sms, cudaStream_t stream) {
+  const int ranks = spread(1, P.rows, bytes, sms);
+  while (1 << P.log_ranks < ranks) ++P.log_ranks;
+  return launch_clusters(kScoreKernels[(P.top > 0 ? 1 : 0) | (bf16 ? 2 : 0)], P, P.rows, kScoreThreads, 0, stream);
+}
+
+cudaError_t launch_loss(LogprobParams P, bool bf16, long long bytes, int sms, cudaStream_t stream) {
+  int ranks = 1;
+  while (bytes > static_cast<long long>(ranks) * kSegmentBytes) ranks *= 2;
+  ranks = spread(ranks, P.rows, bytes, sms);
+  while (1 << P.log_ranks < ranks) ++P.log_ranks;
+  const long long part = (bytes + 15) / 16 / ranks + 1;  // vectors
+  const bool wide = part > 2048;                         // 32 KB: 256 threads take eight vectors each
+  const KernelPtr f = kLossKernels[(wide ? 1 : 0) | (P.top > 0 ? 2 : 0) | (bf16 ? 4 : 0)];
+  const size_t smem = static_cast<size_t>(part) * 16;
+  const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(f), cudaFuncAttributeMaxDynamicSharedMemorySize, kSegmentBytes + 64);
+  if (e != cudaSuccess) return e;
+  // as many clusters as are resident at a time (more would only wait)
+  const long long per_sm = std::min<long long>(wide ? 3 : 8, (228 * 1024) / (smem + kLossStatic));
+  const long long resident = std::max<long long>(1, per_sm * sms / ranks);
+  return launch_clusters(f, P, std::min<long long>(P.rows, resident), wide ? 256 : 128, smem, stream);
 }
 
 // What both directions check and launch; grad, gl: null for a score alone,
@@ -967,7 +1216,7 @@ muon_status_t run(const void* logits, int dtype, int64_t rows, int64_t vocab, in
   const bool held = bytes <= static_cast<int64_t>(kMaxCluster) * kSegmentBytes;
   const int64_t per_cta = 16 * kGradThreads * kGradVecs, chunks = (bytes + per_cta - 1) / per_cta;
   const int64_t vecs = (bytes - 2) / 16;   // at most: rows begin anywhere
-  if (vecs > kWarpVecs && rows > INT32_MAX / std::max<int64_t>(kMaxCluster, chunks)) return MUON_ERR_TOO_LARGE;
+  if (vecs > kWarpVecs && rows > INT32_MAX / chunks) return MUON_ERR_TOO_LARGE;
   const uint64_t r = static_cast<uint64_t>(rows);
   try {
     std::vector<Span> v = {span_of(targets, r * 8, false)};
@@ -1023,12 +1272,8 @@ muon_status_t run(const void* logits, int dtype, int64_t rows, int64_t vocab, in
     kWarpKernels[k + 5 * mode + (bf16 ? 15 : 0)]<<<grid, kWarpThreads, 0, str>>>(P);
     err = cudaGetLastError();
   } else {
-    if (score && held) {
-      err = launch_rows(P, bf16, backward, bytes, sms, str);
-    } else if (score) {
-      (bf16 ? logprob_stream<true> : logprob_stream<false>)<<<static_cast<unsigned>(rows), kStreamThreads, 0, str>>>(P);
-      err = cudaGetLastError();
-    }
+    if (score && backward && held) err = launch_loss(P, bf16, bytes, sms, str);
+    else if (score) err = launch_score(P, bf16, bytes, sms, str);
     if (err == cudaSuccess && backward && !(score && held)) {
       P.chunks = static_cast<int>(chunks);
       (bf16 ? logprob_grad<true> : logprob_grad<false>)<<<static_cast<unsigned>(rows * P.chunks), kGradThreads, 0, str>>>(P);
