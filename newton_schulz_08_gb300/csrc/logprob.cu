@@ -46,9 +46,11 @@ constexpr int kSegmentBytes = 104 * 1024; // of a row in one CTA's shared memory
 constexpr int kGradThreads = 256;
 constexpr int kGradVecs = 4;              // 16-byte vectors per thread of logprob_grad
 constexpr int kScoreThreads = 256;
-constexpr int kCandidates = 512;
-constexpr int kTopGroups = 128;
-constexpr int kLossStatic = 10 * 1024;     // shared memory of a logprob_loss CTA beside its part of the row, at most
+constexpr int kCandidates = 256;
+constexpr int kHits = 256;
+constexpr int kScoreChunks = 16;
+constexpr int kTopGroups = 64;
+constexpr int kLossStatic = 12 * 1024;    // shared memory of a logprob_loss CTA beside its part of the row, at most
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kFloor = -1000.0f;        // least exponent
@@ -133,19 +135,35 @@ __device__ __forceinline__ uint4 masked_vector() {
   return make_uint4(w, w, w, w);
 }
 
-// Largest entry of a vector (NaN left out).
+// Largest entry of vectors (NaN left out); bfloat16 in pairs until value().
+template <bool BF16>
+struct VecMax {
+  uint32_t m = BF16 ? 0xFF80FF80u : 0xFF800000u;
+  __device__ __forceinline__ void add(uint4 q) {
+    if constexpr (BF16) {
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+      __nv_bfloat162 b[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) b[k] = *reinterpret_cast<const __nv_bfloat162*>(&w[k]);
+      const __nv_bfloat162 r = __hmax2(__hmax2(*reinterpret_cast<const __nv_bfloat162*>(&m), b[0]),
+                                       __hmax2(__hmax2(b[1], b[2]), b[3]));
+      m = *reinterpret_cast<const uint32_t*>(&r);
+    } else {
+      m = __float_as_uint(fmaxf(fmaxf(fmaxf(__uint_as_float(m), __uint_as_float(q.x)), __uint_as_float(q.y)),
+                                fmaxf(__uint_as_float(q.z), __uint_as_float(q.w))));
+    }
+  }
+  __device__ __forceinline__ float value() const {
+    if constexpr (BF16) return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+    else return __uint_as_float(m);
+  }
+};
+
 template <bool BF16>
 __device__ __forceinline__ float vec_max(uint4 q) {
-  if constexpr (BF16) {
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-    __nv_bfloat162 b[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) b[k] = *reinterpret_cast<const __nv_bfloat162*>(&w[k]);
-    const __nv_bfloat162 m = __hmax2(__hmax2(b[0], b[1]), __hmax2(b[2], b[3]));
-    return fmaxf(__low2float(m), __high2float(m));
-  } else {
-    return fmaxf(fmaxf(__uint_as_float(q.x), __uint_as_float(q.y)), fmaxf(__uint_as_float(q.z), __uint_as_float(q.w)));
-  }
+  VecMax<BF16> m;
+  m.add(q);
+  return m.value();
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -308,6 +326,46 @@ __device__ __forceinline__ void grad_entries(const RowGrad& g, float scale, int6
     for (int k = 0; k < N; ++k)
       if (at == k) x[k] += g.at_target;
   }
+}
+
+// The same for a vector of a row whose largest logit is of ordinary size.
+// bfloat16: held above -1e30 in pairs, t = log2 p_j in one fused operation.
+struct NearGrad {
+  float c2, K, a2, b;  // t = x c2 + K, grad = 2^t (a2 t + b)
+};
+
+__device__ __forceinline__ NearGrad near_of(const RowGrad& g, float scale) {
+  const float c2 = scale * kLog2e;
+  return {c2, -fmaf(g.m, c2, g.log_s * kLog2e), g.a * kLn2, g.b};
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint4 grad_near(const RowGrad& g, const NearGrad& h, float scale, int64_t target, int j, uint4 q) {
+  float x[kPer<BF16>];
+  if constexpr (BF16) {
+    const __nv_bfloat162 floor2 = __floats2bfloat162_rn(kMasked, kMasked);
+    uint32_t v[4] = {q.x, q.y, q.z, q.w};
+    const float2 c2 = make_float2(h.c2, h.c2), K = make_float2(h.K, h.K), a2 = make_float2(h.a2, h.a2), b = make_float2(h.b, h.b);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const __nv_bfloat162 f = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&v[k]), floor2);
+      v[k] = *reinterpret_cast<const uint32_t*>(&f);
+      const float2 t = __ffma2_rn(make_float2(__uint_as_float(v[k] << 16), __uint_as_float(v[k] & 0xFFFF0000u)), c2, K);
+      const float2 e = __fmul2_rn(make_float2(ex2(t.x), ex2(t.y)), __ffma2_rn(a2, t, b));
+      x[2 * k] = e.x;
+      x[2 * k + 1] = e.y;
+    }
+    const unsigned long long at = static_cast<unsigned long long>(target - j);
+    if (at < 8) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (at == k) x[k] += g.at_target;
+    }
+  } else {
+    unpack<false>(q, x);
+    grad_entries(g, scale, target, j, x);
+  }
+  return pack<BF16>(x);
 }
 
 __device__ __forceinline__ float grad_entry(const RowGrad& g, float scale, int64_t target, int j, float x) {
@@ -543,86 +601,101 @@ __device__ __forceinline__ float2 cta_sum2(float2 v, float2* scratch) {
 
 // The alternatives of the row at hand, or of a CTA's part of it.  Collected
 // are the entries that reach a bound; `top` at least of the row's entries do.
-template <int THREADS>
+template <int THREADS, int CHUNKS>
 struct TopScratch {
   uint32_t group_max[kTopGroups];
   uint32_t bound;
-  int n;
+  int n, hits;
+  uint16_t hit[kHits];                // chunk * THREADS + thread
+  float chunk_max[CHUNKS][THREADS];   // largest entry of each chunk of a thread's vectors
   unsigned long long candidate[kCandidates];
   unsigned long long best[THREADS / 32];
   unsigned long long top[kMaxTop];
 };
 
 // The bound: the top-th largest of the maxima of kTopGroups groups of
-// threads, each over the entries it has seen (`own`).  Two barriers.
-template <int THREADS>
-__device__ __forceinline__ void top_bound(int top, float own, TopScratch<THREADS>& S) {
-  const int t = threadIdx.x;
-  uint32_t g = ordered(own);
+// neighbouring threads, `own` being a thread's largest entry.  A group's
+// threads share its comparison with the others.  Two barriers; the first one
+// also shows what was written to shared memory before.
+template <int THREADS, int CHUNKS>
+__device__ __forceinline__ void top_bound(int top, float own, TopScratch<THREADS, CHUNKS>& S) {
+  constexpr int kGroup = THREADS / kTopGroups, kEach = kTopGroups / kGroup;
+  const int t = threadIdx.x, group = t / kGroup, part = t % kGroup;
+  uint32_t mine = ordered(own);
 #pragma unroll
-  for (int d = 1; d < THREADS / kTopGroups; d *= 2) g = max(g, __shfl_xor_sync(0xFFFFFFFFu, g, d));
-  if (t % (THREADS / kTopGroups) == 0) S.group_max[t / (THREADS / kTopGroups)] = g;
-  if (t == 0) S.n = 0;
+  for (int d = 1; d < kGroup; d *= 2) mine = max(mine, __shfl_xor_sync(0xFFFFFFFFu, mine, d));
+  if (part == 0) S.group_max[group] = mine;
+  if (t == 0) S.n = S.hits = 0;
   if (t < kMaxTop) S.top[t] = 0;
   __syncthreads();
-  if (t < kTopGroups) {
-    const uint32_t mine = S.group_max[t];
-    int rank = 0;  // equal ones by their number
-#pragma unroll 8
-    for (int j = 0; j < kTopGroups; j += 4) {
-      const uint4 o = *reinterpret_cast<const uint4*>(&S.group_max[j]);
-      rank += (o.x > mine || (o.x == mine && j < t)) + (o.y > mine || (o.y == mine && j + 1 < t)) +
-              (o.z > mine || (o.z == mine && j + 2 < t)) + (o.w > mine || (o.w == mine && j + 3 < t));
-    }
-    if (rank == top - 1) S.bound = mine;
+  int rank = 0;  // equal ones by their number
+#pragma unroll
+  for (int j = 0; j < kEach; j += 4) {
+    const int at = part * kEach + j;
+    const uint4 o = *reinterpret_cast<const uint4*>(&S.group_max[at]);
+    rank += (o.x > mine || (o.x == mine && at < group)) + (o.y > mine || (o.y == mine && at + 1 < group)) +
+            (o.z > mine || (o.z == mine && at + 2 < group)) + (o.w > mine || (o.w == mine && at + 3 < group));
   }
+#pragma unroll
+  for (int d = 1; d < kGroup; d *= 2) rank += __shfl_xor_sync(0xFFFFFFFFu, rank, d);
+  if (part == 0 && rank == top - 1) S.bound = mine;
   __syncthreads();
 }
 
-__device__ __forceinline__ void collect_one(bool on, float x, int j, int* n, unsigned long long* candidate) {
-  const unsigned m = __ballot_sync(0xFFFFFFFFu, on);
-  const int lane = threadIdx.x & 31;
-  int i = 0;
-  if (lane == 0) i = atomicAdd(n, __popc(m));
-  i = __shfl_sync(0xFFFFFFFFu, i, 0) + __popc(m & ((1u << lane) - 1));
-  if (on && i < kCandidates) candidate[i] = place(x, j);
+// Collects from one vector, whose first entry is j0.
+template <bool BF16, int THREADS, int CHUNKS>
+__device__ __forceinline__ void collect(uint4 v, int j0, int vocab, TopScratch<THREADS, CHUNKS>& S) {
+  const uint32_t bound = S.bound;
+  if (ordered(vec_max<BF16>(v)) < bound) return;
+  float x[kPer<BF16>];
+  unpack<BF16>(v, x);
+#pragma unroll
+  for (int k = 0; k < kPer<BF16>; ++k) {
+    const int j = j0 + k;
+    if (ordered(x[k]) < bound || j < 0 || j >= vocab) continue;
+    const int at = atomicAdd(&S.n, 1);
+    if (at < kCandidates) S.candidate[at] = place(x[k], j);
+  }
 }
 
-// Collects from the vectors that the threads whose largest entry reaches the
-// bound have seen: the warp takes one such thread after the other and reads
-// its vectors again, a vector a lane, so that it never splits.  vector(i) is
-// vector i of the CTA's part, of which thread t has seen t, t + THREADS, ...
-template <bool BF16, int THREADS, typename V>
-__device__ __forceinline__ void collect_seen(float own, int n, int first, int vocab, V vector, TopScratch<THREADS>& S) {
-  constexpr int kN = kPer<BF16>;
-  const int lane = threadIdx.x & 31;
+// Collects from the chunks whose largest entry reaches the bound, spread over
+// all threads.  vector(i) is vector i of the CTA's part, n in all, entry
+// `first` beginning vector 0; thread t has seen t, t + THREADS, ..., `each` of
+// them to a chunk, and `own` is its largest entry.  Two barriers.
+template <bool BF16, int THREADS, int CHUNKS, typename V>
+__device__ __forceinline__ void collect_seen(float own, int chunks, int each, int n, int first, int vocab, V vector,
+                                             TopScratch<THREADS, CHUNKS>& S) {
   const uint32_t bound = S.bound;
   const float least = place_value(static_cast<unsigned long long>(bound) << 32);
-  for (unsigned hits = __ballot_sync(0xFFFFFFFFu, ordered(own) >= bound); hits != 0; hits &= hits - 1) {
-    const int seen = (threadIdx.x & ~31) + __ffs(hits) - 1;  // the thread
-    for (int i0 = seen; i0 < n; i0 += 32 * THREADS) {
-      const int i = i0 + lane * THREADS;
-      const uint4 v = i < n ? vector(i) : masked_vector<BF16>();
-      const bool reach = i < n && !(vec_max<BF16>(v) < least);
-      if (!__any_sync(0xFFFFFFFFu, reach)) continue;
-      float x[kN];
-      unpack<BF16>(v, x);
-#pragma unroll
-      for (int k = 0; k < kN; ++k) {
-        const int j = first + i * kN + k;
-        const bool on = reach && j >= 0 && j < vocab && ordered(x[k]) >= bound;
-        if (__any_sync(0xFFFFFFFFu, on)) collect_one(on, x[k], j, &S.n, S.candidate);
-      }
+  if (ordered(own) >= bound) {
+    for (int c = 0; c < chunks; ++c) {
+      if (S.chunk_max[c][threadIdx.x] < least) continue;
+      const int h = atomicAdd(&S.hits, 1);
+      if (h < kHits) S.hit[h] = static_cast<uint16_t>(c * THREADS + threadIdx.x);
     }
   }
+  __syncthreads();
+  if (S.hits > kHits) {  // as if there were too many candidates
+    if (threadIdx.x == 0) S.n = kCandidates + 1;
+  } else {
+    const unsigned pairs = S.hits * each;
+    for (unsigned q = threadIdx.x; q < pairs; q += THREADS) {
+      const unsigned h = q / static_cast<unsigned>(each);
+      const int c = S.hit[h] / THREADS, thread = S.hit[h] % THREADS;
+      const int i = thread + (c * each + static_cast<int>(q - h * each)) * THREADS;
+      if (i >= n) continue;
+      collect<BF16>(vector(i), first + i * kPer<BF16>, vocab, S);
+    }
+  }
+  __syncthreads();
 }
 
 // Ranks what was collected by counting, into S.top (0 where there are fewer).
 // Where more was collected than there is room for (ties, masks that leave
 // fewer than `top` entries) it takes one maximum after the other of `x`, the
 // entries first .. last-1 of a row in global memory.
-template <bool BF16, int THREADS>
-__device__ __forceinline__ void top_rank(int top, const void* x, long long base, int first, int last, TopScratch<THREADS>& S) {
+template <bool BF16, int THREADS, int CHUNKS>
+__device__ __forceinline__ void top_rank(int top, const void* x, long long base, int first, int last, TopScratch<THREADS, CHUNKS>& S) {
   const int t = threadIdx.x, n = S.n;
   if (n <= kCandidates) {
     for (int i = t; i < n; i += THREADS) {
@@ -721,7 +794,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 8 : 3) logprob_loss(
   __shared__ float scratch[2][THREADS / 32];
   __shared__ float2 pair_scratch[2][THREADS / 32];
   __shared__ Exchange X;
-  __shared__ __align__(16) TopScratch<TOP ? THREADS : 32> S;
+  __shared__ __align__(16) TopScratch<TOP ? THREADS : 32, TOP ? 4 : 1> S;
   constexpr int kN = kPer<BF16>;
   const cg::cluster_group cluster = cg::this_cluster();
   const int ranks = 1 << P.log_ranks, rank = blockIdx.x & (ranks - 1);
@@ -816,11 +889,16 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 8 : 3) logprob_loss(
     for (int group = 0; group < 4; ++group) {
       asm volatile("cp.async.wait_group 3;" ::: "memory");
       const int end = min(p.n, (group + 1) * p.per);
+      VecMax<BF16> chunk;
 #pragma unroll 2
       for (int i = group * p.per + t; i < end; i += THREADS) {
         const uint4 v = q[i];
-        if (TOP) own = fmaxf(own, vec_max<BF16>(v));
+        if (TOP) chunk.add(v);
         accumulate_near<BF16>(s, w, v, a.m, c2);
+      }
+      if constexpr (TOP) {
+        S.chunk_max[group][t] = chunk.value();
+        own = fmaxf(own, chunk.value());
       }
       copy(np, false, group);
     }
@@ -847,9 +925,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 8 : 3) logprob_loss(
     }
     if constexpr (TOP) {
       top_bound(P.top, own, S);
-      collect_seen<BF16, THREADS>(own, p.n, p.first(0), P.vocab, [&](int i) { return q[i]; }, S);
-      __syncthreads();
-      top_rank<BF16, THREADS>(P.top, P.x, base, j0, j1, S);
+      collect_seen<BF16>(own, 4, p.per / THREADS, p.n, p.first(0), P.vocab, [&](int i) { return q[i]; }, S);
+      top_rank<BF16>(P.top, P.x, base, j0, j1, S);
       if (ranks > 1) {
         if (t < P.top) cluster.map_shared_rank(&X, 0)->top[rank][t] = S.top[t];
         cluster.sync();
@@ -872,19 +949,20 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 8 : 3) logprob_loss(
     }
 
     const RowGrad g = grad_of(P, r, row, target);
-    if (same) {
+    const NearGrad near = near_of(g, P.scale);
+    if (same && fabsf(near.K) < -kMasked) {
 #pragma unroll 1
       for (int group = 0; group < 4; ++group) {
         const int end = min(p.n, (group + 1) * p.per);
 #pragma unroll 2
         for (int i = group * p.per + t; i < end; i += THREADS) {
           const int j = p.first(i);
-          float x[kN];
-          unpack<BF16>(q[i], x);
-          grad_entries(g, P.scale, target, j, x);
+          const uint4 v = grad_near<BF16>(g, near, P.scale, target, j, q[i]);
           if (p.whole(i)) {
-            o[i] = pack<BF16>(x);
+            o[i] = v;
           } else {
+            float x[kN];
+            unpack<BF16>(v, x);
             for (int k = 0; k < kN; ++k)
               if (j + k >= 0 && j + k < P.vocab) put<BF16>(P.grad, out + j + k, x[k]);
           }
@@ -921,7 +999,7 @@ __global__ void __launch_bounds__(kScoreThreads, 4) logprob_score(const __grid_c
   __shared__ float scratch[kWarps];
   __shared__ float2 pair_scratch[kWarps];
   __shared__ Exchange X;
-  __shared__ __align__(16) TopScratch<TOP ? kScoreThreads : 32> S;
+  __shared__ __align__(16) TopScratch<TOP ? kScoreThreads : 32, TOP ? kScoreChunks : 1> S;
   const cg::cluster_group cluster = cg::this_cluster();
   const int ranks = 1 << P.log_ranks, rank = blockIdx.x & (ranks - 1);
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -935,46 +1013,58 @@ __global__ void __launch_bounds__(kScoreThreads, 4) logprob_score(const __grid_c
   // a CTA's shared memory is written by others only once it has begun
   if (ranks > 1) cg::cluster_group::barrier_arrive();
   const RowPart<BF16> p = part_of<BF16, kScoreThreads>(P, row, rank);
-  const uint4* const src = reinterpret_cast<const uint4*>(p.src);
+  // the part's whole vectors src[0 .. n-1]; the row's other two (its ends) are
+  // put together from their entries by one thread each
+  const bool head = p.v0 < p.lo, tail = p.v0 + p.n > p.lo + p.wholes;
+  const uint4* const src = reinterpret_cast<const uint4*>(p.src) + head;
+  const int n = p.n - head - tail;
   const float c2 = P.scale * kLog2e;
-  auto vector = [&](int i) {  // an end of the row is put together from its entries
-    if (p.whole(i)) return load_once(src + i);
-    return RowVectors<BF16>(P.x, base, P.vocab).end(p.v0 + i);
-  };
-  uint4 a[kU], b[kU];
+  uint4 a[kU], b[kU], end = masked_vector<BF16>();
+  if (t == 0 && head) end = RowVectors<BF16>(P.x, base, P.vocab).end(p.v0);
+  if (t == 32 && tail) end = RowVectors<BF16>(P.x, base, P.vocab).end(p.v0 + p.n - 1);
 #pragma unroll
-  for (int u = 0; u < kU; ++u) a[u] = t + u * kScoreThreads < p.n ? vector(t + u * kScoreThreads) : masked_vector<BF16>();
+  for (int u = 0; u < kU; ++u) a[u] = t + u * kScoreThreads < n ? load_once(src + t + u * kScoreThreads) : masked_vector<BF16>();
   float x_target = 0.0f;
   if (t == 0 && rank == 0 && target < P.vocab) x_target = at<BF16>(P.x, base + target);
-  float own = -INFINITY;
-#pragma unroll
-  for (int u = 0; u < kU; ++u) own = fmaxf(own, vec_max<BF16>(a[u]));
   Sums sums{};
-  sums.m = own;
+  VecMax<BF16> near;
+  near.add(end);
+#pragma unroll
+  for (int u = 0; u < kU; ++u) near.add(a[u]);
+  sums.m = near.value();
 #pragma unroll
   for (int d = 16; d > 0; d /= 2) sums.m = fmaxf(sums.m, __shfl_xor_sync(0xFFFFFFFFu, sums.m, d));
   float2 s{}, w{};
   bool found = sums.m != -INFINITY;
-  for (int i = t; i - t < p.n; i += kBatch) {
+  if (warp < 2) accumulate_near<BF16>(s, w, end, reference(sums.m), c2);
+  // a chunk: batches of a thread that share a largest entry, a power of two of them
+  const int batches = (n + kBatch - 1) / kBatch;
+  int log_chunk = 0;
+  while (TOP && batches > kScoreChunks << log_chunk) ++log_chunk;
+  for (int k = 0; k < batches; ++k) {
+    const int i = k * kBatch + t;
     if (!found) {  // masked entries alone so far
 #pragma unroll
-      for (int u = 0; u < kU; ++u) sums.m = i + u * kScoreThreads < p.n ? fmaxf(sums.m, vec_max<BF16>(a[u])) : sums.m;
+      for (int u = 0; u < kU; ++u) sums.m = i + u * kScoreThreads < n ? fmaxf(sums.m, vec_max<BF16>(a[u])) : sums.m;
 #pragma unroll
       for (int d = 16; d > 0; d /= 2) sums.m = fmaxf(sums.m, __shfl_xor_sync(0xFFFFFFFFu, sums.m, d));
       found = sums.m != -INFINITY;
     }
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int k = i + kBatch + u * kScoreThreads;
-      if (k < p.n) b[u] = vector(k);
-    }
+    for (int u = 0; u < kU; ++u)
+      if (i + kBatch + u * kScoreThreads < n) b[u] = load_once(src + i + kBatch + u * kScoreThreads);
+    VecMax<BF16> largest;
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      if (i + u * kScoreThreads < p.n) {
-        if (TOP) own = fmaxf(own, vec_max<BF16>(a[u]));
+      if (i + u * kScoreThreads < n) {
+        if (TOP) largest.add(a[u]);
         accumulate_near<BF16>(s, w, a[u], reference(sums.m), c2);
       }
       a[u] = b[u];
+    }
+    if constexpr (TOP) {
+      float* const chunk = &S.chunk_max[k >> log_chunk][t];
+      *chunk = (k & ((1 << log_chunk) - 1)) == 0 ? largest.value() : fmaxf(*chunk, largest.value());
     }
   }
   sums.s = s.x + s.y;
@@ -987,8 +1077,14 @@ __global__ void __launch_bounds__(kScoreThreads, 4) logprob_score(const __grid_c
   // A warp that saw masked entries alone has m = -inf and no sum; any other sum
   // out of range means that its reference was too far off.
   if (lane == 0) warp_sums[warp] = sums;
-  if constexpr (TOP) top_bound(P.top, own, S);
-  else __syncthreads();
+  const int chunks = (batches + (1 << log_chunk) - 1) >> log_chunk;
+  float own = vec_max<BF16>(end);
+  if constexpr (TOP) {
+    for (int c = 0; c < chunks; ++c) own = fmaxf(own, S.chunk_max[c][t]);
+    top_bound(P.top, own, S);
+  } else {
+    __syncthreads();
+  }
   bool far = false;
 #pragma unroll
   for (int k = 0; k < kWarps; ++k)
@@ -1001,9 +1097,9 @@ __global__ void __launch_bounds__(kScoreThreads, 4) logprob_score(const __grid_c
     for (int k = 1; k < kWarps; ++k) sums = merge(sums, warp_sums[k], c2);
   }
   if constexpr (TOP) {
-    collect_seen<BF16, kScoreThreads>(own, p.n, p.first(0), P.vocab, vector, S);
-    __syncthreads();
-    top_rank<BF16, kScoreThreads>(P.top, P.x, base, max(0, p.first(0)), min(P.vocab, p.first(p.n)), S);
+    if (warp < 2) collect<BF16>(end, p.first(t == 0 ? 0 : p.n - 1), P.vocab, S);
+    collect_seen<BF16>(own, chunks, kU << log_chunk, n, p.first(head), P.vocab, [&](int i) { return load_once(src + i); }, S);
+    top_rank<BF16>(P.top, P.x, base, max(0, p.first(0)), min(P.vocab, p.first(p.n)), S);
   }
   if (ranks > 1) {
     cg::cluster_group::barrier_wait();
