@@ -27,7 +27,7 @@
 // and 21.
 //
 // Work: one warp per 256-element block, 8 elements a lane; eight warps share
-// 32 blocks of one tensor.  One launch covers up to kMaxTensors tensors of
+// eight blocks of one tensor.  One launch covers up to kMaxTensors tensors of
 // the same types; the table is in the kernel's parameters.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -49,7 +49,6 @@ namespace {
 constexpr int kQBlock = 256;       // elements that share a scale
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kCtaBlocks = 32;     // 256-element blocks per CTA
 constexpr int kMaxTensors = 400;   // per launch: the table fills the 32 KB of kernel parameters
 
 struct AdamwTensor {
@@ -87,183 +86,386 @@ __host__ __device__ __forceinline__ uint32_t mix(uint32_t x) {
 
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
-template <bool BF16>
-__device__ __forceinline__ void load8(const void* base, long long i, float (&x)[8]) {
-  if constexpr (BF16) {
-    const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + i);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+__device__ __forceinline__ float sqrt_approx(float x) {  // below 2^-126: 0
+  float y;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max3_abs_nan(float a, float b, float c) {
+  float y;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+__device__ __forceinline__ float warp_max_nan(float a) {
+  float y;
+  asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(a));
+  return y;
+}
+
+// Paired product and sum.  The compiler makes one fused operation of a paired
+// product and a paired sum that takes it, whatever their rounding modifiers:
+// where both have to be rounded the sum is two scalar ones.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 add_apart(float2 a, float2 b) { return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y)); }
+
+// A lane's eight entries as four pairs.
+struct Eight {
+  float2 v[4];
+};
+
+__device__ __forceinline__ Eight widen(uint4 q) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  Eight x;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      x[2 * k] = __uint_as_float(w[k] << 16);
-      x[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+  for (int k = 0; k < 4; ++k) x.v[k] = make_float2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u));
+  return x;
+}
+
+// What a lane reads of the warp's 256 entries of an array from `at` on, eight
+// a lane.  bfloat16 arrays may begin anywhere: off a 4-byte boundary a lane
+// reads the three words inside its entries and one that it shares with the
+// next lane, and takes its first entry from the lane before (align); nothing
+// outside the 256 entries is touched.
+struct Raw {
+  uint4 a, b;      // float32: eight entries; bfloat16: a
+  uint32_t first;  // lane 0's first entry where the words are shared
+};
+
+template <bool BF16>
+__device__ __forceinline__ Raw fetch(const void* base, long long i, int lane) {
+  Raw r{};
+  if constexpr (BF16) {
+    const __nv_bfloat16* at = static_cast<const __nv_bfloat16*>(base) + i;
+    const __nv_bfloat16* a = at + 8 * lane;
+    const unsigned off = static_cast<unsigned>(reinterpret_cast<uintptr_t>(at)) & 15u;
+    if (off == 0) {
+      r.a = *reinterpret_cast<const uint4*>(a);
+    } else if ((off & 2u) == 0) {
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(a);
+      r.a = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(a + 1);
+      const uint16_t* h = reinterpret_cast<const uint16_t*>(a);
+      r.a = make_uint4(w[0], w[1], w[2], lane < 31 ? w[3] : h[7]);
+      if (lane == 0) r.first = static_cast<uint32_t>(h[0]) << 16;
     }
   } else {
-    const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(base) + i);
-    const float4 a = f[0], b = f[1];
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    const uint4* f = reinterpret_cast<const uint4*>(static_cast<const float*>(base) + i + 8 * lane);
+    r.a = f[0];
+    r.b = f[1];
+  }
+  return r;
+}
+
+template <bool BF16>
+__device__ __forceinline__ Eight align(const Raw& r, const void* base, int lane) {
+  if constexpr (BF16) {
+    uint4 q = r.a;
+    if (reinterpret_cast<uintptr_t>(base) & 2u) {  // a block is a multiple of 4 bytes
+      uint32_t before = __shfl_up_sync(0xFFFFFFFFu, q.w, 1);
+      if (lane == 0) before = r.first;
+      q = make_uint4(__byte_perm(before, q.x, 0x5432), __byte_perm(q.x, q.y, 0x5432), __byte_perm(q.y, q.z, 0x5432),
+                     __byte_perm(q.z, q.w, 0x5432));
+    }
+    return widen(q);
+  } else {
+    auto f = [](uint32_t x, uint32_t y) { return make_float2(__uint_as_float(x), __uint_as_float(y)); };
+    return {{f(r.a.x, r.a.y), f(r.a.z, r.a.w), f(r.b.x, r.b.y), f(r.b.z, r.b.w)}};
   }
 }
 
+__device__ __forceinline__ void store_bf16(__nv_bfloat16* at, int lane, uint4 q) {
+  __nv_bfloat16* a = at + 8 * lane;
+  const unsigned off = static_cast<unsigned>(reinterpret_cast<uintptr_t>(at)) & 15u;
+  if (off == 0) {
+    *reinterpret_cast<uint4*>(a) = q;
+    return;
+  }
+  if ((off & 2u) == 0) {
+    uint32_t* w = reinterpret_cast<uint32_t*>(a);
+    w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+    return;
+  }
+  uint32_t* w = reinterpret_cast<uint32_t*>(a + 1);
+  uint16_t* h = reinterpret_cast<uint16_t*>(a);
+  const uint32_t after = __shfl_down_sync(0xFFFFFFFFu, q.x, 1);
+  w[0] = __byte_perm(q.x, q.y, 0x5432);
+  w[1] = __byte_perm(q.y, q.z, 0x5432);
+  w[2] = __byte_perm(q.z, q.w, 0x5432);
+  if (lane < 31) w[3] = __byte_perm(q.w, after, 0x5432);
+  else h[7] = static_cast<uint16_t>(q.w >> 16);
+  if (lane == 0) h[0] = static_cast<uint16_t>(q.x);
+}
+
+__device__ __forceinline__ void store_f32(float* at, int lane, const Eight& x) {
+  float4* f = reinterpret_cast<float4*>(at + 8 * lane);
+  f[0] = make_float4(x.v[0].x, x.v[0].y, x.v[1].x, x.v[1].y);
+  f[1] = make_float4(x.v[2].x, x.v[2].y, x.v[3].x, x.v[3].y);
+}
+
+// Entry `k` of the strided layout: lane + 32 k of the block, 0 past its end.
 template <bool BF16>
-__device__ __forceinline__ float load1(const void* base, long long i) {
-  if constexpr (BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(base)[i]);
-  else return static_cast<const float*>(base)[i];
-}
-
-__device__ __forceinline__ float e4m3(uint32_t c) {
-  return __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(c), __NV_E4M3)));
-}
-__device__ __forceinline__ float e5m2(uint32_t c) {
-  return __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(c), __NV_E5M2)));
-}
-
-// Rounds x down or up to bfloat16 with 16 random bits; NaN and infinity as they are.
-__device__ __forceinline__ uint32_t bf16_stochastic(float x, uint32_t h) {
-  const uint32_t u = __float_as_uint(x);
-  const uint32_t r = (h * kC0) >> 16;
-  const bool finite = (u & 0x7F800000u) != 0x7F800000u;
-  const uint32_t nan = (u & 0x7FFFFFFFu) > 0x7F800000u ? 0x40u : 0u;
-  return finite ? (u + r) >> 16 : (u >> 16) | nan;
-}
-
-// Largest |x| of the warp's block as the bits of a non-negative float; NaN is
-// above infinity, so neither is lost.
-__device__ __forceinline__ uint32_t block_max(const float (&x)[8]) {
-  uint32_t a = 0;
+__device__ __forceinline__ Eight load_strided(const void* base, long long i, int lane, int left) {
+  Eight x;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) a = max(a, __float_as_uint(x[k]) & 0x7FFFFFFFu);
-  return __reduce_max_sync(0xFFFFFFFFu, a);
+  for (int k = 0; k < 8; ++k) {
+    const int at = lane + 32 * k;
+    float y = 0.0f;
+    if (at < left) {
+      if constexpr (BF16) y = __bfloat162float(static_cast<const __nv_bfloat16*>(base)[i + at]);
+      else y = static_cast<const float*>(base)[i + at];
+    }
+    (k & 1 ? x.v[k / 2].y : x.v[k / 2].x) = y;
+  }
+  return x;
 }
+
+__device__ __forceinline__ uint2 load_codes_strided(const void* base, long long i, int lane, int left) {
+  uint32_t w[2] = {0, 0};
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int at = lane + 32 * k;
+    if (at < left) w[k / 4] |= static_cast<uint32_t>(static_cast<const uint8_t*>(base)[i + at]) << (8 * (k & 3));
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+// Values of eight codes, times the block's scale.
+template <bool E4M3>
+__device__ __forceinline__ Eight decode(uint2 c, float scale) {
+  Eight x;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t w = (k < 2 ? c.x : c.y) >> (16 * (k & 1));
+    float2 f;
+    if constexpr (E4M3) {
+      f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w), __NV_E4M3)));
+    } else {  // the upper byte of a half
+      const uint32_t h = __byte_perm(w, 0, 0x1404);
+      f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    }
+    x.v[k] = mul2(f, make_float2(scale, scale));
+  }
+  return x;
+}
+
+// Eight codes of x with 16 random bits each; unit = 2^-E of the block.  The
+// integer is shifted so that the code fills its top byte: what the random bits
+// are added to lies below, and the sign (E4M3) is put back from x.
+template <bool E4M3>
+__device__ __forceinline__ uint2 encode(const Eight& x, float unit, const uint32_t (&h)[8]) {
+  constexpr float kField = E4M3 ? 0x1p-113f : 0x1p-98f;
+  constexpr int kShift = E4M3 ? 4 : 3;
+  uint32_t w[2];
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    uint32_t u[4], c[4];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float2 y = mul2(mul2(x.v[2 * half + k], make_float2(unit, unit)), make_float2(kField, kField));
+      u[2 * k] = __float_as_uint(y.x);
+      u[2 * k + 1] = __float_as_uint(y.y);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)  // 0x80, then the low (E4M3) or high 16 random bits
+      c[k] = (u[k] << kShift) + __byte_perm(h[4 * half + k], 0x80u, E4M3 ? 0x5104 : 0x5324);
+    w[half] = __byte_perm(__byte_perm(c[0], c[1], 0x0073), __byte_perm(c[2], c[3], 0x0073), 0x5410);
+    if constexpr (E4M3)
+      w[half] = (w[half] & 0x7F7F7F7Fu) |
+                (__byte_perm(__byte_perm(u[0], u[1], 0x0073), __byte_perm(u[2], u[3], 0x0073), 0x5410) & 0x80808080u);
+    else
+      w[half] &= 0x7F7F7F7Fu;
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+__device__ __forceinline__ float block_max(const Eight& x) {
+  float a = max3_abs_nan(x.v[0].x, x.v[0].y, x.v[1].x);
+  a = max3_abs_nan(a, x.v[1].y, x.v[2].x);
+  a = max3_abs_nan(a, x.v[2].y, x.v[3].x);
+  return warp_max_nan(max3_abs_nan(a, x.v[3].y, x.v[3].y));
+}
+
+// The step of eight elements: m, v and p in, out.
+__device__ __forceinline__ void update(const AdamwParams& P, float step, float decay, float gs, const Eight& g, Eight& p, Eight& m,
+                                       Eight& v) {
+  auto both = [](float a) { return make_float2(a, a); };
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 gk = mul2(g.v[k], both(gs));
+    m.v[k] = add_apart(mul2(m.v[k], both(P.b1)), mul2(gk, both(P.omb1)));
+    v.v[k] = add_apart(mul2(v.v[k], both(P.b2)), mul2(mul2(gk, gk), both(P.omb2)));
+    const float2 root = make_float2(sqrt_approx(v.v[k].x), sqrt_approx(v.v[k].y));
+    const float2 den = __ffma2_rn(root, both(P.r2), both(P.eps));
+    const float2 u = mul2(m.v[k], make_float2(rcp_approx(den.x), rcp_approx(den.y)));
+    float2 dec = mul2(p.v[k], both(decay));
+    if (P.cautious) {
+      auto agree = [](float a, float b) { return (a > 0.0f && b > 0.0f) || (a < 0.0f && b < 0.0f); };
+      if (!agree(u.x, p.v[k].x)) dec.x = 0.0f;
+      if (!agree(u.y, p.v[k].y)) dec.y = 0.0f;
+    }
+    const float2 move = __ffma2_rn(u, both(step), dec);
+    p.v[k] = __fadd2_rn(p.v[k], make_float2(-move.x, -move.y));
+  }
+}
+
+// Rounds p to bfloat16 with the random bits (NaN and infinity as they are).
+__device__ __forceinline__ uint4 narrow(const Eight& p, const uint32_t (&h)[8]) {
+  float2 bad = make_float2(0.0f, 0.0f);  // 0 times what is not finite is not 0
+#pragma unroll
+  for (int k = 0; k < 4; ++k) bad = __ffma2_rn(p.v[k], make_float2(0.0f, 0.0f), bad);
+  const bool finite = bad.x + bad.y == 0.0f;
+  uint32_t u[8], w[4];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) u[k] = __float_as_uint(k & 1 ? p.v[k / 2].y : p.v[k / 2].x);
+  if (finite) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) u[k] += h[k] * kC0 >> 16;
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if ((u[k] & 0x7F800000u) != 0x7F800000u) u[k] += h[k] * kC0 >> 16;
+      else if (u[k] & 0x7FFFFFu) u[k] |= 0x400000u;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) w[k] = __byte_perm(u[2 * k], u[2 * k + 1], 0x7632);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// What a lane reads of a whole block in the vector layout.
+struct Fetched {
+  Raw p, g, m, v;  // float32 moments; codes: a.x and a.y
+  float sm, sv;
+};
 
 template <bool PB, bool GB, bool B8>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ AdamwParams P) {
+__device__ __forceinline__ Fetched fetch_block(const AdamwTensor& T, long long blk, int lane) {
+  const long long i0 = blk * kQBlock;
+  Fetched f{};
+  f.p = fetch<PB>(T.p, i0, lane);
+  f.g = fetch<GB>(T.g, i0, lane);
+  if constexpr (B8) {
+    const uint2 cm = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(T.m) + i0 + 8 * lane);
+    const uint2 cv = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(T.v) + i0 + 8 * lane);
+    f.m.a = make_uint4(cm.x, cm.y, 0, 0);
+    f.v.a = make_uint4(cv.x, cv.y, 0, 0);
+    f.sm = T.ms[blk];
+    f.sv = T.vs[blk];
+  } else {
+    f.m = fetch<false>(T.m, i0, lane);
+    f.v = fetch<false>(T.v, i0, lane);
+  }
+  return f;
+}
+
+// One block from what has been read of it; `left` entries in the strided
+// layout, all of them (VEC) in the vector layout.
+template <bool PB, bool GB, bool B8, bool VEC>
+__device__ __forceinline__ void step_block(const AdamwParams& P, const AdamwTensor& T, long long blk, int lane, int left, float gs,
+                                           Eight& p, const Eight& g, Eight& m, Eight& v) {
+  const long long i0 = blk * kQBlock;
+  update(P, T.step, T.decay, gs, g, p, m, v);
+  uint32_t h[8];
+  if constexpr (B8 || PB) {
+    const uint32_t key = T.key + static_cast<uint32_t>(static_cast<unsigned long long>(i0) >> 32) * kC1;
+    const uint32_t x0 = static_cast<uint32_t>(i0 + (VEC ? 8 * lane : lane)) * kC0 + key;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) h[k] = mix(x0 + k * (VEC ? kC0 : 32u * kC0));
+  }
+  uint2 cm, cv;
+  if constexpr (B8) {
+    const uint32_t am = __float_as_uint(block_max(m)), av = __float_as_uint(block_max(v));
+    const int em = min(max(static_cast<int>(am >> 23) - 127, -100), 126);
+    const int ev = min(max(static_cast<int>(av >> 23) - 127, -100), 126);
+    cm = encode<true>(m, pow2i(-em), h);
+    cv = encode<false>(v, pow2i(-ev), h);
+    if (lane == 0) {  // a block with a value that is not finite (or 2^127 and more) becomes NaN
+      T.ms[blk] = am < 0x7F000000u ? pow2i(em - 7) : __uint_as_float(0x7FC00000u);
+      T.vs[blk] = av < 0x7F000000u ? pow2i(ev - 14) : __uint_as_float(0x7FC00000u);
+    }
+  }
+  if constexpr (VEC) {
+    if constexpr (PB) store_bf16(static_cast<__nv_bfloat16*>(T.p) + i0, lane, narrow(p, h));
+    else store_f32(static_cast<float*>(T.p) + i0, lane, p);
+    if constexpr (B8) {
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(T.m) + i0 + 8 * lane) = cm;
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(T.v) + i0 + 8 * lane) = cv;
+    } else {
+      store_f32(static_cast<float*>(T.m) + i0, lane, m);
+      store_f32(static_cast<float*>(T.v) + i0, lane, v);
+    }
+  } else {
+    uint4 np = make_uint4(0, 0, 0, 0);
+    if constexpr (PB) np = narrow(p, h);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int at = lane + 32 * k;
+      if (at >= left) continue;
+      auto entry = [k](const Eight& x) { return k & 1 ? x.v[k / 2].y : x.v[k / 2].x; };
+      if constexpr (PB) {
+        const uint32_t w[4] = {np.x, np.y, np.z, np.w};
+        static_cast<uint16_t*>(T.p)[i0 + at] = static_cast<uint16_t>(w[k / 2] >> (16 * (k & 1)));
+      } else {
+        static_cast<float*>(T.p)[i0 + at] = entry(p);
+      }
+      if constexpr (B8) {
+        static_cast<uint8_t*>(T.m)[i0 + at] = static_cast<uint8_t>((k < 4 ? cm.x : cm.y) >> (8 * (k & 3)));
+        static_cast<uint8_t*>(T.v)[i0 + at] = static_cast<uint8_t>((k < 4 ? cv.x : cv.y) >> (8 * (k & 3)));
+      } else {
+        static_cast<float*>(T.m)[i0 + at] = entry(m);
+        static_cast<float*>(T.v)[i0 + at] = entry(v);
+      }
+    }
+  }
+}
+
+// One block a warp: the CTAs at work then cover one stretch of every array.
+// With eight blocks a warp, CTAs 16,384 elements apart, the 8-bit step of
+// 100.7 M float32 parameters took 358 us in place of 250.
+template <bool PB, bool GB, bool B8>
+__global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constant__ AdamwParams P) {
   int lo = 0, hi = P.n - 1;  // the tensor: largest i with first <= blockIdx.x
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (P.t[mid].first <= static_cast<int>(blockIdx.x)) lo = mid; else hi = mid - 1;
   }
   const AdamwTensor& T = P.t[lo];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
   const float gs = P.grad_scale ? *P.grad_scale : 1.0f;
-  const long long b0 = static_cast<long long>(blockIdx.x - T.first) * kCtaBlocks;
-  for (int j = warp; j < kCtaBlocks; j += kWarps) {
-    const long long blk = b0 + j, i0 = blk * kQBlock;
-    if (i0 >= T.numel) break;
-    if (!MUON_CHECK(i0 >= 0)) break;
-    const int left = static_cast<int>(min(static_cast<long long>(kQBlock), T.numel - i0));
-    const bool vec = T.vec && left == kQBlock;
-    float p[8], g[8], m[8], v[8];
-    float sm = 1.0f, sv = 1.0f;
-    if (B8) sm = T.ms[blk], sv = T.vs[blk];
-    const int at0 = vec ? lane * 8 : lane, dat = vec ? 1 : 32;
-    if (vec) {
-      load8<PB>(T.p, i0 + at0, p);
-      load8<GB>(T.g, i0 + at0, g);
-      if constexpr (B8) {
-        const uint2 cm = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(T.m) + i0 + at0);
-        const uint2 cv = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(T.v) + i0 + at0);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          m[k] = e4m3(((k < 4 ? cm.x : cm.y) >> (8 * (k & 3))) & 0xFF);
-          v[k] = e5m2(((k < 4 ? cv.x : cv.y) >> (8 * (k & 3))) & 0xFF);
-        }
-      } else {
-        load8<false>(T.m, i0 + at0, m);
-        load8<false>(T.v, i0 + at0, v);
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int at = lane + 32 * k;
-        p[k] = g[k] = m[k] = v[k] = 0.0f;
-        if (at >= left) continue;
-        p[k] = load1<PB>(T.p, i0 + at);
-        g[k] = load1<GB>(T.g, i0 + at);
-        if constexpr (B8) {
-          m[k] = e4m3(static_cast<const uint8_t*>(T.m)[i0 + at]);
-          v[k] = e5m2(static_cast<const uint8_t*>(T.v)[i0 + at]);
-        } else {
-          m[k] = static_cast<const float*>(T.m)[i0 + at];
-          v[k] = static_cast<const float*>(T.v)[i0 + at];
-        }
-      }
-    }
-    const uint32_t key = T.key + static_cast<uint32_t>(static_cast<unsigned long long>(i0) >> 32) * kC1;
-    uint32_t h[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      if (B8) {
-        m[k] = __fmul_rn(m[k], sm);
-        v[k] = __fmul_rn(v[k], sv);
-      }
-      const float gk = __fmul_rn(g[k], gs);
-      m[k] = __fadd_rn(__fmul_rn(m[k], P.b1), __fmul_rn(gk, P.omb1));
-      v[k] = __fadd_rn(__fmul_rn(v[k], P.b2), __fmul_rn(__fmul_rn(gk, gk), P.omb2));
-      const float u = __fdiv_rn(m[k], __fadd_rn(__fmul_rn(__fsqrt_rn(v[k]), P.r2), P.eps));
-      const bool on = !P.cautious || (u > 0.0f && p[k] > 0.0f) || (u < 0.0f && p[k] < 0.0f);
-      const float dec = on ? __fmul_rn(p[k], T.decay) : 0.0f;
-      p[k] = __fsub_rn(p[k], __fadd_rn(__fmul_rn(u, T.step), dec));
-      if (B8 || PB) h[k] = mix(static_cast<uint32_t>(i0 + at0 + k * dat) * kC0 + key);
-    }
-    uint32_t cm[8], cv[8];
+  const long long blk = static_cast<long long>(blockIdx.x - T.first) * kWarps + (threadIdx.x >> 5), i0 = blk * kQBlock;
+  if (i0 >= T.numel) return;
+  if (!MUON_CHECK(i0 >= 0)) return;
+  const int left = static_cast<int>(min(static_cast<long long>(kQBlock), T.numel - i0));
+  Eight m, v;
+  if (T.vec && left == kQBlock) {
+    const Fetched f = fetch_block<PB, GB, B8>(T, blk, lane);
+    Eight p = align<PB>(f.p, T.p, lane);
+    const Eight g = align<GB>(f.g, T.g, lane);
     if constexpr (B8) {
-      const uint32_t am = block_max(m), av = block_max(v);
-      const int em = min(max(static_cast<int>(am >> 23) - 127, -100), 126);
-      const int ev = min(max(static_cast<int>(av >> 23) - 127, -100), 126);
-      const float im = pow2i(-em), iv = pow2i(-ev);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float ym = __fmul_rn(__fmul_rn(fabsf(m[k]), im), 0x1p-113f);
-        const float yv = __fmul_rn(__fmul_rn(fabsf(v[k]), iv), 0x1p-98f);
-        cm[k] = ((__float_as_uint(ym) + ((h[k] & 0xFFFFu) << 4 | 8u)) >> 20 & 0x7Fu) | (__float_as_uint(m[k]) >> 24 & 0x80u);
-        cv[k] = (__float_as_uint(yv) + ((h[k] >> 16) << 5 | 16u)) >> 21 & 0x7Fu;
-      }
-      if (lane == 0) {  // a block with a value that is not finite (or 2^127 and more) becomes NaN
-        T.ms[blk] = am < 0x7F000000u ? pow2i(em - 7) : __uint_as_float(0x7FC00000u);
-        T.vs[blk] = av < 0x7F000000u ? pow2i(ev - 14) : __uint_as_float(0x7FC00000u);
-      }
-    }
-    if (vec) {
-      if constexpr (PB) {
-        uint32_t w[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          w[k] = bf16_stochastic(p[2 * k], h[2 * k]) | bf16_stochastic(p[2 * k + 1], h[2 * k + 1]) << 16;
-        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(T.p) + i0 + at0) = make_uint4(w[0], w[1], w[2], w[3]);
-      } else {
-        float4* f = reinterpret_cast<float4*>(static_cast<float*>(T.p) + i0 + at0);
-        f[0] = make_float4(p[0], p[1], p[2], p[3]);
-        f[1] = make_float4(p[4], p[5], p[6], p[7]);
-      }
-      if constexpr (B8) {
-        auto four = [](const uint32_t* c) { return c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24; };
-        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(T.m) + i0 + at0) = make_uint2(four(cm), four(cm + 4));
-        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(T.v) + i0 + at0) = make_uint2(four(cv), four(cv + 4));
-      } else {
-        float4* a = reinterpret_cast<float4*>(static_cast<float*>(T.m) + i0 + at0);
-        float4* b = reinterpret_cast<float4*>(static_cast<float*>(T.v) + i0 + at0);
-        a[0] = make_float4(m[0], m[1], m[2], m[3]);
-        a[1] = make_float4(m[4], m[5], m[6], m[7]);
-        b[0] = make_float4(v[0], v[1], v[2], v[3]);
-        b[1] = make_float4(v[4], v[5], v[6], v[7]);
-      }
+      m = decode<true>(make_uint2(f.m.a.x, f.m.a.y), f.sm);
+      v = decode<false>(make_uint2(f.v.a.x, f.v.a.y), f.sv);
     } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int at = lane + 32 * k;
-        if (at >= left) continue;
-        if constexpr (PB) static_cast<uint16_t*>(T.p)[i0 + at] = static_cast<uint16_t>(bf16_stochastic(p[k], h[k]));
-        else static_cast<float*>(T.p)[i0 + at] = p[k];
-        if constexpr (B8) {
-          static_cast<uint8_t*>(T.m)[i0 + at] = static_cast<uint8_t>(cm[k]);
-          static_cast<uint8_t*>(T.v)[i0 + at] = static_cast<uint8_t>(cv[k]);
-        } else {
-          static_cast<float*>(T.m)[i0 + at] = m[k];
-          static_cast<float*>(T.v)[i0 + at] = v[k];
-        }
-      }
+      m = align<false>(f.m, T.m, lane);
+      v = align<false>(f.v, T.v, lane);
     }
+    step_block<PB, GB, B8, true>(P, T, blk, lane, kQBlock, gs, p, g, m, v);
+  } else {  // a tensor's last block, and arrays off the vectors' boundaries
+    Eight p = load_strided<PB>(T.p, i0, lane, left);
+    const Eight g = load_strided<GB>(T.g, i0, lane, left);
+    if constexpr (B8) {
+      m = decode<true>(load_codes_strided(T.m, i0, lane, left), T.ms[blk]);
+      v = decode<false>(load_codes_strided(T.v, i0, lane, left), T.vs[blk]);
+    } else {
+      m = load_strided<false>(T.m, i0, lane, left);
+      v = load_strided<false>(T.v, i0, lane, left);
+    }
+    step_block<PB, GB, B8, false>(P, T, blk, lane, left, gs, p, g, m, v);
   }
 }
 
@@ -276,9 +478,12 @@ const KernelPtr kKernels[8] = {
     adamw_kernel<false, true, true>,   adamw_kernel<true, true, true>,
 };
 
+// Whether a lane may take eight neighbouring elements: 16-byte float32 arrays,
+// 8-byte codes; bfloat16 arrays may begin anywhere.
 bool vector_aligned(const adamw_tensor_desc& d) {
-  return aligned_to(d.param, 16) && aligned_to(d.grad, 16) && aligned_to(d.exp_avg, d.state_bits == 8 ? 8 : 16) &&
-         aligned_to(d.exp_avg_sq, d.state_bits == 8 ? 8 : 16);
+  const uintptr_t state = d.state_bits == 8 ? 8 : 16;
+  return (d.param_dtype == MUON_BF16 || aligned_to(d.param, 16)) && (d.grad_dtype == MUON_BF16 || aligned_to(d.grad, 16)) &&
+         aligned_to(d.exp_avg, state) && aligned_to(d.exp_avg_sq, state);
 }
 
 muon_status_t check_tensors(const adamw_tensor_desc* t, int n, bool need_grads) {
@@ -355,7 +560,7 @@ muon_status_t adamw_plan::build() {
     a.numel = d.numel;
     a.first = static_cast<int>(l.ctas);
     a.vec = vector_aligned(d);
-    l.ctas += (d.numel + kQBlock * kCtaBlocks - 1) / (kQBlock * kCtaBlocks);
+    l.ctas += (d.numel + kQBlock * kWarps - 1) / (kQBlock * kWarps);
     if (l.ctas > 0x7FFFFFFFLL) return MUON_ERR_TOO_LARGE;
     l.t.push_back(a);
     l.index.push_back(static_cast<int>(i));
