@@ -126,14 +126,34 @@ __device__ __forceinline__ Eight widen(uint4 q) {
   return x;
 }
 
-// What a lane reads of the warp's 256 entries of an array from `at` on, eight
-// a lane.  bfloat16 arrays may begin anywhere: off a 4-byte boundary a lane
-// reads the three words inside its entries and one that it shares with the
-// next lane, and takes its first entry from the lane before (align); nothing
-// outside the 256 entries is touched.
+// A block of a bfloat16 array that begins `off` bytes past a 16-byte boundary:
+// its 31 whole 16-byte vectors pass as such, the eight entries at its two ends
+// one by one (nothing outside the block is touched), and shared memory moves
+// the lanes' eight entries to where the vectors put them.
+struct alignas(16) Shift {
+  unsigned char bytes[528];
+};
+
+__device__ __forceinline__ unsigned offset_of(const void* at) { return static_cast<unsigned>(reinterpret_cast<uintptr_t>(at)) & 15u; }
+
+// Which of the block's entries lane 0 .. 7 passes.
+__device__ __forceinline__ int end_entry(int lane, unsigned off) { return lane < static_cast<int>(16 - off) / 2 ? lane : 248 + lane; }
+
+// 16 bytes from an even place on.
+__device__ __forceinline__ uint4 gather16(const Shift& s, unsigned byte) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(s.bytes) + byte / 4;
+  uint4 q = make_uint4(w[0], w[1], w[2], w[3]);
+  if (byte & 2u) {
+    const uint32_t e = w[4];
+    q = make_uint4(__byte_perm(q.x, q.y, 0x5432), __byte_perm(q.y, q.z, 0x5432), __byte_perm(q.z, q.w, 0x5432), __byte_perm(q.w, e, 0x5432));
+  }
+  return q;
+}
+
+// What a lane reads of the warp's 256 entries of an array from `i` on.
 struct Raw {
-  uint4 a, b;      // float32: eight entries; bfloat16: a
-  uint32_t first;  // lane 0's first entry where the words are shared
+  uint4 a, b;  // float32: eight entries; bfloat16: a
+  uint16_t end;
 };
 
 template <bool BF16>
@@ -141,19 +161,10 @@ __device__ __forceinline__ Raw fetch(const void* base, long long i, int lane) {
   Raw r{};
   if constexpr (BF16) {
     const __nv_bfloat16* at = static_cast<const __nv_bfloat16*>(base) + i;
-    const __nv_bfloat16* a = at + 8 * lane;
-    const unsigned off = static_cast<unsigned>(reinterpret_cast<uintptr_t>(at)) & 15u;
-    if (off == 0) {
-      r.a = *reinterpret_cast<const uint4*>(a);
-    } else if ((off & 2u) == 0) {
-      const uint32_t* w = reinterpret_cast<const uint32_t*>(a);
-      r.a = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
-      const uint32_t* w = reinterpret_cast<const uint32_t*>(a + 1);
-      const uint16_t* h = reinterpret_cast<const uint16_t*>(a);
-      r.a = make_uint4(w[0], w[1], w[2], lane < 31 ? w[3] : h[7]);
-      if (lane == 0) r.first = static_cast<uint32_t>(h[0]) << 16;
-    }
+    const unsigned off = offset_of(at);
+    const unsigned char* v = reinterpret_cast<const unsigned char*>(at) - off + 16 * lane;
+    if (off == 0 || lane > 0) r.a = *reinterpret_cast<const uint4*>(v);
+    if (off != 0 && lane < 8) r.end = reinterpret_cast<const uint16_t*>(at)[end_entry(lane, off)];
   } else {
     const uint4* f = reinterpret_cast<const uint4*>(static_cast<const float*>(base) + i + 8 * lane);
     r.a = f[0];
@@ -162,16 +173,17 @@ __device__ __forceinline__ Raw fetch(const void* base, long long i, int lane) {
   return r;
 }
 
+// A lane's eight entries from what the warp has read.
 template <bool BF16>
-__device__ __forceinline__ Eight align(const Raw& r, const void* base, int lane) {
+__device__ __forceinline__ Eight align(const Raw& r, const void* base, int lane, Shift& s) {
   if constexpr (BF16) {
-    uint4 q = r.a;
-    if (reinterpret_cast<uintptr_t>(base) & 2u) {  // a block is a multiple of 4 bytes
-      uint32_t before = __shfl_up_sync(0xFFFFFFFFu, q.w, 1);
-      if (lane == 0) before = r.first;
-      q = make_uint4(__byte_perm(before, q.x, 0x5432), __byte_perm(q.x, q.y, 0x5432), __byte_perm(q.y, q.z, 0x5432),
-                     __byte_perm(q.z, q.w, 0x5432));
-    }
+    const unsigned off = offset_of(base);  // a block is a multiple of 16 bytes
+    if (off == 0) return widen(r.a);
+    if (lane > 0) *reinterpret_cast<uint4*>(s.bytes + 16 * lane) = r.a;
+    if (lane < 8) *reinterpret_cast<uint16_t*>(s.bytes + off + 2 * end_entry(lane, off)) = r.end;
+    __syncwarp();
+    const uint4 q = gather16(s, off + 16 * lane);
+    __syncwarp();
     return widen(q);
   } else {
     auto f = [](uint32_t x, uint32_t y) { return make_float2(__uint_as_float(x), __uint_as_float(y)); };
@@ -179,27 +191,20 @@ __device__ __forceinline__ Eight align(const Raw& r, const void* base, int lane)
   }
 }
 
-__device__ __forceinline__ void store_bf16(__nv_bfloat16* at, int lane, uint4 q) {
-  __nv_bfloat16* a = at + 8 * lane;
-  const unsigned off = static_cast<unsigned>(reinterpret_cast<uintptr_t>(at)) & 15u;
+__device__ __forceinline__ void store_bf16(__nv_bfloat16* at, int lane, uint4 q, Shift& s) {
+  const unsigned off = offset_of(at);
+  unsigned char* v = reinterpret_cast<unsigned char*>(at) - off + 16 * lane;
   if (off == 0) {
-    *reinterpret_cast<uint4*>(a) = q;
+    *reinterpret_cast<uint4*>(v) = q;
     return;
   }
-  if ((off & 2u) == 0) {
-    uint32_t* w = reinterpret_cast<uint32_t*>(a);
-    w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
-    return;
+  *reinterpret_cast<uint4*>(s.bytes + 16 * lane) = q;
+  __syncwarp();
+  if (lane > 0) *reinterpret_cast<uint4*>(v) = gather16(s, 16 * lane - off);
+  if (lane < 8) {
+    const int e = end_entry(lane, off);
+    reinterpret_cast<uint16_t*>(at)[e] = *reinterpret_cast<const uint16_t*>(s.bytes + 2 * e);
   }
-  uint32_t* w = reinterpret_cast<uint32_t*>(a + 1);
-  uint16_t* h = reinterpret_cast<uint16_t*>(a);
-  const uint32_t after = __shfl_down_sync(0xFFFFFFFFu, q.x, 1);
-  w[0] = __byte_perm(q.x, q.y, 0x5432);
-  w[1] = __byte_perm(q.y, q.z, 0x5432);
-  w[2] = __byte_perm(q.z, q.w, 0x5432);
-  if (lane < 31) w[3] = __byte_perm(q.w, after, 0x5432);
-  else h[7] = static_cast<uint16_t>(q.w >> 16);
-  if (lane == 0) h[0] = static_cast<uint16_t>(q.x);
 }
 
 __device__ __forceinline__ void store_f32(float* at, int lane, const Eight& x) {
@@ -368,7 +373,7 @@ __device__ __forceinline__ Fetched fetch_block(const AdamwTensor& T, long long b
 // layout, all of them (VEC) in the vector layout.
 template <bool PB, bool GB, bool B8, bool VEC>
 __device__ __forceinline__ void step_block(const AdamwParams& P, const AdamwTensor& T, long long blk, int lane, int left, float gs,
-                                           Eight& p, const Eight& g, Eight& m, Eight& v) {
+                                           Eight& p, const Eight& g, Eight& m, Eight& v, Shift& s) {
   const long long i0 = blk * kQBlock;
   update(P, T.step, T.decay, gs, g, p, m, v);
   uint32_t h[8];
@@ -391,7 +396,7 @@ __device__ __forceinline__ void step_block(const AdamwParams& P, const AdamwTens
     }
   }
   if constexpr (VEC) {
-    if constexpr (PB) store_bf16(static_cast<__nv_bfloat16*>(T.p) + i0, lane, narrow(p, h));
+    if constexpr (PB) store_bf16(static_cast<__nv_bfloat16*>(T.p) + i0, lane, narrow(p, h), s);
     else store_f32(static_cast<float*>(T.p) + i0, lane, p);
     if constexpr (B8) {
       *reinterpret_cast<uint2*>(static_cast<uint8_t*>(T.m) + i0 + 8 * lane) = cm;
@@ -436,6 +441,8 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constan
     if (P.t[mid].first <= static_cast<int>(blockIdx.x)) lo = mid; else hi = mid - 1;
   }
   const AdamwTensor& T = P.t[lo];
+  __shared__ Shift shift[PB || GB ? kWarps : 1];
+  Shift& s = shift[PB || GB ? threadIdx.x >> 5 : 0];
   const int lane = threadIdx.x & 31;
   const float gs = P.grad_scale ? *P.grad_scale : 1.0f;
   const long long blk = static_cast<long long>(blockIdx.x - T.first) * kWarps + (threadIdx.x >> 5), i0 = blk * kQBlock;
@@ -445,16 +452,16 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constan
   Eight m, v;
   if (T.vec && left == kQBlock) {
     const Fetched f = fetch_block<PB, GB, B8>(T, blk, lane);
-    Eight p = align<PB>(f.p, T.p, lane);
-    const Eight g = align<GB>(f.g, T.g, lane);
+    Eight p = align<PB>(f.p, T.p, lane, s);
+    const Eight g = align<GB>(f.g, T.g, lane, s);
     if constexpr (B8) {
       m = decode<true>(make_uint2(f.m.a.x, f.m.a.y), f.sm);
       v = decode<false>(make_uint2(f.v.a.x, f.v.a.y), f.sv);
     } else {
-      m = align<false>(f.m, T.m, lane);
-      v = align<false>(f.v, T.v, lane);
+      m = align<false>(f.m, T.m, lane, s);
+      v = align<false>(f.v, T.v, lane, s);
     }
-    step_block<PB, GB, B8, true>(P, T, blk, lane, kQBlock, gs, p, g, m, v);
+    step_block<PB, GB, B8, true>(P, T, blk, lane, kQBlock, gs, p, g, m, v, s);
   } else {  // a tensor's last block, and arrays off the vectors' boundaries
     Eight p = load_strided<PB>(T.p, i0, lane, left);
     const Eight g = load_strided<GB>(T.g, i0, lane, left);
@@ -465,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constan
       m = load_strided<false>(T.m, i0, lane, left);
       v = load_strided<false>(T.v, i0, lane, left);
     }
-    step_block<PB, GB, B8, false>(P, T, blk, lane, left, gs, p, g, m, v);
+    step_block<PB, GB, B8, false>(P, T, blk, lane, left, gs, p, g, m, v, s);
   }
 }
 
