@@ -7,8 +7,8 @@ not pass one, and raises ``MuonError`` on a non-OK status.  It loads the
 library on first use and fails loudly if it has not been built.
 """
 
-import contextlib
 import ctypes
+import functools
 import os
 from typing import NamedTuple, Optional
 
@@ -552,9 +552,36 @@ def fp8_mm_backward(g, x_f8, w_f8, x_s, w_s, grad_s, grad_x=None, grad_w=None, g
     return grad_x, grad_w, g_f8.view(torch.float8_e5m2)
 
 
-def _on(dev):
-    """Makes `dev` the current device for a call (nothing to do when it is)."""
-    return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+# The operators below are called for a few microseconds of GPU work at a time:
+# their host side avoids temporary objects (tensor devices, stream objects,
+# context managers, ctypes wrappers).
+
+def _index_of(what, *tensors):
+    """Index of the one CUDA device that all tensors (None: left out) are on."""
+    index = -1
+    for t in tensors:
+        if t is None:
+            continue
+        i = t.get_device()
+        if i < 0 or (i != index and index >= 0):
+            _device_of([u for u in tensors if u is not None], what)  # raises with the reason
+        index = i
+    return index
+
+
+def _call(fn, what, index, stream, *args):
+    """fn(*args, stream) with device `index` current; raises on an error."""
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        stream = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if torch.cuda.current_device() == index:
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, stream)
+    if status != MUON_OK:
+        raise MuonError(status, what)
 
 
 #: elements that share one scale of an 8-bit moment
@@ -624,12 +651,12 @@ def _adamw_descs(params, grads, states, lr, weight_decay):
     return arr, n, every
 
 
-def _grad_scale(t, dev):
+def _grad_scale(t, index):
     if t is None:
         return None
-    if t.dtype != torch.float32 or t.numel() != 1 or t.device != dev:
+    if t.dtype != torch.float32 or t.numel() != 1 or t.get_device() != index:
         raise ValueError("grad_scale must be one float32 value on the parameters' device")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def adamw_step(params, grads, states, step, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01,
@@ -644,11 +671,9 @@ def adamw_step(params, grads, states, step, lr=1e-3, beta1=0.9, beta2=0.999, eps
     arr, n, every = _adamw_descs(params, grads, states, lr, weight_decay)
     if n == 0:
         return
-    dev = _device_of(every, "adamw_step")
-    with _on(dev):
-        st = lib().adamw_step(arr, n, float(beta1), float(beta2), float(eps), int(bool(cautious)), int(step),
-                              int(seed) & (2 ** 64 - 1), _grad_scale(grad_scale, dev), _stream(stream))
-    _check(st, "adamw_step")
+    index = _index_of("adamw_step", *every)
+    _call(lib().adamw_step, "adamw_step", index, stream, arr, n, float(beta1), float(beta2), float(eps),
+          int(bool(cautious)), int(step), int(seed) & (2 ** 64 - 1), _grad_scale(grad_scale, index))
 
 
 class AdamW:
@@ -674,7 +699,7 @@ class AdamW:
         if not self.params:
             raise ValueError("AdamW needs at least one parameter")
         arr, n, every = _adamw_descs(self.params, self.grads, self.states, lr, weight_decay)
-        self.device = _device_of(every, "AdamW")
+        self._index = _index_of("AdamW", *every)
         _check(lib().adamw_plan_create(arr, n, ctypes.byref(self._plan)), "AdamW")
 
     def __del__(self):
@@ -695,8 +720,8 @@ class AdamW:
         if len(grads) != n or any(g.numel() != p.numel() or not g.is_contiguous()
                                   for g, p in zip(grads, self.params)):
             raise ValueError("AdamW: one contiguous gradient of the parameter's size per parameter")
-        if _device_of(grads, "AdamW") != self.device:
-            raise ValueError(f"AdamW: gradients must be on {self.device}")
+        if _index_of("AdamW", *grads) != self._index:
+            raise ValueError("AdamW: gradients must be on the parameters' device")
         ptrs = (ctypes.c_void_p * n)(*[g.data_ptr() for g in grads])
         kinds = (ctypes.c_int32 * n)(*[_dtype_code(g) for g in grads])
         _check(lib().adamw_plan_set_grads(self._plan, ptrs, kinds), "AdamW.set_grads")
@@ -708,10 +733,8 @@ class AdamW:
             self.set_grads(grads)
         elif self.grads is None:
             raise ValueError("AdamW.step: no gradients given, here or at construction")
-        with _on(self.device):
-            st = lib().adamw_plan_step(self._plan, self.beta1, self.beta2, self.eps, self.cautious, self.steps + 1,
-                                       self.seed, _grad_scale(grad_scale, self.device), _stream(stream))
-        _check(st, "AdamW.step")
+        _call(lib().adamw_plan_step, "AdamW.step", self._index, stream, self._plan, self.beta1, self.beta2, self.eps,
+              self.cautious, self.steps + 1, self.seed, _grad_scale(grad_scale, self._index))
         self.steps += 1
 
     def state_values(self):
@@ -741,26 +764,28 @@ def _matrix(t, what):
 
 
 def _per_row(t, rows, dtype, what):
+    if t is None:
+        return None
     if t.shape != (rows,) or t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {dtype} tensor with one entry per row")
-    return ctypes.c_void_p(t.data_ptr())
-
-
-def _ptr(t):
-    return ctypes.c_void_p(t.data_ptr()) if t is not None else None
+    return t.data_ptr()
 
 
 def _score_outputs(rows, top, dev):
-    logprobs, lse, entropy = (torch.empty(rows, dtype=torch.float32, device=dev) for _ in range(3))
+    """(tensors, pointers) of logprobs, lse, entropy, top_logprobs, top_ids."""
+    out = torch.empty((3, rows), dtype=torch.float32, device=dev)
+    p = out.data_ptr()
+    pointers = (p, p + 4 * rows, p + 8 * rows)
     if not top:
-        return logprobs, lse, entropy, None, None
-    return (logprobs, lse, entropy, torch.empty((rows, top), dtype=torch.float32, device=dev),
-            torch.empty((rows, top), dtype=torch.int64, device=dev))
+        return (*out.unbind(), None, None), (*pointers, None, None)
+    values = torch.empty((rows, top), dtype=torch.float32, device=dev)
+    ids = torch.empty((rows, top), dtype=torch.int64, device=dev)
+    return (*out.unbind(), values, ids), (*pointers, values.data_ptr(), ids.data_ptr())
 
 
 def _grad_out(out, logits):
     if out is None:
-        out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        return torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
     if out.shape != logits.shape or out.dtype != logits.dtype:
         raise ValueError("out must have the logits' shape and dtype")
     return out
@@ -772,14 +797,11 @@ def token_logprobs(logits, targets, top=0, scale=1.0, stream=None):
     the `top` (<= 32) most likely entries: a TokenLogprobs.  logits: rows x
     vocab, bfloat16 or float32, any row pitch.  See include/muon.h."""
     rows, vocab, pitch = _matrix(logits, "logits")
-    dev = _device_of((logits, targets), "token_logprobs")
+    index = _index_of("token_logprobs", logits, targets)
     y = _per_row(targets, rows, torch.int64, "targets")
-    out = _score_outputs(rows, top, dev)
-    with _on(dev):
-        st = lib().token_logprobs(_ptr(logits), _dtype_code(logits), rows, vocab, pitch, y, float(scale), int(top),
-                                  _ptr(out[0]), _ptr(out[1]), _ptr(out[2]), _ptr(out[3]), _ptr(out[4]),
-                                  _stream(stream))
-    _check(st, "token_logprobs")
+    out, p = _score_outputs(rows, top, logits.device)
+    _call(lib().token_logprobs, "token_logprobs", index, stream, logits.data_ptr(), _dtype_code(logits), rows, vocab,
+          pitch, y, scale, top, *p)
     return TokenLogprobs(*out)
 
 
@@ -789,22 +811,16 @@ def token_logprobs_backward(logits, targets, lse, grad_logprobs, entropy=None, g
     logprobs and, with `entropy` as token_logprobs gave it, entropy.  `out`
     may be the logits themselves.  See include/muon.h."""
     rows, vocab, pitch = _matrix(logits, "logits")
-    out = _grad_out(out, logits)
-    out_pitch = _matrix(out, "out")[2]
     if grad_entropy is not None and entropy is None:
         raise ValueError("grad_entropy needs entropy")
-    dev = _device_of([t for t in (logits, targets, lse, grad_logprobs, entropy, grad_entropy, out) if t is not None],
-                     "token_logprobs_backward")
+    out = _grad_out(out, logits)
+    index = _index_of("token_logprobs_backward", logits, targets, lse, grad_logprobs, entropy, grad_entropy, out)
     f32 = torch.float32
-    with _on(dev):
-        st = lib().token_logprobs_backward(
-            _ptr(logits), _dtype_code(logits), rows, vocab, pitch, _per_row(targets, rows, torch.int64, "targets"),
-            float(scale), _per_row(lse, rows, f32, "lse"),
-            _per_row(entropy, rows, f32, "entropy") if entropy is not None else None,
-            _per_row(grad_logprobs, rows, f32, "grad_logprobs"),
-            _per_row(grad_entropy, rows, f32, "grad_entropy") if grad_entropy is not None else None,
-            _ptr(out), out_pitch, _stream(stream))
-    _check(st, "token_logprobs_backward")
+    _call(lib().token_logprobs_backward, "token_logprobs_backward", index, stream, logits.data_ptr(),
+          _dtype_code(logits), rows, vocab, pitch, _per_row(targets, rows, torch.int64, "targets"), scale,
+          _per_row(lse, rows, f32, "lse"), _per_row(entropy, rows, f32, "entropy"),
+          _per_row(grad_logprobs, rows, f32, "grad_logprobs"), _per_row(grad_entropy, rows, f32, "grad_entropy"),
+          out.data_ptr(), _matrix(out, "out")[2])
     return out
 
 
@@ -815,33 +831,29 @@ def token_logprobs_loss(logits, targets, grad_logprobs, grad_entropy=None, top=0
     See include/muon.h."""
     rows, vocab, pitch = _matrix(logits, "logits")
     out = _grad_out(out, logits)
-    out_pitch = _matrix(out, "out")[2]
-    dev = _device_of([t for t in (logits, targets, grad_logprobs, grad_entropy, out) if t is not None],
-                     "token_logprobs_loss")
-    y, gl = _per_row(targets, rows, torch.int64, "targets"), _per_row(grad_logprobs, rows, torch.float32, "grad_logprobs")
-    ge = _per_row(grad_entropy, rows, torch.float32, "grad_entropy") if grad_entropy is not None else None
-    got = _score_outputs(rows, top, dev)
-    with _on(dev):
-        st = lib().token_logprobs_loss(_ptr(logits), _dtype_code(logits), rows, vocab, pitch, y, float(scale), int(top),
-                                       gl, ge, _ptr(got[0]), _ptr(got[1]), _ptr(got[2]), _ptr(got[3]), _ptr(got[4]),
-                                       _ptr(out), out_pitch, _stream(stream))
-    _check(st, "token_logprobs_loss")
+    index = _index_of("token_logprobs_loss", logits, targets, grad_logprobs, grad_entropy, out)
+    f32 = torch.float32
+    gl, ge = _per_row(grad_logprobs, rows, f32, "grad_logprobs"), _per_row(grad_entropy, rows, f32, "grad_entropy")
+    y = _per_row(targets, rows, torch.int64, "targets")
+    got, p = _score_outputs(rows, top, logits.device)
+    _call(lib().token_logprobs_loss, "token_logprobs_loss", index, stream, logits.data_ptr(), _dtype_code(logits),
+          rows, vocab, pitch, y, scale, top, gl, ge, *p, out.data_ptr(), _matrix(out, "out")[2])
     return TokenLogprobs(*got, out)
 
 
 class BalanceLoss(NamedTuple):
     """What balance_loss gives: the losses (0-d), int32 counts (groups x
     experts) and token numbers (groups), mean router probabilities (groups x
-    experts), and what balance_loss_backward reads."""
+    experts), and `saved`, which balance_loss_backward reads."""
     balance: torch.Tensor
     z: torch.Tensor
     counts: torch.Tensor
     tokens: torch.Tensor
     mean_probs: torch.Tensor
-    stats: torch.Tensor
-    weights: torch.Tensor
+    saved: torch.Tensor
 
 
+@functools.lru_cache(maxsize=256)
 def balance_loss_workspace_size(tokens, experts, groups=1):
     return lib().balance_loss_workspace_size(int(tokens), int(experts), int(groups))
 
@@ -851,7 +863,7 @@ def _mask(mask, tokens):
         return None
     if mask.shape != (tokens,) or mask.dtype not in (torch.bool, torch.uint8) or not mask.is_contiguous():
         raise ValueError("mask must be a contiguous bool tensor with one entry per token")
-    return ctypes.c_void_p(mask.data_ptr())
+    return mask.data_ptr()
 
 
 def balance_loss(logits, ids, mask=None, groups=1, workspace=None, stream=None):
@@ -862,20 +874,21 @@ def balance_loss(logits, ids, mask=None, groups=1, workspace=None, stream=None):
     tokens, experts, pitch = _matrix(logits, "logits")
     if ids.dim() != 2 or ids.shape[0] != tokens or ids.dtype != torch.int64 or not ids.is_contiguous():
         raise ValueError("ids must be a contiguous tokens x top int64 tensor")
-    dev = _device_of([t for t in (logits, ids, mask, workspace) if t is not None], "balance_loss")
-    f32, i32 = torch.float32, torch.int32
-    stats = torch.empty(4, dtype=f32, device=dev)
-    counts = torch.empty((groups, experts), dtype=i32, device=dev)
-    n_tokens = torch.empty(groups, dtype=i32, device=dev)
-    mean, weights = (torch.empty((groups, experts), dtype=f32, device=dev) for _ in range(2))
-    with _on(dev):
-        if workspace is None:
-            workspace = new_workspace(balance_loss_workspace_size(tokens, experts, groups), dev)
-        st = lib().balance_loss(_ptr(logits), _dtype_code(logits), tokens, experts, pitch, _ptr(ids), ids.shape[1],
-                                _mask(mask, tokens), int(groups), _ptr(stats), _ptr(counts), _ptr(n_tokens),
-                                _ptr(mean), _ptr(weights), _ptr(workspace), workspace.numel(), _stream(stream))
-    _check(st, "balance_loss")
-    return BalanceLoss(stats[0], stats[1], counts, n_tokens, mean, stats, weights)
+    index = _index_of("balance_loss", logits, ids, mask, workspace)
+    dev, f32 = logits.device, torch.float32
+    # saved: the four statistics, then the weights
+    saved = torch.empty(4 + groups * experts, dtype=f32, device=dev)
+    counts = torch.empty((groups, experts), dtype=torch.int32, device=dev)
+    n_tokens = torch.empty(groups, dtype=torch.int32, device=dev)
+    mean = torch.empty((groups, experts), dtype=f32, device=dev)
+    if workspace is None:
+        workspace = torch.empty(max(balance_loss_workspace_size(tokens, experts, groups), 256), dtype=torch.uint8,
+                                device=dev)
+    stats = saved.data_ptr()
+    _call(lib().balance_loss, "balance_loss", index, stream, logits.data_ptr(), _dtype_code(logits), tokens, experts,
+          pitch, ids.data_ptr(), ids.shape[1], _mask(mask, tokens), groups, stats, counts.data_ptr(),
+          n_tokens.data_ptr(), mean.data_ptr(), stats + 16, workspace.data_ptr(), workspace.numel())
+    return BalanceLoss(saved.select(0, 0), saved.select(0, 1), counts, n_tokens, mean, saved)
 
 
 def balance_loss_backward(logits, result, grad_balance, grad_z, mask=None, out=None, stream=None):
@@ -884,18 +897,15 @@ def balance_loss_backward(logits, result, grad_balance, grad_z, mask=None, out=N
     the same logits and mask.  `out` may be the logits themselves."""
     tokens, experts, pitch = _matrix(logits, "logits")
     out = _grad_out(out, logits)
-    out_pitch = _matrix(out, "out")[2]
-    groups = result.counts.shape[0]
-    if result.counts.shape[1] != experts:
+    groups, columns = result.counts.shape
+    if columns != experts:
         raise ValueError("result is of other logits")
-    for t in (grad_balance, grad_z):
-        if t.dtype != torch.float32 or t.numel() != 1:
-            raise ValueError("grad_balance and grad_z must be one-element float32 tensors")
-    dev = _device_of([t for t in (logits, mask, grad_balance, grad_z, out, result.stats) if t is not None],
-                     "balance_loss_backward")
-    with _on(dev):
-        st = lib().balance_loss_backward(_ptr(logits), _dtype_code(logits), tokens, experts, pitch,
-                                         _mask(mask, tokens), groups, _ptr(result.stats), _ptr(result.weights),
-                                         _ptr(grad_balance), _ptr(grad_z), _ptr(out), out_pitch, _stream(stream))
-    _check(st, "balance_loss_backward")
+    if (grad_balance.dtype != torch.float32 or grad_z.dtype != torch.float32 or grad_balance.numel() != 1
+            or grad_z.numel() != 1):
+        raise ValueError("grad_balance and grad_z must be one-element float32 tensors")
+    stats = result.saved.data_ptr()
+    index = _index_of("balance_loss_backward", logits, mask, grad_balance, grad_z, out, result.saved)
+    _call(lib().balance_loss_backward, "balance_loss_backward", index, stream, logits.data_ptr(), _dtype_code(logits),
+          tokens, experts, pitch, _mask(mask, tokens), groups, stats, stats + 16, grad_balance.data_ptr(),
+          grad_z.data_ptr(), out.data_ptr(), _matrix(out, "out")[2])
     return out

@@ -167,7 +167,7 @@ def test_workspace_is_reused_whatever_it_holds():
     ws = torch.full((muon.balance_loss_workspace_size(3000, 40, 3),), 0xAB, dtype=torch.uint8, device="cuda")
     a = muon.balance_loss(x.cuda(), dev(ids), groups=3, workspace=ws)
     b = muon.balance_loss(x.cuda(), dev(ids), groups=3)
-    assert torch.equal(a.stats, b.stats) and torch.equal(a.weights, b.weights)
+    assert torch.equal(a.saved, b.saved) and torch.equal(a.mean_probs, b.mean_probs)
     with pytest.raises(muon.MuonError):
         muon.balance_loss(x.cuda(), dev(ids), groups=3, workspace=ws[:256])
 
