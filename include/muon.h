@@ -428,7 +428,7 @@ muon_status_t token_logprobs_loss(const void* logits, int dtype, int64_t rows, i
  *   z       = mean over all kept tokens of lse^2, lse = log(sum_e exp(logit_e)).
  * A group without tokens has zeros, and without any token both losses are 0.
  *   ids    tokens x top int64;   mask: tokens bytes (0: the token is left
- *          out and its logits are not read), or NULL;
+ *          out, whatever its logits are), or NULL;
  *   stats  4 floats, written: balance, z, 1 / (groups with tokens), 2 / (kept
  *          tokens) (0 where there are none);
  *   counts, n_tokens  int32, written;   mean_probs groups x experts floats;

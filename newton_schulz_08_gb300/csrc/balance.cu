@@ -10,13 +10,21 @@
 // the load is nearly balanced).
 //
 // A row has at most 1024 entries, so it lives in registers: L lanes (a power
-// of two) share a row, 8 entries a lane and chunk of 8 L, and 32 / L rows go
-// through a warp at a time.  HBM-bound: a row is read once forward, read and
-// written once backward.
+// of two) share a row, 8 entries a lane and chunk of 8 L.  A warp takes
+// 32 / L rows side by side and, up to 512 experts, two such sets at a time:
+// the reductions of a row are a chain of ten shuffles, and two chains overlap
+// (131072 x 256 float32: forward 44 -> 36 us, backward 56 -> 48; four sets
+// leave room for fewer warps: 43 and 55).  HBM-bound: a row is read once
+// forward, read and written once backward.
+// Rows off the 16-byte boundaries (an odd number of experts, up to 256) come
+// through shared memory in tiles instead, copied as one run: there a few
+// threads, without a shuffle each, take a row's sums, and then a thread an
+// expert's (65536 x 161 bfloat16: forward 28 -> TT1 us, backward 42 -> TT2,
+// against entry by entry from global memory).
 //
 // Forward, two launches.  balance_rows: each CTA takes consecutive rows of
-// one group and leaves partial sums of p and lse^2, counts and token numbers
-// in the workspace.  balance_finish: one CTA per group adds the partials in
+// one group and leaves partial sums of p and lse^2, counts and the numbers of
+// tokens and assignments in the workspace.  balance_finish: one CTA per group adds the partials in
 // their order, and the last CTA to arrive adds the groups in theirs, so equal
 // calls give equal bits; only whole numbers are added with atomics.
 #include <cuda_bf16.h>
@@ -38,6 +46,8 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kFinishThreads = 512;
 constexpr int kMaxExperts = 1024;
+constexpr int kTileExperts = 256;     // most experts of the tiled kernels
+constexpr int kTileBytes = 42 * 1024;  // of a tile: four CTAs per SM
 constexpr int kTargetCtas = 608;  // four per SM
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -52,11 +62,11 @@ struct BalanceParams {
   long long groups;
   int parts;             // CTAs per group
   int experts, top, lanes;
-  int vec;
-  // partial results of CTA i: sums[i][experts], counts[i][experts], tokens[i], squares[i]
+  int tile_rows;         // rows of a tile, a power of two up to kThreads
+  // partial results of CTA i: sums[i][experts], counts[i][experts], numbers[i] (tokens, assignments), squares[i]
   float* sums;
   int* part_counts;
-  int* part_tokens;
+  int2* numbers;
   float* squares;
   float* group_loss;
   unsigned* arrived;
@@ -78,11 +88,12 @@ __device__ __forceinline__ float ex2(float x) {
 
 // Position of a lane's entry k of chunk c: neighbours in the vector layout,
 // L apart where rows are not aligned.
+template <bool VEC>
 __device__ __forceinline__ int entry(const BalanceParams& P, int c, int k, int sub) {
-  return P.vec ? (c * P.lanes + sub) * 8 + k : c * P.lanes * 8 + k * P.lanes + sub;
+  return VEC ? (c * P.lanes + sub) * 8 + k : c * P.lanes * 8 + k * P.lanes + sub;
 }
 
-template <bool BF16, int NC>
+template <bool BF16, int NC, bool VEC>
 __device__ __forceinline__ void load_row(const BalanceParams& P, long long row, int sub, bool on, float (&x)[NC][8]) {
   const long long base = row * P.stride;
 #pragma unroll
@@ -90,8 +101,8 @@ __device__ __forceinline__ void load_row(const BalanceParams& P, long long row, 
 #pragma unroll
     for (int k = 0; k < 8; ++k) x[c][k] = -INFINITY;
     if (!on) continue;
-    const int e0 = entry(P, c, 0, sub);
-    if (P.vec) {
+    const int e0 = entry<VEC>(P, c, 0, sub);
+    if constexpr (VEC) {
       if (e0 >= P.experts) continue;
       if constexpr (BF16) {
         const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(P.x) + base + e0);
@@ -110,7 +121,7 @@ __device__ __forceinline__ void load_row(const BalanceParams& P, long long row, 
     } else {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const int e = entry(P, c, k, sub);
+        const int e = entry<VEC>(P, c, k, sub);
         if (e >= P.experts) continue;
         if constexpr (BF16) x[c][k] = __bfloat162float(static_cast<const __nv_bfloat16*>(P.x)[base + e]);
         else x[c][k] = static_cast<const float*>(P.x)[base + e];
@@ -119,48 +130,119 @@ __device__ __forceinline__ void load_row(const BalanceParams& P, long long row, 
   }
 }
 
-// x becomes the row's probabilities (0 where the row is off); returns lse.
-template <int NC>
-__device__ __forceinline__ float softmax_row(int lanes, bool on, float (&x)[NC][8]) {
-  float m = -INFINITY;
+template <bool BF16, int NC, bool VEC>
+__device__ __forceinline__ void store_row(const BalanceParams& P, long long row, int sub, const float (&x)[NC][8]) {
+  const long long base = row * P.grad_stride;
 #pragma unroll
-  for (int c = 0; c < NC; ++c)
+  for (int c = 0; c < NC; ++c) {
+    const int e0 = entry<VEC>(P, c, 0, sub);
+    if constexpr (VEC) {
+      if (e0 >= P.experts) continue;
+      if constexpr (BF16) {
+        uint32_t w[4];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) m = fmaxf(m, x[c][k]);
-  for (int d = lanes / 2; d > 0; d /= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-  float s = 0.0f;
+        for (int k = 0; k < 4; ++k) {
+          const __nv_bfloat162 b = __floats2bfloat162_rn(x[c][2 * k], x[c][2 * k + 1]);
+          w[k] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(P.grad) + base + e0) = make_uint4(w[0], w[1], w[2], w[3]);
+      } else {
+        float4* f = reinterpret_cast<float4*>(static_cast<float*>(P.grad) + base + e0);
+        f[0] = make_float4(x[c][0], x[c][1], x[c][2], x[c][3]);
+        f[1] = make_float4(x[c][4], x[c][5], x[c][6], x[c][7]);
+      }
+    } else {
 #pragma unroll
-  for (int c = 0; c < NC; ++c)
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      x[c][k] = ex2((x[c][k] - m) * kLog2e);
-      s += x[c][k];
+      for (int k = 0; k < 8; ++k) {
+        const int e = entry<VEC>(P, c, k, sub);
+        if (e >= P.experts) continue;
+        if constexpr (BF16) static_cast<__nv_bfloat16*>(P.grad)[base + e] = __float2bfloat16_rn(x[c][k]);
+        else static_cast<float*>(P.grad)[base + e] = x[c][k];
+      }
     }
-  for (int d = lanes / 2; d > 0; d /= 2) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
-  const float inv = on ? 1.0f / s : 0.0f;
-#pragma unroll
-  for (int c = 0; c < NC; ++c)
-#pragma unroll
-    for (int k = 0; k < 8; ++k) x[c][k] = on ? x[c][k] * inv : 0.0f;
-  return m + logf(s);
+  }
 }
 
-template <bool BF16, int NC>
-__global__ void __launch_bounds__(kThreads) balance_rows(const __grid_constant__ BalanceParams P) {
+// x becomes the rows' probabilities (0 where a row is off).  U rows of a lane
+// at a time.
+template <int NC, int U>
+__device__ __forceinline__ void softmax_rows(int lanes, const bool (&on)[U], float (&x)[U][NC][8], float (&lse)[U]) {
+  float m[U], s[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    m[u] = -INFINITY;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) m[u] = fmaxf(m[u], x[u][c][k]);
+  }
+  for (int d = lanes / 2; d > 0; d /= 2)
+#pragma unroll
+    for (int u = 0; u < U; ++u) m[u] = fmaxf(m[u], __shfl_xor_sync(0xFFFFFFFFu, m[u], d));
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    s[u] = 0.0f;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        x[u][c][k] = ex2((x[u][c][k] - m[u]) * kLog2e);
+        s[u] += x[u][c][k];
+      }
+  }
+  for (int d = lanes / 2; d > 0; d /= 2)
+#pragma unroll
+    for (int u = 0; u < U; ++u) s[u] += __shfl_xor_sync(0xFFFFFFFFu, s[u], d);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const float inv = 1.0f / s[u];
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[u][c][k] = on[u] ? x[u][c][k] * inv : 0.0f;
+    lse[u] = m[u] + logf(s[u]);
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ T warp_sum(T v) {
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+  return v;
+}
+
+// Sets of rows that a warp works on at a time.
+template <int NC>
+constexpr int kSets = NC <= 2 ? 2 : 1;
+
+template <bool BF16, int NC, bool VEC>
+__global__ void __launch_bounds__(kThreads, 4) balance_rows(const __grid_constant__ BalanceParams P) {
   extern __shared__ float smem[];
   float* sp = smem;                                               // kWarps x experts
   int* sc = reinterpret_cast<int*>(smem + kWarps * P.experts);    // experts
-  __shared__ int s_tokens[kWarps];
+  __shared__ int2 s_numbers[kWarps];
   __shared__ float s_sq[kWarps];
+  constexpr int kU = kSets<NC>;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane & (P.lanes - 1), rows_warp = 32 / P.lanes, mine = lane / P.lanes;
   const long long g = blockIdx.x / P.parts;
   const long long r0 = static_cast<long long>(blockIdx.x % P.parts) * P.cta_rows;
   const long long r1 = min(P.group_rows, r0 + P.cta_rows);
   const long long first = g * P.group_rows;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // balance_finish waits for this grid's end
   if (blockIdx.x == 0 && threadIdx.x == 0) *P.arrived = 0;
   for (int e = threadIdx.x; e < P.experts; e += kThreads) sc[e] = 0;
   __syncthreads();
+  // the assignments of this CTA's rows
+  int assigned = 0;
+  const long long i1 = (first + r1) * P.top;
+#pragma unroll 4
+  for (long long i = (first + r0) * P.top + threadIdx.x; i < i1; i += kThreads) {
+    const int64_t e = P.ids[i];
+    if (e < 0 || e >= P.experts || (P.mask && !P.mask[static_cast<unsigned>(i) / static_cast<unsigned>(P.top)])) continue;
+    atomicAdd(&sc[e], 1);
+    ++assigned;
+  }
 
   float acc[NC][8], sq = 0.0f;
   int tokens = 0;
@@ -168,27 +250,29 @@ __global__ void __launch_bounds__(kThreads) balance_rows(const __grid_constant__
   for (int c = 0; c < NC; ++c)
 #pragma unroll
     for (int k = 0; k < 8; ++k) acc[c][k] = 0.0f;
-  for (long long r = r0 + warp * rows_warp; r < r1; r += kWarps * rows_warp) {
-    const long long row = first + r + mine;
-    const bool on = r + mine < r1 && (!P.mask || P.mask[row]);
-    float x[NC][8];
-    load_row<BF16, NC>(P, row, sub, on, x);
-    const float lse = softmax_row<NC>(P.lanes, on, x);
+  for (long long r = r0 + warp * rows_warp; r < r1; r += kU * kWarps * rows_warp) {
+    float x[kU][NC][8];
+    bool on[kU];
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-      for (int k = 0; k < 8; ++k) acc[c][k] += x[c][k];
-    if (on && sub == 0) {
-      sq += lse * lse;
-      ++tokens;
+    for (int u = 0; u < kU; ++u) {
+      const long long at = r + u * kWarps * rows_warp + mine;
+      on[u] = at < r1 && (!P.mask || P.mask[first + at]);
     }
-  }
-  // the assignments of this CTA's rows
-  const long long i1 = (first + r1) * P.top;
-  for (long long i = (first + r0) * P.top + threadIdx.x; i < i1; i += kThreads) {
-    if (P.mask && !P.mask[i / P.top]) continue;
-    const int64_t e = P.ids[i];
-    if (e >= 0 && e < P.experts) atomicAdd(&sc[e], 1);
+#pragma unroll
+    for (int u = 0; u < kU; ++u) load_row<BF16, NC, VEC>(P, first + r + u * kWarps * rows_warp + mine, sub, on[u], x[u]);
+    float lse[kU];
+    softmax_rows<NC, kU>(P.lanes, on, x, lse);
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc[c][k] += x[u][c][k];
+      if (on[u] && sub == 0) {
+        sq += lse[u] * lse[u];
+        ++tokens;
+      }
+    }
   }
   // rows of a warp, then warps, in order
   for (int d = P.lanes; d < 32; d *= 2) {
@@ -202,63 +286,57 @@ __global__ void __launch_bounds__(kThreads) balance_rows(const __grid_constant__
     for (int c = 0; c < NC; ++c)
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const int e = entry(P, c, k, sub);
+        const int e = entry<VEC>(P, c, k, sub);
         if (e < P.experts) sp[warp * P.experts + e] = acc[c][k];
       }
   }
-  for (int d = 16; d > 0; d /= 2) {
-    sq += __shfl_xor_sync(0xFFFFFFFFu, sq, d);
-    tokens += __shfl_xor_sync(0xFFFFFFFFu, tokens, d);
-  }
-  if (lane == 0) s_sq[warp] = sq, s_tokens[warp] = tokens;
+  sq = warp_sum(sq);
+  tokens = warp_sum(tokens);
+  assigned = warp_sum(assigned);
+  if (lane == 0) s_sq[warp] = sq, s_numbers[warp] = make_int2(tokens, assigned);
   __syncthreads();
   const long long out = static_cast<long long>(blockIdx.x) * P.experts;
   for (int e = threadIdx.x; e < P.experts; e += kThreads) {
     float s = 0.0f;
+#pragma unroll
     for (int w = 0; w < kWarps; ++w) s += sp[w * P.experts + e];
     P.sums[out + e] = s;
     P.part_counts[out + e] = sc[e];
   }
   if (threadIdx.x == 0) {
     float s = 0.0f;
-    int n = 0;
-    for (int w = 0; w < kWarps; ++w) s += s_sq[w], n += s_tokens[w];
+    int2 n = make_int2(0, 0);
+    for (int w = 0; w < kWarps; ++w) s += s_sq[w], n.x += s_numbers[w].x, n.y += s_numbers[w].y;
     P.squares[blockIdx.x] = s;
-    P.part_tokens[blockIdx.x] = n;
+    P.numbers[blockIdx.x] = n;
   }
 }
 
-// Sum over the CTA's threads in a fixed order; every thread gets it.
-template <typename T>
-__device__ __forceinline__ T block_sum(T v, T* scratch) {
-  for (int d = 16; d > 0; d /= 2) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
-  __syncthreads();
-  T s = 0;
-  for (int w = 0; w < kFinishThreads / 32; ++w) s += scratch[w];
-  return s;
-}
-
+// One CTA per group.  Every warp adds up the numbers of tokens and
+// assignments for itself; the experts' partials are dealt over the threads.
 __global__ void __launch_bounds__(kFinishThreads) balance_finish(const __grid_constant__ BalanceParams P) {
   __shared__ float s_sum[kFinishThreads];
   __shared__ int s_cnt[kFinishThreads];
-  __shared__ float s_mean[kMaxExperts];
-  __shared__ int s_total[kMaxExperts];
-  __shared__ float f_scratch[kFinishThreads / 32];
-  __shared__ int i_scratch[kFinishThreads / 32];
+  __shared__ float s_loss[kFinishThreads / 32];
+  __shared__ float3 s_all[kFinishThreads / 32];
   __shared__ unsigned s_last;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int t = threadIdx.x, lane = t & 31;
   const long long g = blockIdx.x, base = g * P.parts;
-  int n = 0;
-  for (int i = threadIdx.x; i < P.parts; i += kFinishThreads) n += P.part_tokens[base + i];
-  n = block_sum(n, i_scratch);
-  const float inv_n = n > 0 ? 1.0f / static_cast<float>(n) : 0.0f;
   // `width` experts at a time, the partials dealt over the threads left
   int width = 32;
   while (width < P.experts && width < kFinishThreads) width *= 2;
-  const int deals = kFinishThreads / width, deal = threadIdx.x / width;
+  const int deals = kFinishThreads / width, deal = t / width;
+  int n = 0, assigned = 0;
+#pragma unroll 4
+  for (int i = lane; i < P.parts; i += 32) {
+    const int2 m = P.numbers[base + i];
+    n += m.x;
+    assigned += m.y;
+  }
+  float loss = 0.0f, inv_n = 0.0f, share = 0.0f;
   for (int e0 = 0; e0 < P.experts; e0 += width) {
-    const int e = e0 + (threadIdx.x & (width - 1));
+    const int e = e0 + (t & (width - 1));
     float s = 0.0f;
     int c = 0;
     if (e < P.experts) {
@@ -268,63 +346,72 @@ __global__ void __launch_bounds__(kFinishThreads) balance_finish(const __grid_co
         c += P.part_counts[(base + i) * P.experts + e];
       }
     }
-    __syncthreads();
-    s_sum[threadIdx.x] = s;
-    s_cnt[threadIdx.x] = c;
-    __syncthreads();
+    if (e0 == 0) {
+      n = warp_sum(n);
+      assigned = warp_sum(assigned);
+      inv_n = n > 0 ? 1.0f / static_cast<float>(n) : 0.0f;
+      share = assigned > 0 ? static_cast<float>(P.experts) / static_cast<float>(assigned) : 0.0f;
+    }
+    if (deals > 1) {
+      s_sum[t] = s;
+      s_cnt[t] = c;
+      __syncthreads();
+      if (deal == 0)
+        for (int k = 1; k < deals; ++k) s += s_sum[k * width + t], c += s_cnt[k * width + t];
+    }
     if (deal == 0 && e < P.experts) {
-      for (int k = 1; k < deals; ++k) s += s_sum[k * width + threadIdx.x], c += s_cnt[k * width + threadIdx.x];
-      s_mean[e] = s * inv_n;
-      s_total[e] = c;
+      const float mean = s * inv_n, f = share * static_cast<float>(c);  // experts * f_e
+      loss += f * mean;
+      P.counts[g * P.experts + e] = c;
+      P.mean[g * P.experts + e] = mean;
+      P.weights[g * P.experts + e] = assigned > 0 ? (f - 1.0f) * inv_n : 0.0f;
     }
   }
+  loss = warp_sum(loss);
+  if (lane == 0) s_loss[t >> 5] = loss;
   __syncthreads();
-  int assigned = 0;
-  for (int e = threadIdx.x; e < P.experts; e += kFinishThreads) assigned += s_total[e];
-  assigned = block_sum(assigned, i_scratch);
-  const float share = assigned > 0 ? static_cast<float>(P.experts) / static_cast<float>(assigned) : 0.0f;
-  float loss = 0.0f;
-  for (int e = threadIdx.x; e < P.experts; e += kFinishThreads) {
-    const float f = share * static_cast<float>(s_total[e]);  // experts * f_e
-    loss += f * s_mean[e];
-    P.counts[g * P.experts + e] = s_total[e];
-    P.mean[g * P.experts + e] = s_mean[e];
-    P.weights[g * P.experts + e] = assigned > 0 ? (f - 1.0f) * inv_n : 0.0f;
-  }
-  loss = block_sum(loss, f_scratch);
-  if (threadIdx.x == 0) {
+  if (t == 0) {
+    loss = 0.0f;
+    for (int w = 0; w < kFinishThreads / 32; ++w) loss += s_loss[w];
     P.group_loss[g] = loss;
     P.tokens[g] = n;
     __threadfence();
-    s_last = atomicAdd(P.arrived, 1u) + 1u == gridDim.x;
+    s_last = gridDim.x == 1 || atomicAdd(P.arrived, 1u) + 1u == gridDim.x;
   }
   __syncthreads();
   if (!s_last) return;
   __threadfence();
-  float balance = 0.0f, squares = 0.0f;
-  float kept = 0.0f;
+  float3 all = make_float3(0.0f, 0.0f, 0.0f);  // losses, squares, tokens
   int some = 0;
-  for (long long i = threadIdx.x; i < P.groups; i += kFinishThreads) {
-    balance += __ldcg(P.group_loss + i);
-    const int t = __ldcg(P.tokens + i);
-    kept += static_cast<float>(t);
-    some += t > 0;
+  for (long long i = t; i < P.groups; i += kFinishThreads) {
+    all.x += __ldcg(P.group_loss + i);
+    const int k = __ldcg(P.tokens + i);
+    all.z += static_cast<float>(k);
+    some += k > 0;
   }
-  for (long long i = threadIdx.x; i < P.groups * P.parts; i += kFinishThreads) squares += P.squares[i];
-  balance = block_sum(balance, f_scratch);
-  squares = block_sum(squares, f_scratch);
-  kept = block_sum(kept, f_scratch);
-  some = block_sum(some, i_scratch);
-  if (threadIdx.x == 0) {
-    P.stats[0] = some > 0 ? balance / static_cast<float>(some) : 0.0f;
-    P.stats[1] = some > 0 ? squares / kept : 0.0f;
+#pragma unroll 4
+  for (long long i = t; i < P.groups * P.parts; i += kFinishThreads) all.y += P.squares[i];
+  all = make_float3(warp_sum(all.x), warp_sum(all.y), warp_sum(all.z));
+  some = warp_sum(some);
+  if (lane == 0) s_all[t >> 5] = all, s_cnt[t >> 5] = some;
+  __syncthreads();
+  if (t == 0) {
+    all = make_float3(0.0f, 0.0f, 0.0f);
+    some = 0;
+    for (int w = 0; w < kFinishThreads / 32; ++w) {
+      all.x += s_all[w].x, all.y += s_all[w].y, all.z += s_all[w].z;
+      some += s_cnt[w];
+    }
+    P.stats[0] = some > 0 ? all.x / static_cast<float>(some) : 0.0f;
+    P.stats[1] = some > 0 ? all.y / all.z : 0.0f;
     P.stats[2] = some > 0 ? 1.0f / static_cast<float>(some) : 0.0f;
-    P.stats[3] = some > 0 ? 2.0f / kept : 0.0f;
+    P.stats[3] = some > 0 ? 2.0f / all.z : 0.0f;
   }
 }
 
-template <bool BF16, int NC>
-__global__ void __launch_bounds__(kThreads) balance_grad(const __grid_constant__ BalanceParams P) {
+template <bool BF16, int NC, bool VEC>
+__global__ void __launch_bounds__(kThreads, 4) balance_grad(const __grid_constant__ BalanceParams P) {
+  constexpr int kU = kSets<NC>;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane & (P.lanes - 1), rows_warp = 32 / P.lanes, mine = lane / P.lanes;
   const long long g = blockIdx.x / P.parts;
@@ -337,66 +424,231 @@ __global__ void __launch_bounds__(kThreads) balance_grad(const __grid_constant__
   for (int c = 0; c < NC; ++c)
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const int e = entry(P, c, k, sub);
+      const int e = entry<VEC>(P, c, k, sub);
       a[c][k] = e < P.experts ? gb * P.weights[g * P.experts + e] : 0.0f;
     }
-  for (long long r = r0 + warp * rows_warp; r < r1; r += kWarps * rows_warp) {
-    const long long row = first + r + mine;
-    const bool in = r + mine < r1, on = in && (!P.mask || P.mask[row]);
-    float x[NC][8];
-    load_row<BF16, NC>(P, row, sub, on, x);
-    const float lse = softmax_row<NC>(P.lanes, on, x);
-    float s = 0.0f;
+  for (long long r = r0 + warp * rows_warp; r < r1; r += kU * kWarps * rows_warp) {
+    float x[kU][NC][8], lse[kU], s[kU];
+    bool in[kU], on[kU];
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
+    for (int u = 0; u < kU; ++u) {
+      const long long at = r + u * kWarps * rows_warp + mine;
+      in[u] = at < r1;
+      on[u] = in[u] && (!P.mask || P.mask[first + at]);
+    }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) s = fmaf(a[c][k], x[c][k], s);
-    for (int d = P.lanes / 2; d > 0; d /= 2) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
-    const float shift = on ? gz * lse - s : 0.0f;
+    for (int u = 0; u < kU; ++u) load_row<BF16, NC, VEC>(P, first + r + u * kWarps * rows_warp + mine, sub, on[u], x[u]);
+    softmax_rows<NC, kU>(P.lanes, on, x, lse);
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
+    for (int u = 0; u < kU; ++u) {
+      s[u] = 0.0f;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) x[c][k] = on ? x[c][k] * (a[c][k] + shift) : 0.0f;
-    if (!in) continue;
-    const long long base = row * P.grad_stride;
+      for (int c = 0; c < NC; ++c)
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const int e0 = entry(P, c, 0, sub);
-      if (P.vec) {
-        if (e0 >= P.experts) continue;
-        if constexpr (BF16) {
-          uint32_t w[4];
+        for (int k = 0; k < 8; ++k) s[u] = fmaf(a[c][k], x[u][c][k], s[u]);
+    }
+    for (int d = P.lanes / 2; d > 0; d /= 2)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(x[c][2 * k], x[c][2 * k + 1]);
-            w[k] = *reinterpret_cast<const uint32_t*>(&b);
-          }
-          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(P.grad) + base + e0) = make_uint4(w[0], w[1], w[2], w[3]);
-        } else {
-          float4* f = reinterpret_cast<float4*>(static_cast<float*>(P.grad) + base + e0);
-          f[0] = make_float4(x[c][0], x[c][1], x[c][2], x[c][3]);
-          f[1] = make_float4(x[c][4], x[c][5], x[c][6], x[c][7]);
-        }
-      } else {
+      for (int u = 0; u < kU; ++u) s[u] += __shfl_xor_sync(0xFFFFFFFFu, s[u], d);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int e = entry(P, c, k, sub);
-          if (e >= P.experts) continue;
-          if constexpr (BF16) static_cast<__nv_bfloat16*>(P.grad)[base + e] = __float2bfloat16_rn(x[c][k]);
-          else static_cast<float*>(P.grad)[base + e] = x[c][k];
-        }
+    for (int u = 0; u < kU; ++u) {
+      if (!in[u]) continue;
+      const float shift = gz * lse[u] - s[u];
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[u][c][k] = on[u] ? x[u][c][k] * (a[c][k] + shift) : 0.0f;
+      store_row<BF16, NC, VEC>(P, first + r + u * kWarps * rows_warp + mine, sub, x[u]);
+    }
+  }
+}
+
+// ------------------------------------------------ tiles (rows off the vectors)
+
+// `rows` rows from row `row` on, into `tile` with their own pitch of `experts`
+// entries; returns where the first one begins.  A run without gaps is copied
+// in 16-byte vectors, its ends entry by entry.  No barrier.
+template <typename T>
+__device__ __forceinline__ T* load_tile(const BalanceParams& P, long long row, int rows, unsigned char* tile) {
+  const T* x = static_cast<const T*>(P.x) + row * P.stride;
+  const int n = rows * P.experts, t = threadIdx.x;
+  if (P.stride != P.experts) {
+    T* const to = reinterpret_cast<T*>(tile);
+    for (int r = t >> 5; r < rows; r += kWarps)
+      for (int e = t & 31; e < P.experts; e += 32) to[r * P.experts + e] = x[r * P.stride + e];
+    return to;
+  }
+  constexpr int kN = 16 / sizeof(T);
+  const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(x) & 15u) / static_cast<int>(sizeof(T));
+  T* const to = reinterpret_cast<T*>(tile) + shift;  // 16-byte boundaries fall together
+  const int head = min(n, (kN - shift) % kN), vecs = (n - head) / kN;
+  const unsigned dst = static_cast<unsigned>(__cvta_generic_to_shared(to + head));
+  for (int i = t; i < vecs; i += kThreads)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 16 * i), "l"(x + head + i * kN) : "memory");
+  if (t < head) to[t] = x[t];
+  const int rest = head + vecs * kN;
+  if (t < n - rest) to[rest + t] = x[rest + t];
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  return to;
+}
+
+__device__ __forceinline__ float value(float x) { return x; }
+__device__ __forceinline__ float value(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// Largest entry and sum of a row that `q` neighbouring lanes share, and with A
+// the sum weighted by a.
+template <typename T, bool A>
+__device__ __forceinline__ void row_sums(const T* x, int experts, int q, int part, const float* a, float& m, float& s, float& sa) {
+  m = -INFINITY;
+#pragma unroll 4
+  for (int e = part; e < experts; e += q) m = fmaxf(m, value(x[e]));
+  for (int d = q / 2; d > 0; d /= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+  s = sa = 0.0f;
+#pragma unroll 4
+  for (int e = part; e < experts; e += q) {
+    const float p = ex2((value(x[e]) - m) * kLog2e);
+    s += p;
+    if (A) sa = fmaf(a[e], p, sa);
+  }
+  for (int d = q / 2; d > 0; d /= 2) {
+    s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
+    if (A) sa += __shfl_xor_sync(0xFFFFFFFFu, sa, d);
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) balance_rows_tile(const __grid_constant__ BalanceParams P) {
+  extern __shared__ __align__(16) unsigned char dynamic[];
+  __shared__ float2 s_row[kThreads];  // largest entry, 1 / sum (0: left out)
+  __shared__ int s_count[kTileExperts];
+  __shared__ float s_acc[kThreads];
+  __shared__ int2 s_numbers[kWarps];
+  __shared__ float s_sq[kWarps];
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int q = kThreads / P.tile_rows, part = t & (q - 1), mine = t / q;
+  const long long g = blockIdx.x / P.parts;
+  const long long r0 = static_cast<long long>(blockIdx.x % P.parts) * P.cta_rows;
+  const long long r1 = min(P.group_rows, r0 + P.cta_rows);
+  const long long first = g * P.group_rows;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // balance_finish waits for this grid's end
+  if (blockIdx.x == 0 && t == 0) *P.arrived = 0;
+  if (t < P.experts) s_count[t] = 0;
+  __syncthreads();
+  int assigned = 0, tokens = 0;
+  const long long i1 = (first + r1) * P.top;
+#pragma unroll 4
+  for (long long i = (first + r0) * P.top + t; i < i1; i += kThreads) {
+    const int64_t e = P.ids[i];
+    if (e < 0 || e >= P.experts || (P.mask && !P.mask[static_cast<unsigned>(i) / static_cast<unsigned>(P.top)])) continue;
+    atomicAdd(&s_count[e], 1);
+    ++assigned;
+  }
+  // an expert's sum: `width` threads for the experts, the rows dealt over the others
+  int width = 32;
+  while (width < P.experts) width *= 2;
+  const int e = t & (width - 1), deal = t / width, deals = kThreads / width;
+  float acc = 0.0f, sq = 0.0f;
+  for (long long r = r0; r < r1; r += P.tile_rows) {
+    const int rows = static_cast<int>(min(static_cast<long long>(P.tile_rows), r1 - r));
+    const T* x = load_tile<T>(P, first + r, rows, dynamic);
+    __syncthreads();
+    const bool in = mine < rows, on = in && (!P.mask || P.mask[first + r + mine]);
+    float m, s, unused;
+    row_sums<T, false>(x + (in ? mine : 0) * P.experts, P.experts, q, part, nullptr, m, s, unused);
+    if (part == 0) {
+      s_row[mine] = make_float2(m, on ? 1.0f / s : 0.0f);
+      if (on) {
+        const float lse = m + logf(s);
+        sq += lse * lse;
+        ++tokens;
       }
     }
+    __syncthreads();
+    if (e < P.experts) {
+#pragma unroll 4
+      for (int k = deal; k < rows; k += deals) {
+        const float2 row = s_row[k];
+        const float p = ex2((value(x[k * P.experts + e]) - row.x) * kLog2e) * row.y;
+        acc += row.y != 0.0f ? p : 0.0f;
+      }
+    }
+    __syncthreads();
+  }
+  s_acc[t] = acc;
+  sq = warp_sum(sq);
+  tokens = warp_sum(tokens);
+  assigned = warp_sum(assigned);
+  if (lane == 0) s_sq[warp] = sq, s_numbers[warp] = make_int2(tokens, assigned);
+  __syncthreads();
+  const long long out = static_cast<long long>(blockIdx.x) * P.experts;
+  if (t < P.experts) {
+    for (int k = 1; k < deals; ++k) acc += s_acc[k * width + t];
+    P.sums[out + t] = acc;
+    P.part_counts[out + t] = s_count[t];
+  }
+  if (t == 0) {
+    float s = 0.0f;
+    int2 n = make_int2(0, 0);
+    for (int w = 0; w < kWarps; ++w) s += s_sq[w], n.x += s_numbers[w].x, n.y += s_numbers[w].y;
+    P.squares[blockIdx.x] = s;
+    P.numbers[blockIdx.x] = n;
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) balance_grad_tile(const __grid_constant__ BalanceParams P) {
+  extern __shared__ __align__(16) unsigned char dynamic[];
+  __shared__ float3 s_row[kThreads];  // largest entry, 1 / sum (0: left out), shift
+  __shared__ float s_a[kTileExperts];
+  constexpr int kPerLane = kTileExperts / 32;
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int q = kThreads / P.tile_rows, part = t & (q - 1), mine = t / q;
+  const long long g = blockIdx.x / P.parts;
+  const long long r0 = static_cast<long long>(blockIdx.x % P.parts) * P.cta_rows;
+  const long long r1 = min(P.group_rows, r0 + P.cta_rows);
+  const long long first = g * P.group_rows;
+  const float gb = *P.grad_balance * P.stats[2], gz = *P.grad_z * P.stats[3];
+  if (t < P.experts) s_a[t] = gb * P.weights[g * P.experts + t];
+  __syncthreads();
+  float a[kPerLane];
+#pragma unroll
+  for (int k = 0; k < kPerLane; ++k) a[k] = lane + 32 * k < P.experts ? s_a[lane + 32 * k] : 0.0f;
+  for (long long r = r0; r < r1; r += P.tile_rows) {
+    const int rows = static_cast<int>(min(static_cast<long long>(P.tile_rows), r1 - r));
+    const T* x = load_tile<T>(P, first + r, rows, dynamic);
+    __syncthreads();
+    const bool in = mine < rows, on = in && (!P.mask || P.mask[first + r + mine]);
+    float m, s, sa;
+    row_sums<T, true>(x + (in ? mine : 0) * P.experts, P.experts, q, part, s_a, m, s, sa);
+    const float inv = 1.0f / s;
+    if (part == 0) s_row[mine] = make_float3(m, on ? inv : 0.0f, gz * (m + logf(s)) - sa * inv);
+    __syncthreads();
+    for (int k = warp; k < rows; k += kWarps) {
+      const float3 row = s_row[k];
+      T* const o = static_cast<T*>(P.grad) + (first + r + k) * P.grad_stride + lane;
+      const T* const from = x + k * P.experts + lane;
+#pragma unroll
+      for (int c = 0; c < kPerLane; ++c) {
+        if (lane + 32 * c >= P.experts) continue;
+        const float p = ex2((value(from[32 * c]) - row.x) * kLog2e) * row.y;
+        const float v = row.y != 0.0f ? p * (a[c] + row.z) : 0.0f;
+        if constexpr (sizeof(T) == 2) o[32 * c] = __float2bfloat16_rn(v);
+        else o[32 * c] = v;
+      }
+    }
+    __syncthreads();
   }
 }
 
 using KernelPtr = void (*)(BalanceParams);
 
-// Index: 0, 1, 2 for up to 256, 512, 1024 experts; + 3 for bfloat16.
-const KernelPtr kRows[6] = {balance_rows<false, 1>, balance_rows<false, 2>, balance_rows<false, 4>,
-                            balance_rows<true, 1>,  balance_rows<true, 2>,  balance_rows<true, 4>};
-const KernelPtr kGrad[6] = {balance_grad<false, 1>, balance_grad<false, 2>, balance_grad<false, 4>,
-                            balance_grad<true, 1>,  balance_grad<true, 2>,  balance_grad<true, 4>};
+#define KERNELS(F)                                                                                       \
+  F<false, 1, false>, F<false, 2, false>, F<false, 4, false>, F<true, 1, false>, F<true, 2, false>, F<true, 4, false>, \
+      F<false, 1, true>, F<false, 2, true>, F<false, 4, true>, F<true, 1, true>, F<true, 2, true>, F<true, 4, true>
+// Index: 0, 1, 2 for up to 256, 512, 1024 experts; + 3 for bfloat16; + 6 where rows are aligned for vectors.
+const KernelPtr kRows[12] = {KERNELS(balance_rows)};
+const KernelPtr kGrad[12] = {KERNELS(balance_grad)};
+#undef KERNELS
 
 // The split of the rows: lanes per row, CTAs per group, rows per CTA.
 struct Split {
@@ -410,17 +662,28 @@ Split split_of(int64_t tokens, int experts, int64_t groups) {
   while (s.lanes < 32 && s.lanes * 8 < experts) s.lanes *= 2;
   s.kernel = experts <= 256 ? 0 : experts <= 512 ? 1 : 2;
   s.group_rows = tokens / groups;
-  const long long pass = static_cast<long long>(kWarps) * (32 / s.lanes);  // rows of a CTA at a time
+  const int sets = s.kernel < 2 ? 2 : 1;
+  const long long pass = static_cast<long long>(kWarps) * (32 / s.lanes);  // rows of a CTA in one set
   const long long most = (s.group_rows + pass - 1) / pass;
   long long parts = (kTargetCtas + groups - 1) / groups;
   if (parts > most) parts = most;
   if (parts < 1) parts = 1;
   s.cta_rows = (s.group_rows + parts - 1) / parts;
-  s.cta_rows = (s.cta_rows + pass - 1) / pass * pass;
+  // whole rounds of all sets, unless that leaves SMs without rows
+  const long long round = s.cta_rows >= pass * sets ? pass * sets : pass;
+  s.cta_rows = (s.cta_rows + round - 1) / round * round;
   if (s.cta_rows < 1) s.cta_rows = 1;
   s.parts = static_cast<int>((s.group_rows + s.cta_rows - 1) / s.cta_rows);
   if (s.parts < 1) s.parts = 1;
   return s;
+}
+
+// Rows of a tile: a power of two, at least 32 (256 float32 experts: 32 KB).
+// Returns the tile's bytes, with room for its shift against 16 bytes.
+size_t use_tiles(BalanceParams& P, int size) {
+  P.tile_rows = kThreads;
+  while (P.tile_rows > 32 && static_cast<long long>(P.tile_rows) * P.experts * size > kTileBytes) P.tile_rows /= 2;
+  return static_cast<size_t>(P.tile_rows) * P.experts * size + 16;
 }
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
@@ -436,7 +699,7 @@ Layout layout_of(const Split& s, int experts, int64_t groups) {
   l.sums = 256;
   l.counts = l.sums + up256(n * experts * 4);
   l.tokens = l.counts + up256(n * experts * 4);
-  l.squares = l.tokens + up256(n * 4);
+  l.squares = l.tokens + up256(n * 8);
   l.loss = l.squares + up256(n * 4);
   l.total = l.loss + up256(static_cast<size_t>(groups) * 4);
   return l;
@@ -512,11 +775,11 @@ extern "C" muon_status_t balance_loss(const void* logits, int dtype, int64_t tok
   P.experts = experts;
   P.top = top;
   P.lanes = s.lanes;
-  P.vec = experts % 8 == 0 && row_stride * size % 16 == 0 && aligned_to(logits, 16);
+  const bool vec = experts % 8 == 0 && row_stride * size % 16 == 0 && aligned_to(logits, 16);
   P.arrived = reinterpret_cast<unsigned*>(ws + l.arrived);
   P.sums = reinterpret_cast<float*>(ws + l.sums);
   P.part_counts = reinterpret_cast<int*>(ws + l.counts);
-  P.part_tokens = reinterpret_cast<int*>(ws + l.tokens);
+  P.numbers = reinterpret_cast<int2*>(ws + l.tokens);
   P.squares = reinterpret_cast<float*>(ws + l.squares);
   P.group_loss = reinterpret_cast<float*>(ws + l.loss);
   P.stats = stats;
@@ -525,11 +788,26 @@ extern "C" muon_status_t balance_loss(const void* logits, int dtype, int64_t tok
   P.mean = mean_probs;
   P.weights = weights;
   cudaStream_t str = static_cast<cudaStream_t>(stream);
-  const size_t smem = static_cast<size_t>(kWarps + 1) * experts * 4;
-  kRows[s.kernel + (dtype == MUON_BF16 ? 3 : 0)]<<<static_cast<unsigned>(s.parts * groups), kThreads, smem, str>>>(P);
+  const bool bf16 = dtype == MUON_BF16;
+  size_t smem = static_cast<size_t>(kWarps + 1) * experts * 4;
+  KernelPtr rows = kRows[s.kernel + (bf16 ? 3 : 0) + (vec ? 6 : 0)];
+  if (!vec && experts <= kTileExperts) {
+    smem = use_tiles(P, size);
+    rows = bf16 ? balance_rows_tile<__nv_bfloat16> : balance_rows_tile<float>;
+  }
+  rows<<<static_cast<unsigned>(s.parts * groups), kThreads, smem, str>>>(P);
   if (cudaGetLastError() != cudaSuccess) return MUON_ERR_CUDA;
-  balance_finish<<<static_cast<unsigned>(groups), kFinishThreads, 0, str>>>(P);
-  return cudaGetLastError() == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+  // launched while balance_rows still runs; it waits for that grid's end
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(groups));
+  cfg.blockDim = dim3(kFinishThreads);
+  cfg.stream = str;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, balance_finish, P) == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
 }
 
 extern "C" muon_status_t balance_loss_backward(const void* logits, int dtype, int64_t tokens, int experts,
@@ -574,13 +852,19 @@ extern "C" muon_status_t balance_loss_backward(const void* logits, int dtype, in
   P.parts = s.parts;
   P.experts = experts;
   P.lanes = s.lanes;
-  P.vec = experts % 8 == 0 && row_stride * size % 16 == 0 && grad_stride * size % 16 == 0 && aligned_to(logits, 16) &&
+  const bool vec = experts % 8 == 0 && row_stride * size % 16 == 0 && grad_stride * size % 16 == 0 && aligned_to(logits, 16) &&
           aligned_to(grad, 16);
   P.stats = const_cast<float*>(stats);
   P.weights = const_cast<float*>(weights);
   P.grad_balance = grad_balance;
   P.grad_z = grad_z;
-  kGrad[s.kernel + (dtype == MUON_BF16 ? 3 : 0)]<<<static_cast<unsigned>(s.parts * groups), kThreads, 0,
-                                                   static_cast<cudaStream_t>(stream)>>>(P);
+  const bool bf16 = dtype == MUON_BF16;
+  size_t smem = 0;
+  KernelPtr rows = kGrad[s.kernel + (bf16 ? 3 : 0) + (vec ? 6 : 0)];
+  if (!vec && experts <= kTileExperts) {
+    smem = use_tiles(P, size);
+    rows = bf16 ? balance_grad_tile<__nv_bfloat16> : balance_grad_tile<float>;
+  }
+  rows<<<static_cast<unsigned>(s.parts * groups), kThreads, smem, static_cast<cudaStream_t>(stream)>>>(P);
   return cudaGetLastError() == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
 }
