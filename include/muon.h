@@ -374,7 +374,7 @@ void adamw_plan_destroy(adamw_plan* plan);
  * contribute nothing.  A row of -inf only has lse = logprobs = top_logprobs =
  * -inf and entropy 0.  A row with NaN or +inf has NaN results (NaN ranks
  * below every number).  A negative target marks a row that is left out: its
- * logits are not read, its outputs are 0 and its top_ids -1.  A target >=
+ * logits do not matter, its outputs are 0 and its top_ids -1.  A target >=
  * vocab gives NaN as logprobs of that row.
  *   targets                        rows;
  *   logprobs, lse, entropy         rows floats each, written;
@@ -391,8 +391,8 @@ muon_status_t token_logprobs(const void* logits, int dtype, int64_t rows, int64_
 /* Gradient of a loss with respect to the logits, from its gradients with
  * respect to logprobs and (optionally) entropy:
  *   grad_j = scale * (gl (1[j = target] - p_j) - ge p_j (log p_j + entropy))
- * in `dtype`, rounded once; 0 for rows that are left out (target < 0, not
- * read) and for entries of -inf; NaN for a row whose target is >= vocab.
+ * in `dtype`, rounded once; 0 for rows that are left out (target < 0,
+ * whatever their logits are) and for entries of -inf; NaN for a row whose target is >= vocab.
  *   lse, entropy      as token_logprobs wrote them for the same logits,
  *                     targets and scale (entropy is read with grad_entropy
  *                     only and may be NULL otherwise);

@@ -11,11 +11,13 @@
 // once for whatever a call computes from them:
 //   - up to 8 KB (logprob_warp): the row stays in the registers of up to 32
 //     lanes, and no warp waits for another;
-//   - beyond (logprob_row): the row stays in shared memory, up to 104 KB a
+//   - a score of longer rows streams through registers (logprob_score), over a
+//     cluster where rows are few;
+//   - the loss keeps longer rows in shared memory (logprob_loss), up to 104 KB a
 //     CTA so that two CTAs of an SM overlap one's loads with the other's
-//     arithmetic, spread over a cluster where it is longer or where rows are
-//     few; the CTAs exchange their sums through distributed shared memory;
-//   - rows that no cluster of eight holds are read again (logprob_stream).
+//     arithmetic, over a cluster of two where they are longer (or more where
+//     rows are few); the CTAs exchange their sums through distributed shared
+//     memory.  Rows beyond 208 KB are scored and then read again.
 // The backward pass alone knows the sums and is elementwise (logprob_grad).
 // Entries of -inf: exponents are held above -1000, where 2^t is 0 and 0 * t
 // stays 0.
@@ -39,13 +41,13 @@ namespace {
 
 constexpr int kMaxTop = 32;
 constexpr int kMaxCluster = 8;
+constexpr int kHeldRanks = 2;             // CTAs that a row's loss is spread over for its length
 constexpr int kWarpVecs = 512;            // longest row of logprob_warp in 16-byte vectors
 constexpr int kWarpThreads = 256;
 constexpr int kWarpCandidates = 192;
 constexpr int kSegmentBytes = 104 * 1024; // of a row in one CTA's shared memory
 constexpr int kGradThreads = 256;
 constexpr int kGradVecs = 4;              // 16-byte vectors per thread of logprob_grad
-constexpr int kScoreThreads = 256;
 constexpr int kCandidates = 256;
 constexpr int kHits = 256;
 constexpr int kScoreChunks = 16;
@@ -279,9 +281,9 @@ struct RowGrad {
   float m, log_s, a, b, at_target;
 };
 
-__device__ __forceinline__ RowGrad grad_of(const LogprobParams& P, const RowStats& r, long long row, int64_t target) {
+__device__ __forceinline__ RowGrad grad_of(const LogprobParams& P, const RowStats& r, float gl, float ge, int64_t target) {
   RowGrad g;
-  const float gl = target < P.vocab ? P.gl[row] : NAN, ge = P.ge ? P.ge[row] : 0.0f;
+  if (target >= P.vocab) gl = NAN;
   g.m = r.m;
   g.log_s = r.log_s;
   g.a = r.empty ? 0.0f : -P.scale * ge;
@@ -405,7 +407,6 @@ struct RowVectors {
 struct WarpTop {
   unsigned long long candidate[kWarpCandidates];
   unsigned long long top[kMaxTop];
-  int n;
 };
 
 // The `top` first places of a row that a whole warp holds, into S.top, found
@@ -424,26 +425,26 @@ __device__ __forceinline__ bool warp_top(const LogprobParams& P, const RowVector
     if (lane == __ffs(__ballot_sync(0xFFFFFFFFu, left == bound)) - 1) left = 0;
   }
   const float least = place_value(static_cast<unsigned long long>(bound) << 32);
-  if (lane == 0) S.n = 0;
-  __syncwarp();
+  int n = 0;  // the same in every lane
 #pragma unroll
   for (int u = 0; u < NV; ++u) {
-    if (!__any_sync(0xFFFFFFFFu, vec_max<BF16>(q[u]) >= least)) continue;
-    float x[kN];
-    unpack<BF16>(q[u], x);
-#pragma unroll
-    for (int k = 0; k < kN; ++k) {
-      const int j = R.first(lane + 32 * u) + k;
-      const unsigned m = __ballot_sync(0xFFFFFFFFu, j >= 0 && j < P.vocab && ordered(x[k]) >= bound);
-      const int i = S.n + __popc(m & ((1u << lane) - 1));
-      if ((m >> lane & 1) && i < kWarpCandidates) S.candidate[i] = place(x[k], j);
-      __syncwarp();
-      if (lane == 0) S.n += __popc(m);
-      __syncwarp();
+    // one vector after the other, an entry a lane
+    for (unsigned hits = __ballot_sync(0xFFFFFFFFu, vec_max<BF16>(q[u]) >= least); hits != 0; hits &= hits - 1) {
+      const int from = __ffs(hits) - 1;
+      const uint32_t w[4] = {__shfl_sync(0xFFFFFFFFu, q[u].x, from), __shfl_sync(0xFFFFFFFFu, q[u].y, from),
+                             __shfl_sync(0xFFFFFFFFu, q[u].z, from), __shfl_sync(0xFFFFFFFFu, q[u].w, from)};
+      const int word = BF16 ? lane >> 1 & 3 : lane & 3;
+      const uint32_t both = word < 2 ? (word == 0 ? w[0] : w[1]) : (word == 2 ? w[2] : w[3]);
+      const float x = __uint_as_float(!BF16 ? both : lane & 1 ? both & 0xFFFF0000u : both << 16);
+      const int j = R.first(from + 32 * u) + lane;
+      const bool on = lane < kN && j >= 0 && j < P.vocab && ordered(x) >= bound;
+      const unsigned m = __ballot_sync(0xFFFFFFFFu, on);
+      const int i = n + __popc(m & ((1u << lane) - 1));
+      if (on && i < kWarpCandidates) S.candidate[i] = place(x, j);
+      n += __popc(m);
     }
   }
   __syncwarp();
-  const int n = S.n;
   if (n > kWarpCandidates) return false;
   for (int i = lane; i < n; i += 32) {
     const unsigned long long mine = S.candidate[i];
@@ -462,18 +463,25 @@ __global__ void __launch_bounds__(kWarpThreads, NV == 16 ? 2 : NV == 8 ? 3 : 4) 
   const int lane = threadIdx.x & 31, sub = lane & (P.lanes - 1), rows_warp = 32 / P.lanes;
   const long long row = (static_cast<long long>(blockIdx.x) * (kWarpThreads / 32) + (threadIdx.x >> 5)) * rows_warp + lane / P.lanes;
   const bool in = row < P.rows;
+  // every load is issued before the first one is waited for, the logits of
+  // rows that are left out among them
   const int64_t target = in ? P.targets[row] : -1;
+  float gl = 0.0f, ge = 0.0f;
+  if (MODE != kScore && in) gl = P.gl[row], ge = P.ge ? P.ge[row] : 0.0f;
   const bool on = target >= 0;
   const RowVectors<BF16> R(P.x, in ? row * P.stride : 0, P.vocab);
+  const int lo = R.shift > 0 ? 1 : 0;  // the vectors inside the row: lo .. lo+wholes-1
+  const int wholes = max(0, static_cast<int>(static_cast<unsigned>(R.shift + P.vocab) / kN) - lo);
   uint4 q[NV];
 #pragma unroll
   for (int u = 0; u < NV; ++u) {
     const int v = sub + P.lanes * u;
     q[u] = masked_vector<BF16>();
-    if (!on || v >= R.count) continue;
-    if (R.whole(v)) q[u] = *reinterpret_cast<const uint4*>(R.base + v * 16LL);
-    else q[u] = R.end(v);
+    if (in && static_cast<unsigned>(v - lo) < static_cast<unsigned>(wholes)) q[u] = *reinterpret_cast<const uint4*>(R.base + v * 16LL);
+    else if (in && v < R.count) q[u] = R.end(v);
   }
+  float x_target = 0.0f;
+  if (MODE != kBackward && on && target < P.vocab) x_target = at<BF16>(P.x, row * P.stride + target);
   RowStats r{};
   if (MODE == kBackward && on) r = stats_from_lse(P, row);
   if (MODE != kBackward || __any_sync(0xFFFFFFFFu, on && log_s_is_lost(r))) {
@@ -481,18 +489,26 @@ __global__ void __launch_bounds__(kWarpThreads, NV == 16 ? 2 : NV == 8 ? 3 : 4) 
 #pragma unroll
     for (int u = 0; u < NV; ++u) a.m = fmaxf(a.m, vec_max<BF16>(q[u]));
     for (int d = P.lanes / 2; d > 0; d /= 2) a.m = fmaxf(a.m, __shfl_xor_sync(0xFFFFFFFFu, a.m, d));
-    float2 s{}, w{};
+    const float c2 = P.scale * kLog2e;
+    auto add_up = [&](auto add) {
+      float2 s{}, w{};
 #pragma unroll
-    for (int u = 0; u < NV; ++u) {
-      float x[kN];
-      unpack<BF16>(q[u], x);
-      accumulate(s, w, x, reference(a.m), P.scale * kLog2e);
-    }
-    a.s = s.x + s.y;
-    a.w = w.x + w.y;
-    for (int d = P.lanes / 2; d > 0; d /= 2) {
-      a.s += __shfl_xor_sync(0xFFFFFFFFu, a.s, d);
-      a.w += __shfl_xor_sync(0xFFFFFFFFu, a.w, d);
+      for (int u = 0; u < NV; ++u) add(s, w, q[u]);
+      a.s = s.x + s.y;
+      a.w = w.x + w.y;
+      for (int d = P.lanes / 2; d > 0; d /= 2) {
+        a.s += __shfl_xor_sync(0xFFFFFFFFu, a.s, d);
+        a.w += __shfl_xor_sync(0xFFFFFFFFu, a.w, d);
+      }
+    };
+    add_up([&](float2& s, float2& w, uint4 v) { accumulate_near<BF16>(s, w, v, reference(a.m), c2); });
+    // against the largest entry S is 1 and more, unless the short form's range does not do
+    if (__any_sync(0xFFFFFFFFu, !(a.s >= 0.5f && a.s < 0x1p60f) && on)) {
+      add_up([&](float2& s, float2& w, uint4 v) {
+        float x[kN];
+        unpack<BF16>(v, x);
+        accumulate(s, w, x, reference(a.m), c2);
+      });
     }
     if (MODE != kBackward || log_s_is_lost(r)) r = stats_of(a, P.scale);
   }
@@ -500,7 +516,7 @@ __global__ void __launch_bounds__(kWarpThreads, NV == 16 ? 2 : NV == 8 ? 3 : 4) 
     if (in && sub == 0) {
       P.lse[row] = on ? r.lse : 0.0f;
       P.entropy[row] = on ? r.entropy : 0.0f;
-      P.logprobs[row] = !on ? 0.0f : target >= P.vocab ? NAN : logprob_of(r, at<BF16>(P.x, row * P.stride + target), P.scale);
+      P.logprobs[row] = !on ? 0.0f : target >= P.vocab ? NAN : logprob_of(r, x_target, P.scale);
     }
     if (P.top > 0) {
       WarpTop& T = S[threadIdx.x >> 5];
@@ -547,21 +563,29 @@ __global__ void __launch_bounds__(kWarpThreads, NV == 16 ? 2 : NV == 8 ? 3 : 4) 
     __syncwarp();  // in place: the target's logit has been read
     if (!in) return;
     RowGrad g{};
-    if (on) g = grad_of(P, r, row, target);
+    if (on) g = grad_of(P, r, gl, ge, target);
+    const NearGrad near = near_of(g, P.scale);
+    const bool ordinary = fabsf(near.K) < -kMasked;
     const RowVectors<BF16> O(P.grad, row * P.grad_stride, P.vocab);
     uint4* const o = reinterpret_cast<uint4*>(const_cast<unsigned char*>(O.base));
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
       const int v = sub + P.lanes * u, j = R.first(v);
       if (v >= R.count) continue;
-      float x[kN] = {};
-      if (on) {
+      uint4 y = make_uint4(0, 0, 0, 0);
+      if (on && ordinary) {
+        y = grad_near<BF16>(g, near, P.scale, target, j, q[u]);
+      } else if (on) {
+        float x[kN];
         unpack<BF16>(q[u], x);
         grad_entries(g, P.scale, target, j, x);
+        y = pack<BF16>(x);
       }
-      if (O.shift == R.shift && R.whole(v)) {
-        o[v] = pack<BF16>(x);
+      if (O.shift == R.shift && static_cast<unsigned>(v - lo) < static_cast<unsigned>(wholes)) {
+        o[v] = y;
       } else {
+        float x[kN];
+        unpack<BF16>(y, x);
 #pragma unroll
         for (int k = 0; k < kN; ++k)
           if (j + k >= 0 && j + k < P.vocab) put<BF16>(P.grad, row * P.grad_stride + j + k, x[k]);
@@ -948,7 +972,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 8 : 3) logprob_loss(
       __syncthreads();  // S is free for the next row
     }
 
-    const RowGrad g = grad_of(P, r, row, target);
+    const RowGrad g = grad_of(P, r, P.gl[row], P.ge ? P.ge[row] : 0.0f, target);
     const NearGrad near = near_of(g, P.scale);
     if (same && fabsf(near.K) < -kMasked) {
 #pragma unroll 1
@@ -989,17 +1013,16 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 8 : 3) logprob_loss(
 // ------------------------------------------------- scores of long rows (CTAs)
 
 // One row per CTA, or per cluster where rows are few.  The logits pass through
-// registers, two batches of four vectors a thread; four CTAs of an SM overlap
-// one's loads with another's reductions.  Each warp adds up against the
-// largest entry of its own first batch.
-template <bool BF16, bool TOP>
-__global__ void __launch_bounds__(kScoreThreads, 4) logprob_score(const __grid_constant__ LogprobParams P) {
-  constexpr int kWarps = kScoreThreads / 32, kU = 4, kBatch = kU * kScoreThreads;
+// registers, two batches of four vectors a thread.  Each warp adds up against
+// the largest entry of its own first batch.
+template <bool BF16, int THREADS, bool TOP>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprob_score(const __grid_constant__ LogprobParams P) {
+  constexpr int kWarps = THREADS / 32, kU = 4, kBatch = kU * THREADS;
   __shared__ Sums warp_sums[kWarps];
   __shared__ float scratch[kWarps];
   __shared__ float2 pair_scratch[kWarps];
   __shared__ Exchange X;
-  __shared__ __align__(16) TopScratch<TOP ? kScoreThreads : 32, TOP ? kScoreChunks : 1> S;
+  __shared__ __align__(16) TopScratch<TOP ? THREADS : 32, TOP ? kScoreChunks : 1> S;
   const cg::cluster_group cluster = cg::this_cluster();
   const int ranks = 1 << P.log_ranks, rank = blockIdx.x & (ranks - 1);
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -1012,7 +1035,7 @@ __global__ void __launch_bounds__(kScoreThreads, 4) logprob_score(const __grid_c
   }
   // a CTA's shared memory is written by others only once it has begun
   if (ranks > 1) cg::cluster_group::barrier_arrive();
-  const RowPart<BF16> p = part_of<BF16, kScoreThreads>(P, row, rank);
+  const RowPart<BF16> p = part_of<BF16, THREADS>(P, row, rank);
   // the part's whole vectors src[0 .. n-1]; the row's other two (its ends) are
   // put together from their entries by one thread each
   const bool head = p.v0 < p.lo, tail = p.v0 + p.n > p.lo + p.wholes;
@@ -1023,7 +1046,7 @@ __global__ void __launch_bounds__(kScoreThreads, 4) logprob_score(const __grid_c
   if (t == 0 && head) end = RowVectors<BF16>(P.x, base, P.vocab).end(p.v0);
   if (t == 32 && tail) end = RowVectors<BF16>(P.x, base, P.vocab).end(p.v0 + p.n - 1);
 #pragma unroll
-  for (int u = 0; u < kU; ++u) a[u] = t + u * kScoreThreads < n ? load_once(src + t + u * kScoreThreads) : masked_vector<BF16>();
+  for (int u = 0; u < kU; ++u) a[u] = t + u * THREADS < n ? load_once(src + t + u * THREADS) : masked_vector<BF16>();
   float x_target = 0.0f;
   if (t == 0 && rank == 0 && target < P.vocab) x_target = at<BF16>(P.x, base + target);
   Sums sums{};
@@ -1045,18 +1068,18 @@ __global__ void __launch_bounds__(kScoreThreads, 4) logprob_score(const __grid_c
     const int i = k * kBatch + t;
     if (!found) {  // masked entries alone so far
 #pragma unroll
-      for (int u = 0; u < kU; ++u) sums.m = i + u * kScoreThreads < n ? fmaxf(sums.m, vec_max<BF16>(a[u])) : sums.m;
+      for (int u = 0; u < kU; ++u) sums.m = i + u * THREADS < n ? fmaxf(sums.m, vec_max<BF16>(a[u])) : sums.m;
 #pragma unroll
       for (int d = 16; d > 0; d /= 2) sums.m = fmaxf(sums.m, __shfl_xor_sync(0xFFFFFFFFu, sums.m, d));
       found = sums.m != -INFINITY;
     }
 #pragma unroll
     for (int u = 0; u < kU; ++u)
-      if (i + kBatch + u * kScoreThreads < n) b[u] = load_once(src + i + kBatch + u * kScoreThreads);
+      if (i + kBatch + u * THREADS < n) b[u] = load_once(src + i + kBatch + u * THREADS);
     VecMax<BF16> largest;
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      if (i + u * kScoreThreads < n) {
+      if (i + u * THREADS < n) {
         if (TOP) largest.add(a[u]);
         accumulate_near<BF16>(s, w, a[u], reference(sums.m), c2);
       }
@@ -1090,7 +1113,7 @@ __global__ void __launch_bounds__(kScoreThreads, 4) logprob_score(const __grid_c
   for (int k = 0; k < kWarps; ++k)
     far |= !(warp_sums[k].s >= 0.5f && warp_sums[k].s < 0x1p60f) && !(warp_sums[k].s == 0.0f && warp_sums[k].m == -INFINITY);
   if (far) {
-    sums = sums_again<BF16, kScoreThreads>(P.x, base, max(0, p.first(0)), min(P.vocab, p.first(p.n)), c2, scratch, pair_scratch);
+    sums = sums_again<BF16, THREADS>(P.x, base, max(0, p.first(0)), min(P.vocab, p.first(p.n)), c2, scratch, pair_scratch);
   } else if (warp == 0) {
     sums = warp_sums[0];
 #pragma unroll
@@ -1113,7 +1136,7 @@ __global__ void __launch_bounds__(kScoreThreads, 4) logprob_score(const __grid_c
     }
     if constexpr (TOP) {
       const int all = ranks * P.top;
-      for (int i = t; i < all; i += kScoreThreads) {
+      for (int i = t; i < all; i += THREADS) {
         const unsigned long long mine = X.top[i / P.top][i % P.top];
         int place_ = 0;
         for (int j = 0; j < all; ++j) place_ += X.top[j / P.top][j % P.top] > mine;
@@ -1173,13 +1196,13 @@ __global__ void __launch_bounds__(kGradThreads) logprob_grad(const __grid_consta
     const float entropy = r.entropy;
     r = stats_of(a, P.scale);
     r.entropy = entropy;
-    const RowGrad g = grad_of(P, r, row, target);
+    const RowGrad g = grad_of(P, r, P.gl[row], P.ge ? P.ge[row] : 0.0f, target);
     for (int j = t; j < P.vocab; j += kGradThreads)
       put<BF16>(P.grad, out + j, grad_entry(g, P.scale, target, j, at<BF16>(P.x, base + j)));
     return;
   }
   RowGrad g{};
-  if (on) g = grad_of(P, r, row, target);
+  if (on) g = grad_of(P, r, P.gl[row], P.ge ? P.ge[row] : 0.0f, target);
   if (same) {
     uint4* const o = reinterpret_cast<uint4*>(const_cast<unsigned char*>(O.base));
 #pragma unroll
@@ -1240,9 +1263,12 @@ const KernelPtr kLossKernels[8] = {
     logprob_loss<true, 128, true>,   logprob_loss<true, 256, true>,
 };
 
-// Index: alternatives | bfloat16 << 1.
-const KernelPtr kScoreKernels[4] = {logprob_score<false, false>, logprob_score<false, true>, logprob_score<true, false>,
-                                    logprob_score<true, true>};
+// Index: 256 threads | alternatives << 1 | bfloat16 << 2.
+const KernelPtr kScoreKernels[8] = {
+    logprob_score<false, 128, false>, logprob_score<false, 256, false>, logprob_score<false, 128, true>,
+    logprob_score<false, 256, true>, logprob_score<true, 128, false>,   logprob_score<true, 256, false>,
+    logprob_score<true, 128, true>,   logprob_score<true, 256, true>,
+};
 
 cudaError_t launch_clusters(KernelPtr f, const LogprobParams& P, long long clusters, int threads, size_t smem, cudaStream_t stream) {
   cudaLaunchConfig_t cfg{};
@@ -1269,7 +1295,12 @@ int spread(int ranks, long long rows, long long bytes, int sms) {
 cudaError_t launch_score(LogprobParams P, bool bf16, long long bytes, int sms, cudaStream_t stream) {
   const int ranks = spread(1, P.rows, bytes, sms);
   while (1 << P.log_ranks < ranks) ++P.log_ranks;
-  return launch_clusters(kScoreKernels[(P.top > 0 ? 1 : 0) | (bf16 ? 2 : 0)], P, P.rows, kScoreThreads, 0, stream);
+  // 128 threads a row: eight rows of an SM overlap one's loads with another's
+  // reductions (4096 x 50257 bfloat16 with 5 alternatives 100 us, 32768 x 6000
+  // 103; 256 threads: 110 and 157; 64: 109 for the latter).  A row that is
+  // spread wants its CTAs' loads in flight at once.
+  const bool wide = ranks > 1;
+  return launch_clusters(kScoreKernels[(wide ? 1 : 0) | (P.top > 0 ? 2 : 0) | (bf16 ? 4 : 0)], P, P.rows, wide ? 256 : 128, 0, stream);
 }
 
 cudaError_t launch_loss(LogprobParams P, bool bf16, long long bytes, int sms, cudaStream_t stream) {
@@ -1309,9 +1340,12 @@ muon_status_t run(const void* logits, int dtype, int64_t rows, int64_t vocab, in
     return MUON_ERR_MISALIGNED;
   const int size = dtype == MUON_F32 ? 4 : 2;
   const int64_t bytes = vocab * size + 32;  // of a row, with both ends' partial vectors
-  const bool held = bytes <= static_cast<int64_t>(kMaxCluster) * kSegmentBytes;
+  // longer rows are read twice: 4096 x 128256 bfloat16 take 515 us so, 603 over clusters of four
+  const bool held = bytes <= static_cast<int64_t>(kHeldRanks) * kSegmentBytes;
   const int64_t per_cta = 16 * kGradThreads * kGradVecs, chunks = (bytes + per_cta - 1) / per_cta;
-  const int64_t vecs = (bytes - 2) / 16;   // at most: rows begin anywhere
+  // a row's vectors: all rows begin on a 16-byte boundary, or anywhere
+  const bool even = aligned_to(logits, 16) && row_stride * size % 16 == 0;
+  const int64_t vecs = even ? (vocab * size + 15) / 16 : (bytes - 2) / 16;
   if (vecs > kWarpVecs && rows > INT32_MAX / chunks) return MUON_ERR_TOO_LARGE;
   const uint64_t r = static_cast<uint64_t>(rows);
   try {
