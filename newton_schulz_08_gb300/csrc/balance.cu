@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 4) balance_rows(const __grid_constan
   // the assignments of this CTA's rows
   int assigned = 0;
   const long long i1 = (first + r1) * P.top;
-#pragma unroll 4
+#pragma unroll 8
   for (long long i = (first + r0) * P.top + threadIdx.x; i < i1; i += kThreads) {
     const int64_t e = P.ids[i];
     if (e < 0 || e >= P.experts || (P.mask && !P.mask[static_cast<unsigned>(i) / static_cast<unsigned>(P.top)])) continue;
@@ -536,7 +536,7 @@ __global__ void __launch_bounds__(kThreads) balance_rows_tile(const __grid_const
   __syncthreads();
   int assigned = 0, tokens = 0;
   const long long i1 = (first + r1) * P.top;
-#pragma unroll 4
+#pragma unroll 8
   for (long long i = (first + r0) * P.top + t; i < i1; i += kThreads) {
     const int64_t e = P.ids[i];
     if (e < 0 || e >= P.experts || (P.mask && !P.mask[static_cast<unsigned>(i) / static_cast<unsigned>(P.top)])) continue;

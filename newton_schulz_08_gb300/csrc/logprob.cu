@@ -1222,11 +1222,18 @@ __global__ void __launch_bounds__(kGradThreads) logprob_grad(const __grid_consta
           if (j + k >= 0 && j + k < P.vocab) put<BF16>(P.grad, out + j + k, on ? grad_entry(g, P.scale, target, j + k, at<BF16>(P.x, base + j + k)) : 0.0f);
       }
     }
-  } else {
+  } else {  // entry by entry, eight loads before the first store
     const int j0 = max(0, R.first(v0)), j1 = min(P.vocab, R.first(v1));
-#pragma unroll 8
-    for (int j = j0 + t; j < j1; j += kGradThreads)
-      put<BF16>(P.grad, out + j, on ? grad_entry(g, P.scale, target, j, at<BF16>(P.x, base + j)) : 0.0f);
+    for (int j = j0 + t; j < j1; j += 8 * kGradThreads) {
+      float x[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = on && j + k * kGradThreads < j1 ? at<BF16>(P.x, base + j + k * kGradThreads) : 0.0f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int i = j + k * kGradThreads;
+        if (i < j1) put<BF16>(P.grad, out + i, on ? grad_entry(g, P.scale, target, i, x[k]) : 0.0f);
+      }
+    }
   }
 }
 

@@ -620,34 +620,47 @@ def _per_tensor(x, n, what):
 
 
 def _adamw_descs(params, grads, states, lr, weight_decay):
+    """(descriptors, number, every tensor) of an AdamW step, checked."""
     n = len(params)
     if len(states) != n or (grads is not None and len(grads) != n):
         raise ValueError("params, grads and states must have the same length")
     lr, weight_decay = _per_tensor(lr, n, "lr"), _per_tensor(weight_decay, n, "weight_decay")
+    f32, m8, v8 = torch.float32, torch.float8_e4m3fn, torch.float8_e5m2
+    codes = {torch.float32: MUON_F32, torch.bfloat16: MUON_BF16}
     arr, every = (adamw_tensor_desc * max(n, 1))(), []
     for i, (p, s) in enumerate(zip(params, states)):
-        g = None if grads is None else grads[i]
+        size = p.numel()
         if len(s) == 2:
-            (m, v), ms, vs, bits, kinds = s, None, None, 32, (torch.float32, torch.float32)
+            m, v = s
+            ms = vs = None
+            fits = m.dtype == f32 and v.dtype == f32
         elif len(s) == 4:
-            (m, ms, v, vs), bits, kinds = s, 8, (torch.float8_e4m3fn, torch.float8_e5m2)
+            m, ms, v, vs = s
+            fits = m.dtype == m8 and v.dtype == v8
+            blocks = -(-size // ADAMW_BLOCK)
+            if ms.dtype != f32 or vs.dtype != f32 or ms.numel() != blocks or vs.numel() != blocks:
+                raise ValueError(f"tensor {i}: scales must be float32, one per {ADAMW_BLOCK} elements")
         else:
             raise ValueError(f"tensor {i}: a state has 2 tensors (32 bits) or 4 (8 bits)")
-        if m.dtype != kinds[0] or v.dtype != kinds[1] or m.numel() != p.numel() or v.numel() != p.numel():
+        if not fits or m.numel() != size or v.numel() != size:
             raise ValueError(f"tensor {i}: moments must have the parameter's size and be float32, or float8_e4m3fn "
                              "and float8_e5m2")
-        if bits == 8 and any(t.dtype != torch.float32 or t.numel() != -(-p.numel() // ADAMW_BLOCK) for t in (ms, vs)):
-            raise ValueError(f"tensor {i}: scales must be float32, one per {ADAMW_BLOCK} elements")
-        if g is not None and g.numel() != p.numel():
-            raise ValueError(f"tensor {i}: the gradient must have the parameter's size")
-        used = [t for t in (p, g, m, v, ms, vs) if t is not None]
-        if not all(t.is_contiguous() for t in used):
-            raise ValueError(f"tensor {i}: tensors must be contiguous")
+        g = None if grads is None else grads[i]
+        used = (p, m, v) if ms is None else (p, m, v, ms, vs)
+        if g is not None:
+            if g.numel() != size:
+                raise ValueError(f"tensor {i}: the gradient must have the parameter's size")
+            used += (g,)
+        for t in used:
+            if not t.is_contiguous():
+                raise ValueError(f"tensor {i}: tensors must be contiguous")
         every += used
-        arr[i] = adamw_tensor_desc(p.data_ptr(), g.data_ptr() if g is not None else 0, m.data_ptr(), v.data_ptr(),
-                                   ms.data_ptr() if ms is not None else 0, vs.data_ptr() if vs is not None else 0,
-                                   p.numel(), lr[i], weight_decay[i], _dtype_code(p),
-                                   _dtype_code(g) if g is not None else MUON_F32, bits, 0)
+        kind, grad_kind = codes.get(p.dtype, -1), MUON_F32 if g is None else codes.get(g.dtype, -1)
+        if kind < 0 or grad_kind < 0:
+            raise TypeError(f"tensor {i}: parameters and gradients must be bfloat16 or float32")
+        arr[i] = (p.data_ptr(), 0 if g is None else g.data_ptr(), m.data_ptr(), v.data_ptr(),
+                  0 if ms is None else ms.data_ptr(), 0 if vs is None else vs.data_ptr(), size, lr[i],
+                  weight_decay[i], kind, grad_kind, 32 if ms is None else 8, 0)
     return arr, n, every
 
 
