@@ -12,15 +12,16 @@
 // A row has at most 1024 entries, so it lives in registers: L lanes (a power
 // of two) share a row, 8 entries a lane and chunk of 8 L.  A warp takes
 // 32 / L rows side by side and, up to 512 experts, two such sets at a time:
-// the reductions of a row are a chain of ten shuffles, and two chains overlap
-// (131072 x 256 float32: forward 44 -> 36 us, backward 56 -> 48; four sets
-// leave room for fewer warps: 43 and 55).  HBM-bound: a row is read once
-// forward, read and written once backward.
+// the reductions of a row are a chain of ten shuffles, and two chains overlap.
+// HBM-bound: a row is read once forward, read and written once backward.
+// 131072 x 256 float32: forward 31 us of 21 that its bytes take, backward 42 of
+// 40 (one set: 44 and 56; four leave room for fewer warps: 43 and 55; scalar
+// arithmetic in place of pairs: 36 and 48).
 // Rows off the 16-byte boundaries (an odd number of experts, up to 256) come
 // through shared memory in tiles instead, copied as one run: there a few
 // threads, without a shuffle each, take a row's sums, and then a thread an
-// expert's (65536 x 161 bfloat16: forward 28 -> TT1 us, backward 42 -> TT2,
-// against entry by entry from global memory).
+// expert's (65536 x 161 bfloat16: forward 28 -> 20 us, backward 42 -> 23,
+// against entry by entry from global memory; the bytes take 4 and 6).
 //
 // Forward, two launches.  balance_rows: each CTA takes consecutive rows of
 // one group and leaves partial sums of p and lse^2, counts and the numbers of
@@ -57,6 +58,7 @@ struct BalanceParams {
   const uint8_t* mask;
   void* grad;
   long long stride, grad_stride;
+  long long tokens_all;  // rows of all groups
   long long group_rows;  // rows of a group
   long long cta_rows;    // rows of a CTA
   long long groups;
@@ -96,6 +98,7 @@ __device__ __forceinline__ int entry(const BalanceParams& P, int c, int k, int s
 template <bool BF16, int NC, bool VEC>
 __device__ __forceinline__ void load_row(const BalanceParams& P, long long row, int sub, bool on, float (&x)[NC][8]) {
   const long long base = row * P.stride;
+  if (!MUON_CHECK(!on || (row >= 0 && row < P.tokens_all))) on = false;
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
 #pragma unroll
@@ -133,6 +136,7 @@ __device__ __forceinline__ void load_row(const BalanceParams& P, long long row, 
 template <bool BF16, int NC, bool VEC>
 __device__ __forceinline__ void store_row(const BalanceParams& P, long long row, int sub, const float (&x)[NC][8]) {
   const long long base = row * P.grad_stride;
+  if (!MUON_CHECK(row >= 0 && row < P.tokens_all)) return;
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     const int e0 = entry<VEC>(P, c, 0, sub);
@@ -163,10 +167,10 @@ __device__ __forceinline__ void store_row(const BalanceParams& P, long long row,
   }
 }
 
-// x becomes the rows' probabilities (0 where a row is off).  U rows of a lane
-// at a time.
+// x becomes exp(x - largest) of its row, which times inv is the probability;
+// both are 0 where a row is off.  U rows of a lane at a time, entries in pairs.
 template <int NC, int U>
-__device__ __forceinline__ void softmax_rows(int lanes, const bool (&on)[U], float (&x)[U][NC][8], float (&lse)[U]) {
+__device__ __forceinline__ void softmax_rows(int lanes, const bool (&on)[U], float (&x)[U][NC][8], float (&inv)[U], float (&lse)[U]) {
   float m[U], s[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
@@ -181,26 +185,27 @@ __device__ __forceinline__ void softmax_rows(int lanes, const bool (&on)[U], flo
     for (int u = 0; u < U; ++u) m[u] = fmaxf(m[u], __shfl_xor_sync(0xFFFFFFFFu, m[u], d));
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    s[u] = 0.0f;
+    const float shift = on[u] ? -m[u] * kLog2e : 0.0f;
+    float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int c = 0; c < NC; ++c)
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        x[u][c][k] = ex2((x[u][c][k] - m[u]) * kLog2e);
-        s[u] += x[u][c][k];
+      for (int k = 0; k < 8; k += 2) {
+        const float2 t = __ffma2_rn(make_float2(x[u][c][k], x[u][c][k + 1]), make_float2(kLog2e, kLog2e), make_float2(shift, shift));
+        const float2 e = make_float2(ex2(t.x), ex2(t.y));
+        sum = __fadd2_rn(sum, e);
+        x[u][c][k] = e.x;
+        x[u][c][k + 1] = e.y;
       }
+    s[u] = sum.x + sum.y;
   }
   for (int d = lanes / 2; d > 0; d /= 2)
 #pragma unroll
     for (int u = 0; u < U; ++u) s[u] += __shfl_xor_sync(0xFFFFFFFFu, s[u], d);
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const float inv = 1.0f / s[u];
-#pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-      for (int k = 0; k < 8; ++k) x[u][c][k] = on[u] ? x[u][c][k] * inv : 0.0f;
-    lse[u] = m[u] + logf(s[u]);
+    inv[u] = on[u] ? __fdividef(1.0f, s[u]) : 0.0f;
+    lse[u] = m[u] + __logf(s[u]);  // 1 <= s <= 1024
   }
 }
 
@@ -260,14 +265,19 @@ __global__ void __launch_bounds__(kThreads, 4) balance_rows(const __grid_constan
     }
 #pragma unroll
     for (int u = 0; u < kU; ++u) load_row<BF16, NC, VEC>(P, first + r + u * kWarps * rows_warp + mine, sub, on[u], x[u]);
-    float lse[kU];
-    softmax_rows<NC, kU>(P.lanes, on, x, lse);
+    float inv[kU], lse[kU];
+    softmax_rows<NC, kU>(P.lanes, on, x, inv, lse);
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
 #pragma unroll
       for (int c = 0; c < NC; ++c)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) acc[c][k] += x[u][c][k];
+        for (int k = 0; k < 8; k += 2) {
+          const float2 p = __ffma2_rn(make_float2(x[u][c][k], x[u][c][k + 1]), make_float2(inv[u], inv[u]),
+                                      make_float2(acc[c][k], acc[c][k + 1]));
+          acc[c][k] = p.x;
+          acc[c][k + 1] = p.y;
+        }
       if (on[u] && sub == 0) {
         sq += lse[u] * lse[u];
         ++tokens;
@@ -428,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 4) balance_grad(const __grid_constan
       a[c][k] = e < P.experts ? gb * P.weights[g * P.experts + e] : 0.0f;
     }
   for (long long r = r0 + warp * rows_warp; r < r1; r += kU * kWarps * rows_warp) {
-    float x[kU][NC][8], lse[kU], s[kU];
+    float x[kU][NC][8], inv[kU], lse[kU], s[kU];
     bool in[kU], on[kU];
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
@@ -438,14 +448,16 @@ __global__ void __launch_bounds__(kThreads, 4) balance_grad(const __grid_constan
     }
 #pragma unroll
     for (int u = 0; u < kU; ++u) load_row<BF16, NC, VEC>(P, first + r + u * kWarps * rows_warp + mine, sub, on[u], x[u]);
-    softmax_rows<NC, kU>(P.lanes, on, x, lse);
+    softmax_rows<NC, kU>(P.lanes, on, x, inv, lse);
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      s[u] = 0.0f;
+      float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
       for (int c = 0; c < NC; ++c)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) s[u] = fmaf(a[c][k], x[u][c][k], s[u]);
+        for (int k = 0; k < 8; k += 2)
+          sum = __ffma2_rn(make_float2(a[c][k], a[c][k + 1]), make_float2(x[u][c][k], x[u][c][k + 1]), sum);
+      s[u] = sum.x + sum.y;
     }
     for (int d = P.lanes / 2; d > 0; d /= 2)
 #pragma unroll
@@ -453,11 +465,17 @@ __global__ void __launch_bounds__(kThreads, 4) balance_grad(const __grid_constan
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       if (!in[u]) continue;
-      const float shift = gz * lse[u] - s[u];
+      // e inv (a + shift), with the sum of a p in the shift
+      const float shift = on[u] ? (gz * lse[u] - s[u] * inv[u]) * inv[u] : 0.0f;
 #pragma unroll
       for (int c = 0; c < NC; ++c)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[u][c][k] = on[u] ? x[u][c][k] * (a[c][k] + shift) : 0.0f;
+        for (int k = 0; k < 8; k += 2) {
+          const float2 w = __ffma2_rn(make_float2(a[c][k], a[c][k + 1]), make_float2(inv[u], inv[u]), make_float2(shift, shift));
+          const float2 v = __fmul2_rn(make_float2(x[u][c][k], x[u][c][k + 1]), w);
+          x[u][c][k] = on[u] ? v.x : 0.0f;
+          x[u][c][k + 1] = on[u] ? v.y : 0.0f;
+        }
       store_row<BF16, NC, VEC>(P, first + r + u * kWarps * rows_warp + mine, sub, x[u]);
     }
   }
@@ -471,6 +489,7 @@ __global__ void __launch_bounds__(kThreads, 4) balance_grad(const __grid_constan
 template <typename T>
 __device__ __forceinline__ T* load_tile(const BalanceParams& P, long long row, int rows, unsigned char* tile) {
   const T* x = static_cast<const T*>(P.x) + row * P.stride;
+  if (!MUON_CHECK(row >= 0 && row + rows <= P.tokens_all && rows <= P.tile_rows)) rows = 0;
   const int n = rows * P.experts, t = threadIdx.x;
   if (P.stride != P.experts) {
     T* const to = reinterpret_cast<T*>(tile);
@@ -768,6 +787,7 @@ extern "C" muon_status_t balance_loss(const void* logits, int dtype, int64_t tok
   P.ids = ids;
   P.mask = mask;
   P.stride = row_stride;
+  P.tokens_all = tokens;
   P.group_rows = s.group_rows;
   P.cta_rows = s.cta_rows;
   P.groups = groups;
@@ -846,6 +866,7 @@ extern "C" muon_status_t balance_loss_backward(const void* logits, int dtype, in
   P.grad = grad;
   P.stride = row_stride;
   P.grad_stride = grad_stride;
+  P.tokens_all = tokens;
   P.group_rows = s.group_rows;
   P.cta_rows = s.cta_rows;
   P.groups = groups;

@@ -75,7 +75,8 @@ struct LogprobParams {
   int vocab, top;
   float scale;
   int lanes;        // logprob_warp: lanes per row
-  int log_ranks;    // logprob_row: CTAs per row, as a power of two
+  int log_ranks;    // logprob_score, logprob_loss: CTAs per row, as a power of two
+  int segment;      // logprob_loss: vectors that a CTA has room for
   int chunks;       // logprob_grad: CTAs per row
 };
 
@@ -800,6 +801,8 @@ __device__ __forceinline__ RowPart<BF16> part_of(const LogprobParams& P, long lo
   p.v0 = static_cast<int>(static_cast<unsigned>(R.count * rank) >> P.log_ranks);
   p.n = static_cast<int>(static_cast<unsigned>(R.count * (rank + 1)) >> P.log_ranks) - p.v0;
   p.per = static_cast<unsigned>(p.n + 4 * THREADS - 1) / (4 * THREADS) * THREADS;
+  if (!MUON_CHECK(row >= 0 && row < P.rows && p.v0 + p.n <= R.count)) p.n = 0;
+  if (!MUON_CHECK(P.segment == 0 || p.n <= P.segment)) p.n = P.segment;
   p.src = R.base + p.v0 * 16LL;
   p.shift = R.shift;
   p.lo = R.shift > 0 ? 1 : 0;
@@ -1318,6 +1321,7 @@ cudaError_t launch_loss(LogprobParams P, bool bf16, long long bytes, int sms, cu
   const long long part = (bytes + 15) / 16 / ranks + 1;  // vectors
   const bool wide = part > 2048;                         // 32 KB: 256 threads take eight vectors each
   const KernelPtr f = kLossKernels[(wide ? 1 : 0) | (P.top > 0 ? 2 : 0) | (bf16 ? 4 : 0)];
+  P.segment = static_cast<int>(part);
   const size_t smem = static_cast<size_t>(part) * 16;
   const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(f), cudaFuncAttributeMaxDynamicSharedMemorySize, kSegmentBytes + 64);
   if (e != cudaSuccess) return e;
