@@ -715,10 +715,51 @@ __device__ __forceinline__ void collect_seen(float own, int chunks, int each, in
   __syncthreads();
 }
 
+// gather() collects what reaches the bound.  Where that is more than there is
+// room for, many entries equal the bound (a mask that leaves fewer than `top`
+// entries, logits that a coarse type makes equal): then it collects what is
+// above the bound, and of the entries first .. last-1 of the row in global
+// memory the first ones that equal it are added, as many as `top` takes.
+template <bool BF16, int THREADS, int CHUNKS, typename G>
+__device__ __forceinline__ void gather_top(int top, const void* x, long long base, int first, int last, TopScratch<THREADS, CHUNKS>& S,
+                                           G gather) {
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  int pass = 0;
+#pragma unroll 1
+  for (;; ++pass) {
+    gather();
+    if (pass == 1 || S.n <= kCandidates) break;
+    __syncthreads();
+    if (t == 0) S.n = S.hits = 0, ++S.bound;
+    __syncthreads();
+  }
+  if (pass == 0 || S.n > kCandidates) return;
+  const uint32_t equal = S.bound - 1;
+  int n = S.n;
+  for (int from = first; n < top && from < last; from += THREADS) {
+    const int j = from + t;
+    const float v = j < last ? at<BF16>(x, base + j) : 0.0f;
+    const bool tie = j < last && ordered(v) == equal;
+    const unsigned ties = __ballot_sync(0xFFFFFFFFu, tie);
+    __syncthreads();  // S.best has been read
+    if (lane == 0) S.best[warp] = __popc(ties);
+    __syncthreads();
+    int place_ = n + __popc(ties & ((1u << lane) - 1));
+    for (int w = 0; w < THREADS / 32; ++w) {
+      const int count = static_cast<int>(S.best[w]);
+      if (w < warp) place_ += count;
+      n += count;
+    }
+    if (tie && place_ < top) S.candidate[place_] = place(v, j);
+  }
+  __syncthreads();
+  if (t == 0) S.n = max(S.n, min(n, top));
+  __syncthreads();
+}
+
 // Ranks what was collected by counting, into S.top (0 where there are fewer).
-// Where more was collected than there is room for (ties, masks that leave
-// fewer than `top` entries) it takes one maximum after the other of `x`, the
-// entries first .. last-1 of a row in global memory.
+// Where more was collected than there is room for it takes one maximum after
+// the other of `x`, the entries first .. last-1 of a row in global memory.
 template <bool BF16, int THREADS, int CHUNKS>
 __device__ __forceinline__ void top_rank(int top, const void* x, long long base, int first, int last, TopScratch<THREADS, CHUNKS>& S) {
   const int t = threadIdx.x, n = S.n;
@@ -797,9 +838,9 @@ template <bool BF16, int THREADS>
 __device__ __forceinline__ RowPart<BF16> part_of(const LogprobParams& P, long long row, int rank) {
   const RowVectors<BF16> R(P.x, row * P.stride, P.vocab);
   RowPart<BF16> p;
-  // fewer than 2^17 vectors and a power of two of CTAs: no division
-  p.v0 = static_cast<int>(static_cast<unsigned>(R.count * rank) >> P.log_ranks);
-  p.n = static_cast<int>(static_cast<unsigned>(R.count * (rank + 1)) >> P.log_ranks) - p.v0;
+  // at most 2^28 + 1 vectors and eight CTAs, a power of two of them: no division
+  p.v0 = static_cast<int>(static_cast<unsigned>(R.count) * rank >> P.log_ranks);
+  p.n = static_cast<int>(static_cast<unsigned>(R.count) * (rank + 1) >> P.log_ranks) - p.v0;
   p.per = static_cast<unsigned>(p.n + 4 * THREADS - 1) / (4 * THREADS) * THREADS;
   if (!MUON_CHECK(row >= 0 && row < P.rows && p.v0 + p.n <= R.count)) p.n = 0;
   if (!MUON_CHECK(P.segment == 0 || p.n <= P.segment)) p.n = P.segment;
@@ -952,7 +993,9 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 8 : 3) logprob_loss(
     }
     if constexpr (TOP) {
       top_bound(P.top, own, S);
-      collect_seen<BF16>(own, 4, p.per / THREADS, p.n, p.first(0), P.vocab, [&](int i) { return q[i]; }, S);
+      gather_top<BF16>(P.top, P.x, base, j0, j1, S, [&] {
+        collect_seen<BF16>(own, 4, p.per / THREADS, p.n, p.first(0), P.vocab, [&](int i) { return q[i]; }, S);
+      });
       top_rank<BF16>(P.top, P.x, base, j0, j1, S);
       if (ranks > 1) {
         if (t < P.top) cluster.map_shared_rank(&X, 0)->top[rank][t] = S.top[t];
@@ -1123,9 +1166,12 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprob_score(const _
     for (int k = 1; k < kWarps; ++k) sums = merge(sums, warp_sums[k], c2);
   }
   if constexpr (TOP) {
-    if (warp < 2) collect<BF16>(end, p.first(t == 0 ? 0 : p.n - 1), P.vocab, S);
-    collect_seen<BF16>(own, chunks, kU << log_chunk, n, p.first(head), P.vocab, [&](int i) { return load_once(src + i); }, S);
-    top_rank<BF16>(P.top, P.x, base, max(0, p.first(0)), min(P.vocab, p.first(p.n)), S);
+    const int j0 = max(0, p.first(0)), j1 = min(P.vocab, p.first(p.n));
+    gather_top<BF16>(P.top, P.x, base, j0, j1, S, [&] {
+      if (warp < 2) collect<BF16>(end, p.first(t == 0 ? 0 : p.n - 1), P.vocab, S);
+      collect_seen<BF16>(own, chunks, kU << log_chunk, n, p.first(head), P.vocab, [&](int i) { return load_once(src + i); }, S);
+    });
+    top_rank<BF16>(P.top, P.x, base, j0, j1, S);
   }
   if (ranks > 1) {
     cg::cluster_group::barrier_wait();

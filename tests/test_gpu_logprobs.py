@@ -157,6 +157,33 @@ def test_alternatives_with_ties_and_orders(what, kind):
     run_all(x, np.array([3, 8999]), kind, 1.0, 32)
 
 
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,vocab", [(3, 50_257), (400, 12_345), (700, 70_001)])
+def test_alternatives_among_many_equal_entries(rows, vocab, kind):
+    """Rows whose best entries are fewer than the alternatives asked for, all others equal (a mask, or a floor):
+    the first of these follow by index; and rows of three values, with and without entries below the equal ones."""
+    rng = np.random.default_rng(vocab)
+    fill = [-np.inf, float(torch.finfo(KIND[kind]).min), -9984.0, 0.0]
+    x = np.stack([np.full(vocab, fill[i % 4]) for i in range(rows)])
+    for i in range(rows):
+        few = rng.integers(0, vocab, (i // 4) % 24)
+        x[i, few] = rng.integers(1, 5, len(few))
+        low = rng.integers(0, vocab, vocab // 2)
+        if i % 8 >= 4:
+            x[i, low] = np.where(x[i, low] == fill[i % 4], -np.inf, x[i, low])
+        if i % 16 == 15:
+            x[i, : vocab // 2] = rng.integers(0, 3, vocab // 2)
+    y = rng.integers(0, vocab, rows)
+    X, Y = place(x, kind), torch.from_numpy(y).cuda()
+    for top in (1, 20):
+        order = np.argsort(-x, axis=1, kind="stable")[:, :top]
+        gl = torch.ones(rows, device="cuda")
+        for r in (muon.token_logprobs(X, Y, top=top), muon.token_logprobs_loss(X, Y, gl, top=top)):
+            np.testing.assert_array_equal(r.top_ids.cpu().numpy(), order)
+    few = np.array([i for i in range(0, rows, 37) if i % 4 != 1])
+    check_score(muon.token_logprobs(X[few], Y[few], top=5), x[few], y[few], 1.0, 5)
+
+
 def test_rows_left_out_are_not_read():
     """Targets below 0: zeros and -1 ids, gradient zero, even where the logits are NaN."""
     x = np.random.default_rng(0).standard_normal((6, 333))
