@@ -1,12 +1,14 @@
 // AdamW over many tensors at once, moments in 32 bits or in 8.
 //
-// Per element, t the step, in float32 (each operation rounded, none fused, so
-// that codes do not depend on how the compiler contracts):
+// Per element, t the step, in float32:
 //   g' = grad_scale * g
 //   m1 = b1 m + (1-b1) g';   v1 = b2 v + (1-b2) (g' g')
 //   u  = m1 / (sqrt(v1) r2 + eps),           r2 = 1 / sqrt(1 - b2^t)
 //   p1 = p - (u lr/(1-b1^t) + lr wd p mask), mask as in the cautious Adam step
-// with the scalars formed in double on the host and rounded once.
+// with the scalars formed in double on the host and rounded once.  In the
+// moments every operation is rounded and none fused, so that codes do not
+// depend on how the compiler contracts; u takes the approximate root and
+// reciprocal (a few units in the last place of a change that is small beside p).
 //
 // 8-bit moments.  A block of 256 consecutive elements of a tensor shares a
 // power-of-two scale.  E = floor(log2 max |x|) (at least -100); the first
@@ -29,6 +31,11 @@
 // Work: one warp per 256-element block, 8 elements a lane; eight warps share
 // eight blocks of one tensor.  One launch covers up to kMaxTensors tensors of
 // the same types; the table is in the kernel's parameters.
+// Bound: 32-bit moments by HBM (float32 parameters, bfloat16 gradients: 26
+// bytes an element, 154.5 M of them 565 us, 7.1 TB/s); 8-bit ones by HBM and
+// instruction issue alike (14 bytes, about 53 instructions: 373 us, 5.8 TB/s);
+// bfloat16 parameters off a 16-byte boundary by issue (10 bytes, 62
+// instructions: 226 us for 82.3 M, 3.6 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -50,6 +57,7 @@ constexpr int kQBlock = 256;       // elements that share a scale
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxTensors = 400;   // per launch: the table fills the 32 KB of kernel parameters
+constexpr int kFewTensors = 44;    // 4 KB: a call of one tensor takes 8.3 us, 9.7 with the large table
 
 struct AdamwTensor {
   void* p;
@@ -68,13 +76,16 @@ struct AdamwTensor {
 };
 
 struct AdamwParams {
-  AdamwTensor t[kMaxTensors];
   int n;
   int cautious;
   float b1, b2, omb1, omb2, r2, eps;
   const float* grad_scale;
 };
-static_assert(sizeof(AdamwParams) <= 32764, "kernel parameters are limited to 32764 bytes");
+template <int N>
+struct AdamwTable : AdamwParams {
+  AdamwTensor t[N];
+};
+static_assert(sizeof(AdamwTable<kMaxTensors>) <= 32764, "kernel parameters are limited to 32764 bytes");
 
 constexpr uint32_t kC0 = 0x9E3779B1u, kC1 = 0x6A09E667u, kC2 = 0xBB67AE85u;
 
@@ -433,8 +444,8 @@ __device__ __forceinline__ void step_block(const AdamwParams& P, const AdamwTens
 // One block a warp: the CTAs at work then cover one stretch of every array.
 // With eight blocks a warp, CTAs 16,384 elements apart, the 8-bit step of
 // 100.7 M float32 parameters took 358 us in place of 250.
-template <bool PB, bool GB, bool B8>
-__global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constant__ AdamwParams P) {
+template <bool PB, bool GB, bool B8, int N>
+__global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constant__ AdamwTable<N> P) {
   int lo = 0, hi = P.n - 1;  // the tensor: largest i with first <= blockIdx.x
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -476,13 +487,15 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constan
   }
 }
 
-using KernelPtr = void (*)(AdamwParams);
+template <int N>
+using KernelPtr = void (*)(AdamwTable<N>);
 
 // Index: bfloat16 parameters | bfloat16 gradients << 1 | 8-bit moments << 2.
-const KernelPtr kKernels[8] = {
-    adamw_kernel<false, false, false>, adamw_kernel<true, false, false>, adamw_kernel<false, true, false>,
-    adamw_kernel<true, true, false>,   adamw_kernel<false, false, true>, adamw_kernel<true, false, true>,
-    adamw_kernel<false, true, true>,   adamw_kernel<true, true, true>,
+template <int N>
+const KernelPtr<N> kKernels[8] = {
+    adamw_kernel<false, false, false, N>, adamw_kernel<true, false, false, N>, adamw_kernel<false, true, false, N>,
+    adamw_kernel<true, true, false, N>,   adamw_kernel<false, false, true, N>, adamw_kernel<true, false, true, N>,
+    adamw_kernel<false, true, true, N>,   adamw_kernel<true, true, true, N>,
 };
 
 // Whether a lane may take eight neighbouring elements: 16-byte float32 arrays,
@@ -578,6 +591,23 @@ muon_status_t adamw_plan::build() {
 namespace muon {
 namespace {
 
+template <int N>
+cudaError_t launch(const adamw_plan& plan, const adamw_plan::Launch& l, const AdamwParams& scalars, double bc1, uint32_t key,
+                   cudaStream_t s) {
+  AdamwTable<N> P;
+  static_cast<AdamwParams&>(P) = scalars;
+  P.n = static_cast<int>(l.t.size());
+  std::memcpy(P.t, l.t.data(), l.t.size() * sizeof(AdamwTensor));
+  for (int i = 0; i < P.n; ++i) {
+    const adamw_tensor_desc& d = plan.desc[l.index[i]];
+    P.t[i].step = static_cast<float>(d.lr / bc1);
+    P.t[i].decay = static_cast<float>(d.lr * d.weight_decay);
+    P.t[i].key = mix(key + kC0 * static_cast<uint32_t>(l.index[i]));
+  }
+  kKernels<N>[l.kind]<<<static_cast<unsigned>(l.ctas), kThreads, 0, s>>>(P);
+  return cudaGetLastError();
+}
+
 muon_status_t run_plan(const adamw_plan& plan, double beta1, double beta2, double eps, int cautious, int64_t step,
                        uint64_t seed, const float* grad_scale, cudaStream_t s) {
   if (step < 1 || !(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || !(eps >= 0.0) ||
@@ -595,26 +625,19 @@ muon_status_t run_plan(const adamw_plan& plan, double beta1, double beta2, doubl
   const muon_status_t st = device_sms(sms);
   if (st != MUON_OK) return st;
   const uint32_t k = mix(mix(static_cast<uint32_t>(seed) + kC0 * static_cast<uint32_t>(step)) ^ static_cast<uint32_t>(seed >> 32));
+  AdamwParams P;
+  P.cautious = cautious ? 1 : 0;
+  P.b1 = static_cast<float>(beta1);
+  P.b2 = static_cast<float>(beta2);
+  P.omb1 = static_cast<float>(1.0 - beta1);
+  P.omb2 = static_cast<float>(1.0 - beta2);
+  P.r2 = static_cast<float>(1.0 / std::sqrt(bc2));
+  P.eps = static_cast<float>(eps);
+  P.grad_scale = grad_scale;
   for (const auto& l : plan.launches) {
-    AdamwParams P;
-    P.n = static_cast<int>(l.t.size());
-    std::memcpy(P.t, l.t.data(), l.t.size() * sizeof(AdamwTensor));
-    for (int i = 0; i < P.n; ++i) {
-      const adamw_tensor_desc& d = plan.desc[l.index[i]];
-      P.t[i].step = static_cast<float>(d.lr / bc1);
-      P.t[i].decay = static_cast<float>(d.lr * d.weight_decay);
-      P.t[i].key = mix(k + kC0 * static_cast<uint32_t>(l.index[i]));
-    }
-    P.cautious = cautious ? 1 : 0;
-    P.b1 = static_cast<float>(beta1);
-    P.b2 = static_cast<float>(beta2);
-    P.omb1 = static_cast<float>(1.0 - beta1);
-    P.omb2 = static_cast<float>(1.0 - beta2);
-    P.r2 = static_cast<float>(1.0 / std::sqrt(bc2));
-    P.eps = static_cast<float>(eps);
-    P.grad_scale = grad_scale;
-    kKernels[l.kind]<<<static_cast<unsigned>(l.ctas), kThreads, 0, s>>>(P);
-    if (cudaGetLastError() != cudaSuccess) return MUON_ERR_CUDA;
+    const cudaError_t e = l.t.size() <= static_cast<size_t>(kFewTensors) ? launch<kFewTensors>(plan, l, P, bc1, k, s)
+                                                                         : launch<kMaxTensors>(plan, l, P, bc1, k, s);
+    if (e != cudaSuccess) return MUON_ERR_CUDA;
   }
   return MUON_OK;
 }
