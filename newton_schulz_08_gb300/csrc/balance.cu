@@ -51,6 +51,7 @@ constexpr int kTileExperts = 256;     // most experts of the tiled kernels
 constexpr int kTileBytes = 42 * 1024;  // of a tile: four CTAs per SM
 constexpr int kTargetCtas = 608;  // four per SM
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kFar = 1e30f;     // beyond it x log2(e) may leave float32's range
 
 struct BalanceParams {
   const void* x;
@@ -185,7 +186,14 @@ __device__ __forceinline__ void softmax_rows(int lanes, const bool (&on)[U], flo
     for (int u = 0; u < U; ++u) m[u] = fmaxf(m[u], __shfl_xor_sync(0xFFFFFFFFu, m[u], d));
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const float shift = on[u] ? -m[u] * kLog2e : 0.0f;
+    float shift = on[u] ? -m[u] * kLog2e : 0.0f;
+    if (on[u] && fabsf(m[u]) > kFar) {  // a mask of the type's lowest value over the whole row
+      shift = 0.0f;
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[u][c][k] -= m[u];
+    }
     float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int c = 0; c < NC; ++c)

@@ -149,6 +149,34 @@ def test_masked_experts_and_non_finite_rows():
     assert torch.isnan(G[5]).all()
 
 
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("experts", [16, 21, 256, 301, 520, 1024])
+def test_experts_masked_with_the_lowest_value(experts, kind):
+    """A mask of the type's lowest value over some experts, and over whole rows, whose
+    probabilities are then equal; the balance loss and its gradient are as in any other row."""
+    x, ids, _ = case(64, experts, 2, kind, seed=3)
+    x[:, experts // 2] = x[::2, 3] = x[7] = x[33] = torch.finfo(KIND[kind]).min
+    z = host(x)
+    want, one, zero = oracle.balance_loss(z, ids, None, 4), torch.ones(1, device="cuda"), torch.zeros(1, device="cuda")
+    X = x.cuda()
+    r = muon.balance_loss(X, dev(ids), groups=4)
+    live = np.where(z > -1e30, z, 0)
+    D = float((live.max(axis=1) - live.min(axis=1)).max())
+    eps = 2.0 ** -21 * (1 + D)
+    assert (np.abs(host(r.mean_probs) - want["mean"]) <= (eps + 2.0 ** -19) * want["mean"] + 1e-40).all()
+    assert abs(float(r.balance) - want["balance"]) <= (eps + 2.0 ** -18) * want["balance"]
+    G = host(muon.balance_loss_backward(X, r, one, zero))
+    wg = oracle.balance_loss_grad(z, ids, np.float32(1), np.float32(0), None, 4)
+    p = np.exp(z - z.max(axis=1, keepdims=True))
+    p = p / p.sum(axis=1, keepdims=True)
+    f = want["counts"] / want["counts"].sum(axis=1, keepdims=True)
+    w = np.repeat(experts / 4 / 16 * (f.max(axis=1, keepdims=True) * 2 + 1.0 / experts), 16, axis=0)
+    tol = 2 * eps * p * w + 2.0 ** -22 * np.abs(wg) + 1e-42
+    if kind == "bf16":
+        tol = tol * (1 + 2.0 ** -8) + 2.0 ** -8 * 1.01 * np.abs(wg) + 2.0 ** -133
+    assert (np.abs(G - wg) <= tol).all()
+
+
 def test_equal_calls_and_other_stream_give_equal_bits():
     x, ids, mask = case(50_000, 96, 4, "bf16", masked=0.1)
     X, I, M = x.cuda(), dev(ids), dev(mask)
