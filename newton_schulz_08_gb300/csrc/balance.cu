@@ -25,9 +25,10 @@
 //
 // Forward, two launches.  balance_rows: each CTA takes consecutive rows of
 // one group and leaves partial sums of p and lse^2, counts and the numbers of
-// tokens and assignments in the workspace.  balance_finish: one CTA per group adds the partials in
-// their order, and the last CTA to arrive adds the groups in theirs, so equal
-// calls give equal bits; only whole numbers are added with atomics.
+// tokens and assignments in the workspace.  balance_finish: each CTA adds the
+// partials of some experts of a group in their order, and the last CTA to
+// arrive adds the losses in theirs, so equal calls give equal bits; only whole
+// numbers are added with atomics.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -66,12 +67,14 @@ struct BalanceParams {
   int parts;             // CTAs per group
   int experts, top, lanes;
   int tile_rows;         // rows of a tile, a power of two up to kThreads
+  int width, slices;     // balance_finish: experts of a CTA (a power of two), CTAs per group
   // partial results of CTA i: sums[i][experts], counts[i][experts], numbers[i] (tokens, assignments), squares[i]
   float* sums;
   int* part_counts;
   int2* numbers;
   float* squares;
-  float* group_loss;
+  float* group_loss;     // of balance_finish's CTAs
+  float* group_squares;
   unsigned* arrived;
   // results
   float* stats;
@@ -330,69 +333,68 @@ __global__ void __launch_bounds__(kThreads, 4) balance_rows(const __grid_constan
   }
 }
 
-// One CTA per group.  Every warp adds up the numbers of tokens and
-// assignments for itself; the experts' partials are dealt over the threads.
+// A CTA takes `width` experts of a group, their partials dealt over its threads.
 __global__ void __launch_bounds__(kFinishThreads) balance_finish(const __grid_constant__ BalanceParams P) {
+  constexpr int kFinishWarps = kFinishThreads / 32;
   __shared__ float s_sum[kFinishThreads];
   __shared__ int s_cnt[kFinishThreads];
-  __shared__ float s_loss[kFinishThreads / 32];
-  __shared__ float3 s_all[kFinishThreads / 32];
+  __shared__ float3 s_all[kFinishWarps];
+  __shared__ int2 s_numbers[kFinishWarps];
+  __shared__ float s_loss[kFinishWarps];
   __shared__ unsigned s_last;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int t = threadIdx.x, lane = t & 31;
-  const long long g = blockIdx.x, base = g * P.parts;
-  // `width` experts at a time, the partials dealt over the threads left
-  int width = 32;
-  while (width < P.experts && width < kFinishThreads) width *= 2;
-  const int deals = kFinishThreads / width, deal = t / width;
-  int n = 0, assigned = 0;
-#pragma unroll 4
-  for (int i = lane; i < P.parts; i += 32) {
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int slice = blockIdx.x % P.slices, deals = kFinishThreads / P.width, deal = t / P.width;
+  const long long g = blockIdx.x / P.slices, base = g * P.parts;
+  const int e = slice * P.width + (t & (P.width - 1));
+  int2 n = make_int2(0, 0);  // tokens, assignments
+  float squares = 0.0f;
+  for (int i = t; i < P.parts; i += kFinishThreads) {
     const int2 m = P.numbers[base + i];
-    n += m.x;
-    assigned += m.y;
+    squares += P.squares[base + i];
+    n.x += m.x;
+    n.y += m.y;
   }
-  float loss = 0.0f, inv_n = 0.0f, share = 0.0f;
-  for (int e0 = 0; e0 < P.experts; e0 += width) {
-    const int e = e0 + (t & (width - 1));
-    float s = 0.0f;
-    int c = 0;
-    if (e < P.experts) {
+  float s = 0.0f;
+  int c = 0;
+  if (e < P.experts) {
 #pragma unroll 8
-      for (int i = deal; i < P.parts; i += deals) {
-        s += P.sums[(base + i) * P.experts + e];
-        c += P.part_counts[(base + i) * P.experts + e];
-      }
+    for (int i = deal; i < P.parts; i += deals) {
+      s += P.sums[(base + i) * P.experts + e];
+      c += P.part_counts[(base + i) * P.experts + e];
     }
-    if (e0 == 0) {
-      n = warp_sum(n);
-      assigned = warp_sum(assigned);
-      inv_n = n > 0 ? 1.0f / static_cast<float>(n) : 0.0f;
-      share = assigned > 0 ? static_cast<float>(P.experts) / static_cast<float>(assigned) : 0.0f;
-    }
-    if (deals > 1) {
-      s_sum[t] = s;
-      s_cnt[t] = c;
-      __syncthreads();
-      if (deal == 0)
-        for (int k = 1; k < deals; ++k) s += s_sum[k * width + t], c += s_cnt[k * width + t];
-    }
-    if (deal == 0 && e < P.experts) {
-      const float mean = s * inv_n, f = share * static_cast<float>(c);  // experts * f_e
-      loss += f * mean;
-      P.counts[g * P.experts + e] = c;
-      P.mean[g * P.experts + e] = mean;
-      P.weights[g * P.experts + e] = assigned > 0 ? (f - 1.0f) * inv_n : 0.0f;
-    }
+  }
+  n.x = warp_sum(n.x);
+  n.y = warp_sum(n.y);
+  squares = warp_sum(squares);
+  if (lane == 0) s_numbers[warp] = n, s_loss[warp] = squares;
+  s_sum[t] = s;
+  s_cnt[t] = c;
+  __syncthreads();
+  n = make_int2(0, 0);
+  squares = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kFinishWarps; ++w) n.x += s_numbers[w].x, n.y += s_numbers[w].y, squares += s_loss[w];
+  const float inv_n = n.x > 0 ? 1.0f / static_cast<float>(n.x) : 0.0f;
+  const float share = n.y > 0 ? static_cast<float>(P.experts) / static_cast<float>(n.y) : 0.0f;
+  float loss = 0.0f;
+  if (deal == 0 && e < P.experts) {
+    for (int k = 1; k < deals; ++k) s += s_sum[k * P.width + t], c += s_cnt[k * P.width + t];
+    const float mean = s * inv_n, f = share * static_cast<float>(c);  // experts * f_e
+    loss = f * mean;
+    P.counts[g * P.experts + e] = c;
+    P.mean[g * P.experts + e] = mean;
+    P.weights[g * P.experts + e] = n.y > 0 ? (f - 1.0f) * inv_n : 0.0f;
   }
   loss = warp_sum(loss);
-  if (lane == 0) s_loss[t >> 5] = loss;
+  __syncthreads();
+  if (lane == 0) s_loss[warp] = loss;
   __syncthreads();
   if (t == 0) {
     loss = 0.0f;
-    for (int w = 0; w < kFinishThreads / 32; ++w) loss += s_loss[w];
-    P.group_loss[g] = loss;
-    P.tokens[g] = n;
+    for (int w = 0; w < kFinishWarps; ++w) loss += s_loss[w];
+    P.group_loss[blockIdx.x] = loss;
+    if (slice == 0) P.tokens[g] = n.x, P.group_squares[g] = squares;
     __threadfence();
     s_last = gridDim.x == 1 || atomicAdd(P.arrived, 1u) + 1u == gridDim.x;
   }
@@ -401,22 +403,22 @@ __global__ void __launch_bounds__(kFinishThreads) balance_finish(const __grid_co
   __threadfence();
   float3 all = make_float3(0.0f, 0.0f, 0.0f);  // losses, squares, tokens
   int some = 0;
-  for (long long i = t; i < P.groups; i += kFinishThreads) {
+  for (long long i = t; i < P.groups * P.slices; i += kFinishThreads) {
     all.x += __ldcg(P.group_loss + i);
+    if (i >= P.groups) continue;
     const int k = __ldcg(P.tokens + i);
+    all.y += __ldcg(P.group_squares + i);
     all.z += static_cast<float>(k);
     some += k > 0;
   }
-#pragma unroll 4
-  for (long long i = t; i < P.groups * P.parts; i += kFinishThreads) all.y += P.squares[i];
   all = make_float3(warp_sum(all.x), warp_sum(all.y), warp_sum(all.z));
   some = warp_sum(some);
-  if (lane == 0) s_all[t >> 5] = all, s_cnt[t >> 5] = some;
+  if (lane == 0) s_all[warp] = all, s_cnt[warp] = some;
   __syncthreads();
   if (t == 0) {
     all = make_float3(0.0f, 0.0f, 0.0f);
     some = 0;
-    for (int w = 0; w < kFinishThreads / 32; ++w) {
+    for (int w = 0; w < kFinishWarps; ++w) {
       all.x += s_all[w].x, all.y += s_all[w].y, all.z += s_all[w].z;
       some += s_cnt[w];
     }
@@ -677,9 +679,10 @@ const KernelPtr kRows[12] = {KERNELS(balance_rows)};
 const KernelPtr kGrad[12] = {KERNELS(balance_grad)};
 #undef KERNELS
 
-// The split of the rows: lanes per row, CTAs per group, rows per CTA.
+// The split of the rows: lanes per row, CTAs per group, rows per CTA; and of
+// balance_finish: experts of a CTA, CTAs per group.
 struct Split {
-  int lanes, kernel, parts;
+  int lanes, kernel, parts, width, slices;
   long long group_rows, cta_rows;
 };
 
@@ -702,6 +705,12 @@ Split split_of(int64_t tokens, int experts, int64_t groups) {
   if (s.cta_rows < 1) s.cta_rows = 1;
   s.parts = static_cast<int>((s.group_rows + s.cta_rows - 1) / s.cta_rows);
   if (s.parts < 1) s.parts = 1;
+  // at least one partial a thread, 32 experts a warp: 131072 x 256 in one group
+  // leaves 608 partials an expert: the call takes 60 us over eight CTAs, 86 in
+  // one (65536 x 160: 36 and 60; 16384 x 520: 42 and 116)
+  s.width = 32;
+  while (s.width < kFinishThreads && s.width < experts && kFinishThreads / s.width > s.parts) s.width *= 2;
+  s.slices = (experts + s.width - 1) / s.width;
   return s;
 }
 
@@ -716,7 +725,7 @@ size_t use_tiles(BalanceParams& P, int size) {
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 struct Layout {
-  size_t arrived, sums, counts, tokens, squares, loss, total;
+  size_t arrived, sums, counts, tokens, squares, loss, group_squares, total;
 };
 
 Layout layout_of(const Split& s, int experts, int64_t groups) {
@@ -728,7 +737,8 @@ Layout layout_of(const Split& s, int experts, int64_t groups) {
   l.tokens = l.counts + up256(n * experts * 4);
   l.squares = l.tokens + up256(n * 8);
   l.loss = l.squares + up256(n * 4);
-  l.total = l.loss + up256(static_cast<size_t>(groups) * 4);
+  l.group_squares = l.loss + up256(static_cast<size_t>(groups) * s.slices * 4);
+  l.total = l.group_squares + up256(static_cast<size_t>(groups) * 4);
   return l;
 }
 
@@ -737,7 +747,8 @@ muon_status_t check_shape(int dtype, int64_t tokens, int experts, int64_t stride
   if (tokens < 0 || experts < 1 || experts > kMaxExperts || groups < 1 || stride < experts) return MUON_ERR_INVALID_ARG;
   if (tokens % groups != 0) return MUON_ERR_INVALID_ARG;
   if (tokens > INT32_MAX || groups > INT32_MAX || stride > (1LL << 32)) return MUON_ERR_TOO_LARGE;
-  if (split_of(tokens, experts, groups).parts * groups > INT32_MAX) return MUON_ERR_TOO_LARGE;
+  const Split s = split_of(tokens, experts, groups);
+  if (s.parts * groups > INT32_MAX || s.slices * groups > INT32_MAX) return MUON_ERR_TOO_LARGE;
   return MUON_OK;
 }
 
@@ -803,6 +814,8 @@ extern "C" muon_status_t balance_loss(const void* logits, int dtype, int64_t tok
   P.experts = experts;
   P.top = top;
   P.lanes = s.lanes;
+  P.width = s.width;
+  P.slices = s.slices;
   const bool vec = experts % 8 == 0 && row_stride * size % 16 == 0 && aligned_to(logits, 16);
   P.arrived = reinterpret_cast<unsigned*>(ws + l.arrived);
   P.sums = reinterpret_cast<float*>(ws + l.sums);
@@ -810,6 +823,7 @@ extern "C" muon_status_t balance_loss(const void* logits, int dtype, int64_t tok
   P.numbers = reinterpret_cast<int2*>(ws + l.tokens);
   P.squares = reinterpret_cast<float*>(ws + l.squares);
   P.group_loss = reinterpret_cast<float*>(ws + l.loss);
+  P.group_squares = reinterpret_cast<float*>(ws + l.group_squares);
   P.stats = stats;
   P.counts = counts;
   P.tokens = n_tokens;
@@ -827,7 +841,7 @@ extern "C" muon_status_t balance_loss(const void* logits, int dtype, int64_t tok
   if (cudaGetLastError() != cudaSuccess) return MUON_ERR_CUDA;
   // launched while balance_rows still runs; it waits for that grid's end
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(groups));
+  cfg.gridDim = dim3(static_cast<unsigned>(s.slices * groups));
   cfg.blockDim = dim3(kFinishThreads);
   cfg.stream = str;
   cudaLaunchAttribute attr[1];
