@@ -17,7 +17,7 @@
 // 131072 x 256 float32: forward 31 us of 21 that its bytes take, backward 42 of
 // 40 (one set: 44 and 56; four leave room for fewer warps: 43 and 55; scalar
 // arithmetic in place of pairs: 36 and 48).
-// Rows off the 16-byte boundaries (an odd number of experts, up to 256) come
+// Rows off the 16-byte boundaries (a number of experts that is no multiple of 8) come
 // through shared memory in tiles instead, copied as one run: there a few
 // threads, without a shuffle each, take a row's sums, and then a thread an
 // expert's (65536 x 161 bfloat16: forward 28 -> 20 us, backward 42 -> 23,
@@ -48,7 +48,6 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kFinishThreads = 512;
 constexpr int kMaxExperts = 1024;
-constexpr int kTileExperts = 256;     // most experts of the tiled kernels
 constexpr int kTileBytes = 42 * 1024;  // of a tile: four CTAs per SM
 constexpr int kTargetCtas = 608;  // four per SM
 constexpr float kLog2e = 1.4426950408889634f;
@@ -92,14 +91,10 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Position of a lane's entry k of chunk c: neighbours in the vector layout,
-// L apart where rows are not aligned.
-template <bool VEC>
-__device__ __forceinline__ int entry(const BalanceParams& P, int c, int k, int sub) {
-  return VEC ? (c * P.lanes + sub) * 8 + k : c * P.lanes * 8 + k * P.lanes + sub;
-}
+// First entry of a lane's chunk c.
+__device__ __forceinline__ int entry(const BalanceParams& P, int c, int sub) { return (c * P.lanes + sub) * 8; }
 
-template <bool BF16, int NC, bool VEC>
+template <bool BF16, int NC>
 __device__ __forceinline__ void load_row(const BalanceParams& P, long long row, int sub, bool on, float (&x)[NC][8]) {
   const long long base = row * P.stride;
   if (!MUON_CHECK(!on || (row >= 0 && row < P.tokens_all))) on = false;
@@ -107,66 +102,45 @@ __device__ __forceinline__ void load_row(const BalanceParams& P, long long row, 
   for (int c = 0; c < NC; ++c) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) x[c][k] = -INFINITY;
-    if (!on) continue;
-    const int e0 = entry<VEC>(P, c, 0, sub);
-    if constexpr (VEC) {
-      if (e0 >= P.experts) continue;
-      if constexpr (BF16) {
-        const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(P.x) + base + e0);
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    const int e0 = entry(P, c, sub);
+    if (!on || e0 >= P.experts) continue;
+    if constexpr (BF16) {
+      const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(P.x) + base + e0);
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          x[c][2 * k] = __uint_as_float(w[k] << 16);
-          x[c][2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
-        }
-      } else {
-        const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(P.x) + base + e0);
-        const float4 a = f[0], b = f[1];
-        x[c][0] = a.x; x[c][1] = a.y; x[c][2] = a.z; x[c][3] = a.w;
-        x[c][4] = b.x; x[c][5] = b.y; x[c][6] = b.z; x[c][7] = b.w;
+      for (int k = 0; k < 4; ++k) {
+        x[c][2 * k] = __uint_as_float(w[k] << 16);
+        x[c][2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
       }
     } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int e = entry<VEC>(P, c, k, sub);
-        if (e >= P.experts) continue;
-        if constexpr (BF16) x[c][k] = __bfloat162float(static_cast<const __nv_bfloat16*>(P.x)[base + e]);
-        else x[c][k] = static_cast<const float*>(P.x)[base + e];
-      }
+      const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(P.x) + base + e0);
+      const float4 a = f[0], b = f[1];
+      x[c][0] = a.x; x[c][1] = a.y; x[c][2] = a.z; x[c][3] = a.w;
+      x[c][4] = b.x; x[c][5] = b.y; x[c][6] = b.z; x[c][7] = b.w;
     }
   }
 }
 
-template <bool BF16, int NC, bool VEC>
+template <bool BF16, int NC>
 __device__ __forceinline__ void store_row(const BalanceParams& P, long long row, int sub, const float (&x)[NC][8]) {
   const long long base = row * P.grad_stride;
   if (!MUON_CHECK(row >= 0 && row < P.tokens_all)) return;
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
-    const int e0 = entry<VEC>(P, c, 0, sub);
-    if constexpr (VEC) {
-      if (e0 >= P.experts) continue;
-      if constexpr (BF16) {
-        uint32_t w[4];
+    const int e0 = entry(P, c, sub);
+    if (e0 >= P.experts) continue;
+    if constexpr (BF16) {
+      uint32_t w[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const __nv_bfloat162 b = __floats2bfloat162_rn(x[c][2 * k], x[c][2 * k + 1]);
-          w[k] = *reinterpret_cast<const uint32_t*>(&b);
-        }
-        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(P.grad) + base + e0) = make_uint4(w[0], w[1], w[2], w[3]);
-      } else {
-        float4* f = reinterpret_cast<float4*>(static_cast<float*>(P.grad) + base + e0);
-        f[0] = make_float4(x[c][0], x[c][1], x[c][2], x[c][3]);
-        f[1] = make_float4(x[c][4], x[c][5], x[c][6], x[c][7]);
+      for (int k = 0; k < 4; ++k) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(x[c][2 * k], x[c][2 * k + 1]);
+        w[k] = *reinterpret_cast<const uint32_t*>(&b);
       }
+      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(P.grad) + base + e0) = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int e = entry<VEC>(P, c, k, sub);
-        if (e >= P.experts) continue;
-        if constexpr (BF16) static_cast<__nv_bfloat16*>(P.grad)[base + e] = __float2bfloat16_rn(x[c][k]);
-        else static_cast<float*>(P.grad)[base + e] = x[c][k];
-      }
+      float4* f = reinterpret_cast<float4*>(static_cast<float*>(P.grad) + base + e0);
+      f[0] = make_float4(x[c][0], x[c][1], x[c][2], x[c][3]);
+      f[1] = make_float4(x[c][4], x[c][5], x[c][6], x[c][7]);
     }
   }
 }
@@ -231,7 +205,7 @@ __device__ __forceinline__ T warp_sum(T v) {
 template <int NC>
 constexpr int kSets = NC <= 2 ? 2 : 1;
 
-template <bool BF16, int NC, bool VEC>
+template <bool BF16, int NC>
 __global__ void __launch_bounds__(kThreads, 4) balance_rows(const __grid_constant__ BalanceParams P) {
   extern __shared__ float smem[];
   float* sp = smem;                                               // kWarps x experts
@@ -275,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 4) balance_rows(const __grid_constan
       on[u] = at < r1 && (!P.mask || P.mask[first + at]);
     }
 #pragma unroll
-    for (int u = 0; u < kU; ++u) load_row<BF16, NC, VEC>(P, first + r + u * kWarps * rows_warp + mine, sub, on[u], x[u]);
+    for (int u = 0; u < kU; ++u) load_row<BF16, NC>(P, first + r + u * kWarps * rows_warp + mine, sub, on[u], x[u]);
     float inv[kU], lse[kU];
     softmax_rows<NC, kU>(P.lanes, on, x, inv, lse);
 #pragma unroll
@@ -307,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 4) balance_rows(const __grid_constan
     for (int c = 0; c < NC; ++c)
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const int e = entry<VEC>(P, c, k, sub);
+        const int e = entry(P, c, sub) + k;
         if (e < P.experts) sp[warp * P.experts + e] = acc[c][k];
       }
   }
@@ -429,7 +403,7 @@ __global__ void __launch_bounds__(kFinishThreads) balance_finish(const __grid_co
   }
 }
 
-template <bool BF16, int NC, bool VEC>
+template <bool BF16, int NC>
 __global__ void __launch_bounds__(kThreads, 4) balance_grad(const __grid_constant__ BalanceParams P) {
   constexpr int kU = kSets<NC>;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -444,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 4) balance_grad(const __grid_constan
   for (int c = 0; c < NC; ++c)
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const int e = entry<VEC>(P, c, k, sub);
+      const int e = entry(P, c, sub) + k;
       a[c][k] = e < P.experts ? gb * P.weights[g * P.experts + e] : 0.0f;
     }
   for (long long r = r0 + warp * rows_warp; r < r1; r += kU * kWarps * rows_warp) {
@@ -457,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 4) balance_grad(const __grid_constan
       on[u] = in[u] && (!P.mask || P.mask[first + at]);
     }
 #pragma unroll
-    for (int u = 0; u < kU; ++u) load_row<BF16, NC, VEC>(P, first + r + u * kWarps * rows_warp + mine, sub, on[u], x[u]);
+    for (int u = 0; u < kU; ++u) load_row<BF16, NC>(P, first + r + u * kWarps * rows_warp + mine, sub, on[u], x[u]);
     softmax_rows<NC, kU>(P.lanes, on, x, inv, lse);
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
@@ -486,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 4) balance_grad(const __grid_constan
           x[u][c][k] = on[u] ? v.x : 0.0f;
           x[u][c][k + 1] = on[u] ? v.y : 0.0f;
         }
-      store_row<BF16, NC, VEC>(P, first + r + u * kWarps * rows_warp + mine, sub, x[u]);
+      store_row<BF16, NC>(P, first + r + u * kWarps * rows_warp + mine, sub, x[u]);
     }
   }
 }
@@ -545,11 +519,12 @@ __device__ __forceinline__ void row_sums(const T* x, int experts, int q, int par
   }
 }
 
-template <typename T>
+// NE: experts of a thread, 256 apart.
+template <typename T, int NE>
 __global__ void __launch_bounds__(kThreads) balance_rows_tile(const __grid_constant__ BalanceParams P) {
   extern __shared__ __align__(16) unsigned char dynamic[];
   __shared__ float2 s_row[kThreads];  // largest entry, 1 / sum (0: left out)
-  __shared__ int s_count[kTileExperts];
+  __shared__ int s_count[NE * kThreads];
   __shared__ float s_acc[kThreads];
   __shared__ int2 s_numbers[kWarps];
   __shared__ float s_sq[kWarps];
@@ -561,7 +536,7 @@ __global__ void __launch_bounds__(kThreads) balance_rows_tile(const __grid_const
   const long long first = g * P.group_rows;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // balance_finish waits for this grid's end
   if (blockIdx.x == 0 && t == 0) *P.arrived = 0;
-  if (t < P.experts) s_count[t] = 0;
+  for (int e = t; e < P.experts; e += kThreads) s_count[e] = 0;
   __syncthreads();
   int assigned = 0, tokens = 0;
   const long long i1 = (first + r1) * P.top;
@@ -574,9 +549,9 @@ __global__ void __launch_bounds__(kThreads) balance_rows_tile(const __grid_const
   }
   // an expert's sum: `width` threads for the experts, the rows dealt over the others
   int width = 32;
-  while (width < P.experts) width *= 2;
+  while (width < P.experts && width < kThreads) width *= 2;
   const int e = t & (width - 1), deal = t / width, deals = kThreads / width;
-  float acc = 0.0f, sq = 0.0f;
+  float acc[NE] = {}, sq = 0.0f;
   for (long long r = r0; r < r1; r += P.tile_rows) {
     const int rows = static_cast<int>(min(static_cast<long long>(P.tile_rows), r1 - r));
     const T* x = load_tile<T>(P, first + r, rows, dynamic);
@@ -593,27 +568,34 @@ __global__ void __launch_bounds__(kThreads) balance_rows_tile(const __grid_const
       }
     }
     __syncthreads();
-    if (e < P.experts) {
+#pragma unroll
+    for (int c = 0; c < NE; ++c) {
+      if (e + c * kThreads >= P.experts) continue;
+      const T* const from = x + e + c * kThreads;
 #pragma unroll 4
       for (int k = deal; k < rows; k += deals) {
         const float2 row = s_row[k];
-        const float p = ex2((value(x[k * P.experts + e]) - row.x) * kLog2e) * row.y;
-        acc += row.y != 0.0f ? p : 0.0f;
+        const float p = ex2((value(from[k * P.experts]) - row.x) * kLog2e) * row.y;
+        acc[c] += row.y != 0.0f ? p : 0.0f;
       }
     }
     __syncthreads();
   }
-  s_acc[t] = acc;
+  s_acc[t] = acc[0];
   sq = warp_sum(sq);
   tokens = warp_sum(tokens);
   assigned = warp_sum(assigned);
   if (lane == 0) s_sq[warp] = sq, s_numbers[warp] = make_int2(tokens, assigned);
   __syncthreads();
   const long long out = static_cast<long long>(blockIdx.x) * P.experts;
-  if (t < P.experts) {
-    for (int k = 1; k < deals; ++k) acc += s_acc[k * width + t];
-    P.sums[out + t] = acc;
-    P.part_counts[out + t] = s_count[t];
+#pragma unroll
+  for (int c = 0; c < NE; ++c) {
+    const int at = t + c * kThreads;
+    if (at >= P.experts) continue;
+    if (c == 0)  // deals = 1 where there are more experts than threads
+      for (int k = 1; k < deals; ++k) acc[0] += s_acc[k * width + t];
+    P.sums[out + at] = acc[c];
+    P.part_counts[out + at] = s_count[at];
   }
   if (t == 0) {
     float s = 0.0f;
@@ -624,12 +606,12 @@ __global__ void __launch_bounds__(kThreads) balance_rows_tile(const __grid_const
   }
 }
 
-template <typename T>
+template <typename T, int NE>
 __global__ void __launch_bounds__(kThreads) balance_grad_tile(const __grid_constant__ BalanceParams P) {
   extern __shared__ __align__(16) unsigned char dynamic[];
   __shared__ float3 s_row[kThreads];  // largest entry, 1 / sum (0: left out), shift
-  __shared__ float s_a[kTileExperts];
-  constexpr int kPerLane = kTileExperts / 32;
+  __shared__ float s_a[NE * kThreads];
+  constexpr int kPerLane = kThreads / 32;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int q = kThreads / P.tile_rows, part = t & (q - 1), mine = t / q;
   const long long g = blockIdx.x / P.parts;
@@ -637,9 +619,9 @@ __global__ void __launch_bounds__(kThreads) balance_grad_tile(const __grid_const
   const long long r1 = min(P.group_rows, r0 + P.cta_rows);
   const long long first = g * P.group_rows;
   const float gb = *P.grad_balance * P.stats[2], gz = *P.grad_z * P.stats[3];
-  if (t < P.experts) s_a[t] = gb * P.weights[g * P.experts + t];
+  for (int e = t; e < P.experts; e += kThreads) s_a[e] = gb * P.weights[g * P.experts + e];
   __syncthreads();
-  float a[kPerLane];
+  float a[kPerLane];  // NE = 1
 #pragma unroll
   for (int k = 0; k < kPerLane; ++k) a[k] = lane + 32 * k < P.experts ? s_a[lane + 32 * k] : 0.0f;
   for (long long r = r0; r < r1; r += P.tile_rows) {
@@ -656,13 +638,19 @@ __global__ void __launch_bounds__(kThreads) balance_grad_tile(const __grid_const
       const float3 row = s_row[k];
       T* const o = static_cast<T*>(P.grad) + (first + r + k) * P.grad_stride + lane;
       const T* const from = x + k * P.experts + lane;
-#pragma unroll
-      for (int c = 0; c < kPerLane; ++c) {
-        if (lane + 32 * c >= P.experts) continue;
+      auto entry_ = [&](int c, float weight) {
         const float p = ex2((value(from[32 * c]) - row.x) * kLog2e) * row.y;
-        const float v = row.y != 0.0f ? p * (a[c] + row.z) : 0.0f;
+        const float v = row.y != 0.0f ? p * (weight + row.z) : 0.0f;
         if constexpr (sizeof(T) == 2) o[32 * c] = __float2bfloat16_rn(v);
         else o[32 * c] = v;
+      };
+      if constexpr (NE == 1) {
+#pragma unroll
+        for (int c = 0; c < kPerLane; ++c)
+          if (lane + 32 * c < P.experts) entry_(c, a[c]);
+      } else {
+#pragma unroll 4
+        for (int c = 0; lane + 32 * c < P.experts; ++c) entry_(c, s_a[lane + 32 * c]);
       }
     }
     __syncthreads();
@@ -671,13 +659,16 @@ __global__ void __launch_bounds__(kThreads) balance_grad_tile(const __grid_const
 
 using KernelPtr = void (*)(BalanceParams);
 
-#define KERNELS(F)                                                                                       \
-  F<false, 1, false>, F<false, 2, false>, F<false, 4, false>, F<true, 1, false>, F<true, 2, false>, F<true, 4, false>, \
-      F<false, 1, true>, F<false, 2, true>, F<false, 4, true>, F<true, 1, true>, F<true, 2, true>, F<true, 4, true>
-// Index: 0, 1, 2 for up to 256, 512, 1024 experts; + 3 for bfloat16; + 6 where rows are aligned for vectors.
-const KernelPtr kRows[12] = {KERNELS(balance_rows)};
-const KernelPtr kGrad[12] = {KERNELS(balance_grad)};
+#define KERNELS(F) F<false, 1>, F<false, 2>, F<false, 4>, F<true, 1>, F<true, 2>, F<true, 4>
+// Index: 0, 1, 2 for up to 256, 512, 1024 experts; + 3 for bfloat16.
+const KernelPtr kRows[6] = {KERNELS(balance_rows)};
+const KernelPtr kGrad[6] = {KERNELS(balance_grad)};
 #undef KERNELS
+// Index: more than kThreads experts; + 2 for bfloat16.
+const KernelPtr kRowsTile[4] = {balance_rows_tile<float, 1>, balance_rows_tile<float, 4>, balance_rows_tile<__nv_bfloat16, 1>,
+                                balance_rows_tile<__nv_bfloat16, 4>};
+const KernelPtr kGradTile[4] = {balance_grad_tile<float, 1>, balance_grad_tile<float, 4>, balance_grad_tile<__nv_bfloat16, 1>,
+                                balance_grad_tile<__nv_bfloat16, 4>};
 
 // The split of the rows: lanes per row, CTAs per group, rows per CTA; and of
 // balance_finish: experts of a CTA, CTAs per group.
@@ -714,11 +705,13 @@ Split split_of(int64_t tokens, int experts, int64_t groups) {
   return s;
 }
 
-// Rows of a tile: a power of two, at least 32 (256 float32 experts: 32 KB).
+// Rows of a tile: a power of two, at least 8 (1024 float32 experts: 32 KB).
 // Returns the tile's bytes, with room for its shift against 16 bytes.
 size_t use_tiles(BalanceParams& P, int size) {
+  // the kernels for more experts hold 3 KB more of their own; all stay below 48 KB
+  const long long most = kTileBytes - (P.experts > kThreads ? 3 * 1024 : 0);
   P.tile_rows = kThreads;
-  while (P.tile_rows > 32 && static_cast<long long>(P.tile_rows) * P.experts * size > kTileBytes) P.tile_rows /= 2;
+  while (P.tile_rows > 8 && static_cast<long long>(P.tile_rows) * P.experts * size > most) P.tile_rows /= 2;
   return static_cast<size_t>(P.tile_rows) * P.experts * size + 16;
 }
 
@@ -832,10 +825,10 @@ extern "C" muon_status_t balance_loss(const void* logits, int dtype, int64_t tok
   cudaStream_t str = static_cast<cudaStream_t>(stream);
   const bool bf16 = dtype == MUON_BF16;
   size_t smem = static_cast<size_t>(kWarps + 1) * experts * 4;
-  KernelPtr rows = kRows[s.kernel + (bf16 ? 3 : 0) + (vec ? 6 : 0)];
-  if (!vec && experts <= kTileExperts) {
+  KernelPtr rows = kRows[s.kernel + (bf16 ? 3 : 0)];
+  if (!vec) {
     smem = use_tiles(P, size);
-    rows = bf16 ? balance_rows_tile<__nv_bfloat16> : balance_rows_tile<float>;
+    rows = kRowsTile[(experts > kThreads ? 1 : 0) + (bf16 ? 2 : 0)];
   }
   rows<<<static_cast<unsigned>(s.parts * groups), kThreads, smem, str>>>(P);
   if (cudaGetLastError() != cudaSuccess) return MUON_ERR_CUDA;
@@ -903,10 +896,10 @@ extern "C" muon_status_t balance_loss_backward(const void* logits, int dtype, in
   P.grad_z = grad_z;
   const bool bf16 = dtype == MUON_BF16;
   size_t smem = 0;
-  KernelPtr rows = kGrad[s.kernel + (bf16 ? 3 : 0) + (vec ? 6 : 0)];
-  if (!vec && experts <= kTileExperts) {
+  KernelPtr rows = kGrad[s.kernel + (bf16 ? 3 : 0)];
+  if (!vec) {
     smem = use_tiles(P, size);
-    rows = bf16 ? balance_grad_tile<__nv_bfloat16> : balance_grad_tile<float>;
+    rows = kGradTile[(experts > kThreads ? 1 : 0) + (bf16 ? 2 : 0)];
   }
   rows<<<static_cast<unsigned>(s.parts * groups), kThreads, smem, static_cast<cudaStream_t>(stream)>>>(P);
   return cudaGetLastError() == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
