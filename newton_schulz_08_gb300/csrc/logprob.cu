@@ -402,6 +402,26 @@ struct RowVectors {
   }
 };
 
+// A vector of entries that begin anywhere (rows of logits and gradient that
+// fall differently: the gradient is stored in vectors, the logits are read in
+// words).  An odd place of bfloat16 reads the entry before and the one after.
+// Backward of 2398 x 114679 bfloat16: 208 us so, 167 where rows fall alike; of
+// 4096 x 32001 float32 160 (entry by entry 166).
+template <bool BF16>
+__device__ __forceinline__ uint4 unaligned(const void* x, long long i) {
+  if constexpr (BF16) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(static_cast<const __nv_bfloat16*>(x) + i);
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(a & ~static_cast<uintptr_t>(3));
+    uint4 q = make_uint4(w[0], w[1], w[2], w[3]);
+    if (a & 2) q = make_uint4(__byte_perm(q.x, q.y, 0x5432), __byte_perm(q.y, q.z, 0x5432), __byte_perm(q.z, q.w, 0x5432),
+                              __byte_perm(q.w, w[4], 0x5432));
+    return q;
+  } else {
+    const uint32_t* w = static_cast<const uint32_t*>(x) + i;
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
 // --------------------------------------------------- rows in registers (warps)
 
 // Collected places of one warp, and of its first entries in order.
@@ -1039,10 +1059,19 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 8 : 3) logprob_loss(
         }
         copy(np, next_on, group);
       }
-    } else {  // entry by entry, whichever thread copied it
-      const int from = p.first(0);
-#pragma unroll 4
-      for (int j = j0 + t; j < j1; j += THREADS)
+    } else {  // the gradient's whole vectors and its ends, whichever thread copied the logits
+      const int from = p.first(0), v0 = (j0 + O.shift + kN - 1) / kN, v1 = max(v0, (j1 + O.shift) / kN);
+      uint4* const whole = reinterpret_cast<uint4*>(const_cast<unsigned char*>(O.base));
+#pragma unroll 2
+      for (int v = v0 + t; v < v1; v += THREADS) {
+        float x[kN];
+        unpack<BF16>(unaligned<BF16>(segment, O.first(v) - from), x);
+        grad_entries(g, P.scale, target, O.first(v), x);
+        whole[v] = pack<BF16>(x);
+      }
+      const int head = min(j1, O.first(v0)) - j0, tail = O.first(v1);
+      const int j = t < head ? j0 + t : tail + t - head;
+      if (t < head || j < j1)
         put<BF16>(P.grad, out + j, grad_entry(g, P.scale, target, j, at<BF16>(segment, j - from)));
       __syncthreads();
 #pragma unroll 1
@@ -1271,16 +1300,31 @@ __global__ void __launch_bounds__(kGradThreads) logprob_grad(const __grid_consta
           if (j + k >= 0 && j + k < P.vocab) put<BF16>(P.grad, out + j + k, on ? grad_entry(g, P.scale, target, j + k, at<BF16>(P.x, base + j + k)) : 0.0f);
       }
     }
-  } else {  // entry by entry, eight loads before the first store
-    const int j0 = max(0, R.first(v0)), j1 = min(P.vocab, R.first(v1));
-    for (int j = j0 + t; j < j1; j += 8 * kGradThreads) {
-      float x[8];
+  } else {  // the gradient's vectors
+    uint4* const o = reinterpret_cast<uint4*>(const_cast<unsigned char*>(O.base));
+    const int end = min(O.count, v0 + kGradThreads * kGradVecs);
+    auto inside = [&](int v) { return O.first(v) > 0 && O.first(v) + kN < P.vocab; };
 #pragma unroll
-      for (int k = 0; k < 8; ++k) x[k] = on && j + k * kGradThreads < j1 ? at<BF16>(P.x, base + j + k * kGradThreads) : 0.0f;
+    for (int u = 0; u < kGradVecs; ++u) {
+      const int v = v0 + u * kGradThreads + t;
+      q[u] = make_uint4(0, 0, 0, 0);
+      if (on && v < end && inside(v)) q[u] = unaligned<BF16>(P.x, base + O.first(v));
+    }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int i = j + k * kGradThreads;
-        if (i < j1) put<BF16>(P.grad, out + i, on ? grad_entry(g, P.scale, target, i, x[k]) : 0.0f);
+    for (int u = 0; u < kGradVecs; ++u) {
+      const int v = v0 + u * kGradThreads + t;
+      if (v >= end) continue;
+      const int j = O.first(v);
+      if (inside(v)) {
+        float x[kN] = {};
+        if (on) {
+          unpack<BF16>(q[u], x);
+          grad_entries(g, P.scale, target, j, x);
+        }
+        o[v] = pack<BF16>(x);
+      } else {
+        for (int k = 0; k < kN; ++k)
+          if (j + k >= 0 && j + k < P.vocab) put<BF16>(P.grad, out + j + k, on ? grad_entry(g, P.scale, target, j + k, at<BF16>(P.x, base + j + k)) : 0.0f);
       }
     }
   }

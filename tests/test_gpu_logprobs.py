@@ -158,6 +158,30 @@ def test_alternatives_with_ties_and_orders(what, kind):
 
 
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,vocab", [(9, 4500), (300, 12_346), (5, 60_000), (170, 60_001), (9, 130_001)])
+def test_gradients_that_fall_differently_from_the_logits(rows, vocab, kind):
+    """Pitches and offsets of logits and gradient that differ, so that every distance to the vectors' boundaries occurs."""
+    rng = np.random.default_rng(vocab)
+    x, y = case(rng, rows, vocab, kind)
+    y[::7] = -1
+    x[y < 0] = 0.0
+    for pad, shift, out_pad, out_shift in ((1, 0, 0, 3), (3, 5, 2, 0)):
+        X, Y = place(x, kind, pad, shift), torch.from_numpy(y).cuda()
+        gl, ge = (rng.standard_normal(rows).astype(np.float32) for _ in range(2))
+        GL, GE = torch.from_numpy(gl).cuda(), torch.from_numpy(ge).cuda()
+        outs = [place(np.full((rows, vocab), 7.0), kind, out_pad, out_shift) for _ in range(2)]
+        r = muon.token_logprobs_loss(X, Y, GL, GE, out=outs[0])
+        muon.token_logprobs_backward(X, Y, r.lse, GL, r.entropy, GE, out=outs[1])
+        live = y >= 0
+        for G in outs:
+            check_grad(G[torch.from_numpy(live).cuda()], x[live], y[live], gl[live], ge[live], 1.0, kind)
+            assert not host(G)[~live].any()
+            if out_pad:  # the gap between rows is left as it was
+                whole = torch.as_strided(G, (rows - 1, out_pad), (vocab + out_pad, 1), G.storage_offset() + vocab)
+                assert (whole == torch.tensor(9e9, device="cuda").to(KIND[kind])).all()
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
 @pytest.mark.parametrize("rows,vocab", [(3, 50_257), (400, 12_345), (700, 70_001)])
 def test_alternatives_among_many_equal_entries(rows, vocab, kind):
     """Rows whose best entries are fewer than the alternatives asked for, all others equal (a mask, or a floor):
