@@ -1493,8 +1493,16 @@ muon_status_t run(const void* logits, int dtype, int64_t rows, int64_t vocab, in
   const bool bf16 = dtype == MUON_BF16;
   cudaError_t err = cudaSuccess;
   if (vecs <= kWarpVecs) {
+    // A lane takes one vector before the row takes more lanes; eight where there
+    // are rows for every warp, as a warp's instructions then serve several rows
+    // (65536 x 300 bfloat16: score 32 us, 49 with one; loss 51 and 65; backward
+    // 36 and 50).  Four for the loss of longer rows, whose registers leave room
+    // for fewer warps (65536 x 1000 bfloat16: 73 us, 84 with eight), and one for
+    // alternatives, which a whole warp finds faster (65536 x 300 with five: 82 us,
+    // 190 with eight).
+    const int each = P.top > 0 || rows < 32LL * sms ? 1 : score && backward && vecs > 64 ? 4 : 8;
     P.lanes = 1;
-    while (P.lanes < 32 && P.lanes < vecs) P.lanes *= 2;
+    while (P.lanes < 32 && P.lanes * each < vecs) P.lanes *= 2;
     int k = 0;
     while (P.lanes << k < vecs) ++k;
     const long long per = static_cast<long long>(kWarpThreads / 32) * (32 / P.lanes);

@@ -136,6 +136,32 @@ def test_alternatives_and_temperature(top, scale):
     run_all(x, y, "bf16", scale, top, entropy=top % 2 == 0)
 
 
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("vocab", [1, 2, 31, 64, 65, 130, 257, 301, 513, 600, 1025])
+def test_many_short_rows(vocab, kind):
+    """Rows enough for every warp: a few lanes then take a row."""
+    rng = np.random.default_rng(vocab)
+    x, y = case(rng, 5003, vocab, kind)
+    y[::11] = -1
+    x[y < 0] = 0.0
+    x[5::50] = -np.inf
+    live = (y >= 0) & np.isfinite(x).any(axis=1)
+    gl, ge = (rng.standard_normal(len(y)).astype(np.float32) for _ in range(2))
+    GL, GE, Y, keep = torch.from_numpy(gl).cuda(), torch.from_numpy(ge).cuda(), torch.from_numpy(y).cuda(), torch.from_numpy(live).cuda()
+    for pad, shift in ((0, 0), (1, 2)):
+        X = place(x, kind, pad, shift)
+        r = muon.token_logprobs(X, Y)
+        B = muon.token_logprobs_backward(X, Y, r.lse, GL, r.entropy, GE)
+        q = muon.token_logprobs_loss(X, Y, GL, GE, out=X)
+        empty = (y >= 0) & ~live
+        for o in (r, q):
+            check_score(muon.TokenLogprobs(o.logprobs[keep], o.lse[keep], o.entropy[keep], None, None), x[live], y[live], 1.0, 0)
+            assert (host(o.lse)[empty] == -np.inf).all() and not host(o.entropy)[empty].any() and not host(o.lse)[y < 0].any()
+        for G in (B, q.grad):
+            check_grad(G[keep], x[live], y[live], gl[live], ge[live], 1.0, kind)
+            assert not host(G)[~live].any()
+
+
 @pytest.mark.parametrize("rows", [1, 2, 19, 151, 153, 700, 1300])
 def test_rows_from_one_to_many(rows):
     """From one row that many blocks share to many rows a block each."""
