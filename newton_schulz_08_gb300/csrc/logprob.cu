@@ -424,6 +424,16 @@ __device__ __forceinline__ uint4 unaligned(const void* x, long long i) {
 
 // --------------------------------------------------- rows in registers (warps)
 
+// The entries of a vector that lie inside the row, one by one.
+template <bool BF16>
+__device__ __noinline__ void store_entries(void* grad, long long out, int j, int vocab, uint4 y) {
+  float x[kPer<BF16>];
+  unpack<BF16>(y, x);
+#pragma unroll
+  for (int k = 0; k < kPer<BF16>; ++k)
+    if (j + k >= 0 && j + k < vocab) put<BF16>(grad, out + j + k, x[k]);
+}
+
 // Collected places of one warp, and of its first entries in order.
 struct WarpTop {
   unsigned long long candidate[kWarpCandidates];
@@ -587,29 +597,36 @@ __global__ void __launch_bounds__(kWarpThreads, NV == 16 ? 2 : NV == 8 ? 3 : 4) 
     if (on) g = grad_of(P, r, gl, ge, target);
     const NearGrad near = near_of(g, P.scale);
     const bool ordinary = fabsf(near.K) < -kMasked;
-    const RowVectors<BF16> O(P.grad, row * P.grad_stride, P.vocab);
+    const long long out = row * P.grad_stride;
+    const RowVectors<BF16> O(P.grad, out, P.vocab);
     uint4* const o = reinterpret_cast<uint4*>(const_cast<unsigned char*>(O.base));
+    const bool same = O.shift == R.shift;
+    // the logits are widened anew: kept from the sums they would take the
+    // registers of twice as many warps
 #pragma unroll
-    for (int u = 0; u < NV; ++u) {
-      const int v = sub + P.lanes * u, j = R.first(v);
-      if (v >= R.count) continue;
-      uint4 y = make_uint4(0, 0, 0, 0);
-      if (on && ordinary) {
-        y = grad_near<BF16>(g, near, P.scale, target, j, q[u]);
-      } else if (on) {
-        float x[kN];
-        unpack<BF16>(q[u], x);
-        grad_entries(g, P.scale, target, j, x);
-        y = pack<BF16>(x);
+    for (int u = 0; u < NV; ++u) asm volatile("" : "+r"(q[u].x), "+r"(q[u].y), "+r"(q[u].z), "+r"(q[u].w));
+    if (!on || ordinary) {
+#pragma unroll
+      for (int u = 0; u < NV; ++u) {
+        const int v = sub + P.lanes * u;
+        if (v >= R.count) continue;
+        uint4 y = make_uint4(0, 0, 0, 0);
+        if (on) y = grad_near<BF16>(g, near, P.scale, target, R.first(v), q[u]);
+        if (same && static_cast<unsigned>(v - lo) < static_cast<unsigned>(wholes)) o[v] = y;
+        else store_entries<BF16>(P.grad, out, R.first(v), P.vocab, y);
       }
-      if (O.shift == R.shift && static_cast<unsigned>(v - lo) < static_cast<unsigned>(wholes)) {
-        o[v] = y;
-      } else {
-        float x[kN];
-        unpack<BF16>(y, x);
+    } else {  // a row of the type's lowest value
+#pragma unroll 1
+      for (int u = 0; u < NV; ++u) {
+        uint4 qu = q[0];
 #pragma unroll
-        for (int k = 0; k < kN; ++k)
-          if (j + k >= 0 && j + k < P.vocab) put<BF16>(P.grad, row * P.grad_stride + j + k, x[k]);
+        for (int i = 1; i < NV; ++i) qu = i == u ? q[i] : qu;
+        const int v = sub + P.lanes * u;
+        if (v >= R.count) continue;
+        float x[kN];
+        unpack<BF16>(qu, x);
+        grad_entries(g, P.scale, target, R.first(v), x);
+        store_entries<BF16>(P.grad, out, R.first(v), P.vocab, pack<BF16>(x));
       }
     }
   }
