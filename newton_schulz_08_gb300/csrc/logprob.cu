@@ -400,6 +400,17 @@ struct RowVectors {
     }
     return pack<BF16>(x);
   }
+  // The same from what the vector holds.
+  __device__ __noinline__ uint4 mask(int v, uint4 q) const {
+    float x[kPer<BF16>];
+    unpack<BF16>(q, x);
+#pragma unroll
+    for (int k = 0; k < kPer<BF16>; ++k) {
+      const int j = first(v) + k;
+      if (j < 0 || j >= vocab) x[k] = -INFINITY;
+    }
+    return pack<BF16>(x);
+  }
 };
 
 // A vector of entries that begin anywhere (rows of logits and gradient that
@@ -503,16 +514,30 @@ __global__ void __launch_bounds__(kWarpThreads, NV == 16 ? 2 : NV == 8 ? 3 : 4) 
   const RowVectors<BF16> R(P.x, in ? row * P.stride : 0, P.vocab);
   const int lo = R.shift > 0 ? 1 : 0;  // the vectors inside the row: lo .. lo+wholes-1
   const int wholes = max(0, static_cast<int>(static_cast<unsigned>(R.shift + P.vocab) / kN) - lo);
+  // A vector at an end of the row is read whole where what it holds of other
+  // rows or of the gap between rows lies inside the matrix (what another warp
+  // may be writing there is masked): all loads of the row are in flight at once
+  const unsigned char* const x0 = static_cast<const unsigned char*>(P.x);
+  const unsigned char* const x1 = x0 + ((P.rows - 1) * P.stride + P.vocab) * (BF16 ? 2 : 4);
+  const int from = R.base < x0 ? 1 : 0;
+  const unsigned safe = in ? max(0, R.count - from - (R.base + R.count * 16LL > x1 ? 1 : 0)) : 0;
   uint4 q[NV];
 #pragma unroll
   for (int u = 0; u < NV; ++u) {
     const int v = sub + P.lanes * u;
     q[u] = masked_vector<BF16>();
-    if (in && static_cast<unsigned>(v - lo) < static_cast<unsigned>(wholes)) q[u] = *reinterpret_cast<const uint4*>(R.base + v * 16LL);
+    if (static_cast<unsigned>(v - from) < safe) q[u] = *reinterpret_cast<const uint4*>(R.base + v * 16LL);
     else if (in && v < R.count) q[u] = R.end(v);
   }
   float x_target = 0.0f;
   if (MODE != kBackward && on && target < P.vocab) x_target = at<BF16>(P.x, row * P.stride + target);
+  if (wholes < R.count) {
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      const int v = sub + P.lanes * u;
+      if (static_cast<unsigned>(v - lo) >= static_cast<unsigned>(wholes) && v < R.count) q[u] = R.mask(v, q[u]);
+    }
+  }
   RowStats r{};
   if (MODE == kBackward && on) r = stats_from_lse(P, row);
   if (MODE != kBackward || __any_sync(0xFFFFFFFFu, on && log_s_is_lost(r))) {
@@ -1512,12 +1537,10 @@ muon_status_t run(const void* logits, int dtype, int64_t rows, int64_t vocab, in
   if (vecs <= kWarpVecs) {
     // A lane takes one vector before the row takes more lanes; eight where there
     // are rows for every warp, as a warp's instructions then serve several rows
-    // (65536 x 300 bfloat16: score 32 us, 49 with one; loss 51 and 65; backward
-    // 36 and 50).  Four for the loss of longer rows, whose registers leave room
-    // for fewer warps (65536 x 1000 bfloat16: 73 us, 84 with eight), and one for
-    // alternatives, which a whole warp finds faster (65536 x 300 with five: 82 us,
-    // 190 with eight).
-    const int each = P.top > 0 || rows < 32LL * sms ? 1 : score && backward && vecs > 64 ? 4 : 8;
+    // (65536 x 300 bfloat16: score 32 us, 49 with one; loss 45 and 65; backward
+    // 36 and 50).  One for alternatives, which a whole warp finds faster
+    // (65536 x 300 with five: 82 us, 190 with eight).
+    const int each = P.top > 0 || rows < 32LL * sms ? 1 : 8;
     P.lanes = 1;
     while (P.lanes < 32 && P.lanes * each < vecs) P.lanes *= 2;
     int k = 0;
