@@ -44,7 +44,8 @@ constexpr int kMaxCluster = 8;
 constexpr int kHeldRanks = 2;             // CTAs that a row's loss is spread over for its length
 constexpr int kWarpVecs = 512;            // longest row of logprob_warp in 16-byte vectors
 constexpr int kWarpThreads = 256;
-constexpr int kWarpCandidates = 192;
+constexpr int kWarpCandidates = 256;
+constexpr int kWarpFew = 96;              // more than that may be ties
 constexpr int kSegmentBytes = 104 * 1024; // of a row in one CTA's shared memory
 constexpr int kGradThreads = 256;
 constexpr int kGradVecs = 4;              // 16-byte vectors per thread of logprob_grad
@@ -435,6 +436,9 @@ __device__ __forceinline__ uint4 unaligned(const void* x, long long i) {
 
 // --------------------------------------------------- rows in registers (warps)
 
+// Has what is computed from q computed again rather than kept in registers.
+__device__ __forceinline__ void anew(uint4& q) { asm volatile("" : "+r"(q.x), "+r"(q.y), "+r"(q.z), "+r"(q.w)); }
+
 // The entries of a vector that lie inside the row, one by one.
 template <bool BF16>
 __device__ __noinline__ void store_entries(void* grad, long long out, int j, int vocab, uint4 y) {
@@ -452,42 +456,98 @@ struct WarpTop {
 };
 
 // The `top` first places of a row that a whole warp holds, into S.top, found
-// as described at TopScratch with the lanes as groups; false where more
-// entries reach the bound than there is room for.
+// as described at TopScratch with the halves of a lane's entries as groups;
+// false where more entries reach the bound than there is room for, ties apart.
 template <bool BF16, int NV>
-__device__ __forceinline__ bool warp_top(const LogprobParams& P, const RowVectors<BF16>& R, const uint4 (&q)[NV], int lane,
-                                         WarpTop& S) {
+__device__ __forceinline__ bool warp_top(const LogprobParams& P, const RowVectors<BF16>& R, uint4 (&q)[NV], int lane, WarpTop& S) {
   constexpr int kN = kPer<BF16>;
-  float own = -INFINITY;
+  const unsigned before = (1u << lane) - 1;
+  float half[2] = {-INFINITY, -INFINITY};
+  if constexpr (NV == 1) {
+    constexpr uint32_t kNone = BF16 ? 0xFF80FF80u : 0xFF800000u;
+    half[0] = vec_max<BF16>(make_uint4(q[0].x, q[0].y, kNone, kNone));
+    half[1] = vec_max<BF16>(make_uint4(q[0].z, q[0].w, kNone, kNone));
+  } else {
 #pragma unroll
-  for (int u = 0; u < NV; ++u) own = fmaxf(own, vec_max<BF16>(q[u]));
-  uint32_t left = ordered(own), bound = 0;
-  for (int k = 0; k < P.top; ++k) {
-    bound = __reduce_max_sync(0xFFFFFFFFu, left);
-    if (lane == __ffs(__ballot_sync(0xFFFFFFFFu, left == bound)) - 1) left = 0;
+    for (int u = 0; u < NV; ++u) half[u & 1] = fmaxf(half[u & 1], vec_max<BF16>(q[u]));
   }
-  const float least = place_value(static_cast<unsigned long long>(bound) << 32);
+  uint32_t bound = 0, left[2] = {ordered(half[0]), ordered(half[1])};
+  for (int k = 0; k < P.top; ++k) {  // one maximum after the other (32 of them take less than ranking all 64 by counting)
+    const uint32_t own = max(left[0], left[1]);
+    bound = __reduce_max_sync(0xFFFFFFFFu, own);
+    if (lane == __ffs(__ballot_sync(0xFFFFFFFFu, own == bound)) - 1) (left[0] == bound ? left[0] : left[1]) = 0;
+  }
   int n = 0;  // the same in every lane
+  auto add = [&](bool on, float x, int j) {
+    const unsigned m = __ballot_sync(0xFFFFFFFFu, on);
+    const int i = n + __popc(m & before);
+    if (on && i < kWarpCandidates) S.candidate[i] = place(x, j);
+    n += __popc(m);
+  };
+  int pass = 0;
+#pragma unroll 1
+  for (;; ++pass) {
+    const float least = place_value(static_cast<unsigned long long>(bound) << 32);
+    n = 0;
 #pragma unroll
-  for (int u = 0; u < NV; ++u) {
-    // one vector after the other, an entry a lane
-    for (unsigned hits = __ballot_sync(0xFFFFFFFFu, vec_max<BF16>(q[u]) >= least); hits != 0; hits &= hits - 1) {
-      const int from = __ffs(hits) - 1;
-      const uint32_t w[4] = {__shfl_sync(0xFFFFFFFFu, q[u].x, from), __shfl_sync(0xFFFFFFFFu, q[u].y, from),
-                             __shfl_sync(0xFFFFFFFFu, q[u].z, from), __shfl_sync(0xFFFFFFFFu, q[u].w, from)};
-      const int word = BF16 ? lane >> 1 & 3 : lane & 3;
-      const uint32_t both = word < 2 ? (word == 0 ? w[0] : w[1]) : (word == 2 ? w[2] : w[3]);
-      const float x = __uint_as_float(!BF16 ? both : lane & 1 ? both & 0xFFFF0000u : both << 16);
-      const int j = R.first(from + 32 * u) + lane;
-      const bool on = lane < kN && j >= 0 && j < P.vocab && ordered(x) >= bound;
-      const unsigned m = __ballot_sync(0xFFFFFFFFu, on);
-      const int i = n + __popc(m & ((1u << lane) - 1));
-      if (on && i < kWarpCandidates) S.candidate[i] = place(x, j);
-      n += __popc(m);
+    for (int u = 0; u < NV; ++u) {
+      anew(q[u]);  // what depends on it is not kept for the other pass
+      unsigned hits = __ballot_sync(0xFFFFFFFFu, vec_max<BF16>(q[u]) >= least);
+      if (__popc(hits) > 16) {  // an entry of every lane at a time
+        float x[kN];
+        unpack<BF16>(q[u], x);
+#pragma unroll
+        for (int k = 0; k < kN; ++k) {
+          const int j = R.first(lane + 32 * u) + k;
+          add(j >= 0 && j < P.vocab && ordered(x[k]) >= bound, x[k], j);
+        }
+        continue;
+      }
+      for (; hits != 0; hits &= hits - 1) {  // one vector after the other, an entry a lane
+        const int from = __ffs(hits) - 1;
+        const uint32_t w[4] = {__shfl_sync(0xFFFFFFFFu, q[u].x, from), __shfl_sync(0xFFFFFFFFu, q[u].y, from),
+                               __shfl_sync(0xFFFFFFFFu, q[u].z, from), __shfl_sync(0xFFFFFFFFu, q[u].w, from)};
+        const int word = BF16 ? lane >> 1 & 3 : lane & 3;
+        const uint32_t both = word < 2 ? (word == 0 ? w[0] : w[1]) : (word == 2 ? w[2] : w[3]);
+        const float x = __uint_as_float(!BF16 ? both : lane & 1 ? both & 0xFFFF0000u : both << 16);
+        const int j = R.first(from + 32 * u) + lane;
+        add(lane < kN && j >= 0 && j < P.vocab && ordered(x) >= bound, x, j);
+      }
+    }
+    if (n <= kWarpFew || pass == 1) break;
+    ++bound;  // what is above it, then the first of the equal entries
+  }
+  if (n > kWarpCandidates) return false;
+  if (pass == 1) {
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      if (n >= P.top) continue;  // the same in every lane
+      float x[kN];
+      unpack<BF16>(q[u], x);
+      unsigned ties = 0;
+#pragma unroll
+      for (int k = 0; k < kN; ++k) {
+        const int j = R.first(lane + 32 * u) + k;
+        ties |= static_cast<unsigned>(j >= 0 && j < P.vocab && ordered(x[k]) == bound - 1) << k;
+      }
+      int upto = __popc(ties);
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const int o = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+        if (lane >= d) upto += o;
+      }
+      int i = n + upto - __popc(ties);
+#pragma unroll
+      for (int k = 0; k < kN; ++k) {
+        if (!(ties >> k & 1)) continue;
+        if (i < P.top) S.candidate[i] = place(x[k], R.first(lane + 32 * u) + k);
+        ++i;
+      }
+      n += __shfl_sync(0xFFFFFFFFu, upto, 31);
+      if (n > P.top) n = P.top;
     }
   }
   __syncwarp();
-  if (n > kWarpCandidates) return false;
   for (int i = lane; i < n; i += 32) {
     const unsigned long long mine = S.candidate[i];
     int rank = 0;
@@ -629,7 +689,7 @@ __global__ void __launch_bounds__(kWarpThreads, NV == 16 ? 2 : NV == 8 ? 3 : 4) 
     // the logits are widened anew: kept from the sums they would take the
     // registers of twice as many warps
 #pragma unroll
-    for (int u = 0; u < NV; ++u) asm volatile("" : "+r"(q[u].x), "+r"(q[u].y), "+r"(q[u].z), "+r"(q[u].w));
+    for (int u = 0; u < NV; ++u) anew(q[u]);
     if (!on || ordinary) {
 #pragma unroll
       for (int u = 0; u < NV; ++u) {
@@ -1537,8 +1597,8 @@ muon_status_t run(const void* logits, int dtype, int64_t rows, int64_t vocab, in
   if (vecs <= kWarpVecs) {
     // A lane takes one vector before the row takes more lanes; eight where there
     // are rows for every warp, as a warp's instructions then serve several rows
-    // (65536 x 300 bfloat16: score 32 us, 49 with one; loss 45 and 65; backward
-    // 36 and 50).  One for alternatives, which a whole warp finds faster
+    // (65536 x 300 bfloat16: score 25 us, 42 with one; loss 37 and 61; backward
+    // 29 and 44).  One for alternatives, which a whole warp finds faster
     // (65536 x 300 with five: 82 us, 190 with eight).
     const int each = P.top > 0 || rows < 32LL * sms ? 1 : 8;
     P.lanes = 1;

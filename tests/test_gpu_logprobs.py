@@ -208,7 +208,7 @@ def test_gradients_that_fall_differently_from_the_logits(rows, vocab, kind):
 
 
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
-@pytest.mark.parametrize("rows,vocab", [(3, 50_257), (400, 12_345), (700, 70_001)])
+@pytest.mark.parametrize("rows,vocab", [(3, 50_257), (400, 12_345), (700, 70_001), (800, 2047), (800, 1030), (800, 520), (800, 256), (800, 137)])
 def test_alternatives_among_many_equal_entries(rows, vocab, kind):
     """Rows whose best entries are fewer than the alternatives asked for, all others equal (a mask, or a floor):
     the first of these follow by index; and rows of three values, with and without entries below the equal ones."""
@@ -216,7 +216,7 @@ def test_alternatives_among_many_equal_entries(rows, vocab, kind):
     fill = [-np.inf, float(torch.finfo(KIND[kind]).min), -9984.0, 0.0]
     x = np.stack([np.full(vocab, fill[i % 4]) for i in range(rows)])
     for i in range(rows):
-        few = rng.integers(0, vocab, (i // 4) % 24)
+        few = rng.integers(0, vocab, (i // 4) % 24)  # and of these some twice
         x[i, few] = rng.integers(1, 5, len(few))
         low = rng.integers(0, vocab, vocab // 2)
         if i % 8 >= 4:
