@@ -34,8 +34,8 @@
 // Bound: 32-bit moments by HBM (float32 parameters, bfloat16 gradients: 26
 // bytes an element, 154.5 M of them 565 us, 7.1 TB/s); 8-bit ones by HBM and
 // instruction issue alike (14 bytes, about 53 instructions: 373 us, 5.8 TB/s);
-// bfloat16 parameters off a 16-byte boundary by issue (10 bytes, 62
-// instructions: 226 us for 82.3 M, 3.6 TB/s).
+// bfloat16 parameters by issue (10 bytes; 62 instructions, off a 16-byte
+// boundary 78: 226 us for 82.3 M, 3.7 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
