@@ -33,9 +33,9 @@
 // the same types; the table is in the kernel's parameters.
 // Bound: 32-bit moments by HBM (float32 parameters, bfloat16 gradients: 26
 // bytes an element, 154.5 M of them 565 us, 7.1 TB/s); 8-bit ones by HBM and
-// instruction issue alike (14 bytes, about 53 instructions: 373 us, 5.8 TB/s);
+// instruction issue alike (14 bytes, about 54 instructions: 373 us, 5.8 TB/s);
 // bfloat16 parameters by issue (10 bytes; 62 instructions, off a 16-byte
-// boundary 78: 226 us for 82.3 M, 3.7 TB/s).
+// boundary 76: 213 us for 82.3 M, 3.9 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -72,7 +72,7 @@ struct AdamwTensor {
   uint32_t key;   // of the random bits
   int first;      // first CTA of this tensor in the launch
   int vec;        // every array is aligned for the vector path
-  int pad;
+  int even;       // and its bfloat16 ones begin on 16-byte boundaries
 };
 
 struct AdamwParams {
@@ -137,34 +137,35 @@ __device__ __forceinline__ Eight widen(uint4 q) {
   return x;
 }
 
-// A block of a bfloat16 array that begins `off` bytes past a 16-byte boundary:
-// its 31 whole 16-byte vectors pass as such, the eight entries at its two ends
-// one by one (nothing outside the block is touched), and shared memory moves
-// the lanes' eight entries to where the vectors put them.
-struct alignas(16) Shift {
-  unsigned char bytes[528];
-};
-
+// A block of a bfloat16 array that begins `off` bytes past a 16-byte boundary
+// passes as the 16-byte vectors it touches; shuffles move entries between
+// neighbouring lanes (through shared memory the step of 82.3 M bfloat16
+// parameters took 226 us in place of 213).  The vectors at its two ends reach into
+// the neighbouring blocks: they are read whole (what is not the block's own is
+// not used, and another warp may be writing it) and written entry by entry.
 __device__ __forceinline__ unsigned offset_of(const void* at) { return static_cast<unsigned>(reinterpret_cast<uintptr_t>(at)) & 15u; }
 
-// Which of the block's entries lane 0 .. 7 passes.
-__device__ __forceinline__ int end_entry(int lane, unsigned off) { return lane < static_cast<int>(16 - off) / 2 ? lane : 248 + lane; }
-
-// 16 bytes from an even place on.
-__device__ __forceinline__ uint4 gather16(const Shift& s, unsigned byte) {
-  const uint32_t* w = reinterpret_cast<const uint32_t*>(s.bytes) + byte / 4;
-  uint4 q = make_uint4(w[0], w[1], w[2], w[3]);
-  if (byte & 2u) {
-    const uint32_t e = w[4];
-    q = make_uint4(__byte_perm(q.x, q.y, 0x5432), __byte_perm(q.y, q.z, 0x5432), __byte_perm(q.z, q.w, 0x5432), __byte_perm(q.w, e, 0x5432));
+// Bytes `by` (even, 2 to 14) and on of the eight words a, b.
+__device__ __forceinline__ uint4 cut(uint4 a, uint4 b, unsigned by) {
+  uint32_t w[7] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z};
+  if (by & 8u) w[0] = a.z, w[1] = a.w, w[2] = b.x, w[3] = b.y, w[4] = b.z, w[5] = b.w;
+  if (by & 4u) {
+#pragma unroll
+    for (int k = 0; k < 5; ++k) w[k] = w[k + 1];
   }
-  return q;
+  const uint32_t pick = by & 2u ? 0x5432u : 0x3210u;
+  return make_uint4(__byte_perm(w[0], w[1], pick), __byte_perm(w[1], w[2], pick), __byte_perm(w[2], w[3], pick),
+                    __byte_perm(w[3], w[4], pick));
+}
+
+__device__ __forceinline__ uint4 shuffle(uint4 q, int from) {
+  return make_uint4(__shfl_sync(0xFFFFFFFFu, q.x, from), __shfl_sync(0xFFFFFFFFu, q.y, from), __shfl_sync(0xFFFFFFFFu, q.z, from),
+                    __shfl_sync(0xFFFFFFFFu, q.w, from));
 }
 
 // What a lane reads of the warp's 256 entries of an array from `i` on.
 struct Raw {
-  uint4 a, b;  // float32: eight entries; bfloat16: a
-  uint16_t end;
+  uint4 a, b;  // float32: eight entries; bfloat16: a, and lane 0 the vector past lane 31's
 };
 
 template <bool BF16>
@@ -173,9 +174,9 @@ __device__ __forceinline__ Raw fetch(const void* base, long long i, int lane) {
   if constexpr (BF16) {
     const __nv_bfloat16* at = static_cast<const __nv_bfloat16*>(base) + i;
     const unsigned off = offset_of(at);
-    const unsigned char* v = reinterpret_cast<const unsigned char*>(at) - off + 16 * lane;
-    if (off == 0 || lane > 0) r.a = *reinterpret_cast<const uint4*>(v);
-    if (off != 0 && lane < 8) r.end = reinterpret_cast<const uint16_t*>(at)[end_entry(lane, off)];
+    const uint4* v = reinterpret_cast<const uint4*>(reinterpret_cast<const unsigned char*>(at) - off) + lane;
+    r.a = *v;
+    if (off != 0 && lane == 0) r.b = v[32];
   } else {
     const uint4* f = reinterpret_cast<const uint4*>(static_cast<const float*>(base) + i + 8 * lane);
     r.a = f[0];
@@ -186,36 +187,31 @@ __device__ __forceinline__ Raw fetch(const void* base, long long i, int lane) {
 
 // A lane's eight entries from what the warp has read.
 template <bool BF16>
-__device__ __forceinline__ Eight align(const Raw& r, const void* base, int lane, Shift& s) {
+__device__ __forceinline__ Eight align(const Raw& r, const void* base, int lane) {
   if constexpr (BF16) {
     const unsigned off = offset_of(base);  // a block is a multiple of 16 bytes
     if (off == 0) return widen(r.a);
-    if (lane > 0) *reinterpret_cast<uint4*>(s.bytes + 16 * lane) = r.a;
-    if (lane < 8) *reinterpret_cast<uint16_t*>(s.bytes + off + 2 * end_entry(lane, off)) = r.end;
-    __syncwarp();
-    const uint4 q = gather16(s, off + 16 * lane);
-    __syncwarp();
-    return widen(q);
+    return widen(cut(r.a, shuffle(lane == 0 ? r.b : r.a, (lane + 1) & 31), off));
   } else {
     auto f = [](uint32_t x, uint32_t y) { return make_float2(__uint_as_float(x), __uint_as_float(y)); };
     return {{f(r.a.x, r.a.y), f(r.a.z, r.a.w), f(r.b.x, r.b.y), f(r.b.z, r.b.w)}};
   }
 }
 
-__device__ __forceinline__ void store_bf16(__nv_bfloat16* at, int lane, uint4 q, Shift& s) {
+__device__ __forceinline__ void store_bf16(__nv_bfloat16* at, int lane, uint4 q) {
   const unsigned off = offset_of(at);
-  unsigned char* v = reinterpret_cast<unsigned char*>(at) - off + 16 * lane;
+  uint4* v = reinterpret_cast<uint4*>(reinterpret_cast<unsigned char*>(at) - off) + lane;
   if (off == 0) {
-    *reinterpret_cast<uint4*>(v) = q;
+    *v = q;
     return;
   }
-  *reinterpret_cast<uint4*>(s.bytes + 16 * lane) = q;
-  __syncwarp();
-  if (lane > 0) *reinterpret_cast<uint4*>(v) = gather16(s, 16 * lane - off);
-  if (lane < 8) {
-    const int e = end_entry(lane, off);
-    reinterpret_cast<uint16_t*>(at)[e] = *reinterpret_cast<const uint16_t*>(s.bytes + 2 * e);
-  }
+  const uint4 own = cut(shuffle(q, (lane - 1) & 31), q, 16 - off);
+  if (lane > 0) *v = own;
+  // the first entries, before the first boundary, and the last ones
+  const bool head = lane < static_cast<int>(16 - off) / 2;
+  const uint4 end = shuffle(q, head ? 0 : 31);
+  const uint32_t word = lane & 4 ? (lane & 2 ? end.w : end.z) : (lane & 2 ? end.y : end.x);
+  if (lane < 8) reinterpret_cast<uint16_t*>(at)[head ? lane : 248 + lane] = static_cast<uint16_t>(lane & 1 ? word >> 16 : word);
 }
 
 __device__ __forceinline__ void store_f32(float* at, int lane, const Eight& x) {
@@ -384,7 +380,7 @@ __device__ __forceinline__ Fetched fetch_block(const AdamwTensor& T, long long b
 // layout, all of them (VEC) in the vector layout.
 template <bool PB, bool GB, bool B8, bool VEC>
 __device__ __forceinline__ void step_block(const AdamwParams& P, const AdamwTensor& T, long long blk, int lane, int left, float gs,
-                                           Eight& p, const Eight& g, Eight& m, Eight& v, Shift& s) {
+                                           Eight& p, const Eight& g, Eight& m, Eight& v) {
   const long long i0 = blk * kQBlock;
   update(P, T.step, T.decay, gs, g, p, m, v);
   uint32_t h[8];
@@ -407,7 +403,7 @@ __device__ __forceinline__ void step_block(const AdamwParams& P, const AdamwTens
     }
   }
   if constexpr (VEC) {
-    if constexpr (PB) store_bf16(static_cast<__nv_bfloat16*>(T.p) + i0, lane, narrow(p, h), s);
+    if constexpr (PB) store_bf16(static_cast<__nv_bfloat16*>(T.p) + i0, lane, narrow(p, h));
     else store_f32(static_cast<float*>(T.p) + i0, lane, p);
     if constexpr (B8) {
       *reinterpret_cast<uint2*>(static_cast<uint8_t*>(T.m) + i0 + 8 * lane) = cm;
@@ -452,8 +448,6 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constan
     if (P.t[mid].first <= static_cast<int>(blockIdx.x)) lo = mid; else hi = mid - 1;
   }
   const AdamwTensor& T = P.t[lo];
-  __shared__ Shift shift[PB || GB ? kWarps : 1];
-  Shift& s = shift[PB || GB ? threadIdx.x >> 5 : 0];
   const int lane = threadIdx.x & 31;
   const float gs = P.grad_scale ? *P.grad_scale : 1.0f;
   const long long blk = static_cast<long long>(blockIdx.x - T.first) * kWarps + (threadIdx.x >> 5), i0 = blk * kQBlock;
@@ -461,19 +455,20 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constan
   if (!MUON_CHECK(i0 >= 0)) return;
   const int left = static_cast<int>(min(static_cast<long long>(kQBlock), T.numel - i0));
   Eight m, v;
-  if (T.vec && left == kQBlock) {
+  const bool inner = blk > 0 && i0 + kQBlock + 8 <= T.numel;  // with room for the vectors at both ends
+  if (T.vec && left == kQBlock && (T.even || inner)) {
     const Fetched f = fetch_block<PB, GB, B8>(T, blk, lane);
-    Eight p = align<PB>(f.p, T.p, lane, s);
-    const Eight g = align<GB>(f.g, T.g, lane, s);
+    Eight p = align<PB>(f.p, T.p, lane);
+    const Eight g = align<GB>(f.g, T.g, lane);
     if constexpr (B8) {
       m = decode<true>(make_uint2(f.m.a.x, f.m.a.y), f.sm);
       v = decode<false>(make_uint2(f.v.a.x, f.v.a.y), f.sv);
     } else {
-      m = align<false>(f.m, T.m, lane, s);
-      v = align<false>(f.v, T.v, lane, s);
+      m = align<false>(f.m, T.m, lane);
+      v = align<false>(f.v, T.v, lane);
     }
-    step_block<PB, GB, B8, true>(P, T, blk, lane, kQBlock, gs, p, g, m, v, s);
-  } else {  // a tensor's last block, and arrays off the vectors' boundaries
+    step_block<PB, GB, B8, true>(P, T, blk, lane, kQBlock, gs, p, g, m, v);
+  } else {  // a tensor's last block (and first), and arrays off the vectors' boundaries
     Eight p = load_strided<PB>(T.p, i0, lane, left);
     const Eight g = load_strided<GB>(T.g, i0, lane, left);
     if constexpr (B8) {
@@ -483,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constan
       m = load_strided<false>(T.m, i0, lane, left);
       v = load_strided<false>(T.v, i0, lane, left);
     }
-    step_block<PB, GB, B8, false>(P, T, blk, lane, left, gs, p, g, m, v, s);
+    step_block<PB, GB, B8, false>(P, T, blk, lane, left, gs, p, g, m, v);
   }
 }
 
@@ -580,6 +575,7 @@ muon_status_t adamw_plan::build() {
     a.numel = d.numel;
     a.first = static_cast<int>(l.ctas);
     a.vec = vector_aligned(d);
+    a.even = aligned_to(d.param, 16) && aligned_to(d.grad, 16);
     l.ctas += (d.numel + kQBlock * kWarps - 1) / (kQBlock * kWarps);
     if (l.ctas > 0x7FFFFFFFLL) return MUON_ERR_TOO_LARGE;
     l.t.push_back(a);
