@@ -1499,7 +1499,7 @@ cudaError_t launch_score(LogprobParams P, bool bf16, long long bytes, int sms, c
   while (1 << P.log_ranks < ranks) ++P.log_ranks;
   // 128 threads a row: eight rows of an SM overlap one's loads with another's
   // reductions (4096 x 50257 bfloat16 with 5 alternatives 100 us, 32768 x 6000
-  // 103; 256 threads: 110 and 157; 64: 109 for the latter).  A row that is
+  // without 100; 256 threads: 110 and 157; 64: 109 for the latter).  A row that is
   // spread wants its CTAs' loads in flight at once.
   const bool wide = ranks > 1;
   return launch_clusters(kScoreKernels[(wide ? 1 : 0) | (P.top > 0 ? 2 : 0) | (bf16 ? 4 : 0)], P, P.rows, wide ? 256 : 128, 0, stream);

@@ -259,3 +259,27 @@ def test_unsupported_arguments_raise_on_device():
         step_all([t], 1, grad_scale=torch.ones(1))
     with pytest.raises(ValueError):
         step_all([t], 1, grad_scale=torch.ones(2, device="cuda"))
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+@pytest.mark.parametrize("numel", [255, 256, 257, 512, 519, 520, 521, 768, 100_003])
+def test_bits_do_not_depend_on_where_arrays_begin(numel, bits):
+    """bfloat16 parameters and gradients at every distance to a 16-byte boundary: the same bits as on one, the neighbours untouched."""
+    gen = torch.Generator("cuda").manual_seed(numel)
+    p, g = (torch.randn(numel, generator=gen, device="cuda").mul_(s).bfloat16() for s in (0.02, 1e-3))
+
+    def run(po, go):
+        whole = torch.full((numel + 32,), 3.0, dtype=torch.bfloat16, device="cuda")
+        grads = torch.full((numel + 32,), float("nan"), dtype=torch.bfloat16, device="cuda")
+        P, G = whole[8 + po:8 + po + numel], grads[8 + go:8 + go + numel]
+        P.copy_(p), G.copy_(g)
+        state = muon.adamw_state(P, bits)
+        for step in (1, 2):
+            muon.adamw_step([P], [G], [state], step, lr=1e-3, seed=7)
+        assert (whole[:8 + po] == 3.0).all() and (whole[8 + po + numel:] == 3.0).all()
+        return [t.reshape(-1).contiguous().view(torch.uint8) for t in (P, *state)]
+
+    want = run(0, 0)
+    for po, go in [(k, 0) for k in range(1, 8)] + [(0, 3), (1, 6), (5, 5), (7, 2)]:
+        for a, b in zip(run(po, go), want):
+            assert torch.equal(a, b), (po, go)
