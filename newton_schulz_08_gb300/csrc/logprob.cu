@@ -940,7 +940,8 @@ __device__ __noinline__ Sums sums_again(const void* x, long long base, int first
 }
 
 // What the CTAs of a cluster tell one another.  Sums of one row are read while
-// the next row's are written.
+// the next row's are written; the row after that may only write once the next
+// row's exchange has kept every CTA.
 struct Exchange {
   Sums sums[2][kMaxCluster];
   unsigned long long top[kMaxCluster][kMaxTop];
@@ -1027,7 +1028,10 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 8 : 3) logprob_loss(
   for (int g = 0; g < 4; ++g) copy(p, target >= 0, g);
   if (ranks > 1) cg::cluster_group::barrier_wait();
 
-  for (int turn = 0; row < P.rows; turn ^= 1) {
+  // `turn` flips with every row that is exchanged, not with rows that are left
+  // out: between two writes of a slot of X.sums there is then the exchange of
+  // the other slot, which a CTA passes only after it has read the first
+  for (int turn = 0; row < P.rows;) {
     const long long next = row + clusters;
     const int64_t next_target = next < P.rows ? P.targets[next] : -1;
     const bool next_on = next_target >= 0;
@@ -1179,6 +1183,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 8 : 3) logprob_loss(
 #pragma unroll 1
       for (int group = 0; group < 4; ++group) copy(np, next_on, group);
     }
+    turn ^= 1;
     row = next;
     target = next_target;
     p = np;
