@@ -188,6 +188,39 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def _tensors(out):
+    if isinstance(out, torch.Tensor):
+        yield out
+    elif isinstance(out, (tuple, list)):
+        for t in out:
+            yield from _tensors(t)
+
+
+def _on(stream, tensor, fn, *args):
+    """fn(*args) under `stream` of the tensor's device: what the call allocates
+    belongs to that stream, so that neither a workspace nor an output is memory
+    that the caller's own stream still uses or is given next.  What it returns
+    may be used on the caller's stream, which must wait for `stream` as for
+    any work there, and freed at any time."""
+    if not tensor.is_cuda:
+        return fn(*args)  # refuses it
+    if getattr(stream, "device", tensor.device) != tensor.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {tensor.device}")
+    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if handle == torch._C._cuda_getCurrentRawStream(tensor.get_device()):
+        return fn(*args)
+    own = torch.cuda.current_stream(tensor.device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = (torch.cuda.ExternalStream(handle, tensor.device) if handle
+                  else torch.cuda.default_stream(tensor.device))
+    with torch.cuda.stream(stream):
+        out = fn(*args)
+    for t in _tensors(out):
+        if t.is_cuda:
+            t.record_stream(own)
+    return out
+
+
 def _check(status, where, ok=(MUON_OK,)):
     if status not in ok:
         raise MuonError(status, where)
@@ -251,6 +284,8 @@ def new_workspace(nbytes, device=None):
 def muon_step(params, grads, bufs, lr=0.02, momentum=0.95, nesterov=True, ns_steps=5,
               workspace=None, stream=None):
     """One Muon step over a bank (lists of 2-D CUDA tensors), in place."""
+    if stream is not None and workspace is None and len(params):
+        return _on(stream, params[0], muon_step, params, grads, bufs, lr, momentum, nesterov, ns_steps)
     arr, n = _descs(params, grads, bufs)
     if n == 0:
         return workspace
@@ -311,6 +346,8 @@ def ns5_workspace_size(batch, rows, cols):
 
 def ns5(G, ns_steps=5, out=None, workspace=None, stream=None):
     """zeropower_via_newtonschulz5 on a (batch x) rows x cols CUDA tensor -> bf16."""
+    if stream is not None:
+        return _on(stream, G, ns5, G, ns_steps, out, workspace)
     squeeze = G.dim() == 2
     G3 = G.unsqueeze(0) if squeeze else G
     if G3.dim() != 3 or not G3.is_contiguous():
@@ -340,6 +377,8 @@ def ns5_bank_workspace_size(shapes):
 
 def ns5_bank(Gs, ns_steps=5, outs=None, workspace=None, stream=None):
     """Newton-Schulz on a list of differently shaped 2-D CUDA tensors -> bf16 list."""
+    if stream is not None and len(Gs):
+        return _on(stream, Gs[0], ns5_bank, Gs, ns_steps, outs, workspace)
     n = len(Gs)
     if outs is None:
         outs = [torch.empty(g.shape, dtype=torch.bfloat16, device=g.device) for g in Gs]
@@ -403,6 +442,8 @@ def ns5_noalloc(G, ns_steps=5, out=None, stream=None):
     """ns5 without a workspace: the library's own static device scratch is
     used (for callers that may not allocate device memory; see include/muon.h).
     Only `out` is allocated here when the caller does not pass one."""
+    if stream is not None:
+        return _on(stream, G, ns5_noalloc, G, ns_steps, out)
     squeeze = G.dim() == 2
     G3 = G.unsqueeze(0) if squeeze else G
     if G3.dim() != 3 or not G3.is_contiguous():
@@ -474,6 +515,8 @@ def fp8_mm(x, w, x_s, w_s, out=None, x_f8=None, w_f8=None, workspace=None, strea
     returns (out, x_f8, w_f8), out = bf16(x_s w_s (x_f8 . w_f8^T)) with
     x_f8 = E4M3(bf16(x / x_s)), w_f8 = E4M3(bf16(w / w_s)) as float8_e4m3fn
     tensors.  See fp8_mm in include/muon.h."""
+    if stream is not None:
+        return _on(stream, x, fp8_mm, x, w, x_s, w_s, out, x_f8, w_f8, workspace)
     for t in (x, w):
         if t.dim() != 2 or t.dtype != torch.bfloat16 or not t.is_contiguous() or not t.is_cuda:
             raise ValueError("x and w must be contiguous 2-D bfloat16 CUDA tensors")
@@ -519,6 +562,8 @@ def fp8_mm_backward(g, x_f8, w_f8, x_s, w_s, grad_s, grad_x=None, grad_w=None, g
     grad_x = bf16(grad_s w_s (g_f8 . w_f8)), grad_w = bf16(grad_s x_s
     (g_f8^T . x_f8)), g_f8 = E5M2(bf16(g / grad_s)) as a float8_e5m2 tensor.
     See fp8_mm_backward in include/muon.h."""
+    if stream is not None:
+        return _on(stream, g, fp8_mm_backward, g, x_f8, w_f8, x_s, w_s, grad_s, grad_x, grad_w, g_f8, workspace)
     if g.dim() != 2 or g.dtype != torch.bfloat16 or not g.is_contiguous():
         raise ValueError("g must be a contiguous 2-D bfloat16 CUDA tensor")
     M, N = g.shape
@@ -809,6 +854,8 @@ def token_logprobs(logits, targets, top=0, scale=1.0, stream=None):
     is left out) under softmax(scale * logits), with log-sum-exp, entropy and
     the `top` (<= 32) most likely entries: a TokenLogprobs.  logits: rows x
     vocab, bfloat16 or float32, any row pitch.  See include/muon.h."""
+    if stream is not None:
+        return _on(stream, logits, token_logprobs, logits, targets, top, scale)
     rows, vocab, pitch = _matrix(logits, "logits")
     index = _index_of("token_logprobs", logits, targets)
     y = _per_row(targets, rows, torch.int64, "targets")
@@ -823,6 +870,9 @@ def token_logprobs_backward(logits, targets, lse, grad_logprobs, entropy=None, g
     """Gradient with respect to the logits from those with respect to
     logprobs and, with `entropy` as token_logprobs gave it, entropy.  `out`
     may be the logits themselves.  See include/muon.h."""
+    if stream is not None:
+        return _on(stream, logits, token_logprobs_backward, logits, targets, lse, grad_logprobs, entropy, grad_entropy,
+                   scale, out)
     rows, vocab, pitch = _matrix(logits, "logits")
     if grad_entropy is not None and entropy is None:
         raise ValueError("grad_entropy needs entropy")
@@ -842,6 +892,8 @@ def token_logprobs_loss(logits, targets, grad_logprobs, grad_entropy=None, top=0
     (TokenLogprobs.grad), for a loss whose gradients with respect to logprobs
     and entropy are known beforehand; `out` may be the logits themselves.
     See include/muon.h."""
+    if stream is not None:
+        return _on(stream, logits, token_logprobs_loss, logits, targets, grad_logprobs, grad_entropy, top, scale, out)
     rows, vocab, pitch = _matrix(logits, "logits")
     out = _grad_out(out, logits)
     index = _index_of("token_logprobs_loss", logits, targets, grad_logprobs, grad_entropy, out)
@@ -884,6 +936,8 @@ def balance_loss(logits, ids, mask=None, groups=1, workspace=None, stream=None):
     tokens x experts (bfloat16 or float32, any row pitch), ids tokens x top
     int64 (the experts each token goes to), mask one bool per token (False:
     left out), `groups` sequences of equal length.  See include/muon.h."""
+    if stream is not None:
+        return _on(stream, logits, balance_loss, logits, ids, mask, groups, workspace)
     tokens, experts, pitch = _matrix(logits, "logits")
     if ids.dim() != 2 or ids.shape[0] != tokens or ids.dtype != torch.int64 or not ids.is_contiguous():
         raise ValueError("ids must be a contiguous tokens x top int64 tensor")
@@ -908,6 +962,8 @@ def balance_loss_backward(logits, result, grad_balance, grad_z, mask=None, out=N
     """Gradient of grad_balance * balance + grad_z * z (one-element float32
     CUDA tensors) with respect to the logits; `result` is balance_loss's for
     the same logits and mask.  `out` may be the logits themselves."""
+    if stream is not None:
+        return _on(stream, logits, balance_loss_backward, logits, result, grad_balance, grad_z, mask, out)
     tokens, experts, pitch = _matrix(logits, "logits")
     out = _grad_out(out, logits)
     groups, columns = result.counts.shape
