@@ -51,7 +51,11 @@ constexpr int kMaxExperts = 1024;
 constexpr int kTileBytes = 42 * 1024;  // of a tile: four CTAs per SM
 constexpr int kTargetCtas = 608;  // four per SM
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kFar = 1e30f;     // beyond it x log2(e) may leave float32's range
+// Up to here one fused operation x log2(e) - m log2(e) does for an exponent: the
+// product of m is rounded, which multiplies every power of the row by at most
+// 1 +- 2^-14.  Probabilities do not see a common factor; lse is off by less than its
+// own spacing.  Beyond it the factor would leave float32's range in the end.
+constexpr float kFar = 1024.0f;
 
 struct BalanceParams {
   const void* x;
@@ -164,7 +168,7 @@ __device__ __forceinline__ void softmax_rows(int lanes, const bool (&on)[U], flo
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     float shift = on[u] ? -m[u] * kLog2e : 0.0f;
-    if (on[u] && fabsf(m[u]) > kFar) {  // a mask of the type's lowest value over the whole row
+    if (on[u] && fabsf(m[u]) > kFar) {  // a row far from zero, or masked as a whole: the difference first
       shift = 0.0f;
 #pragma unroll
       for (int c = 0; c < NC; ++c)
@@ -190,7 +194,10 @@ __device__ __forceinline__ void softmax_rows(int lanes, const bool (&on)[U], flo
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     inv[u] = on[u] ? __fdividef(1.0f, s[u]) : 0.0f;
-    lse[u] = m[u] + __logf(s[u]);  // 1 <= s <= 1024
+    // s lies between 1 and 1024, but for the rounding of the shift.  The fast
+    // logarithm is off by 2^-21 near 1, else by 3 units in the last place, which
+    // is of the size of what its terms' powers (2 units) leave in s
+    lse[u] = m[u] + __logf(s[u]);
   }
 }
 
