@@ -27,6 +27,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <cstring>
 #include <new>
 #include <vector>
 
@@ -58,6 +59,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kFloor = -1000.0f;        // least exponent
 constexpr float kMasked = -1e30f;         // below: log S is lost beside the largest logit
+constexpr float kNear = 65536.0f;         // largest exponent of a reference in the short form for bfloat16
+constexpr float kNearScale = 1e-30f;      // and least scale: its floor is a bfloat16 number
 
 enum Mode { kScore = 0, kLoss = 1, kBackward = 2 };
 
@@ -79,6 +82,7 @@ struct LogprobParams {
   int log_ranks;    // logprob_score, logprob_loss: CTAs per row, as a power of two
   int segment;      // logprob_loss: vectors that a CTA has room for
   int chunks;       // logprob_grad: CTAs per row
+  uint32_t floor2;  // two bfloat16 numbers whose exponent is -2 kNear, for the short form
 };
 
 template <bool BF16>
@@ -220,19 +224,34 @@ __device__ __forceinline__ void accumulate(float2& s, float2& w, const float (&x
   }
 }
 
-// Adds a vector.  bfloat16: entries are held above -1e30 in pairs before they
-// are widened, and the exponent is one fused operation of K = -ref c2 (44
-// instructions a vector against 52); a reference for which that does not do
-// gives sums that are no number of order 1, and they are taken again.
+// The short form for bfloat16, where the exponent of the reference, ref c2, is
+// below kNear: entries are held above `floor2` in pairs before they are widened
+// (with ref c2 taken off its exponent is below -kNear, a power of 0, and a
+// product with it stays finite), and the exponent is one fused operation of
+// K = -ref c2 (44 instructions a vector against 52).  K is rounded, by up to 2^-9;
+// that goes into every exponent alike and is taken out of the sums (settle) and
+// of the gradient's factors (near_of).
 template <bool BF16>
-__device__ __forceinline__ void accumulate_near(float2& s, float2& w, uint4 q, float ref, float c2) {
+__device__ __forceinline__ bool near_fits(float ref, float c2) {
+  return !BF16 || (fabsf(ref * c2) < kNear && c2 >= kNearScale);
+}
+
+// 2^d for |d| <= 2^-8.
+__device__ __forceinline__ float ex2_small(float d) {
+  const float x = d * kLn2;
+  return fmaf(x, fmaf(x, 0.5f, 1.0f), 1.0f);
+}
+
+// Adds a vector.
+template <bool BF16>
+__device__ __forceinline__ void accumulate_near(float2& s, float2& w, uint4 q, float ref, float c2, uint32_t floor2) {
   if constexpr (BF16) {
-    const __nv_bfloat162 floor2 = __floats2bfloat162_rn(kMasked, kMasked);
     uint32_t v[4] = {q.x, q.y, q.z, q.w};
-    const float2 scale = make_float2(c2, c2), K = make_float2(-ref * c2, -ref * c2);
+    const float k = __fmul_rn(-ref, c2);
+    const float2 scale = make_float2(c2, c2), K = make_float2(k, k);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const __nv_bfloat162 b = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&v[k]), floor2);
+      const __nv_bfloat162 b = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&v[k]), *reinterpret_cast<const __nv_bfloat162*>(&floor2));
       v[k] = *reinterpret_cast<const uint32_t*>(&b);
       const float2 t = __ffma2_rn(make_float2(__uint_as_float(v[k] << 16), __uint_as_float(v[k] & 0xFFFF0000u)), scale, K);
       const float2 e = make_float2(ex2(t.x), ex2(t.y));
@@ -243,6 +262,17 @@ __device__ __forceinline__ void accumulate_near(float2& s, float2& w, uint4 q, f
     float x[4];
     unpack<false>(q, x);
     accumulate(s, w, x, ref, c2);
+  }
+}
+
+// Sums of accumulate_near against a.m become what they stand for: the exponents
+// were less by d = -(ref c2 + K), which one fused operation gives exactly.
+template <bool BF16>
+__device__ __forceinline__ void settle(Sums& a, float c2) {
+  if constexpr (BF16) {
+    const float ref = reference(a.m), d = -fmaf(ref, c2, __fmul_rn(-ref, c2)), f = ex2_small(d);
+    a.w = fmaf(d, a.s, a.w) * f;
+    a.s *= f;
   }
 }
 
@@ -274,7 +304,8 @@ __device__ __forceinline__ RowStats stats_of(const Sums& a, float scale) {
 }
 
 __device__ __forceinline__ float logprob_of(const RowStats& r, float x, float scale) {
-  return r.empty ? -INFINITY : (x - r.m) * scale - r.log_s;
+  const float v = r.empty ? -INFINITY : (x - r.m) * scale - r.log_s;
+  return v > 0.0f ? 0.0f : v;  // rounding alone takes the logarithm of a share above 0
 }
 
 // The gradient of a row: with d = log p_j = (x_j - m) scale - log_s,
@@ -332,27 +363,35 @@ __device__ __forceinline__ void grad_entries(const RowGrad& g, float scale, int6
   }
 }
 
-// The same for a vector of a row whose largest logit is of ordinary size.
-// bfloat16: held above -1e30 in pairs, t = log2 p_j in one fused operation.
+// The same for a vector.  bfloat16 in the short form, t = log2 p_j in one fused operation.
 struct NearGrad {
   float c2, K, a2, b;  // t = x c2 + K, grad = 2^t (a2 t + b)
+  bool fits;
 };
 
+template <bool BF16>
 __device__ __forceinline__ NearGrad near_of(const RowGrad& g, float scale) {
-  const float c2 = scale * kLog2e;
-  return {c2, -fmaf(g.m, c2, g.log_s * kLog2e), g.a * kLn2, g.b};
+  NearGrad h;
+  const float l = g.log_s * kLog2e;
+  h.c2 = scale * kLog2e;
+  h.K = -fmaf(g.m, h.c2, l);
+  h.fits = !BF16 || (fabsf(h.K) < kNear && h.c2 >= kNearScale);
+  // log2 p_j is t + d, as K is rounded; the difference from m c2 is exact but for a rounding of the size of l
+  const float d = -(fmaf(g.m, h.c2, h.K) + l), f = ex2_small(d), a2 = g.a * kLn2;
+  h.a2 = a2 * f;
+  h.b = fmaf(a2, d, g.b) * f;
+  return h;
 }
 
 template <bool BF16>
-__device__ __forceinline__ uint4 grad_near(const RowGrad& g, const NearGrad& h, float scale, int64_t target, int j, uint4 q) {
+__device__ __forceinline__ uint4 grad_near(const LogprobParams& P, const RowGrad& g, const NearGrad& h, int64_t target, int j, uint4 q) {
   float x[kPer<BF16>];
   if constexpr (BF16) {
-    const __nv_bfloat162 floor2 = __floats2bfloat162_rn(kMasked, kMasked);
     uint32_t v[4] = {q.x, q.y, q.z, q.w};
     const float2 c2 = make_float2(h.c2, h.c2), K = make_float2(h.K, h.K), a2 = make_float2(h.a2, h.a2), b = make_float2(h.b, h.b);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const __nv_bfloat162 f = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&v[k]), floor2);
+      const __nv_bfloat162 f = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&v[k]), *reinterpret_cast<const __nv_bfloat162*>(&P.floor2));
       v[k] = *reinterpret_cast<const uint32_t*>(&f);
       const float2 t = __ffma2_rn(make_float2(__uint_as_float(v[k] << 16), __uint_as_float(v[k] & 0xFFFF0000u)), c2, K);
       const float2 e = __fmul2_rn(make_float2(ex2(t.x), ex2(t.y)), __ffma2_rn(a2, t, b));
@@ -367,7 +406,7 @@ __device__ __forceinline__ uint4 grad_near(const RowGrad& g, const NearGrad& h, 
     }
   } else {
     unpack<false>(q, x);
-    grad_entries(g, scale, target, j, x);
+    grad_entries(g, P.scale, target, j, x);
   }
   return pack<BF16>(x);
 }
@@ -606,7 +645,7 @@ __global__ void __launch_bounds__(kWarpThreads, NV == 16 ? 2 : NV == 8 ? 3 : 4) 
     for (int u = 0; u < NV; ++u) a.m = fmaxf(a.m, vec_max<BF16>(q[u]));
     for (int d = P.lanes / 2; d > 0; d /= 2) a.m = fmaxf(a.m, __shfl_xor_sync(0xFFFFFFFFu, a.m, d));
     const float c2 = P.scale * kLog2e;
-    auto add_up = [&](auto add) {
+    auto add_up = [&](Sums& a, auto add) {
       float2 s{}, w{};
 #pragma unroll
       for (int u = 0; u < NV; ++u) add(s, w, q[u]);
@@ -617,14 +656,17 @@ __global__ void __launch_bounds__(kWarpThreads, NV == 16 ? 2 : NV == 8 ? 3 : 4) 
         a.w += __shfl_xor_sync(0xFFFFFFFFu, a.w, d);
       }
     };
-    add_up([&](float2& s, float2& w, uint4 v) { accumulate_near<BF16>(s, w, v, reference(a.m), c2); });
-    // against the largest entry S is 1 and more, unless the short form's range does not do
-    if (__any_sync(0xFFFFFFFFu, !(a.s >= 0.5f && a.s < 0x1p60f) && on)) {
-      add_up([&](float2& s, float2& w, uint4 v) {
+    const bool near = near_fits<BF16>(reference(a.m), c2);
+    add_up(a, [&](float2& s, float2& w, uint4 v) { accumulate_near<BF16>(s, w, v, reference(a.m), c2, P.floor2); });
+    settle<BF16>(a, c2);
+    if (BF16 && __any_sync(0xFFFFFFFFu, !near && on)) {
+      Sums far = a;
+      add_up(far, [&](float2& s, float2& w, uint4 v) {
         float x[kN];
         unpack<BF16>(v, x);
         accumulate(s, w, x, reference(a.m), c2);
       });
+      if (!near) a = far;
     }
     if (MODE != kBackward || log_s_is_lost(r)) r = stats_of(a, P.scale);
   }
@@ -680,8 +722,7 @@ __global__ void __launch_bounds__(kWarpThreads, NV == 16 ? 2 : NV == 8 ? 3 : 4) 
     if (!in) return;
     RowGrad g{};
     if (on) g = grad_of(P, r, gl, ge, target);
-    const NearGrad near = near_of(g, P.scale);
-    const bool ordinary = fabsf(near.K) < -kMasked;
+    const NearGrad near = near_of<BF16>(g, P.scale);
     const long long out = row * P.grad_stride;
     const RowVectors<BF16> O(P.grad, out, P.vocab);
     uint4* const o = reinterpret_cast<uint4*>(const_cast<unsigned char*>(O.base));
@@ -690,17 +731,17 @@ __global__ void __launch_bounds__(kWarpThreads, NV == 16 ? 2 : NV == 8 ? 3 : 4) 
     // registers of twice as many warps
 #pragma unroll
     for (int u = 0; u < NV; ++u) anew(q[u]);
-    if (!on || ordinary) {
+    if (!on || near.fits) {
 #pragma unroll
       for (int u = 0; u < NV; ++u) {
         const int v = sub + P.lanes * u;
         if (v >= R.count) continue;
         uint4 y = make_uint4(0, 0, 0, 0);
-        if (on) y = grad_near<BF16>(g, near, P.scale, target, R.first(v), q[u]);
+        if (on) y = grad_near<BF16>(P, g, near, target, R.first(v), q[u]);
         if (same && static_cast<unsigned>(v - lo) < static_cast<unsigned>(wholes)) o[v] = y;
         else store_entries<BF16>(P.grad, out, R.first(v), P.vocab, y);
       }
-    } else {  // a row of the type's lowest value
+    } else {  // a row far from zero
 #pragma unroll 1
       for (int u = 0; u < NV; ++u) {
         uint4 qu = q[0];
@@ -1088,7 +1129,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 8 : 3) logprob_loss(
       for (int i = group * p.per + t; i < end; i += THREADS) {
         const uint4 v = q[i];
         if (TOP) chunk.add(v);
-        accumulate_near<BF16>(s, w, v, a.m, c2);
+        accumulate_near<BF16>(s, w, v, a.m, c2, P.floor2);
       }
       if constexpr (TOP) {
         S.chunk_max[group][t] = chunk.value();
@@ -1099,7 +1140,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 8 : 3) logprob_loss(
     const float2 sums = cta_sum2<THREADS>(make_float2(s.x + s.y, w.x + w.y), pair_scratch[turn]);
     a.s = sums.x;
     a.w = sums.y;
-    if (!(a.s >= 0.5f && a.s < 0x1p60f)) {
+    settle<BF16>(a, c2);
+    if (!(near_fits<BF16>(a.m, c2) && a.s >= 0.5f && a.s < 0x1p60f)) {
       __syncthreads();  // the scratch arrays have been read
       a = sums_again<BF16, THREADS>(P.x, base, j0, j1, c2, scratch[turn], pair_scratch[turn]);
     }
@@ -1145,15 +1187,15 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 8 : 3) logprob_loss(
     }
 
     const RowGrad g = grad_of(P, r, P.gl[row], P.ge ? P.ge[row] : 0.0f, target);
-    const NearGrad near = near_of(g, P.scale);
-    if (same && fabsf(near.K) < -kMasked) {
+    const NearGrad near = near_of<BF16>(g, P.scale);
+    if (same && near.fits) {
 #pragma unroll 1
       for (int group = 0; group < 4; ++group) {
         const int end = min(p.n, (group + 1) * p.per);
 #pragma unroll 2
         for (int i = group * p.per + t; i < end; i += THREADS) {
           const int j = p.first(i);
-          const uint4 v = grad_near<BF16>(g, near, P.scale, target, j, q[i]);
+          const uint4 v = grad_near<BF16>(P, g, near, target, j, q[i]);
           if (p.whole(i)) {
             o[i] = v;
           } else {
@@ -1241,7 +1283,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprob_score(const _
   for (int d = 16; d > 0; d /= 2) sums.m = fmaxf(sums.m, __shfl_xor_sync(0xFFFFFFFFu, sums.m, d));
   float2 s{}, w{};
   bool found = sums.m != -INFINITY;
-  if (warp < 2) accumulate_near<BF16>(s, w, end, reference(sums.m), c2);
+  if (warp < 2) accumulate_near<BF16>(s, w, end, reference(sums.m), c2, P.floor2);
   // a chunk: batches of a thread that share a largest entry, a power of two of them
   const int batches = (n + kBatch - 1) / kBatch;
   int log_chunk = 0;
@@ -1263,7 +1305,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprob_score(const _
     for (int u = 0; u < kU; ++u) {
       if (i + u * THREADS < n) {
         if (TOP) largest.add(a[u]);
-        accumulate_near<BF16>(s, w, a[u], reference(sums.m), c2);
+        accumulate_near<BF16>(s, w, a[u], reference(sums.m), c2, P.floor2);
       }
       a[u] = b[u];
     }
@@ -1279,8 +1321,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprob_score(const _
     sums.s += __shfl_xor_sync(0xFFFFFFFFu, sums.s, d);
     sums.w += __shfl_xor_sync(0xFFFFFFFFu, sums.w, d);
   }
+  settle<BF16>(sums, c2);
+  if (!near_fits<BF16>(reference(sums.m), c2)) sums.s = NAN;
   // A warp that saw masked entries alone has m = -inf and no sum; any other sum
-  // out of range means that its reference was too far off.
+  // out of range means that its reference was too far off, or too large.
   if (lane == 0) warp_sums[warp] = sums;
   const int chunks = (batches + (1 << log_chunk) - 1) >> log_chunk;
   float own = vec_max<BF16>(end);
@@ -1596,6 +1640,10 @@ muon_status_t run(const void* logits, int dtype, int64_t rows, int64_t vocab, in
   P.vocab = static_cast<int>(vocab);
   P.top = score ? top : 0;
   P.scale = scale;
+  const float floor = -2.0f * kNear / (scale * kLog2e);  // rounded to bfloat16 towards 0
+  uint32_t bits = 0;
+  std::memcpy(&bits, &floor, 4);
+  P.floor2 = (bits >> 16) | (bits & 0xFFFF0000u);
   const cudaStream_t str = static_cast<cudaStream_t>(stream);
   const bool bf16 = dtype == MUON_BF16;
   cudaError_t err = cudaSuccess;
