@@ -58,7 +58,7 @@ constexpr int kLossStatic = 12 * 1024;    // shared memory of a logprob_loss CTA
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kFloor = -1000.0f;        // least exponent
-constexpr float kMasked = -1e30f;         // below: log S is lost beside the largest logit
+constexpr float kLost = 1024.0f;          // an lse beyond it may be off by 2^-14 and more
 constexpr float kNear = 65536.0f;         // largest exponent of a reference in the short form for bfloat16
 constexpr float kNearScale = 1e-30f;      // and least scale: its floor is a bfloat16 number
 
@@ -337,9 +337,11 @@ __device__ __forceinline__ RowStats stats_from_lse(const LogprobParams& P, long 
   return r;
 }
 
-// Whether every logit of the row is so low (a mask of the type's lowest
-// value) that lse does not hold log S any more.
-__device__ __forceinline__ bool log_s_is_lost(const RowStats& r) { return r.lse < kMasked && !r.empty; }
+// Whether lse is so large beside log S (a row far from zero, masked as a whole,
+// or at a low temperature) that probabilities taken from it would be off by its
+// rounding: beyond kLost by more than 2^-14 of themselves, in the end altogether.
+// An infinite lse is that of an empty row or a product beyond float32's range.
+__device__ __forceinline__ bool log_s_is_lost(const RowStats& r) { return fabsf(r.lse) > kLost; }
 
 // x[k], entries j .. j+N-1 of the row, become their gradients.
 template <int N>
@@ -668,7 +670,13 @@ __global__ void __launch_bounds__(kWarpThreads, NV == 16 ? 2 : NV == 8 ? 3 : 4) 
       });
       if (!near) a = far;
     }
-    if (MODE != kBackward || log_s_is_lost(r)) r = stats_of(a, P.scale);
+    if (MODE != kBackward) {
+      r = stats_of(a, P.scale);
+    } else if (log_s_is_lost(r)) {
+      const float entropy = r.entropy;
+      r = stats_of(a, P.scale);
+      r.entropy = entropy;
+    }
   }
   if constexpr (MODE != kBackward) {
     if (in && sub == 0) {
@@ -1391,7 +1399,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprob_score(const _
 
 template <bool BF16>
 __global__ void __launch_bounds__(kGradThreads) logprob_grad(const __grid_constant__ LogprobParams P) {
-  __shared__ float scratch[2][kGradThreads / 32];
+  __shared__ float scratch[kGradThreads / 32];
+  __shared__ float2 pair_scratch[kGradThreads / 32];
   constexpr int kN = kPer<BF16>;
   const long long row = blockIdx.x / P.chunks;
   const int chunk = blockIdx.x % P.chunks, t = threadIdx.x;
@@ -1413,21 +1422,25 @@ __global__ void __launch_bounds__(kGradThreads) logprob_grad(const __grid_consta
   if (on) r = stats_from_lse(P, row);
   if (on && log_s_is_lost(r)) {  // the row's first CTA takes all of it, with its own sums
     if (chunk != 0) return;
-    Sums a{-INFINITY, 0.0f, 0.0f};
-    for (int j = t; j < P.vocab; j += kGradThreads) a.m = fmaxf(a.m, at<BF16>(P.x, base + j));
-    a.m = cta_reduce<kGradThreads>(a.m, [](float x, float y) { return fmaxf(x, y); }, scratch[0]);
-    float2 s{}, w{};
-    for (int j = t; j < P.vocab; j += kGradThreads) {
-      const float x[2] = {at<BF16>(P.x, base + j), -INFINITY};
-      accumulate(s, w, x, reference(a.m), P.scale * kLog2e);
-    }
-    a.s = cta_reduce<kGradThreads>(s.x + s.y, [](float x, float y) { return x + y; }, scratch[1]);
+    const Sums a = sums_again<BF16, kGradThreads>(P.x, base, 0, P.vocab, P.scale * kLog2e, scratch, pair_scratch);
     const float entropy = r.entropy;
     r = stats_of(a, P.scale);
     r.entropy = entropy;
     const RowGrad g = grad_of(P, r, P.gl[row], P.ge ? P.ge[row] : 0.0f, target);
-    for (int j = t; j < P.vocab; j += kGradThreads)
-      put<BF16>(P.grad, out + j, grad_entry(g, P.scale, target, j, at<BF16>(P.x, base + j)));
+    constexpr int kU = 8;  // loads before the first store: the gradient may be written over the logits
+    for (int j0 = t; j0 < P.vocab; j0 += kU * kGradThreads) {
+      float x[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int j = j0 + u * kGradThreads;
+        x[u] = j < P.vocab ? at<BF16>(P.x, base + j) : 0.0f;
+      }
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int j = j0 + u * kGradThreads;
+        if (j < P.vocab) put<BF16>(P.grad, out + j, grad_entry(g, P.scale, target, j, x[u]));
+      }
+    }
     return;
   }
   RowGrad g{};

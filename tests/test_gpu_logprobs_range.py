@@ -173,3 +173,45 @@ def test_a_row_does_not_depend_on_its_neighbours(kind):
     a, b = (muon.token_logprobs_loss(put(z, kind), y, gl, gl) for z in (x, rounded(w, kind)))
     for p, q in zip((*a[:3], a.grad), (*b[:3], b.grad)):
         assert torch.equal(p[::2], q[::2])
+
+
+def backward(c, loss):
+    if loss and not c.held:
+        for k in (c.top, 0):
+            q = muon.token_logprobs_loss(c.X, c.Y, c.GL, c.GE, top=k, scale=c.scale)
+            check_grad(q.grad, c.grad, c.size, c.rel + c.saved, c.scale, c.kind, f"loss gradient, top {k}")
+    r = muon.token_logprobs(c.X, c.Y, scale=c.scale)
+    for out in (None, c.X):
+        G = muon.token_logprobs_backward(c.X, c.Y, r.lse, c.GL, entropy=r.entropy, grad_entropy=c.GE, scale=c.scale, out=out)
+        check_grad(G, c.grad, c.size, c.rel + c.saved, c.scale, c.kind, "backward" + (" in place" if out is not None else ""))
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,vocab", SHAPES)
+def test_backward_of_rows_at_large_constants(rows, vocab, kind):
+    x, y = rows_of(np.random.default_rng(vocab), rows, vocab, kind)
+    backward(Case(x, y, kind, 1.0), True)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("scale", [1e-30, 100.0, 1e4, 1e6])
+@pytest.mark.parametrize("rows,vocab", [(6000, 150), (40, 301), (24, 9001), (16, 130_001)])
+def test_backward_at_low_and_high_temperatures(rows, vocab, scale, kind):
+    backward(Case(*hot_rows(rows, vocab, kind), kind, scale, pad=3), True)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("vocab", [130, 9001])
+def test_backward_where_lse_overflows(vocab, kind):
+    """The lowest value at scale 4: lse is -inf, as for an empty row, which has no gradient; the row is uniform."""
+    x = np.full((4, vocab), float(torch.finfo(KIND[kind]).min))
+    x[2] = -np.inf
+    X, y, one = put(x, kind), torch.tensor([1, 2, 3, -1], device="cuda"), torch.ones(4, device="cuda")
+    r = muon.token_logprobs(X, y, scale=4.0)
+    assert r.lse.tolist() == [-np.inf] * 3 + [0.0]
+    want = -4.0 / vocab * np.ones((4, vocab))
+    want[[0, 1], [1, 2]] += 4.0
+    want[2:] = 0
+    for G in (muon.token_logprobs_backward(X, y, r.lse, one, scale=4.0), muon.token_logprobs_loss(X, y, one, scale=4.0).grad):
+        # a probability 2^-20 (1 + 2 log V) off, half a spacing of bfloat16
+        assert (np.abs(host(G) - want) <= (2.0 ** -15 + (2.0 ** -9 if kind == "bf16" else 0)) * np.abs(want)).all()
