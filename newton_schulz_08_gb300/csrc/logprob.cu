@@ -60,7 +60,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kFloor = -1000.0f;        // least exponent
 constexpr float kLost = 1024.0f;          // an lse beyond it may be off by 2^-14 and more
 constexpr float kNear = 65536.0f;         // largest exponent of a reference in the short form for bfloat16
-constexpr float kNearScale = 1e-30f;      // and least scale: its floor is a bfloat16 number
+constexpr float kMasked = -1e30f;         // its floor for logits in sums
+constexpr float kNearScale = 1e-24f;      // and least scale: the floor's exponent is -10^6
 
 enum Mode { kScore = 0, kLoss = 1, kBackward = 2 };
 
@@ -82,7 +83,7 @@ struct LogprobParams {
   int log_ranks;    // logprob_score, logprob_loss: CTAs per row, as a power of two
   int segment;      // logprob_loss: vectors that a CTA has room for
   int chunks;       // logprob_grad: CTAs per row
-  uint32_t floor2;  // two bfloat16 numbers whose exponent is -2 kNear, for the short form
+  uint32_t floor2;  // two bfloat16 numbers whose exponent is -2 kNear, for the short form of gradients
 };
 
 template <bool BF16>
@@ -225,12 +226,11 @@ __device__ __forceinline__ void accumulate(float2& s, float2& w, const float (&x
 }
 
 // The short form for bfloat16, where the exponent of the reference, ref c2, is
-// below kNear: entries are held above `floor2` in pairs before they are widened
-// (with ref c2 taken off its exponent is below -kNear, a power of 0, and a
-// product with it stays finite), and the exponent is one fused operation of
-// K = -ref c2 (44 instructions a vector against 52).  K is rounded, by up to 2^-9;
-// that goes into every exponent alike and is taken out of the sums (settle) and
-// of the gradient's factors (near_of).
+// below kNear: entries are held above a floor in pairs before they are widened
+// (whatever the reference, its exponent is one of a power of 0), and the exponent
+// is one fused operation of K = -ref c2 (44 instructions a vector against 52).
+// K is rounded, by up to 2^-9; that goes into every exponent alike and is taken
+// out of the sums (settle) and of the gradient's factors (near_of).
 template <bool BF16>
 __device__ __forceinline__ bool near_fits(float ref, float c2) {
   return !BF16 || (fabsf(ref * c2) < kNear && c2 >= kNearScale);
@@ -244,14 +244,15 @@ __device__ __forceinline__ float ex2_small(float d) {
 
 // Adds a vector.
 template <bool BF16>
-__device__ __forceinline__ void accumulate_near(float2& s, float2& w, uint4 q, float ref, float c2, uint32_t floor2) {
+__device__ __forceinline__ void accumulate_near(float2& s, float2& w, uint4 q, float ref, float c2) {
   if constexpr (BF16) {
+    const __nv_bfloat162 floor2 = __floats2bfloat162_rn(kMasked, kMasked);
     uint32_t v[4] = {q.x, q.y, q.z, q.w};
     const float k = __fmul_rn(-ref, c2);
     const float2 scale = make_float2(c2, c2), K = make_float2(k, k);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const __nv_bfloat162 b = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&v[k]), *reinterpret_cast<const __nv_bfloat162*>(&floor2));
+      const __nv_bfloat162 b = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&v[k]), floor2);
       v[k] = *reinterpret_cast<const uint32_t*>(&b);
       const float2 t = __ffma2_rn(make_float2(__uint_as_float(v[k] << 16), __uint_as_float(v[k] & 0xFFFF0000u)), scale, K);
       const float2 e = make_float2(ex2(t.x), ex2(t.y));
@@ -365,7 +366,8 @@ __device__ __forceinline__ void grad_entries(const RowGrad& g, float scale, int6
   }
 }
 
-// The same for a vector.  bfloat16 in the short form, t = log2 p_j in one fused operation.
+// The same for a vector.  bfloat16 in the short form, t = log2 p_j in one fused operation;
+// the floor follows the scale, so that a2 t stays finite (0 times it is 0).
 struct NearGrad {
   float c2, K, a2, b;  // t = x c2 + K, grad = 2^t (a2 t + b)
   bool fits;
@@ -659,7 +661,7 @@ __global__ void __launch_bounds__(kWarpThreads, NV == 16 ? 2 : NV == 8 ? 3 : 4) 
       }
     };
     const bool near = near_fits<BF16>(reference(a.m), c2);
-    add_up(a, [&](float2& s, float2& w, uint4 v) { accumulate_near<BF16>(s, w, v, reference(a.m), c2, P.floor2); });
+    add_up(a, [&](float2& s, float2& w, uint4 v) { accumulate_near<BF16>(s, w, v, reference(a.m), c2); });
     settle<BF16>(a, c2);
     if (BF16 && __any_sync(0xFFFFFFFFu, !near && on)) {
       Sums far = a;
@@ -1137,7 +1139,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 8 : 3) logprob_loss(
       for (int i = group * p.per + t; i < end; i += THREADS) {
         const uint4 v = q[i];
         if (TOP) chunk.add(v);
-        accumulate_near<BF16>(s, w, v, a.m, c2, P.floor2);
+        accumulate_near<BF16>(s, w, v, a.m, c2);
       }
       if constexpr (TOP) {
         S.chunk_max[group][t] = chunk.value();
@@ -1291,7 +1293,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprob_score(const _
   for (int d = 16; d > 0; d /= 2) sums.m = fmaxf(sums.m, __shfl_xor_sync(0xFFFFFFFFu, sums.m, d));
   float2 s{}, w{};
   bool found = sums.m != -INFINITY;
-  if (warp < 2) accumulate_near<BF16>(s, w, end, reference(sums.m), c2, P.floor2);
+  if (warp < 2) accumulate_near<BF16>(s, w, end, reference(sums.m), c2);
   // a chunk: batches of a thread that share a largest entry, a power of two of them
   const int batches = (n + kBatch - 1) / kBatch;
   int log_chunk = 0;
@@ -1313,7 +1315,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprob_score(const _
     for (int u = 0; u < kU; ++u) {
       if (i + u * THREADS < n) {
         if (TOP) largest.add(a[u]);
-        accumulate_near<BF16>(s, w, a[u], reference(sums.m), c2, P.floor2);
+        accumulate_near<BF16>(s, w, a[u], reference(sums.m), c2);
       }
       a[u] = b[u];
     }
