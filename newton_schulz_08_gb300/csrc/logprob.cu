@@ -82,6 +82,7 @@ struct LogprobParams {
   int lanes;        // logprob_warp: lanes per row
   int log_ranks;    // logprob_score, logprob_loss: CTAs per row, as a power of two
   int segment;      // logprob_loss: vectors that a CTA has room for
+  int group;        // and of them in each of its four groups of copies, a multiple of the threads
   int chunks;       // logprob_grad: CTAs per row
   uint32_t floor2;  // two bfloat16 numbers whose exponent is -2 kNear, for the short form of gradients
 };
@@ -998,26 +999,25 @@ struct Exchange {
   unsigned long long top[kMaxCluster][kMaxTop];
 };
 
-// One CTA's part of a row: vectors v0 .. v0+n-1, `per` of each of four groups.
+// One CTA's part of a row: vectors v0 .. v0+n-1.
 template <bool BF16>
 struct RowPart {
   const unsigned char* src;  // vector v0
-  int shift, v0, n, per;
+  int shift, v0, n;
   int lo, wholes;            // the row's whole vectors: lo .. lo+wholes-1
   __device__ __forceinline__ int first(int i) const { return (v0 + i) * kPer<BF16> - shift; }
   __device__ __forceinline__ bool whole(int i) const { return static_cast<unsigned>(v0 + i - lo) < static_cast<unsigned>(wholes); }
 };
 
-template <bool BF16, int THREADS>
+template <bool BF16>
 __device__ __forceinline__ RowPart<BF16> part_of(const LogprobParams& P, long long row, int rank) {
   const RowVectors<BF16> R(P.x, row * P.stride, P.vocab);
   RowPart<BF16> p;
   // at most 2^28 + 1 vectors and eight CTAs, a power of two of them: no division
   p.v0 = static_cast<int>(static_cast<unsigned>(R.count) * rank >> P.log_ranks);
   p.n = static_cast<int>(static_cast<unsigned>(R.count) * (rank + 1) >> P.log_ranks) - p.v0;
-  p.per = static_cast<unsigned>(p.n + 4 * THREADS - 1) / (4 * THREADS) * THREADS;
   if (!MUON_CHECK(row >= 0 && row < P.rows && p.v0 + p.n <= R.count)) p.n = 0;
-  if (!MUON_CHECK(P.segment == 0 || p.n <= P.segment)) p.n = P.segment;
+  if (!MUON_CHECK(P.segment == 0 || (p.n <= P.segment && p.n <= 4 * P.group))) p.n = min(P.segment, 4 * P.group);
   p.src = R.base + p.v0 * 16LL;
   p.shift = R.shift;
   p.lo = R.shift > 0 ? 1 : 0;
@@ -1029,7 +1029,9 @@ __device__ __forceinline__ RowPart<BF16> part_of(const LogprobParams& P, long lo
 // row lies in its shared memory as vectors in four groups; a thread's vectors
 // are the ones it copies, so it works on a group without waiting for other
 // threads, and copies the next row's group as soon as it is done with one:
-// the loads go on while sums are exchanged and alternatives ranked.
+// the loads go on while sums are exchanged and alternatives ranked.  Groups are
+// the same vectors of every row, however many the row's place makes of it: what
+// is copied for the next row then lies where this row is done with.
 template <bool BF16, int THREADS, bool TOP>
 __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 8 : 3) logprob_loss(const __grid_constant__ LogprobParams P) {
   extern __shared__ __align__(16) unsigned char segment[];
@@ -1049,8 +1051,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 8 : 3) logprob_loss(
   // one group of copies, empty past the last row and for rows that are left out
   auto copy = [&](const RowPart<BF16>& p, bool on, int group) {
     if (on) {
-      const int end = min(p.n, (group + 1) * p.per);
-      int i = group * p.per + t;
+      const int end = min(p.n, (group + 1) * P.group);
+      int i = group * P.group + t;
       const unsigned char* src = p.src + i * 16LL;
       unsigned dst = static_cast<unsigned>(__cvta_generic_to_shared(q + i));
       for (; i < end; i += THREADS, src += THREADS * 16, dst += THREADS * 16) {
@@ -1072,7 +1074,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 8 : 3) logprob_loss(
 
   long long row = blockIdx.x >> P.log_ranks;
   int64_t target = P.targets[row];
-  RowPart<BF16> p = part_of<BF16, THREADS>(P, row, rank);
+  RowPart<BF16> p = part_of<BF16>(P, row, rank);
   // a CTA's shared memory is written by others only once it has begun
   if (ranks > 1) cg::cluster_group::barrier_arrive();
 #pragma unroll 1
@@ -1086,7 +1088,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 8 : 3) logprob_loss(
     const long long next = row + clusters;
     const int64_t next_target = next < P.rows ? P.targets[next] : -1;
     const bool next_on = next_target >= 0;
-    const RowPart<BF16> np = part_of<BF16, THREADS>(P, next_on ? next : row, rank);
+    const RowPart<BF16> np = part_of<BF16>(P, next_on ? next : row, rank);
     const long long base = row * P.stride, out = row * P.grad_stride;
     const int j0 = max(0, p.first(0)), j1 = min(P.vocab, p.first(p.n));  // this CTA's entries
     // the gradient's vectors begin where the row's do
@@ -1133,10 +1135,10 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 8 : 3) logprob_loss(
 #pragma unroll 1
     for (int group = 0; group < 4; ++group) {
       asm volatile("cp.async.wait_group 3;" ::: "memory");
-      const int end = min(p.n, (group + 1) * p.per);
+      const int end = min(p.n, (group + 1) * P.group);
       VecMax<BF16> chunk;
 #pragma unroll 2
-      for (int i = group * p.per + t; i < end; i += THREADS) {
+      for (int i = group * P.group + t; i < end; i += THREADS) {
         const uint4 v = q[i];
         if (TOP) chunk.add(v);
         accumulate_near<BF16>(s, w, v, a.m, c2);
@@ -1172,7 +1174,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 8 : 3) logprob_loss(
     if constexpr (TOP) {
       top_bound(P.top, own, S);
       gather_top<BF16>(P.top, P.x, base, j0, j1, S, [&] {
-        collect_seen<BF16>(own, 4, p.per / THREADS, p.n, p.first(0), P.vocab, [&](int i) { return q[i]; }, S);
+        collect_seen<BF16>(own, 4, P.group / THREADS, p.n, p.first(0), P.vocab, [&](int i) { return q[i]; }, S);
       });
       top_rank<BF16>(P.top, P.x, base, j0, j1, S);
       if (ranks > 1) {
@@ -1201,9 +1203,9 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 8 : 3) logprob_loss(
     if (same && near.fits) {
 #pragma unroll 1
       for (int group = 0; group < 4; ++group) {
-        const int end = min(p.n, (group + 1) * p.per);
+        const int end = min(p.n, (group + 1) * P.group);
 #pragma unroll 2
-        for (int i = group * p.per + t; i < end; i += THREADS) {
+        for (int i = group * P.group + t; i < end; i += THREADS) {
           const int j = p.first(i);
           const uint4 v = grad_near<BF16>(P, g, near, target, j, q[i]);
           if (p.whole(i)) {
@@ -1269,7 +1271,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprob_score(const _
   }
   // a CTA's shared memory is written by others only once it has begun
   if (ranks > 1) cg::cluster_group::barrier_arrive();
-  const RowPart<BF16> p = part_of<BF16, THREADS>(P, row, rank);
+  const RowPart<BF16> p = part_of<BF16>(P, row, rank);
   // the part's whole vectors src[0 .. n-1]; the row's other two (its ends) are
   // put together from their entries by one thread each
   const bool head = p.v0 < p.lo, tail = p.v0 + p.n > p.lo + p.wholes;
@@ -1569,7 +1571,8 @@ cudaError_t launch_score(LogprobParams P, bool bf16, long long bytes, int sms, c
   return launch_clusters(kScoreKernels[(wide ? 1 : 0) | (P.top > 0 ? 2 : 0) | (bf16 ? 4 : 0)], P, P.rows, wide ? 256 : 128, 0, stream);
 }
 
-cudaError_t launch_loss(LogprobParams P, bool bf16, long long bytes, int sms, cudaStream_t stream) {
+// vecs: the most vectors that a row of `bytes` with its ends can have here.
+cudaError_t launch_loss(LogprobParams P, bool bf16, long long bytes, long long vecs, int sms, cudaStream_t stream) {
   int ranks = 1;
   while (bytes > static_cast<long long>(ranks) * kSegmentBytes) ranks *= 2;
   ranks = spread(ranks, P.rows, bytes, sms);
@@ -1577,14 +1580,16 @@ cudaError_t launch_loss(LogprobParams P, bool bf16, long long bytes, int sms, cu
   const long long part = (bytes + 15) / 16 / ranks + 1;  // vectors
   const bool wide = part > 2048;                         // 32 KB: 256 threads take eight vectors each
   const KernelPtr f = kLossKernels[(wide ? 1 : 0) | (P.top > 0 ? 2 : 0) | (bf16 ? 4 : 0)];
+  const int threads = wide ? 256 : 128;
   P.segment = static_cast<int>(part);
+  P.group = static_cast<int>(((vecs + ranks - 1) / ranks + 4 * threads - 1) / (4 * threads)) * threads;
   const size_t smem = static_cast<size_t>(part) * 16;
   const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(f), cudaFuncAttributeMaxDynamicSharedMemorySize, kSegmentBytes + 64);
   if (e != cudaSuccess) return e;
   // as many clusters as are resident at a time (more would only wait)
   const long long per_sm = std::min<long long>(wide ? 3 : 8, (228 * 1024) / (smem + kLossStatic));
   const long long resident = std::max<long long>(1, per_sm * sms / ranks);
-  return launch_clusters(f, P, std::min<long long>(P.rows, resident), wide ? 256 : 128, smem, stream);
+  return launch_clusters(f, P, std::min<long long>(P.rows, resident), threads, smem, stream);
 }
 
 // What both directions check and launch; grad, gl: null for a score alone,
@@ -1679,7 +1684,7 @@ muon_status_t run(const void* logits, int dtype, int64_t rows, int64_t vocab, in
     kWarpKernels[k + 5 * mode + (bf16 ? 15 : 0)]<<<grid, kWarpThreads, 0, str>>>(P);
     err = cudaGetLastError();
   } else {
-    if (score && backward && held) err = launch_loss(P, bf16, bytes, sms, str);
+    if (score && backward && held) err = launch_loss(P, bf16, bytes, vecs, sms, str);
     else if (score) err = launch_score(P, bf16, bytes, sms, str);
     if (err == cudaSuccess && backward && !(score && held)) {
       P.chunks = static_cast<int>(chunks);
