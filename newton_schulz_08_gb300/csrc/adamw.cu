@@ -8,7 +8,11 @@
 // with the scalars formed in double on the host and rounded once.  In the
 // moments every operation is rounded and none fused, so that codes do not
 // depend on how the compiler contracts; u takes the approximate root and
-// reciprocal (a few units in the last place of a change that is small beside p).
+// reciprocal (a few units in the last place of a change that is small beside p),
+// which take subnormals for zeros.  A second moment below 2^-126 has a root below
+// 2^-63: where eps does not cover that (eps < 2^-41 r2), u takes a root and a
+// quotient of the whole range, in kernels of their own (as a branch in the others
+// it cost the 8-bit steps 3 to 8 %: 386 us for 373, 231 for 213).
 //
 // 8-bit moments.  A block of 256 consecutive elements of a tensor shares a
 // power-of-two scale.  E = floor(log2 max |x|) (at least -100); the first
@@ -106,6 +110,16 @@ __device__ __forceinline__ float rcp_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+__device__ __forceinline__ float sqrt_whole(float x) {
+  float y;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float div_whole(float x, float y) {
+  float z;
+  asm("div.full.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
+  return z;
 }
 __device__ __forceinline__ float max3_abs_nan(float a, float b, float c) {
   float y;
@@ -304,6 +318,7 @@ __device__ __forceinline__ float block_max(const Eight& x) {
 }
 
 // The step of eight elements: m, v and p in, out.
+template <bool WHOLE>
 __device__ __forceinline__ void update(const AdamwParams& P, float step, float decay, float gs, const Eight& g, Eight& p, Eight& m,
                                        Eight& v) {
   auto both = [](float a) { return make_float2(a, a); };
@@ -312,9 +327,14 @@ __device__ __forceinline__ void update(const AdamwParams& P, float step, float d
     const float2 gk = mul2(g.v[k], both(gs));
     m.v[k] = add_apart(mul2(m.v[k], both(P.b1)), mul2(gk, both(P.omb1)));
     v.v[k] = add_apart(mul2(v.v[k], both(P.b2)), mul2(mul2(gk, gk), both(P.omb2)));
-    const float2 root = make_float2(sqrt_approx(v.v[k].x), sqrt_approx(v.v[k].y));
-    const float2 den = __ffma2_rn(root, both(P.r2), both(P.eps));
-    const float2 u = mul2(m.v[k], make_float2(rcp_approx(den.x), rcp_approx(den.y)));
+    float2 u;
+    if constexpr (WHOLE) {
+      const float2 den = __ffma2_rn(make_float2(sqrt_whole(v.v[k].x), sqrt_whole(v.v[k].y)), both(P.r2), both(P.eps));
+      u = make_float2(div_whole(m.v[k].x, den.x), div_whole(m.v[k].y, den.y));
+    } else {
+      const float2 den = __ffma2_rn(make_float2(sqrt_approx(v.v[k].x), sqrt_approx(v.v[k].y)), both(P.r2), both(P.eps));
+      u = mul2(m.v[k], make_float2(rcp_approx(den.x), rcp_approx(den.y)));
+    }
     float2 dec = mul2(p.v[k], both(decay));
     if (P.cautious) {
       auto agree = [](float a, float b) { return (a > 0.0f && b > 0.0f) || (a < 0.0f && b < 0.0f); };
@@ -378,11 +398,11 @@ __device__ __forceinline__ Fetched fetch_block(const AdamwTensor& T, long long b
 
 // One block from what has been read of it; `left` entries in the strided
 // layout, all of them (VEC) in the vector layout.
-template <bool PB, bool GB, bool B8, bool VEC>
+template <bool PB, bool GB, bool B8, bool VEC, bool WHOLE>
 __device__ __forceinline__ void step_block(const AdamwParams& P, const AdamwTensor& T, long long blk, int lane, int left, float gs,
                                            Eight& p, const Eight& g, Eight& m, Eight& v) {
   const long long i0 = blk * kQBlock;
-  update(P, T.step, T.decay, gs, g, p, m, v);
+  update<WHOLE>(P, T.step, T.decay, gs, g, p, m, v);
   uint32_t h[8];
   if constexpr (B8 || PB) {
     const uint32_t key = T.key + static_cast<uint32_t>(static_cast<unsigned long long>(i0) >> 32) * kC1;
@@ -440,7 +460,7 @@ __device__ __forceinline__ void step_block(const AdamwParams& P, const AdamwTens
 // One block a warp: the CTAs at work then cover one stretch of every array.
 // With eight blocks a warp, CTAs 16,384 elements apart, the 8-bit step of
 // 100.7 M float32 parameters took 358 us in place of 250.
-template <bool PB, bool GB, bool B8, int N>
+template <bool PB, bool GB, bool B8, int N, bool WHOLE>
 __global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constant__ AdamwTable<N> P) {
   int lo = 0, hi = P.n - 1;  // the tensor: largest i with first <= blockIdx.x
   while (lo < hi) {
@@ -467,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constan
       m = align<false>(f.m, T.m, lane);
       v = align<false>(f.v, T.v, lane);
     }
-    step_block<PB, GB, B8, true>(P, T, blk, lane, kQBlock, gs, p, g, m, v);
+    step_block<PB, GB, B8, true, WHOLE>(P, T, blk, lane, kQBlock, gs, p, g, m, v);
   } else {  // a tensor's last block (and first), and arrays off the vectors' boundaries
     Eight p = load_strided<PB>(T.p, i0, lane, left);
     const Eight g = load_strided<GB>(T.g, i0, lane, left);
@@ -478,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constan
       m = load_strided<false>(T.m, i0, lane, left);
       v = load_strided<false>(T.v, i0, lane, left);
     }
-    step_block<PB, GB, B8, false>(P, T, blk, lane, left, gs, p, g, m, v);
+    step_block<PB, GB, B8, false, WHOLE>(P, T, blk, lane, left, gs, p, g, m, v);
   }
 }
 
@@ -486,11 +506,12 @@ template <int N>
 using KernelPtr = void (*)(AdamwTable<N>);
 
 // Index: bfloat16 parameters | bfloat16 gradients << 1 | 8-bit moments << 2.
-template <int N>
+template <int N, bool WHOLE>
 const KernelPtr<N> kKernels[8] = {
-    adamw_kernel<false, false, false, N>, adamw_kernel<true, false, false, N>, adamw_kernel<false, true, false, N>,
-    adamw_kernel<true, true, false, N>,   adamw_kernel<false, false, true, N>, adamw_kernel<true, false, true, N>,
-    adamw_kernel<false, true, true, N>,   adamw_kernel<true, true, true, N>,
+    adamw_kernel<false, false, false, N, WHOLE>, adamw_kernel<true, false, false, N, WHOLE>,
+    adamw_kernel<false, true, false, N, WHOLE>,  adamw_kernel<true, true, false, N, WHOLE>,
+    adamw_kernel<false, false, true, N, WHOLE>,  adamw_kernel<true, false, true, N, WHOLE>,
+    adamw_kernel<false, true, true, N, WHOLE>,   adamw_kernel<true, true, true, N, WHOLE>,
 };
 
 // Whether a lane may take eight neighbouring elements: 16-byte float32 arrays,
@@ -587,7 +608,7 @@ muon_status_t adamw_plan::build() {
 namespace muon {
 namespace {
 
-template <int N>
+template <int N, bool WHOLE>
 cudaError_t launch(const adamw_plan& plan, const adamw_plan::Launch& l, const AdamwParams& scalars, double bc1, uint32_t key,
                    cudaStream_t s) {
   AdamwTable<N> P;
@@ -600,7 +621,7 @@ cudaError_t launch(const adamw_plan& plan, const adamw_plan::Launch& l, const Ad
     P.t[i].decay = static_cast<float>(d.lr * d.weight_decay);
     P.t[i].key = mix(key + kC0 * static_cast<uint32_t>(l.index[i]));
   }
-  kKernels<N>[l.kind]<<<static_cast<unsigned>(l.ctas), kThreads, 0, s>>>(P);
+  kKernels<N, WHOLE>[l.kind]<<<static_cast<unsigned>(l.ctas), kThreads, 0, s>>>(P);
   return cudaGetLastError();
 }
 
@@ -630,9 +651,12 @@ muon_status_t run_plan(const adamw_plan& plan, double beta1, double beta2, doubl
   P.r2 = static_cast<float>(1.0 / std::sqrt(bc2));
   P.eps = static_cast<float>(eps);
   P.grad_scale = grad_scale;
+  const bool whole = P.eps < 0x1p-41f * P.r2;
   for (const auto& l : plan.launches) {
-    const cudaError_t e = l.t.size() <= static_cast<size_t>(kFewTensors) ? launch<kFewTensors>(plan, l, P, bc1, k, s)
-                                                                         : launch<kMaxTensors>(plan, l, P, bc1, k, s);
+    const bool few = l.t.size() <= static_cast<size_t>(kFewTensors);
+    const cudaError_t e = whole ? launch<kMaxTensors, true>(plan, l, P, bc1, k, s)
+                          : few ? launch<kFewTensors, false>(plan, l, P, bc1, k, s)
+                                : launch<kMaxTensors, false>(plan, l, P, bc1, k, s);
     if (e != cudaSuccess) return MUON_ERR_CUDA;
   }
   return MUON_OK;
