@@ -336,10 +336,10 @@ typedef struct adamw_tensor_desc {
  *                       tensor is skipped);
  *   step >= 1; beta1, beta2 in [0, 1); eps >= 0 and finite;
  *   grad_scale          device pointer to one float (a clipping factor), or
- *                       NULL; it must lie outside the written arrays.
+ *                       NULL; it lies outside the written arrays.
  * Errors (nothing enqueued): MUON_ERR_INVALID_ARG, MUON_ERR_MISALIGNED (a
  * pointer not aligned to its element), MUON_ERR_ALIASING (a written array
- * overlaps another array; gradients may be shared), MUON_ERR_TOO_LARGE,
+ * overlaps another array or grad_scale; gradients may be shared), MUON_ERR_TOO_LARGE,
  * MUON_ERR_UNSUPPORTED_DEVICE, MUON_ERR_HOST_MEMORY; MUON_ERR_CUDA (launch
  * failure).  Asynchronous on `stream`; no workspace; one launch per 400
  * tensors of the same types. */

@@ -44,9 +44,11 @@
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <memory>
 #include <new>
 #include <vector>
 
@@ -522,6 +524,24 @@ bool vector_aligned(const adamw_tensor_desc& d) {
          aligned_to(d.exp_avg, state) && aligned_to(d.exp_avg_sq, state);
 }
 
+// The written ranges of a checked list, by address.
+void written_ranges(const adamw_tensor_desc* t, int n, std::vector<Span>& spans) {
+  spans.clear();
+  spans.reserve(static_cast<size_t>(n) * 5);
+  for (int i = 0; i < n; ++i) {
+    const adamw_tensor_desc& d = t[i];
+    if (d.numel == 0) continue;
+    const uint64_t n64 = static_cast<uint64_t>(d.numel), nb = (n64 + kQBlock - 1) / kQBlock, ns = d.state_bits == 8 ? 1 : 4;
+    spans.push_back(span_of(d.param, n64 * (d.param_dtype == MUON_F32 ? 4 : 2), true));
+    spans.push_back(span_of(d.exp_avg, n64 * ns, true));
+    spans.push_back(span_of(d.exp_avg_sq, n64 * ns, true));
+    if (d.state_bits != 8) continue;
+    spans.push_back(span_of(d.exp_avg_scale, nb * 4, true));
+    spans.push_back(span_of(d.exp_avg_sq_scale, nb * 4, true));
+  }
+  std::sort(spans.begin(), spans.end(), [](const Span& a, const Span& b) { return a.lo < b.lo; });
+}
+
 muon_status_t check_tensors(const adamw_tensor_desc* t, int n, bool need_grads) {
   if (n < 0 || (n > 0 && !t)) return MUON_ERR_INVALID_ARG;
   std::vector<Span> spans;
@@ -568,8 +588,10 @@ struct adamw_plan {
   };
   std::vector<adamw_tensor_desc> desc;
   std::vector<Launch> launches;
+  std::vector<muon::Span> written;  // no two of them overlap; left empty where no grad_scale comes
 
   muon_status_t build();
+  bool writes(const void* p, uint64_t bytes) const;  // any of these bytes
 };
 
 muon_status_t adamw_plan::build() {
@@ -605,6 +627,12 @@ muon_status_t adamw_plan::build() {
   return MUON_OK;
 }
 
+bool adamw_plan::writes(const void* p, uint64_t bytes) const {
+  const muon::Span s = muon::span_of(p, bytes, false);
+  auto next = std::upper_bound(written.begin(), written.end(), s.lo, [](uintptr_t at, const muon::Span& w) { return at < w.lo; });
+  return (next != written.begin() && (next - 1)->hi > s.lo) || (next != written.end() && next->lo < s.hi);
+}
+
 namespace muon {
 namespace {
 
@@ -631,6 +659,7 @@ muon_status_t run_plan(const adamw_plan& plan, double beta1, double beta2, doubl
       !std::isfinite(eps))
     return MUON_ERR_INVALID_ARG;
   if (!aligned_to(grad_scale, 4)) return MUON_ERR_MISALIGNED;
+  if (grad_scale && plan.writes(grad_scale, 4)) return MUON_ERR_ALIASING;
   const double bc1 = 1.0 - std::pow(beta1, static_cast<double>(step));
   const double bc2 = 1.0 - std::pow(beta2, static_cast<double>(step));
   if (!(bc1 > 0.0) || !(bc2 > 0.0)) return MUON_ERR_INVALID_ARG;
@@ -675,14 +704,12 @@ muon_status_t adamw_plan_create(const adamw_tensor_desc* tensors, int n_tensors,
   try {
     muon_status_t st = muon::check_tensors(tensors, n_tensors, false);
     if (st != MUON_OK) return st;
-    adamw_plan* p = new adamw_plan;
+    std::unique_ptr<adamw_plan> p(new adamw_plan);
     p->desc.assign(tensors, tensors + n_tensors);
     st = p->build();
-    if (st != MUON_OK) {
-      delete p;
-      return st;
-    }
-    *plan = p;
+    if (st != MUON_OK) return st;
+    muon::written_ranges(tensors, n_tensors, p->written);
+    *plan = p.release();
     return MUON_OK;
   } catch (const std::bad_alloc&) {
     return MUON_ERR_HOST_MEMORY;
@@ -701,6 +728,7 @@ muon_status_t adamw_plan_set_grads(adamw_plan* plan, const void* const* grads, c
     muon_status_t st = muon::check_tensors(next.desc.data(), static_cast<int>(next.desc.size()), true);
     if (st == MUON_OK) st = next.build();
     if (st != MUON_OK) return st;
+    next.written.swap(plan->written);  // the same arrays
     std::swap(*plan, next);
     return MUON_OK;
   } catch (const std::bad_alloc&) {
@@ -736,6 +764,7 @@ muon_status_t adamw_step(const adamw_tensor_desc* tensors, int n_tensors, double
     p.desc.assign(tensors, tensors + n_tensors);
     st = p.build();
     if (st != MUON_OK) return st;
+    if (grad_scale) muon::written_ranges(tensors, n_tensors, p.written);
     return muon::run_plan(p, beta1, beta2, eps, cautious, step, seed, grad_scale, static_cast<cudaStream_t>(stream));
   } catch (const std::bad_alloc&) {
     return MUON_ERR_HOST_MEMORY;
