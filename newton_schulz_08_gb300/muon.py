@@ -744,6 +744,10 @@ class AdamW:
     grads    the gradients' tensors when they stay in place (a bucket);
              otherwise pass them to step();
     step     steps already taken.
+
+    The addresses of the tensors are kept, and their memory with them: a
+    parameter or moment that is given other memory afterwards (``p.data = ...``,
+    ``module.to(...)``) is not followed and needs a new AdamW.
     """
 
     def __init__(self, params, grads=None, states=None, bits=32, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8,
@@ -758,6 +762,7 @@ class AdamW:
             raise ValueError("AdamW needs at least one parameter")
         arr, n, every = _adamw_descs(self.params, self.grads, self.states, lr, weight_decay)
         self._index = _index_of("AdamW", *every)
+        self._memory = [t.untyped_storage() for t in every]
         _check(lib().adamw_plan_create(arr, n, ctypes.byref(self._plan)), "AdamW")
 
     def __del__(self):

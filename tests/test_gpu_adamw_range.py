@@ -1,9 +1,11 @@
 """AdamW where second moments are float32 subnormals and eps does not cover
-them: against the oracle, at the tolerances of test_gpu_adamw."""
+them: against the oracle, at the tolerances of test_gpu_adamw.  And what the
+object holds."""
 
 import pytest
 import torch
 
+from newton_schulz_08_gb300 import muon
 from tests.test_gpu_adamw import HP, Tensor, step_all
 
 pytestmark = pytest.mark.gpu
@@ -33,3 +35,14 @@ def test_subnormal_eps(bits):
     step_all([t], 1, eps=2.0 ** -130, seed=2)
     t.check(1, 0, 2, hp=hp)
     assert bool(torch.isfinite(t.P).all())
+
+
+def test_the_object_keeps_its_tensors_memory():
+    """A parameter given other data after the object was made: the memory that the object steps is not handed out again."""
+    p, g = torch.nn.Parameter(torch.zeros(1 << 20, device="cuda")), torch.zeros(1 << 20, device="cuda")
+    opt = muon.AdamW([p], grads=[g])
+    old = {t.data_ptr() for t in (p, g)}
+    p.data, g.data = torch.ones(4, device="cuda"), torch.ones(4, device="cuda")
+    new = [torch.empty(1 << 20, device="cuda") for _ in range(8)]
+    assert not old & {t.data_ptr() for t in new}
+    del opt
