@@ -321,6 +321,14 @@ typedef struct adamw_tensor_desc {
  * E4M3, the second's 2^(E-14) and E5M2; a value is code * scale.  All-zero
  * codes with finite scales are the zero state.  A block with a value that is
  * not finite, or 2^127 or more, gets a NaN scale.
+ * What a block can hold: first moments of 2^-13 and second ones of 2^-28 of its
+ * power of two and more have 3 and 2 fraction bits; smaller ones are held as
+ * multiples of 2^-16 and 2^-30, at random but right in the mean.  Gradients
+ * of one block may therefore differ in size by up to 2^12.  Where an
+ * element's are smaller by 2^14 and more, its second moment is mostly held as
+ * 0 while its first one now and then is not, and u, of order 1 otherwise, may
+ * become as large as 2^-15 max |m| / eps: keep such tensors (a table
+ * whose rows are no multiple of 256 wide and differ that much) in 32 bits.
  * Codes, and bfloat16 parameters, are rounded stochastically (up with the
  * probability of the remainder), so that averages whose change per step is
  * below their spacing stay unbiased.  The 32 random bits of element i of

@@ -27,6 +27,10 @@
 // takes come from a counter hash of (seed, step, tensor, element): the result
 // does not depend on the launch.  bfloat16 parameters are rounded in the same
 // way with 16 other bits, since updates are often below half their spacing.
+// A block's range is that of the codes: gradients that differ by more than 2^12
+// within it leave small second moments at 0 beside first ones that are not, and
+// u grows far beyond 1 (its root mean square against the exact one's, eps 1e-12:
+// 1.03 at 2^12, 24 at 2^14, 390 at 2^16; the largest is bounded by eps alone).
 // Codes are made in the integer representation: |x| 2^-E 2^(14-127) has in its
 // exponent field the exponent field of the E4M3 code (subnormals included),
 // so adding 20 random bits and dropping 20 rounds it; E5M2 likewise with 29

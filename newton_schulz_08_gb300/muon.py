@@ -637,7 +637,9 @@ def adamw_state(param, bits=32):
     """Zero moments for one parameter of an AdamW step: (exp_avg, exp_avg_sq)
     float32, or with bits=8 (exp_avg, exp_avg_scale, exp_avg_sq,
     exp_avg_sq_scale): float8_e4m3fn and float8_e5m2 codes with one float32
-    scale per 256 elements."""
+    scale per 256 elements.  8 bits are for tensors whose gradients differ by
+    no more than 2^12 within 256 neighbouring elements (include/muon.h says
+    what happens beyond)."""
     if bits == 32:
         return tuple(torch.zeros(param.numel(), dtype=torch.float32, device=param.device) for _ in range(2))
     if bits != 8:
