@@ -314,7 +314,8 @@ typedef struct adamw_tensor_desc {
  *   u  = m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
  *   p <- p - (lr / (1 - beta1^t) u + lr weight_decay p mask)
  * with adam_step's mask when `cautious` is non-zero, 1 otherwise.  Float32
- * arithmetic; the scalars are formed in double and rounded once.
+ * arithmetic; the scalars are formed in double and rounded once.  Subnormal
+ * moments count; where float32 makes v 0 and eps is 0, u is m / 0.
  * 8-bit moments: a block of 256 consecutive elements of a tensor (the last
  * one may be shorter) shares a scale.  With E = floor(log2(max |x|)) of the
  * block, at least -100, the first moment's scale is 2^(E-7) and its codes are
@@ -350,7 +351,11 @@ typedef struct adamw_tensor_desc {
  * overlaps another array or grad_scale; gradients may be shared), MUON_ERR_TOO_LARGE,
  * MUON_ERR_UNSUPPORTED_DEVICE, MUON_ERR_HOST_MEMORY; MUON_ERR_CUDA (launch
  * failure).  Asynchronous on `stream`; no workspace; one launch per 400
- * tensors of the same types. */
+ * tensors of the same types.  The scalars, `step` among them, are part of the
+ * launch: a recorded call that is replayed (a CUDA graph) repeats one step's
+ * bias correction and one step's random bits, so that rounding is no longer
+ * unbiased over the replays.  Record the work before the step, or renew the
+ * recording for each step. */
 muon_status_t adamw_step(const adamw_tensor_desc* tensors, int n_tensors, double beta1, double beta2, double eps,
                          int cautious, int64_t step, uint64_t seed, const float* grad_scale, void* stream);
 
@@ -380,10 +385,12 @@ void adamw_plan_destroy(adamw_plan* plan);
  *   lower index (top_logprobs: their z - lse).
  * Sums are float32.  Entries of -inf (masked tokens) have probability 0 and
  * contribute nothing.  A row of -inf only has lse = logprobs = top_logprobs =
- * -inf and entropy 0.  A row with NaN or +inf has NaN results (NaN ranks
- * below every number).  A negative target marks a row that is left out: its
- * logits do not matter, its outputs are 0 and its top_ids -1.  A target >=
- * vocab gives NaN as logprobs of that row.
+ * -inf and entropy 0.  logprobs, top_logprobs and entropy come from differences
+ * with the row's largest logit: their errors go with those, not with |z| (lse
+ * has the rounding of its own size), and no logprob is above 0.  A row with NaN
+ * or +inf has NaN results (NaN ranks below every number).  A negative target
+ * marks a row that is left out: its logits do not matter, its outputs are 0 and
+ * its top_ids -1.  A target >= vocab gives NaN as logprobs of that row.
  *   targets                        rows;
  *   logprobs, lse, entropy         rows floats each, written;
  *   top_logprobs, top_ids          rows x top, written (top = 0: may be NULL).
@@ -400,10 +407,14 @@ muon_status_t token_logprobs(const void* logits, int dtype, int64_t rows, int64_
  * respect to logprobs and (optionally) entropy:
  *   grad_j = scale * (gl (1[j = target] - p_j) - ge p_j (log p_j + entropy))
  * in `dtype`, rounded once; 0 for rows that are left out (target < 0,
- * whatever their logits are) and for entries of -inf; NaN for a row whose target is >= vocab.
+ * whatever their logits are), for rows of -inf only and for entries of -inf,
+ * the target apart (an entry of -inf that is the target has scale * gl); NaN for
+ * a row whose target is >= vocab.
  *   lse, entropy      as token_logprobs wrote them for the same logits,
  *                     targets and scale (entropy is read with grad_entropy
- *                     only and may be NULL otherwise);
+ *                     only and may be NULL otherwise).  Up to |lse| = 1024
+ *                     its rounding is a probability's (2^-14 of it at
+ *                     most); a row beyond is read twice more for its own sums;
  *   grad_logprobs     rows floats; grad_entropy rows floats or NULL;
  *   grad              rows x vocab, row pitch grad_stride elements; it may be
  *                     `logits` itself (same pointer and pitch), else it
@@ -447,7 +458,9 @@ muon_status_t token_logprobs_loss(const void* logits, int dtype, int64_t rows, i
  * Limits: 1 <= experts <= 1024, 1 <= top <= experts, groups >= 1 divides
  * tokens, tokens * top < 2^31.  tokens = 0 gives zeros.  Sums are float32 in
  * a fixed order: equal calls give equal bits.  Rows with NaN or +inf give
- * NaN; entries of -inf have probability 0; a row of -inf only is NaN.
+ * NaN; entries of -inf have probability 0; a row of -inf only is NaN.  Scores
+ * of any finite size do: a row's probabilities come from differences with its
+ * largest one (z is infinite where a lse^2 leaves float32's range).
  * Written arrays overlap nothing else.  Asynchronous on `stream`.  Returns
  * MUON_OK, MUON_ERR_INVALID_ARG, MUON_ERR_MISALIGNED, MUON_ERR_ALIASING,
  * MUON_ERR_WORKSPACE_TOO_SMALL, MUON_ERR_TOO_LARGE,
