@@ -84,6 +84,7 @@ struct LogprobParams {
   int segment;      // logprob_loss: vectors that a CTA has room for
   int group;        // and of them in each of its four groups of copies, a multiple of the threads
   int chunks;       // logprob_grad: CTAs per row
+  float near;       // largest exponent of a reference in the short form for bfloat16 (0: none does)
   uint32_t floor2;  // two bfloat16 numbers whose exponent is -2 kNear, for the short form of gradients
 };
 
@@ -233,8 +234,8 @@ __device__ __forceinline__ void accumulate(float2& s, float2& w, const float (&x
 // K is rounded, by up to 2^-9; that goes into every exponent alike and is taken
 // out of the sums (settle) and of the gradient's factors (near_of).
 template <bool BF16>
-__device__ __forceinline__ bool near_fits(float ref, float c2) {
-  return !BF16 || (fabsf(ref * c2) < kNear && c2 >= kNearScale);
+__device__ __forceinline__ bool near_fits(const LogprobParams& P, float ref, float c2) {
+  return !BF16 || fabsf(__fmul_rn(-ref, c2)) < P.near;
 }
 
 // 2^d for |d| <= 2^-8.
@@ -267,12 +268,18 @@ __device__ __forceinline__ void accumulate_near(float2& s, float2& w, uint4 q, f
   }
 }
 
-// Sums of accumulate_near against a.m become what they stand for: the exponents
-// were less by d = -(ref c2 + K), which one fused operation gives exactly.
+// What the exponents of accumulate_near were short of, -(ref c2 + K): one fused
+// operation gives it exactly.
+template <bool BF16>
+__device__ __forceinline__ float near_residue(float ref, float c2) {
+  return BF16 ? -fmaf(ref, c2, __fmul_rn(-ref, c2)) : 0.0f;
+}
+
+// Sums of accumulate_near against a.m become what they stand for.
 template <bool BF16>
 __device__ __forceinline__ void settle(Sums& a, float c2) {
   if constexpr (BF16) {
-    const float ref = reference(a.m), d = -fmaf(ref, c2, __fmul_rn(-ref, c2)), f = ex2_small(d);
+    const float d = near_residue<BF16>(reference(a.m), c2), f = ex2_small(d);
     a.w = fmaf(d, a.s, a.w) * f;
     a.s *= f;
   }
@@ -295,12 +302,14 @@ struct RowStats {
   bool empty;  // every entry -inf
 };
 
-__device__ __forceinline__ RowStats stats_of(const Sums& a, float scale) {
+// d: of sums that are not settled.  It multiplies S and moves W / S alike.
+__device__ __forceinline__ RowStats stats_of(const Sums& a, float scale, float d = 0.0f) {
   RowStats r;
   r.empty = a.s == 0.0f;
   r.m = reference(a.m);
   r.log_s = r.empty ? 0.0f : logf(a.s);
   r.entropy = r.empty ? 0.0f : r.log_s - kLn2 * (a.w / a.s);
+  r.log_s = fmaf(d, kLn2, r.log_s);
   r.lse = r.empty ? -INFINITY : fmaf(r.m, scale, r.log_s);
   return r;
 }
@@ -375,12 +384,12 @@ struct NearGrad {
 };
 
 template <bool BF16>
-__device__ __forceinline__ NearGrad near_of(const RowGrad& g, float scale) {
+__device__ __forceinline__ NearGrad near_of(const LogprobParams& P, const RowGrad& g) {
   NearGrad h;
   const float l = g.log_s * kLog2e;
-  h.c2 = scale * kLog2e;
+  h.c2 = P.scale * kLog2e;
   h.K = -fmaf(g.m, h.c2, l);
-  h.fits = !BF16 || (fabsf(h.K) < kNear && h.c2 >= kNearScale);
+  h.fits = !BF16 || fabsf(h.K) < P.near;
   // log2 p_j is t + d, as K is rounded; the difference from m c2 is exact but for a rounding of the size of l
   const float d = -(fmaf(g.m, h.c2, h.K) + l), f = ex2_small(d), a2 = g.a * kLn2;
   h.a2 = a2 * f;
@@ -661,9 +670,9 @@ __global__ void __launch_bounds__(kWarpThreads, NV == 16 ? 2 : NV == 8 ? 3 : 4) 
         a.w += __shfl_xor_sync(0xFFFFFFFFu, a.w, d);
       }
     };
-    const bool near = near_fits<BF16>(reference(a.m), c2);
+    const bool near = near_fits<BF16>(P, reference(a.m), c2);
+    float d = near_residue<BF16>(reference(a.m), c2);
     add_up(a, [&](float2& s, float2& w, uint4 v) { accumulate_near<BF16>(s, w, v, reference(a.m), c2); });
-    settle<BF16>(a, c2);
     if (BF16 && __any_sync(0xFFFFFFFFu, !near && on)) {
       Sums far = a;
       add_up(far, [&](float2& s, float2& w, uint4 v) {
@@ -671,13 +680,13 @@ __global__ void __launch_bounds__(kWarpThreads, NV == 16 ? 2 : NV == 8 ? 3 : 4) 
         unpack<BF16>(v, x);
         accumulate(s, w, x, reference(a.m), c2);
       });
-      if (!near) a = far;
+      if (!near) a = far, d = 0.0f;
     }
     if (MODE != kBackward) {
-      r = stats_of(a, P.scale);
+      r = stats_of(a, P.scale, d);
     } else if (log_s_is_lost(r)) {
       const float entropy = r.entropy;
-      r = stats_of(a, P.scale);
+      r = stats_of(a, P.scale, d);
       r.entropy = entropy;
     }
   }
@@ -733,7 +742,7 @@ __global__ void __launch_bounds__(kWarpThreads, NV == 16 ? 2 : NV == 8 ? 3 : 4) 
     if (!in) return;
     RowGrad g{};
     if (on) g = grad_of(P, r, gl, ge, target);
-    const NearGrad near = near_of<BF16>(g, P.scale);
+    const NearGrad near = near_of<BF16>(P, g);
     const long long out = row * P.grad_stride;
     const RowVectors<BF16> O(P.grad, out, P.vocab);
     uint4* const o = reinterpret_cast<uint4*>(const_cast<unsigned char*>(O.base));
@@ -1153,7 +1162,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 8 : 3) logprob_loss(
     a.s = sums.x;
     a.w = sums.y;
     settle<BF16>(a, c2);
-    if (!(near_fits<BF16>(a.m, c2) && a.s >= 0.5f && a.s < 0x1p60f)) {
+    if (!(near_fits<BF16>(P, a.m, c2) && a.s >= 0.5f && a.s < 0x1p60f)) {
       __syncthreads();  // the scratch arrays have been read
       a = sums_again<BF16, THREADS>(P.x, base, j0, j1, c2, scratch[turn], pair_scratch[turn]);
     }
@@ -1199,7 +1208,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 8 : 3) logprob_loss(
     }
 
     const RowGrad g = grad_of(P, r, P.gl[row], P.ge ? P.ge[row] : 0.0f, target);
-    const NearGrad near = near_of<BF16>(g, P.scale);
+    const NearGrad near = near_of<BF16>(P, g);
     if (same && near.fits) {
 #pragma unroll 1
       for (int group = 0; group < 4; ++group) {
@@ -1334,7 +1343,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprob_score(const _
     sums.w += __shfl_xor_sync(0xFFFFFFFFu, sums.w, d);
   }
   settle<BF16>(sums, c2);
-  if (!near_fits<BF16>(reference(sums.m), c2)) sums.s = NAN;
+  if (!near_fits<BF16>(P, reference(sums.m), c2)) sums.s = NAN;
   // A warp that saw masked entries alone has m = -inf and no sum; any other sum
   // out of range means that its reference was too far off, or too large.
   if (lane == 0) warp_sums[warp] = sums;
@@ -1660,6 +1669,7 @@ muon_status_t run(const void* logits, int dtype, int64_t rows, int64_t vocab, in
   P.vocab = static_cast<int>(vocab);
   P.top = score ? top : 0;
   P.scale = scale;
+  P.near = scale * kLog2e >= kNearScale ? kNear : 0.0f;
   const float floor = -2.0f * kNear / (scale * kLog2e);  // rounded to bfloat16 towards 0
   uint32_t bits = 0;
   std::memcpy(&bits, &floor, 4);
