@@ -412,8 +412,8 @@ muon_status_t token_logprobs(const void* logits, int dtype, int64_t rows, int64_
  * a row whose target is >= vocab.
  *   lse, entropy      as token_logprobs wrote them for the same logits,
  *                     targets and scale (entropy is read with grad_entropy
- *                     only and may be NULL otherwise).  Up to |lse| = 1024
- *                     its rounding is a probability's (2^-14 of it at
+ *                     only and may be NULL otherwise).  Up to |lse| = 4096
+ *                     its rounding is a probability's (2^-13 of it at
  *                     most); a row beyond is read twice more for its own sums;
  *   grad_logprobs     rows floats; grad_entropy rows floats or NULL;
  *   grad              rows x vocab, row pitch grad_stride elements; it may be

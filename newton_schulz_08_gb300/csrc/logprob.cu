@@ -58,7 +58,7 @@ constexpr int kLossStatic = 12 * 1024;    // shared memory of a logprob_loss CTA
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kFloor = -1000.0f;        // least exponent
-constexpr float kLost = 1024.0f;          // an lse beyond it may be off by 2^-14 and more
+constexpr float kLost = 4096.0f;          // an lse beyond it may be off by 2^-12 and more
 constexpr float kNear = 65536.0f;         // largest exponent of a reference in the short form for bfloat16
 constexpr float kMasked = -1e30f;         // its floor for logits in sums
 constexpr float kNearScale = 1e-24f;      // and least scale: the floor's exponent is -10^6
@@ -350,7 +350,8 @@ __device__ __forceinline__ RowStats stats_from_lse(const LogprobParams& P, long 
 
 // Whether lse is so large beside log S (a row far from zero, masked as a whole,
 // or at a low temperature) that probabilities taken from it would be off by its
-// rounding: beyond kLost by more than 2^-14 of themselves, in the end altogether.
+// rounding: up to kLost by 2^-13 of themselves at most (a thirty-second of what
+// rounding to bfloat16 may do), beyond by more, in the end altogether.
 // An infinite lse is that of an empty row or a product beyond float32's range.
 __device__ __forceinline__ bool log_s_is_lost(const RowStats& r) { return fabsf(r.lse) > kLost; }
 

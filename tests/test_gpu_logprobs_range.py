@@ -13,7 +13,8 @@ largest logit), and for the entropy twice the first with the share-weighted
 square of log p, as p log p moves by |log p| times what log p does:
 2^-20 (1 + log V + sum p (log p)^2 + (log V)^2).  A probability is relatively
 off by 2^-20 (1 + |log p| + log V).  The backward pass takes log S from lse:
-2^-22 |lse| more up to 1024, beyond which it takes log S again.  Gradients
+2^-22 |lse| more, at most 2^-12: 2^-24 of |lse| up to 4096, beyond which it
+takes log S again.  Gradients
 in bfloat16, of 8 significant bits, add half a spacing: 2^-8."""
 
 import numpy as np
