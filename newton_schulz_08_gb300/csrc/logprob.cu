@@ -19,6 +19,13 @@
 //     rows are few); the CTAs exchange their sums through distributed shared
 //     memory.  Rows beyond 208 KB are scored and then read again.
 // The backward pass alone knows the sums and is elementwise (logprob_grad).
+// Long rows are added up in parts of 16 to 52 entries a lane, and then the parts;
+// and where sums show entries far above their reference, a larger one is taken and
+// a score's batch, or the loss's row in shared memory, added up again.  2^t t of an
+// entry with t far above 0 carries a rounding of that size into the entropy, and
+// small shares are lost beside a large one in a long chain: entropies of 130000
+// logits with few large shares were 5e-6 off so (rms; the largest 5e-5), and are
+// 9e-8 (8e-7).
 // Entries of -inf: exponents are held above -1000, where 2^t is 0 and 0 * t
 // stays 0.
 #include <cooperative_groups.h>
@@ -59,6 +66,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kFloor = -1000.0f;        // least exponent
 constexpr float kLost = 4096.0f;          // an lse beyond it may be off by 2^-12 and more
+constexpr float kAbove = 6.0f;            // mean exponent that asks for a larger reference
+constexpr float kAboveSum = 64.0f;        // and the sum of a batch: an entry of exponent 6, or many
 constexpr float kNear = 65536.0f;         // largest exponent of a reference in the short form for bfloat16
 constexpr float kMasked = -1e30f;         // its floor for logits in sums
 constexpr float kNearScale = 1e-24f;      // and least scale: the floor's exponent is -10^6
@@ -294,6 +303,14 @@ __device__ __forceinline__ Sums merge(const Sums& a, const Sums& b, float c2) {
   r.s = a.s * fa + b.s * fb;
   r.w = fmaf(a.s, ta, a.w) * fa + fmaf(b.s, tb, b.w) * fb;
   return r;
+}
+
+// Sums that accumulate_near has taken against `from` become those against `to`.
+template <bool BF16>
+__device__ __forceinline__ void move_reference(float2& s, float2& w, float from, float to, float c2) {
+  const float t = max_nan((from - to) * c2 + (near_residue<BF16>(from, c2) - near_residue<BF16>(to, c2)), kFloor), f = ex2(t);
+  w = __fmul2_rn(__ffma2_rn(s, make_float2(t, t), w), make_float2(f, f));
+  s = __fmul2_rn(s, make_float2(f, f));
 }
 
 // What follows from a row's sums.
@@ -990,10 +1007,16 @@ __device__ __noinline__ Sums sums_again(const void* x, long long base, int first
   Sums a{};
   a.m = cta_reduce<THREADS>(m, [](float p, float q) { return fmaxf(p, q); }, scratch);
   float2 s{}, w{};
+  constexpr int kPass = 16 * 2 * THREADS;
+  for (int j0 = first + static_cast<int>(threadIdx.x); j0 < last; j0 += kPass) {
+    float2 sp{}, wp{};
 #pragma unroll 2
-  for (int j = first + static_cast<int>(threadIdx.x); j < last; j += 2 * THREADS) {
-    const float v[2] = {at<BF16>(x, base + j), j + THREADS < last ? at<BF16>(x, base + j + THREADS) : -INFINITY};
-    accumulate(s, w, v, reference(a.m), c2);
+    for (int j = j0; j < min(last, j0 + kPass); j += 2 * THREADS) {
+      const float v[2] = {at<BF16>(x, base + j), j + THREADS < last ? at<BF16>(x, base + j + THREADS) : -INFINITY};
+      accumulate(sp, wp, v, reference(a.m), c2);
+    }
+    s = __fadd2_rn(s, sp);
+    w = __fadd2_rn(w, wp);
   }
   const float2 sums = cta_sum2<THREADS>(make_float2(s.x + s.y, w.x + w.y), pair_scratch);
   a.s = sums.x;
@@ -1035,6 +1058,32 @@ __device__ __forceinline__ RowPart<BF16> part_of(const LogprobParams& P, long lo
   return p;
 }
 
+// Sums of a CTA's part of a row in shared memory against its largest entry.
+template <bool BF16, int THREADS>
+__device__ __noinline__ Sums segment_again(const uint4* q, int n, float c2, float* scratch, float2* pair_scratch) {
+  VecMax<BF16> largest;
+  for (int i = threadIdx.x; i < n; i += THREADS) largest.add(q[i]);
+  Sums a{};
+  a.m = cta_reduce<THREADS>(largest.value(), [](float x, float y) { return fmaxf(x, y); }, scratch);
+  float2 s{}, w{};
+#pragma unroll 1
+  for (int i0 = threadIdx.x; i0 < n; i0 += 8 * THREADS) {
+    float2 sp{}, wp{};
+#pragma unroll 2
+    for (int i = i0; i < min(n, i0 + 8 * THREADS); i += THREADS) {
+      float x[kPer<BF16>];
+      unpack<BF16>(q[i], x);
+      accumulate(sp, wp, x, reference(a.m), c2);
+    }
+    s = __fadd2_rn(s, sp);
+    w = __fadd2_rn(w, wp);
+  }
+  const float2 sums = cta_sum2<THREADS>(make_float2(s.x + s.y, w.x + w.y), pair_scratch);
+  a.s = sums.x;
+  a.w = sums.y;
+  return a;
+}
+
 // A cluster takes one row after the other (persistent).  A CTA's part of a
 // row lies in its shared memory as vectors in four groups; a thread's vectors
 // are the ones it copies, so it works on a group without waiting for other
@@ -1050,6 +1099,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 8 : 3) logprob_loss(
   __shared__ Exchange X;
   __shared__ __align__(16) TopScratch<TOP ? THREADS : 32, TOP ? 4 : 1> S;
   constexpr int kN = kPer<BF16>;
+  constexpr bool kParts = THREADS == 256;  // 128 threads have at most 16 vectors each
   const cg::cluster_group cluster = cg::this_cluster();
   const int ranks = 1 << P.log_ranks, rank = blockIdx.x & (ranks - 1);
   const int t = threadIdx.x;
@@ -1135,7 +1185,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 8 : 3) logprob_loss(
     if (t == 0 && rank == 0 && target < P.vocab) x_target = at<BF16>(P.x, base + target);
 
     // Sums against the largest of the first vectors, which is near enough to
-    // the row's largest entry unless S says otherwise.
+    // the row's largest entry unless S or W says otherwise.
     float2 s{}, w{};
     Sums a{};
     float own = -INFINITY;
@@ -1147,11 +1197,16 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 8 : 3) logprob_loss(
       asm volatile("cp.async.wait_group 3;" ::: "memory");
       const int end = min(p.n, (group + 1) * P.group);
       VecMax<BF16> chunk;
+      float2 sg{}, wg{};
 #pragma unroll 2
       for (int i = group * P.group + t; i < end; i += THREADS) {
         const uint4 v = q[i];
         if (TOP) chunk.add(v);
-        accumulate_near<BF16>(s, w, v, a.m, c2);
+        accumulate_near<BF16>(kParts ? sg : s, kParts ? wg : w, v, a.m, c2);
+      }
+      if constexpr (kParts) {
+        s = __fadd2_rn(s, sg);
+        w = __fadd2_rn(w, wg);
       }
       if constexpr (TOP) {
         S.chunk_max[group][t] = chunk.value();
@@ -1163,9 +1218,9 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 8 : 3) logprob_loss(
     a.s = sums.x;
     a.w = sums.y;
     settle<BF16>(a, c2);
-    if (!(near_fits<BF16>(P, a.m, c2) && a.s >= 0.5f && a.s < 0x1p60f)) {
+    if (!(near_fits<BF16>(P, a.m, c2) && a.s >= 0.5f && a.s < 0x1p60f && a.w <= kAbove * a.s)) {
       __syncthreads();  // the scratch arrays have been read
-      a = sums_again<BF16, THREADS>(P.x, base, j0, j1, c2, scratch[turn], pair_scratch[turn]);
+      a = segment_again<BF16, THREADS>(q, p.n, c2, scratch[turn], pair_scratch[turn]);
     }
     if (ranks > 1) {
       if (t < ranks) cluster.map_shared_rank(&X, t)->sums[turn][rank] = a;
@@ -1258,9 +1313,40 @@ __global__ void __launch_bounds__(THREADS, THREADS == 128 ? 8 : 3) logprob_loss(
 
 // ------------------------------------------------- scores of long rows (CTAs)
 
+// A warp's sums of a row up to a batch, and of the batch, against m.
+struct BatchSums {
+  float2 s, w, sb, wb;
+  float m;
+};
+
+// The batch, vectors first, first + THREADS, ... before `end`, held entries far
+// above m: a new reference, and the batch again.
+template <bool BF16, int THREADS>
+__device__ __forceinline__ BatchSums batch_again(BatchSums g, const uint4* src, int first, int end, float c2) {
+  VecMax<BF16> largest;
+  for (int i = first; i < end; i += THREADS) largest.add(src[i]);
+  float m = fmaxf(g.m, largest.value());
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+  if (!(m > g.m)) return g;
+  move_reference<BF16>(g.s, g.w, reference(g.m), m, c2);
+  g.m = m;
+  g.sb = g.wb = make_float2(0.0f, 0.0f);
+  for (int i = first; i < end; i += THREADS) accumulate_near<BF16>(g.sb, g.wb, src[i], m, c2);
+  return g;
+}
+
+// As a call it leaves the kernels with alternatives their registers (16384 x 50304
+// bfloat16 with 5: 282 us, 292 in line); the others are faster with it in line (239 and 257).
+template <bool BF16, int THREADS>
+__device__ __noinline__ BatchSums batch_again_called(BatchSums g, const uint4* src, int first, int end, float c2) {
+  return batch_again<BF16, THREADS>(g, src, first, end, c2);
+}
+
 // One row per CTA, or per cluster where rows are few.  The logits pass through
 // registers, two batches of four vectors a thread.  Each warp adds up against
-// the largest entry of its own first batch.
+// the largest entry of its own first batch, or of a later one that stands far
+// above it.
 template <bool BF16, int THREADS, bool TOP>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprob_score(const __grid_constant__ LogprobParams P) {
   constexpr int kWarps = THREADS / 32, kU = 4, kBatch = kU * THREADS;
@@ -1323,14 +1409,22 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprob_score(const _
     for (int u = 0; u < kU; ++u)
       if (i + kBatch + u * THREADS < n) b[u] = load_once(src + i + kBatch + u * THREADS);
     VecMax<BF16> largest;
+    float2 sb{}, wb{};
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       if (i + u * THREADS < n) {
         if (TOP) largest.add(a[u]);
-        accumulate_near<BF16>(s, w, a[u], reference(sums.m), c2);
+        accumulate_near<BF16>(sb, wb, a[u], reference(sums.m), c2);
       }
       a[u] = b[u];
     }
+    if (__any_sync(0xFFFFFFFFu, fmaxf(sb.x, sb.y) > kAboveSum)) {
+      constexpr auto again = TOP ? batch_again_called<BF16, THREADS> : batch_again<BF16, THREADS>;
+      const BatchSums g = again({s, w, sb, wb, sums.m}, src, i, min(n, (k + 1) * kBatch), c2);
+      s = g.s, w = g.w, sb = g.sb, wb = g.wb, sums.m = g.m;
+    }
+    s = __fadd2_rn(s, sb);
+    w = __fadd2_rn(w, wb);
     if constexpr (TOP) {
       float* const chunk = &S.chunk_max[k >> log_chunk][t];
       *chunk = (k & ((1 << log_chunk) - 1)) == 0 ? largest.value() : fmaxf(*chunk, largest.value());
