@@ -726,8 +726,9 @@ def adamw_step(params, grads, states, step, lr=1e-3, beta1=0.9, beta2=0.999, eps
     tensor).  lr and weight_decay: one number, or one per tensor.  grad_scale:
     a one-element float32 CUDA tensor that the gradients are multiplied with
     (a clipping factor).  seed: of the stochastic rounding of 8-bit states and
-    bfloat16 parameters.  See adamw_step in include/muon.h; AdamW keeps what
-    is the same in every step."""
+    bfloat16 parameters.  A call recorded in a CUDA graph repeats its own step
+    number.  See adamw_step in include/muon.h; AdamW keeps what is the same in
+    every step (this call describes every tensor anew)."""
     arr, n, every = _adamw_descs(params, grads, states, lr, weight_decay)
     if n == 0:
         return
@@ -780,7 +781,8 @@ class AdamW:
         _check(lib().adamw_plan_set_rates(self._plan, double(*lr), double(*wd)), "AdamW.set_rates")
 
     def set_grads(self, grads):
-        """Other gradient tensors from the next step on."""
+        """Other gradient tensors from the next step on.  Every tensor is
+        checked again: gradients that stay in place are given once."""
         n, grads = len(self.params), list(grads)
         if len(grads) != n or any(g.numel() != p.numel() or not g.is_contiguous()
                                   for g, p in zip(grads, self.params)):
