@@ -544,6 +544,121 @@ muon_status_t fp8_mm_backward(const void* g, const void* x_f8, const void* w_f8,
                               void* grad_x, void* grad_w, void* g_f8, int64_t M, int64_t N, int64_t K,
                               void* workspace, size_t workspace_bytes, void* stream);
 
+/* A matrix in 4-bit floating point with block scales, an operand of fp4_mm:
+ * rows x cols entries, contracted along cols.  Caller-owned DEVICE memory.
+ *   codes   fp4_codes_size(rows, cols) bytes: E2M1 (1 sign, 2 exponent, 1
+ *           fraction bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6), two per byte, the even
+ *           column in the low half; a row takes ceil(cols / 32) * 16 bytes
+ *           (codes past its end are 0);
+ *   scales  fp4_scales_size(rows, cols, block) bytes: one per row and `block`
+ *           columns, E8M0 (2^(byte - 127); 255 is NaN) for blocks of 32, E4M3
+ *           without a sign for blocks of 16.  The scale of row r and block b is
+ *           at ((r / 128) * T + b / 4) * 512 + (r % 32) * 16 + (r % 128) / 32 * 4
+ *           + b % 4, T = ceil(cols / 256) * 64 / block (zeros where there is
+ *           no block);
+ *   scale   blocks of 16: two floats, the tensor's factor (a power of two) and
+ *           the largest finite |x| it comes from; blocks of 32: NULL.
+ * An entry is code * block scale * factor.  codes and scales are 16-byte
+ * aligned. */
+typedef struct fp4_matrix {
+  void* codes;
+  void* scales;
+  float* scale;
+  int64_t rows, cols;  /* >= 0 */
+  int32_t block;       /* 32 or 16 */
+  int32_t reserved;    /* 0 */
+} fp4_matrix;
+size_t fp4_codes_size(int64_t rows, int64_t cols);
+size_t fp4_scales_size(int64_t rows, int64_t cols, int block);
+
+/* Quantises x (rows x cols of `dtype`, row pitch row_stride elements, any
+ * alignment of the element) to 4 bits: `along` is x itself (rows x cols, blocks
+ * along a row), `across` its transpose (cols x rows, blocks down a column); one
+ * of them may be NULL, both cost one read of x.
+ *   block 32: a block's scale is the smallest power of two that is at least
+ *     max |x| / 6 (at least 2^-127);
+ *   block 16: the tensor's factor 2^k is the smallest with max |x| <= 2688 2^k
+ *     over its finite entries (k >= -127), a block's scale the E4M3 number
+ *     nearest to q = fl32(max |x| / 6) / 2^k; both targets have the same scale
+ *     array.
+ * A code is fl32(x / scale) rounded to nearest even, magnitudes above 6 to 6.
+ * With `stochastic` it is rounded up with the probability of the remainder (16
+ * bits of it), and a block's E4M3 scale is the smallest that is at least q, so
+ * that nothing is cut off and the values are right in the mean.  The random bits of entry
+ * (r, c) of a target depend on (seed, target, r, c) alone: with mix as in
+ * adamw_step, key = mix(mix(lo(seed) + 0x9E3779B1 a) ^ hi(seed)), a = 1 for along
+ * and 0 for across, j = r ceil(cols / 2) + c / 2 (the target's cols),
+ *   h = mix(0x9E3779B1 lo(j) + key + 0x6A09E667 hi(j)),
+ * its low half for even c and its high half for odd c.
+ * A block with an infinite or NaN entry has a NaN scale, and codes 0.
+ * rows = 0 or cols = 0 is a no-op.  Asynchronous on `stream`; nothing is
+ * allocated; equal calls give equal bits.  Returns MUON_OK,
+ * MUON_ERR_INVALID_ARG, MUON_ERR_MISALIGNED, MUON_ERR_ALIASING,
+ * MUON_ERR_TOO_LARGE, MUON_ERR_UNSUPPORTED_DEVICE, MUON_ERR_HOST_MEMORY or
+ * MUON_ERR_CUDA. */
+muon_status_t fp4_quantize(const void* x, int dtype, int64_t rows, int64_t cols, int64_t row_stride,
+                           const fp4_matrix* along, const fp4_matrix* across, int stochastic, uint64_t seed,
+                           void* stream);
+
+/* The numbers that a quantised matrix stands for, rows x cols of `dtype` with
+ * row pitch out_stride.  They are exact in bfloat16 too, down to its subnormal
+ * numbers. */
+muon_status_t fp4_values(const fp4_matrix* q, void* out, int dtype, int64_t out_stride, void* stream);
+
+/* Product out = a b^T of two matrices of equal cols and block: out is a->rows x
+ * b->rows of `dtype` (bfloat16 or float32), row pitch out_stride elements, any
+ * alignment of the element.  Products are exact and accumulated in fp32; the
+ * sum is rounded once.  cols = 0 gives zeros.  A NaN scale makes its row (column)
+ * of out NaN.  out and workspace overlap nothing else.
+ *   workspace  at least 256 bytes, 256-byte aligned, holding the device status
+ *              word (muon_device_status).
+ * Asynchronous on `stream`; nothing is allocated; equal calls give equal bits.
+ * Returns MUON_OK, MUON_ERR_INVALID_ARG, MUON_ERR_MISALIGNED,
+ * MUON_ERR_ALIASING, MUON_ERR_WORKSPACE_TOO_SMALL, MUON_ERR_TOO_LARGE,
+ * MUON_ERR_UNSUPPORTED_DEVICE, MUON_ERR_HOST_MEMORY or MUON_ERR_CUDA. */
+muon_status_t fp4_mm(const fp4_matrix* a, const fp4_matrix* b, void* out, int dtype, int64_t out_stride,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* Layer norm over the rows of x (rows x cols of `dtype`, row pitch row_stride
+ * elements, any alignment of the element):
+ *   s = x + residual, rounded to `dtype` (residual NULL: s = x),
+ *   y = (s - mean) rstd weight + bias,  rstd = 1 / sqrt(mean((s - mean)^2) + eps).
+ * Sums and statistics are float32, the variance of differences with the mean.
+ *   residual, sum  both or neither: s is written to sum (it may be x or
+ *                  residual itself: same pointer and pitch);
+ *   weight, bias   cols of weight_dtype each, or NULL (1 and 0);
+ *   mean, rstd     rows floats each, written.
+ * 1 <= cols <= 2^24; rows = 0 is a no-op; eps >= 0.  A row with NaN or an
+ * infinity is NaN, and so is a constant row where eps is 0.  y may be x itself
+ * where there is no residual (same pointer and pitch); written arrays overlap
+ * nothing else.  Asynchronous on `stream`; no workspace.  Returns MUON_OK,
+ * MUON_ERR_INVALID_ARG, MUON_ERR_MISALIGNED, MUON_ERR_ALIASING,
+ * MUON_ERR_TOO_LARGE, MUON_ERR_UNSUPPORTED_DEVICE, MUON_ERR_HOST_MEMORY or
+ * MUON_ERR_CUDA. */
+muon_status_t layer_norm(const void* x, int dtype, int64_t rows, int64_t cols, int64_t row_stride,
+                         const void* residual, int64_t residual_stride, const void* weight, const void* bias,
+                         int weight_dtype, float eps, void* y, int64_t y_stride, void* sum, int64_t sum_stride,
+                         float* mean, float* rstd, void* stream);
+
+/* Its backward pass: with x the normalised rows (s above), mean and rstd as
+ * layer_norm wrote them, grad the gradient of y,
+ *   gw = grad weight,  xhat = (x - mean) rstd,
+ *   grad_x = rstd (gw - mean(gw) - xhat mean(gw xhat)) + grad_sum,
+ *   grad_weight = sum over rows of grad xhat,  grad_bias = sum over rows of grad.
+ * grad_sum (or NULL) is the gradient that reaches s by another way; grad_x,
+ * rounded once to `dtype`, is that of both x and residual, and may be grad or
+ * grad_sum itself (same pointer and pitch).  grad_weight and grad_bias are cols
+ * floats each, or NULL.  Sums are float32 in a fixed order: equal calls give
+ * equal bits.  rows = 0 writes zeros to grad_weight and grad_bias.
+ *   workspace  layer_norm_backward_workspace_size() bytes, 256-byte aligned.
+ * Limits, errors (and MUON_ERR_WORKSPACE_TOO_SMALL) and stream as layer_norm. */
+muon_status_t layer_norm_backward(const void* grad, int64_t grad_stride, const void* x, int64_t row_stride, int dtype,
+                                  int64_t rows, int64_t cols, const float* mean, const float* rstd,
+                                  const void* weight, int weight_dtype, const void* grad_sum,
+                                  int64_t grad_sum_stride, void* grad_x, int64_t grad_x_stride, float* grad_weight,
+                                  float* grad_bias, void* workspace, size_t workspace_bytes, void* stream);
+size_t layer_norm_backward_workspace_size(int64_t rows, int64_t cols);
+
 /* Assigns each matrix of a bank to one of `world` ranks, for running the
  * step on several GPUs, one process per GPU, each updating only the matrices
  * it owns (every matrix's step depends on that matrix alone, so no data is

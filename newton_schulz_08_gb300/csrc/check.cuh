@@ -46,4 +46,7 @@ cudaError_t check_failures_adam(int* out);
 cudaError_t check_failures_adamw(int* out);
 cudaError_t check_failures_logprob(int* out);
 cudaError_t check_failures_balance(int* out);
+cudaError_t check_failures_fp4(int* out);
+cudaError_t check_failures_fp4_mm(int* out);
+cudaError_t check_failures_layernorm(int* out);
 }  // namespace muon

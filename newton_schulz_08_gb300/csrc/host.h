@@ -2,6 +2,8 @@
 // overlap check of a call's byte ranges.
 #pragma once
 
+#include <cuda.h>
+
 #include <algorithm>
 #include <cstdint>
 #include <vector>
@@ -13,6 +15,15 @@ namespace muon {
 // MUON_OK and the SM count when the current device is compute capability
 // 10.3, else the error to return (muon_capi.cu).
 muon_status_t device_sms(int& sms);
+
+// The knobs of muon_set_debug that other units' kernels follow (muon_capi.cu).
+long long wait_budget();
+int inject_stall();
+
+// 2-D tensor map of rows x cols elements of 1 or 4 bytes (row pitch in bytes),
+// with or without 128-byte swizzle; false on failure (muon_capi.cu).
+bool encode_map_2d(CUtensorMap* map, const void* base, int size, uint64_t cols, uint64_t rows, uint64_t pitch,
+                   uint32_t box_cols, uint32_t box_rows, bool swizzle);
 
 struct Span {
   uintptr_t lo, hi;  // [lo, hi)

@@ -835,6 +835,19 @@ using namespace muon;
 
 // For the entry points of the other units (host.h).
 muon_status_t muon::device_sms(int& sms) { return muon::current_device(sms); }
+long long muon::wait_budget() { return g_wait_budget.load(); }
+int muon::inject_stall() { return g_inject_stall.load(); }
+bool muon::encode_map_2d(CUtensorMap* map, const void* base, int size, uint64_t cols, uint64_t rows, uint64_t pitch,
+                         uint32_t box_cols, uint32_t box_rows, bool swizzle) {
+  auto enc = tensor_map_encoder();
+  if (!enc || g_fail_encode.load()) return false;
+  const cuuint64_t dims[2] = {cols, rows}, strides[1] = {pitch};
+  const cuuint32_t box[2] = {box_cols, box_rows}, estr[2] = {1, 1};
+  return enc(map, size == 4 ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base),
+             dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 extern "C" {
 
@@ -1070,7 +1083,8 @@ int muon_debug_check_failures(long long* failures) {
   long long total = 0;
   for (cudaError_t (*f)(int*) : {&check_failures_elementwise, &check_failures_gemm, &check_failures_fp8,
                                  &check_failures_adam, &check_failures_adamw, &check_failures_logprob,
-                                 &check_failures_balance}) {
+                                 &check_failures_balance, &check_failures_fp4, &check_failures_fp4_mm,
+                                 &check_failures_layernorm}) {
     int v = 0;
     if (f(&v) != cudaSuccess) {
       cudaGetLastError();

@@ -244,6 +244,75 @@ __device__ __forceinline__ void mma_f8_pair(uint32_t d_tmem, uint64_t adesc, uin
       : "memory");
 }
 
+// ------------------------------------------- tcgen05, E2M1 with block scales
+// D (+)= (A sa) * (B sb): codes in shared memory, scales in TMEM.  BLOCK 32 or
+// 16 entries share a scale; PAIR: both CTAs of a pair (M = 256).
+template <int BLOCK, bool PAIR>
+__device__ __forceinline__ void mma_fp4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
+                                        uint32_t sfb, uint32_t accumulate) {
+#define MUON_MMA_FP4(GROUP, KIND)                                                                       \
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"                                      \
+               "tcgen05.mma." GROUP "." KIND " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),    \
+               "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)                  \
+               : "memory")
+  if constexpr (PAIR) {
+    if constexpr (BLOCK == 32)
+      MUON_MMA_FP4("cta_group::2", "kind::mxf4.block_scale.scale_vec::2X");
+    else
+      MUON_MMA_FP4("cta_group::2", "kind::mxf4nvf4.block_scale.scale_vec::4X");
+  } else {
+    if constexpr (BLOCK == 32)
+      MUON_MMA_FP4("cta_group::1", "kind::mxf4.block_scale.scale_vec::2X");
+    else
+      MUON_MMA_FP4("cta_group::1", "kind::mxf4nvf4.block_scale.scale_vec::4X");
+  }
+#undef MUON_MMA_FP4
+}
+
+// Copies 512 bytes of shared memory (32 rows of 16) to 4 TMEM columns, the
+// same 32 lanes four times; ordered with the MMAs that this thread issues.
+template <bool PAIR>
+__device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint64_t sdesc) {
+  if constexpr (PAIR)
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+
+// ------------------------------------------------------ tcgen05, one CTA
+__device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)
+               : "memory");
+}
+
+__device__ __forceinline__ void tmem_relinquish() {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// A float of the same shared-memory location in another CTA of the cluster.
+__device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
+
+// 2-D tile load by either CTA of a pair, counted on a barrier of either.
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+      : "memory");
+}
+
 // Arrive once on `bar` in every CTA of `mask` when the pair's MMAs issued so
 // far by this thread are done.
 __device__ __forceinline__ void mma_commit_pair_mc(uint32_t bar, uint16_t mask) {
@@ -345,6 +414,12 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo, ui
   return d;
 }
 
+// Without swizzle: rows of 16 bytes, 8-row groups `sbo` bytes apart (what a
+// copy of block scales to TMEM reads).
+__device__ __forceinline__ uint64_t sdesc_plain(uint32_t saddr, uint32_t sbo) {
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32 | 1ull << 46;
+}
+
 // Operand format codes of kind::f8f6f4.
 constexpr uint32_t kFmtE4M3 = 0;
 constexpr uint32_t kFmtE5M2 = 1;
@@ -357,6 +432,19 @@ __host__ __device__ constexpr uint32_t idesc_f8(int M, int N, uint32_t a_fmt, ui
          | (b_fmt << 10)                          // B format
          | (static_cast<uint32_t>(N >> 3) << 17)  // N / 8
          | (static_cast<uint32_t>(M >> 4) << 24);  // M / 16
+}
+
+// Instruction descriptor for E2M1 operands with block scales, both K-major, an
+// fp32 accumulator and K = 64: block 32 has UE8M0 scales (two per row and
+// instruction, bytes sf and sf + 1 of a row's word in TMEM), block 16 UE4M3
+// ones (four, sf = 0).
+__host__ __device__ constexpr uint32_t idesc_fp4(int M, int N, int block, uint32_t sf) {
+  return (sf << 4)                                  // scales of B: first byte
+         | (1u << 7) | (1u << 10)                   // A and B: E2M1
+         | (static_cast<uint32_t>(N >> 3) << 17)    // N / 8
+         | (block == 32 ? 1u << 23 : 0u)            // scale type: UE8M0 / UE4M3
+         | (static_cast<uint32_t>(M >> 4) << 24)    // M / 16
+         | (sf << 29);                              // scales of A: first byte
 }
 
 // Instruction descriptor for kind::f16 with bf16 A/B and an fp32 accumulator.

@@ -42,7 +42,8 @@ EXPORTS = ["muon_workspace_size", "muon_step", "ns5_workspace_size", "ns5", "ns5
            "fp8_mm_backward", "fp8_mm_backward_workspace_size", "muon_debug_check_failures",
            "adamw_step", "adamw_plan_create", "adamw_plan_set_grads", "adamw_plan_set_rates", "adamw_plan_step",
            "adamw_plan_destroy", "token_logprobs", "token_logprobs_backward", "token_logprobs_loss", "balance_loss",
-           "balance_loss_workspace_size", "balance_loss_backward"]
+           "balance_loss_workspace_size", "balance_loss_backward", "fp4_codes_size", "fp4_scales_size", "fp4_quantize",
+           "fp4_values", "fp4_mm", "layer_norm", "layer_norm_backward", "layer_norm_backward_workspace_size"]
 
 #: bytes of the static device scratch ns5_noalloc uses (MUON_NOALLOC_SCRATCH_BYTES)
 NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -82,6 +83,12 @@ class adamw_tensor_desc(ctypes.Structure):
                 ("exp_avg_sq_scale", ctypes.c_void_p), ("numel", ctypes.c_int64), ("lr", ctypes.c_double),
                 ("weight_decay", ctypes.c_double), ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
                 ("state_bits", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class fp4_matrix(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("block", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
 
 
 _lib = None
@@ -171,6 +178,24 @@ def load(path):
     L.balance_loss_backward.argtypes = [c_vp, c_int, c_i64, c_int, c_i64, c_vp, c_i64, c_vp, c_vp, c_vp, c_vp, c_vp,
                                         c_i64, c_vp]
     L.balance_loss_backward.restype = c_int
+    L.fp4_codes_size.argtypes = [c_i64, c_i64]
+    L.fp4_codes_size.restype = c_sz
+    L.fp4_scales_size.argtypes = [c_i64, c_i64, c_int]
+    L.fp4_scales_size.restype = c_sz
+    L.fp4_quantize.argtypes = [c_vp, c_int, c_i64, c_i64, c_i64, P(fp4_matrix), P(fp4_matrix), c_int, c_u64, c_vp]
+    L.fp4_quantize.restype = c_int
+    L.fp4_values.argtypes = [P(fp4_matrix), c_vp, c_int, c_i64, c_vp]
+    L.fp4_values.restype = c_int
+    L.fp4_mm.argtypes = [P(fp4_matrix), P(fp4_matrix), c_vp, c_int, c_i64, c_vp, c_sz, c_vp]
+    L.fp4_mm.restype = c_int
+    L.layer_norm.argtypes = [c_vp, c_int, c_i64, c_i64, c_i64, c_vp, c_i64, c_vp, c_vp, c_int, c_f, c_vp, c_i64, c_vp,
+                             c_i64, c_vp, c_vp, c_vp]
+    L.layer_norm.restype = c_int
+    L.layer_norm_backward.argtypes = [c_vp, c_i64, c_vp, c_i64, c_int, c_i64, c_i64, c_vp, c_vp, c_vp, c_int, c_vp, c_i64,
+                                      c_vp, c_i64, c_vp, c_vp, c_vp, c_sz, c_vp]
+    L.layer_norm_backward.restype = c_int
+    L.layer_norm_backward_workspace_size.argtypes = [c_i64, c_i64]
+    L.layer_norm_backward_workspace_size.restype = c_sz
     L.muon_plan_cache_clear.argtypes = []
     L.muon_plan_cache_clear.restype = None
     L.muon_debug_check_failures.argtypes = [P(ctypes.c_longlong)]
@@ -191,6 +216,8 @@ def _stream(stream):
 def _tensors(out):
     if isinstance(out, torch.Tensor):
         yield out
+    elif isinstance(out, FP4):
+        yield from (t for t in (out.codes, out.scales, out.scale) if t is not None)
     elif isinstance(out, (tuple, list)):
         for t in out:
             yield from _tensors(t)
@@ -987,3 +1014,204 @@ def balance_loss_backward(logits, result, grad_balance, grad_z, mask=None, out=N
           tokens, experts, pitch, _mask(mask, tokens), groups, stats, stats + 16, grad_balance.data_ptr(),
           grad_z.data_ptr(), out.data_ptr(), _matrix(out, "out")[2])
     return out
+
+
+class FP4:
+    """A matrix in 4-bit floating point with block scales (fp4_matrix in
+    include/muon.h), rows x cols, contracted along its columns by fp4_mm.
+
+    codes    uint8, rows x ceil(cols / 32) * 16: E2M1, two per byte;
+    scales   uint8: one E8M0 (block 32) or E4M3 (block 16) number per row and
+             block, in tiles of 128 rows by 4 blocks;
+    scale    block 16: float32 [2], the tensor's power of two and the largest
+             magnitude it comes from; block 32: None.
+
+    ``fp4_quantize`` makes one; made of a program's own arrays, they are
+    contiguous and on one CUDA device.
+    """
+
+    __slots__ = ("codes", "scales", "scale", "rows", "cols", "block", "_desc")
+
+    def __init__(self, codes, scales, rows, cols, block=32, scale=None):
+        if block not in (16, 32):
+            raise ValueError("block must be 32 or 16")
+        if (scale is None) != (block == 32):
+            raise ValueError("blocks of 16 have a scale of the tensor, blocks of 32 none")
+        if rows < 0 or cols < 0:
+            raise ValueError("rows and cols must not be negative")
+        for t, size, what in ((codes, rows * (-(-cols // 32) * 16), "codes"),
+                              (scales, -(-rows // 128) * (-(-cols // 256) * (64 // block)) * 512, "scales")):
+            if t.dtype != torch.uint8 or not t.is_contiguous() or t.numel() != size:
+                raise ValueError(f"{what} must be a contiguous uint8 tensor of {size} bytes")
+        if scale is not None and (scale.dtype != torch.float32 or scale.numel() != 2 or not scale.is_contiguous()):
+            raise ValueError("scale must be two float32 numbers")
+        _index_of("FP4", codes, scales, scale)
+        self.codes, self.scales, self.scale = codes, scales, scale
+        self.rows, self.cols, self.block = rows, cols, block
+        self._desc = fp4_matrix(codes.data_ptr(), scales.data_ptr(), 0 if scale is None else scale.data_ptr(), rows, cols,
+                                block, 0)
+
+    @property
+    def shape(self):
+        return self.rows, self.cols
+
+
+def _fp4_new(rows, cols, block, dev, scale):
+    pitch = -(-cols // 32) * 16
+    # one allocation: codes, then scales on a boundary of 512 bytes
+    first = -(-rows * pitch // 512) * 512
+    size = -(-rows // 128) * (-(-cols // 256) * (64 // block)) * 512
+    data = torch.empty(first + size, dtype=torch.uint8, device=dev)
+    return FP4(data[:rows * pitch].view(rows, pitch), data[first:], rows, cols, block, scale)
+
+
+def fp4_quantize(x, block=32, axis=1, seed=None, stream=None):
+    """x (2-D, bfloat16 or float32, any row pitch) in 4 bits, as FP4: with
+    axis=1 x itself, blocks along its rows; with axis=0 its transpose, blocks
+    down its columns; with axis="both" the two of them (one read of x).
+    block: 32 (power-of-two scales) or 16 (E4M3 scales and a power of two for
+    the tensor).  seed: round stochastically, with the random bits of that
+    seed; None: to nearest.  See fp4_quantize in include/muon.h."""
+    if stream is not None:
+        return _on(stream, x, fp4_quantize, x, block, axis, seed)
+    rows, cols, pitch = _matrix(x, "x")
+    if block not in (16, 32):
+        raise ValueError("block must be 32 or 16")
+    if axis not in (0, 1, "both"):
+        raise ValueError('axis must be 1, 0 or "both"')
+    index = _index_of("fp4_quantize", x)
+    kind, dev = _dtype_code(x), x.device
+    scale = torch.empty(2, dtype=torch.float32, device=dev) if block == 16 else None
+    along = None if axis == 0 else _fp4_new(rows, cols, block, dev, scale)
+    across = None if axis == 1 else _fp4_new(cols, rows, block, dev, scale)
+    _call(lib().fp4_quantize, "fp4_quantize", index, stream, x.data_ptr(), kind, rows, cols, pitch,
+          None if along is None else along._desc, None if across is None else across._desc, 0 if seed is None else 1,
+          0 if seed is None else int(seed) & (2 ** 64 - 1))
+    return (along, across) if axis == "both" else across if along is None else along
+
+
+def fp4_values(q, dtype=torch.bfloat16, out=None, stream=None):
+    """The numbers that an FP4 matrix stands for, rows x cols, bfloat16 (exact
+    there too) or float32."""
+    if stream is not None:
+        return _on(stream, q.codes, fp4_values, q, dtype, out)
+    if out is None:
+        out = torch.empty((q.rows, q.cols), dtype=dtype, device=q.codes.device)
+    elif out.shape != (q.rows, q.cols):
+        raise ValueError("out must be rows x cols")
+    _call(lib().fp4_values, "fp4_values", _index_of("fp4_values", q.codes, out), stream, q._desc, out.data_ptr(),
+          _dtype_code(out), _matrix(out, "out")[2])
+    return out
+
+
+def fp4_mm(a, b, dtype=torch.bfloat16, out=None, workspace=None, stream=None):
+    """a b^T of two FP4 matrices of equal cols and block: a.rows x b.rows,
+    bfloat16 or float32 (out's dtype where `out`, of any row pitch, is given).
+    See fp4_mm in include/muon.h."""
+    if stream is not None:
+        return _on(stream, a.codes, fp4_mm, a, b, dtype, out, workspace)
+    if a.cols != b.cols or a.block != b.block:
+        raise ValueError("a and b must have the same number of columns and the same block")
+    dev = a.codes.device
+    if out is None:
+        out = torch.empty((a.rows, b.rows), dtype=dtype, device=dev)
+    elif out.shape != (a.rows, b.rows):
+        raise ValueError("out must be a.rows x b.rows")
+    if workspace is None:
+        workspace = torch.empty(256, dtype=torch.uint8, device=dev)
+    _call(lib().fp4_mm, "fp4_mm", _index_of("fp4_mm", a.codes, b.codes, out, workspace), stream, a._desc, b._desc,
+          out.data_ptr(), _dtype_code(out), _matrix(out, "out")[2], workspace.data_ptr(), workspace.numel())
+    return out
+
+
+class LayerNorm(NamedTuple):
+    """What layer_norm gives: y, mean and rstd of each row, and the rows that
+    were normalised where a residual was added (else None)."""
+    y: torch.Tensor
+    mean: torch.Tensor
+    rstd: torch.Tensor
+    sum: Optional[torch.Tensor] = None
+
+
+def _rows_out(out, like, what):
+    """(tensor, row pitch) of an output shaped like `like`."""
+    if out is None:
+        out = torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    elif out.shape != like.shape or out.dtype != like.dtype:
+        raise ValueError(f"{what} must have x's shape and dtype")
+    return out, _matrix(out, what)[2]
+
+
+def _rows_like(t, x, what):
+    """(address, row pitch) of an optional input shaped like x."""
+    if t is None:
+        return None, 0
+    if t.shape != x.shape or t.dtype != x.dtype:
+        raise ValueError(f"{what} must have x's shape and dtype")
+    return t.data_ptr(), _matrix(t, what)[2]
+
+
+def _per_column(t, cols, what):
+    if t is None:
+        return None
+    if t.shape != (cols,) or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous tensor with one entry per column")
+    return t.data_ptr()
+
+
+def layer_norm(x, weight=None, bias=None, eps=1e-5, residual=None, out=None, stream=None):
+    """Layer norm of each row of x (2-D, bfloat16 or float32, any row pitch): a
+    LayerNorm.  weight and bias: one entry per column, float32 or bfloat16 (both
+    the same); residual: added to x first, the sum rounded to x's type and
+    returned.  `out` may be x itself where there is no residual.  See
+    layer_norm in include/muon.h."""
+    if stream is not None:
+        return _on(stream, x, layer_norm, x, weight, bias, eps, residual, out)
+    rows, cols, pitch = _matrix(x, "x")
+    kind = _dtype_code(x)
+    w, b = _per_column(weight, cols, "weight"), _per_column(bias, cols, "bias")
+    if w is not None and b is not None and weight.dtype != bias.dtype:
+        raise ValueError("weight and bias must have the same dtype")
+    wkind = _dtype_code(weight) if w is not None else _dtype_code(bias) if b is not None else MUON_F32
+    index = _index_of("layer_norm", x, weight, bias, residual, out)
+    r, r_pitch = _rows_like(residual, x, "residual")
+    y, y_pitch = _rows_out(out, x, "out")
+    s, s_pitch = (None, 0) if residual is None else _rows_out(None, x, "sum")
+    stats = torch.empty((2, rows), dtype=torch.float32, device=x.device)
+    p = stats.data_ptr()
+    _call(lib().layer_norm, "layer_norm", index, stream, x.data_ptr(), kind, rows, cols, pitch, r, r_pitch, w, b, wkind,
+          float(eps), y.data_ptr(), y_pitch, None if s is None else s.data_ptr(), s_pitch, p, p + 4 * rows)
+    return LayerNorm(y, *stats.unbind(), s)
+
+
+@functools.lru_cache(maxsize=256)
+def layer_norm_backward_workspace_size(rows, cols):
+    return lib().layer_norm_backward_workspace_size(int(rows), int(cols))
+
+
+def layer_norm_backward(grad, x, mean, rstd, weight=None, bias=True, grad_sum=None, out=None, workspace=None,
+                        stream=None):
+    """Gradients (grad_x, grad_weight, grad_bias) of layer_norm from that of y:
+    x the rows that were normalised (LayerNorm.sum where there was a
+    residual), mean and rstd as layer_norm gave them.  grad_weight (None without
+    a weight) and grad_bias (None with bias=False) are float32.  grad_sum: the gradient
+    that reaches the normalised rows by another way (the residual stream), added to grad_x.
+    `out` may be grad or grad_sum itself.  See layer_norm_backward in include/muon.h."""
+    if stream is not None:
+        return _on(stream, x, layer_norm_backward, grad, x, mean, rstd, weight, bias, grad_sum, out, workspace)
+    rows, cols, pitch = _matrix(x, "x")
+    kind, f32, dev = _dtype_code(x), torch.float32, x.device
+    g, g_pitch = _rows_like(grad, x, "grad")
+    gs, gs_pitch = _rows_like(grad_sum, x, "grad_sum")
+    w = _per_column(weight, cols, "weight")
+    mu, rs = _per_row(mean, rows, f32, "mean"), _per_row(rstd, rows, f32, "rstd")
+    index = _index_of("layer_norm_backward", grad, x, mean, rstd, weight, grad_sum, out, workspace)
+    out, out_pitch = _rows_out(out, x, "out")
+    columns = torch.empty((2, cols), dtype=f32, device=dev) if bias or w is not None else None
+    p = 0 if columns is None else columns.data_ptr()
+    if workspace is None:
+        workspace = torch.empty(max(layer_norm_backward_workspace_size(rows, cols), 256), dtype=torch.uint8, device=dev)
+    _call(lib().layer_norm_backward, "layer_norm_backward", index, stream, g, g_pitch, x.data_ptr(), pitch, kind, rows,
+          cols, mu, rs, w, MUON_F32 if w is None else _dtype_code(weight), gs, gs_pitch, out.data_ptr(), out_pitch,
+          None if w is None else p, p + 4 * cols if bias else None, workspace.data_ptr(), workspace.numel())
+    return out, None if w is None else columns.select(0, 0), columns.select(0, 1) if bias else None
