@@ -602,7 +602,8 @@ muon_status_t fp4_quantize(const void* x, int dtype, int64_t rows, int64_t cols,
 
 /* The numbers that a quantised matrix stands for, rows x cols of `dtype` with
  * row pitch out_stride.  They are exact in bfloat16 too, down to its subnormal
- * numbers. */
+ * numbers; what a code stands for past float32's range (the nearest one to a
+ * number of nearly 2^128 may be 2^128) is infinite. */
 muon_status_t fp4_values(const fp4_matrix* q, void* out, int dtype, int64_t out_stride, void* stream);
 
 /* Product out = a b^T of two matrices of equal cols and block: out is a->rows x

@@ -93,7 +93,7 @@ __device__ __forceinline__ Scale block_scale(uint32_t amax, float up_tensor) {
     q.up = bad ? 0.0f : pow2(-e);
     q.s = q.r = 1.0f;
   } else {
-    const float want = __fdiv_rn(__uint_as_float(amax), 6.0f) * up_tensor;
+    const float sixth = __fdiv_rn(__uint_as_float(amax), 6.0f), want = sixth * up_tensor;
     uint16_t c;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(0.0f), "f"(bad ? 0.0f : want));
     auto value = [](uint32_t code) {
@@ -101,7 +101,8 @@ __device__ __forceinline__ Scale block_scale(uint32_t amax, float up_tensor) {
       return code < 8 ? static_cast<float>(code) * 0.001953125f : normal;
     };
     uint32_t code = c & 0x7Fu;
-    if (SR && value(code) < want && !bad) ++code;  // upwards: nothing is cut off, so that rounding stays right in the mean
+    // upwards: nothing is cut off, so that rounding stays right in the mean (`want` may have left float32's range)
+    if (SR && !bad && (code == 0 ? sixth > 0.0f : value(code) < want)) ++code;
     q.s = value(code);
     q.code = bad ? 0x7Fu : code;
     q.up = bad ? 0.0f : up_tensor;
@@ -115,8 +116,9 @@ __device__ __forceinline__ float in_units(float x, const Scale& q) {
   float y = x * q.up;
   if constexpr (BLOCK == 16) {
     // y / s to nearest: the product with the rounded reciprocal, corrected by its remainder
+    // (which would turn -0 into 0)
     const float t = y * q.r;
-    y = fmaf(fmaf(-t, q.s, y), q.r, t);
+    y = copysignf(fmaf(fmaf(-t, q.s, y), q.r, t), x);
   }
   return y;
 }

@@ -29,6 +29,8 @@ Adam") describes for the embedding-type banks; its readings are stated there.
 ``oracle.adamw`` and ``oracle.losses`` restate the operators at the two ends
 of a training step from their formulas: AdamW over tensors with moments in 32
 bits or in 8, token log probabilities, and the balance loss of a router.
+``oracle.fp4`` and ``oracle.layer_norm`` do so for the 4-bit format with block
+scales and for layer norm.
 
 Pin status: every public function is pinned by the CPU tests
 (closed form via SVD, invariants, brute force in exact rational arithmetic,
@@ -38,13 +40,17 @@ FP8: bit-exact casts against torch's float8 conversions and a bit-field
 decoding of all 256 codes, exact products of representable operands, power-of-
 two scale invariance, brute force in rational arithmetic; for AdamW and the
 losses: torch.optim.AdamW, torch's autograd and differences in float64, the
-formats' representable values, the mean of the stochastic rounding).
+formats' representable values, the mean of the stochastic rounding; for the
+4-bit format: every code and scale tried in rational arithmetic; for layer
+norm: torch's autograd and differences in float64).
 """
 
 from .adam import ADAM_DEFAULTS, adam_constants, adam_step, cautious_mask
 from .adamw import (adamw_bits, adamw_dequantize, adamw_moments, adamw_quantize, adamw_update,
                     bf16_stochastic)
 from .losses import balance_loss, balance_loss_grad, token_logprobs, token_logprobs_grad
+from .fp4 import fp4_bits, fp4_dequantize, fp4_pack, fp4_quantize
+from .layer_norm import layer_norm, layer_norm_grad
 from .fp8 import FP8_FORMATS, fp8_mm, fp8_mm_backward, quantize, round_to_fp8
 from .bf16 import round_to_bf16, BF16_MAX
 from .muon import (
@@ -64,6 +70,12 @@ from .muon import (
 )
 
 __all__ = [
+    "fp4_bits",
+    "fp4_dequantize",
+    "fp4_pack",
+    "fp4_quantize",
+    "layer_norm",
+    "layer_norm_grad",
     "FP8_FORMATS",
     "fp8_mm",
     "fp8_mm_backward",
