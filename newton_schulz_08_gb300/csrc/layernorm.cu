@@ -18,12 +18,16 @@
 
 #include <algorithm>
 #include <cmath>
+#include <map>
+#include <mutex>
 #include <new>
+#include <tuple>
 #include <vector>
 
 #include "../../include/muon.h"
 #include "check.cuh"
 #include "host.h"
+#include "rows.cuh"
 
 namespace muon {
 namespace {
@@ -47,89 +51,14 @@ struct RowParams {
   long long rows;
   int cols, parts;
   int weight_f32;
-  int vec;                // every row of every array may be read in vectors
+  int units_lane;         // 16-byte units of a row that a lane has
+  int stages;             // 2: a row is copied while the one before it is worked on
+  int weights_shared;     // weight (and bias) are held in shared memory
   float eps;
-};
-
-template <bool BF16>
-struct Raw {
-  uint4 q[BF16 ? 1 : 2];
 };
 
 __device__ __forceinline__ float weight_at(const void* w, int f32, int c) {
   return f32 ? static_cast<const float*>(w)[c] : __bfloat162float(static_cast<const __nv_bfloat16*>(w)[c]);
-}
-
-// Column of entry e of a thread's group v: 8 neighbours where rows are read in
-// vectors, else neighbours in neighbouring threads.
-template <bool VEC, int T>
-__device__ __forceinline__ int column(int v, int e, int t) { return VEC ? (v * T + t) * 8 + e : (v * 8 + e) * T + t; }
-
-template <bool BF16, bool VEC, int T>
-__device__ __forceinline__ void load(const void* base, long long at, int cols, int v, int t, float (&x)[8]) {
-  if constexpr (VEC) {
-    const int c = (v * T + t) * 8;
-    if (c + 8 <= cols) {
-      if constexpr (BF16) {
-        const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + at + c);
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          x[2 * k] = __uint_as_float(w[k] << 16);
-          x[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
-        }
-      } else {
-        const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at + c);
-        const float4 a = f[0], b = f[1];
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-      }
-      return;
-    }
-  }
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int c = column<VEC, T>(v, e, t);
-    x[e] = 0.0f;
-    if (c < cols) {
-      if constexpr (BF16)
-        x[e] = __bfloat162float(static_cast<const __nv_bfloat16*>(base)[at + c]);
-      else
-        x[e] = static_cast<const float*>(base)[at + c];
-    }
-  }
-}
-
-template <bool BF16, bool VEC, int T>
-__device__ __forceinline__ void store(void* base, long long at, int cols, int v, int t, const float (&x)[8]) {
-  if constexpr (VEC) {
-    const int c = (v * T + t) * 8;
-    if (c + 8 <= cols) {
-      if constexpr (BF16) {
-        uint32_t w[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
-          w[k] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(base) + at + c) = make_uint4(w[0], w[1], w[2], w[3]);
-      } else {
-        float4* f = reinterpret_cast<float4*>(static_cast<float*>(base) + at + c);
-        f[0] = make_float4(x[0], x[1], x[2], x[3]);
-        f[1] = make_float4(x[4], x[5], x[6], x[7]);
-      }
-      return;
-    }
-  }
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int c = column<VEC, T>(v, e, t);
-    if (c < cols) {
-      if constexpr (BF16)
-        static_cast<__nv_bfloat16*>(base)[at + c] = __float2bfloat16_rn(x[e]);
-      else
-        static_cast<float*>(base)[at + c] = x[e];
-    }
-  }
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -138,16 +67,37 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
+using rows::Pair;
+
 __device__ __forceinline__ float rounded_sum(float a, float b, bool bf16) {
   const float s = a + b;
   return bf16 ? __bfloat162float(__float2bfloat16_rn(s)) : s;
 }
 
-// Sum over the W warps of a row group; `slot`: W floats of shared memory per
-// use.  Every use of a row has slots of its own, and a barrier of the group.
-template <int W>
+// A row's place in a CTA: L lanes of a warp (several rows a warp), or W whole
+// warps, each with a piece of it.  A lane has up to V units of 16 bytes (32
+// entries).
+template <bool BF16, int L, int W>
+struct Shape {
+  static constexpr int kV = BF16 ? 4 : 8, kE = rows::Unit<BF16>::n;
+  static constexpr int kThreads = W > 8 ? 32 * W : 256, kWarps = kThreads / 32;
+  static constexpr int kGroups = kWarps / W;       // row groups of W warps
+  static constexpr int kRows = 32 / L;             // rows of a warp at a time
+  static constexpr int kCapacity = L * W * kV * kE;
+};
+
+template <int L>
+__device__ __forceinline__ float lane_sum(float v) {
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+
+// Sums over a row; `slot`: W entries of shared memory.  Every use within a row
+// has slots of its own, and so have neighbouring rows.
+template <int L, int W>
 __device__ __forceinline__ float row_sum(float v, float* slot, int group, int warp_in) {
-  v = warp_sum(v);
+  v = lane_sum<L>(v);
   if constexpr (W > 1) {
     if ((threadIdx.x & 31) == 0) slot[warp_in] = v;
     asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(W * 32) : "memory");
@@ -158,10 +108,10 @@ __device__ __forceinline__ float row_sum(float v, float* slot, int group, int wa
   return v;
 }
 
-template <int W>
+template <int L, int W>
 __device__ __forceinline__ float2 row_sum2(float a, float b, float2* slot, int group, int warp_in) {
-  a = warp_sum(a);
-  b = warp_sum(b);
+  a = lane_sum<L>(a);
+  b = lane_sum<L>(b);
   if constexpr (W > 1) {
     if ((threadIdx.x & 31) == 0) slot[warp_in] = make_float2(a, b);
     asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(W * 32) : "memory");
@@ -176,177 +126,362 @@ __device__ __forceinline__ float2 row_sum2(float a, float b, float2* slot, int g
   return make_float2(a, b);
 }
 
-__host__ __device__ constexpr int threads_of(int w) { return w >= 4 ? 32 * w : 128; }
+template <bool BF16>
+__device__ __forceinline__ char* row_of(const void* base, long long r, long long pitch, int c0) {
+  return const_cast<char*>(static_cast<const char*>(base)) + (r * pitch + c0) * (BF16 ? 2 : 4);
+}
 
-// Forward: a row group of W warps takes rows one after another.
-template <bool BF16, bool VEC, int W, int V>
-__global__ void __launch_bounds__(threads_of(W)) norm_forward(const __grid_constant__ RowParams P) {
-  constexpr int T = 32 * W, kGroups = threads_of(W) / T;
-  __shared__ float slots[kGroups][2][2][W];  // by parity of the row, use
-  const int group = threadIdx.x / T, t = threadIdx.x % T, warp_in = t >> 5;
+// Weights in shared memory, float32: four-entry parts of a unit apart, so that a
+// warp reads whole lines.  `units` of a row.
+template <bool BF16>
+__device__ __forceinline__ void stage_weights(uint32_t at, const void* w, int f32, float none, int cols, int units, int threads) {
+  constexpr int E = rows::Unit<BF16>::n;
+  for (int i = threadIdx.x; i < units * E; i += threads) {
+    const int u = i / E, e = i - u * E;
+    const float v = w && i < cols ? weight_at(w, f32, i) : none;
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + ((e >> 2) * units + u) * 16 + (e & 3) * 4), "f"(v) : "memory");
+  }
+}
+
+template <bool BF16>
+__device__ __forceinline__ void weights(const RowParams& P, uint32_t at, const void* w, float none, int unit, int units,
+                                        Pair (&x)[rows::Unit<BF16>::n / 2]) {
+  constexpr int E = rows::Unit<BF16>::n;
+  if (P.weights_shared) {
+#pragma unroll
+    for (int p = 0; p < E / 4; ++p) {
+      const uint4 q = rows::shared_load(at + (p * units + unit) * 16);
+      x[2 * p] = rows::pair(__uint_as_float(q.x), __uint_as_float(q.y));
+      x[2 * p + 1] = rows::pair(__uint_as_float(q.z), __uint_as_float(q.w));
+    }
+  } else {
+    auto at_column = [&](int c) { return w && c < P.cols ? weight_at(w, P.weight_f32, c) : none; };
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) x[i] = rows::pair(at_column(unit * E + 2 * i), at_column(unit * E + 2 * i + 1));
+  }
+}
+
+// Forward: the row groups of all CTAs take rows in turn.
+template <bool BF16, bool ALIGNED, int L, int W>
+__global__ void __launch_bounds__(Shape<BF16, L, W>::kThreads, W > 8 ? 1 : 2) norm_forward(const __grid_constant__ RowParams P) {
+  using S = Shape<BF16, L, W>;
+  constexpr int V = S::kV, E = S::kE, H = E / 2;
+  extern __shared__ uint4 dynamic[];
+  __shared__ float slots[S::kGroups][2][2][W];  // by parity of the row, use
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int group = warp / W, warp_in = warp % W, sub = lane % L;
+  const int units = P.units_lane * L * W;
+  const int unit0 = warp_in * P.units_lane * L, c0 = unit0 * E;  // this warp's piece of a row
+  const int piece = P.cols - c0;                                  // entries from there on
+  const int n = min(P.units_lane, max(0, (piece + L * E - 1) / (L * E)));
+  uint32_t at = rows::shared_address(dynamic);
+  const uint32_t wa = at, ba = at + units * E * 4;
+  if (P.weights_shared) at += 2 * units * E * 4;
+  // slots: [stage][array][warp][row of the warp]
+  const uint32_t slot_bytes = (P.units_lane * L + 1) * 16, array_bytes = slot_bytes * S::kRows * S::kWarps;
+  const uint32_t stage_bytes = (P.residual ? 2 : 1) * array_bytes;
+  at += slot_bytes * (warp * S::kRows + lane / L);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const float inv = 1.0f / static_cast<float>(P.cols);
-  int parity = 0;
-  for (long long r = static_cast<long long>(blockIdx.x) * kGroups + group; r < P.rows;
-       r += static_cast<long long>(gridDim.x) * kGroups, parity ^= 1) {
-    float x[V][8];
-#pragma unroll
-    for (int v = 0; v < V; ++v) load<BF16, VEC, T>(P.x, r * P.sx, P.cols, v, t, x[v]);
+  const long long step = static_cast<long long>(gridDim.x) * S::kGroups * S::kRows;
+  long long r0 = (static_cast<long long>(blockIdx.x) * S::kGroups + group) * S::kRows;
+  auto fetch = [&](long long base, int stage) {
+    const long long r = base + lane / L;
+    if (base < P.rows && MUON_CHECK(r >= 0)) {
+      const uint32_t to = at + stage * stage_bytes;
+      const int have = r < P.rows ? piece : -16;  // a warp's rows past the last one are zeros
+      const long long from = min(r, P.rows - 1);
+      rows::fetch<BF16, ALIGNED, L, V>(to, row_of<BF16>(P.x, from, P.sx, c0), have, sub, n);
+      if (P.residual) rows::fetch<BF16, ALIGNED, L, V>(to + array_bytes, row_of<BF16>(P.residual, from, P.sr, c0), have, sub, n);
+    }
+    rows::copies_commit();
+  };
+  const bool ahead = P.stages == 2;
+  if (ahead) fetch(r0, 0);
+  if (P.weights_shared) {
+    stage_weights<BF16>(wa, P.weight, P.weight_f32, 1.0f, P.cols, units, S::kThreads);
+    stage_weights<BF16>(ba, P.bias, P.weight_f32, 0.0f, P.cols, units, S::kThreads);
+    __syncthreads();
+  }
+  for (int it = 0; r0 < P.rows; r0 += step, ++it) {
+    const int stage = ahead ? it & 1 : 0;
+    if (ahead)
+      fetch(r0 + step, stage ^ 1);
+    else
+      fetch(r0, 0);
+    rows::copies_wait(ahead);
+    if (!ALIGNED) __syncwarp();
+    const long long r = r0 + lane / L;
+    const int left = r < P.rows ? piece : 0;
+    const uint32_t slot = at + stage * stage_bytes;
+    Pair x[V][H], s = rows::pair(0.0f);
+    const uint32_t shift = ALIGNED ? 0u : rows::shift_of(row_of<BF16>(P.x, r, P.sx, c0));
     if (P.residual) {
+      const uint32_t shift_r = ALIGNED ? 0u : rows::shift_of(row_of<BF16>(P.residual, r, P.sr, c0));
+      char* out = row_of<BF16>(P.sum, r, P.ssum, c0);
+      uint4 q[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        float a[8];
-        load<BF16, VEC, T>(P.residual, r * P.sr, P.cols, v, t, a);
+        if (v >= n) break;
+        const int k = v * L + sub;
+        Pair a[H];
+        rows::numbers<BF16>(rows::unit<ALIGNED>(slot, shift, k), x[v]);
+        rows::numbers<BF16>(rows::unit<ALIGNED>(slot + array_bytes, shift_r, k), a);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[v][e] = rounded_sum(x[v][e], a[e], BF16);
-        store<BF16, VEC, T>(P.sum, r * P.ssum, P.cols, v, t, x[v]);
+        for (int i = 0; i < H; ++i) x[v][i] = rows::add(x[v][i], a[i]);
+        q[v] = rows::pack<BF16>(x[v]);
+        rows::numbers<BF16>(q[v], x[v]);
+        if (ALIGNED) rows::store_aligned<BF16>(out, k, left, q[v]);
+      }
+      if (!ALIGNED) {
+        __syncwarp();  // every lane has read its neighbours' units
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          if (v < n) rows::shared_store(slot + 16 * (v * L + sub), q[v]);
+        __syncwarp();
+        rows::store_shifted<BF16, L, V>(slot, out, left, sub, n);
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        if (v >= n) break;
+        rows::numbers<BF16>(rows::unit<ALIGNED>(slot, shift, v * L + sub), x[v]);
       }
     }
-    float s = 0.0f;
 #pragma unroll
-    for (int v = 0; v < V; ++v)
+    for (int v = 0; v < V; ++v) {
+      if (v >= n) break;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s += x[v][e];  // (zeros past the row's end)
-    const float mean = row_sum<W>(s, slots[group][parity][0], group, warp_in) * inv;
-    s = 0.0f;
+      for (int i = 0; i < H; ++i) s = rows::add(s, x[v][i]);  // (zeros past the row's end)
+    }
+    const float mean = row_sum<L, W>(rows::total(s), slots[group][it & 1][0], group, warp_in) * inv;
+    s = rows::pair(0.0f);
+    const Pair minus = rows::pair(-mean);
 #pragma unroll
-    for (int v = 0; v < V; ++v)
+    for (int v = 0; v < V; ++v) {
+      if (v >= n) break;
+      if ((v + 1) * L * E > piece) {  // (the same in every lane)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float d = column<VEC, T>(v, e, t) < P.cols ? x[v][e] - mean : 0.0f;
-        s = fmaf(d, d, s);
+        for (int i = 0; i < H; ++i) {
+          const int c = (v * L + sub) * E + 2 * i;
+          float a, b;
+          rows::split(x[v][i], a, b);
+          x[v][i] = rows::pair(c < piece ? a : mean, c + 1 < piece ? b : mean);
+        }
       }
-    const float var = row_sum<W>(s, slots[group][parity][1], group, warp_in) * inv;
+#pragma unroll
+      for (int i = 0; i < H; ++i) {
+        x[v][i] = rows::add(x[v][i], minus);
+        s = rows::fma(x[v][i], x[v][i], s);
+      }
+    }
+    const float var = row_sum<L, W>(rows::total(s), slots[group][it & 1][1], group, warp_in) * inv;
     const float rstd = 1.0f / sqrtf(var + P.eps);
-    if (t == 0) {
+    if (sub == 0 && warp_in == 0 && r < P.rows) {
       P.mean[r] = mean;
       P.rstd[r] = rstd;
     }
+    char* out = row_of<BF16>(P.y, r, P.sy, c0);
+    const Pair scale = rows::pair(rstd);
+    if (!ALIGNED) __syncwarp();
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      float y[8];
+      if (v >= n) break;
+      const int k = v * L + sub;
+      Pair w[H], b[H];
+      weights<BF16>(P, wa, P.weight, 1.0f, unit0 + k, units, w);
+      weights<BF16>(P, ba, P.bias, 0.0f, unit0 + k, units, b);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int c = column<VEC, T>(v, e, t);
-        float w = 1.0f, b = 0.0f;
-        if (c < P.cols) {
-          if (P.weight) w = weight_at(P.weight, P.weight_f32, c);
-          if (P.bias) b = weight_at(P.bias, P.weight_f32, c);
-        }
-        y[e] = fmaf((x[v][e] - mean) * rstd, w, b);
-      }
-      store<BF16, VEC, T>(P.y, r * P.sy, P.cols, v, t, y);
+      for (int i = 0; i < H; ++i) x[v][i] = rows::fma(rows::mul(x[v][i], scale), w[i], b[i]);
+      if (ALIGNED)
+        rows::store_aligned<BF16>(out, k, left, rows::pack<BF16>(x[v]));
+      else
+        rows::shared_store(slot + 16 * k, rows::pack<BF16>(x[v]));
+    }
+    if (!ALIGNED) {
+      __syncwarp();
+      rows::store_shifted<BF16, L, V>(slot, out, left, sub, n);
+      __syncwarp();  // before the slot is filled again
     }
   }
+  rows::copies_wait(0);
 }
 
-// Backward: as norm_forward; a CTA leaves one row of partial sums.
-template <bool BF16, bool VEC, int W, int V>
-__global__ void __launch_bounds__(threads_of(W)) norm_backward(const __grid_constant__ RowParams P) {
-  constexpr int T = 32 * W, kGroups = threads_of(W) / T;
-  __shared__ float2 slots[kGroups][2][W];
-  extern __shared__ float sums[];  // kGroups > 1: [2][V * 8 * T]
-  const int group = threadIdx.x / T, t = threadIdx.x % T, warp_in = t >> 5;
+// Backward: as norm_forward.  The two means are taken in one pass over the row
+// in shared memory and the gradient in a second one, so that registers hold the
+// columns' sums; a CTA leaves one row of partial sums.
+template <bool BF16, bool ALIGNED, int L, int W>
+__global__ void __launch_bounds__(Shape<BF16, L, W>::kThreads, W > 8 ? 1 : 2) norm_backward(const __grid_constant__ RowParams P) {
+  using S = Shape<BF16, L, W>;
+  constexpr int V = S::kV, E = S::kE, H = E / 2;
+  extern __shared__ uint4 dynamic[];
+  __shared__ float2 slots[S::kGroups][2][W];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int group = warp / W, warp_in = warp % W, sub = lane % L;
+  const int units = P.units_lane * L * W;
+  const int unit0 = warp_in * P.units_lane * L, c0 = unit0 * E;
+  const int piece = P.cols - c0;
+  const int n = min(P.units_lane, max(0, (piece + L * E - 1) / (L * E)));
+  uint32_t at = rows::shared_address(dynamic);
+  const uint32_t wa = at;
+  if (P.weights_shared) at += units * E * 4;
+  const uint32_t slot_bytes = (P.units_lane * L + 1) * 16, array_bytes = slot_bytes * S::kRows * S::kWarps;
+  const uint32_t stage_bytes = (P.grad_sum ? 3 : 2) * array_bytes;
+  at += slot_bytes * (warp * S::kRows + lane / L);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const float inv = 1.0f / static_cast<float>(P.cols);
-  float dw[V][8], db[V][8];
+  const long long step = static_cast<long long>(gridDim.x) * S::kGroups * S::kRows;
+  long long r0 = (static_cast<long long>(blockIdx.x) * S::kGroups + group) * S::kRows;
+  float mean = 0.0f, rstd = 0.0f;  // of the row that is fetched
+  auto fetch = [&](long long base, int stage) {
+    const long long r = base + lane / L;
+    if (base < P.rows && MUON_CHECK(r >= 0)) {
+      const uint32_t to = at + stage * stage_bytes;
+      const int have = r < P.rows ? piece : -16;
+      const long long from = min(r, P.rows - 1);
+      rows::fetch<BF16, ALIGNED, L, V>(to, row_of<BF16>(P.x, from, P.sx, c0), have, sub, n);
+      rows::fetch<BF16, ALIGNED, L, V>(to + array_bytes, row_of<BF16>(P.grad, from, P.sg, c0), have, sub, n);
+      if (P.grad_sum)
+        rows::fetch<BF16, ALIGNED, L, V>(to + 2 * array_bytes, row_of<BF16>(P.grad_sum, from, P.sgs, c0), have, sub, n);
+      mean = P.mean[from];
+      rstd = P.rstd[from];
+    }
+    rows::copies_commit();
+  };
+  const bool ahead = P.stages == 2;
+  if (ahead) fetch(r0, 0);
+  if (P.weights_shared) {
+    stage_weights<BF16>(wa, P.weight, P.weight_f32, 1.0f, P.cols, units, S::kThreads);
+    __syncthreads();
+  }
+  Pair dw[V][H], db[V][H];
 #pragma unroll
   for (int v = 0; v < V; ++v)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dw[v][e] = db[v][e] = 0.0f;
-  int parity = 0;
-  for (long long r = static_cast<long long>(blockIdx.x) * kGroups + group; r < P.rows;
-       r += static_cast<long long>(gridDim.x) * kGroups, parity ^= 1) {
-    const float mean = P.mean[r], rstd = P.rstd[r];
-    float g[V][8], h[V][8];
+    for (int i = 0; i < H; ++i) dw[v][i] = db[v][i] = rows::pair(0.0f);
+  for (int it = 0; r0 < P.rows; r0 += step, ++it) {
+    const int stage = ahead ? it & 1 : 0;
+    if (!ahead) fetch(r0, 0);
+    const long long r = r0 + lane / L;
+    // (gradients past the row's end are zeros, and with them all that is added up; rows past the
+    // last one are left out by their own)
+    const Pair minus = rows::pair(-mean), scale = rows::pair(rstd);
+    if (ahead) fetch(r0 + step, stage ^ 1);
+    rows::copies_wait(ahead);
+    if (!ALIGNED) __syncwarp();
+    const int left = r < P.rows ? piece : 0;
+    const uint32_t slot = at + stage * stage_bytes;
+    const uint32_t shift_x = ALIGNED ? 0u : rows::shift_of(row_of<BF16>(P.x, r, P.sx, c0));
+    const uint32_t shift_g = ALIGNED ? 0u : rows::shift_of(row_of<BF16>(P.grad, r, P.sg, c0));
+    Pair a = rows::pair(0.0f), b = rows::pair(0.0f);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      load<BF16, VEC, T>(P.grad, r * P.sg, P.cols, v, t, g[v]);
-      load<BF16, VEC, T>(P.x, r * P.sx, P.cols, v, t, h[v]);
-    }
-    float a = 0.0f, b = 0.0f;
+      if (v >= n) break;
+      const int k = v * L + sub;
+      Pair x[H], g[H], w[H];
+      rows::numbers<BF16>(rows::unit<ALIGNED>(slot, shift_x, k), x);
+      rows::numbers<BF16>(rows::unit<ALIGNED>(slot + array_bytes, shift_g, k), g);
+      weights<BF16>(P, wa, P.weight, 1.0f, unit0 + k, units, w);
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int c = column<VEC, T>(v, e, t);
-        if (c < P.cols) {
-          const float xhat = (h[v][e] - mean) * rstd;
-          dw[v][e] = fmaf(g[v][e], xhat, dw[v][e]);
-          db[v][e] += g[v][e];
-          if (P.weight) g[v][e] *= weight_at(P.weight, P.weight_f32, c);
-          h[v][e] = xhat;
-          a += g[v][e];
-          b = fmaf(g[v][e], xhat, b);
-        }
+      for (int i = 0; i < H; ++i) {
+        const Pair xhat = rows::mul(rows::add(x[i], minus), scale);
+        dw[v][i] = rows::fma(g[i], xhat, dw[v][i]);
+        db[v][i] = rows::add(db[v][i], g[i]);
+        const Pair gw = rows::mul(g[i], w[i]);
+        a = rows::add(a, gw);
+        b = rows::fma(gw, xhat, b);
       }
-    const float2 s = row_sum2<W>(a, b, slots[group][parity], group, warp_in);
-    const float c1 = s.x * inv, c2 = s.y * inv;
+    }
+    const float2 s = row_sum2<L, W>(rows::total(a), rows::total(b), slots[group][it & 1], group, warp_in);
+    const Pair c1 = rows::pair(-s.x * inv), c2 = rows::pair(-s.y * inv);
+    char* out = row_of<BF16>(P.y, r, P.sy, c0);
+    const uint32_t shift_s = ALIGNED ? 0u : rows::shift_of(row_of<BF16>(P.grad_sum, r, P.sgs, c0));
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      float o[8];
+      if (v >= n) break;
+      const int k = v * L + sub;
+      Pair x[H], g[H], w[H], o[H];
+      rows::numbers<BF16>(rows::unit<ALIGNED>(slot, shift_x, k), x);
+      rows::numbers<BF16>(rows::unit<ALIGNED>(slot + array_bytes, shift_g, k), g);
+      weights<BF16>(P, wa, P.weight, 1.0f, unit0 + k, units, w);
+#pragma unroll
+      for (int i = 0; i < H; ++i) {
+        const Pair xhat = rows::mul(rows::add(x[i], minus), scale);
+        o[i] = rows::fma(xhat, c2, rows::fma(g[i], w[i], c1));
+      }
       if (P.grad_sum) {
-        load<BF16, VEC, T>(P.grad_sum, r * P.sgs, P.cols, v, t, o);
+        rows::numbers<BF16>(rows::unit<ALIGNED>(slot + 2 * array_bytes, shift_s, k), x);
+#pragma unroll
+        for (int i = 0; i < H; ++i) o[i] = rows::fma(scale, o[i], x[i]);
       } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = 0.0f;
+        for (int i = 0; i < H; ++i) o[i] = rows::mul(scale, o[i]);
       }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = fmaf(rstd, g[v][e] - c1 - h[v][e] * c2, o[e]);
-      store<BF16, VEC, T>(P.y, r * P.sy, P.cols, v, t, o);
+      if (ALIGNED) {
+        rows::store_aligned<BF16>(out, k, left, rows::pack<BF16>(o));
+      } else {
+        __syncwarp();  // the neighbours have read this unit of x
+        rows::shared_store(slot + 16 * k, rows::pack<BF16>(o));
+      }
+    }
+    if (!ALIGNED) {
+      __syncwarp();
+      rows::store_shifted<BF16, L, V>(slot, out, left, sub, n);
+      __syncwarp();
     }
   }
+  rows::copies_wait(0);
   if (!P.partial) return;
-  float* out = P.partial + static_cast<long long>(blockIdx.x) * 2 * P.cols;
-  if constexpr (kGroups > 1) {
-    // the groups' sums, one group after another
-    for (int k = 0; k < kGroups; ++k) {
-      if (group == k) {
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int i = (v * 8 + e) * T + t;
-            sums[i] = k ? sums[i] + dw[v][e] : dw[v][e];
-            sums[V * 8 * T + i] = k ? sums[V * 8 * T + i] + db[v][e] : db[v][e];
-          }
-      }
-      __syncthreads();
-    }
-    if (group != 0) return;
+  // the rows of a warp, then the groups one after another in shared memory
+  if constexpr (L < 32) {
 #pragma unroll
     for (int v = 0; v < V; ++v)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        dw[v][e] = sums[(v * 8 + e) * T + t];
-        db[v][e] = sums[V * 8 * T + (v * 8 + e) * T + t];
-      }
+      for (int i = 0; i < H; ++i)
+#pragma unroll
+        for (int o = L; o < 32; o <<= 1) {
+          dw[v][i] = rows::add(dw[v][i], __shfl_xor_sync(0xFFFFFFFFu, dw[v][i], o));
+          db[v][i] = rows::add(db[v][i], __shfl_xor_sync(0xFFFFFFFFu, db[v][i], o));
+        }
   }
+  Pair* sums = reinterpret_cast<Pair*>(dynamic);  // [2][units * H]
+  __syncthreads();                                // (every slot and weight has been read)
+  for (int q = 0; q < S::kGroups; ++q) {
+    if (group == q && lane < L) {
 #pragma unroll
-  for (int v = 0; v < V; ++v)
+      for (int v = 0; v < V; ++v) {
+        if (v >= n) break;
+        const int c = (unit0 + v * L + sub) * H;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int c = column<VEC, T>(v, e, t);
-      if (c < P.cols && MUON_CHECK(static_cast<int>(blockIdx.x) < P.parts)) {
-        out[c] = dw[v][e];
-        out[P.cols + c] = db[v][e];
+        for (int i = 0; i < H; ++i) {
+          sums[c + i] = q ? rows::add(sums[c + i], dw[v][i]) : dw[v][i];
+          sums[units * H + c + i] = q ? rows::add(sums[units * H + c + i], db[v][i]) : db[v][i];
+        }
       }
     }
+    __syncthreads();
+  }
+  if (!MUON_CHECK(static_cast<int>(blockIdx.x) < P.parts)) return;
+  float* out = P.partial + static_cast<long long>(blockIdx.x) * 2 * P.cols;
+  const float* all = reinterpret_cast<const float*>(dynamic);
+  for (int i = threadIdx.x; i < 2 * P.cols; i += S::kThreads) out[i] = all[i < P.cols ? i : units * E + i - P.cols];
 }
 
-// Adds the partial sums: 32 columns a CTA, its 8 warps take parts in turn.
-__global__ void __launch_bounds__(256) norm_columns(const __grid_constant__ RowParams P) {
-  __shared__ float2 part[8][33];
+// Adds the partial sums: 32 columns a CTA, its warps take parts in turn.
+constexpr int kColumnWarps = 32;
+
+__global__ void __launch_bounds__(32 * kColumnWarps) norm_columns(const __grid_constant__ RowParams P) {
+  __shared__ float2 part[kColumnWarps][33];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int c = static_cast<int>(blockIdx.x) * 32 + lane;
   float a = 0.0f, b = 0.0f;
   if (c < P.cols) {
-#pragma unroll 4
-    for (int p = w; p < P.parts; p += 8) {
+#pragma unroll 8
+    for (int p = w; p < P.parts; p += kColumnWarps) {
       const float* row = P.partial + static_cast<long long>(p) * 2 * P.cols;
       a += row[c];
       b += row[P.cols + c];
@@ -354,15 +489,14 @@ __global__ void __launch_bounds__(256) norm_columns(const __grid_constant__ RowP
   }
   part[w][lane] = make_float2(a, b);
   __syncthreads();
-  if (w == 0 && c < P.cols) {
-    a = b = 0.0f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      a += part[k][lane].x;
-      b += part[k][lane].y;
-    }
-    if (P.grad_weight) P.grad_weight[c] = a;
-    if (P.grad_bias) P.grad_bias[c] = b;
+  // a warp a column: its 32 parts
+  const float2 q = part[lane][w];
+  a = warp_sum(q.x);
+  b = warp_sum(q.y);
+  const int col = static_cast<int>(blockIdx.x) * 32 + w;
+  if (lane == 0 && col < P.cols) {
+    if (P.grad_weight) P.grad_weight[col] = a;
+    if (P.grad_bias) P.grad_bias[col] = b;
   }
 }
 
@@ -477,48 +611,81 @@ __global__ void __launch_bounds__(256) norm_columns_wide(const __grid_constant__
 
 // ---------------------------------------------------------------- launches
 using KernelPtr = void (*)(RowParams);
+constexpr int kSmemLimit = 220 * 1024;
 
-struct Choice {
+struct Form {
   KernelPtr fn;
-  int threads, rows_per_cta, capacity, smem;
+  int threads, rows_per_cta, capacity;  // capacity: entries of a row
+  int lanes, warps, entries;            // lanes of a warp and warps per row, entries of a unit
 };
 
-template <bool BACKWARD, bool BF16, bool VEC, int W, int V>
-Choice choice() {
-  Choice c;
+template <bool BACKWARD, bool BF16, bool ALIGNED, int L, int W>
+Form form() {
+  using S = Shape<BF16, L, W>;
+  KernelPtr fn;
   if constexpr (BACKWARD)
-    c.fn = norm_backward<BF16, VEC, W, V>;
+    fn = norm_backward<BF16, ALIGNED, L, W>;
   else
-    c.fn = norm_forward<BF16, VEC, W, V>;
-  c.threads = threads_of(W);
-  c.rows_per_cta = c.threads / (32 * W);
-  c.capacity = 32 * W * V * 8;
-  c.smem = BACKWARD && c.rows_per_cta > 1 ? 2 * V * 8 * 32 * W * 4 : 0;
-  return c;
+    fn = norm_forward<BF16, ALIGNED, L, W>;
+  return {fn, S::kThreads, S::kGroups * S::kRows, S::kCapacity, L, W, S::kE};
 }
 
-// The narrowest form that holds a row; false: none does.
-template <bool BACKWARD, bool BF16, bool VEC>
-bool choose(int64_t cols, Choice& out) {
-  const Choice all[] = {choice<BACKWARD, BF16, VEC, 1, 1>(), choice<BACKWARD, BF16, VEC, 1, 2>(),
-                        choice<BACKWARD, BF16, VEC, 1, 3>(), choice<BACKWARD, BF16, VEC, 1, 4>(),
-                        choice<BACKWARD, BF16, VEC, 4, 2>(), choice<BACKWARD, BF16, VEC, 8, 2>(),
-                        choice<BACKWARD, BF16, VEC, 16, 2>(), choice<BACKWARD, BF16, VEC, 16, 4>()};
-  for (const Choice& c : all)
-    if (cols <= c.capacity) {
-      out = c;
-      return true;
-    }
-  return false;
+// The narrowest form that holds a row: 4 lanes up to 128 entries, doubled up to a
+// warp (1024), then whole warps up to 16 (16384).  Null: none does.  Where rows are
+// few, a form with one unit a lane, for their latency.
+template <bool BACKWARD, bool BF16, bool ALIGNED>
+const Form* choose(int64_t cols, bool few) {
+  static const Form all[] = {form<BACKWARD, BF16, ALIGNED, 4, 1>(),  form<BACKWARD, BF16, ALIGNED, 8, 1>(),
+                             form<BACKWARD, BF16, ALIGNED, 16, 1>(), form<BACKWARD, BF16, ALIGNED, 32, 1>(),
+                             form<BACKWARD, BF16, ALIGNED, 32, 2>(), form<BACKWARD, BF16, ALIGNED, 32, 4>(),
+                             form<BACKWARD, BF16, ALIGNED, 32, 8>(), form<BACKWARD, BF16, ALIGNED, 32, 16>()};
+  const int64_t want = few ? cols * Shape<BF16, 32, 1>::kV : cols;
+  for (const Form& f : all)
+    if (want <= f.capacity) return &f;
+  return cols <= all[7].capacity ? &all[7] : nullptr;
 }
 
 template <bool BACKWARD>
-bool choose(bool bf16, bool vec, int64_t cols, Choice& c) {
-  if (bf16) return vec ? choose<BACKWARD, true, true>(cols, c) : choose<BACKWARD, true, false>(cols, c);
-  return vec ? choose<BACKWARD, false, true>(cols, c) : choose<BACKWARD, false, false>(cols, c);
+const Form* choose(bool bf16, bool aligned, int64_t cols, bool few) {
+  if (bf16) return aligned ? choose<BACKWARD, true, true>(cols, few) : choose<BACKWARD, true, false>(cols, few);
+  return aligned ? choose<BACKWARD, false, true>(cols, few) : choose<BACKWARD, false, false>(cols, few);
 }
 
-constexpr int kMaxParts = 608;  // rows of partial sums: four CTAs per SM
+// CTAs of a kernel that an SM holds with so much shared memory; the first
+// query on a device raises the kernel's limit there.  0: an error.
+int resident(const Form& f, int smem) {
+  static std::mutex mu;
+  static std::map<std::tuple<int, KernelPtr, int>, int> known;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  std::lock_guard<std::mutex> lk(mu);
+  int& n = known[{dev, f.fn, smem}];
+  if (n == 0) {
+    const void* fn = reinterpret_cast<const void*>(f.fn);
+    int q = 0;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&q, fn, f.threads, smem) != cudaSuccess)
+      return 0;
+    n = std::max(q, 1);
+  }
+  return n;
+}
+
+// How a CTA's shared memory is used for rows of `cols` entries: `arrays` of them
+// are copied ahead, `vectors` weights held.  Two stages where they fit; weights
+// where they fit beside those.
+int layout(RowParams& P, const Form& f, int arrays, int vectors) {
+  const int lane_entries = f.lanes * f.warps * f.entries;
+  P.units_lane = static_cast<int>((P.cols + lane_entries - 1) / lane_entries);
+  const int units = P.units_lane * f.lanes * f.warps;
+  const int stage = arrays * (P.units_lane * f.lanes + 1) * 16 * (f.threads / f.lanes);
+  const int held = vectors * units * f.entries * 4;
+  P.stages = 2 * stage <= kSmemLimit ? 2 : 1;
+  P.weights_shared = held + P.stages * stage <= kSmemLimit;
+  return P.stages * stage + (P.weights_shared ? held : 0);
+}
+
+constexpr int kMaxParts = 608;  // rows of partial sums: four CTAs per SM at most
 constexpr int kWideParts = 64;
 
 cudaError_t launch(const void* fn, dim3 grid, int threads, int smem, const RowParams& P, cudaStream_t stream) {
@@ -606,11 +773,12 @@ extern "C" muon_status_t layer_norm(const void* x, int dtype, int64_t rows, int6
                    rows_aligned(sum, sum_stride);
   cudaStream_t str = static_cast<cudaStream_t>(stream);
   const bool bf16 = dtype == MUON_BF16;
-  Choice c;
   cudaError_t e;
-  if (choose<false>(bf16, vec, cols, c)) {
-    const int64_t ctas = std::min<int64_t>((rows + c.rows_per_cta - 1) / c.rows_per_cta, static_cast<int64_t>(sms) * 64);
-    e = launch(reinterpret_cast<const void*>(c.fn), dim3(static_cast<unsigned>(ctas)), c.threads, c.smem, P, str);
+  if (const Form* f = choose<false>(bf16, vec, cols, rows <= 2 * sms)) {
+    const int smem = layout(P, *f, residual ? 2 : 1, 2), per_sm = resident(*f, smem);
+    if (per_sm == 0) return MUON_ERR_CUDA;
+    const int64_t ctas = std::min<int64_t>((rows + f->rows_per_cta - 1) / f->rows_per_cta, static_cast<int64_t>(sms) * per_sm);
+    e = launch(reinterpret_cast<const void*>(f->fn), dim3(static_cast<unsigned>(ctas)), f->threads, smem, P, str);
   } else {
     e = launch(bf16 ? reinterpret_cast<const void*>(&norm_forward_wide<true>) : reinterpret_cast<const void*>(&norm_forward_wide<false>),
                dim3(static_cast<unsigned>(std::min<int64_t>(rows, sms * 2))), kWide, 0, P, str);
@@ -620,8 +788,7 @@ extern "C" muon_status_t layer_norm(const void* x, int dtype, int64_t rows, int6
 
 extern "C" size_t layer_norm_backward_workspace_size(int64_t rows, int64_t cols) {
   if (rows < 0 || cols < 1 || cols > kMaxCols || rows > 0x7FFFFFFF) return 0;
-  Choice c;
-  const bool wide = !choose<true>(true, true, cols, c);
+  const bool wide = !choose<true>(true, true, cols, false);
   return static_cast<size_t>(wide ? kWideParts : kMaxParts) * 2 * cols * 4 + (wide ? static_cast<size_t>(rows) * 8 : 0);
 }
 
@@ -638,8 +805,7 @@ extern "C" muon_status_t layer_norm_backward(const void* grad, int64_t grad_stri
   if (std::max({row_stride, grad_stride, grad_x_stride, grad_sum ? grad_sum_stride : 0}) > (1LL << 32))
     return MUON_ERR_TOO_LARGE;
   const bool columns = grad_weight || grad_bias;
-  Choice c;
-  const bool wide = !choose<true>(true, true, cols, c);
+  const bool wide = !choose<true>(true, true, cols, false);
   const size_t need = layer_norm_backward_workspace_size(rows, cols);
   if (rows > 0) {
     if (!grad || !x || !mean || !rstd || !grad_x) return MUON_ERR_INVALID_ARG;
@@ -696,11 +862,13 @@ extern "C" muon_status_t layer_norm_backward(const void* grad, int64_t grad_stri
     auto rows_aligned = [&](const void* p, int64_t stride) { return !p || (aligned_to(p, 16) && stride * size % 16 == 0); };
     const bool vec = rows_aligned(x, row_stride) && rows_aligned(grad, grad_stride) &&
                      rows_aligned(grad_sum, grad_sum_stride) && rows_aligned(grad_x, grad_x_stride);
-    choose<true>(bf16, vec, cols, c);
-    P.parts = static_cast<int>(std::min<int64_t>({(rows + c.rows_per_cta - 1) / c.rows_per_cta, sms * 4, kMaxParts}));
-    e = launch(reinterpret_cast<const void*>(c.fn), dim3(static_cast<unsigned>(P.parts)), c.threads, c.smem, P, str);
+    const Form& f = *choose<true>(bf16, vec, cols, rows <= 2 * sms);
+    const int smem = layout(P, f, grad_sum ? 3 : 2, 1), per_sm = resident(f, smem);
+    if (per_sm == 0) return MUON_ERR_CUDA;
+    P.parts = static_cast<int>(std::min<int64_t>({(rows + f.rows_per_cta - 1) / f.rows_per_cta, static_cast<int64_t>(sms) * per_sm, kMaxParts}));
+    e = launch(reinterpret_cast<const void*>(f.fn), dim3(static_cast<unsigned>(P.parts)), f.threads, smem, P, str);
   } else {
-    P.rows2 = reinterpret_cast<float2*>(static_cast<char*>(workspace) + static_cast<size_t>(kWideParts) * 2 * cols * 4);
+    P.rows2 = reinterpret_cast<float2*>(static_cast<char*>(workspace) + static_cast<size_t>(kWideParts) * 2 * P.cols * 4);
     P.parts = static_cast<int>(std::min<int64_t>(rows, kWideParts));
     e = launch(bf16 ? reinterpret_cast<const void*>(&norm_rows_wide<true>) : reinterpret_cast<const void*>(&norm_rows_wide<false>),
                dim3(static_cast<unsigned>(std::min<int64_t>(rows, sms * 2))), kWide, 0, P, str);
@@ -709,6 +877,6 @@ extern "C" muon_status_t layer_norm_backward(const void* grad, int64_t grad_stri
                  dim3(static_cast<unsigned>((cols + 255) / 256), static_cast<unsigned>(P.parts)), 256, 0, P, str);
   }
   if (e == cudaSuccess && columns)
-    e = launch(reinterpret_cast<const void*>(&norm_columns), dim3(static_cast<unsigned>((cols + 31) / 32)), 256, 0, P, str);
+    e = launch(reinterpret_cast<const void*>(&norm_columns), dim3(static_cast<unsigned>((cols + 31) / 32)), 32 * kColumnWarps, 0, P, str);
   return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
 }
