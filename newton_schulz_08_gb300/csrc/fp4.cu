@@ -26,6 +26,7 @@
 #include "check.cuh"
 #include "fp4.h"
 #include "host.h"
+#include "rows.cuh"
 
 namespace muon {
 namespace {
@@ -60,13 +61,15 @@ __host__ __device__ __forceinline__ uint32_t mix(uint32_t x) {
   return x ^ x >> 16;
 }
 
-// Random bits of entries 2 j and 2 j + 1 of a row of the operand (low and
-// high half), j counted through the operand.
-__device__ __forceinline__ uint32_t random32(uint64_t j, uint32_t key) {
-  return mix(static_cast<uint32_t>(j) * kC0 + key + static_cast<uint32_t>(j >> 32) * kC1);
+// Random bits of entries 2 (j + k) and 2 (j + k) + 1 of the operand (low and high
+// half), counted through its rows; j is a multiple of 4 or k is 0 .. 3 of
+// one row, so that only j may carry into the upper half.
+__device__ __forceinline__ uint32_t random32(uint64_t j, int k, uint32_t key) {
+  const uint64_t i = j + static_cast<uint64_t>(k);
+  return mix(static_cast<uint32_t>(i) * kC0 + key + static_cast<uint32_t>(i >> 32) * kC1);
 }
 
-__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+using rows::Pair;
 
 // 2^e, e in -127 .. 127.
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(e < -126 ? 1u << 22 : static_cast<uint32_t>(e + 127) << 23); }
@@ -78,10 +81,13 @@ __device__ __forceinline__ int tensor_exponent(uint32_t amax) {
 
 // A block's scale: its code, and what its entries are divided by.
 struct Scale {
-  uint32_t code;
-  float up;     // block 32: entries times this are in units of the scale; block 16: times 2^-k
-  float s, r;   // block 16: then divided by s, r = 1 / s rounded
+  uint32_t code;  // 0xFF / 0x7F: NaN
+  float up;       // block 32: entries times this are in units of the scale; block 16: times 2^-k
+  float s, r;     // block 16: then divided by s, r = 1 / s rounded (0 for 0)
 };
+
+template <int BLOCK>
+__host__ __device__ constexpr uint32_t nan_code() { return BLOCK == 32 ? 0xFFu : 0x7Fu; }
 
 template <int BLOCK, bool SR>
 __device__ __forceinline__ Scale block_scale(uint32_t amax, float up_tensor) {
@@ -89,8 +95,8 @@ __device__ __forceinline__ Scale block_scale(uint32_t amax, float up_tensor) {
   const bool bad = amax >= 0x7F800000u;  // infinite or NaN
   if constexpr (BLOCK == 32) {
     const int e = max(static_cast<int>((amax + 0x3FFFFFu) >> 23) - 129, -127);  // 6 = 1.5 * 2^2
-    q.code = bad ? 0xFFu : static_cast<uint32_t>(e + 127);
-    q.up = bad ? 0.0f : pow2(-e);
+    q.code = bad ? nan_code<32>() : static_cast<uint32_t>(e + 127);
+    q.up = bad ? 0.0f : __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
     q.s = q.r = 1.0f;
   } else {
     const float sixth = __fdiv_rn(__uint_as_float(amax), 6.0f), want = sixth * up_tensor;
@@ -104,82 +110,156 @@ __device__ __forceinline__ Scale block_scale(uint32_t amax, float up_tensor) {
     // upwards: nothing is cut off, so that rounding stays right in the mean (`want` may have left float32's range)
     if (SR && !bad && (code == 0 ? sixth > 0.0f : value(code) < want)) ++code;
     q.s = value(code);
-    q.code = bad ? 0x7Fu : code;
+    q.code = bad ? nan_code<16>() : code;
     q.up = bad ? 0.0f : up_tensor;
     q.r = code == 0 ? 0.0f : __frcp_rn(q.s);
   }
   return q;
 }
 
+// Eight numbers by their scale, rounded to nearest.  Blocks of 16: x / s is the
+// product with the rounded reciprocal, corrected by its remainder, which
+// makes it the correctly rounded quotient; signs are chosen so that a zero keeps its own.
 template <int BLOCK>
-__device__ __forceinline__ float in_units(float x, const Scale& q) {
-  float y = x * q.up;
-  if constexpr (BLOCK == 16) {
-    // y / s to nearest: the product with the rounded reciprocal, corrected by its remainder
-    // (which would turn -0 into 0)
-    const float t = y * q.r;
-    y = copysignf(fmaf(fmaf(-t, q.s, y), q.r, t), x);
-  }
-  return y;
-}
-
-// Two codes, `lo` in the low half of a byte.
-__device__ __forceinline__ uint32_t codes_nearest(float lo, float hi) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\tcvt.u32.u8 %0, b;\n\t}" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-// One code: the significand's kept bits after a random number below the last
-// of them is added.  Magnitudes below 1 are moved up by 1, where the spacing
-// 0.5 of the codes is that of the kept bits; the sum is rounded towards zero,
-// which decides as the exact one does.
-__device__ __forceinline__ uint32_t code_random(float y, uint32_t r16) {
-  const float a = fminf(fabsf(y), 6.0f);
-  const bool small = a < 1.0f;
-  const float t = small ? __fadd_rz(a, 1.0f) : a;
-  const uint32_t c = ((__float_as_uint(t) + (r16 << 6) + 32u) >> 22) - (small ? 254u : 252u);
-  return c | (__float_as_uint(y) >> 28 & 8u);
-}
-
-template <bool SR>
-__device__ __forceinline__ uint32_t code_pair(float lo, float hi, uint32_t bits) {
-  if constexpr (SR) return code_random(lo, bits & 0xFFFFu) | code_random(hi, bits >> 16) << 4;
-  return codes_nearest(lo, hi);
-}
-
-// Eight entries of a row from column c0 on, zeros past its end.
-template <bool BF16>
-__device__ __forceinline__ void load8(const QuantParams& P, long long row, int c0, float (&v)[8]) {
+__device__ __forceinline__ void in_units(Pair (&x)[4], const Scale& q) {
+  if constexpr (BLOCK == 32) {
+    const Pair up = rows::pair(q.up);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) v[k] = 0.0f;
-  if (row >= P.rows || c0 >= P.cols) return;
-  const long long at = row * P.stride + c0;
-  if (P.vec && c0 + 8 <= P.cols) {
-    if constexpr (BF16) {
-      const uint4 q = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(P.x) + at));
-      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    for (int k = 0; k < 4; ++k) x[k] = rows::mul(x[k], up);
+  } else {
+    const Pair up = rows::pair(-q.up), r = rows::pair(-q.r), s = rows::pair(q.s);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const Pair y = rows::mul(x[k], up), t = rows::mul(y, r);
+      x[k] = rows::fma(rows::fma(t, s, y), r, t);
+    }
+  }
+}
+
+// Eight codes, the first in the low bits, of numbers in units of their scale.
+__device__ __forceinline__ uint32_t codes_nearest(const Pair (&y)[4]) {
+  float v[8];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) rows::split(y[k], v[2 * k], v[2 * k + 1]);
+  uint32_t w;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(w)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return w;
+}
+
+// The same with random numbers: a random number below the last kept bit of the
+// significand is added and the rest dropped.  Times 2^-126, rounded towards zero
+// (which decides as the exact number does), magnitudes below 1 are float32's
+// subnormal numbers, whose spacing is that of the codes 0 and 0.5: then the
+// exponent and the highest bit of the significand are the code.  `bits`: one word per two numbers.
+template <int BLOCK>
+__device__ __forceinline__ uint32_t codes_random(const Pair (&y)[4], const uint32_t (&bits)[4]) {
+  const Pair least = rows::pair(__uint_as_float(1u << 23));  // 2^-126
+  uint32_t w = 0;
+#pragma unroll
+  for (int k = 3; k >= 0; --k) {
+    Pair t;
+    asm("mul.rz.f32x2 %0, %1, %2;" : "=l"(t) : "l"(y[k]), "l"(least));
+    float v[2];
+    rows::split(t, v[0], v[1]);
+#pragma unroll
+    for (int h = 1; h >= 0; --h) {
+      const uint32_t b = __float_as_uint(v[h]);
+      // (the largest code may be passed by the quotient's rounding: blocks of 16)
+      uint32_t m = b << 6;
+      if (BLOCK == 16) m = min(m, 7u << 28);
+      const uint32_t r = ((h ? bits[k] >> 4 : bits[k] << 12) & 0x0FFFF000u) | 0x800u;
+      w = __funnelshift_l((m + r) | (b & 0x80000000u), w, 4);
+    }
+  }
+  return w;
+}
+
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {  // of unsigned halves
+  uint32_t m;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(m) : "r"(a), "r"(b));
+  return m;
+}
+
+// A thread's 8 entries of a row, as loaded: one more unit where rows do not
+// begin on 16 bytes.
+template <bool BF16>
+struct Loaded {
+  static constexpr int n = BF16 ? 1 : 2;
+  uint4 q[n + 1];
+};
+
+// Entries [c, c + 8) of row `row`; 16 neighbouring lanes have 128 neighbouring
+// entries.  Only units that hold an entry of the row are read.
+template <bool BF16>
+__device__ __forceinline__ void load8(const QuantParams& P, int row, int c, Loaded<BF16>& l) {
+  constexpr int size = BF16 ? 2 : 4, n = Loaded<BF16>::n;
+  const char* p = static_cast<const char*>(P.x) + (row * P.stride + c) * size;
+  const uint32_t shift = P.vec ? 0u : rows::shift_of(p);
+  p -= shift;
+  const int have = row < P.rows ? (P.cols - c) * size + static_cast<int>(shift) : 0;  // bytes from p on
+#pragma unroll
+  for (int i = 0; i <= n; ++i) {
+    l.q[i] = make_uint4(0, 0, 0, 0);
+    if (have > 16 * i && (i < n || (shift != 0 && (threadIdx.x & 15) == 15))) l.q[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+  }
+}
+
+// The entries, zeros past the row's end (all lanes of a warp).
+template <bool BF16>
+__device__ __forceinline__ void settle(const QuantParams& P, int row, int c, Loaded<BF16>& l) {
+  constexpr int size = BF16 ? 2 : 4, n = Loaded<BF16>::n, per = 16 / size;
+  if (!P.vec) {
+    const uint32_t shift = rows::shift_of(static_cast<const char*>(P.x) + (row * P.stride + c) * size);
+    uint4 next;
+    next.x = __shfl_down_sync(0xFFFFFFFFu, l.q[0].x, 1);
+    next.y = __shfl_down_sync(0xFFFFFFFFu, l.q[0].y, 1);
+    next.z = __shfl_down_sync(0xFFFFFFFFu, l.q[0].z, 1);
+    next.w = __shfl_down_sync(0xFFFFFFFFu, l.q[0].w, 1);
+    if ((threadIdx.x & 15) == 15) next = l.q[n];
+    if (shift) {
+#pragma unroll
+      for (int i = 0; i < n; ++i) l.q[i] = rows::funnel(l.q[i], i + 1 < n ? l.q[i + 1] : next, shift);
+    }
+  }
+  if (c + 8 > P.cols) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      uint32_t w[4] = {l.q[i].x, l.q[i].y, l.q[i].z, l.q[i].w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        v[2 * k] = __uint_as_float(w[k] << 16);
-        v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+        const int e = c + i * per + (BF16 ? 2 * k : k);
+        if (e >= P.cols) w[k] = 0;
+        if (BF16 && e + 1 >= P.cols) w[k] &= 0xFFFFu;
       }
-    } else {
-      const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(P.x) + at);
-      const float4 a = __ldg(f), b = __ldg(f + 1);
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+      l.q[i] = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    return;
-  }
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    if (c0 + k >= P.cols) continue;
-    if constexpr (BF16)
-      v[k] = __bfloat162float(static_cast<const __nv_bfloat16*>(P.x)[at + k]);
-    else
-      v[k] = static_cast<const float*>(P.x)[at + k];
   }
 }
+
+// Largest magnitude of 8 entries, as the bits of a float.
+template <bool BF16>
+__device__ __forceinline__ uint32_t largest(const Loaded<BF16>& l) {
+  if constexpr (BF16) {
+    const uint4& q = l.q[0];
+    return max2(max2(q.x & 0x7FFF7FFFu, q.y & 0x7FFF7FFFu), max2(q.z & 0x7FFF7FFFu, q.w & 0x7FFF7FFFu));
+  } else {
+    const uint4 &a = l.q[0], &b = l.q[1];
+    constexpr uint32_t m = 0x7FFFFFFFu;
+    return max(max(max(a.x & m, a.y & m), max(a.z & m, a.w & m)), max(max(b.x & m, b.y & m), max(b.z & m, b.w & m)));
+  }
+}
+
+// (bfloat16: `m` holds two columns' halves until here)
+template <bool BF16>
+__device__ __forceinline__ uint32_t magnitude_bits(uint32_t m) { return BF16 ? max(m << 16, m & 0xFFFF0000u) : m; }
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return BF16 ? max2(a, b) : max(a, b); }
 
 constexpr int kStagePitch = 80;  // bytes of a staged row of codes across: 64 and a gap
 
@@ -187,7 +267,7 @@ template <bool BF16>
 __host__ __device__ constexpr int tile_bytes() { return kTile * kTile * (BF16 ? 2 : 4); }
 
 template <bool BF16, int BLOCK, bool SR, bool ALONG, bool ACROSS>
-__global__ void __launch_bounds__(kThreads) fp4_quantize_kernel(const __grid_constant__ QuantParams P) {
+__global__ void __launch_bounds__(kThreads, 3) fp4_quantize_kernel(const __grid_constant__ QuantParams P) {
   extern __shared__ __align__(16) uint8_t smem[];
   constexpr int kTiles = 32 / BLOCK;  // scale tiles of 128 entries of K
   __shared__ __align__(16) uint8_t sf_along[kTiles * 512], sf_across[kTiles * 512];
@@ -196,58 +276,61 @@ __global__ void __launch_bounds__(kThreads) fp4_quantize_kernel(const __grid_con
   const int tid = threadIdx.x;
   const int by = static_cast<int>(blockIdx.x) / P.tiles_x, bx = static_cast<int>(blockIdx.x) - by * P.tiles_x;
   const int r0 = by * kTile, c0 = bx * kTile;
-  float up = 1.0f;
-  if constexpr (BLOCK == 16) {
-    const int k = tensor_exponent(__float_as_uint(P.scale[1]));
-    up = pow2(-k);
-    if (blockIdx.x == 0 && tid == 0) P.scale[0] = pow2(k);
-  }
   uint8_t* tile = smem;
   uint8_t* stage = smem + tile_bytes<BF16>();
+  float up = 1.0f;
   {
     const int g = tid & 15;  // 8 columns
     const int col = c0 + 8 * g;
-    constexpr int kBatch = 4;
+    constexpr int kBatch = BF16 ? 8 : 4;  // rows of a thread in flight
 #pragma unroll
     for (int half = 0; half < 8 / kBatch; ++half) {
-      float v[kBatch][8];
+      Loaded<BF16> l[kBatch];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) load8<BF16>(P, r0 + (half * kBatch + i) * 16 + (tid >> 4), col, v[i]);
+      for (int i = 0; i < kBatch; ++i) load8<BF16>(P, r0 + (half * kBatch + i) * 16 + (tid >> 4), col, l[i]);
+      if constexpr (BLOCK == 16) {
+        if (half == 0) {
+          const int k = tensor_exponent(__float_as_uint(P.scale[1]));
+          up = pow2(-k);
+          if (blockIdx.x == 0 && tid == 0) P.scale[0] = pow2(k);
+        }
+      }
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         const int r = (half * kBatch + i) * 16 + (tid >> 4);
+        settle<BF16>(P, r0 + r, col, l[i]);
         if constexpr (ACROSS) {
-          if constexpr (BF16) {
-            uint4 w;
-            w.x = __byte_perm(__float_as_uint(v[i][0]), __float_as_uint(v[i][1]), 0x7632);
-            w.y = __byte_perm(__float_as_uint(v[i][2]), __float_as_uint(v[i][3]), 0x7632);
-            w.z = __byte_perm(__float_as_uint(v[i][4]), __float_as_uint(v[i][5]), 0x7632);
-            w.w = __byte_perm(__float_as_uint(v[i][6]), __float_as_uint(v[i][7]), 0x7632);
-            *reinterpret_cast<uint4*>(tile + r * (kTile * 2) + g * 16) = w;
-          } else {
-            float4* t = reinterpret_cast<float4*>(tile + r * (kTile * 4) + g * 32);
-            t[0] = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
-            t[1] = make_float4(v[i][4], v[i][5], v[i][6], v[i][7]);
-          }
+#pragma unroll
+          for (int u = 0; u < Loaded<BF16>::n; ++u)
+            *reinterpret_cast<uint4*>(tile + r * (kTile * (BF16 ? 2 : 4)) + (g * Loaded<BF16>::n + u) * 16) = l[i].q[u];
         }
         if constexpr (ALONG) {
-          uint32_t m = 0;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) m = max(m, magnitude(v[i][k]));
-          m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-          if constexpr (BLOCK == 32) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-          const Scale q = block_scale<BLOCK, SR>(m, up);
-          uint32_t word = 0;
-          const uint64_t j = static_cast<uint64_t>(r0 + r) * ((P.cols + 1) / 2) + col / 2;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t bits = SR ? random32(j + k, P.along.key) : 0u;
-            float lo = in_units<BLOCK>(v[i][2 * k], q), hi = in_units<BLOCK>(v[i][2 * k + 1], q);
-            if (q.up == 0.0f) lo = hi = 0.0f;  // 0 times what is not finite
-            word |= code_pair<SR>(lo, hi, bits) << (8 * k);
+          uint32_t m = largest<BF16>(l[i]);
+          m = larger<BF16>(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+          if constexpr (BLOCK == 32) m = larger<BF16>(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+          const Scale q = block_scale<BLOCK, SR>(magnitude_bits<BF16>(m), up);
+          Pair x[4];
+          if constexpr (BF16) {
+            rows::numbers<true>(l[i].q[0], x);
+          } else {
+            x[0] = rows::pair(__uint_as_float(l[i].q[0].x), __uint_as_float(l[i].q[0].y));
+            x[1] = rows::pair(__uint_as_float(l[i].q[0].z), __uint_as_float(l[i].q[0].w));
+            x[2] = rows::pair(__uint_as_float(l[i].q[1].x), __uint_as_float(l[i].q[1].y));
+            x[3] = rows::pair(__uint_as_float(l[i].q[1].z), __uint_as_float(l[i].q[1].w));
           }
-          if (r0 + r < P.rows && col / 2 < P.along.pitch &&
-              MUON_CHECK(col >= 0 && col / 2 + 4 <= P.along.pitch))
+          in_units<BLOCK>(x, q);
+          uint32_t word;
+          if constexpr (SR) {
+            const uint64_t j = static_cast<uint64_t>(r0 + r) * ((P.cols + 1) / 2) + col / 2;
+            uint32_t bits[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) bits[k] = random32(j, k, P.along.key);
+            word = codes_random<BLOCK>(x, bits);
+          } else {
+            word = codes_nearest(x);
+          }
+          if (q.code == nan_code<BLOCK>()) word = 0;  // (0 times what is not finite)
+          if (r0 + r < P.rows && col / 2 < P.along.pitch && MUON_CHECK(col >= 0 && col / 2 + 4 <= P.along.pitch))
             *reinterpret_cast<uint32_t*>(P.along.codes + (r0 + r) * P.along.pitch + col / 2) = word;
           const int b = BLOCK == 32 ? g >> 2 : g >> 1;
           if ((g & (BLOCK / 8 - 1)) == 0)
@@ -264,45 +347,60 @@ __global__ void __launch_bounds__(kThreads) fp4_quantize_kernel(const __grid_con
           reinterpret_cast<const uint4*>(sf_along)[tid];
   }
   if constexpr (ACROSS) {
-    // two columns by 32 rows a thread
-    const int cp = tid & 63, rb = tid >> 6;
-    float v[2][32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const int r = rb * 32 + i;
-      if constexpr (BF16) {
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(tile + r * (kTile * 2) + cp * 4);
-        v[0][i] = __uint_as_float(w << 16);
-        v[1][i] = __uint_as_float(w & 0xFFFF0000u);
-      } else {
-        const float2 f = *reinterpret_cast<const float2*>(tile + r * (kTile * 4) + cp * 8);
-        v[0][i] = f.x;
-        v[1][i] = f.y;
-      }
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int c = 2 * cp + h;
-      uint32_t word[4] = {0u, 0u, 0u, 0u};
+    // 32 rows of a column at a time: bfloat16, two columns a thread; float32, one, twice
+    constexpr int kColumns = BF16 ? 2 : 1;
+    auto column = [&](int c, int rb, const uint32_t (&v)[32], int h, const uint32_t (&top)[32 / BLOCK]) {
+      uint32_t word[4];
 #pragma unroll
       for (int b = 0; b < 32 / BLOCK; ++b) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < BLOCK; ++i) m = max(m, magnitude(v[h][b * BLOCK + i]));
+        const uint32_t m = BF16 ? (h ? top[b] & 0xFFFF0000u : top[b] << 16) : top[b];
         const Scale q = block_scale<BLOCK, SR>(m, up);
-        const uint64_t j = static_cast<uint64_t>(c0 + c) * ((P.rows + 1) / 2) + (r0 + rb * 32 + b * BLOCK) / 2;
+        uint64_t j = 0;
+        if constexpr (SR) j = static_cast<uint64_t>(c0 + c) * ((P.rows + 1) / 2) + (r0 + rb * 32 + b * BLOCK) / 2;
 #pragma unroll
-        for (int k = 0; k < BLOCK / 2; ++k) {
-          const uint32_t bits = SR ? random32(j + k, P.across.key) : 0u;
-          float lo = in_units<BLOCK>(v[h][b * BLOCK + 2 * k], q), hi = in_units<BLOCK>(v[h][b * BLOCK + 2 * k + 1], q);
-          if (q.up == 0.0f) lo = hi = 0.0f;
-          const int byte = b * BLOCK / 2 + k;
-          word[byte >> 2] |= code_pair<SR>(lo, hi, bits) << (8 * (byte & 3));
+        for (int o = 0; o < BLOCK / 8; ++o) {
+          Pair x[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t lo = v[b * BLOCK + o * 8 + 2 * k], hi = v[b * BLOCK + o * 8 + 2 * k + 1];
+            if constexpr (BF16)
+              x[k] = h ? rows::pair(__uint_as_float(lo & 0xFFFF0000u), __uint_as_float(hi & 0xFFFF0000u))
+                       : rows::pair(__uint_as_float(lo << 16), __uint_as_float(hi << 16));
+            else
+              x[k] = rows::pair(__uint_as_float(lo), __uint_as_float(hi));
+          }
+          in_units<BLOCK>(x, q);
+          uint32_t w;
+          if constexpr (SR) {
+            uint32_t bits[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) bits[k] = random32(j, o * 4 + k, P.across.key);
+            w = codes_random<BLOCK>(x, bits);
+          } else {
+            w = codes_nearest(x);
+          }
+          word[b * BLOCK / 8 + o] = q.code == nan_code<BLOCK>() ? 0u : w;
         }
         const int blk = rb * (32 / BLOCK) + b;  // along K within the tile
         sf_across[(blk >> 2) * 512 + (c & 31) * 16 + (c >> 5) * 4 + (blk & 3)] = c0 + c < P.cols ? q.code : 0;
       }
       *reinterpret_cast<uint4*>(stage + c * kStagePitch + rb * 16) = make_uint4(word[0], word[1], word[2], word[3]);
+    };
+#pragma unroll 1
+    for (int pass = 0; pass < 2 / kColumns; ++pass) {
+      const int item = pass * kThreads + tid;
+      const int cp = BF16 ? item & 63 : item & 127, rb = BF16 ? item >> 6 : item >> 7;
+      uint32_t v[32], top[32 / BLOCK];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = *reinterpret_cast<const uint32_t*>(tile + (rb * 32 + i) * (kTile * (BF16 ? 2 : 4)) + cp * 4);
+#pragma unroll
+      for (int b = 0; b < 32 / BLOCK; ++b) {
+        top[b] = 0;
+#pragma unroll
+        for (int i = 0; i < BLOCK; ++i) top[b] = larger<BF16>(top[b], v[b * BLOCK + i] & (BF16 ? 0x7FFF7FFFu : 0x7FFFFFFFu));
+      }
+#pragma unroll
+      for (int h = 0; h < kColumns; ++h) column(kColumns * cp + h, rb, v, h, top);
     }
     __syncthreads();
 #pragma unroll
@@ -320,84 +418,113 @@ __global__ void __launch_bounds__(kThreads) fp4_quantize_kernel(const __grid_con
   }
 }
 
-// Largest finite magnitude of a matrix, as the bits of a float, into *out (0 before).
+// Largest finite magnitude of a matrix, as the bits of a float, into *out (0
+// before): 128 x 128 entries a step, all of a thread's loads in flight.
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads) fp4_amax_kernel(const __grid_constant__ QuantParams P, uint32_t* out) {
+__global__ void __launch_bounds__(kThreads) fp4_amax_kernel(const __grid_constant__ QuantParams P, uint32_t* out, int steps) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  uint32_t m = 0;
-  const int groups = (P.cols + 7) / 8;
-  // 16 rows x 128 columns a step: 16 threads a row
-  const long long steps_c = (groups + 15) / 16, steps = steps_c * ((P.rows + 15) / 16);
-  for (long long s = blockIdx.x; s < steps; s += gridDim.x) {
-    float v[8];
-    const long long sr = s / steps_c;
-    load8<BF16>(P, sr * 16 + (threadIdx.x >> 4), static_cast<int>(s - sr * steps_c) * 128 + (threadIdx.x & 15) * 8, v);
+  uint32_t top = 0;
+  for (int s = blockIdx.x; s < steps; s += gridDim.x) {
+    const int by = s / P.tiles_x, r0 = by * kTile + (threadIdx.x >> 4), c = (s - by * P.tiles_x) * kTile + (threadIdx.x & 15) * 8;
+    Loaded<BF16> l[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const uint32_t a = magnitude(v[k]);
-      if (a < 0x7F800000u) m = max(m, a);
+    for (int i = 0; i < 8; ++i) load8<BF16>(P, r0 + 16 * i, c, l[i]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      settle<BF16>(P, r0 + 16 * i, c, l[i]);
+      uint32_t m = magnitude_bits<BF16>(largest<BF16>(l[i]));
+      if (m >= 0x7F800000u) {  // some are not finite: the others one by one
+        m = 0;
+#pragma unroll
+        for (int u = 0; u < Loaded<BF16>::n; ++u) {
+          const uint32_t w[4] = {l[i].q[u].x, l[i].q[u].y, l[i].q[u].z, l[i].q[u].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t a = BF16 ? w[k] << 16 & 0x7FFFFFFFu : w[k] & 0x7FFFFFFFu, b = BF16 ? w[k] & 0x7FFF0000u : 0u;
+            if (a < 0x7F800000u) m = max(m, a);
+            if (b < 0x7F800000u) m = max(m, b);
+          }
+        }
+      }
+      top = max(top, m);
     }
   }
-  m = __reduce_max_sync(0xFFFFFFFFu, m);
-  if ((threadIdx.x & 31) == 0 && m) atomicMax(out, m);
+  top = __reduce_max_sync(0xFFFFFFFFu, top);
+  if ((threadIdx.x & 31) == 0 && top) atomicMax(out, top);
 }
 
-// The numbers that codes stand for: 8 codes a thread.
+// The numbers that codes stand for: a lane takes 8 codes (4 bytes), a warp 256
+// of a row.  E2M1 numbers as bfloat16 come byte-wise from two tables of 8 that fit in registers.
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads) fp4_values_kernel(const uint8_t* codes, const uint8_t* scales, const float* scale,
                                                               int rows, int cols, int block, long long pitch,
                                                               long long ktiles, void* out, long long stride, int vec) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int groups = (cols + 7) / 8;
+  const int pieces = (cols + 255) / 256, lane = threadIdx.x & 31;
   const float tensor = block == 16 ? *scale : 1.0f;
-  const long long total = static_cast<long long>(rows) * groups;
-  for (long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; i < total;
-       i += static_cast<long long>(gridDim.x) * kThreads) {
-    const long long r = i / groups;
-    const int c = static_cast<int>(i - r * groups) * 8;
-    const uint32_t word = *reinterpret_cast<const uint32_t*>(codes + r * pitch + c / 2);
-    const long long b = c / block;
-    const uint32_t code = scales[((r >> 7) * ktiles + (b >> 2)) * 512 + (r & 31) * 16 + ((r & 127) >> 5) * 4 + (b & 3)];
-    float s;
-    if (block == 32) {
-      s = code == 255 ? NAN : pow2(static_cast<int>(code) - 127);
-    } else {
-      s = code == 0x7F ? NAN : code < 8 ? code * 0.001953125f : __uint_as_float((code << 20) + (120u << 23));
-      s *= tensor;
-    }
-    float v[8];
+  const int shift = block == 16 ? 4 : 5;
+  const long long total = static_cast<long long>(rows) * pieces, step = static_cast<long long>(gridDim.x) * (kThreads / 32);
+  constexpr int kBatch = 4;  // pieces of a warp in flight
+  for (long long base = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); base < total; base += step * kBatch) {
+    uint32_t word[kBatch], code[kBatch];
+    long long at[kBatch];
+    int from[kBatch];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const uint32_t q = word >> (4 * k) & 15u, e = q >> 1 & 3u, m = q & 1u;
-      const float a = e == 0 ? 0.5f * m : __uint_as_float((126u + e) << 23 | m << 22);
-      v[k] = (q & 8u ? -a : a) * s;
-    }
-    if constexpr (BF16) {
-      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out) + r * stride + c;
-      if (vec && c + 8 <= cols) {
-        uint32_t w[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
-          w[k] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        *reinterpret_cast<uint4*>(o) = make_uint4(w[0], w[1], w[2], w[3]);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (c + k < cols) o[k] = __float2bfloat16_rn(v[k]);
+    for (int i = 0; i < kBatch; ++i) {
+      const long long piece = base + i * step;
+      const long long r = total <= 0x7FFFFFFF ? static_cast<long long>(static_cast<uint32_t>(piece) / static_cast<uint32_t>(pieces)) : piece / pieces;
+      const int c = static_cast<int>(piece - r * pieces) * 256 + lane * 8;
+      from[i] = piece < total ? c : cols;
+      at[i] = r * stride + c;
+      word[i] = code[i] = 0;
+      if (from[i] < cols) {
+        word[i] = __ldg(reinterpret_cast<const uint32_t*>(codes + r * pitch + c / 2));
+        const int b = c >> shift;
+        code[i] = __ldg(scales + ((r >> 7) * ktiles + (b >> 2)) * 512 + (r & 31) * 16 + ((r & 127) >> 5) * 4 + (b & 3));
       }
-    } else {
-      float* o = static_cast<float*>(out) + r * stride + c;
-      if (vec && c + 8 <= cols) {
-        reinterpret_cast<float4*>(o)[0] = make_float4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<float4*>(o)[1] = make_float4(v[4], v[5], v[6], v[7]);
-      } else {
+    }
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (c + k < cols) o[k] = v[k];
+    for (int i = 0; i < kBatch; ++i) {
+      if (from[i] >= cols) continue;
+      float s;
+      if (block == 32) {
+        s = code[i] == 255 ? NAN : pow2(static_cast<int>(code[i]) - 127);
+      } else {
+        s = code[i] == 0x7F ? NAN : code[i] < 8 ? code[i] * 0.001953125f : __uint_as_float((code[i] << 20) + (120u << 23));
+        s *= tensor;
+      }
+      Pair v[4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t four = word[i] >> (16 * h), select = four & 0x7777u;
+        const uint32_t hi = __byte_perm(0x3F3F3F00u, 0x40404040u, select), lo = __byte_perm(0xC0800000u, 0xC0804000u, select);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t a = __byte_perm(lo, hi, k ? 0x62 : 0x40) << 16, b = __byte_perm(lo, hi, k ? 0x73 : 0x51) << 16;
+          const uint32_t sa = four << (28 - 8 * k) & 0x80000000u, sb = four << (24 - 8 * k) & 0x80000000u;
+          v[2 * h + k] = rows::mul(rows::pair(__uint_as_float(a | sa), __uint_as_float(b | sb)), rows::pair(s));
+        }
+      }
+      if constexpr (BF16) {
+        const uint4 q = rows::pack<true>(v);
+        char* o = static_cast<char*>(out) + at[i] * 2;
+        if (vec && from[i] + 8 <= cols)
+          *reinterpret_cast<uint4*>(o) = q;
+        else
+          rows::store_some<true>(o, q, 0, cols - from[i]);
+      } else {
+        char* o = static_cast<char*>(out) + at[i] * 4;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const Pair two[2] = {v[2 * h], v[2 * h + 1]};
+          const uint4 q = rows::pack<false>(two);
+          if (vec && from[i] + 8 <= cols)
+            reinterpret_cast<uint4*>(o)[h] = q;
+          else
+            rows::store_some<false>(o + 16 * h, q, 0, cols - from[i] - 4 * h);
+        }
       }
     }
   }
@@ -523,10 +650,13 @@ extern "C" muon_status_t fp4_quantize(const void* x, int dtype, int64_t rows, in
   if (block == 16) {
     if (cudaMemsetAsync(P.scale + 1, 0, 4, str) != cudaSuccess) return MUON_ERR_CUDA;
     uint32_t* bits = reinterpret_cast<uint32_t*>(P.scale + 1);
-    const int64_t steps = (rows + 15) / 16 * ((cols + 127) / 128);
-    void* args[] = {&P, &bits};
+    const int64_t across_tiles = (cols + kTile - 1) / kTile;
+    QuantParams A = P;
+    A.tiles_x = static_cast<int>(across_tiles);
+    int steps = static_cast<int>((rows + kTile - 1) / kTile * across_tiles);
+    void* args[] = {&A, &bits, &steps};
     if (launch(bf16 ? reinterpret_cast<const void*>(&fp4_amax_kernel<true>) : reinterpret_cast<const void*>(&fp4_amax_kernel<false>),
-               dim3(static_cast<unsigned>(std::min<int64_t>(steps, sms * 8))), 0, args, str) != cudaSuccess)
+               dim3(static_cast<unsigned>(std::min(steps, sms * 8))), 0, args, str) != cudaSuccess)
       return MUON_ERR_CUDA;
   }
   void* args[] = {&P};
@@ -560,11 +690,11 @@ extern "C" muon_status_t fp4_values(const fp4_matrix* q, void* out, int dtype, i
   int rows = static_cast<int>(q->rows), cols = static_cast<int>(q->cols), block = q->block;
   long long pitch = fp4_pitch(q->cols), ktiles = fp4_ktiles(q->cols, block), stride = out_stride;
   int vec = aligned_to(out, 16) && out_stride * size % 16 == 0;
-  const int64_t groups = q->rows * ((q->cols + 7) / 8);
+  const int64_t groups = q->rows * ((q->cols + 255) / 256);  // warps' pieces
   void* args[] = {&codes, &scales, &scale, &rows, &cols, &block, &pitch, &ktiles, &out, &stride, &vec};
   if (launch(dtype == MUON_BF16 ? reinterpret_cast<const void*>(&fp4_values_kernel<true>)
                                 : reinterpret_cast<const void*>(&fp4_values_kernel<false>),
-             dim3(static_cast<unsigned>(std::min<int64_t>((groups + kThreads - 1) / kThreads, sms * 32))), 0, args,
+             dim3(static_cast<unsigned>(std::min<int64_t>((groups + 7) / 8, sms * 8))), 0, args,
              static_cast<cudaStream_t>(stream)) != cudaSuccess)
     return MUON_ERR_CUDA;
   return MUON_OK;
