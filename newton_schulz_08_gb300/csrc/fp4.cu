@@ -99,7 +99,11 @@ __device__ __forceinline__ Scale block_scale(uint32_t amax, float up_tensor) {
     q.up = bad ? 0.0f : __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
     q.s = q.r = 1.0f;
   } else {
-    const float sixth = __fdiv_rn(__uint_as_float(amax), 6.0f), want = sixth * up_tensor;
+    // max / 6 to nearest: corrected by its remainder, where that is no subnormal number
+    const float top = __uint_as_float(amax), t = top * (1.0f / 6.0f);
+    float sixth = fmaf(fmaf(t, -6.0f, top), 1.0f / 6.0f, t);
+    if (amax < (27u << 23) || bad) sixth = __fdiv_rn(top, 6.0f);  // below 2^-100
+    const float want = sixth * up_tensor;
     uint16_t c;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(0.0f), "f"(bad ? 0.0f : want));
     auto value = [](uint32_t code) {
@@ -112,7 +116,10 @@ __device__ __forceinline__ Scale block_scale(uint32_t amax, float up_tensor) {
     q.s = value(code);
     q.code = bad ? nan_code<16>() : code;
     q.up = bad ? 0.0f : up_tensor;
-    q.r = code == 0 ? 0.0f : __frcp_rn(q.s);
+    // 1 / s to nearest: one step from the hardware's reciprocal (s has four significant bits)
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(q.s));
+    q.r = code == 0 ? 0.0f : fmaf(r, fmaf(-q.s, r, 1.0f), r);
   }
   return q;
 }
@@ -185,89 +192,57 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {  // of unsign
   return m;
 }
 
-// A thread's 8 entries of a row, as loaded: one more unit where rows do not
-// begin on 16 bytes.
+// A row of the tile in shared memory: 128 entries, and where rows do not begin on
+// 16 bytes one unit more, as they lie in memory.
 template <bool BF16>
-struct Loaded {
-  static constexpr int n = BF16 ? 1 : 2;
-  uint4 q[n + 1];
+struct Tile {
+  static constexpr int size = BF16 ? 2 : 4;
+  static constexpr int units = BF16 ? 1 : 2;            // of a lane's 8 entries
+  static constexpr int pitch = kTile * size + 16;       // bytes of a row
+  static constexpr int bytes = kTile * pitch;
 };
 
-// Entries [c, c + 8) of row `row`; 16 neighbouring lanes have 128 neighbouring
-// entries.  Only units that hold an entry of the row are read.
-template <bool BF16>
-__device__ __forceinline__ void load8(const QuantParams& P, int row, int c, Loaded<BF16>& l) {
-  constexpr int size = BF16 ? 2 : 4, n = Loaded<BF16>::n;
-  const char* p = static_cast<const char*>(P.x) + (row * P.stride + c) * size;
-  const uint32_t shift = P.vec ? 0u : rows::shift_of(p);
-  p -= shift;
-  const int have = row < P.rows ? (P.cols - c) * size + static_cast<int>(shift) : 0;  // bytes from p on
-#pragma unroll
-  for (int i = 0; i <= n; ++i) {
-    l.q[i] = make_uint4(0, 0, 0, 0);
-    if (have > 16 * i && (i < n || (shift != 0 && (threadIdx.x & 15) == 15))) l.q[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
-  }
-}
+constexpr int kStagePitch = kTile + 4;            // words: codes of 8 rows, by row and column
+constexpr int kStageBytes = 16 * kStagePitch * 4;
 
-// The entries, zeros past the row's end (all lanes of a warp).
-template <bool BF16>
-__device__ __forceinline__ void settle(const QuantParams& P, int row, int c, Loaded<BF16>& l) {
-  constexpr int size = BF16 ? 2 : 4, n = Loaded<BF16>::n, per = 16 / size;
-  if (!P.vec) {
-    const uint32_t shift = rows::shift_of(static_cast<const char*>(P.x) + (row * P.stride + c) * size);
-    uint4 next;
-    next.x = __shfl_down_sync(0xFFFFFFFFu, l.q[0].x, 1);
-    next.y = __shfl_down_sync(0xFFFFFFFFu, l.q[0].y, 1);
-    next.z = __shfl_down_sync(0xFFFFFFFFu, l.q[0].z, 1);
-    next.w = __shfl_down_sync(0xFFFFFFFFu, l.q[0].w, 1);
-    if ((threadIdx.x & 15) == 15) next = l.q[n];
-    if (shift) {
-#pragma unroll
-      for (int i = 0; i < n; ++i) l.q[i] = rows::funnel(l.q[i], i + 1 < n ? l.q[i + 1] : next, shift);
-    }
-  }
-  if (c + 8 > P.cols) {
-#pragma unroll
-    for (int i = 0; i < n; ++i) {
-      uint32_t w[4] = {l.q[i].x, l.q[i].y, l.q[i].z, l.q[i].w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int e = c + i * per + (BF16 ? 2 * k : k);
-        if (e >= P.cols) w[k] = 0;
-        if (BF16 && e + 1 >= P.cols) w[k] &= 0xFFFFu;
-      }
-      l.q[i] = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-  }
-}
-
-// Largest magnitude of 8 entries, as the bits of a float.
-template <bool BF16>
-__device__ __forceinline__ uint32_t largest(const Loaded<BF16>& l) {
-  if constexpr (BF16) {
-    const uint4& q = l.q[0];
-    return max2(max2(q.x & 0x7FFF7FFFu, q.y & 0x7FFF7FFFu), max2(q.z & 0x7FFF7FFFu, q.w & 0x7FFF7FFFu));
-  } else {
-    const uint4 &a = l.q[0], &b = l.q[1];
-    constexpr uint32_t m = 0x7FFFFFFFu;
-    return max(max(max(a.x & m, a.y & m), max(a.z & m, a.w & m)), max(max(b.x & m, b.y & m), max(b.z & m, b.w & m)));
-  }
-}
-
-// (bfloat16: `m` holds two columns' halves until here)
-template <bool BF16>
-__device__ __forceinline__ uint32_t magnitude_bits(uint32_t m) { return BF16 ? max(m << 16, m & 0xFFFF0000u) : m; }
+template <bool BF16, bool ACROSS>
+__host__ __device__ constexpr int tile_smem() { return Tile<BF16>::bytes + (ACROSS ? kStageBytes : 0); }
 
 template <bool BF16>
 __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return BF16 ? max2(a, b) : max(a, b); }
 
-constexpr int kStagePitch = 80;  // bytes of a staged row of codes across: 64 and a gap
-
+// Eight numbers of a lane's units.
 template <bool BF16>
-__host__ __device__ constexpr int tile_bytes() { return kTile * kTile * (BF16 ? 2 : 4); }
+__device__ __forceinline__ void numbers8(const uint4 (&q)[Tile<BF16>::units], Pair (&x)[4]) {
+  if constexpr (BF16) {
+    rows::numbers<true>(q[0], x);
+  } else {
+    x[0] = rows::pair(__uint_as_float(q[0].x), __uint_as_float(q[0].y));
+    x[1] = rows::pair(__uint_as_float(q[0].z), __uint_as_float(q[0].w));
+    x[2] = rows::pair(__uint_as_float(q[1].x), __uint_as_float(q[1].y));
+    x[3] = rows::pair(__uint_as_float(q[1].z), __uint_as_float(q[1].w));
+  }
+}
+
+// The codes of eight numbers with this scale; `j`: of their first pair.
+template <int BLOCK, bool SR>
+__device__ __forceinline__ uint32_t codes8(Pair (&x)[4], const Scale& q, uint64_t j, uint32_t key) {
+  in_units<BLOCK>(x, q);
+  uint32_t w;
+  if constexpr (SR) {
+    uint32_t bits[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) bits[k] = random32(j, k, key);
+    w = codes_random<BLOCK>(x, bits);
+  } else {
+    w = codes_nearest(x);
+  }
+  return q.code == nan_code<BLOCK>() ? 0u : w;  // (0 times what is not finite)
+}
 
 template <bool BF16, int BLOCK, bool SR, bool ALONG, bool ACROSS>
-__global__ void __launch_bounds__(kThreads, 3) fp4_quantize_kernel(const __grid_constant__ QuantParams P) {
+__global__ void __launch_bounds__(kThreads, BF16 ? 5 : 3) fp4_quantize_kernel(const __grid_constant__ QuantParams P) {
+  using T = Tile<BF16>;
   extern __shared__ __align__(16) uint8_t smem[];
   constexpr int kTiles = 32 / BLOCK;  // scale tiles of 128 entries of K
   __shared__ __align__(16) uint8_t sf_along[kTiles * 512], sf_across[kTiles * 512];
@@ -276,67 +251,84 @@ __global__ void __launch_bounds__(kThreads, 3) fp4_quantize_kernel(const __grid_
   const int tid = threadIdx.x;
   const int by = static_cast<int>(blockIdx.x) / P.tiles_x, bx = static_cast<int>(blockIdx.x) - by * P.tiles_x;
   const int r0 = by * kTile, c0 = bx * kTile;
-  uint8_t* tile = smem;
-  uint8_t* stage = smem + tile_bytes<BF16>();
-  float up = 1.0f;
+  const uint32_t tile = rows::shared_address(smem);
+  // 16 lanes a row, 8 entries a lane, 16 rows at a time
+  const int g = tid & 15, row = tid >> 4, col = c0 + 8 * g;
   {
-    const int g = tid & 15;  // 8 columns
-    const int col = c0 + 8 * g;
-    constexpr int kBatch = BF16 ? 8 : 4;  // rows of a thread in flight
+    const char* p = static_cast<const char*>(P.x) + ((r0 + row) * P.stride + c0) * T::size;
+    uint32_t to = tile + row * T::pitch + g * (16 * T::units);
 #pragma unroll
-    for (int half = 0; half < 8 / kBatch; ++half) {
-      Loaded<BF16> l[kBatch];
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t shift = P.vec ? 0u : rows::shift_of(p);
+      const char* from = p - shift;
+      // bytes from the row's first unit here on that belong to it
+      const int bytes = r0 + row + 16 * i < P.rows ? min(P.cols - c0, kTile + 8) * T::size + static_cast<int>(shift) : 0;
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) load8<BF16>(P, r0 + (half * kBatch + i) * 16 + (tid >> 4), col, l[i]);
-      if constexpr (BLOCK == 16) {
-        if (half == 0) {
-          const int k = tensor_exponent(__float_as_uint(P.scale[1]));
-          up = pow2(-k);
-          if (blockIdx.x == 0 && tid == 0) P.scale[0] = pow2(k);
-        }
+      for (int u = 0; u < T::units + 1; ++u) {
+        const int at = (g * T::units + u) * 16, have = min(max(bytes - at, 0), 16);
+        if (u < T::units || (g == 15 && shift != 0)) rows::copy_ahead(to + 16 * u, have ? from + at : static_cast<const char*>(P.x) - rows::shift_of(P.x), have);
       }
+      p += 16 * P.stride * T::size;
+      to += 16 * T::pitch;
+    }
+    rows::copies_commit();
+  }
+  float up = 1.0f;
+  if constexpr (BLOCK == 16) {
+    const int k = tensor_exponent(__float_as_uint(P.scale[1]));
+    up = pow2(-k);
+    if (blockIdx.x == 0 && tid == 0) P.scale[0] = pow2(k);
+  }
+  rows::copies_wait(0);
+  __syncwarp();
+  if (ALONG || !P.vec) {
+    uint32_t at = tile + row * T::pitch + g * (16 * T::units);
+    uint8_t* out = P.along.codes + (r0 + row) * P.along.pitch + col / 2;
+    uint64_t j = static_cast<uint64_t>(r0 + row) * ((P.cols + 1) / 2) + col / 2;
+    const char* p = static_cast<const char*>(P.x) + ((r0 + row) * P.stride + c0) * T::size;
+#pragma unroll 2
+    for (int i = 0; i < 8; ++i) {
+      const int r = row + 16 * i;
+      uint4 q[T::units];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int r = (half * kBatch + i) * 16 + (tid >> 4);
-        settle<BF16>(P, r0 + r, col, l[i]);
+      for (int u = 0; u < T::units; ++u) q[u] = rows::shared_load(at + 16 * u);
+      if (!P.vec) {  // to the lane's own place, for those who read columns
+        const uint32_t shift = rows::shift_of(p);
+        const uint4 next = rows::shared_load(at + 16 * T::units);
+        if (shift) {
+#pragma unroll
+          for (int u = 0; u < T::units; ++u) q[u] = rows::funnel(q[u], u + 1 < T::units ? q[u + 1] : next, shift);
+        }
+        __syncwarp();
         if constexpr (ACROSS) {
 #pragma unroll
-          for (int u = 0; u < Loaded<BF16>::n; ++u)
-            *reinterpret_cast<uint4*>(tile + r * (kTile * (BF16 ? 2 : 4)) + (g * Loaded<BF16>::n + u) * 16) = l[i].q[u];
+          for (int u = 0; u < T::units; ++u) rows::shared_store(at + 16 * u, q[u]);
         }
-        if constexpr (ALONG) {
-          uint32_t m = largest<BF16>(l[i]);
-          m = larger<BF16>(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-          if constexpr (BLOCK == 32) m = larger<BF16>(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-          const Scale q = block_scale<BLOCK, SR>(magnitude_bits<BF16>(m), up);
-          Pair x[4];
-          if constexpr (BF16) {
-            rows::numbers<true>(l[i].q[0], x);
-          } else {
-            x[0] = rows::pair(__uint_as_float(l[i].q[0].x), __uint_as_float(l[i].q[0].y));
-            x[1] = rows::pair(__uint_as_float(l[i].q[0].z), __uint_as_float(l[i].q[0].w));
-            x[2] = rows::pair(__uint_as_float(l[i].q[1].x), __uint_as_float(l[i].q[1].y));
-            x[3] = rows::pair(__uint_as_float(l[i].q[1].z), __uint_as_float(l[i].q[1].w));
-          }
-          in_units<BLOCK>(x, q);
-          uint32_t word;
-          if constexpr (SR) {
-            const uint64_t j = static_cast<uint64_t>(r0 + r) * ((P.cols + 1) / 2) + col / 2;
-            uint32_t bits[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) bits[k] = random32(j, k, P.along.key);
-            word = codes_random<BLOCK>(x, bits);
-          } else {
-            word = codes_nearest(x);
-          }
-          if (q.code == nan_code<BLOCK>()) word = 0;  // (0 times what is not finite)
-          if (r0 + r < P.rows && col / 2 < P.along.pitch && MUON_CHECK(col >= 0 && col / 2 + 4 <= P.along.pitch))
-            *reinterpret_cast<uint32_t*>(P.along.codes + (r0 + r) * P.along.pitch + col / 2) = word;
-          const int b = BLOCK == 32 ? g >> 2 : g >> 1;
-          if ((g & (BLOCK / 8 - 1)) == 0)
-            sf_along[(b >> 2) * 512 + (r & 31) * 16 + (r >> 5) * 4 + (b & 3)] = r0 + r < P.rows ? q.code : 0;
-        }
+        p += 16 * P.stride * T::size;
       }
+      if constexpr (ALONG) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int u = 0; u < T::units; ++u) {
+          constexpr uint32_t k = BF16 ? 0x7FFF7FFFu : 0x7FFFFFFFu;
+          m = larger<BF16>(m, larger<BF16>(larger<BF16>(q[u].x & k, q[u].y & k), larger<BF16>(q[u].z & k, q[u].w & k)));
+        }
+        m = larger<BF16>(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+        if constexpr (BLOCK == 32) m = larger<BF16>(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+        if constexpr (BF16) m = max(m << 16, m & 0xFFFF0000u);
+        const Scale sc = block_scale<BLOCK, SR>(m, up);
+        Pair x[4];
+        numbers8<BF16>(q, x);
+        const uint32_t word = codes8<BLOCK, SR>(x, sc, j, P.along.key);
+        const bool inside = r0 + r < P.rows;
+        if (inside && col / 2 < P.along.pitch && MUON_CHECK(col >= 0 && col / 2 + 4 <= P.along.pitch)) *reinterpret_cast<uint32_t*>(out) = word;
+        const int b = BLOCK == 32 ? g >> 2 : g >> 1;
+        if ((g & (BLOCK / 8 - 1)) == 0)
+          sf_along[(b >> 2) * 512 + (r & 31) * 16 + (r >> 5) * 4 + (b & 3)] = inside ? sc.code : 0;
+        out += 16 * P.along.pitch;
+        j += 16ull * ((P.cols + 1) / 2);
+      }
+      at += 16 * T::pitch;
     }
   }
   __syncthreads();
@@ -349,67 +341,62 @@ __global__ void __launch_bounds__(kThreads, 3) fp4_quantize_kernel(const __grid_
   if constexpr (ACROSS) {
     // 32 rows of a column at a time: bfloat16, two columns a thread; float32, one, twice
     constexpr int kColumns = BF16 ? 2 : 1;
-    auto column = [&](int c, int rb, const uint32_t (&v)[32], int h, const uint32_t (&top)[32 / BLOCK]) {
-      uint32_t word[4];
-#pragma unroll
-      for (int b = 0; b < 32 / BLOCK; ++b) {
-        const uint32_t m = BF16 ? (h ? top[b] & 0xFFFF0000u : top[b] << 16) : top[b];
-        const Scale q = block_scale<BLOCK, SR>(m, up);
-        uint64_t j = 0;
-        if constexpr (SR) j = static_cast<uint64_t>(c0 + c) * ((P.rows + 1) / 2) + (r0 + rb * 32 + b * BLOCK) / 2;
-#pragma unroll
-        for (int o = 0; o < BLOCK / 8; ++o) {
-          Pair x[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t lo = v[b * BLOCK + o * 8 + 2 * k], hi = v[b * BLOCK + o * 8 + 2 * k + 1];
-            if constexpr (BF16)
-              x[k] = h ? rows::pair(__uint_as_float(lo & 0xFFFF0000u), __uint_as_float(hi & 0xFFFF0000u))
-                       : rows::pair(__uint_as_float(lo << 16), __uint_as_float(hi << 16));
-            else
-              x[k] = rows::pair(__uint_as_float(lo), __uint_as_float(hi));
-          }
-          in_units<BLOCK>(x, q);
-          uint32_t w;
-          if constexpr (SR) {
-            uint32_t bits[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) bits[k] = random32(j, o * 4 + k, P.across.key);
-            w = codes_random<BLOCK>(x, bits);
-          } else {
-            w = codes_nearest(x);
-          }
-          word[b * BLOCK / 8 + o] = q.code == nan_code<BLOCK>() ? 0u : w;
-        }
-        const int blk = rb * (32 / BLOCK) + b;  // along K within the tile
-        sf_across[(blk >> 2) * 512 + (c & 31) * 16 + (c >> 5) * 4 + (blk & 3)] = c0 + c < P.cols ? q.code : 0;
-      }
-      *reinterpret_cast<uint4*>(stage + c * kStagePitch + rb * 16) = make_uint4(word[0], word[1], word[2], word[3]);
-    };
+    uint32_t* stage = reinterpret_cast<uint32_t*>(smem + T::bytes);
 #pragma unroll 1
     for (int pass = 0; pass < 2 / kColumns; ++pass) {
       const int item = pass * kThreads + tid;
       const int cp = BF16 ? item & 63 : item & 127, rb = BF16 ? item >> 6 : item >> 7;
-      uint32_t v[32], top[32 / BLOCK];
-#pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = *reinterpret_cast<const uint32_t*>(tile + (rb * 32 + i) * (kTile * (BF16 ? 2 : 4)) + cp * 4);
-#pragma unroll
+      const uint32_t from = tile + rb * 32 * T::pitch + cp * 4;
+      auto word_at = [&](int i) {
+        uint32_t w;
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(from + i * T::pitch) : "memory");
+        return w;
+      };
+#pragma unroll 1
       for (int b = 0; b < 32 / BLOCK; ++b) {
-        top[b] = 0;
+        uint32_t top = 0;
 #pragma unroll
-        for (int i = 0; i < BLOCK; ++i) top[b] = larger<BF16>(top[b], v[b * BLOCK + i] & (BF16 ? 0x7FFF7FFFu : 0x7FFFFFFFu));
+        for (int i = 0; i < BLOCK; ++i) top = larger<BF16>(top, word_at(b * BLOCK + i) & (BF16 ? 0x7FFF7FFFu : 0x7FFFFFFFu));
+        Scale sc[kColumns];
+#pragma unroll
+        for (int h = 0; h < kColumns; ++h) {
+          const int c = kColumns * cp + h, blk = rb * (32 / BLOCK) + b;  // blk: along K within the tile
+          sc[h] = block_scale<BLOCK, SR>(BF16 ? (h ? top & 0xFFFF0000u : top << 16) : top, up);
+          sf_across[(blk >> 2) * 512 + (c & 31) * 16 + (c >> 5) * 4 + (blk & 3)] = c0 + c < P.cols ? sc[h].code : 0;
+        }
+#pragma unroll 1
+        for (int o = b * (BLOCK / 8); o < (b + 1) * (BLOCK / 8); ++o) {
+          uint32_t v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = word_at(8 * o + i);
+#pragma unroll
+          for (int h = 0; h < kColumns; ++h) {
+            const int c = kColumns * cp + h;
+            Pair x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t lo = v[2 * k], hi = v[2 * k + 1];
+              if constexpr (BF16)
+                x[k] = h ? rows::pair(__uint_as_float(lo & 0xFFFF0000u), __uint_as_float(hi & 0xFFFF0000u))
+                         : rows::pair(__uint_as_float(lo << 16), __uint_as_float(hi << 16));
+              else
+                x[k] = rows::pair(__uint_as_float(lo), __uint_as_float(hi));
+            }
+            const uint64_t j = SR ? static_cast<uint64_t>(c0 + c) * ((P.rows + 1) / 2) + (r0 + rb * 32 + 8 * o) / 2 : 0;
+            stage[(rb * 4 + o) * kStagePitch + c] = codes8<BLOCK, SR>(x, sc[h], j, P.across.key);
+          }
+        }
       }
-#pragma unroll
-      for (int h = 0; h < kColumns; ++h) column(kColumns * cp + h, rb, v, h, top);
     }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int piece = i * kThreads + tid, c = piece >> 2, at = (piece & 3) * 16;
-      const long long byte = r0 / 2 + at;
+      const int piece = i * kThreads + tid, c = piece >> 2, w = (piece & 3) * 4;
+      const long long byte = r0 / 2 + w * 4;
       if (c0 + c < P.cols && byte < P.across.pitch && MUON_CHECK(byte + 16 <= P.across.pitch))
         *reinterpret_cast<uint4*>(P.across.codes + (c0 + c) * P.across.pitch + byte) =
-            *reinterpret_cast<const uint4*>(stage + c * kStagePitch + at);
+            make_uint4(stage[w * kStagePitch + c], stage[(w + 1) * kStagePitch + c], stage[(w + 2) * kStagePitch + c],
+                       stage[(w + 3) * kStagePitch + c]);
     }
     const long long kt = static_cast<long long>(by) * kTiles + (tid >> 5);
     if (tid < 32 * kTiles && bx < P.across.row_tiles && kt < P.across.ktiles)
@@ -419,39 +406,52 @@ __global__ void __launch_bounds__(kThreads, 3) fp4_quantize_kernel(const __grid_
 }
 
 // Largest finite magnitude of a matrix, as the bits of a float, into *out (0
-// before): 128 x 128 entries a step, all of a thread's loads in flight.
+// before): a warp takes 128 units of 16 bytes of a row.  Units are those of
+// memory; entries beside the row are left out of the first and the last one.
+// Contiguous rows are read as rows of any other length (the last one shorter).
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads) fp4_amax_kernel(const __grid_constant__ QuantParams P, uint32_t* out, int steps) {
+__global__ void __launch_bounds__(kThreads) fp4_amax_kernel(const char* x, long long stride, int cols, long long total, int pieces,
+                                                            long long items, uint32_t* out) {
+  constexpr int size = BF16 ? 2 : 4, per = 16 / size;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int lane = threadIdx.x & 31;
   uint32_t top = 0;
-  for (int s = blockIdx.x; s < steps; s += gridDim.x) {
-    const int by = s / P.tiles_x, r0 = by * kTile + (threadIdx.x >> 4), c = (s - by * P.tiles_x) * kTile + (threadIdx.x & 15) * 8;
-    Loaded<BF16> l[8];
+  const long long step = static_cast<long long>(gridDim.x) * (kThreads / 32);
+  for (long long item = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); item < items; item += step) {
+    const long long r = items <= 0x7FFFFFFF ? static_cast<long long>(static_cast<uint32_t>(item) / static_cast<uint32_t>(pieces)) : item / pieces;
+    const int k0 = static_cast<int>(item - r * pieces) * 128 + lane;
+    const char* p = x + r * stride * size;
+    const int before = static_cast<int>(rows::shift_of(p)) / size;
+    const int n = static_cast<int>(min(static_cast<long long>(cols), total - r * stride));
+    p -= before * size;
+    uint4 q[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) load8<BF16>(P, r0 + 16 * i, c, l[i]);
+    for (int i = 0; i < 4; ++i) {
+      const int k = k0 + 32 * i;
+      q[i] = k * per < before + n ? __ldg(reinterpret_cast<const uint4*>(p) + k) : make_uint4(0, 0, 0, 0);
+    }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      settle<BF16>(P, r0 + 16 * i, c, l[i]);
-      uint32_t m = magnitude_bits<BF16>(largest<BF16>(l[i]));
-      if (m >= 0x7F800000u) {  // some are not finite: the others one by one
+    for (int i = 0; i < 4; ++i) {
+      constexpr uint32_t mask = BF16 ? 0x7FFF7FFFu : 0x7FFFFFFFu;
+      const uint4 a = make_uint4(q[i].x & mask, q[i].y & mask, q[i].z & mask, q[i].w & mask);
+      uint32_t m = larger<BF16>(larger<BF16>(a.x, a.y), larger<BF16>(a.z, a.w));
+      if constexpr (BF16) m = max(m << 16, m & 0xFFFF0000u);
+      const int e0 = (k0 + 32 * i) * per - before;  // entry of the row that the unit begins with
+      if (m >= 0x7F800000u || e0 < 0 || e0 + per > n) {  // some are not finite or not the row's: one by one
         m = 0;
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-        for (int u = 0; u < Loaded<BF16>::n; ++u) {
-          const uint32_t w[4] = {l[i].q[u].x, l[i].q[u].y, l[i].q[u].z, l[i].q[u].w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t a = BF16 ? w[k] << 16 & 0x7FFFFFFFu : w[k] & 0x7FFFFFFFu, b = BF16 ? w[k] & 0x7FFF0000u : 0u;
-            if (a < 0x7F800000u) m = max(m, a);
-            if (b < 0x7F800000u) m = max(m, b);
-          }
+        for (int k = 0; k < per; ++k) {
+          const uint32_t v = BF16 ? (k & 1 ? w[k >> 1] & 0xFFFF0000u : w[k >> 1] << 16) : w[k & 3];
+          if (v < 0x7F800000u && e0 + k >= 0 && e0 + k < n) m = max(m, v);
         }
       }
       top = max(top, m);
     }
   }
   top = __reduce_max_sync(0xFFFFFFFFu, top);
-  if ((threadIdx.x & 31) == 0 && top) atomicMax(out, top);
+  if (lane == 0 && top) atomicMax(out, top);
 }
 
 // The numbers that codes stand for: a lane takes 8 codes (4 bytes), a warp 256
@@ -644,19 +644,25 @@ extern "C" muon_status_t fp4_quantize(const void* x, int dtype, int64_t rows, in
   const bool bf16 = dtype == MUON_BF16;
   const void* fn = bf16 ? quantize_fn<true>(block, stochastic != 0, along != nullptr, across != nullptr)
                         : quantize_fn<false>(block, stochastic != 0, along != nullptr, across != nullptr);
-  const int smem = across ? (bf16 ? tile_bytes<true>() : tile_bytes<false>()) + kTile * kStagePitch : 0;
+  const int smem = across ? (bf16 ? tile_smem<true, true>() : tile_smem<false, true>())
+                          : (bf16 ? tile_smem<true, false>() : tile_smem<false, false>());
   if (smem > 40 * 1024 && cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return MUON_ERR_CUDA;
   if (block == 16) {
     if (cudaMemsetAsync(P.scale + 1, 0, 4, str) != cudaSuccess) return MUON_ERR_CUDA;
     uint32_t* bits = reinterpret_cast<uint32_t*>(P.scale + 1);
-    const int64_t across_tiles = (cols + kTile - 1) / kTile;
-    QuantParams A = P;
-    A.tiles_x = static_cast<int>(across_tiles);
-    int steps = static_cast<int>((rows + kTile - 1) / kTile * across_tiles);
-    void* args[] = {&A, &bits, &steps};
+    const int per = 16 / size;
+    const char* p = static_cast<const char*>(x);
+    // contiguous rows as rows of 128 units of memory
+    const bool begin = aligned_to(x, 16), flat = row_stride == cols && rows * cols > 128 * per;
+    const int run = (begin ? 128 : 127) * per;
+    long long stride = flat ? run : row_stride, total = flat ? rows * cols : INT64_MAX;
+    int length = static_cast<int>(flat ? run : cols);
+    int pieces = static_cast<int>(((length + per - 1LL) / per + (begin && stride % per == 0 ? 0 : 1) + 127) / 128);
+    long long items = (flat ? (total + stride - 1) / stride : rows) * pieces;
+    void* args[] = {&p, &stride, &length, &total, &pieces, &items, &bits};
     if (launch(bf16 ? reinterpret_cast<const void*>(&fp4_amax_kernel<true>) : reinterpret_cast<const void*>(&fp4_amax_kernel<false>),
-               dim3(static_cast<unsigned>(std::min(steps, sms * 8))), 0, args, str) != cudaSuccess)
+               dim3(static_cast<unsigned>(std::min<int64_t>((items + 7) / 8, sms * 8))), 0, args, str) != cudaSuccess)
       return MUON_ERR_CUDA;
   }
   void* args[] = {&P};
