@@ -18,9 +18,9 @@
 //     the next tile's MMAs start then.
 //   fp4_tile_kernel   few tiles: a CTA computes 128 x BN (BN 32, 64, 128; the
 //     larger matrix gives the 128 rows, so a few tokens are the narrow side), and
-//     a cluster of up to 8 CTAs splits K: each leaves its partial sums in its own
-//     shared memory, and each adds a slice of the tile over the cluster in
-//     the order of the CTAs, so equal calls give equal bits.
+//     a cluster of up to 8 CTAs splits K: each sends every CTA its partial sums
+//     of that one's rows of the tile, and each adds them in the order of the
+//     CTAs, so equal calls give equal bits.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* never = reinterpret_cast<volatile int*>(tmem_slot + 2);  // stays 0
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = ptx::cluster_ctarank();
   const int pair = static_cast<int>(ptx::cluster_id_x()), npairs = static_cast<int>(ptx::nclusters_x());
   const int total = P.tiles_m * P.tiles_n;
@@ -243,53 +243,60 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0 && !P.inject_stall) {
+    if (rank == 0 && !P.inject_stall) {
       // -------------------------------------------------------- MMA issuer
+      // The whole warp runs the loop and one lane issues: what the instructions
+      // take is the same in every lane and stays in uniform registers.
       int stage = 0, it = 0;
       uint32_t phase = 0;
       bool ok = true;
       for (int t = pair; ok && t < total; t += npairs, ++it) {
         const int acc = it & 1;
         // the epilogue has read what this tile's accumulator shares with the last one's
-        if (it > 0 && !ptx::mbar_wait_cluster(ptx::smem_addr(tempty), (it - 1) & 1, budget, abort)) {
-          raise_timeout(P, abort);
-          break;
-        }
+        ok = it == 0 || ptx::mbar_wait_cluster(ptx::smem_addr(tempty), (it - 1) & 1, budget, abort);
+        if (!ok) raise_timeout(P, abort);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
         ptx::tc_fence_after();
         const uint32_t d = tmem + acc * kAccStep;
         for (int kb = 0; kb < kblocks; ++kb) {
           const uint32_t sa = ptx::smem_addr(smem + stage * kPairStage), sb = sa + kPairCodes;
           const uint32_t fa = sb + kPairCodes, fb = fa + kPairScalesA;
           const uint64_t a0 = ptx::sdesc_sw128(sa, 16, 1024), b0 = ptx::sdesc_sw128(sb, 16, 1024);
+          const uint64_t fa0 = ptx::sdesc_plain(fa, 128), fb0 = ptx::sdesc_plain(fb, 128);  // (512 bytes on: + 32)
           const int steps = min(4, (P.k - kb * kFp4Depth + 63) / 64);
-          if (!ptx::mbar_wait(ptx::smem_addr(&full[stage]), phase, budget, abort)) {
-            raise_timeout(P, abort);
-            ok = false;
-            break;
-          }
+          ok = ptx::mbar_wait(ptx::smem_addr(&full[stage]), phase, budget, abort);
+          if (!ok) raise_timeout(P, abort);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
           ptx::tc_fence_after();
+          if (ptx::elect_one()) {
 #pragma unroll
-          for (int g = 0; g < kG; ++g) {
-            ptx::tmem_copy_scales<true>(tmem + kScaleCol + 4 * g, ptx::sdesc_plain(fa + g * 512, 128));
+            for (int g = 0; g < kG; ++g) {
+              ptx::tmem_copy_scales<true>(tmem + kScaleCol + 4 * g, fa0 + 32 * g);
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-              ptx::tmem_copy_scales<true>(tmem + kScaleCol + 16 + 8 * g + 4 * j, ptx::sdesc_plain(fb + (j * kG + g) * 512, 128));
+              for (int j = 0; j < 2; ++j)
+                ptx::tmem_copy_scales<true>(tmem + kScaleCol + 16 + 8 * g + 4 * j, fb0 + 32 * (j * kG + g));
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (k >= steps) break;
+              const int g = BLOCK == 32 ? k >> 1 : k;
+              const uint32_t idesc = ptx::idesc_fp4(256, 256, BLOCK, BLOCK == 32 ? 2 * (k & 1) : 0);
+              ptx::mma_fp4<BLOCK, true>(d, a0 + 2 * k, b0 + 2 * k, idesc, tmem + kScaleCol + 4 * g,
+                                        tmem + kScaleCol + 16 + 8 * g, (kb | k) != 0 ? 1u : 0u);
+            }
+            ptx::mma_commit_pair_mc(ptx::smem_addr(&empty[stage]), 0x3);
           }
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (k >= steps) break;
-            const int g = BLOCK == 32 ? k >> 1 : k;
-            const uint32_t idesc = ptx::idesc_fp4(256, 256, BLOCK, BLOCK == 32 ? 2 * (k & 1) : 0);
-            ptx::mma_fp4<BLOCK, true>(d, a0 + 2 * k, b0 + 2 * k, idesc, tmem + kScaleCol + 4 * g,
-                                      tmem + kScaleCol + 16 + 8 * g, (kb | k) != 0 ? 1u : 0u);
-          }
-          ptx::mma_commit_pair_mc(ptx::smem_addr(&empty[stage]), 0x3);
+          __syncwarp();
           if (++stage == kPairStages) stage = 0, phase ^= 1;
         }
         if (!ok) break;
-        ptx::mma_commit_pair_mc(ptx::smem_addr(&tfull[acc]), 0x3);
+        if (ptx::elect_one()) ptx::mma_commit_pair_mc(ptx::smem_addr(&tfull[acc]), 0x3);
+        __syncwarp();
       }
-      ptx::mma_commit_pair(ptx::smem_addr(drain));
+      if (ptx::elect_one()) ptx::mma_commit_pair(ptx::smem_addr(drain));
+      __syncwarp();
       ptx::mbar_wait(ptx::smem_addr(drain), 0, budget, never);
     }
   } else {
@@ -356,8 +363,7 @@ struct TileShape {
   static constexpr int stages = BN == 128 ? 3 : 4;
   static constexpr int stage = 128 * kDepthBytes + BN * kDepthBytes + 2 * kTileScales;
   static constexpr int smem = stages * stage + 1024 + 256;
-  static constexpr int pitch = BN + 1;  // floats of a row of partial sums
-  static_assert(stages * stage >= 128 * pitch * 4 && stages * stage >= 4 * 4096, "the ring is reused");
+  static_assert(stages * stage >= BN * (128 + 8) * 4 && stages * stage >= 4 * 4096, "the ring is reused");
   static_assert(stage % 1024 == 0, "swizzled tiles begin on 1 KB");
 };
 
@@ -474,11 +480,18 @@ __global__ void __launch_bounds__(kTileThreads) fp4_tile_kernel(const __grid_con
     ptx::tc_fence_after();
   }
   const Factors f = tensor_factors(P);
-  float* partial = reinterpret_cast<float*>(smem);  // every copy has landed and been read
+  const int slice = 128 / splits;  // rows of the tile that a CTA of the cluster adds up
+  // partial sums: [CTA they are of][column][row of the slice], rows padded by one float
+  const uint32_t partial = ptx::smem_addr(smem);
+  if (splits > 1) {
+    __syncwarp();
+    ptx::cluster_sync();  // no CTA of the cluster still reads its operands
+  }
   if (warp >= 2 && ok) {
     const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16);
     const int row = q * 32 + lane;
     if (splits > 1) {
+      const uint32_t to = ptx::map_to_rank(partial + (rank * BN * (slice + 1) + row % slice) * 4, row / slice);
 #pragma unroll 1
       for (int c = 0; c < BN; c += 32) {
         uint32_t r[32];
@@ -486,7 +499,7 @@ __global__ void __launch_bounds__(kTileThreads) fp4_tile_kernel(const __grid_con
         ptx::tmem_ld32(tb + c, r);
         ptx::tmem_ld_wait(r);
 #pragma unroll
-        for (int k = 0; k < 32; ++k) partial[row * Shape::pitch + c + k] = kb0 < kb1 ? __uint_as_float(r[k]) : 0.0f;
+        for (int k = 0; k < 32; ++k) ptx::st_cluster_b32(to + (c + k) * (slice + 1) * 4, kb0 < kb1 ? r[k] : 0u);
       }
     } else if (P.swapped) {
       // a lane is a column of out, an accumulator column a row of it
@@ -538,32 +551,25 @@ __global__ void __launch_bounds__(kTileThreads) fp4_tile_kernel(const __grid_con
   if (splits > 1) {
     __syncwarp();
     ptx::cluster_sync();  // every CTA's partial sums are there
-    // this CTA's share of the tile, lanes along out's rows
-    const uint32_t base = ptx::smem_addr(partial);
-    const int rows = 128 / splits;
-    for (int i = static_cast<int>(threadIdx.x); i < rows * BN; i += kTileThreads) {
-      int r, c;
-      if (P.swapped) {
-        r = rank * rows + i % rows;
-        c = i / rows;
-      } else {
-        r = rank * rows + i / BN;
-        c = i % BN;
-      }
-      const int gm = I * 128 + r, gn = n0 + c;
-      if (gm >= P.m || gn >= P.n) continue;
-      const uint32_t at = base + (r * Shape::pitch + c) * 4;
+    // this CTA's rows of the tile, lanes along out's rows
+#pragma unroll 4
+    for (int i = static_cast<int>(threadIdx.x); i < slice * BN; i += kTileThreads) {
+      const int r = P.swapped ? i % slice : i / BN, c = P.swapped ? i / slice : i % BN;
+      const int gm = I * 128 + rank * slice + r, gn = n0 + c;
       float v = 0.0f;
-      for (int s = 0; s < splits; ++s) v += ptx::ld_cluster_f32(ptx::map_to_rank(at, s));
+      for (int s = 0; s < splits; ++s) {
+        float p;
+        ptx::lds32(partial + ((s * BN + c) * (slice + 1) + r) * 4, p);
+        v += p;
+      }
       v = v * f.a * f.b;
+      if (gm >= P.m || gn >= P.n) continue;
       const long long o = P.swapped ? gn * P.stride + gm : gm * P.stride + gn;
       if (P.f32)
         static_cast<float*>(P.out)[o] = v;
       else
         static_cast<__nv_bfloat16*>(P.out)[o] = __float2bfloat16_rn(v);
     }
-    __syncwarp();
-    ptx::cluster_sync();  // nobody leaves while its partial sums are read
   } else {
     __syncthreads();
   }
