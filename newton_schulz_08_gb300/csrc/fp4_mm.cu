@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
         if (p == 0) {
           ptx::tc_fence_before();
           __syncwarp();
-          if (lane == 0) ptx::mbar_arrive_cluster(tempty_leader);
+          if (lane == 0) ptx::mbar_arrive_cluster_relaxed(tempty_leader);
         }
         const int col0 = J * 256 + half * 128 + c;
         if (row0 < P.m && col0 < P.n) store_rows(P, stage, lane, row0, col0, lo, hi, f);
@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(kTileThreads) fp4_tile_kernel(const __grid_con
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* never = reinterpret_cast<volatile int*>(tmem_slot + 2);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
   const int rank = static_cast<int>(ptx::cluster_ctarank());
   const int tile = static_cast<int>(ptx::cluster_id_x());
   const int splits = static_cast<int>(gridDim.x / ptx::nclusters_x());
@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(kTileThreads) fp4_tile_kernel(const __grid_con
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && !P.inject_stall && kb0 < kb1) {
+    if (!P.inject_stall && kb0 < kb1) {  // (uniform, as in the pair kernel)
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
@@ -443,31 +443,35 @@ __global__ void __launch_bounds__(kTileThreads) fp4_tile_kernel(const __grid_con
         const uint32_t sa = ptx::smem_addr(smem + stage * Shape::stage), sb = sa + 128 * kDepthBytes;
         const uint32_t fa = sb + BN * kDepthBytes, fb = fa + kTileScales;
         const uint64_t a0 = ptx::sdesc_sw128(sa, 16, 1024), b0 = ptx::sdesc_sw128(sb, 16, 1024);
+        const uint64_t fa0 = ptx::sdesc_plain(fa, 128), fb0 = ptx::sdesc_plain(fb, 128);
         const int steps = min(4, (P.k - kb * kFp4Depth + 63) / 64);
-        if (!ptx::mbar_wait(ptx::smem_addr(&full[stage]), phase, budget, abort)) {
-          raise_timeout(P, abort);
-          ok = false;
-          break;
-        }
+        ok = ptx::mbar_wait(ptx::smem_addr(&full[stage]), phase, budget, abort);
+        if (!ok) raise_timeout(P, abort);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
         ptx::tc_fence_after();
+        if (ptx::elect_one()) {
 #pragma unroll
-        for (int g = 0; g < kG; ++g) {
-          ptx::tmem_copy_scales<false>(tsa + 4 * g, ptx::sdesc_plain(fa + g * 512, 128));
-          ptx::tmem_copy_scales<false>(tsb + 4 * g, ptx::sdesc_plain(fb + g * 512, 128));
-        }
+          for (int g = 0; g < kG; ++g) {
+            ptx::tmem_copy_scales<false>(tsa + 4 * g, fa0 + 32 * g);
+            ptx::tmem_copy_scales<false>(tsb + 4 * g, fb0 + 32 * g);
+          }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (k >= steps) break;
-          const int g = BLOCK == 32 ? k >> 1 : k;
-          const uint32_t idesc = ptx::idesc_fp4(128, BN, BLOCK, BLOCK == 32 ? 2 * (k & 1) : 0);
-          ptx::mma_fp4<BLOCK, false>(tmem, a0 + 2 * k, b0 + 2 * k, idesc, tsa + 4 * g, tsb + 4 * g + word,
-                                     kb > kb0 || k > 0 ? 1u : 0u);
+          for (int k = 0; k < 4; ++k) {
+            if (k >= steps) break;
+            const int g = BLOCK == 32 ? k >> 1 : k;
+            const uint32_t idesc = ptx::idesc_fp4(128, BN, BLOCK, BLOCK == 32 ? 2 * (k & 1) : 0);
+            ptx::mma_fp4<BLOCK, false>(tmem, a0 + 2 * k, b0 + 2 * k, idesc, tsa + 4 * g, tsb + 4 * g + word,
+                                       kb > kb0 || k > 0 ? 1u : 0u);
+          }
+          ptx::mma_commit(ptx::smem_addr(&empty[stage]));
         }
-        ptx::mma_commit(ptx::smem_addr(&empty[stage]));
+        __syncwarp();
         if (++stage == kSt) stage = 0, phase ^= 1;
       }
       // (also after a timeout: what was issued completes before the CTA goes on)
-      ptx::mma_commit(ptx::smem_addr(tfull));
+      if (ptx::elect_one()) ptx::mma_commit(ptx::smem_addr(tfull));
+      __syncwarp();
       if (!ok) ptx::mbar_wait(ptx::smem_addr(tfull), 0, budget, never);
     }
   }
@@ -551,11 +555,12 @@ __global__ void __launch_bounds__(kTileThreads) fp4_tile_kernel(const __grid_con
   if (splits > 1) {
     __syncwarp();
     ptx::cluster_sync();  // every CTA's partial sums are there
-    // this CTA's rows of the tile, lanes along out's rows
+    // this CTA's rows of the tile, lanes along out's rows (slice and BN are powers of two)
+    const int lanes = P.swapped ? 31 - __clz(slice) : 31 - __clz(BN), m0 = I * 128 + rank * slice;
 #pragma unroll 4
     for (int i = static_cast<int>(threadIdx.x); i < slice * BN; i += kTileThreads) {
-      const int r = P.swapped ? i % slice : i / BN, c = P.swapped ? i / slice : i % BN;
-      const int gm = I * 128 + rank * slice + r, gn = n0 + c;
+      const int in = i & ((1 << lanes) - 1), over = i >> lanes;
+      const int r = P.swapped ? in : over, c = P.swapped ? over : in;
       float v = 0.0f;
       for (int s = 0; s < splits; ++s) {
         float p;
@@ -563,6 +568,7 @@ __global__ void __launch_bounds__(kTileThreads) fp4_tile_kernel(const __grid_con
         v += p;
       }
       v = v * f.a * f.b;
+      const int gm = m0 + r, gn = n0 + c;
       if (gm >= P.m || gn >= P.n) continue;
       const long long o = P.swapped ? gn * P.stride + gm : gm * P.stride + gn;
       if (P.f32)
