@@ -207,6 +207,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp4_pair_kernel(const __grid_
   __syncwarp();
   ptx::cluster_sync();
   ptx::tc_fence_after();
+  if (threadIdx.x == 0) {
+    ptx::prefetch_tmap(&P.codes_a);
+    ptx::prefetch_tmap(&P.codes_b);
+    ptx::prefetch_tmap(&P.scales_a);
+    ptx::prefetch_tmap(&P.scales_b);
+  }
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
   if (blockIdx.x == 0 && threadIdx.x == 0) *P.status = 0;
@@ -363,7 +369,7 @@ struct TileShape {
   static constexpr int stages = BN == 128 ? 3 : 4;
   static constexpr int stage = 128 * kDepthBytes + BN * kDepthBytes + 2 * kTileScales;
   static constexpr int smem = stages * stage + 1024 + 256;
-  static_assert(stages * stage >= BN * (128 + 8) * 4 && stages * stage >= 4 * 4096, "the ring is reused");
+  static_assert(stages * stage >= BN * (128 + 4 * 8) * 4 && stages * stage >= 4 * 4096, "the ring is reused");
   static_assert(stage % 1024 == 0, "swizzled tiles begin on 1 KB");
 };
 
@@ -406,6 +412,12 @@ __global__ void __launch_bounds__(kTileThreads) fp4_tile_kernel(const __grid_con
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
+  if (threadIdx.x == 0) {
+    ptx::prefetch_tmap(&P.codes_a);
+    ptx::prefetch_tmap(&P.codes_b);
+    ptx::prefetch_tmap(&P.scales_a);
+    ptx::prefetch_tmap(&P.scales_b);
+  }
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
   if (blockIdx.x == 0 && threadIdx.x == 0) *P.status = 0;
@@ -485,7 +497,8 @@ __global__ void __launch_bounds__(kTileThreads) fp4_tile_kernel(const __grid_con
   }
   const Factors f = tensor_factors(P);
   const int slice = 128 / splits;  // rows of the tile that a CTA of the cluster adds up
-  // partial sums: [CTA they are of][column][row of the slice], rows padded by one float
+  // partial sums: [CTA they are of][column][row of the slice], 4 floats of padding a column: lanes
+  // next to one another along either side read their 16 bytes from different banks
   const uint32_t partial = ptx::smem_addr(smem);
   if (splits > 1) {
     __syncwarp();
@@ -495,7 +508,7 @@ __global__ void __launch_bounds__(kTileThreads) fp4_tile_kernel(const __grid_con
     const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16);
     const int row = q * 32 + lane;
     if (splits > 1) {
-      const uint32_t to = ptx::map_to_rank(partial + (rank * BN * (slice + 1) + row % slice) * 4, row / slice);
+      const uint32_t to = ptx::map_to_rank(partial + (rank * BN * (slice + 4) + (row & (slice - 1))) * 4, row / slice);
 #pragma unroll 1
       for (int c = 0; c < BN; c += 32) {
         uint32_t r[32];
@@ -503,7 +516,7 @@ __global__ void __launch_bounds__(kTileThreads) fp4_tile_kernel(const __grid_con
         ptx::tmem_ld32(tb + c, r);
         ptx::tmem_ld_wait(r);
 #pragma unroll
-        for (int k = 0; k < 32; ++k) ptx::st_cluster_b32(to + (c + k) * (slice + 1) * 4, kb0 < kb1 ? r[k] : 0u);
+        for (int k = 0; k < 32; ++k) ptx::st_cluster_b32(to + (c + k) * (slice + 4) * 4, kb0 < kb1 ? r[k] : 0u);
       }
     } else if (P.swapped) {
       // a lane is a column of out, an accumulator column a row of it
@@ -555,26 +568,40 @@ __global__ void __launch_bounds__(kTileThreads) fp4_tile_kernel(const __grid_con
   if (splits > 1) {
     __syncwarp();
     ptx::cluster_sync();  // every CTA's partial sums are there
-    // this CTA's rows of the tile, lanes along out's rows (slice and BN are powers of two)
-    const int lanes = P.swapped ? 31 - __clz(slice) : 31 - __clz(BN), m0 = I * 128 + rank * slice;
+    // this CTA's rows of the tile, 4 of a column a thread, lanes along out's rows
+    // (slice and BN are powers of two)
+    const int quads = slice / 4, bits = P.swapped ? 31 - __clz(quads) : 31 - __clz(BN), m0 = I * 128 + rank * slice;
+#pragma unroll 2
+    for (int i = static_cast<int>(threadIdx.x); i < quads * BN; i += kTileThreads) {
+      const int in = i & ((1 << bits) - 1), over = i >> bits;
+      const int r = 4 * (P.swapped ? in : over), c = P.swapped ? over : in;
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-    for (int i = static_cast<int>(threadIdx.x); i < slice * BN; i += kTileThreads) {
-      const int in = i & ((1 << lanes) - 1), over = i >> lanes;
-      const int r = P.swapped ? in : over, c = P.swapped ? over : in;
-      float v = 0.0f;
       for (int s = 0; s < splits; ++s) {
-        float p;
-        ptx::lds32(partial + ((s * BN + c) * (slice + 1) + r) * 4, p);
-        v += p;
+        float4 p;
+        ptx::lds128f(partial + ((s * BN + c) * (slice + 4) + r) * 4, p);
+        v.x += p.x, v.y += p.y, v.z += p.z, v.w += p.w;
       }
-      v = v * f.a * f.b;
+      const float x[4] = {v.x * f.a * f.b, v.y * f.a * f.b, v.z * f.a * f.b, v.w * f.a * f.b};
       const int gm = m0 + r, gn = n0 + c;
       if (gm >= P.m || gn >= P.n) continue;
       const long long o = P.swapped ? gn * P.stride + gm : gm * P.stride + gn;
-      if (P.f32)
-        static_cast<float*>(P.out)[o] = v;
-      else
-        static_cast<__nv_bfloat16*>(P.out)[o] = __float2bfloat16_rn(v);
+      if (P.swapped && P.vec && gm + 4 <= P.m) {
+        if (P.f32)
+          *reinterpret_cast<float4*>(static_cast<float*>(P.out) + o) = make_float4(x[0], x[1], x[2], x[3]);
+        else
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(P.out) + o) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+        continue;
+      }
+      const long long next = P.swapped ? 1 : P.stride;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (gm + k >= P.m) break;
+        if (P.f32)
+          static_cast<float*>(P.out)[o + k * next] = x[k];
+        else
+          static_cast<__nv_bfloat16*>(P.out)[o + k * next] = __float2bfloat16_rn(x[k]);
+      }
     }
   } else {
     __syncthreads();
