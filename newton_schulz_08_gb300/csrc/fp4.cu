@@ -19,7 +19,10 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <mutex>
 #include <new>
+#include <set>
+#include <utility>
 #include <vector>
 
 #include "../../include/muon.h"
@@ -558,6 +561,20 @@ const void* quantize_fn(int block, bool random, bool along, bool across) {
   return random ? quantize_fn<BF16, 16, true>(along, across) : quantize_fn<BF16, 16, false>(along, across);
 }
 
+// Raises a kernel's limit of shared memory at its first use on the current device.
+bool raise_limit(const void* fn, int smem) {
+  static std::mutex mu;
+  static std::set<std::pair<int, const void*>> done;
+  int dev = 0;
+  if (smem <= 40 * 1024) return true;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  std::lock_guard<std::mutex> lk(mu);
+  if (done.count({dev, fn})) return true;
+  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return false;
+  done.insert({dev, fn});
+  return true;
+}
+
 uint64_t matrix_bytes(int64_t rows, int64_t cols, int64_t stride, int size) {
   return rows && cols ? (static_cast<uint64_t>(rows - 1) * stride + cols) * size : 0;
 }
@@ -646,8 +663,7 @@ extern "C" muon_status_t fp4_quantize(const void* x, int dtype, int64_t rows, in
                         : quantize_fn<false>(block, stochastic != 0, along != nullptr, across != nullptr);
   const int smem = across ? (bf16 ? tile_smem<true, true>() : tile_smem<false, true>())
                           : (bf16 ? tile_smem<true, false>() : tile_smem<false, false>());
-  if (smem > 40 * 1024 && cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return MUON_ERR_CUDA;
+  if (!raise_limit(fn, smem)) return MUON_ERR_CUDA;
   if (block == 16) {
     if (cudaMemsetAsync(P.scale + 1, 0, 4, str) != cudaSuccess) return MUON_ERR_CUDA;
     uint32_t* bits = reinterpret_cast<uint32_t*>(P.scale + 1);

@@ -36,6 +36,7 @@
 #include "host.h"
 #include "plan.h"
 #include "ptx.cuh"
+#include "rows.cuh"
 
 namespace muon {
 namespace {
@@ -131,21 +132,39 @@ __device__ __forceinline__ void store_rows(const MmParams& P, uint32_t stage, in
           *reinterpret_cast<uint4*>(out + ((row0 + r) * P.stride + c0) * size + j * 16) = make_uint4(a, b, c, d);
       }
     } else {
-      const int rows = min(32, P.m - row0);
-      for (int r = 0; r < rows; ++r) {
-        const long long at = (row0 + r) * P.stride + c0;
-        if (P.f32) {
-          float v;
-          ptx::lds32(stage + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4, v);
-          if (c0 + lane < P.n) static_cast<float*>(P.out)[at + lane] = v;
-        } else {
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int c = u * 32 + lane;
-            uint16_t v;
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(stage + r * 128 + (((c >> 3) ^ (r & 7)) << 4) + (c & 7) * 2) : "memory");
-            if (c0 + c < P.n) static_cast<uint16_t*>(P.out)[at + c] = v;
-          }
+      // rows off the 16-byte boundaries, or ending here: each lane composes an
+      // aligned unit of two neighbouring pieces; units with entries of others are stored by the entry
+      const int per = 16 / size, have = min(width, P.n - c0);
+#pragma unroll 1
+      for (int k = 0; k < 8; ++k) {
+        const int r = 4 * k + (lane >> 3), j = lane & 7;
+        auto piece = [&](int p) {
+          uint4 q;
+          ptx::lds128(stage + r * 128 + ((p ^ (r & 7)) << 4), q.x, q.y, q.z, q.w);
+          return q;
+        };
+        char* at = out + ((row0 + r) * P.stride + c0) * size;
+        const uint32_t shift = rows::shift_of(at);
+        const int before = static_cast<int>(shift) / size;
+        if (row0 + r >= P.m) continue;
+        uint4 q = piece(j);
+        const uint4 last = q;
+        if (shift) q = rows::funnel(piece(j ? j - 1 : 0), q, 16 - shift);
+        const int first = j ? 0 : before, room = min(per, have + before - j * per);
+        at += 16 * j - static_cast<int>(shift);
+        if (first == 0 && room == per)
+          *reinterpret_cast<uint4*>(at) = q;
+        else if (P.f32)
+          rows::store_some<false>(at, q, first, room);
+        else
+          rows::store_some<true>(at, q, first, room);
+        if (j == 7 && shift) {
+          q = rows::funnel(last, last, 16 - shift);
+          const int to = min(before, have + before - 8 * per);
+          if (P.f32)
+            rows::store_some<false>(at + 16, q, 0, to);
+          else
+            rows::store_some<true>(at + 16, q, 0, to);
         }
       }
     }

@@ -217,7 +217,7 @@ def _tensors(out):
     if isinstance(out, torch.Tensor):
         yield out
     elif isinstance(out, FP4):
-        yield from (t for t in (out.codes, out.scales, out.scale) if t is not None)
+        yield from (t for t in (out.codes, out.scales, out.scale) if t is not None)  # (views of its memory)
     elif isinstance(out, (tuple, list)):
         for t in out:
             yield from _tensors(t)
@@ -1016,6 +1016,18 @@ def balance_loss_backward(logits, result, grad_balance, grad_z, mask=None, out=N
     return out
 
 
+@functools.lru_cache(maxsize=64)
+def _device(index):
+    return torch.device("cuda", index)
+
+
+def _same_device(what, index, *tensors):
+    for t in tensors:
+        if t.get_device() != index:
+            raise ValueError(f"{what}: every tensor must be on cuda:{index}")
+    return index
+
+
 class FP4:
     """A matrix in 4-bit floating point with block scales (fp4_matrix in
     include/muon.h), rows x cols, contracted along its columns by fp4_mm.
@@ -1030,7 +1042,7 @@ class FP4:
     contiguous and on one CUDA device.
     """
 
-    __slots__ = ("codes", "scales", "scale", "rows", "cols", "block", "_desc")
+    __slots__ = ("rows", "cols", "block", "_desc", "_index", "_codes", "_scales", "_scale", "_memory")
 
     def __init__(self, codes, scales, rows, cols, block=32, scale=None):
         if block not in (16, 32):
@@ -1039,14 +1051,13 @@ class FP4:
             raise ValueError("blocks of 16 have a scale of the tensor, blocks of 32 none")
         if rows < 0 or cols < 0:
             raise ValueError("rows and cols must not be negative")
-        for t, size, what in ((codes, rows * (-(-cols // 32) * 16), "codes"),
-                              (scales, -(-rows // 128) * (-(-cols // 256) * (64 // block)) * 512, "scales")):
+        for t, size, what in zip((codes, scales), _fp4_bytes(rows, cols, block), ("codes", "scales")):
             if t.dtype != torch.uint8 or not t.is_contiguous() or t.numel() != size:
                 raise ValueError(f"{what} must be a contiguous uint8 tensor of {size} bytes")
         if scale is not None and (scale.dtype != torch.float32 or scale.numel() != 2 or not scale.is_contiguous()):
             raise ValueError("scale must be two float32 numbers")
-        _index_of("FP4", codes, scales, scale)
-        self.codes, self.scales, self.scale = codes, scales, scale
+        self._index = _index_of("FP4", codes, scales, scale)
+        self._codes, self._scales, self._scale, self._memory = codes, scales, scale, None
         self.rows, self.cols, self.block = rows, cols, block
         self._desc = fp4_matrix(codes.data_ptr(), scales.data_ptr(), 0 if scale is None else scale.data_ptr(), rows, cols,
                                 block, 0)
@@ -1055,14 +1066,45 @@ class FP4:
     def shape(self):
         return self.rows, self.cols
 
+    def _part(self, address, size):
+        start = address - self._memory.data_ptr()
+        return self._memory[start:start + size]
 
-def _fp4_new(rows, cols, block, dev, scale):
-    pitch = -(-cols // 32) * 16
-    # one allocation: codes, then scales on a boundary of 512 bytes
-    first = -(-rows * pitch // 512) * 512
-    size = -(-rows // 128) * (-(-cols // 256) * (64 // block)) * 512
-    data = torch.empty(first + size, dtype=torch.uint8, device=dev)
-    return FP4(data[:rows * pitch].view(rows, pitch), data[first:], rows, cols, block, scale)
+    @property
+    def codes(self):
+        if self._codes is None:
+            size = _fp4_bytes(self.rows, self.cols, self.block)[0]
+            self._codes = self._part(self._desc.codes or self._memory.data_ptr(), size).view(self.rows, -(-self.cols // 32) * 16)
+        return self._codes
+
+    @property
+    def scales(self):
+        if self._scales is None:
+            size = _fp4_bytes(self.rows, self.cols, self.block)[1]
+            self._scales = self._part(self._desc.scales or self._memory.data_ptr(), size)
+        return self._scales
+
+    @property
+    def scale(self):
+        if self._scale is None and self.block == 16:
+            self._scale = self._part(self._desc.scale, 8).view(torch.float32)
+        return self._scale
+
+
+def _fp4_bytes(rows, cols, block):
+    """Bytes of codes and of scales."""
+    return rows * (-(-cols // 32) * 16), -(-rows // 128) * (-(-cols // 256) * (64 // block)) * 512
+
+
+def _fp4_at(address, rows, cols, block, scale, memory, index):
+    """(an FP4 in `memory` from `address` on, the address behind it)."""
+    q = FP4.__new__(FP4)
+    q._codes = q._scales = q._scale = None
+    q._memory, q._index, q.rows, q.cols, q.block = memory, index, rows, cols, block
+    codes, scales = _fp4_bytes(rows, cols, block)
+    at = address + -(-codes // 512) * 512
+    q._desc = fp4_matrix(address, at, scale, rows, cols, block, 0)
+    return q, at + scales
 
 
 def fp4_quantize(x, block=32, axis=1, seed=None, stream=None):
@@ -1075,15 +1117,25 @@ def fp4_quantize(x, block=32, axis=1, seed=None, stream=None):
     if stream is not None:
         return _on(stream, x, fp4_quantize, x, block, axis, seed)
     rows, cols, pitch = _matrix(x, "x")
-    if block not in (16, 32):
+    if block != 32 and block != 16:
         raise ValueError("block must be 32 or 16")
     if axis not in (0, 1, "both"):
         raise ValueError('axis must be 1, 0 or "both"')
-    index = _index_of("fp4_quantize", x)
-    kind, dev = _dtype_code(x), x.device
-    scale = torch.empty(2, dtype=torch.float32, device=dev) if block == 16 else None
-    along = None if axis == 0 else _fp4_new(rows, cols, block, dev, scale)
-    across = None if axis == 1 else _fp4_new(cols, rows, block, dev, scale)
+    index, kind = _index_of("fp4_quantize", x), _dtype_code(x)
+    # one allocation for everything: the tensor's scale, then codes and scales of each operand
+    size = 512 if block == 16 else 0
+    for r, c in ((rows, cols), (cols, rows))[axis == 0:1 if axis == 1 else 2]:
+        codes, scales = _fp4_bytes(r, c, block)
+        size += -(-codes // 512) * 512 + scales
+    memory = torch.empty(size, dtype=torch.uint8, device=x.device)
+    at = memory.data_ptr()
+    scale, along, across = 0, None, None
+    if block == 16:
+        scale, at = at, at + 512
+    if axis != 0:
+        along, at = _fp4_at(at, rows, cols, block, scale, memory, index)
+    if axis != 1:
+        across, at = _fp4_at(at, cols, rows, block, scale, memory, index)
     _call(lib().fp4_quantize, "fp4_quantize", index, stream, x.data_ptr(), kind, rows, cols, pitch,
           None if along is None else along._desc, None if across is None else across._desc, 0 if seed is None else 1,
           0 if seed is None else int(seed) & (2 ** 64 - 1))
@@ -1094,12 +1146,12 @@ def fp4_values(q, dtype=torch.bfloat16, out=None, stream=None):
     """The numbers that an FP4 matrix stands for, rows x cols, bfloat16 (exact
     there too) or float32."""
     if stream is not None:
-        return _on(stream, q.codes, fp4_values, q, dtype, out)
+        return _on(stream, q.scales, fp4_values, q, dtype, out)
     if out is None:
-        out = torch.empty((q.rows, q.cols), dtype=dtype, device=q.codes.device)
+        out = torch.empty((q.rows, q.cols), dtype=dtype, device=_device(q._index))
     elif out.shape != (q.rows, q.cols):
         raise ValueError("out must be rows x cols")
-    _call(lib().fp4_values, "fp4_values", _index_of("fp4_values", q.codes, out), stream, q._desc, out.data_ptr(),
+    _call(lib().fp4_values, "fp4_values", _same_device("fp4_values", q._index, out), stream, q._desc, out.data_ptr(),
           _dtype_code(out), _matrix(out, "out")[2])
     return out
 
@@ -1109,18 +1161,23 @@ def fp4_mm(a, b, dtype=torch.bfloat16, out=None, workspace=None, stream=None):
     bfloat16 or float32 (out's dtype where `out`, of any row pitch, is given).
     See fp4_mm in include/muon.h."""
     if stream is not None:
-        return _on(stream, a.codes, fp4_mm, a, b, dtype, out, workspace)
+        return _on(stream, a.scales, fp4_mm, a, b, dtype, out, workspace)
     if a.cols != b.cols or a.block != b.block:
         raise ValueError("a and b must have the same number of columns and the same block")
-    dev = a.codes.device
+    index = a._index
+    if b._index != index:
+        raise ValueError("fp4_mm: a and b must be on one device")
     if out is None:
-        out = torch.empty((a.rows, b.rows), dtype=dtype, device=dev)
-    elif out.shape != (a.rows, b.rows):
-        raise ValueError("out must be a.rows x b.rows")
+        dev = _device(index)
+        out, pitch = torch.empty((a.rows, b.rows), dtype=dtype, device=dev), b.rows
+    else:
+        if out.shape != (a.rows, b.rows):
+            raise ValueError("out must be a.rows x b.rows")
+        pitch, dev = _matrix(out, "out")[2], out.device
     if workspace is None:
         workspace = torch.empty(256, dtype=torch.uint8, device=dev)
-    _call(lib().fp4_mm, "fp4_mm", _index_of("fp4_mm", a.codes, b.codes, out, workspace), stream, a._desc, b._desc,
-          out.data_ptr(), _dtype_code(out), _matrix(out, "out")[2], workspace.data_ptr(), workspace.numel())
+    _call(lib().fp4_mm, "fp4_mm", _same_device("fp4_mm", index, out, workspace), stream, a._desc, b._desc,
+          out.data_ptr(), _dtype_code(out), pitch, workspace.data_ptr(), workspace.numel())
     return out
 
 
