@@ -612,7 +612,8 @@ muon_status_t fp4_values(const fp4_matrix* q, void* out, int dtype, int64_t out_
  * sum is rounded once.  cols = 0 gives zeros.  A NaN scale makes its row (column)
  * of out NaN.  out and workspace overlap nothing else.
  *   workspace  at least 256 bytes, 256-byte aligned, holding the device status
- *              word (muon_device_status).
+ *              word (muon_device_status) and nothing else: calls whose status
+ *              is not read may share one.
  * Asynchronous on `stream`; nothing is allocated; equal calls give equal bits.
  * Returns MUON_OK, MUON_ERR_INVALID_ARG, MUON_ERR_MISALIGNED,
  * MUON_ERR_ALIASING, MUON_ERR_WORKSPACE_TOO_SMALL, MUON_ERR_TOO_LARGE,

@@ -1021,6 +1021,11 @@ def _device(index):
     return torch.device("cuda", index)
 
 
+@functools.lru_cache(maxsize=64)
+def _unread_status(index):
+    return torch.empty(256, dtype=torch.uint8, device=_device(index))
+
+
 def _same_device(what, index, *tensors):
     for t in tensors:
         if t.get_device() != index:
@@ -1168,14 +1173,13 @@ def fp4_mm(a, b, dtype=torch.bfloat16, out=None, workspace=None, stream=None):
     if b._index != index:
         raise ValueError("fp4_mm: a and b must be on one device")
     if out is None:
-        dev = _device(index)
-        out, pitch = torch.empty((a.rows, b.rows), dtype=dtype, device=dev), b.rows
+        out, pitch = torch.empty((a.rows, b.rows), dtype=dtype, device=_device(index)), b.rows
     else:
         if out.shape != (a.rows, b.rows):
             raise ValueError("out must be a.rows x b.rows")
-        pitch, dev = _matrix(out, "out")[2], out.device
-    if workspace is None:
-        workspace = torch.empty(256, dtype=torch.uint8, device=dev)
+        pitch = _matrix(out, "out")[2]
+    if workspace is None:  # a status word that nobody reads: calls may share it
+        workspace = _unread_status(index)
     _call(lib().fp4_mm, "fp4_mm", _same_device("fp4_mm", index, out, workspace), stream, a._desc, b._desc,
           out.data_ptr(), _dtype_code(out), pitch, workspace.data_ptr(), workspace.numel())
     return out
@@ -1234,11 +1238,10 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, residual=None, out=None, str
     r, r_pitch = _rows_like(residual, x, "residual")
     y, y_pitch = _rows_out(out, x, "out")
     s, s_pitch = (None, 0) if residual is None else _rows_out(None, x, "sum")
-    stats = torch.empty((2, rows), dtype=torch.float32, device=x.device)
-    p = stats.data_ptr()
+    mean, rstd = (torch.empty(rows, dtype=torch.float32, device=x.device) for _ in range(2))
     _call(lib().layer_norm, "layer_norm", index, stream, x.data_ptr(), kind, rows, cols, pitch, r, r_pitch, w, b, wkind,
-          float(eps), y.data_ptr(), y_pitch, None if s is None else s.data_ptr(), s_pitch, p, p + 4 * rows)
-    return LayerNorm(y, *stats.unbind(), s)
+          float(eps), y.data_ptr(), y_pitch, None if s is None else s.data_ptr(), s_pitch, mean.data_ptr(), rstd.data_ptr())
+    return LayerNorm(y, mean, rstd, s)
 
 
 @functools.lru_cache(maxsize=256)
@@ -1264,11 +1267,12 @@ def layer_norm_backward(grad, x, mean, rstd, weight=None, bias=True, grad_sum=No
     mu, rs = _per_row(mean, rows, f32, "mean"), _per_row(rstd, rows, f32, "rstd")
     index = _index_of("layer_norm_backward", grad, x, mean, rstd, weight, grad_sum, out, workspace)
     out, out_pitch = _rows_out(out, x, "out")
-    columns = torch.empty((2, cols), dtype=f32, device=dev) if bias or w is not None else None
-    p = 0 if columns is None else columns.data_ptr()
+    grad_weight = None if w is None else torch.empty(cols, dtype=f32, device=dev)
+    grad_bias = torch.empty(cols, dtype=f32, device=dev) if bias else None
     if workspace is None:
         workspace = torch.empty(max(layer_norm_backward_workspace_size(rows, cols), 256), dtype=torch.uint8, device=dev)
     _call(lib().layer_norm_backward, "layer_norm_backward", index, stream, g, g_pitch, x.data_ptr(), pitch, kind, rows,
           cols, mu, rs, w, MUON_F32 if w is None else _dtype_code(weight), gs, gs_pitch, out.data_ptr(), out_pitch,
-          None if w is None else p, p + 4 * cols if bias else None, workspace.data_ptr(), workspace.numel())
-    return out, None if w is None else columns.select(0, 0), columns.select(0, 1) if bias else None
+          None if w is None else grad_weight.data_ptr(), grad_bias.data_ptr() if bias else None, workspace.data_ptr(),
+          workspace.numel())
+    return out, grad_weight, grad_bias
