@@ -186,19 +186,25 @@ __global__ void __launch_bounds__(Shape<BF16, L, W>::kThreads, W > 8 ? 1 : 2) no
   const float inv = 1.0f / static_cast<float>(P.cols);
   const long long step = static_cast<long long>(gridDim.x) * S::kGroups * S::kRows;
   long long r0 = (static_cast<long long>(blockIdx.x) * S::kGroups + group) * S::kRows;
-  auto fetch = [&](long long base, int stage) {
-    const long long r = base + lane / L;
-    if (base < P.rows && MUON_CHECK(r >= 0)) {
+  // this lane's row, here and (`next`) where rows are fetched
+  long long r = r0 + lane / L, next = r;
+  const char *nx = row_of<BF16>(P.x, next, P.sx, c0), *nr = row_of<BF16>(P.residual, next, P.sr, c0);
+  char *py = row_of<BF16>(P.y, r, P.sy, c0), *ps = row_of<BF16>(P.sum, r, P.ssum, c0);
+  uint32_t shift_x = rows::shift_of(nx), shift_r = rows::shift_of(nr);
+  auto fetch = [&](int stage) {
+    if (next - lane / L < P.rows && MUON_CHECK(next >= 0)) {
       const uint32_t to = at + stage * stage_bytes;
-      const int have = r < P.rows ? piece : -16;  // a warp's rows past the last one are zeros
-      const long long from = min(r, P.rows - 1);
-      rows::fetch<BF16, ALIGNED, L, V>(to, row_of<BF16>(P.x, from, P.sx, c0), have, sub, n);
-      if (P.residual) rows::fetch<BF16, ALIGNED, L, V>(to + array_bytes, row_of<BF16>(P.residual, from, P.sr, c0), have, sub, n);
+      const bool none = L < 32 && next >= P.rows;  // a warp's rows past the last one are zeros
+      rows::fetch<BF16, ALIGNED, L, V>(to, none ? row_of<BF16>(P.x, 0, 0, 0) : nx, piece, sub, n, none);
+      if (P.residual) rows::fetch<BF16, ALIGNED, L, V>(to + array_bytes, none ? row_of<BF16>(P.residual, 0, 0, 0) : nr, piece, sub, n, none);
     }
     rows::copies_commit();
+    next += step;
+    nx += step * P.sx * (16 / E);
+    nr += step * P.sr * (16 / E);
   };
   const bool ahead = P.stages == 2;
-  if (ahead) fetch(r0, 0);
+  if (ahead) fetch(0);
   if (P.weights_shared) {
     stage_weights<BF16>(wa, P.weight, P.weight_f32, 1.0f, P.cols, units, S::kThreads);
     stage_weights<BF16>(ba, P.bias, P.weight_f32, 0.0f, P.cols, units, S::kThreads);
@@ -206,20 +212,15 @@ __global__ void __launch_bounds__(Shape<BF16, L, W>::kThreads, W > 8 ? 1 : 2) no
   }
   for (int it = 0; r0 < P.rows; r0 += step, ++it) {
     const int stage = ahead ? it & 1 : 0;
-    if (ahead)
-      fetch(r0 + step, stage ^ 1);
-    else
-      fetch(r0, 0);
+    fetch(ahead ? stage ^ 1 : 0);
     rows::copies_wait(ahead);
     if (!ALIGNED) __syncwarp();
-    const long long r = r0 + lane / L;
-    const int left = r < P.rows ? piece : 0;
+    const bool inside = L == 32 || r < P.rows;
+    const int left = inside ? piece : 0;
     const uint32_t slot = at + stage * stage_bytes;
     Pair x[V][H], s = rows::pair(0.0f);
-    const uint32_t shift = ALIGNED ? 0u : rows::shift_of(row_of<BF16>(P.x, r, P.sx, c0));
+    const uint32_t shift = ALIGNED ? 0u : shift_x;
     if (P.residual) {
-      const uint32_t shift_r = ALIGNED ? 0u : rows::shift_of(row_of<BF16>(P.residual, r, P.sr, c0));
-      char* out = row_of<BF16>(P.sum, r, P.ssum, c0);
       uint4 q[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
@@ -227,12 +228,12 @@ __global__ void __launch_bounds__(Shape<BF16, L, W>::kThreads, W > 8 ? 1 : 2) no
         const int k = v * L + sub;
         Pair a[H];
         rows::numbers<BF16>(rows::unit<ALIGNED>(slot, shift, k), x[v]);
-        rows::numbers<BF16>(rows::unit<ALIGNED>(slot + array_bytes, shift_r, k), a);
+        rows::numbers<BF16>(rows::unit<ALIGNED>(slot + array_bytes, ALIGNED ? 0u : shift_r, k), a);
 #pragma unroll
         for (int i = 0; i < H; ++i) x[v][i] = rows::add(x[v][i], a[i]);
         q[v] = rows::pack<BF16>(x[v]);
         rows::numbers<BF16>(q[v], x[v]);
-        if (ALIGNED) rows::store_aligned<BF16>(out, k, left, q[v]);
+        if (ALIGNED) rows::store_unit<BF16>(ps, k, left, q[v], inside && v + 1 < n);
       }
       if (!ALIGNED) {
         __syncwarp();  // every lane has read its neighbours' units
@@ -240,7 +241,7 @@ __global__ void __launch_bounds__(Shape<BF16, L, W>::kThreads, W > 8 ? 1 : 2) no
         for (int v = 0; v < V; ++v)
           if (v < n) rows::shared_store(slot + 16 * (v * L + sub), q[v]);
         __syncwarp();
-        rows::store_shifted<BF16, L, V>(slot, out, left, sub, n);
+        rows::store_shifted<BF16, L, V>(slot, ps, left, sub, n);
       }
     } else {
 #pragma unroll
@@ -282,7 +283,6 @@ __global__ void __launch_bounds__(Shape<BF16, L, W>::kThreads, W > 8 ? 1 : 2) no
       P.mean[r] = mean;
       P.rstd[r] = rstd;
     }
-    char* out = row_of<BF16>(P.y, r, P.sy, c0);
     const Pair scale = rows::pair(rstd);
     if (!ALIGNED) __syncwarp();
 #pragma unroll
@@ -295,15 +295,20 @@ __global__ void __launch_bounds__(Shape<BF16, L, W>::kThreads, W > 8 ? 1 : 2) no
 #pragma unroll
       for (int i = 0; i < H; ++i) x[v][i] = rows::fma(rows::mul(x[v][i], scale), w[i], b[i]);
       if (ALIGNED)
-        rows::store_aligned<BF16>(out, k, left, rows::pack<BF16>(x[v]));
+        rows::store_unit<BF16>(py, k, left, rows::pack<BF16>(x[v]), inside && v + 1 < n);
       else
         rows::shared_store(slot + 16 * k, rows::pack<BF16>(x[v]));
     }
     if (!ALIGNED) {
       __syncwarp();
-      rows::store_shifted<BF16, L, V>(slot, out, left, sub, n);
+      rows::store_shifted<BF16, L, V>(slot, py, left, sub, n);
       __syncwarp();  // before the slot is filled again
+      shift_x = (shift_x + static_cast<uint32_t>(step * P.sx) * (16 / E)) & 15;
+      shift_r = (shift_r + static_cast<uint32_t>(step * P.sr) * (16 / E)) & 15;
     }
+    r += step;
+    py += step * P.sy * (16 / E);
+    ps += step * P.ssum * (16 / E);
   }
   rows::copies_wait(0);
 }
@@ -335,23 +340,30 @@ __global__ void __launch_bounds__(Shape<BF16, L, W>::kThreads, W > 8 ? 1 : 2) no
   const long long step = static_cast<long long>(gridDim.x) * S::kGroups * S::kRows;
   long long r0 = (static_cast<long long>(blockIdx.x) * S::kGroups + group) * S::kRows;
   float mean = 0.0f, rstd = 0.0f;  // of the row that is fetched
-  auto fetch = [&](long long base, int stage) {
-    const long long r = base + lane / L;
-    if (base < P.rows && MUON_CHECK(r >= 0)) {
+  long long r = r0 + lane / L, next = r;
+  const char *nx = row_of<BF16>(P.x, next, P.sx, c0), *ng = row_of<BF16>(P.grad, next, P.sg, c0);
+  const char* ns = row_of<BF16>(P.grad_sum, next, P.sgs, c0);
+  char* out = row_of<BF16>(P.y, r, P.sy, c0);
+  uint32_t shift_x = rows::shift_of(nx), shift_g = rows::shift_of(ng), shift_s = rows::shift_of(ns);
+  auto fetch = [&](int stage) {
+    if (next - lane / L < P.rows && MUON_CHECK(next >= 0)) {
       const uint32_t to = at + stage * stage_bytes;
-      const int have = r < P.rows ? piece : -16;
-      const long long from = min(r, P.rows - 1);
-      rows::fetch<BF16, ALIGNED, L, V>(to, row_of<BF16>(P.x, from, P.sx, c0), have, sub, n);
-      rows::fetch<BF16, ALIGNED, L, V>(to + array_bytes, row_of<BF16>(P.grad, from, P.sg, c0), have, sub, n);
-      if (P.grad_sum)
-        rows::fetch<BF16, ALIGNED, L, V>(to + 2 * array_bytes, row_of<BF16>(P.grad_sum, from, P.sgs, c0), have, sub, n);
+      const bool none = L < 32 && next >= P.rows;
+      rows::fetch<BF16, ALIGNED, L, V>(to, none ? row_of<BF16>(P.x, 0, 0, 0) : nx, piece, sub, n, none);
+      rows::fetch<BF16, ALIGNED, L, V>(to + array_bytes, none ? row_of<BF16>(P.grad, 0, 0, 0) : ng, piece, sub, n, none);
+      if (P.grad_sum) rows::fetch<BF16, ALIGNED, L, V>(to + 2 * array_bytes, none ? row_of<BF16>(P.grad_sum, 0, 0, 0) : ns, piece, sub, n, none);
+      const long long from = L == 32 ? next : min(next, P.rows - 1);
       mean = P.mean[from];
       rstd = P.rstd[from];
     }
     rows::copies_commit();
+    next += step;
+    nx += step * P.sx * (16 / E);
+    ng += step * P.sg * (16 / E);
+    ns += step * P.sgs * (16 / E);
   };
   const bool ahead = P.stages == 2;
-  if (ahead) fetch(r0, 0);
+  if (ahead) fetch(0);
   if (P.weights_shared) {
     stage_weights<BF16>(wa, P.weight, P.weight_f32, 1.0f, P.cols, units, S::kThreads);
     __syncthreads();
@@ -363,26 +375,24 @@ __global__ void __launch_bounds__(Shape<BF16, L, W>::kThreads, W > 8 ? 1 : 2) no
     for (int i = 0; i < H; ++i) dw[v][i] = db[v][i] = rows::pair(0.0f);
   for (int it = 0; r0 < P.rows; r0 += step, ++it) {
     const int stage = ahead ? it & 1 : 0;
-    if (!ahead) fetch(r0, 0);
-    const long long r = r0 + lane / L;
-    // (gradients past the row's end are zeros, and with them all that is added up; rows past the
-    // last one are left out by their own)
+    if (!ahead) fetch(0);
+    // (gradients past the row's end are zeros, and with them all that is added up; so are those of
+    // a warp's rows past the last one)
     const Pair minus = rows::pair(-mean), scale = rows::pair(rstd);
-    if (ahead) fetch(r0 + step, stage ^ 1);
+    if (ahead) fetch(stage ^ 1);
     rows::copies_wait(ahead);
     if (!ALIGNED) __syncwarp();
-    const int left = r < P.rows ? piece : 0;
+    const bool inside = L == 32 || r < P.rows;
+    const int left = inside ? piece : 0;
     const uint32_t slot = at + stage * stage_bytes;
-    const uint32_t shift_x = ALIGNED ? 0u : rows::shift_of(row_of<BF16>(P.x, r, P.sx, c0));
-    const uint32_t shift_g = ALIGNED ? 0u : rows::shift_of(row_of<BF16>(P.grad, r, P.sg, c0));
     Pair a = rows::pair(0.0f), b = rows::pair(0.0f);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       if (v >= n) break;
       const int k = v * L + sub;
       Pair x[H], g[H], w[H];
-      rows::numbers<BF16>(rows::unit<ALIGNED>(slot, shift_x, k), x);
-      rows::numbers<BF16>(rows::unit<ALIGNED>(slot + array_bytes, shift_g, k), g);
+      rows::numbers<BF16>(rows::unit<ALIGNED>(slot, ALIGNED ? 0u : shift_x, k), x);
+      rows::numbers<BF16>(rows::unit<ALIGNED>(slot + array_bytes, ALIGNED ? 0u : shift_g, k), g);
       weights<BF16>(P, wa, P.weight, 1.0f, unit0 + k, units, w);
 #pragma unroll
       for (int i = 0; i < H; ++i) {
@@ -396,15 +406,13 @@ __global__ void __launch_bounds__(Shape<BF16, L, W>::kThreads, W > 8 ? 1 : 2) no
     }
     const float2 s = row_sum2<L, W>(rows::total(a), rows::total(b), slots[group][it & 1], group, warp_in);
     const Pair c1 = rows::pair(-s.x * inv), c2 = rows::pair(-s.y * inv);
-    char* out = row_of<BF16>(P.y, r, P.sy, c0);
-    const uint32_t shift_s = ALIGNED ? 0u : rows::shift_of(row_of<BF16>(P.grad_sum, r, P.sgs, c0));
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       if (v >= n) break;
       const int k = v * L + sub;
       Pair x[H], g[H], w[H], o[H];
-      rows::numbers<BF16>(rows::unit<ALIGNED>(slot, shift_x, k), x);
-      rows::numbers<BF16>(rows::unit<ALIGNED>(slot + array_bytes, shift_g, k), g);
+      rows::numbers<BF16>(rows::unit<ALIGNED>(slot, ALIGNED ? 0u : shift_x, k), x);
+      rows::numbers<BF16>(rows::unit<ALIGNED>(slot + array_bytes, ALIGNED ? 0u : shift_g, k), g);
       weights<BF16>(P, wa, P.weight, 1.0f, unit0 + k, units, w);
 #pragma unroll
       for (int i = 0; i < H; ++i) {
@@ -412,7 +420,7 @@ __global__ void __launch_bounds__(Shape<BF16, L, W>::kThreads, W > 8 ? 1 : 2) no
         o[i] = rows::fma(xhat, c2, rows::fma(g[i], w[i], c1));
       }
       if (P.grad_sum) {
-        rows::numbers<BF16>(rows::unit<ALIGNED>(slot + 2 * array_bytes, shift_s, k), x);
+        rows::numbers<BF16>(rows::unit<ALIGNED>(slot + 2 * array_bytes, ALIGNED ? 0u : shift_s, k), x);
 #pragma unroll
         for (int i = 0; i < H; ++i) o[i] = rows::fma(scale, o[i], x[i]);
       } else {
@@ -420,7 +428,7 @@ __global__ void __launch_bounds__(Shape<BF16, L, W>::kThreads, W > 8 ? 1 : 2) no
         for (int i = 0; i < H; ++i) o[i] = rows::mul(scale, o[i]);
       }
       if (ALIGNED) {
-        rows::store_aligned<BF16>(out, k, left, rows::pack<BF16>(o));
+        rows::store_unit<BF16>(out, k, left, rows::pack<BF16>(o), inside && v + 1 < n);
       } else {
         __syncwarp();  // the neighbours have read this unit of x
         rows::shared_store(slot + 16 * k, rows::pack<BF16>(o));
@@ -430,7 +438,12 @@ __global__ void __launch_bounds__(Shape<BF16, L, W>::kThreads, W > 8 ? 1 : 2) no
       __syncwarp();
       rows::store_shifted<BF16, L, V>(slot, out, left, sub, n);
       __syncwarp();
+      shift_x = (shift_x + static_cast<uint32_t>(step * P.sx) * (16 / E)) & 15;
+      shift_g = (shift_g + static_cast<uint32_t>(step * P.sg) * (16 / E)) & 15;
+      shift_s = (shift_s + static_cast<uint32_t>(step * P.sgs) * (16 / E)) & 15;
     }
+    r += step;
+    out += step * P.sy * (16 / E);
   }
   rows::copies_wait(0);
   if (!P.partial) return;
@@ -464,9 +477,9 @@ __global__ void __launch_bounds__(Shape<BF16, L, W>::kThreads, W > 8 ? 1 : 2) no
     __syncthreads();
   }
   if (!MUON_CHECK(static_cast<int>(blockIdx.x) < P.parts)) return;
-  float* out = P.partial + static_cast<long long>(blockIdx.x) * 2 * P.cols;
+  float* to = P.partial + static_cast<long long>(blockIdx.x) * 2 * P.cols;
   const float* all = reinterpret_cast<const float*>(dynamic);
-  for (int i = threadIdx.x; i < 2 * P.cols; i += S::kThreads) out[i] = all[i < P.cols ? i : units * E + i - P.cols];
+  for (int i = threadIdx.x; i < 2 * P.cols; i += S::kThreads) to[i] = all[i < P.cols ? i : units * E + i - P.cols];
 }
 
 // Adds the partial sums: 32 columns a CTA, its warps take parts in turn.

@@ -58,28 +58,39 @@ __device__ __forceinline__ uint4 funnel(const uint4& a, const uint4& b, uint32_t
 
 __device__ __forceinline__ uint32_t shift_of(const void* p) { return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15); }
 
+__device__ __forceinline__ void copy_ahead(uint32_t at, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
+}
+
 // Starts the copies of units k = sub, sub + L, ... (n of them) of a piece of a
-// row that begins at `p` and has `left` entries (< 0: none), zeros behind those; the
-// last lane also copies the unit past the piece's last one.
+// row that begins at `p` and has `left` entries, more than (n - 1) L units of
+// them: only the last one may reach past them, and has zeros there.  The last
+// lane also copies the unit behind the piece's last one.  `none`: zeros throughout.
 template <bool BF16, bool ALIGNED, int L, int V>
-__device__ __forceinline__ void fetch(uint32_t slot, const char* p, int left, int sub, int n) {
+__device__ __forceinline__ void fetch(uint32_t slot, const char* p, int left, int sub, int n, bool none) {
   using U = Unit<BF16>;
   const uint32_t shift = ALIGNED ? 0u : shift_of(p);
   const char* from = p - shift + 16 * sub;
-  const int bytes = left * U::size + static_cast<int>(shift);  // from the first unit's begin on
-  int have = bytes - 16 * sub;
+  const uint32_t to = slot + 16 * sub;
+  // bytes of the last unit, and of the one behind the piece
+  const int have = min(left, n * L * U::n + U::n) * U::size + static_cast<int>(shift) - 16 * (n - 1) * L;
+  const int last = none ? 0 : min(max(have - 16 * sub, 0), 16);
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    if (v >= n) break;
-    // (nothing is read where `bytes` is 0, so the address does not matter then)
-    copy_ahead(slot + 16 * (v * L + sub), have > 0 ? from : p - shift, min(max(have, 0), 16));
-    from += 16 * L;
-    have -= 16 * L;
+    if (v + 1 < n) {
+      if (none)
+        copy_ahead(to + 16 * L * v, from, 0);
+      else
+        copy_ahead(to + 16 * L * v, from + 16 * L * v);
+    } else if (v + 1 == n) {
+      // (nothing is read where there are 0 bytes, so the address does not matter then)
+      copy_ahead(to + 16 * L * v, last ? from + 16 * L * v : p - shift, last);
+    }
   }
   if constexpr (!ALIGNED) {
-    if (sub == L - 1) {
-      have = bytes - 16 * n * L;
-      copy_ahead(slot + 16 * n * L, have > 0 ? p - shift + 16 * n * L : p - shift, min(max(have, 0), 16));
+    if (sub == L - 1 && n > 0) {
+      const int behind = none ? 0 : min(max(have - 16 * L, 0), 16);
+      copy_ahead(slot + 16 * n * L, behind ? p - shift + 16 * n * L : p - shift, behind);
     }
   }
 }
@@ -174,14 +185,15 @@ __device__ __forceinline__ void store_some(char* p, const uint4& q, int from, in
   }
 }
 
-// Unit k of a piece that begins on 16 bytes.
+// Unit k of a piece that begins on 16 bytes; `whole`: it lies within the piece.
 template <bool BF16>
-__device__ __forceinline__ void store_aligned(char* p, int k, int left, const uint4& q) {
+__device__ __forceinline__ void store_unit(char* p, int k, int left, const uint4& q, bool whole) {
   using U = Unit<BF16>;
-  if ((k + 1) * U::n <= left)
+  const int room = left - k * U::n;
+  if (whole || room >= U::n)
     *reinterpret_cast<uint4*>(p + 16 * k) = q;
-  else
-    store_some<BF16>(p + 16 * k, q, 0, left - k * U::n);
+  else if (room > 0)
+    store_some<BF16>(p + 16 * k, q, 0, room);
 }
 
 // The piece at `p` from the units that the warp has put into the slot.
