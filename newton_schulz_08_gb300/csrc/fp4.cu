@@ -200,7 +200,9 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {  // of unsign
 template <bool BF16>
 struct Tile {
   static constexpr int size = BF16 ? 2 : 4;
-  static constexpr int units = BF16 ? 1 : 2;            // of a lane's 8 entries
+  // a lane's entries of a row: two units of 16 bytes (float32 with 16 entries a lane, whose units lie 64 bytes
+  // apart: 144 us for 16384 x 6400 both ways, 121 with 8; bfloat16 with 8: 68, 60 with 16)
+  static constexpr int units = 2, entries = 32 / size, lanes = kTile / entries, rows = kThreads / lanes;
   static constexpr int pitch = kTile * size + 16;       // bytes of a row
   static constexpr int bytes = kTile * pitch;
 };
@@ -214,11 +216,11 @@ __host__ __device__ constexpr int tile_smem() { return Tile<BF16>::bytes + (ACRO
 template <bool BF16>
 __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return BF16 ? max2(a, b) : max(a, b); }
 
-// Eight numbers of a lane's units.
+// Eight numbers of a lane's: bfloat16, the first (h = 0) or second half.
 template <bool BF16>
-__device__ __forceinline__ void numbers8(const uint4 (&q)[Tile<BF16>::units], Pair (&x)[4]) {
+__device__ __forceinline__ void numbers8(const uint4 (&q)[2], int h, Pair (&x)[4]) {
   if constexpr (BF16) {
-    rows::numbers<true>(q[0], x);
+    rows::numbers<true>(q[h], x);
   } else {
     x[0] = rows::pair(__uint_as_float(q[0].x), __uint_as_float(q[0].y));
     x[1] = rows::pair(__uint_as_float(q[0].z), __uint_as_float(q[0].w));
@@ -255,24 +257,24 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 5 : 3) fp4_quantize_kernel(co
   const int by = static_cast<int>(blockIdx.x) / P.tiles_x, bx = static_cast<int>(blockIdx.x) - by * P.tiles_x;
   const int r0 = by * kTile, c0 = bx * kTile;
   const uint32_t tile = rows::shared_address(smem);
-  // 16 lanes a row, 8 entries a lane, 16 rows at a time
-  const int g = tid & 15, row = tid >> 4, col = c0 + 8 * g;
+  // T::lanes lanes a row, T::rows rows at a time
+  const int g = tid % T::lanes, row = tid / T::lanes, col = c0 + T::entries * g;
   {
     const char* p = static_cast<const char*>(P.x) + ((r0 + row) * P.stride + c0) * T::size;
     uint32_t to = tile + row * T::pitch + g * (16 * T::units);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < kTile / T::rows; ++i) {
       const uint32_t shift = P.vec ? 0u : rows::shift_of(p);
       const char* from = p - shift;
       // bytes from the row's first unit here on that belong to it
-      const int bytes = r0 + row + 16 * i < P.rows ? min(P.cols - c0, kTile + 8) * T::size + static_cast<int>(shift) : 0;
+      const int bytes = r0 + row + T::rows * i < P.rows ? min(P.cols - c0, kTile + 8) * T::size + static_cast<int>(shift) : 0;
 #pragma unroll
       for (int u = 0; u < T::units + 1; ++u) {
         const int at = (g * T::units + u) * 16, have = min(max(bytes - at, 0), 16);
-        if (u < T::units || (g == 15 && shift != 0)) rows::copy_ahead(to + 16 * u, have ? from + at : static_cast<const char*>(P.x) - rows::shift_of(P.x), have);
+        if (u < T::units || (g == T::lanes - 1 && shift != 0)) rows::copy_ahead(to + 16 * u, have ? from + at : static_cast<const char*>(P.x) - rows::shift_of(P.x), have);
       }
-      p += 16 * P.stride * T::size;
-      to += 16 * T::pitch;
+      p += T::rows * P.stride * T::size;
+      to += T::rows * T::pitch;
     }
     rows::copies_commit();
   }
@@ -289,9 +291,9 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 5 : 3) fp4_quantize_kernel(co
     uint8_t* out = P.along.codes + (r0 + row) * P.along.pitch + col / 2;
     uint64_t j = static_cast<uint64_t>(r0 + row) * ((P.cols + 1) / 2) + col / 2;
     const char* p = static_cast<const char*>(P.x) + ((r0 + row) * P.stride + c0) * T::size;
-#pragma unroll 2
-    for (int i = 0; i < 8; ++i) {
-      const int r = row + 16 * i;
+#pragma unroll 1
+    for (int i = 0; i < kTile / T::rows; ++i) {
+      const int r = row + T::rows * i;
       uint4 q[T::units];
 #pragma unroll
       for (int u = 0; u < T::units; ++u) q[u] = rows::shared_load(at + 16 * u);
@@ -307,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 5 : 3) fp4_quantize_kernel(co
 #pragma unroll
           for (int u = 0; u < T::units; ++u) rows::shared_store(at + 16 * u, q[u]);
         }
-        p += 16 * P.stride * T::size;
+        p += T::rows * P.stride * T::size;
       }
       if constexpr (ALONG) {
         uint32_t m = 0;
@@ -316,22 +318,31 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 5 : 3) fp4_quantize_kernel(co
           constexpr uint32_t k = BF16 ? 0x7FFF7FFFu : 0x7FFFFFFFu;
           m = larger<BF16>(m, larger<BF16>(larger<BF16>(q[u].x & k, q[u].y & k), larger<BF16>(q[u].z & k, q[u].w & k)));
         }
-        m = larger<BF16>(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-        if constexpr (BLOCK == 32) m = larger<BF16>(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+        constexpr int kShare = BLOCK / T::entries;  // lanes of a block
+        if constexpr (kShare > 1) m = larger<BF16>(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+        if constexpr (kShare > 2) m = larger<BF16>(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
         if constexpr (BF16) m = max(m << 16, m & 0xFFFF0000u);
         const Scale sc = block_scale<BLOCK, SR>(m, up);
-        Pair x[4];
-        numbers8<BF16>(q, x);
-        const uint32_t word = codes8<BLOCK, SR>(x, sc, j, P.along.key);
+        uint32_t word[2];
+#pragma unroll
+        for (int h = 0; h < T::entries / 8; ++h) {
+          Pair x[4];
+          numbers8<BF16>(q, h, x);
+          word[h] = codes8<BLOCK, SR>(x, sc, j + 4 * h, P.along.key);
+        }
         const bool inside = r0 + r < P.rows;
-        if (inside && col / 2 < P.along.pitch && MUON_CHECK(col >= 0 && col / 2 + 4 <= P.along.pitch)) *reinterpret_cast<uint32_t*>(out) = word;
-        const int b = BLOCK == 32 ? g >> 2 : g >> 1;
-        if ((g & (BLOCK / 8 - 1)) == 0)
-          sf_along[(b >> 2) * 512 + (r & 31) * 16 + (r >> 5) * 4 + (b & 3)] = inside ? sc.code : 0;
-        out += 16 * P.along.pitch;
-        j += 16ull * ((P.cols + 1) / 2);
+        if (inside && col / 2 < P.along.pitch && MUON_CHECK(col >= 0 && col / 2 + T::entries / 2 <= P.along.pitch)) {
+          if constexpr (BF16)
+            *reinterpret_cast<uint2*>(out) = make_uint2(word[0], word[1]);
+          else
+            *reinterpret_cast<uint32_t*>(out) = word[0];
+        }
+        const int b = g / kShare;
+        if (g % kShare == 0) sf_along[(b >> 2) * 512 + (r & 31) * 16 + (r >> 5) * 4 + (b & 3)] = inside ? sc.code : 0;
+        out += T::rows * P.along.pitch;
+        j += static_cast<uint64_t>(T::rows) * ((P.cols + 1) / 2);
       }
-      at += 16 * T::pitch;
+      at += T::rows * T::pitch;
     }
   }
   __syncthreads();
