@@ -468,45 +468,43 @@ __global__ void __launch_bounds__(kThreads) fp4_amax_kernel(const char* x, long 
   if (lane == 0 && top) atomicMax(out, top);
 }
 
-// The numbers that codes stand for: a lane takes 8 codes (4 bytes), a warp 256
-// of a row.  E2M1 numbers as bfloat16 come byte-wise from two tables of 8 that fit in registers.
-template <bool BF16>
+// The numbers that codes stand for: 128 rows x 256 columns a CTA, whose scales are
+// whole tiles; a warp takes 16 rows, a lane 8 codes (4 bytes) of each.  E2M1 numbers
+// as bfloat16 come byte-wise from two tables of 8 that fit in registers.
+template <bool BF16, int BLOCK>
 __global__ void __launch_bounds__(kThreads) fp4_values_kernel(const uint8_t* codes, const uint8_t* scales, const float* scale,
-                                                              int rows, int cols, int block, long long pitch,
+                                                              int rows, int cols, int tiles_x, long long pitch,
                                                               long long ktiles, void* out, long long stride, int vec) {
+  constexpr int kTiles = 64 / BLOCK, kRows = kTile / (kThreads / 32), kBatch = 8;
+  __shared__ __align__(16) uint8_t sf[kTiles * 512];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int pieces = (cols + 255) / 256, lane = threadIdx.x & 31;
-  const float tensor = block == 16 ? *scale : 1.0f;
-  const int shift = block == 16 ? 4 : 5;
-  const long long total = static_cast<long long>(rows) * pieces, step = static_cast<long long>(gridDim.x) * (kThreads / 32);
-  constexpr int kBatch = 4;  // pieces of a warp in flight
-  for (long long base = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); base < total; base += step * kBatch) {
-    uint32_t word[kBatch], code[kBatch];
-    long long at[kBatch];
-    int from[kBatch];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int by = static_cast<int>(blockIdx.x) / tiles_x, bx = static_cast<int>(blockIdx.x) - by * tiles_x;
+  const int c = bx * 256 + lane * 8, r0 = warp * kRows;  // r0: within the tile
+  const float tensor = BLOCK == 16 ? *scale : 1.0f;
+  if (threadIdx.x < 32 * kTiles)
+    reinterpret_cast<uint4*>(sf)[threadIdx.x] = __ldg(reinterpret_cast<const uint4*>(scales + (by * ktiles + bx * kTiles) * 512) + threadIdx.x);
+  const uint8_t* from = codes + (static_cast<long long>(by) * kTile + r0) * pitch + c / 2;
+  const long long at = (static_cast<long long>(by) * kTile + r0) * stride + c;
+  const int n = c < cols ? min(kRows, rows - by * kTile - r0) : 0;
+  __syncthreads();
+#pragma unroll 1
+  for (int base = 0; base < kRows; base += kBatch) {
+    uint32_t word[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      word[i] = base + i < n ? __ldg(reinterpret_cast<const uint32_t*>(from + (base + i) * pitch)) : 0u;
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      const long long piece = base + i * step;
-      const long long r = total <= 0x7FFFFFFF ? static_cast<long long>(static_cast<uint32_t>(piece) / static_cast<uint32_t>(pieces)) : piece / pieces;
-      const int c = static_cast<int>(piece - r * pieces) * 256 + lane * 8;
-      from[i] = piece < total ? c : cols;
-      at[i] = r * stride + c;
-      word[i] = code[i] = 0;
-      if (from[i] < cols) {
-        word[i] = __ldg(reinterpret_cast<const uint32_t*>(codes + r * pitch + c / 2));
-        const int b = c >> shift;
-        code[i] = __ldg(scales + ((r >> 7) * ktiles + (b >> 2)) * 512 + (r & 31) * 16 + ((r & 127) >> 5) * 4 + (b & 3));
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      if (from[i] >= cols) continue;
+      if (base + i >= n) continue;
+      const int r = r0 + base + i, b = lane * 8 / BLOCK;
+      const uint32_t code = sf[(b >> 2) * 512 + (r & 31) * 16 + (r >> 5) * 4 + (b & 3)];
       float s;
-      if (block == 32) {
-        s = code[i] == 255 ? NAN : pow2(static_cast<int>(code[i]) - 127);
+      if constexpr (BLOCK == 32) {
+        s = code == 255 ? NAN : pow2(static_cast<int>(code) - 127);
       } else {
-        s = code[i] == 0x7F ? NAN : code[i] < 8 ? code[i] * 0.001953125f : __uint_as_float((code[i] << 20) + (120u << 23));
+        s = code == 0x7F ? NAN : code < 8 ? code * 0.001953125f : __uint_as_float((code << 20) + (120u << 23));
         s *= tensor;
       }
       Pair v[4];
@@ -516,28 +514,27 @@ __global__ void __launch_bounds__(kThreads) fp4_values_kernel(const uint8_t* cod
         const uint32_t hi = __byte_perm(0x3F3F3F00u, 0x40404040u, select), lo = __byte_perm(0xC0800000u, 0xC0804000u, select);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const uint32_t a = __byte_perm(lo, hi, k ? 0x62 : 0x40) << 16, b = __byte_perm(lo, hi, k ? 0x73 : 0x51) << 16;
-          const uint32_t sa = four << (28 - 8 * k) & 0x80000000u, sb = four << (24 - 8 * k) & 0x80000000u;
-          v[2 * h + k] = rows::mul(rows::pair(__uint_as_float(a | sa), __uint_as_float(b | sb)), rows::pair(s));
+          const uint32_t x = __byte_perm(lo, hi, k ? 0x62 : 0x40) << 16, y = __byte_perm(lo, hi, k ? 0x73 : 0x51) << 16;
+          const uint32_t sx = four << (28 - 8 * k) & 0x80000000u, sy = four << (24 - 8 * k) & 0x80000000u;
+          v[2 * h + k] = rows::mul(rows::pair(__uint_as_float(x | sx), __uint_as_float(y | sy)), rows::pair(s));
         }
       }
+      char* o = static_cast<char*>(out) + (at + (base + i) * stride) * (BF16 ? 2 : 4);
       if constexpr (BF16) {
         const uint4 q = rows::pack<true>(v);
-        char* o = static_cast<char*>(out) + at[i] * 2;
-        if (vec && from[i] + 8 <= cols)
+        if (vec && c + 8 <= cols)
           *reinterpret_cast<uint4*>(o) = q;
         else
-          rows::store_some<true>(o, q, 0, cols - from[i]);
+          rows::store_some<true>(o, q, 0, cols - c);
       } else {
-        char* o = static_cast<char*>(out) + at[i] * 4;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const Pair two[2] = {v[2 * h], v[2 * h + 1]};
           const uint4 q = rows::pack<false>(two);
-          if (vec && from[i] + 8 <= cols)
+          if (vec && c + 8 <= cols)
             reinterpret_cast<uint4*>(o)[h] = q;
           else
-            rows::store_some<false>(o + 16 * h, q, 0, cols - from[i] - 4 * h);
+            rows::store_some<false>(o + 16 * h, q, 0, cols - c - 4 * h);
         }
       }
     }
@@ -720,15 +717,17 @@ extern "C" muon_status_t fp4_values(const fp4_matrix* q, void* out, int dtype, i
   const uint8_t* codes = static_cast<const uint8_t*>(q->codes);
   const uint8_t* scales = static_cast<const uint8_t*>(q->scales);
   const float* scale = q->scale;
-  int rows = static_cast<int>(q->rows), cols = static_cast<int>(q->cols), block = q->block;
-  long long pitch = fp4_pitch(q->cols), ktiles = fp4_ktiles(q->cols, block), stride = out_stride;
+  const int64_t tiles = (q->cols + 255) / 256;
+  if (tiles * fp4_row_tiles(q->rows) > 0x7FFFFFFF) return MUON_ERR_TOO_LARGE;
+  int rows = static_cast<int>(q->rows), cols = static_cast<int>(q->cols), tiles_x = static_cast<int>(tiles);
+  long long pitch = fp4_pitch(q->cols), ktiles = fp4_ktiles(q->cols, q->block), stride = out_stride;
   int vec = aligned_to(out, 16) && out_stride * size % 16 == 0;
-  const int64_t groups = q->rows * ((q->cols + 255) / 256);  // warps' pieces
-  void* args[] = {&codes, &scales, &scale, &rows, &cols, &block, &pitch, &ktiles, &out, &stride, &vec};
-  if (launch(dtype == MUON_BF16 ? reinterpret_cast<const void*>(&fp4_values_kernel<true>)
-                                : reinterpret_cast<const void*>(&fp4_values_kernel<false>),
-             dim3(static_cast<unsigned>(std::min<int64_t>((groups + 7) / 8, sms * 8))), 0, args,
-             static_cast<cudaStream_t>(stream)) != cudaSuccess)
+  void* args[] = {&codes, &scales, &scale, &rows, &cols, &tiles_x, &pitch, &ktiles, &out, &stride, &vec};
+  const void* fn = q->block == 32 ? (dtype == MUON_BF16 ? reinterpret_cast<const void*>(&fp4_values_kernel<true, 32>)
+                                                        : reinterpret_cast<const void*>(&fp4_values_kernel<false, 32>))
+                                  : (dtype == MUON_BF16 ? reinterpret_cast<const void*>(&fp4_values_kernel<true, 16>)
+                                                        : reinterpret_cast<const void*>(&fp4_values_kernel<false, 16>));
+  if (launch(fn, dim3(static_cast<unsigned>(tiles * fp4_row_tiles(q->rows))), 0, args, static_cast<cudaStream_t>(stream)) != cudaSuccess)
     return MUON_ERR_CUDA;
   return MUON_OK;
 }
