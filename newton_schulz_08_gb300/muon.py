@@ -1121,7 +1121,7 @@ def fp4_quantize(x, block=32, axis=1, seed=None, stream=None):
     seed; None: to nearest.  See fp4_quantize in include/muon.h."""
     if stream is not None:
         return _on(stream, x, fp4_quantize, x, block, axis, seed)
-    rows, cols, pitch = _matrix(x, "x")
+    rows, cols, pitch = _rows(x, "x")
     if block != 32 and block != 16:
         raise ValueError("block must be 32 or 16")
     if axis not in (0, 1, "both"):
@@ -1132,7 +1132,7 @@ def fp4_quantize(x, block=32, axis=1, seed=None, stream=None):
     for r, c in ((rows, cols), (cols, rows))[axis == 0:1 if axis == 1 else 2]:
         codes, scales = _fp4_bytes(r, c, block)
         size += -(-codes // 512) * 512 + scales
-    memory = torch.empty(size, dtype=torch.uint8, device=x.device)
+    memory = torch.empty(size, dtype=torch.uint8, device=_device(index))
     at = memory.data_ptr()
     scale, along, across = 0, None, None
     if block == 16:
@@ -1194,13 +1194,24 @@ class LayerNorm(NamedTuple):
     sum: Optional[torch.Tensor] = None
 
 
-def _rows_out(out, like, what):
-    """(tensor, row pitch) of an output shaped like `like`."""
+def _rows(t, what):
+    """_matrix(t, what), with fewer questions to a contiguous tensor."""
+    shape = t.shape
+    if len(shape) == 2 and t.is_contiguous():
+        return shape[0], shape[1], shape[1]
+    return _matrix(t, what)
+
+
+def _rows_out(out, like, pitch, what):
+    """(tensor, row pitch) of an output shaped like `like` (row pitch `pitch`)."""
     if out is None:
-        out = torch.empty(like.shape, dtype=like.dtype, device=like.device)
-    elif out.shape != like.shape or out.dtype != like.dtype:
+        cols = like.shape[1]
+        if pitch == cols:
+            return torch.empty_like(like), cols
+        return torch.empty(like.shape, dtype=like.dtype, device=like.device), cols
+    if out.shape != like.shape or out.dtype != like.dtype:
         raise ValueError(f"{what} must have x's shape and dtype")
-    return out, _matrix(out, what)[2]
+    return out, _rows(out, what)[2]
 
 
 def _rows_like(t, x, what):
@@ -1209,7 +1220,7 @@ def _rows_like(t, x, what):
         return None, 0
     if t.shape != x.shape or t.dtype != x.dtype:
         raise ValueError(f"{what} must have x's shape and dtype")
-    return t.data_ptr(), _matrix(t, what)[2]
+    return t.data_ptr(), _rows(t, what)[2]
 
 
 def _per_column(t, cols, what):
@@ -1228,19 +1239,24 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, residual=None, out=None, str
     layer_norm in include/muon.h."""
     if stream is not None:
         return _on(stream, x, layer_norm, x, weight, bias, eps, residual, out)
-    rows, cols, pitch = _matrix(x, "x")
+    rows, cols, pitch = _rows(x, "x")
     kind = _dtype_code(x)
     w, b = _per_column(weight, cols, "weight"), _per_column(bias, cols, "bias")
     if w is not None and b is not None and weight.dtype != bias.dtype:
         raise ValueError("weight and bias must have the same dtype")
     wkind = _dtype_code(weight) if w is not None else _dtype_code(bias) if b is not None else MUON_F32
     index = _index_of("layer_norm", x, weight, bias, residual, out)
-    r, r_pitch = _rows_like(residual, x, "residual")
-    y, y_pitch = _rows_out(out, x, "out")
-    s, s_pitch = (None, 0) if residual is None else _rows_out(None, x, "sum")
-    mean, rstd = (torch.empty(rows, dtype=torch.float32, device=x.device) for _ in range(2))
+    y, y_pitch = _rows_out(out, x, pitch, "out")
+    r = s_ptr = s = None
+    r_pitch = s_pitch = 0
+    if residual is not None:
+        r, r_pitch = _rows_like(residual, x, "residual")
+        s, s_pitch = _rows_out(None, x, pitch, "sum")
+        s_ptr = s.data_ptr()
+    dev = _device(index)
+    mean, rstd = torch.empty(rows, dtype=torch.float32, device=dev), torch.empty(rows, dtype=torch.float32, device=dev)
     _call(lib().layer_norm, "layer_norm", index, stream, x.data_ptr(), kind, rows, cols, pitch, r, r_pitch, w, b, wkind,
-          float(eps), y.data_ptr(), y_pitch, None if s is None else s.data_ptr(), s_pitch, mean.data_ptr(), rstd.data_ptr())
+          eps, y.data_ptr(), y_pitch, s_ptr, s_pitch, mean.data_ptr(), rstd.data_ptr())
     return LayerNorm(y, mean, rstd, s)
 
 
@@ -1259,14 +1275,15 @@ def layer_norm_backward(grad, x, mean, rstd, weight=None, bias=True, grad_sum=No
     `out` may be grad or grad_sum itself.  See layer_norm_backward in include/muon.h."""
     if stream is not None:
         return _on(stream, x, layer_norm_backward, grad, x, mean, rstd, weight, bias, grad_sum, out, workspace)
-    rows, cols, pitch = _matrix(x, "x")
-    kind, f32, dev = _dtype_code(x), torch.float32, x.device
+    rows, cols, pitch = _rows(x, "x")
+    kind, f32 = _dtype_code(x), torch.float32
     g, g_pitch = _rows_like(grad, x, "grad")
     gs, gs_pitch = _rows_like(grad_sum, x, "grad_sum")
     w = _per_column(weight, cols, "weight")
     mu, rs = _per_row(mean, rows, f32, "mean"), _per_row(rstd, rows, f32, "rstd")
     index = _index_of("layer_norm_backward", grad, x, mean, rstd, weight, grad_sum, out, workspace)
-    out, out_pitch = _rows_out(out, x, "out")
+    dev = _device(index)
+    out, out_pitch = _rows_out(out, x, pitch, "out")
     grad_weight = None if w is None else torch.empty(cols, dtype=f32, device=dev)
     grad_bias = torch.empty(cols, dtype=f32, device=dev) if bias else None
     if workspace is None:
