@@ -75,12 +75,12 @@ __device__ __forceinline__ float rounded_sum(float a, float b, bool bf16) {
 }
 
 // A row's place in a CTA: L lanes of a warp (several rows a warp), or W whole
-// warps, each with a piece of it.  A lane has up to V units of 16 bytes (32
-// entries).
-template <bool BF16, int L, int W>
+// warps, each with a piece of it.  A lane has up to V units of 16 bytes (N entries).
+template <bool BF16, int L, int W, int N>
 struct Shape {
-  static constexpr int kV = BF16 ? 4 : 8, kE = rows::Unit<BF16>::n;
+  static constexpr int kE = rows::Unit<BF16>::n, kV = N / kE;
   static constexpr int kThreads = W > 8 ? 32 * W : 256, kWarps = kThreads / 32;
+  static constexpr int kResident = kThreads > 256 ? 1 : 2;  // CTAs per SM that registers are kept for
   static constexpr int kGroups = kWarps / W;       // row groups of W warps
   static constexpr int kRows = 32 / L;             // rows of a warp at a time
   static constexpr int kCapacity = L * W * kV * kE;
@@ -162,9 +162,9 @@ __device__ __forceinline__ void weights(const RowParams& P, uint32_t at, const v
 }
 
 // Forward: the row groups of all CTAs take rows in turn.
-template <bool BF16, bool ALIGNED, int L, int W>
-__global__ void __launch_bounds__(Shape<BF16, L, W>::kThreads, W > 8 ? 1 : 2) norm_forward(const __grid_constant__ RowParams P) {
-  using S = Shape<BF16, L, W>;
+template <bool BF16, bool ALIGNED, int L, int W, int N>
+__global__ void __launch_bounds__(Shape<BF16, L, W, N>::kThreads, Shape<BF16, L, W, N>::kResident) norm_forward(const __grid_constant__ RowParams P) {
+  using S = Shape<BF16, L, W, N>;
   constexpr int V = S::kV, E = S::kE, H = E / 2;
   extern __shared__ uint4 dynamic[];
   __shared__ float slots[S::kGroups][2][2][W];  // by parity of the row, use
@@ -316,9 +316,9 @@ __global__ void __launch_bounds__(Shape<BF16, L, W>::kThreads, W > 8 ? 1 : 2) no
 // Backward: as norm_forward.  The two means are taken in one pass over the row
 // in shared memory and the gradient in a second one, so that registers hold the
 // columns' sums; a CTA leaves one row of partial sums.
-template <bool BF16, bool ALIGNED, int L, int W>
-__global__ void __launch_bounds__(Shape<BF16, L, W>::kThreads, W > 8 ? 1 : 2) norm_backward(const __grid_constant__ RowParams P) {
-  using S = Shape<BF16, L, W>;
+template <bool BF16, bool ALIGNED, int L, int W, int N>
+__global__ void __launch_bounds__(Shape<BF16, L, W, N>::kThreads, Shape<BF16, L, W, N>::kResident) norm_backward(const __grid_constant__ RowParams P) {
+  using S = Shape<BF16, L, W, N>;
   constexpr int V = S::kV, E = S::kE, H = E / 2;
   extern __shared__ uint4 dynamic[];
   __shared__ float2 slots[S::kGroups][2][W];
@@ -632,30 +632,41 @@ struct Form {
   int lanes, warps, entries;            // lanes of a warp and warps per row, entries of a unit
 };
 
-template <bool BACKWARD, bool BF16, bool ALIGNED, int L, int W>
+template <bool BACKWARD, bool BF16, bool ALIGNED, int L, int W, int N = 32>
 Form form() {
-  using S = Shape<BF16, L, W>;
+  using S = Shape<BF16, L, W, N>;
   KernelPtr fn;
   if constexpr (BACKWARD)
-    fn = norm_backward<BF16, ALIGNED, L, W>;
+    fn = norm_backward<BF16, ALIGNED, L, W, N>;
   else
-    fn = norm_forward<BF16, ALIGNED, L, W>;
+    fn = norm_forward<BF16, ALIGNED, L, W, N>;
   return {fn, S::kThreads, S::kGroups * S::kRows, S::kCapacity, L, W, S::kE};
 }
 
 // The narrowest form that holds a row: 4 lanes up to 128 entries, doubled up to a
-// warp (1024), then whole warps up to 16 (16384).  Null: none does.  Where rows are
-// few, a form with one unit a lane, for their latency.
+// warp (1024), then whole warps (up to 16384).  Null: none does.  Where rows are
+// few, a form with one unit a lane, for their latency.  Backward, rows of whole warps
+// have 16 entries a lane up to 8192, as the sums of 32 columns leave too few registers
+// beside them (32 and 16 a lane: 20000 x 2048 float32 121 and 92 us, 9000 x 8192
+// bfloat16 121 and 103, 32768 x 1600 113 and 108, 16384 x 4096 110 and 118).  Forward, 32
+// are better throughout (16384 x 4096 68 us, 85 with 16; 64: 104 us in place of 71 for
+// 32768 x 1600, as the code outgrows the instruction cache).
 template <bool BACKWARD, bool BF16, bool ALIGNED>
 const Form* choose(int64_t cols, bool few) {
-  static const Form all[] = {form<BACKWARD, BF16, ALIGNED, 4, 1>(),  form<BACKWARD, BF16, ALIGNED, 8, 1>(),
-                             form<BACKWARD, BF16, ALIGNED, 16, 1>(), form<BACKWARD, BF16, ALIGNED, 32, 1>(),
-                             form<BACKWARD, BF16, ALIGNED, 32, 2>(), form<BACKWARD, BF16, ALIGNED, 32, 4>(),
-                             form<BACKWARD, BF16, ALIGNED, 32, 8>(), form<BACKWARD, BF16, ALIGNED, 32, 16>()};
-  const int64_t want = few ? cols * Shape<BF16, 32, 1>::kV : cols;
+  static const std::vector<Form> all = [] {
+    std::vector<Form> v = {form<BACKWARD, BF16, ALIGNED, 4, 1>(), form<BACKWARD, BF16, ALIGNED, 8, 1>(),
+                           form<BACKWARD, BF16, ALIGNED, 16, 1>(), form<BACKWARD, BF16, ALIGNED, 32, 1>()};
+    if constexpr (BACKWARD)
+      v.insert(v.end(), {form<true, BF16, ALIGNED, 32, 4, 16>(), form<true, BF16, ALIGNED, 32, 8, 16>(), form<true, BF16, ALIGNED, 32, 16, 16>()});
+    else
+      v.insert(v.end(), {form<false, BF16, ALIGNED, 32, 2>(), form<false, BF16, ALIGNED, 32, 4>(), form<false, BF16, ALIGNED, 32, 8>()});
+    v.push_back(form<BACKWARD, BF16, ALIGNED, 32, 16>());
+    return v;
+  }();
+  const int64_t want = few ? cols * Shape<BF16, 32, 1, 32>::kV : cols;
   for (const Form& f : all)
     if (want <= f.capacity) return &f;
-  return cols <= all[7].capacity ? &all[7] : nullptr;
+  return cols <= all.back().capacity ? &all.back() : nullptr;
 }
 
 template <bool BACKWARD>
