@@ -464,8 +464,16 @@ __global__ void __launch_bounds__(kThreads) fp4_amax_kernel(const char* x, long 
       top = max(top, m);
     }
   }
+  // one number a CTA, and no atomic where it is not larger: thousands at one address take longer than
+  // the reads of a small matrix
+  __shared__ uint32_t part[kThreads / 32];
   top = __reduce_max_sync(0xFFFFFFFFu, top);
-  if (lane == 0 && top) atomicMax(out, top);
+  if (lane == 0) part[threadIdx.x >> 5] = top;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    top = __reduce_max_sync(0xFFFFFFFFu, lane < kThreads / 32 ? part[lane] : 0u);
+    if (lane == 0 && top > *static_cast<volatile uint32_t*>(out)) atomicMax(out, top);
+  }
 }
 
 // The numbers that codes stand for: 128 rows x 256 columns a CTA, whose scales are

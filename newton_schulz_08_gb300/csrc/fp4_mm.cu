@@ -83,6 +83,17 @@ __device__ __forceinline__ Factors tensor_factors(const MmParams& P) {
   return {pow2(first), pow2(e - first)};
 }
 
+// The tensors' powers of two, on 32 accumulators.
+__device__ __forceinline__ void scale32(const MmParams& P, const Factors& f, uint32_t (&r)[32]) {
+  if (!P.scale_a) return;
+#pragma unroll
+  for (int k = 0; k < 32; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * f.a);
+  if (f.b != 1.0f) {
+#pragma unroll
+    for (int k = 0; k < 32; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * f.b);
+  }
+}
+
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -96,75 +107,75 @@ constexpr int kGroups = kFp4Depth / (4 * BLOCK);
 // warp's 4 KB of shared memory in whole 128-byte lines: rows row0 .. and
 // columns col0 .. of out.
 __device__ __forceinline__ void store_rows(const MmParams& P, uint32_t stage, int lane, int row0, int col0,
-                                           const uint32_t (&lo)[32], const uint32_t (&hi)[32], const Factors& f) {
-  const int pieces = P.f32 ? 2 : 1;
+                                           uint32_t (&lo)[32], uint32_t (&hi)[32], const Factors& f) {
   const int size = P.f32 ? 4 : 2, width = 128 / size;
-  for (int h = 0; h < pieces; ++h) {
+  scale32(P, f, lo);
+  scale32(P, f, hi);
+  // this lane's 16 bytes of every fourth row
+  const int j = lane & 7, r0 = lane >> 3, left = P.m - row0 - r0;
+  const long long step = 4 * P.stride * size;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int c0 = col0 + h * width;
+    if ((h && !P.f32) || c0 >= P.n) break;
     __syncwarp();
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int k = 0; k < 8; ++k) {
       uint32_t w[4];
-      if (P.f32) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          w[e] = __float_as_uint(__uint_as_float(h ? hi[4 * j + e] : lo[4 * j + e]) * f.a * f.b);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t x = j < 4 ? lo[8 * (j & 3) + 2 * e] : hi[8 * (j & 3) + 2 * e];
-          const uint32_t y = j < 4 ? lo[8 * (j & 3) + 2 * e + 1] : hi[8 * (j & 3) + 2 * e + 1];
-          w[e] = pack_bf16x2(__uint_as_float(x) * f.a * f.b, __uint_as_float(y) * f.a * f.b);
+      for (int e = 0; e < 4; ++e) {
+        if (P.f32) {
+          w[e] = h ? hi[4 * k + e] : lo[4 * k + e];
+        } else {
+          const uint32_t(&half)[32] = k < 4 ? lo : hi;
+          w[e] = pack_bf16x2(__uint_as_float(half[8 * (k & 3) + 2 * e]), __uint_as_float(half[8 * (k & 3) + 2 * e + 1]));
         }
       }
-      ptx::sts128(stage + lane * 128 + ((j ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
+      ptx::sts128(stage + lane * 128 + ((k ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
     }
     __syncwarp();
-    const int c0 = col0 + h * width;
-    if (c0 >= P.n) break;
-    char* out = static_cast<char*>(P.out);
+    char* at = static_cast<char*>(P.out) + ((row0 + r0) * P.stride + c0) * size;
     if (P.vec && c0 + width <= P.n) {
+      at += j * 16;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const int r = 4 * k + (lane >> 3), j = lane & 7;
         uint32_t a, b, c, d;
-        ptx::lds128(stage + r * 128 + ((j ^ (r & 7)) << 4), a, b, c, d);
-        if (row0 + r < P.m && MUON_CHECK(c0 + (j + 1) * 16 / size <= P.n))
-          *reinterpret_cast<uint4*>(out + ((row0 + r) * P.stride + c0) * size + j * 16) = make_uint4(a, b, c, d);
+        ptx::lds128(stage + (4 * k + r0) * 128 + ((j ^ ((4 * k + r0) & 7)) << 4), a, b, c, d);
+        if (4 * k < left && MUON_CHECK(c0 + (j + 1) * 16 / size <= P.n)) *reinterpret_cast<uint4*>(at) = make_uint4(a, b, c, d);
+        at += step;
       }
     } else {
       // rows off the 16-byte boundaries, or ending here: each lane composes an
       // aligned unit of two neighbouring pieces; units with entries of others are stored by the entry
       const int per = 16 / size, have = min(width, P.n - c0);
 #pragma unroll 1
-      for (int k = 0; k < 8; ++k) {
-        const int r = 4 * k + (lane >> 3), j = lane & 7;
+      for (int k = 0; 4 * k < min(left, 32 - r0); ++k, at += step) {
+        const int r = 4 * k + r0;
         auto piece = [&](int p) {
           uint4 q;
           ptx::lds128(stage + r * 128 + ((p ^ (r & 7)) << 4), q.x, q.y, q.z, q.w);
           return q;
         };
-        char* at = out + ((row0 + r) * P.stride + c0) * size;
         const uint32_t shift = rows::shift_of(at);
         const int before = static_cast<int>(shift) / size;
-        if (row0 + r >= P.m) continue;
-        uint4 q = piece(j);
-        const uint4 last = q;
+        const uint4 last = piece(j);
+        uint4 q = last;
         if (shift) q = rows::funnel(piece(j ? j - 1 : 0), q, 16 - shift);
         const int first = j ? 0 : before, room = min(per, have + before - j * per);
-        at += 16 * j - static_cast<int>(shift);
+        char* to = at + 16 * j - static_cast<int>(shift);
         if (first == 0 && room == per)
-          *reinterpret_cast<uint4*>(at) = q;
+          *reinterpret_cast<uint4*>(to) = q;
         else if (P.f32)
-          rows::store_some<false>(at, q, first, room);
+          rows::store_some<false>(to, q, first, room);
         else
-          rows::store_some<true>(at, q, first, room);
+          rows::store_some<true>(to, q, first, room);
         if (j == 7 && shift) {
           q = rows::funnel(last, last, 16 - shift);
-          const int to = min(before, have + before - 8 * per);
+          const int end = min(before, have + before - 8 * per);
           if (P.f32)
-            rows::store_some<false>(at + 16, q, 0, to);
+            rows::store_some<false>(to + 16, q, 0, end);
           else
-            rows::store_some<true>(at + 16, q, 0, to);
+            rows::store_some<true>(to + 16, q, 0, end);
         }
       }
     }
@@ -527,35 +538,44 @@ __global__ void __launch_bounds__(kTileThreads) fp4_tile_kernel(const __grid_con
     const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16);
     const int row = q * 32 + lane;
     if (splits > 1) {
-      const uint32_t to = ptx::map_to_rank(partial + (rank * BN * (slice + 4) + (row & (slice - 1))) * 4, row / slice);
+      uint32_t to = ptx::map_to_rank(partial + (rank * BN * (slice + 4) + (row & (slice - 1))) * 4, row / slice);
 #pragma unroll 1
       for (int c = 0; c < BN; c += 32) {
-        uint32_t r[32];
-        __syncwarp();
-        ptx::tmem_ld32(tb + c, r);
-        ptx::tmem_ld_wait(r);
-#pragma unroll
-        for (int k = 0; k < 32; ++k) ptx::st_cluster_b32(to + (c + k) * (slice + 4) * 4, kb0 < kb1 ? r[k] : 0u);
-      }
-    } else if (P.swapped) {
-      // a lane is a column of out, an accumulator column a row of it
-      const int col = I * 128 + row;
-#pragma unroll 1
-      for (int c = 0; c < BN; c += 32) {
-        if (n0 + c >= P.n) break;
         uint32_t r[32];
         __syncwarp();
         ptx::tmem_ld32(tb + c, r);
         ptx::tmem_ld_wait(r);
 #pragma unroll
         for (int k = 0; k < 32; ++k) {
-          const float v = __uint_as_float(r[k]) * f.a * f.b;
-          const long long at = (n0 + c + k) * P.stride + col;
-          if (col >= P.m || n0 + c + k >= P.n) continue;
-          if (P.f32)
-            static_cast<float*>(P.out)[at] = v;
-          else
-            static_cast<__nv_bfloat16*>(P.out)[at] = __float2bfloat16_rn(v);
+          ptx::st_cluster_b32(to, kb0 < kb1 ? r[k] : 0u);
+          to += (slice + 4) * 4;
+        }
+      }
+    } else if (P.swapped) {
+      // a lane is a column of out, an accumulator column a row of it
+      const int col = I * 128 + row, size = P.f32 ? 4 : 2;
+      char* at = static_cast<char*>(P.out) + (n0 * P.stride + col) * size;
+      const long long step = P.stride * size;
+#pragma unroll 1
+      for (int c = 0; c < BN; c += 32) {
+        const int have = P.n - n0 - c;  // rows of out from here on
+        if (have <= 0) break;
+        uint32_t r[32];
+        __syncwarp();
+        ptx::tmem_ld32(tb + c, r);
+        ptx::tmem_ld_wait(r);
+        scale32(P, f, r);
+        if (col < P.m) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            if (k < have) {
+              if (P.f32)
+                *reinterpret_cast<uint32_t*>(at) = r[k];
+              else
+                *reinterpret_cast<__nv_bfloat16*>(at) = __float2bfloat16_rn(__uint_as_float(r[k]));
+            }
+            at += step;
+          }
         }
       }
     } else {
