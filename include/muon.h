@@ -557,9 +557,12 @@ muon_status_t fp8_mm_backward(const void* g, const void* x_f8, const void* w_f8,
  *           + b % 4, T = ceil(cols / 256) * 64 / block (zeros where there is
  *           no block);
  *   scale   blocks of 16: two floats, the tensor's factor (a power of two) and
- *           the largest finite |x| it comes from; blocks of 32: NULL.
+ *           the largest finite |x| it comes from; where fp4_quantize writes
+ *           them, FP4_SCALE_FLOATS floats, of which it uses the others on the
+ *           way; blocks of 32: NULL.
  * An entry is code * block scale * factor.  codes and scales are 16-byte
  * aligned. */
+#define FP4_SCALE_FLOATS 256
 typedef struct fp4_matrix {
   void* codes;
   void* scales;

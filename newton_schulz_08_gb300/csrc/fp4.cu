@@ -53,8 +53,12 @@ struct QuantParams {
   int vec;            // rows may be read in 16-byte vectors
   int tiles_x;        // CTAs along a row
   Target along, across;
-  float* scale;       // block 16: the tensor's 2^k and max |x|
+  float* scale;       // block 16: the tensor's 2^k, its max |x|, and that of each of the `parts` of fp4_amax_kernel
+  int parts;
 };
+
+constexpr int kMaxParts = FP4_SCALE_FLOATS - 2;
+constexpr int kAmaxThreads = 1024;
 
 constexpr uint32_t kC0 = 0x9E3779B1u, kC1 = 0x6A09E667u, kC2 = 0xBB67AE85u;
 
@@ -280,9 +284,15 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 5 : 3) fp4_quantize_kernel(co
   }
   float up = 1.0f;
   if constexpr (BLOCK == 16) {
-    const int k = tensor_exponent(__float_as_uint(P.scale[1]));
+    uint32_t top = 0;
+    for (int i = tid & 31; i < P.parts; i += 32) top = max(top, __float_as_uint(P.scale[2 + i]));
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    const int k = tensor_exponent(top);
     up = pow2(-k);
-    if (blockIdx.x == 0 && tid == 0) P.scale[0] = pow2(k);
+    if (blockIdx.x == 0 && tid == 0) {
+      P.scale[0] = pow2(k);
+      P.scale[1] = __uint_as_float(top);
+    }
   }
   rows::copies_wait(0);
   __syncwarp();
@@ -419,20 +429,22 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 5 : 3) fp4_quantize_kernel(co
   }
 }
 
-// Largest finite magnitude of a matrix, as the bits of a float, into *out (0
-// before): a warp takes 128 units of 16 bytes of a row.  Units are those of
-// memory; entries beside the row are left out of the first and the last one.
-// Contiguous rows are read as rows of any other length (the last one shorter).
+// Largest finite magnitude of a matrix: each CTA leaves that of its part in
+// out[blockIdx.x] (one atomic maximum would have to be cleared first).  A warp takes 128
+// units of 16 bytes of a row.  Units are those of memory; entries beside the
+// row are left out of the first and the last one.  Contiguous rows are read as rows of any
+// other length (the last one shorter).
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads) fp4_amax_kernel(const char* x, long long stride, int cols, long long total, int pieces,
-                                                            long long items, uint32_t* out) {
+__global__ void __launch_bounds__(kAmaxThreads) fp4_amax_kernel(const char* x, long long stride, int cols, long long total, int pieces,
+                                                            long long items, float* out) {
   constexpr int size = BF16 ? 2 : 4, per = 16 / size;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31;
   uint32_t top = 0;
-  const long long step = static_cast<long long>(gridDim.x) * (kThreads / 32);
-  for (long long item = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); item < items; item += step) {
+  constexpr int kWarps = kAmaxThreads / 32;
+  const long long step = static_cast<long long>(gridDim.x) * kWarps;
+  for (long long item = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5); item < items; item += step) {
     const long long r = items <= 0x7FFFFFFF ? static_cast<long long>(static_cast<uint32_t>(item) / static_cast<uint32_t>(pieces)) : item / pieces;
     const int k0 = static_cast<int>(item - r * pieces) * 128 + lane;
     const char* p = x + r * stride * size;
@@ -464,15 +476,13 @@ __global__ void __launch_bounds__(kThreads) fp4_amax_kernel(const char* x, long 
       top = max(top, m);
     }
   }
-  // one number a CTA, and no atomic where it is not larger: thousands at one address take longer than
-  // the reads of a small matrix
-  __shared__ uint32_t part[kThreads / 32];
+  __shared__ uint32_t part[kWarps];
   top = __reduce_max_sync(0xFFFFFFFFu, top);
   if (lane == 0) part[threadIdx.x >> 5] = top;
   __syncthreads();
   if (threadIdx.x < 32) {
-    top = __reduce_max_sync(0xFFFFFFFFu, lane < kThreads / 32 ? part[lane] : 0u);
-    if (lane == 0 && top > *static_cast<volatile uint32_t*>(out)) atomicMax(out, top);
+    top = __reduce_max_sync(0xFFFFFFFFu, part[lane]);
+    if (lane == 0) out[blockIdx.x] = __uint_as_float(top);
   }
 }
 
@@ -549,13 +559,13 @@ __global__ void __launch_bounds__(kThreads) fp4_values_kernel(const uint8_t* cod
   }
 }
 
-cudaError_t launch(const void* fn, dim3 grid, int smem, void** args, cudaStream_t stream) {
+cudaError_t launch(const void* fn, dim3 grid, int smem, void** args, cudaStream_t stream, int threads = kThreads) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
@@ -681,8 +691,6 @@ extern "C" muon_status_t fp4_quantize(const void* x, int dtype, int64_t rows, in
                           : (bf16 ? tile_smem<true, false>() : tile_smem<false, false>());
   if (!raise_limit(fn, smem)) return MUON_ERR_CUDA;
   if (block == 16) {
-    if (cudaMemsetAsync(P.scale + 1, 0, 4, str) != cudaSuccess) return MUON_ERR_CUDA;
-    uint32_t* bits = reinterpret_cast<uint32_t*>(P.scale + 1);
     const int per = 16 / size;
     const char* p = static_cast<const char*>(x);
     // contiguous rows as rows of 128 units of memory
@@ -692,9 +700,11 @@ extern "C" muon_status_t fp4_quantize(const void* x, int dtype, int64_t rows, in
     int length = static_cast<int>(flat ? run : cols);
     int pieces = static_cast<int>(((length + per - 1LL) / per + (begin && stride % per == 0 ? 0 : 1) + 127) / 128);
     long long items = (flat ? (total + stride - 1) / stride : rows) * pieces;
-    void* args[] = {&p, &stride, &length, &total, &pieces, &items, &bits};
+    float* parts = P.scale + 2;
+    P.parts = static_cast<int>(std::min<int64_t>((items + kAmaxThreads / 32 - 1) / (kAmaxThreads / 32), std::min(sms, kMaxParts)));
+    void* args[] = {&p, &stride, &length, &total, &pieces, &items, &parts};
     if (launch(bf16 ? reinterpret_cast<const void*>(&fp4_amax_kernel<true>) : reinterpret_cast<const void*>(&fp4_amax_kernel<false>),
-               dim3(static_cast<unsigned>(std::min<int64_t>((items + 7) / 8, sms * 8))), 0, args, str) != cudaSuccess)
+               dim3(static_cast<unsigned>(P.parts)), 0, args, str, kAmaxThreads) != cudaSuccess)
       return MUON_ERR_CUDA;
   }
   void* args[] = {&P};

@@ -41,7 +41,7 @@ inline uint64_t fp4_scale_bytes(const fp4_matrix& m) {
 inline void fp4_spans(std::vector<Span>& v, const fp4_matrix& m, bool write) {
   v.push_back(span_of(m.codes, fp4_code_bytes(m), write));
   v.push_back(span_of(m.scales, fp4_scale_bytes(m), write));
-  v.push_back(span_of(m.scale, m.scale ? 8 : 0, write));
+  v.push_back(span_of(m.scale, m.scale ? (write ? FP4_SCALE_FLOATS : 2) * 4 : 0, write));
 }
 
 }  // namespace muon

@@ -1128,7 +1128,7 @@ def fp4_quantize(x, block=32, axis=1, seed=None, stream=None):
         raise ValueError('axis must be 1, 0 or "both"')
     index, kind = _index_of("fp4_quantize", x), _dtype_code(x)
     # one allocation for everything: the tensor's scale, then codes and scales of each operand
-    size = 512 if block == 16 else 0
+    size = 1024 if block == 16 else 0
     for r, c in ((rows, cols), (cols, rows))[axis == 0:1 if axis == 1 else 2]:
         codes, scales = _fp4_bytes(r, c, block)
         size += -(-codes // 512) * 512 + scales
@@ -1136,7 +1136,7 @@ def fp4_quantize(x, block=32, axis=1, seed=None, stream=None):
     at = memory.data_ptr()
     scale, along, across = 0, None, None
     if block == 16:
-        scale, at = at, at + 512
+        scale, at = at, at + 1024
     if axis != 0:
         along, at = _fp4_at(at, rows, cols, block, scale, memory, index)
     if axis != 1:
