@@ -19,6 +19,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <exception>
 #include <mutex>
 #include <new>
 #include <set>
@@ -588,7 +589,7 @@ const void* quantize_fn(int block, bool random, bool along, bool across) {
 }
 
 // Raises a kernel's limit of shared memory at its first use on the current device.
-bool raise_limit(const void* fn, int smem) {
+bool raise_limit(const void* fn, int smem) try {
   static std::mutex mu;
   static std::set<std::pair<int, const void*>> done;
   int dev = 0;
@@ -599,6 +600,8 @@ bool raise_limit(const void* fn, int smem) {
   if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return false;
   done.insert({dev, fn});
   return true;
+} catch (const std::exception&) {  // (none crosses a C entry)
+  return false;
 }
 
 uint64_t matrix_bytes(int64_t rows, int64_t cols, int64_t stride, int size) {

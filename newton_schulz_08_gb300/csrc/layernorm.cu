@@ -18,6 +18,8 @@
 
 #include <algorithm>
 #include <cmath>
+#include <exception>
+#include <iterator>
 #include <map>
 #include <mutex>
 #include <new>
@@ -545,14 +547,15 @@ __global__ void __launch_bounds__(kWide) norm_forward_wide(const __grid_constant
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const float inv = 1.0f / static_cast<float>(P.cols);
   for (long long r = blockIdx.x; r < P.rows; r += gridDim.x) {
-    auto value = [&](int c) {
-      const float x = entry<BF16>(P.x, r * P.sx + c);
-      return P.residual ? rounded_sum(x, entry<BF16>(P.residual, r * P.sr + c), BF16) : x;
-    };
+    // (a thread reads its own sums again, not x, which they may have taken the place of)
+    auto value = [&](int c) { return P.residual ? entry<BF16>(P.sum, r * P.ssum + c) : entry<BF16>(P.x, r * P.sx + c); };
     float s = 0.0f;
     for (int c = threadIdx.x; c < P.cols; c += kWide) {
-      const float x = value(c);
-      if (P.residual) put<BF16>(P.sum, r * P.ssum + c, x);
+      float x = entry<BF16>(P.x, r * P.sx + c);
+      if (P.residual) {
+        x = rounded_sum(x, entry<BF16>(P.residual, r * P.sr + c), BF16);
+        put<BF16>(P.sum, r * P.ssum + c, x);
+      }
       s += x;
     }
     const float mean = block_sum(s, slots) * inv;
@@ -653,20 +656,17 @@ Form form() {
 // 32768 x 1600, as the code outgrows the instruction cache).
 template <bool BACKWARD, bool BF16, bool ALIGNED>
 const Form* choose(int64_t cols, bool few) {
-  static const std::vector<Form> all = [] {
-    std::vector<Form> v = {form<BACKWARD, BF16, ALIGNED, 4, 1>(), form<BACKWARD, BF16, ALIGNED, 8, 1>(),
-                           form<BACKWARD, BF16, ALIGNED, 16, 1>(), form<BACKWARD, BF16, ALIGNED, 32, 1>()};
-    if constexpr (BACKWARD)
-      v.insert(v.end(), {form<true, BF16, ALIGNED, 32, 4, 16>(), form<true, BF16, ALIGNED, 32, 8, 16>(), form<true, BF16, ALIGNED, 32, 16, 16>()});
-    else
-      v.insert(v.end(), {form<false, BF16, ALIGNED, 32, 2>(), form<false, BF16, ALIGNED, 32, 4>(), form<false, BF16, ALIGNED, 32, 8>()});
-    v.push_back(form<BACKWARD, BF16, ALIGNED, 32, 16>());
-    return v;
-  }();
+  static const Form all[] = {form<BACKWARD, BF16, ALIGNED, 4, 1>(), form<BACKWARD, BF16, ALIGNED, 8, 1>(),
+                             form<BACKWARD, BF16, ALIGNED, 16, 1>(), form<BACKWARD, BF16, ALIGNED, 32, 1>(),
+                             form<BACKWARD, BF16, ALIGNED, 32, BACKWARD ? 4 : 2, BACKWARD ? 16 : 32>(),
+                             form<BACKWARD, BF16, ALIGNED, 32, BACKWARD ? 8 : 4, BACKWARD ? 16 : 32>(),
+                             form<BACKWARD, BF16, ALIGNED, 32, BACKWARD ? 16 : 8, BACKWARD ? 16 : 32>(),
+                             form<BACKWARD, BF16, ALIGNED, 32, 16>()};
+  const Form& last = all[std::size(all) - 1];
   const int64_t want = few ? cols * Shape<BF16, 32, 1, 32>::kV : cols;
   for (const Form& f : all)
     if (want <= f.capacity) return &f;
-  return cols <= all.back().capacity ? &all.back() : nullptr;
+  return cols <= last.capacity ? &last : nullptr;
 }
 
 template <bool BACKWARD>
@@ -677,7 +677,7 @@ const Form* choose(bool bf16, bool aligned, int64_t cols, bool few) {
 
 // CTAs of a kernel that an SM holds with so much shared memory; the first
 // query on a device raises the kernel's limit there.  0: an error.
-int resident(const Form& f, int smem) {
+int resident(const Form& f, int smem) try {
   static std::mutex mu;
   static std::map<std::tuple<int, KernelPtr, int>, int> known;
   int dev = 0;
@@ -693,6 +693,8 @@ int resident(const Form& f, int smem) {
     n = std::max(q, 1);
   }
   return n;
+} catch (const std::exception&) {  // (none crosses a C entry)
+  return 0;
 }
 
 // How a CTA's shared memory is used for rows of `cols` entries: `arrays` of them

@@ -238,3 +238,19 @@ def test_differences():
         e = torch.zeros_like(w)
         e[j] = h
         assert abs((f(x, w + e) - f(x, w - e)) / (2 * h) - float(gw[j])) < 3e-3
+
+
+@pytest.mark.parametrize("cols", [100, 1600, 1601, 20001])
+@pytest.mark.parametrize("kind", [B, F])
+@pytest.mark.parametrize("into", ["x", "residual"])
+def test_sum_in_place(into, kind, cols):
+    """The sum may take the place of x or of residual."""
+    x, res, w = make(30, cols, kind), make(30, cols, kind, seed=1), make(1, cols, F, seed=2)[0]
+    want = muon.layer_norm(x, w, residual=res)
+    y, mean, rstd = torch.empty_like(x), torch.empty(30, device="cuda"), torch.empty(30, device="cuda")
+    total = x if into == "x" else res
+    muon._call(muon.lib().layer_norm, "layer_norm", 0, None, x.data_ptr(), muon._dtype_code(x), 30, cols, cols, res.data_ptr(),
+               cols, w.data_ptr(), None, muon.MUON_F32, 1e-5, y.data_ptr(), cols, total.data_ptr(), cols, mean.data_ptr(),
+               rstd.data_ptr())
+    for a, b in ((total, want.sum), (y, want.y), (mean, want.mean), (rstd, want.rstd)):
+        assert torch.equal(a, b)
