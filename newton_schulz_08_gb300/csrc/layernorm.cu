@@ -53,7 +53,9 @@ struct RowParams {
   long long rows;
   int cols, parts;
   int weight_f32;
-  int units_lane;         // 16-byte units of a row that a lane has
+  int weight_vec;         // weight and bias begin on 16 bytes
+  int units_lane;         // 16-byte units of a row that a lane has (norm_forward_long: of a row)
+  int warps;              // norm_forward_long: of a row
   int stages;             // 2: a row is copied while the one before it is worked on
   int weights_shared;     // weight (and bias) are held in shared memory
   float eps;
@@ -155,6 +157,22 @@ __device__ __forceinline__ void weights(const RowParams& P, uint32_t at, const v
       const uint4 q = rows::shared_load(at + (p * units + unit) * 16);
       x[2 * p] = rows::pair(__uint_as_float(q.x), __uint_as_float(q.y));
       x[2 * p + 1] = rows::pair(__uint_as_float(q.z), __uint_as_float(q.w));
+    }
+  } else if (w && P.weight_vec && (unit + 1) * E <= P.cols) {
+    if (P.weight_f32) {
+#pragma unroll
+      for (int p = 0; p < E / 4; ++p) {
+        const float4 q = __ldg(static_cast<const float4*>(w) + unit * (E / 4) + p);
+        x[2 * p] = rows::pair(q.x, q.y);
+        x[2 * p + 1] = rows::pair(q.z, q.w);
+      }
+    } else {
+#pragma unroll
+      for (int p = 0; p < E / 4; ++p) {
+        const uint2 q = __ldg(static_cast<const uint2*>(w) + unit * (E / 4) + p);
+        x[2 * p] = rows::pair(__uint_as_float(q.x << 16), __uint_as_float(q.x & 0xFFFF0000u));
+        x[2 * p + 1] = rows::pair(__uint_as_float(q.y << 16), __uint_as_float(q.y & 0xFFFF0000u));
+      }
     }
   } else {
     auto at_column = [&](int c) { return w && c < P.cols ? weight_at(w, P.weight_f32, c) : none; };
@@ -313,6 +331,177 @@ __global__ void __launch_bounds__(Shape<BF16, L, W, N>::kThreads, Shape<BF16, L,
     ps += step * P.ssum * (16 / E);
   }
   rows::copies_wait(0);
+}
+
+// Forward for long rows, and for rows off 16 bytes in the same way in all arrays
+// (COMMON).  A row stays in shared memory for three passes: W warps a row, one
+// row at a time each, and as many rows a CTA as fit, whose copies and barriers
+// hide behind one another (two slots a row and half the rows: 3001 x 12289
+// bfloat16 66 us, 58 so).  Units are those of memory: nothing moves between
+// lanes, a thread reads what it has copied, and entries beside the row are left
+// out of its first and last unit.  Where rows begin off 16 bytes, weights lie by their
+// entry of a unit, which turns with the row: lanes read neighbouring words at any offset.
+template <bool BF16, bool COMMON>
+__global__ void __launch_bounds__(1024) norm_forward_long(const __grid_constant__ RowParams P) {
+  constexpr int E = rows::Unit<BF16>::n, H = E / 2, kSize = 16 / E;
+  extern __shared__ uint4 dynamic[];
+  __shared__ float slots[2][2][32];  // by parity of the row, use
+  const int W = P.warps, T = 32 * W, group = static_cast<int>(threadIdx.x) / T, t = static_cast<int>(threadIdx.x) - group * T;
+  const int units = P.units_lane;  // of a row
+  uint32_t at = rows::shared_address(dynamic);
+  const int pitch = COMMON ? (units + 31) / 32 * 32 + 4 : units;
+  const uint32_t wa = at, ba = at + E * pitch * 4;
+  if (P.weights_shared) at += 2 * E * pitch * 4;
+  const uint32_t array_bytes = units * 16, slot = at + group * (P.residual ? 2 : 1) * array_bytes;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const float inv = 1.0f / static_cast<float>(P.cols);
+  const long long step = static_cast<long long>(gridDim.x) * (blockDim.x / T);
+  long long r = static_cast<long long>(blockIdx.x) * (blockDim.x / T) + group;
+  const int row_bytes = P.cols * kSize;
+  auto copy = [&](uint32_t to, const void* base, long long p) {
+    const char* from = row_of<BF16>(base, r, p, 0);
+    const int shift = COMMON ? static_cast<int>(rows::shift_of(from)) : 0, bytes = row_bytes + shift;
+    from -= shift;
+#pragma unroll 4
+    for (int k = 16 * t; k < bytes; k += 16 * T) rows::copy_ahead(to + k, from + k, min(bytes - k, 16));
+  };
+  auto fetch = [&] {
+    if (r < P.rows && MUON_CHECK(r >= 0)) {
+      copy(slot, P.x, P.sx);
+      if (P.residual) copy(slot + array_bytes, P.residual, P.sr);
+    }
+    rows::copies_commit();
+  };
+  fetch();
+  if (P.weights_shared) {
+    if constexpr (COMMON) {
+      for (int i = threadIdx.x; i < units * E; i += blockDim.x) {
+        const uint32_t to = ((i % E) * pitch + i / E) * 4;
+        const float w = P.weight && i < P.cols ? weight_at(P.weight, P.weight_f32, i) : 1.0f;
+        const float b = P.bias && i < P.cols ? weight_at(P.bias, P.weight_f32, i) : 0.0f;
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(wa + to), "f"(w) : "memory");
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(ba + to), "f"(b) : "memory");
+      }
+    } else {
+      stage_weights<BF16>(wa, P.weight, P.weight_f32, 1.0f, P.cols, units, blockDim.x);
+      stage_weights<BF16>(ba, P.bias, P.weight_f32, 0.0f, P.cols, units, blockDim.x);
+    }
+    __syncthreads();
+  }
+  auto sum_of_row = [&](float v, float* slot) {
+    v = warp_sum(v);
+    if (W > 1) {
+      slot += group * W;
+      if ((t & 31) == 0) slot[t >> 5] = v;
+      asm volatile("bar.sync %0, %1;" ::"r"(group), "r"(T) : "memory");
+      v = 0.0f;
+#pragma unroll 4
+      for (int w = 0; w < W; ++w) v += slot[w];
+    }
+    return v;
+  };
+  for (int it = 0; r < P.rows; ++it) {
+    rows::copies_wait(0);
+    char* y = row_of<BF16>(P.y, r, P.sy, 0);
+    const int shift = COMMON ? static_cast<int>(rows::shift_of(y)) : 0, before = shift / kSize;
+    y -= shift;
+    const int n = before + P.cols, last = (n - 1) / E;  // entries up to the row's end; its last unit
+    // entries [from, to) of unit k are the row's
+    auto first = [&](int k) { return COMMON && k == 0 ? before : 0; };
+    auto end = [&](int k) { return min(n - k * E, E); };
+    auto edge = [&](int k) { return k == last || (COMMON && k == 0); };
+    auto only = [&](Pair (&x)[H], int k) {
+#pragma unroll
+      for (int i = 0; i < H; ++i) {
+        float a, b;
+        rows::split(x[i], a, b);
+        x[i] = rows::pair(2 * i >= first(k) && 2 * i < end(k) ? a : 0.0f, 2 * i + 1 >= first(k) && 2 * i + 1 < end(k) ? b : 0.0f);
+      }
+    };
+    auto store = [&](char* p, int k, const uint4& q) {
+      if (!edge(k) || (first(k) == 0 && end(k) == E))
+        *reinterpret_cast<uint4*>(p + 16 * k) = q;
+      else
+        rows::store_some<BF16>(p + 16 * k, q, first(k), end(k));
+    };
+    Pair s = rows::pair(0.0f);
+#pragma unroll 2
+    for (int k = t; k <= last; k += T) {
+      Pair x[H];
+      rows::numbers<BF16>(rows::shared_load(slot + 16 * k), x);
+      if (P.residual) {
+        Pair a[H];
+        rows::numbers<BF16>(rows::shared_load(slot + array_bytes + 16 * k), a);
+#pragma unroll
+        for (int i = 0; i < H; ++i) x[i] = rows::add(x[i], a[i]);
+        const uint4 q = rows::pack<BF16>(x);
+        rows::shared_store(slot + 16 * k, q);
+        store(row_of<BF16>(P.sum, r, P.ssum, 0) - shift, k, q);
+        rows::numbers<BF16>(q, x);
+      }
+      if (COMMON && k == 0) only(x, k);
+#pragma unroll
+      for (int i = 0; i < H; ++i) s = rows::add(s, x[i]);
+    }
+    const float mean = sum_of_row(rows::total(s), slots[it & 1][0]) * inv;
+    const Pair minus = rows::pair(-mean);
+    s = rows::pair(0.0f);
+#pragma unroll 2
+    for (int k = t; k <= last; k += T) {
+      Pair x[H];
+      rows::numbers<BF16>(rows::shared_load(slot + 16 * k), x);
+#pragma unroll
+      for (int i = 0; i < H; ++i) x[i] = rows::add(x[i], minus);
+      if (edge(k)) only(x, k);
+#pragma unroll
+      for (int i = 0; i < H; ++i) s = rows::fma(x[i], x[i], s);
+    }
+    const float var = sum_of_row(rows::total(s), slots[it & 1][1]) * inv;
+    const float rstd = 1.0f / sqrtf(var + P.eps);
+    if (t == 0) {
+      P.mean[r] = mean;
+      P.rstd[r] = rstd;
+    }
+    const Pair scale = rows::pair(rstd);
+#pragma unroll 2
+    for (int k = t; k <= last; k += T) {
+      Pair x[H], w[H], b[H];
+      rows::numbers<BF16>(rows::shared_load(slot + 16 * k), x);
+      if constexpr (COMMON) {
+        if (P.weights_shared) {
+          // entry e of the unit is entry e - before of the row's own unit k, or of the one in front of it
+          float v[2][E];
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const uint32_t from = (((e - before) & (E - 1)) * pitch + k - (e < before)) * 4;
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[0][e]) : "r"(wa + from) : "memory");
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[1][e]) : "r"(ba + from) : "memory");
+          }
+#pragma unroll
+          for (int i = 0; i < H; ++i) w[i] = rows::pair(v[0][2 * i], v[0][2 * i + 1]), b[i] = rows::pair(v[1][2 * i], v[1][2 * i + 1]);
+        } else {
+          auto at_column = [&](const void* p, float none, int e) {
+            const int c = k * E + e - before;
+            return p && c >= 0 && c < P.cols ? weight_at(p, P.weight_f32, c) : none;
+          };
+#pragma unroll
+          for (int i = 0; i < H; ++i) {
+            w[i] = rows::pair(at_column(P.weight, 1.0f, 2 * i), at_column(P.weight, 1.0f, 2 * i + 1));
+            b[i] = rows::pair(at_column(P.bias, 0.0f, 2 * i), at_column(P.bias, 0.0f, 2 * i + 1));
+          }
+        }
+      } else {
+        weights<BF16>(P, wa, P.weight, 1.0f, k, units, w);
+        weights<BF16>(P, ba, P.bias, 0.0f, k, units, b);
+      }
+#pragma unroll
+      for (int i = 0; i < H; ++i) x[i] = rows::fma(rows::mul(rows::add(x[i], minus), scale), w[i], b[i]);
+      store(y, k, rows::pack<BF16>(x));
+    }
+    r += step;
+    fetch();
+  }
 }
 
 // Backward: as norm_forward.  The two means are taken in one pass over the row
@@ -711,6 +900,30 @@ int layout(RowParams& P, const Form& f, int arrays, int vectors) {
   return P.stages * stage + (P.weights_shared ? held : 0);
 }
 
+struct Long {
+  int threads, groups, smem;
+};
+
+// How norm_forward_long takes rows of P.cols entries (`per` a unit).  False: a row does not fit.
+// Weights are held where three rows fit beside them (6000 x 12800 bfloat16 93 us,
+// 100 read from L2; with a residual, two rows beside them: 161 and 134), or their
+// loads would be by the entry (COMMON).  Warps: 32 a CTA, with five units a lane or more (10000 x 4099 with a
+// residual 79 us with 2 warps a row, 95 with 4), but more of them where rows are few.
+bool long_shape(RowParams& P, int arrays, bool common, int per, int64_t rows, int sms, Long& shape) {
+  P.units_lane = static_cast<int>((P.cols + static_cast<int64_t>(common ? per - 1 : 0) + per - 1) / per);
+  const int64_t row = static_cast<int64_t>(arrays) * P.units_lane * 16;
+  const int64_t held = 2LL * per * (common ? (P.units_lane + 31) / 32 * 32 + 4 : P.units_lane) * 4;
+  if (row > kSmemLimit) return false;
+  P.weights_shared = held + (common ? 1 : 3) * row <= kSmemLimit;
+  const int64_t room = kSmemLimit - (P.weights_shared ? held : 0), fit = std::min<int64_t>(room / row, 32);
+  P.warps = 1;
+  while (P.warps * fit < 32 && 2 * P.warps * 160 <= P.units_lane) P.warps *= 2;
+  while (P.warps < 32 && 2 * P.warps * rows <= 32 * sms && 2 * P.warps * 8 <= P.units_lane) P.warps *= 2;
+  const int groups = static_cast<int>(std::min<int64_t>({32 / P.warps, fit, rows}));
+  shape = {32 * P.warps * groups, groups, static_cast<int>((P.weights_shared ? held : 0) + groups * row)};
+  return true;
+}
+
 constexpr int kMaxParts = 608;  // rows of partial sums: four CTAs per SM at most
 constexpr int kWideParts = 64;
 
@@ -794,13 +1007,30 @@ extern "C" muon_status_t layer_norm(const void* x, int dtype, int64_t rows, int6
   P.cols = static_cast<int>(cols);
   P.weight_f32 = weight_dtype == MUON_F32;
   P.eps = eps;
+  P.weight_vec = aligned_to(weight, 16) && aligned_to(bias, 16);
   auto rows_aligned = [&](const void* p, int64_t stride) { return !p || (aligned_to(p, 16) && stride * size % 16 == 0); };
   const bool vec = rows_aligned(x, row_stride) && rows_aligned(residual, residual_stride) && rows_aligned(y, y_stride) &&
                    rows_aligned(sum, sum_stride);
   cudaStream_t str = static_cast<cudaStream_t>(stream);
   const bool bf16 = dtype == MUON_BF16;
   cudaError_t e;
-  if (const Form* f = choose<false>(bf16, vec, cols, rows <= 2 * sms)) {
+  const uint32_t low = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(x)) & 15;
+  auto alike = [&](const void* p, int64_t stride) {
+    return !p || ((static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15) == low && (stride - row_stride) * size % 16 == 0);
+  };
+  const bool common = !vec && alike(residual, residual_stride) && alike(y, y_stride) && alike(sum, sum_stride);
+  // Long rows, and rows that begin off 16 bytes alike, if they are not short: 40000 x 1601 bfloat16 with a residual
+  // 157 us in the registers, 115 so; 30000 x 515 float32 48 and 39; 100000 x 255 bfloat16 66 and 134.
+  Long shape{};
+  if ((common ? cols * size >= 1536 : vec && cols > 8192) && long_shape(P, residual ? 2 : 1, common, 16 / size, rows, sms, shape)) {
+    const KernelPtr fn = bf16 ? (common ? norm_forward_long<true, true> : norm_forward_long<true, false>)
+                              : (common ? norm_forward_long<false, true> : norm_forward_long<false, false>);
+    const Form f{fn, shape.threads, shape.groups, 0, 32, P.warps, 16 / size};
+    const int per_sm = resident(f, shape.smem);
+    if (per_sm == 0) return MUON_ERR_CUDA;
+    const int64_t ctas = std::min<int64_t>((rows + shape.groups - 1) / shape.groups, static_cast<int64_t>(sms) * per_sm);
+    e = launch(reinterpret_cast<const void*>(fn), dim3(static_cast<unsigned>(ctas)), shape.threads, shape.smem, P, str);
+  } else if (const Form* f = choose<false>(bf16, vec, cols, rows <= 2 * sms)) {
     const int smem = layout(P, *f, residual ? 2 : 1, 2), per_sm = resident(*f, smem);
     if (per_sm == 0) return MUON_ERR_CUDA;
     const int64_t ctas = std::min<int64_t>((rows + f->rows_per_cta - 1) / f->rows_per_cta, static_cast<int64_t>(sms) * per_sm);
@@ -880,6 +1110,7 @@ extern "C" muon_status_t layer_norm_backward(const void* grad, int64_t grad_stri
   P.rows = rows;
   P.cols = static_cast<int>(cols);
   P.weight_f32 = weight_dtype == MUON_F32;
+  P.weight_vec = aligned_to(weight, 16);
   P.grad_weight = grad_weight, P.grad_bias = grad_bias;
   P.partial = columns ? static_cast<float*>(workspace) : nullptr;
   const bool bf16 = dtype == MUON_BF16;
