@@ -136,20 +136,23 @@ __device__ __forceinline__ char* row_of(const void* base, long long r, long long
 }
 
 // Weights in shared memory, float32: four-entry parts of a unit apart, so that a
-// warp reads whole lines.  `units` of a row.
+// warp reads whole lines.  `units` of a row, of whose first one `before` entries are in front of it.
 template <bool BF16>
-__device__ __forceinline__ void stage_weights(uint32_t at, const void* w, int f32, float none, int cols, int units, int threads) {
+__device__ __forceinline__ void stage_weights(uint32_t at, const void* w, int f32, float none, int cols, int units, int thread,
+                                              int threads, int before = 0) {
   constexpr int E = rows::Unit<BF16>::n;
-  for (int i = threadIdx.x; i < units * E; i += threads) {
+  for (int i = thread; i < units * E; i += threads) {
     const int u = i / E, e = i - u * E;
-    const float v = w && i < cols ? weight_at(w, f32, i) : none;
+    const float v = w && i >= before && i - before < cols ? weight_at(w, f32, i - before) : none;
     asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + ((e >> 2) * units + u) * 16 + (e & 3) * 4), "f"(v) : "memory");
   }
 }
 
-template <bool BF16>
+// VECTORS: not held ones may be read by the vector (norm_forward_long; beside the other kernels' unrolled loops the code
+// for it costs more than it gives: gradients of 9000 x 8192 103 us, 152 with it).
+template <bool BF16, bool VECTORS = false, bool COMMON = false>
 __device__ __forceinline__ void weights(const RowParams& P, uint32_t at, const void* w, float none, int unit, int units,
-                                        Pair (&x)[rows::Unit<BF16>::n / 2]) {
+                                        Pair (&x)[rows::Unit<BF16>::n / 2], int before = 0) {
   constexpr int E = rows::Unit<BF16>::n;
   if (P.weights_shared) {
 #pragma unroll
@@ -158,7 +161,7 @@ __device__ __forceinline__ void weights(const RowParams& P, uint32_t at, const v
       x[2 * p] = rows::pair(__uint_as_float(q.x), __uint_as_float(q.y));
       x[2 * p + 1] = rows::pair(__uint_as_float(q.z), __uint_as_float(q.w));
     }
-  } else if (w && P.weight_vec && (unit + 1) * E <= P.cols) {
+  } else if (VECTORS && w && P.weight_vec && (unit + 1) * E <= P.cols) {
     if (P.weight_f32) {
 #pragma unroll
       for (int p = 0; p < E / 4; ++p) {
@@ -175,11 +178,50 @@ __device__ __forceinline__ void weights(const RowParams& P, uint32_t at, const v
       }
     }
   } else {
-    auto at_column = [&](int c) { return w && c < P.cols ? weight_at(w, P.weight_f32, c) : none; };
+    auto at_column = [&](int c) { return w && (!COMMON || c >= 0) && c < P.cols ? weight_at(w, P.weight_f32, c) : none; };
+    const int c0 = unit * E - (COMMON ? before : 0);
 #pragma unroll
-    for (int i = 0; i < E / 2; ++i) x[i] = rows::pair(at_column(unit * E + 2 * i), at_column(unit * E + 2 * i + 1));
+    for (int i = 0; i < E / 2; ++i) x[i] = rows::pair(at_column(c0 + 2 * i), at_column(c0 + 2 * i + 1));
   }
 }
+
+// Where rows begin off 16 bytes alike, weights lie by their entry of a unit,
+// which turns with the row's offset: lanes read neighbouring words at any offset.
+__host__ __device__ constexpr int turned_pitch(int units) { return (units + 31) / 32 * 32 + 4; }
+
+template <bool BF16>
+__device__ __forceinline__ void stage_turned(uint32_t at, const void* w, int f32, float none, int cols, int units, int threads) {
+  constexpr int E = rows::Unit<BF16>::n;
+  const int pitch = turned_pitch(units);
+  for (int i = threadIdx.x; i < units * E; i += threads) {
+    const float v = w && i < cols ? weight_at(w, f32, i) : none;
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + ((i % E) * pitch + i / E) * 4), "f"(v) : "memory");
+  }
+}
+
+// Weights of a unit of memory, whose first `before` entries belong to the
+// unit in front (any number where that is not the row's).
+template <bool BF16>
+__device__ __forceinline__ void turned_weights(const RowParams& P, uint32_t at, const void* w, float none, int unit, int pitch,
+                                               int before, Pair (&x)[rows::Unit<BF16>::n / 2]) {
+  constexpr int E = rows::Unit<BF16>::n;
+  float v[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    if (P.weights_shared) {
+      const uint32_t from = (((e - before) & (E - 1)) * pitch + unit - (e < before)) * 4;
+      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[e]) : "r"(at + from) : "memory");
+    } else {
+      const int c = unit * E + e - before;
+      v[e] = w && c >= 0 && c < P.cols ? weight_at(w, P.weight_f32, c) : none;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) x[i] = rows::pair(v[2 * i], v[2 * i + 1]);
+}
+
+// Where rows begin: anywhere, on 16 bytes, or off them at the same offset in all arrays.
+enum Begin : int { kAny, kAligned, kAlike };
 
 // Forward: the row groups of all CTAs take rows in turn.
 template <bool BF16, bool ALIGNED, int L, int W, int N>
@@ -226,8 +268,8 @@ __global__ void __launch_bounds__(Shape<BF16, L, W, N>::kThreads, Shape<BF16, L,
   const bool ahead = P.stages == 2;
   if (ahead) fetch(0);
   if (P.weights_shared) {
-    stage_weights<BF16>(wa, P.weight, P.weight_f32, 1.0f, P.cols, units, S::kThreads);
-    stage_weights<BF16>(ba, P.bias, P.weight_f32, 0.0f, P.cols, units, S::kThreads);
+    stage_weights<BF16>(wa, P.weight, P.weight_f32, 1.0f, P.cols, units, threadIdx.x, S::kThreads);
+    stage_weights<BF16>(ba, P.bias, P.weight_f32, 0.0f, P.cols, units, threadIdx.x, S::kThreads);
     __syncthreads();
   }
   for (int it = 0; r0 < P.rows; r0 += step, ++it) {
@@ -339,8 +381,7 @@ __global__ void __launch_bounds__(Shape<BF16, L, W, N>::kThreads, Shape<BF16, L,
 // hide behind one another (two slots a row and half the rows: 3001 x 12289
 // bfloat16 66 us, 58 so).  Units are those of memory: nothing moves between
 // lanes, a thread reads what it has copied, and entries beside the row are left
-// out of its first and last unit.  Where rows begin off 16 bytes, weights lie by their
-// entry of a unit, which turns with the row: lanes read neighbouring words at any offset.
+// out of its first and last unit.
 template <bool BF16, bool COMMON>
 __global__ void __launch_bounds__(1024) norm_forward_long(const __grid_constant__ RowParams P) {
   constexpr int E = rows::Unit<BF16>::n, H = E / 2, kSize = 16 / E;
@@ -349,7 +390,7 @@ __global__ void __launch_bounds__(1024) norm_forward_long(const __grid_constant_
   const int W = P.warps, T = 32 * W, group = static_cast<int>(threadIdx.x) / T, t = static_cast<int>(threadIdx.x) - group * T;
   const int units = P.units_lane;  // of a row
   uint32_t at = rows::shared_address(dynamic);
-  const int pitch = COMMON ? (units + 31) / 32 * 32 + 4 : units;
+  const int pitch = COMMON ? turned_pitch(units) : units;
   const uint32_t wa = at, ba = at + E * pitch * 4;
   if (P.weights_shared) at += 2 * E * pitch * 4;
   const uint32_t array_bytes = units * 16, slot = at + group * (P.residual ? 2 : 1) * array_bytes;
@@ -376,16 +417,11 @@ __global__ void __launch_bounds__(1024) norm_forward_long(const __grid_constant_
   fetch();
   if (P.weights_shared) {
     if constexpr (COMMON) {
-      for (int i = threadIdx.x; i < units * E; i += blockDim.x) {
-        const uint32_t to = ((i % E) * pitch + i / E) * 4;
-        const float w = P.weight && i < P.cols ? weight_at(P.weight, P.weight_f32, i) : 1.0f;
-        const float b = P.bias && i < P.cols ? weight_at(P.bias, P.weight_f32, i) : 0.0f;
-        asm volatile("st.shared.f32 [%0], %1;" ::"r"(wa + to), "f"(w) : "memory");
-        asm volatile("st.shared.f32 [%0], %1;" ::"r"(ba + to), "f"(b) : "memory");
-      }
+      stage_turned<BF16>(wa, P.weight, P.weight_f32, 1.0f, P.cols, units, blockDim.x);
+      stage_turned<BF16>(ba, P.bias, P.weight_f32, 0.0f, P.cols, units, blockDim.x);
     } else {
-      stage_weights<BF16>(wa, P.weight, P.weight_f32, 1.0f, P.cols, units, blockDim.x);
-      stage_weights<BF16>(ba, P.bias, P.weight_f32, 0.0f, P.cols, units, blockDim.x);
+      stage_weights<BF16>(wa, P.weight, P.weight_f32, 1.0f, P.cols, units, threadIdx.x, blockDim.x);
+      stage_weights<BF16>(ba, P.bias, P.weight_f32, 0.0f, P.cols, units, threadIdx.x, blockDim.x);
     }
     __syncthreads();
   }
@@ -469,31 +505,11 @@ __global__ void __launch_bounds__(1024) norm_forward_long(const __grid_constant_
       Pair x[H], w[H], b[H];
       rows::numbers<BF16>(rows::shared_load(slot + 16 * k), x);
       if constexpr (COMMON) {
-        if (P.weights_shared) {
-          // entry e of the unit is entry e - before of the row's own unit k, or of the one in front of it
-          float v[2][E];
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const uint32_t from = (((e - before) & (E - 1)) * pitch + k - (e < before)) * 4;
-            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[0][e]) : "r"(wa + from) : "memory");
-            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[1][e]) : "r"(ba + from) : "memory");
-          }
-#pragma unroll
-          for (int i = 0; i < H; ++i) w[i] = rows::pair(v[0][2 * i], v[0][2 * i + 1]), b[i] = rows::pair(v[1][2 * i], v[1][2 * i + 1]);
-        } else {
-          auto at_column = [&](const void* p, float none, int e) {
-            const int c = k * E + e - before;
-            return p && c >= 0 && c < P.cols ? weight_at(p, P.weight_f32, c) : none;
-          };
-#pragma unroll
-          for (int i = 0; i < H; ++i) {
-            w[i] = rows::pair(at_column(P.weight, 1.0f, 2 * i), at_column(P.weight, 1.0f, 2 * i + 1));
-            b[i] = rows::pair(at_column(P.bias, 0.0f, 2 * i), at_column(P.bias, 0.0f, 2 * i + 1));
-          }
-        }
+        turned_weights<BF16>(P, wa, P.weight, 1.0f, k, pitch, before, w);
+        turned_weights<BF16>(P, ba, P.bias, 0.0f, k, pitch, before, b);
       } else {
-        weights<BF16>(P, wa, P.weight, 1.0f, k, units, w);
-        weights<BF16>(P, ba, P.bias, 0.0f, k, units, b);
+        weights<BF16, true>(P, wa, P.weight, 1.0f, k, units, w);
+        weights<BF16, true>(P, ba, P.bias, 0.0f, k, units, b);
       }
 #pragma unroll
       for (int i = 0; i < H; ++i) x[i] = rows::fma(rows::mul(rows::add(x[i], minus), scale), w[i], b[i]);
@@ -507,29 +523,35 @@ __global__ void __launch_bounds__(1024) norm_forward_long(const __grid_constant_
 // Backward: as norm_forward.  The two means are taken in one pass over the row
 // in shared memory and the gradient in a second one, so that registers hold the
 // columns' sums; a CTA leaves one row of partial sums.
-template <bool BF16, bool ALIGNED, int L, int W, int N>
+template <bool BF16, int ROWS, int L, int W, int N>
 __global__ void __launch_bounds__(Shape<BF16, L, W, N>::kThreads, Shape<BF16, L, W, N>::kResident) norm_backward(const __grid_constant__ RowParams P) {
   using S = Shape<BF16, L, W, N>;
   constexpr int V = S::kV, E = S::kE, H = E / 2;
+  constexpr bool COMMON = ROWS == kAlike, ALIGNED = ROWS != kAny;  // (alike: units of memory, as if aligned)
+  static_assert(!COMMON || L == 32, "the rows of a warp begin at one offset");
   extern __shared__ uint4 dynamic[];
   __shared__ float2 slots[S::kGroups][2][W];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int group = warp / W, warp_in = warp % W, sub = lane % L;
   const int units = P.units_lane * L * W;
-  const int unit0 = warp_in * P.units_lane * L, c0 = unit0 * E;
+  const long long step = static_cast<long long>(gridDim.x) * S::kGroups * S::kRows;
+  const long long r0_first = (static_cast<long long>(blockIdx.x) * S::kGroups + group) * S::kRows;
+  // entries that the row's first unit holds of others: the same in every row of this group
+  const int before = COMMON ? static_cast<int>(rows::shift_of(row_of<BF16>(P.x, r0_first, P.sx, 0))) / (16 / E) : 0;
+  const int unit0 = warp_in * P.units_lane * L, c0 = unit0 * E - before;
   const int piece = P.cols - c0;
   const int n = min(P.units_lane, max(0, (piece + L * E - 1) / (L * E)));
   uint32_t at = rows::shared_address(dynamic);
-  const uint32_t wa = at;
-  if (P.weights_shared) at += units * E * 4;
+  // (alike: a group has weights of its own, moved by what its rows begin with)
+  const uint32_t wa = at + (COMMON ? group * units * E * 4 : 0);
+  if (P.weights_shared) at += (COMMON ? S::kGroups : 1) * units * E * 4;
   const uint32_t slot_bytes = (P.units_lane * L + 1) * 16, array_bytes = slot_bytes * S::kRows * S::kWarps;
   const uint32_t stage_bytes = (P.grad_sum ? 3 : 2) * array_bytes;
   at += slot_bytes * (warp * S::kRows + lane / L);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const float inv = 1.0f / static_cast<float>(P.cols);
-  const long long step = static_cast<long long>(gridDim.x) * S::kGroups * S::kRows;
-  long long r0 = (static_cast<long long>(blockIdx.x) * S::kGroups + group) * S::kRows;
+  long long r0 = r0_first;
   float mean = 0.0f, rstd = 0.0f;  // of the row that is fetched
   long long r = r0 + lane / L, next = r;
   const char *nx = row_of<BF16>(P.x, next, P.sx, c0), *ng = row_of<BF16>(P.grad, next, P.sg, c0);
@@ -556,9 +578,20 @@ __global__ void __launch_bounds__(Shape<BF16, L, W, N>::kThreads, Shape<BF16, L,
   const bool ahead = P.stages == 2;
   if (ahead) fetch(0);
   if (P.weights_shared) {
-    stage_weights<BF16>(wa, P.weight, P.weight_f32, 1.0f, P.cols, units, S::kThreads);
+    stage_weights<BF16>(wa, P.weight, P.weight_f32, 1.0f, P.cols, units, static_cast<int>(threadIdx.x) - (COMMON ? group * W * 32 : 0),
+                        COMMON ? W * 32 : S::kThreads, before);
     __syncthreads();
   }
+  // zeros for entries in front of the row
+  auto only = [&](int unit, Pair (&x)[H]) {
+    if (unit != 0) return;
+#pragma unroll
+    for (int i = 0; i < H; ++i) {
+      float a, b;
+      rows::split(x[i], a, b);
+      x[i] = rows::pair(2 * i >= before ? a : 0.0f, 2 * i + 1 >= before ? b : 0.0f);
+    }
+  };
   Pair dw[V][H], db[V][H];
 #pragma unroll
   for (int v = 0; v < V; ++v)
@@ -584,7 +617,11 @@ __global__ void __launch_bounds__(Shape<BF16, L, W, N>::kThreads, Shape<BF16, L,
       Pair x[H], g[H], w[H];
       rows::numbers<BF16>(rows::unit<ALIGNED>(slot, ALIGNED ? 0u : shift_x, k), x);
       rows::numbers<BF16>(rows::unit<ALIGNED>(slot + array_bytes, ALIGNED ? 0u : shift_g, k), g);
-      weights<BF16>(P, wa, P.weight, 1.0f, unit0 + k, units, w);
+      weights<BF16, false, COMMON>(P, wa, P.weight, 1.0f, unit0 + k, units, w, before);
+      if (COMMON && v == 0) {
+        only(unit0 + k, x);
+        only(unit0 + k, g);
+      }
 #pragma unroll
       for (int i = 0; i < H; ++i) {
         const Pair xhat = rows::mul(rows::add(x[i], minus), scale);
@@ -604,7 +641,7 @@ __global__ void __launch_bounds__(Shape<BF16, L, W, N>::kThreads, Shape<BF16, L,
       Pair x[H], g[H], w[H], o[H];
       rows::numbers<BF16>(rows::unit<ALIGNED>(slot, ALIGNED ? 0u : shift_x, k), x);
       rows::numbers<BF16>(rows::unit<ALIGNED>(slot + array_bytes, ALIGNED ? 0u : shift_g, k), g);
-      weights<BF16>(P, wa, P.weight, 1.0f, unit0 + k, units, w);
+      weights<BF16, false, COMMON>(P, wa, P.weight, 1.0f, unit0 + k, units, w, before);
 #pragma unroll
       for (int i = 0; i < H; ++i) {
         const Pair xhat = rows::mul(rows::add(x[i], minus), scale);
@@ -619,7 +656,10 @@ __global__ void __launch_bounds__(Shape<BF16, L, W, N>::kThreads, Shape<BF16, L,
         for (int i = 0; i < H; ++i) o[i] = rows::mul(scale, o[i]);
       }
       if (ALIGNED) {
-        rows::store_unit<BF16>(out, k, left, rows::pack<BF16>(o), inside && v + 1 < n);
+        if (COMMON && v == 0 && before != 0 && unit0 + k == 0)
+          rows::store_some<BF16>(out + 16 * k, rows::pack<BF16>(o), before, min(left, E));
+        else
+          rows::store_unit<BF16>(out, k, left, rows::pack<BF16>(o), inside && v + 1 < n);
       } else {
         __syncwarp();  // the neighbours have read this unit of x
         rows::shared_store(slot + 16 * k, rows::pack<BF16>(o));
@@ -658,6 +698,20 @@ __global__ void __launch_bounds__(Shape<BF16, L, W, N>::kThreads, Shape<BF16, L,
       for (int v = 0; v < V; ++v) {
         if (v >= n) break;
         const int c = (unit0 + v * L + sub) * H;
+        if constexpr (COMMON) {
+          float* column = reinterpret_cast<float*>(dynamic);
+#pragma unroll
+          for (int i = 0; i < E; ++i) {
+            const int at_column = 2 * c + i - before;
+            if (at_column < 0 || at_column >= P.cols) continue;
+            float w0, w1, b0, b1;
+            rows::split(dw[v][i / 2], w0, w1);
+            rows::split(db[v][i / 2], b0, b1);
+            column[at_column] = (q ? column[at_column] : 0.0f) + (i & 1 ? w1 : w0);
+            column[units * E + at_column] = (q ? column[units * E + at_column] : 0.0f) + (i & 1 ? b1 : b0);
+          }
+          continue;
+        }
 #pragma unroll
         for (int i = 0; i < H; ++i) {
           sums[c + i] = q ? rows::add(sums[c + i], dw[v][i]) : dw[v][i];
@@ -822,17 +876,19 @@ struct Form {
   KernelPtr fn;
   int threads, rows_per_cta, capacity;  // capacity: entries of a row
   int lanes, warps, entries;            // lanes of a warp and warps per row, entries of a unit
+  bool alike;                           // for rows that begin off 16 bytes alike
 };
 
-template <bool BACKWARD, bool BF16, bool ALIGNED, int L, int W, int N = 32>
+template <bool BACKWARD, bool BF16, int ROWS, int L, int W, int N = 32>
 Form form() {
   using S = Shape<BF16, L, W, N>;
   KernelPtr fn;
   if constexpr (BACKWARD)
-    fn = norm_backward<BF16, ALIGNED, L, W, N>;
+    fn = norm_backward<BF16, ROWS, L, W, N>;
   else
-    fn = norm_forward<BF16, ALIGNED, L, W, N>;
-  return {fn, S::kThreads, S::kGroups * S::kRows, S::kCapacity, L, W, S::kE};
+    fn = norm_forward<BF16, ROWS == kAligned, L, W, N>;
+  // (a row that begins off 16 bytes takes up to E - 1 entries more)
+  return {fn, S::kThreads, S::kGroups * S::kRows, S::kCapacity - (ROWS == kAlike ? S::kE - 1 : 0), L, W, S::kE, ROWS == kAlike};
 }
 
 // The narrowest form that holds a row: 4 lanes up to 128 entries, doubled up to a
@@ -843,14 +899,18 @@ Form form() {
 // bfloat16 121 and 103, 32768 x 1600 113 and 108, 16384 x 4096 110 and 118).  Forward, 32
 // are better throughout (16384 x 4096 68 us, 85 with 16; 64: 104 us in place of 71 for
 // 32768 x 1600, as the code outgrows the instruction cache).
-template <bool BACKWARD, bool BF16, bool ALIGNED>
+template <bool BACKWARD, bool BF16, int ROWS>
 const Form* choose(int64_t cols, bool few) {
-  static const Form all[] = {form<BACKWARD, BF16, ALIGNED, 4, 1>(), form<BACKWARD, BF16, ALIGNED, 8, 1>(),
-                             form<BACKWARD, BF16, ALIGNED, 16, 1>(), form<BACKWARD, BF16, ALIGNED, 32, 1>(),
-                             form<BACKWARD, BF16, ALIGNED, 32, BACKWARD ? 4 : 2, BACKWARD ? 16 : 32>(),
-                             form<BACKWARD, BF16, ALIGNED, 32, BACKWARD ? 8 : 4, BACKWARD ? 16 : 32>(),
-                             form<BACKWARD, BF16, ALIGNED, 32, BACKWARD ? 16 : 8, BACKWARD ? 16 : 32>(),
-                             form<BACKWARD, BF16, ALIGNED, 32, 16>()};
+  constexpr int kHalf = BACKWARD ? 2 : 1, kEntries = 32 / kHalf;
+  // (rows that begin alike: one row a warp at least)
+  static const Form all[] = {form<BACKWARD, BF16, ROWS == kAlike ? kAny : ROWS, 4, 1>(),
+                             form<BACKWARD, BF16, ROWS == kAlike ? kAny : ROWS, 8, 1>(),
+                             form<BACKWARD, BF16, ROWS == kAlike ? kAny : ROWS, 16, 1>(),
+                             form<BACKWARD, BF16, ROWS, 32, 1>(),
+                             form<BACKWARD, BF16, ROWS, 32, 2 * kHalf, kEntries>(),
+                             form<BACKWARD, BF16, ROWS, 32, 4 * kHalf, kEntries>(),
+                             form<BACKWARD, BF16, ROWS, 32, 8 * kHalf, kEntries>(),
+                             form<BACKWARD, BF16, ROWS, 32, 16>()};
   const Form& last = all[std::size(all) - 1];
   const int64_t want = few ? cols * Shape<BF16, 32, 1, 32>::kV : cols;
   for (const Form& f : all)
@@ -859,9 +919,12 @@ const Form* choose(int64_t cols, bool few) {
 }
 
 template <bool BACKWARD>
-const Form* choose(bool bf16, bool aligned, int64_t cols, bool few) {
-  if (bf16) return aligned ? choose<BACKWARD, true, true>(cols, few) : choose<BACKWARD, true, false>(cols, few);
-  return aligned ? choose<BACKWARD, false, true>(cols, few) : choose<BACKWARD, false, false>(cols, few);
+const Form* choose(bool bf16, Begin rows, int64_t cols, bool few) {
+  if constexpr (BACKWARD) {
+    if (rows == kAlike) return bf16 ? choose<true, true, kAlike>(cols, few) : choose<true, false, kAlike>(cols, few);
+  }
+  if (bf16) return rows == kAligned ? choose<BACKWARD, true, kAligned>(cols, few) : choose<BACKWARD, true, kAny>(cols, few);
+  return rows == kAligned ? choose<BACKWARD, false, kAligned>(cols, few) : choose<BACKWARD, false, kAny>(cols, few);
 }
 
 // CTAs of a kernel that an SM holds with so much shared memory; the first
@@ -889,12 +952,12 @@ int resident(const Form& f, int smem) try {
 // How a CTA's shared memory is used for rows of `cols` entries: `arrays` of them
 // are copied ahead, `vectors` weights held.  Two stages where they fit; weights
 // where they fit beside those.
-int layout(RowParams& P, const Form& f, int arrays, int vectors) {
+int layout(RowParams& P, const Form& f, int arrays, int vectors, bool alike) {
   const int lane_entries = f.lanes * f.warps * f.entries;
-  P.units_lane = static_cast<int>((P.cols + lane_entries - 1) / lane_entries);
+  P.units_lane = static_cast<int>((P.cols + (alike ? f.entries - 1 : 0) + lane_entries - 1) / lane_entries);
   const int units = P.units_lane * f.lanes * f.warps;
   const int stage = arrays * (P.units_lane * f.lanes + 1) * 16 * (f.threads / f.lanes);
-  const int held = vectors * units * f.entries * 4;
+  const int held = vectors * (alike ? f.threads / (32 * f.warps) : 1) * units * f.entries * 4;
   P.stages = 2 * stage <= kSmemLimit ? 2 : 1;
   P.weights_shared = held + P.stages * stage <= kSmemLimit;
   return P.stages * stage + (P.weights_shared ? held : 0);
@@ -912,7 +975,7 @@ struct Long {
 bool long_shape(RowParams& P, int arrays, bool common, int per, int64_t rows, int sms, Long& shape) {
   P.units_lane = static_cast<int>((P.cols + static_cast<int64_t>(common ? per - 1 : 0) + per - 1) / per);
   const int64_t row = static_cast<int64_t>(arrays) * P.units_lane * 16;
-  const int64_t held = 2LL * per * (common ? (P.units_lane + 31) / 32 * 32 + 4 : P.units_lane) * 4;
+  const int64_t held = 2LL * per * (common ? turned_pitch(P.units_lane) : P.units_lane) * 4;
   if (row > kSmemLimit) return false;
   P.weights_shared = held + (common ? 1 : 3) * row <= kSmemLimit;
   const int64_t room = kSmemLimit - (P.weights_shared ? held : 0), fit = std::min<int64_t>(room / row, 32);
@@ -1025,13 +1088,13 @@ extern "C" muon_status_t layer_norm(const void* x, int dtype, int64_t rows, int6
   if ((common ? cols * size >= 1536 : vec && cols > 8192) && long_shape(P, residual ? 2 : 1, common, 16 / size, rows, sms, shape)) {
     const KernelPtr fn = bf16 ? (common ? norm_forward_long<true, true> : norm_forward_long<true, false>)
                               : (common ? norm_forward_long<false, true> : norm_forward_long<false, false>);
-    const Form f{fn, shape.threads, shape.groups, 0, 32, P.warps, 16 / size};
+    const Form f{fn, shape.threads, shape.groups, 0, 32, P.warps, 16 / size, common};
     const int per_sm = resident(f, shape.smem);
     if (per_sm == 0) return MUON_ERR_CUDA;
     const int64_t ctas = std::min<int64_t>((rows + shape.groups - 1) / shape.groups, static_cast<int64_t>(sms) * per_sm);
     e = launch(reinterpret_cast<const void*>(fn), dim3(static_cast<unsigned>(ctas)), shape.threads, shape.smem, P, str);
-  } else if (const Form* f = choose<false>(bf16, vec, cols, rows <= 2 * sms)) {
-    const int smem = layout(P, *f, residual ? 2 : 1, 2), per_sm = resident(*f, smem);
+  } else if (const Form* f = choose<false>(bf16, vec ? kAligned : kAny, cols, rows <= 2 * sms)) {
+    const int smem = layout(P, *f, residual ? 2 : 1, 2, false), per_sm = resident(*f, smem);
     if (per_sm == 0) return MUON_ERR_CUDA;
     const int64_t ctas = std::min<int64_t>((rows + f->rows_per_cta - 1) / f->rows_per_cta, static_cast<int64_t>(sms) * per_sm);
     e = launch(reinterpret_cast<const void*>(f->fn), dim3(static_cast<unsigned>(ctas)), f->threads, smem, P, str);
@@ -1044,7 +1107,7 @@ extern "C" muon_status_t layer_norm(const void* x, int dtype, int64_t rows, int6
 
 extern "C" size_t layer_norm_backward_workspace_size(int64_t rows, int64_t cols) {
   if (rows < 0 || cols < 1 || cols > kMaxCols || rows > 0x7FFFFFFF) return 0;
-  const bool wide = !choose<true>(true, true, cols, false);
+  const bool wide = !choose<true>(true, kAny, cols, false);
   return static_cast<size_t>(wide ? kWideParts : kMaxParts) * 2 * cols * 4 + (wide ? static_cast<size_t>(rows) * 8 : 0);
 }
 
@@ -1061,7 +1124,7 @@ extern "C" muon_status_t layer_norm_backward(const void* grad, int64_t grad_stri
   if (std::max({row_stride, grad_stride, grad_x_stride, grad_sum ? grad_sum_stride : 0}) > (1LL << 32))
     return MUON_ERR_TOO_LARGE;
   const bool columns = grad_weight || grad_bias;
-  const bool wide = !choose<true>(true, true, cols, false);
+  const bool wide = !choose<true>(true, kAny, cols, false);
   const size_t need = layer_norm_backward_workspace_size(rows, cols);
   if (rows > 0) {
     if (!grad || !x || !mean || !rstd || !grad_x) return MUON_ERR_INVALID_ARG;
@@ -1110,7 +1173,6 @@ extern "C" muon_status_t layer_norm_backward(const void* grad, int64_t grad_stri
   P.rows = rows;
   P.cols = static_cast<int>(cols);
   P.weight_f32 = weight_dtype == MUON_F32;
-  P.weight_vec = aligned_to(weight, 16);
   P.grad_weight = grad_weight, P.grad_bias = grad_bias;
   P.partial = columns ? static_cast<float*>(workspace) : nullptr;
   const bool bf16 = dtype == MUON_BF16;
@@ -1119,11 +1181,21 @@ extern "C" muon_status_t layer_norm_backward(const void* grad, int64_t grad_stri
     auto rows_aligned = [&](const void* p, int64_t stride) { return !p || (aligned_to(p, 16) && stride * size % 16 == 0); };
     const bool vec = rows_aligned(x, row_stride) && rows_aligned(grad, grad_stride) &&
                      rows_aligned(grad_sum, grad_sum_stride) && rows_aligned(grad_x, grad_x_stride);
-    const Form& f = *choose<true>(bf16, vec, cols, rows <= 2 * sms);
-    const int smem = layout(P, f, grad_sum ? 3 : 2, 1), per_sm = resident(f, smem);
+    const uint32_t low = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(x)) & 15;
+    auto alike = [&](const void* p, int64_t stride) {
+      return !p || ((static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15) == low && (stride - row_stride) * size % 16 == 0);
+    };
+    const Begin begin = vec ? kAligned : alike(grad, grad_stride) && alike(grad_sum, grad_sum_stride) && alike(grad_x, grad_x_stride) ? kAlike : kAny;
+    const Form* f = choose<true>(bf16, begin, cols, rows <= 2 * sms);
+    if (!f) f = choose<true>(bf16, kAny, cols, rows <= 2 * sms);
+    const bool turned = begin == kAlike && f->alike;
+    const int smem = layout(P, *f, grad_sum ? 3 : 2, 1, turned), per_sm = resident(*f, smem);
     if (per_sm == 0) return MUON_ERR_CUDA;
-    P.parts = static_cast<int>(std::min<int64_t>({(rows + f.rows_per_cta - 1) / f.rows_per_cta, static_cast<int64_t>(sms) * per_sm, kMaxParts}));
-    e = launch(reinterpret_cast<const void*>(f.fn), dim3(static_cast<unsigned>(P.parts)), f.threads, smem, P, str);
+    int64_t parts = std::min<int64_t>({(rows + f->rows_per_cta - 1) / f->rows_per_cta, static_cast<int64_t>(sms) * per_sm, kMaxParts});
+    // a group's rows begin at one offset where a multiple of 8 (float32: 4) rows lies between them
+    if (turned) parts = (parts + 7) / 8 * 8;
+    P.parts = static_cast<int>(std::min<int64_t>(parts, kMaxParts));
+    e = launch(reinterpret_cast<const void*>(f->fn), dim3(static_cast<unsigned>(P.parts)), f->threads, smem, P, str);
   } else {
     P.rows2 = reinterpret_cast<float2*>(static_cast<char*>(workspace) + static_cast<size_t>(kWideParts) * 2 * P.cols * 4);
     P.parts = static_cast<int>(std::min<int64_t>(rows, kWideParts));
