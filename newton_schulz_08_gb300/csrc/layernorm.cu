@@ -190,34 +190,46 @@ __device__ __forceinline__ void weights(const RowParams& P, uint32_t at, const v
 __host__ __device__ constexpr int turned_pitch(int units) { return (units + 31) / 32 * 32 + 4; }
 
 template <bool BF16>
-__device__ __forceinline__ void stage_turned(uint32_t at, const void* w, int f32, float none, int cols, int units, int threads) {
+__device__ __forceinline__ void stage_turned(const RowParams& P, uint32_t wa, uint32_t ba, int units) {
   constexpr int E = rows::Unit<BF16>::n;
   const int pitch = turned_pitch(units);
-  for (int i = threadIdx.x; i < units * E; i += threads) {
-    const float v = w && i < cols ? weight_at(w, f32, i) : none;
-    asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + ((i % E) * pitch + i / E) * 4), "f"(v) : "memory");
+#pragma unroll 4
+  for (int i = threadIdx.x; i < units * E; i += blockDim.x) {
+    const uint32_t to = ((i % E) * pitch + i / E) * 4;
+    const float w = P.weight && i < P.cols ? weight_at(P.weight, P.weight_f32, i) : 1.0f;
+    const float b = P.bias && i < P.cols ? weight_at(P.bias, P.weight_f32, i) : 0.0f;
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(wa + to), "f"(w) : "memory");
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(ba + to), "f"(b) : "memory");
   }
 }
 
-// Weights of a unit of memory, whose first `before` entries belong to the
+// Weights and biases of a unit of memory, whose first `before` entries belong to the
 // unit in front (any number where that is not the row's).
 template <bool BF16>
-__device__ __forceinline__ void turned_weights(const RowParams& P, uint32_t at, const void* w, float none, int unit, int pitch,
-                                               int before, Pair (&x)[rows::Unit<BF16>::n / 2]) {
+__device__ __forceinline__ void turned_weights(const RowParams& P, uint32_t wa, uint32_t ba, int unit, int pitch, int before,
+                                               Pair (&w)[rows::Unit<BF16>::n / 2], Pair (&b)[rows::Unit<BF16>::n / 2]) {
   constexpr int E = rows::Unit<BF16>::n;
-  float v[E];
+  if (P.weights_shared) {
+    float v[2][E];
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    if (P.weights_shared) {
+    for (int e = 0; e < E; ++e) {
       const uint32_t from = (((e - before) & (E - 1)) * pitch + unit - (e < before)) * 4;
-      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[e]) : "r"(at + from) : "memory");
-    } else {
+      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[0][e]) : "r"(wa + from) : "memory");
+      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[1][e]) : "r"(ba + from) : "memory");
+    }
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) w[i] = rows::pair(v[0][2 * i], v[0][2 * i + 1]), b[i] = rows::pair(v[1][2 * i], v[1][2 * i + 1]);
+  } else {
+    auto at_column = [&](const void* p, float none, int e) {
       const int c = unit * E + e - before;
-      v[e] = w && c >= 0 && c < P.cols ? weight_at(w, P.weight_f32, c) : none;
+      return p && c >= 0 && c < P.cols ? weight_at(p, P.weight_f32, c) : none;
+    };
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) {
+      w[i] = rows::pair(at_column(P.weight, 1.0f, 2 * i), at_column(P.weight, 1.0f, 2 * i + 1));
+      b[i] = rows::pair(at_column(P.bias, 0.0f, 2 * i), at_column(P.bias, 0.0f, 2 * i + 1));
     }
   }
-#pragma unroll
-  for (int i = 0; i < E / 2; ++i) x[i] = rows::pair(v[2 * i], v[2 * i + 1]);
 }
 
 // Where rows begin: anywhere, on 16 bytes, or off them at the same offset in all arrays.
@@ -417,8 +429,7 @@ __global__ void __launch_bounds__(1024) norm_forward_long(const __grid_constant_
   fetch();
   if (P.weights_shared) {
     if constexpr (COMMON) {
-      stage_turned<BF16>(wa, P.weight, P.weight_f32, 1.0f, P.cols, units, blockDim.x);
-      stage_turned<BF16>(ba, P.bias, P.weight_f32, 0.0f, P.cols, units, blockDim.x);
+      stage_turned<BF16>(P, wa, ba, units);
     } else {
       stage_weights<BF16>(wa, P.weight, P.weight_f32, 1.0f, P.cols, units, threadIdx.x, blockDim.x);
       stage_weights<BF16>(ba, P.bias, P.weight_f32, 0.0f, P.cols, units, threadIdx.x, blockDim.x);
@@ -505,8 +516,7 @@ __global__ void __launch_bounds__(1024) norm_forward_long(const __grid_constant_
       Pair x[H], w[H], b[H];
       rows::numbers<BF16>(rows::shared_load(slot + 16 * k), x);
       if constexpr (COMMON) {
-        turned_weights<BF16>(P, wa, P.weight, 1.0f, k, pitch, before, w);
-        turned_weights<BF16>(P, ba, P.bias, 0.0f, k, pitch, before, b);
+        turned_weights<BF16>(P, wa, ba, k, pitch, before, w, b);
       } else {
         weights<BF16, true>(P, wa, P.weight, 1.0f, k, units, w);
         weights<BF16, true>(P, ba, P.bias, 0.0f, k, units, b);
@@ -887,8 +897,10 @@ Form form() {
     fn = norm_backward<BF16, ROWS, L, W, N>;
   else
     fn = norm_forward<BF16, ROWS == kAligned, L, W, N>;
-  // (a row that begins off 16 bytes takes up to E - 1 entries more)
-  return {fn, S::kThreads, S::kGroups * S::kRows, S::kCapacity - (ROWS == kAlike ? S::kE - 1 : 0), L, W, S::kE, ROWS == kAlike};
+  // A row that begins off 16 bytes takes up to E - 1 entries more.  One warp has such rows up to 768 entries, as
+  // its groups' weights do not fit beside more (30000 x 1001 float32 with grad_sum 179 us, 108 with four warps; 30000 x 515 60 and 76).
+  constexpr int kLess = ROWS != kAlike ? 0 : W == 1 ? S::kCapacity / 4 : S::kE - 1;
+  return {fn, S::kThreads, S::kGroups * S::kRows, S::kCapacity - kLess, L, W, S::kE, ROWS == kAlike};
 }
 
 // The narrowest form that holds a row: 4 lanes up to 128 entries, doubled up to a
