@@ -728,6 +728,21 @@ cudaError_t prepare(const Kernel& k, int slot, bool pair, int sms, int* pairs) {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// CTAs that share a tile's K blocks.  A block takes a CTA 0.25 us; sending and
+// adding partial sums costs as much as `cost` blocks, more between two CTAs, who add half a
+// tile each, than among more.  us with 1, 2, 4 and 8 CTAs: 13 tiles of 32 columns, 7 blocks
+// 5.1, 6.0, 4.4, 4.5, 64 blocks 19.8, 13.4, 9.0, 7.4; 32 tiles of 128 columns, 7 blocks 7.1, 10.5, 7.4, 7.5, 64
+// blocks 21.3, 18.2, 13.2, 15.8; 76 tiles of 128, 25 blocks 11.6, 13.6, 20.1.  They have an SM each, but two
+// narrow ones may share one (64 tiles of 32 columns, 64 blocks 20.1, 14.1, 11.0, 16.6; 50 of them, 7 blocks 5.5, 6.0, 6.0).
+int tile_splits(int64_t tiles, int64_t kblocks, int bn, int sms) {
+  for (int s = 8; s > 1; s /= 2) {
+    const bool shared = s == 4 && bn == 32 && kblocks >= 16;
+    const int64_t cost = s == 2 ? 2 + bn / 8 : 2 + bn / 32;
+    if (s <= kblocks && tiles * s <= (shared ? 2 : 1) * sms && kblocks - kblocks / s >= cost) return s;
+  }
+  return 1;
+}
+
 }  // namespace
 
 MUON_CHECK_READER(check_failures_fp4_mm)
@@ -772,14 +787,18 @@ extern "C" muon_status_t fp4_mm(const fp4_matrix* a, const fp4_matrix* b, void* 
   }
   MmParams P;
   std::memset(&P, 0, sizeof(P));
-  // Pairs where they have half of the SMs to run on (200 x 4800 x 1600, 19 tiles of 256 x 256: 11 us in small tiles;
-  // 1600 x 1600 x 16384, 49: 27).  The tile kernel's 128 rows are the larger matrix's.
+  // The tile kernel's 128 rows are the larger matrix's.  Pairs take over where its
+  // tiles are more than the SMs (m x n x k, bfloat16 out, us, tiles and pairs: 1024 x 2048 x 6400
+  // 12.2 and 13.1; 1600 x 1600 x 1600 8.0 and 7.7, x 16384 28.9 and 25.3; 64 x 50304 x 1600
+  // 15.7 and 13.6), but not for up to 32 rows, whose 256 would be mostly empty (8 x 50304 x 1600 11.6 and 18.2).
   const int64_t pair_tiles = ceil_div(m, 256) * ceil_div(n, 256);
-  const bool pair = pair_tiles * 2 >= sms;
+  const int64_t narrow = std::min(m, n);
+  const int width = narrow <= 32 ? 32 : narrow <= 64 ? 64 : 128;
+  const bool pair = width > 32 && ceil_div(std::max(m, n), 128) * ceil_div(narrow, width) > sms;
   const bool swapped = !pair && n > m;
   const fp4_matrix& big = swapped ? *b : *a;
   const fp4_matrix& small = swapped ? *a : *b;
-  const int bn = pair ? 0 : small.rows <= 32 ? 32 : small.rows <= 64 ? 64 : 128;
+  const int bn = pair ? 0 : width;
   const int rows_b = pair ? 128 : bn;
   P.tiles_m = static_cast<int>(ceil_div(big.rows, pair ? 256 : 128));
   P.tiles_n = static_cast<int>(ceil_div(small.rows, pair ? 256 : bn));
@@ -816,8 +835,7 @@ extern "C" muon_status_t fp4_mm(const fp4_matrix* a, const fp4_matrix* b, void* 
     cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(pairs, pair_tiles)));
   } else {
     const int64_t tiles = static_cast<int64_t>(P.tiles_m) * P.tiles_n, kblocks = ceil_div(k, kFp4Depth);
-    int splits = 1;
-    while (splits < 8 && tiles * splits < sms && kblocks >= 2 * splits) splits *= 2;
+    const int splits = tile_splits(tiles, kblocks, bn, sms);
     config(cfg, attr, kern, splits, str);
     cfg.gridDim = dim3(static_cast<unsigned>(tiles * splits));
   }

@@ -194,6 +194,22 @@ def test_product_into_views(offset, pad, m, n, dtype):
     assert (flat == 7.0).all()  # and nothing beside it was written
 
 
+@pytest.mark.parametrize("offset,pad", [(0, 0), (1, 3)])
+@pytest.mark.parametrize("m,n,k", [(30, 700, 1600), (700, 30, 2500), (20, 300, 2500), (5, 6400, 3300), (6400, 3, 4500), (9, 8192, 4500),
+                                   (50, 6400, 6000), (64, 500, 9000), (100, 6400, 10_000), (6401, 100, 10_000), (130, 1200, 2100)])
+def test_product_of_shared_sums(m, n, k, offset, pad):
+    """Tiles whose K blocks are shared by 2, 4 or 8 CTAs, some of them without a block."""
+    for block, dtype in ((32, B), (16, F)):
+        a, b = operands(m, n, k, block, seed=5)
+        flat = torch.full(((m + 2) * (n + pad) + 16,), 7.0, dtype=dtype, device="cuda")
+        out = flat[offset:offset + m * (n + pad)].view(m, n + pad)[:, :n]
+        product(a, b, out=out)
+        check_product(a, b, out)
+        assert torch.equal(out, product(a, b, dtype=dtype))
+        out.fill_(7.0)
+        assert (flat == 7.0).all()
+
+
 def test_product_of_extreme_tensors():
     """Factors of 2^-127 and 2^116: their product is taken before anything is lost."""
     x, y = rand(50, 96, spread=0.1), rand(60, 96, seed=1, spread=0.1)
