@@ -158,7 +158,7 @@ muon_status_t ns5_workspace_layout(int batch, int64_t rows, int64_t cols, muon_w
 /* Process-wide knobs for tests and diagnostics.  Keys:
  *   "wait_budget_cycles"  clock64 cycles a kernel waits on one barrier
  *                         before giving up (default 4e9, about 2 s);
- *   "inject_stall"        1: the Newton-Schulz kernels' MMA warp issues
+ *   "inject_stall"        1: the Newton-Schulz and fp4_mm kernels' MMA warp issues
  *                         nothing, so their waits expire (tests the bounded
  *                         wait path; combine with a small budget);
  *   "wait_profile_buffer" device address of a zeroed int64 array of
