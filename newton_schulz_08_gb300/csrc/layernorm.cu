@@ -17,7 +17,8 @@
 //   - a row belongs to 4 to 32 lanes of a warp, or 2 to 32 warps, by its length;
 //   - rows off 16 bytes at one offset in all arrays (odd lengths, contiguous)
 //     are taken in units of memory, the row's entries turned within them; at
-//     different offsets, every lane moves bytes between two units (rows.cuh).
+//     different offsets, entries move between neighbouring lanes (long rows
+//     forward) or between two units in shared memory (rows.cuh).
 // Backward, a thread has the same columns in every row and adds their
 // gradients of weight and bias in registers; it makes two passes over the row
 // in shared memory (its two means, then grad_x).  Each CTA leaves one row of
@@ -411,8 +412,9 @@ __global__ void __launch_bounds__(Shape<BF16, L, W, N>::kThreads, Shape<BF16, L,
 // hide behind one another (two slots a row and half the rows: 3001 x 12289
 // bfloat16 66 us, 58 so).  Units are those of memory: nothing moves between
 // lanes, a thread reads what it has copied, and entries beside the row are left
-// out of its first and last unit.
-template <bool BF16, bool COMMON>
+// out of its first and last unit.  MOVED: results begin at other offsets than what is read;
+// a unit of theirs comes from two neighbouring lanes.
+template <bool BF16, bool COMMON, bool MOVED>
 __global__ void __launch_bounds__(1024) norm_forward_long(const __grid_constant__ RowParams P) {
   constexpr int E = rows::Unit<BF16>::n, H = E / 2, kSize = 16 / E;
   extern __shared__ uint4 dynamic[];
@@ -468,9 +470,8 @@ __global__ void __launch_bounds__(1024) norm_forward_long(const __grid_constant_
   };
   for (int it = 0; r < P.rows; ++it) {
     rows::copies_wait(0);
-    char* y = row_of<BF16>(P.y, r, P.sy, 0);
-    const int shift = COMMON ? static_cast<int>(rows::shift_of(y)) : 0, before = shift / kSize;
-    y -= shift;
+    const int shift = COMMON ? static_cast<int>(rows::shift_of(row_of<BF16>(P.x, r, P.sx, 0))) : 0, before = shift / kSize;
+    char* y = row_of<BF16>(P.y, r, P.sy, 0) - shift;
     const int n = before + P.cols, last = (n - 1) / E;  // entries up to the row's end; its last unit
     // entries [from, to) of unit k are the row's
     auto first = [&](int k) { return COMMON && k == 0 ? before : 0; };
@@ -485,24 +486,48 @@ __global__ void __launch_bounds__(1024) norm_forward_long(const __grid_constant_
       }
     };
     auto store = [&](char* p, int k, const uint4& q) {
+      if constexpr (MOVED) {
+        const int lane = threadIdx.x & 31;
+        const uint32_t rel = rows::shift_of(p);
+        if (rel != 0) {  // (the same in every lane)
+          const uint4 front = make_uint4(__shfl_up_sync(0xFFFFFFFFu, q.x, 1), __shfl_up_sync(0xFFFFFFFFu, q.y, 1),
+                                         __shfl_up_sync(0xFFFFFFFFu, q.z, 1), __shfl_up_sync(0xFFFFFFFFu, q.w, 1));
+          if (k > last) return;
+          const int moved = static_cast<int>(rel) / kSize, left = n + moved - k * E;
+          char* unit = p - rel + 16 * k;
+          const int from = max(lane == 0 ? moved : 0, before + moved - k * E), to = min(left, E);
+          if (from <= 0 && to == E)
+            *reinterpret_cast<uint4*>(unit) = rows::funnel(front, q, 16 - rel);
+          else
+            rows::store_some<BF16>(unit, rows::funnel(front, q, 16 - rel), from, to);
+          if (lane == 31 || k == last)
+            rows::store_some<BF16>(unit + 16, rows::funnel(q, q, 16 - rel), max(0, before + moved - (k + 1) * E), min(left - E, moved));
+          return;
+        }
+        if (k > last) return;
+      }
       if (!edge(k) || (first(k) == 0 && end(k) == E))
         *reinterpret_cast<uint4*>(p + 16 * k) = q;
       else
         rows::store_some<BF16>(p + 16 * k, q, first(k), end(k));
     };
+    // (with stores from two lanes a warp goes on together, lanes past the row's end with any numbers)
+    auto goes_on = [&](int k) { return MOVED ? k - static_cast<int>(threadIdx.x & 31) <= last : k <= last; };
     Pair s = rows::pair(0.0f);
 #pragma unroll 2
-    for (int k = t; k <= last; k += T) {
+    for (int k = t; P.residual ? goes_on(k) : k <= last; k += T) {
+      const uint32_t unit = 16 * (MOVED ? min(k, last) : k);
       Pair x[H];
-      rows::numbers<BF16>(rows::shared_load(slot + 16 * k), x);
+      rows::numbers<BF16>(rows::shared_load(slot + unit), x);
       if (P.residual) {
         Pair a[H];
-        rows::numbers<BF16>(rows::shared_load(slot + array_bytes + 16 * k), a);
+        rows::numbers<BF16>(rows::shared_load(slot + array_bytes + unit), a);
 #pragma unroll
         for (int i = 0; i < H; ++i) x[i] = rows::add(x[i], a[i]);
         const uint4 q = rows::pack<BF16>(x);
-        rows::shared_store(slot + 16 * k, q);
+        if (!MOVED || k <= last) rows::shared_store(slot + 16 * k, q);
         store(row_of<BF16>(P.sum, r, P.ssum, 0) - shift, k, q);
+        if (MOVED && k > last) break;
         rows::numbers<BF16>(q, x);
       }
       if (COMMON && k == 0) only(x, k);
@@ -530,14 +555,15 @@ __global__ void __launch_bounds__(1024) norm_forward_long(const __grid_constant_
     }
     const Pair scale = rows::pair(rstd);
 #pragma unroll 2
-    for (int k = t; k <= last; k += T) {
+    for (int k = t; goes_on(k); k += T) {
+      const int unit = MOVED ? min(k, last) : k;
       Pair x[H], w[H], b[H];
-      rows::numbers<BF16>(rows::shared_load(slot + 16 * k), x);
+      rows::numbers<BF16>(rows::shared_load(slot + 16 * unit), x);
       if constexpr (COMMON) {
-        turned_weights<BF16>(P, wa, ba, k, pitch, before, w, b);
+        turned_weights<BF16>(P, wa, ba, unit, pitch, before, w, b);
       } else {
-        weights<BF16, true>(P, wa, P.weight, 1.0f, k, units, w);
-        weights<BF16, true>(P, ba, P.bias, 0.0f, k, units, b);
+        weights<BF16, true>(P, wa, P.weight, 1.0f, unit, units, w);
+        weights<BF16, true>(P, ba, P.bias, 0.0f, unit, units, b);
       }
 #pragma unroll
       for (int i = 0; i < H; ++i) x[i] = rows::fma(rows::mul(rows::add(x[i], minus), scale), w[i], b[i]);
@@ -1111,13 +1137,18 @@ extern "C" muon_status_t layer_norm(const void* x, int dtype, int64_t rows, int6
   auto alike = [&](const void* p, int64_t stride) {
     return !p || ((static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15) == low && (stride - row_stride) * size % 16 == 0);
   };
-  const bool common = !vec && alike(residual, residual_stride) && alike(y, y_stride) && alike(sum, sum_stride);
+  const bool together = alike(residual, residual_stride), common = !rows_aligned(x, row_stride);
+  const bool moved = !alike(y, y_stride) || !alike(sum, sum_stride);
   // Long rows, and rows that begin off 16 bytes alike, if they are not short: 40000 x 1601 bfloat16 with a residual
-  // 157 us in the registers, 115 so; 30000 x 515 float32 48 and 39; 100000 x 255 bfloat16 66 and 134.
+  // 157 us in the registers, 116 so; 30000 x 515 float32 48 and 39; 100000 x 255 bfloat16 66 and 134.  Results at other
+  // offsets (from rows a multiple of 16 bytes apart): 3001 x 12289 78 us and 71, 40000 x 1601 with a residual 157 and 169.
   Long shape{};
-  if ((common ? cols * size >= 1536 : vec && cols > 8192) && long_shape(P, residual ? 2 : 1, common, 16 / size, rows, sms, shape)) {
-    const KernelPtr fn = bf16 ? (common ? norm_forward_long<true, true> : norm_forward_long<true, false>)
-                              : (common ? norm_forward_long<false, true> : norm_forward_long<false, false>);
+  if (together && (vec || moved ? cols > 8192 : cols * size >= 1536) && long_shape(P, residual ? 2 : 1, common, 16 / size, rows, sms, shape)) {
+    const KernelPtr fns[2][2][2] = {{{norm_forward_long<false, false, false>, norm_forward_long<false, false, true>},
+                                     {norm_forward_long<false, true, false>, norm_forward_long<false, true, true>}},
+                                    {{norm_forward_long<true, false, false>, norm_forward_long<true, false, true>},
+                                     {norm_forward_long<true, true, false>, norm_forward_long<true, true, true>}}};
+    const KernelPtr fn = fns[bf16][common][moved];
     const Form f{fn, shape.threads, shape.groups, 0, 32, P.warps, 16 / size, common};
     const int per_sm = resident(f, shape.smem);
     if (per_sm == 0) return MUON_ERR_CUDA;

@@ -254,3 +254,43 @@ def test_sum_in_place(into, kind, cols):
                rstd.data_ptr())
     for a, b in ((total, want.sum), (y, want.y), (mean, want.mean), (rstd, want.rstd)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("cols", [520, 1601, 4099, 9001, 12289])
+@pytest.mark.parametrize("kind", [B, F])
+def test_in_place_odd(cols, kind):
+    """Rows that share 16 bytes with their neighbours, results in place of what is read."""
+    x, g, gs = (make(300, cols, kind, seed=k) for k in range(3))
+    w, b = make(1, cols, F, seed=3)[0], make(1, cols, F, seed=4)[0]
+    r = muon.layer_norm(x, w, b)
+    check_forward(r, x, w, b, 1e-5)
+    want = muon.layer_norm_backward(g, x, r.mean, r.rstd, w, grad_sum=gs)
+    check_backward(want, g, x, r.mean, r.rstd, w, gs)
+    for at in (g, gs):
+        held = at.clone()
+        got = muon.layer_norm_backward(g, x, r.mean, r.rstd, w, grad_sum=gs, out=at)
+        assert torch.equal(at, want[0]) and torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
+        at.copy_(held)
+    assert muon.layer_norm(x, w, b, out=x).y is x and torch.equal(x, r.y)
+
+
+@pytest.mark.parametrize("rows,cols", [(5, 800), (70, 1601), (2000, 777), (40, 9000), (33, 12289), (4, 30001), (9, 2049)])
+@pytest.mark.parametrize("kind", [B, F])
+@pytest.mark.parametrize("pads", [(7, 0, 1), (0, 3, 2), (1, 1, 5)])
+def test_results_at_other_offsets(pads, kind, rows, cols):
+    """x and residual of one pitch, y of another, at offsets that move against one another from row to row."""
+    x, res = make(rows, cols, kind, pads[0], pads[1]), make(rows, cols, kind, pads[0], pads[1], seed=1)
+    w, b = make(1, cols, B, seed=2)[0], make(1, cols, B, seed=3)[0]
+    for residual in (None, res):
+        y = make(rows, cols, kind, pads[2], 1, seed=4)
+        between = torch.as_strided(y, ((rows - 1) * y.stride(0) + cols,), (1,))
+        edge = torch.ones(rows, cols + pads[2], dtype=torch.bool, device="cuda")
+        edge[:, :cols] = False
+        edge = edge.view(-1)[:between.numel()]
+        between[edge] = 3.0
+        r = muon.layer_norm(x, w, b, residual=residual, out=y)
+        s = x if residual is None else r.sum
+        if residual is not None:
+            assert torch.equal(s, (x.float() + res.float()).to(kind))
+        check_forward(r, s, w, b, 1e-5)
+        assert (between[edge] == 3.0).all()
