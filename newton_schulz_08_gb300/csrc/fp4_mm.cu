@@ -31,8 +31,8 @@
 //   - scales by tcgen05.cp: put into TMEM by warps (tcgen05.st) 8192^3 took 397 us.
 // Measured (blocks of 32, bfloat16 out, m x n x k): 8192^3 155 us, 7.1 PFLOP/s (3.65 times the
 // measured bf16 rate), blocks of 16 160; 16384 x 6400 x 1600 75 (0.58 of four times
-// that rate, 0.48 of the bandwidth), 6400 x 1600 x 16384 66; 512 x 6400 x 1600
-// 9.0, 3 x 6400 x 1600 6.1, 64 x 8192 x 8192 15.7 (0.34 of the bandwidth).
+// that rate, 0.46 of the bandwidth), 6400 x 1600 x 16384 66; 512 x 6400 x 1600
+// 8.0, 3 x 6400 x 1600 5.4, 64 x 8192 x 8192 11.6 (0.48 of the bandwidth).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
