@@ -634,7 +634,8 @@ muon_status_t fp4_mm(const fp4_matrix* a, const fp4_matrix* b, void* out, int dt
  *   weight, bias   cols of weight_dtype each, or NULL (1 and 0);
  *   mean, rstd     rows floats each, written.
  * 1 <= cols <= 2^24; rows = 0 is a no-op; eps >= 0.  A row with NaN or an
- * infinity is NaN, and so is a constant row where eps is 0.  y may be x itself
+ * infinity is NaN, and so is a constant row where eps is 0 (its mean is the
+ * constant, its differences are 0).  y may be x itself
  * where there is no residual (same pointer and pitch); written arrays overlap
  * nothing else.  Asynchronous on `stream`; no workspace.  Returns MUON_OK,
  * MUON_ERR_INVALID_ARG, MUON_ERR_MISALIGNED, MUON_ERR_ALIASING,
