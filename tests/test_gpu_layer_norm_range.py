@@ -9,7 +9,7 @@ import pytest
 import torch
 
 from newton_schulz_08_gb300 import muon
-from tests.test_gpu_layer_norm import check_forward, f64, make, within
+from tests.test_gpu_layer_norm import check_backward, check_forward, f64, make, within
 
 pytestmark = pytest.mark.gpu
 B, F = torch.bfloat16, torch.float32
@@ -64,3 +64,19 @@ def test_rows_that_differ_in_one_entry(rows, cols, kind):
     e_var = (2 * np.abs(true - mean[:, None]) * e_mean + e_mean ** 2).mean(1) + (D + 8) * U * var
     rstd = f64(r.rstd)
     assert ((rstd >= (var + e_var) ** -0.5 * (1 - 8 * U)) & (rstd <= np.maximum(var - e_var, 0) ** -0.5 * (1 + 8 * U))).all()
+
+
+@pytest.mark.parametrize("rows,cols", [(41, 1), (41, 5), (900, 33), (37, 100), (301, 257), (900, 601), (41, 1000), (33, 1601),
+                                       (900, 2047), (20, 5001), (9, 12_290), (5, 20_001)])
+@pytest.mark.parametrize("kind", [B, F])
+@pytest.mark.parametrize("pad,offset", [(0, 0), (1, 1)])
+@pytest.mark.parametrize("value,eps", [(2.0 ** 100, 1e-20), (-2.0 ** 113, 1e-12)])
+def test_gradients_of_constant_rows_far_from_zero(value, eps, pad, offset, kind, rows, cols):
+    """mean rstd is past float32's range, every difference is 0: grad_x = rstd (gw - mean(gw)), nothing for the weight's."""
+    x, g, gs = (make(rows, cols, kind, pad, offset, seed=k) for k in range(3))
+    w = make(1, cols, F, seed=3)[0]
+    x[::5], x[-1] = value, value
+    r = muon.layer_norm(x, w, eps=eps)
+    assert bool((r.mean[::5].double() * r.rstd[::5].double()).abs().ge(2.0 ** 128).all())
+    check_backward(muon.layer_norm_backward(g, x, r.mean, r.rstd, w, grad_sum=gs), g, x, r.mean, r.rstd, w, gs)
+    check_backward(muon.layer_norm_backward(g, x, r.mean, r.rstd, w), g, x, r.mean, r.rstd, w, None)
