@@ -556,8 +556,9 @@ muon_status_t fp8_mm_backward(const void* g, const void* x_f8, const void* w_f8,
  *           at ((r / 128) * T + b / 4) * 512 + (r % 32) * 16 + (r % 128) / 32 * 4
  *           + b % 4, T = ceil(cols / 256) * 64 / block (zeros where there is
  *           no block);
- *   scale   blocks of 16: two floats, the tensor's factor (a power of two) and
- *           the largest finite |x| it comes from; where fp4_quantize writes
+ *   scale   blocks of 16: two floats, the tensor's factor (any finite number;
+ *           fp4_quantize's is a power of two) and the largest finite |x| it
+ *           comes from, which nothing here reads; where fp4_quantize writes
  *           them, FP4_SCALE_FLOATS floats, of which it uses the others on the
  *           way; blocks of 32: NULL.
  * An entry is code * block scale * factor.  codes and scales are 16-byte
@@ -606,13 +607,15 @@ muon_status_t fp4_quantize(const void* x, int dtype, int64_t rows, int64_t cols,
 /* The numbers that a quantised matrix stands for, rows x cols of `dtype` with
  * row pitch out_stride.  They are exact in bfloat16 too, down to its subnormal
  * numbers; what a code stands for past float32's range (the nearest one to a
- * number of nearly 2^128 may be 2^128) is infinite. */
+ * number of nearly 2^128 may be 2^128) is infinite.  With a factor that is no
+ * power of two they are rounded to float32, after each of the two products, and then to `dtype`. */
 muon_status_t fp4_values(const fp4_matrix* q, void* out, int dtype, int64_t out_stride, void* stream);
 
 /* Product out = a b^T of two matrices of equal cols and block: out is a->rows x
  * b->rows of `dtype` (bfloat16 or float32), row pitch out_stride elements, any
  * alignment of the element.  Products are exact and accumulated in fp32; the
- * sum is rounded once.  cols = 0 gives zeros.  A NaN scale makes its row (column)
+ * sum, times both factors (whose product is rounded to float32, if they are no
+ * powers of two), is rounded once.  cols = 0 gives zeros.  A NaN scale makes its row (column)
  * of out NaN.  out and workspace overlap nothing else.
  *   workspace  at least 256 bytes, 256-byte aligned, holding the device status
  *              word (muon_device_status) and nothing else: calls whose status

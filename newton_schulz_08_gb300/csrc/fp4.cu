@@ -511,7 +511,12 @@ __global__ void __launch_bounds__(kThreads) fp4_values_kernel(const uint8_t* cod
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int by = static_cast<int>(blockIdx.x) / tiles_x, bx = static_cast<int>(blockIdx.x) - by * tiles_x;
   const int c = bx * 256 + lane * 8, r0 = warp * kRows;  // r0: within the tile
-  const float tensor = BLOCK == 16 ? *scale : 1.0f;
+  // A factor past 2^118, whose product with a block's scale may leave float32's range though 0 times it, or half of it,
+  // does not, is taken as 2^16 times less and the codes' numbers as that much more (never so with fp4_quantize's factors).
+  float tensor = BLOCK == 16 ? *scale : 1.0f;
+  const bool far = BLOCK == 16 && fabsf(tensor) > 0x1p118f && !isinf(tensor);
+  if (far) tensor *= 0x1p-16f;
+  const uint32_t below2 = far ? 0x47474700u : 0x3F3F3F00u, from2 = far ? 0x48484848u : 0x40404040u;
   if (threadIdx.x < 32 * kTiles)
     reinterpret_cast<uint4*>(sf)[threadIdx.x] = __ldg(reinterpret_cast<const uint4*>(scales + (by * ktiles + bx * kTiles) * 512) + threadIdx.x);
   const uint8_t* from = codes + (static_cast<long long>(by) * kTile + r0) * pitch + c / 2;
@@ -540,7 +545,7 @@ __global__ void __launch_bounds__(kThreads) fp4_values_kernel(const uint8_t* cod
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const uint32_t four = word[i] >> (16 * h), select = four & 0x7777u;
-        const uint32_t hi = __byte_perm(0x3F3F3F00u, 0x40404040u, select), lo = __byte_perm(0xC0800000u, 0xC0804000u, select);
+        const uint32_t hi = __byte_perm(below2, from2, select), lo = __byte_perm(0xC0800000u, 0xC0804000u, select);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const uint32_t x = __byte_perm(lo, hi, k ? 0x62 : 0x40) << 16, y = __byte_perm(lo, hi, k ? 0x73 : 0x51) << 16;

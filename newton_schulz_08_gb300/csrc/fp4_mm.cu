@@ -4,7 +4,7 @@
 //
 //   out[i][j] = sum over blocks b of  sa[i][b] sb[j][b] sum_k a[i][k] b[j][k]
 //
-// (times the tensors' powers of two for blocks of 16).  Codes arrive in shared
+// (times the tensors' factors for blocks of 16).  Codes arrive in shared
 // memory by TMA, 256 entries of K (128 bytes, 128-byte swizzle) a stage; their
 // scales arrive as whole 512-byte tiles and one instruction copies such a tile
 // to the 4 TMEM columns where the MMAs read it.
@@ -58,7 +58,7 @@ constexpr int kDepthBytes = kFp4Depth / 2;  // of a row of codes per stage
 struct MmParams {
   CUtensorMap codes_a, codes_b;    // bytes, box 128 x 128 (narrow side: BN rows), 128-byte swizzle
   CUtensorMap scales_a, scales_b;  // 512-byte tiles as rows, box: the tiles of a stage
-  const float* scale_a;            // powers of two of the tensors, or null
+  const float* scale_a;            // factors of the tensors, or null
   const float* scale_b;
   void* out;
   long long stride;
@@ -78,24 +78,26 @@ __device__ __forceinline__ void raise_timeout(const MmParams& P, volatile int* a
   atomicOr(P.status, kStatusTimeout);
 }
 
-// The product of the tensors' powers of two as two factors that both exist as
-// floats and whose first is the whole product where that exists.
+// The product of the tensors' factors as two factors: what an accumulator is
+// multiplied with, one after the other.  Where the product is a normal number it is the first one, rounded
+// once (exact for powers of two, which fp4_quantize writes), and the second is 1.  Where
+// it is below those, the first is the product times 2^126, so that the sum is rounded at the last step;
+// where it is above float32's range, the two are as they are.
 struct Factors {
   float a, b;
 };
 __device__ __forceinline__ Factors tensor_factors(const MmParams& P) {
   if (!P.scale_a) return {1.0f, 1.0f};
-  auto exponent = [](float s) {
-    const int e = static_cast<int>(__float_as_uint(s) >> 23 & 255u);
-    return e ? e - 127 : -127;
-  };
-  auto pow2 = [](int e) { return __uint_as_float(e < -126 ? 1u << 22 : static_cast<uint32_t>(e + 127) << 23); };
-  const int e = exponent(*P.scale_a) + exponent(*P.scale_b);
-  const int first = e < -126 || e > 127 ? e / 2 : e;
-  return {pow2(first), pow2(e - first)};
+  const float x = *P.scale_a, y = *P.scale_b, p = x * y;
+  if (isinf(p)) return {x, y};
+  if (fabsf(p) < 0x1p-126f) {  // (then the smaller one is below 2^-63)
+    const bool less = fabsf(x) < fabsf(y);
+    return {(less ? x : y) * 0x1p126f * (less ? y : x), 0x1p-126f};
+  }
+  return {p, 1.0f};
 }
 
-// The tensors' powers of two, on 32 accumulators.
+// The tensors' factors, on 32 accumulators.
 __device__ __forceinline__ void scale32(const MmParams& P, const Factors& f, uint32_t (&r)[32]) {
   if (!P.scale_a) return;
 #pragma unroll

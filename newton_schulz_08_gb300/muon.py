@@ -1040,7 +1040,8 @@ class FP4:
     codes    uint8, rows x ceil(cols / 32) * 16: E2M1, two per byte;
     scales   uint8: one E8M0 (block 32) or E4M3 (block 16) number per row and
              block, in tiles of 128 rows by 4 blocks;
-    scale    block 16: float32 [2], the tensor's power of two and the largest
+    scale    block 16: float32 [2], the tensor's factor (a power of two where
+             fp4_quantize makes it, else any finite number) and the largest
              magnitude it comes from; block 32: None.
 
     ``fp4_quantize`` makes one; made of a program's own arrays, they are
