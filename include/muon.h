@@ -615,8 +615,9 @@ muon_status_t fp4_values(const fp4_matrix* q, void* out, int dtype, int64_t out_
  * b->rows of `dtype` (bfloat16 or float32), row pitch out_stride elements, any
  * alignment of the element.  Products are exact and accumulated in fp32; the
  * sum, times both factors (whose product is rounded to float32, if they are no
- * powers of two), is rounded once.  cols = 0 gives zeros.  A NaN scale makes its row (column)
- * of out NaN.  out and workspace overlap nothing else.
+ * powers of two), is rounded once.  cols = 0 gives zeros; rows = 0 of a or b is
+ * a no-op, the status word included.  A NaN scale makes its row (column) of out
+ * NaN.  out and workspace overlap nothing else.
  *   workspace  at least 256 bytes, 256-byte aligned, holding the device status
  *              word (muon_device_status) and nothing else: calls whose status
  *              is not read may share one.
