@@ -593,7 +593,10 @@ size_t fp4_scales_size(int64_t rows, int64_t cols, int block);
  * adamw_step, key = mix(mix(lo(seed) + 0x9E3779B1 a) ^ hi(seed)), a = 1 for along
  * and 0 for across, j = r ceil(cols / 2) + c / 2 (the target's cols),
  *   h = mix(0x9E3779B1 lo(j) + key + 0x6A09E667 hi(j)),
- * its low half for even c and its high half for odd c.
+ * its low half for even c and its high half for odd c.  The seed is part of
+ * the launch: a recorded call that is replayed (a CUDA graph) rounds with the
+ * same bits each time, which is not unbiased over the replays.  Record
+ * roundings to nearest, or renew the recording for each step.
  * A block with an infinite or NaN entry has a NaN scale, and codes 0.
  * rows = 0 or cols = 0 is a no-op.  Asynchronous on `stream`; nothing is
  * allocated; equal calls give equal bits.  Returns MUON_OK,
@@ -632,7 +635,9 @@ muon_status_t fp4_mm(const fp4_matrix* a, const fp4_matrix* b, void* out, int dt
  * elements, any alignment of the element):
  *   s = x + residual, rounded to `dtype` (residual NULL: s = x),
  *   y = (s - mean) rstd weight + bias,  rstd = 1 / sqrt(mean((s - mean)^2) + eps).
- * Sums and statistics are float32, the variance of differences with the mean.
+ * Sums and statistics are float32, the variance of differences with the mean:
+ * a row whose sum leaves float32's range is NaN, and one whose sum of squared
+ * differences does has rstd 0.
  *   residual, sum  both or neither: s is written to sum (it may be x or
  *                  residual itself: same pointer and pitch);
  *   weight, bias   cols of weight_dtype each, or NULL (1 and 0);

@@ -1119,7 +1119,8 @@ def fp4_quantize(x, block=32, axis=1, seed=None, stream=None):
     down its columns; with axis="both" the two of them (one read of x).
     block: 32 (power-of-two scales) or 16 (E4M3 scales and a power of two for
     the tensor).  seed: round stochastically, with the random bits of that
-    seed; None: to nearest.  See fp4_quantize in include/muon.h."""
+    seed (a call recorded in a CUDA graph repeats its own); None: to nearest.
+    See fp4_quantize in include/muon.h."""
     if stream is not None:
         return _on(stream, x, fp4_quantize, x, block, axis, seed)
     rows, cols, pitch = _rows(x, "x")

@@ -80,3 +80,14 @@ def test_gradients_of_constant_rows_far_from_zero(value, eps, pad, offset, kind,
     assert bool((r.mean[::5].double() * r.rstd[::5].double()).abs().ge(2.0 ** 128).all())
     check_backward(muon.layer_norm_backward(g, x, r.mean, r.rstd, w, grad_sum=gs), g, x, r.mean, r.rstd, w, gs)
     check_backward(muon.layer_norm_backward(g, x, r.mean, r.rstd, w), g, x, r.mean, r.rstd, w, None)
+
+
+def test_rows_past_float32s_range():
+    """What the header says of them: NaN where the sum is infinite, rstd 0 (and the bias) where the sum of squares is."""
+    x = torch.zeros(3, 64, device="cuda")
+    x[0, ::2], x[0, 1::2] = 1e30, -1e30
+    x[1] = 1e37
+    b = torch.arange(64.0, device="cuda")
+    r = muon.layer_norm(x, None, b)
+    assert float(r.rstd[0]) == 0 and torch.equal(r.y[0], b)
+    assert r.y[1].isnan().all() and torch.equal(r.y[2], b)
