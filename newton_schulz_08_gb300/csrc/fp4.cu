@@ -6,8 +6,10 @@
 //   block 16: 2^k s, s = E4M3(max |x| / 6 / 2^k), 2^k the tensor's, the least
 //     with max |x| <= 6 448 2^k (fp4_amax_kernel finds the maximum).
 // Power-of-two factors are exact, so the quotient x / scale is rounded at most
-// once (a division by s, whose reciprocal is corrected by its remainder),
-// and nothing depends on the launch.
+// once, and nothing depends on the launch.  Quotients by s and by 6 are products
+// with the divisor's reciprocal, corrected by their remainder (Markstein 1990): the
+// result is the correctly rounded quotient where the reciprocal is the nearest number to 1 / s, the
+// product within a spacing of the quotient, and the remainder no subnormal number.
 //
 // One pass writes the codes along the rows, those across them (the operand of
 // the transposed product), or both: a CTA takes 128 x 128 entries, so that
@@ -20,7 +22,7 @@
 // Bound by memory while rounding to nearest with blocks of 32 (maxima are taken of
 // packed halves, quotients by multiplication), by instructions with
 // stochastic rounding (a hash per two entries, an addition and a shift each:
-// arithmetic pipes 75-80 % busy); blocks of 16 read x once more for the tensor's
+// arithmetic pipes 86 % busy); blocks of 16 read x once more for the tensor's
 // maximum.  Measured, 16384 x 6400 bfloat16: along 44 us (0.90 of the
 // measured copy bandwidth), across 45, both 60 (0.80), both stochastic 130;
 // blocks of 16: along 83, both 126, both stochastic 219.  fp4_values of
@@ -116,7 +118,7 @@ __device__ __forceinline__ Scale block_scale(uint32_t amax, float up_tensor) {
     q.up = bad ? 0.0f : __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
     q.s = q.r = 1.0f;
   } else {
-    // max / 6 to nearest: corrected by its remainder, where that is no subnormal number
+    // max / 6 to nearest: Markstein's correction; by a division where the remainder may be a subnormal number
     const float top = __uint_as_float(amax), t = top * (1.0f / 6.0f);
     float sixth = fmaf(fmaf(t, -6.0f, top), 1.0f / 6.0f, t);
     if (amax < (27u << 23) || bad) sixth = __fdiv_rn(top, 6.0f);  // below 2^-100
@@ -133,7 +135,8 @@ __device__ __forceinline__ Scale block_scale(uint32_t amax, float up_tensor) {
     q.s = value(code);
     q.code = bad ? nan_code<16>() : code;
     q.up = bad ? 0.0f : up_tensor;
-    // 1 / s to nearest: one step from the hardware's reciprocal (s has four significant bits)
+    // 1 / s to nearest: a Newton-Raphson step from the hardware's reciprocal, which is within a spacing (the step rounds to
+    // nearest for any significand but one of all ones; s has four significant bits)
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(q.s));
     q.r = code == 0 ? 0.0f : fmaf(r, fmaf(-q.s, r, 1.0f), r);
@@ -141,9 +144,9 @@ __device__ __forceinline__ Scale block_scale(uint32_t amax, float up_tensor) {
   return q;
 }
 
-// Eight numbers by their scale, rounded to nearest.  Blocks of 16: x / s is the
-// product with the rounded reciprocal, corrected by its remainder, which
-// makes it the correctly rounded quotient; signs are chosen so that a zero keeps its own.
+// Eight numbers by their scale, rounded to nearest.  Blocks of 16: x / s by
+// Markstein's correction; its remainder is a subnormal number only where the
+// quotient is far below the least code either way.  Signs are chosen so that a zero keeps its own.
 template <int BLOCK>
 __device__ __forceinline__ void in_units(Pair (&x)[4], const Scale& q) {
   if constexpr (BLOCK == 32) {

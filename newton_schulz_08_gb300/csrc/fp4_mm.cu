@@ -32,7 +32,7 @@
 // Measured (blocks of 32, bfloat16 out, m x n x k): 8192^3 155 us, 7.1 PFLOP/s (3.65 times the
 // measured bf16 rate), blocks of 16 160; 16384 x 6400 x 1600 75 (0.58 of four times
 // that rate, 0.46 of the bandwidth), 6400 x 1600 x 16384 66; 512 x 6400 x 1600
-// 8.0, 3 x 6400 x 1600 5.4, 64 x 8192 x 8192 11.6 (0.48 of the bandwidth).
+// 8.0, 3 x 6400 x 1600 5.4, 64 x 8192 x 8192 11.6 (weights in the L2; 16 from memory, 0.35 of the bandwidth).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

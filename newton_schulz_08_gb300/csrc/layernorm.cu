@@ -23,14 +23,16 @@
 // gradients of weight and bias in registers; it makes two passes over the row
 // in shared memory (its two means, then grad_x).  Each CTA leaves one row of
 // partial sums, which norm_columns adds in their order: equal calls give equal
-// bits.  Rows that fit into neither are read again (norm_forward_wide past
-// 220 KB; norm_rows_wide and norm_columns_wide past 16384 entries).
+// bits.  Rows that fit into neither are read again: forward past 220 KB (with its
+// residual's), and past 16384 entries where the residual begins at another offset
+// than x, which norm_forward_long does not turn (3500 x 20000 bfloat16 with a
+// residual 154 us at one offset, 250 so; 2000 x 20000 float32 142 and 169); backward past 16384 entries.
 //
-// Measured, of the measured copy bandwidth: forward 32768 x 1600 bfloat16 with a residual 71 us
-// (0.88), 20000 x 2048 float32 59 (0.82), 6000 x 12800 bfloat16 91 (0.51),
-// 3001 x 12289 bfloat16 58 (0.38), 40000 x 1601 with a residual 116 (0.66);
+// Measured, of the measured copy bandwidth: forward 32768 x 1600 bfloat16 with a residual 72 us
+// (0.87), 20000 x 2048 float32 59 (0.83), 6000 x 12800 bfloat16 93 (0.50),
+// 3001 x 12289 bfloat16 58 (0.38), 40000 x 1601 with a residual 117 (0.66);
 // backward 32768 x 1600 with grad_sum 107 (0.59), 20000 x 2048 float32 91 (0.81),
-// 3001 x 12289 77 (0.43), 40000 x 1601 with grad_sum 143 (0.54), 3500 x 20000 372 (0.17).
+// 3001 x 12289 78 (0.43), 40000 x 1601 with grad_sum 143 (0.54), 3500 x 20000 372 (0.17).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
